@@ -126,6 +126,8 @@ def kernel_bytes(name, cfg):
     write given its own inputs and outputs (intermediates included)."""
     if cfg["variant"] == "kda":
         return kda_kernel_bytes(name, cfg)
+    if name.startswith(("k_delta_", "k_norm_")):
+        return 0  # kernels of the delta rule and the layer norm: no scan workload launches them
     t = tensor_bytes(cfg)
     b, T, H, P, N = (cfg[k] for k in ("batch", "seqlen", "nheads", "headdim", "dstate"))
     L = cfg["chunk"]

@@ -377,6 +377,144 @@ ssd_status ssd_kda_backward(const ssd_kda_problem* prob, const float* dout, cons
                             void* ws, size_t ws_bytes, void* cuda_stream);
 
 /*
+ * The gated delta rule with one log-decay per head, by chunks on the tensor
+ * cores and step by step on a cache of states.  Per sequence and value head,
+ * with state S [K, V]:
+ *     S_dec = exp(g_t) S_{t-1}
+ *     r_t   = beta_t (v_t - S_dec^T k_t)
+ *     S_t   = S_dec + k_t (x) r_t
+ *     o_t   = scale S_t^T q_t
+ * (the KDA recurrence above with the same decay for every key row, on bf16
+ * tensors).  Value head hv reads query / key head hv / G, G = value_heads /
+ * nheads; dq, dk of a query / key head are the sums over its G value heads.
+ *
+ * ssd_delta_problem:
+ *   io_dtype    of q, k, v, o and their gradients: SSD_BF16; ssd_delta_step
+ *               also takes SSD_F32 (the others return SSD_ERR_DTYPE).
+ *   gate_dtype  of g, beta, dg, dbeta: SSD_F32 or SSD_BF16.  (g <= 0 in
+ *               earnest; -inf forgets the state.)
+ *   packed      0: batch sequences of seqlen steps each, q [b,T,H,K] and so
+ *               on.  1: batch sequences of lengths of their own, one after
+ *               another on one axis of seqlen steps in all, q [T,H,K] and so
+ *               on; the call's cu_seqlens (device, int32 [batch + 1], 4-byte
+ *               aligned) holds 0, the ends of the first sequences, seqlen.
+ *               Empty sequences are allowed.  The kernels clamp its values to
+ *               0 .. seqlen and to ascending order; steps that belong to no
+ *               sequence are not written.  ssd_delta_step takes packed = 0.
+ *   batch, seqlen, nheads (H), value_heads (HV, a multiple of H), key_dim (K),
+ *   value_dim (V): >= 1.  Limits of this build: K, V <= 128, H <= 65535, steps
+ *               and b*HV below 2^31 (SSD_ERR_SHAPE).
+ *   q_stride, k_stride, v_stride: elements from a step to the next, for
+ *               tensors that lie inside wider ones; 0 = dense (H*K, H*K,
+ *               HV*V).  Batches follow one another at T strides.  Everything
+ *               else is dense.
+ * Layouts (row-major): q, k, dq, dk [b,T,H,K]; v, o, do, dv [b,T,HV,V];
+ * g, beta, dg, dbeta [b,T,HV]; s0, s_final, ds_final, ds0 [b,HV,K,V] fp32.
+ * q, k, v need the alignment of their type (rows of whole 16-byte pieces that
+ * start on 16 bytes are read faster); every other pointer of the chunked calls
+ * is 16-byte aligned.
+ *
+ * Precision.  The state is fp32 over any length: what the chunk products read
+ * of it enters the tensor cores as two bf16 numbers, so s_final (and ds0) are
+ * good to about 1e-5 of their size, and o is rounded once to bf16.  The other
+ * gradients are sums of products of bf16-rounded tiles: their relative error
+ * is about 2^-8 whatever type they are stored in.  A NaN or infinity in q, k,
+ * v, g or beta may reach every step of its chunk of 64 steps and every later
+ * one of its sequence; other sequences and steps past a sequence's end take
+ * nothing from it.
+ *
+ * ssd_delta_workspace_size: device workspace of ssd_delta_forward (backward ==
+ *   0) or ssd_delta_backward; stashed != 0: of the call with a stash, which
+ *   needs less.  Host-only.  Its first 4 bytes are the device status word, as
+ *   for ssd_forward.
+ * ssd_delta_stash_size: bytes of the stash that a training forward may keep
+ *   for its backward: per chunk and value head the bf16 state that enters it
+ *   (V16*KP*2 bytes, V16 = V rounded up to 16, KP = K rounded up to 64 or
+ *   128), the written rows r (64*V16*2) and the chunk's triangular inverse,
+ *   scores and decays (25.25 KiB).  Host-only.
+ * ssd_delta_forward: o, and s_final unless it is NULL, from s0 (NULL: zeros).
+ *   stash NULL, or a device buffer (16-byte aligned) that is filled.
+ * ssd_delta_backward: dq, dk, dv, dg, dbeta and (unless NULL) ds0 of <do, o> +
+ *   <ds_final, s_final> (ds_final NULL: zeros) from the leaf inputs, exactly as
+ *   passed to the forward.  With the stash that a forward of the same problem
+ *   and inputs filled it reads the chunk states instead of making them again;
+ *   the results are the same bit for bit.
+ * ssd_delta_step: seqlen >= 1 steps of each of batch sequences on `state`
+ *   [num_slots,HV,K,V] (fp32, 16-byte aligned), updated in place.  Sequence n
+ *   uses slot slots[n] (device, int32 [batch]; NULL: slot n, num_slots >=
+ *   batch).  A slot number outside 0 .. num_slots - 1 marks a place without a
+ *   sequence: its o is zero and no state is touched.  Two sequences of a call
+ *   must not share a slot.  fp32 arithmetic, no workspace.  Other pointers
+ *   need the alignment of their type.
+ * Errors as for ssd_forward; every error is returned before anything is
+ * enqueued.  Results are bitwise reproducible.
+ */
+typedef struct {
+  int32_t io_dtype;
+  int32_t gate_dtype;
+  int32_t packed;
+  int32_t reserved; /* 0 */
+  int64_t batch;
+  int64_t seqlen;
+  int64_t nheads;
+  int64_t value_heads;
+  int64_t key_dim;
+  int64_t value_dim;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+} ssd_delta_problem;
+
+ssd_status ssd_delta_workspace_size(const ssd_delta_problem* prob, int backward, int stashed, size_t* bytes);
+ssd_status ssd_delta_stash_size(const ssd_delta_problem* prob, size_t* bytes);
+ssd_status ssd_delta_forward(const ssd_delta_problem* prob, const void* q, const void* k, const void* v, const void* g,
+                             const void* beta, const float* s0, const int32_t* cu_seqlens, float scale, void* o,
+                             float* s_final, void* stash, size_t stash_bytes, void* ws, size_t ws_bytes,
+                             void* cuda_stream);
+ssd_status ssd_delta_backward(const ssd_delta_problem* prob, const void* dout, const float* ds_final, const void* q,
+                              const void* k, const void* v, const void* g, const void* beta, const float* s0,
+                              const int32_t* cu_seqlens, float scale, void* dq, void* dk, void* dv, void* dg,
+                              void* dbeta, float* ds0, const void* stash, size_t stash_bytes, void* ws,
+                              size_t ws_bytes, void* cuda_stream);
+ssd_status ssd_delta_step(const ssd_delta_problem* prob, const void* q, const void* k, const void* v, const void* g,
+                          const void* beta, float* state, const int32_t* slots, int64_t num_slots, float scale, void* o,
+                          void* cuda_stream);
+
+/*
+ * Layer norm over the last dimension and its backward: the norm in front of a
+ * mixer (rows of the model's width) and of its heads' outputs (rows of a head).
+ *     mean = sum x / D, var = sum (x - mean)^2 / D, rstd = (var + eps)^-1/2,
+ *     y = (x - mean) rstd * weight + bias
+ *
+ * ssd_norm_problem: io_dtype of x, y, dy, dx and weight_dtype of weight, bias,
+ * dw, db (SSD_F32 or SSD_BF16 each; sums are fp32); rows >= 1 (< 2^31), dim
+ * 1 .. 16384 (SSD_ERR_SHAPE), x_stride: elements from a row of x to the next
+ * (0 = dense).  y, dy, dx are dense [rows, dim]; mean, rstd fp32 [rows].  x
+ * needs the alignment of its type, every other pointer 16 bytes.
+ *
+ * ssd_norm_forward: y, and mean and rstd unless NULL.  weight NULL: ones, bias
+ *   NULL: zeros; eps >= 0.
+ * ssd_norm_backward: dx, and dw and db (summed over the rows in a fixed order)
+ *   unless NULL, from the forward's x, mean, rstd and weight.  ws (at least
+ *   ssd_norm_workspace_size bytes) may be NULL where dw and db are.
+ * Errors as for ssd_forward.  Results are bitwise reproducible.
+ */
+typedef struct {
+  int32_t io_dtype;
+  int32_t weight_dtype;
+  int64_t rows;
+  int64_t dim;
+  int64_t x_stride;
+} ssd_norm_problem;
+
+ssd_status ssd_norm_workspace_size(const ssd_norm_problem* prob, size_t* bytes);
+ssd_status ssd_norm_forward(const ssd_norm_problem* prob, const void* x, const void* weight, const void* bias, float eps,
+                            void* y, float* mean, float* rstd, void* cuda_stream);
+ssd_status ssd_norm_backward(const ssd_norm_problem* prob, const void* dy, const void* x, const float* mean,
+                             const float* rstd, const void* weight, void* dx, void* dw, void* db, void* ws,
+                             size_t ws_bytes, void* cuda_stream);
+
+/*
  * Per-launch timing, for diagnostics and roofline measurement.
  *
  * ssd_profile_start(capacity): every later ssd_forward / ssd_backward call

@@ -44,12 +44,27 @@ EXPORTS = ("ssd_workspace_size", "ssd_forward", "ssd_backward", "ssd_forward_sta
            "ssd_profile_stop", "ssd_status_string", "ssd_version", "ssd_states_size", "ssd_forward_stash",
            "ssd_backward_stashed", "ssd_forward_static_status", "ssd_read_status", "ssd_wait_selftest",
            "ssd_checkpoints_size", "ssd_forward_checkpointed", "ssd_backward_checkpointed",
-           "ssd_kda_workspace_size", "ssd_kda_forward", "ssd_kda_backward")
+           "ssd_kda_workspace_size", "ssd_kda_forward", "ssd_kda_backward", "ssd_delta_workspace_size",
+           "ssd_delta_stash_size", "ssd_delta_forward", "ssd_delta_backward", "ssd_delta_step",
+           "ssd_norm_workspace_size", "ssd_norm_forward", "ssd_norm_backward")
 
 
 class ssd_kda_problem(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("nheads", ctypes.c_int64),
                 ("value_heads", ctypes.c_int64), ("key_dim", ctypes.c_int64), ("value_dim", ctypes.c_int64)]
+
+
+class ssd_delta_problem(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("packed", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("nheads", ctypes.c_int64), ("value_heads", ctypes.c_int64), ("key_dim", ctypes.c_int64),
+                ("value_dim", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
+class ssd_norm_problem(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("x_stride", ctypes.c_int64)]
 
 
 class ssd_kernel_time(ctypes.Structure):
@@ -117,6 +132,24 @@ def load(path: str | None = None):
         lib.ssd_kda_forward.restype = i32
         lib.ssd_kda_backward.argtypes = [kp] + [vp] * 8 + [ctypes.c_float] + [vp] * 6 + [vp, sz, vp]
         lib.ssd_kda_backward.restype = i32
+        dp, f32 = ctypes.POINTER(ssd_delta_problem), ctypes.c_float
+        lib.ssd_delta_workspace_size.argtypes = [dp, i32, i32, ctypes.POINTER(sz)]
+        lib.ssd_delta_workspace_size.restype = i32
+        lib.ssd_delta_stash_size.argtypes = [dp, ctypes.POINTER(sz)]
+        lib.ssd_delta_stash_size.restype = i32
+        lib.ssd_delta_forward.argtypes = [dp] + [vp] * 7 + [f32, vp, vp, vp, sz, vp, sz, vp]
+        lib.ssd_delta_forward.restype = i32
+        lib.ssd_delta_backward.argtypes = [dp] + [vp] * 9 + [f32] + [vp] * 6 + [vp, sz, vp, sz, vp]
+        lib.ssd_delta_backward.restype = i32
+        lib.ssd_delta_step.argtypes = [dp] + [vp] * 7 + [i64, f32, vp, vp]
+        lib.ssd_delta_step.restype = i32
+        np_ = ctypes.POINTER(ssd_norm_problem)
+        lib.ssd_norm_workspace_size.argtypes = [np_, ctypes.POINTER(sz)]
+        lib.ssd_norm_workspace_size.restype = i32
+        lib.ssd_norm_forward.argtypes = [np_] + [vp] * 3 + [f32] + [vp] * 4
+        lib.ssd_norm_forward.restype = i32
+        lib.ssd_norm_backward.argtypes = [np_] + [vp] * 9 + [sz, vp]
+        lib.ssd_norm_backward.restype = i32
         _lib = lib
         return lib
 
@@ -421,3 +454,232 @@ def kda_backward(cfg: dict, dout, ds_final, q, k, v, g, beta, s0=None, scale=Non
     ssd_kda_backward(prob, dout, ds_final, q, k, v, g, beta, s0, scale, out["dq"], out["dk"], out["dv"], out["dg"],
                      out["dbeta"], out["ds0"], ws, n, stream)
     return out
+
+
+# ------------------------------------------------------------- gated delta rule, one decay per head
+def delta_problem(cfg: dict, q=None, k=None, v=None, packed: bool = False) -> ssd_delta_problem:
+    """An ``ssd_delta_problem`` from a config dict (``configs.DELTA_CONFIGS``); q, k, v (if given) set the strides from
+    step to step and are checked against the sizes."""
+    p = ssd_delta_problem(DTYPES[cfg["dtype"]], DTYPES[cfg.get("gate_dtype", "f32")], int(packed), 0, cfg["batch"],
+                          cfg["seqlen"], cfg["nheads"], cfg["value_heads"], cfg["key_dim"], cfg["value_dim"], 0, 0, 0)
+    lead = (1 if packed else p.batch, p.seqlen)
+    for name, t, heads, dim in (("q", q, p.nheads, p.key_dim), ("k", k, p.nheads, p.key_dim),
+                                ("v", v, p.value_heads, p.value_dim)):
+        if t is not None:
+            setattr(p, name + "_stride", _step_stride(name, t, lead + (heads, dim), cfg["dtype"]))
+    return p
+
+
+def _step_stride(name: str, t, shape: tuple, dtype: str) -> int:
+    """Elements from a step to the next of a tensor [b, T, heads, dim] whose heads are dense and whose batches follow
+    one another at T steps; raises ValueError for any other tensor."""
+    if t.dtype != _TORCH_DTYPE[dtype]:
+        raise ValueError(f"{name}: {t.dtype}, expected {_TORCH_DTYPE[dtype]}")
+    got, (b, steps, heads, dim) = tuple(t.shape), shape
+    if got != shape and not (b == 1 and got == shape[1:]):
+        raise ValueError(f"{name}: shape {got}, expected {shape}")
+    if t.is_contiguous():
+        return 0
+    sb, st, sh, sd = t.stride() if t.dim() == 4 else (0,) + tuple(t.stride())
+    if steps == 1:  # one step a batch: the batches are the steps
+        st = sb if b > 1 else heads * dim
+    if (dim > 1 and sd != 1) or (heads > 1 and sh != dim) or (b > 1 and sb != steps * st) or st < heads * dim:
+        raise ValueError(f"{name}: strides {tuple(t.stride())}: heads have to be dense and batches follow one another")
+    return st
+
+
+def _dense(name: str, t, shape: tuple, dtype) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) not in (tuple(shape), tuple(shape[1:]) if shape[0] == 1 else ()):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} (contiguous: {t.is_contiguous()}), expected contiguous "
+                         f"{dtype} {tuple(shape)}")
+
+
+def ssd_delta_workspace_size(prob: ssd_delta_problem, backward: bool, stashed: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().ssd_delta_workspace_size(ctypes.byref(prob), int(bool(backward)), int(bool(stashed)), ctypes.byref(out))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_delta_workspace_size")
+    return out.value
+
+
+def ssd_delta_stash_size(prob: ssd_delta_problem) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().ssd_delta_stash_size(ctypes.byref(prob), ctypes.byref(out))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_delta_stash_size")
+    return out.value
+
+
+def ssd_delta_forward(prob, q, k, v, g, beta, s0, cu_seqlens, scale, o, s_final, stash, stash_bytes, ws, ws_bytes,
+                      stream=None) -> None:
+    st = load().ssd_delta_forward(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(s0),
+                                  _ptr(cu_seqlens), float(scale), _ptr(o), _ptr(s_final), _ptr(stash),
+                                  int(stash_bytes), _ptr(ws), int(ws_bytes), _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_delta_forward")
+
+
+def ssd_delta_backward(prob, dout, ds_final, q, k, v, g, beta, s0, cu_seqlens, scale, dq, dk, dv, dg, dbeta, ds0, stash,
+                       stash_bytes, ws, ws_bytes, stream=None) -> None:
+    st = load().ssd_delta_backward(ctypes.byref(prob), _ptr(dout), _ptr(ds_final), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                                   _ptr(beta), _ptr(s0), _ptr(cu_seqlens), float(scale), _ptr(dq), _ptr(dk), _ptr(dv),
+                                   _ptr(dg), _ptr(dbeta), _ptr(ds0), _ptr(stash), int(stash_bytes), _ptr(ws),
+                                   int(ws_bytes), _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_delta_backward")
+
+
+def ssd_delta_step(prob, q, k, v, g, beta, state, slots, num_slots, scale, o, stream=None) -> None:
+    st = load().ssd_delta_step(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
+                               _ptr(slots), int(num_slots), float(scale), _ptr(o), _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_delta_step")
+
+
+def _delta_check(cfg, prob, q, g, beta, s0, cu_seqlens):
+    lead = (1 if prob.packed else prob.batch, prob.seqlen)
+    gt = _TORCH_DTYPE[cfg.get("gate_dtype", "f32")]
+    _dense("g", g, lead + (prob.value_heads,), gt)
+    _dense("beta", beta, lead + (prob.value_heads,), gt)
+    _dense("s0", s0, (prob.batch, prob.value_heads, prob.key_dim, prob.value_dim), torch.float32)
+    _dense("cu_seqlens", cu_seqlens, (prob.batch + 1,), torch.int32)
+    return lead
+
+
+def delta_stash(cfg: dict, device="cuda", packed: bool = False):
+    """A buffer for what ``delta_forward`` keeps for ``delta_backward`` (uint8)."""
+    n = ssd_delta_stash_size(delta_problem(cfg, packed=packed))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _delta_workspace(prob, backward, stashed, device):
+    n = ssd_delta_workspace_size(prob, backward, stashed)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device), n
+
+
+def delta_forward(cfg: dict, q, k, v, g, beta, s0=None, scale=None, cu_seqlens=None, stash=None, stream=None,
+                  workspace=None):
+    """Allocate o and s_final, run ``ssd_delta_forward``; returns (o, s_final).  With ``cu_seqlens`` (int32,
+    [batch + 1]) the sequences are packed on one axis of seqlen steps; ``stash`` (``delta_stash``) is filled for
+    ``delta_backward``; scale defaults to key_dim^-1/2."""
+    packed = cu_seqlens is not None
+    prob = delta_problem(cfg, q, k, v, packed)
+    _delta_check(cfg, prob, q, g, beta, s0, cu_seqlens)
+    scale = cfg["key_dim"] ** -0.5 if scale is None else scale
+    o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    s_final = torch.empty((cfg["batch"], cfg["value_heads"], cfg["key_dim"], cfg["value_dim"]), dtype=torch.float32,
+                          device=v.device)
+    ws, n = workspace if workspace is not None else _delta_workspace(prob, False, stash is not None, v.device)
+    ssd_delta_forward(prob, q, k, v, g, beta, s0, cu_seqlens, scale, o, s_final, stash,
+                      0 if stash is None else stash.numel(), ws, n, stream)
+    return o, s_final
+
+
+def delta_backward(cfg: dict, dout, q, k, v, g, beta, ds_final=None, s0=None, scale=None, cu_seqlens=None, stash=None,
+                   stream=None, workspace=None):
+    """Allocate the gradients and run ``ssd_delta_backward``; returns dq, dk, dv, dg, dbeta and ds0 (None where s0 is
+    None).  ``stash``: what ``delta_forward`` filled on the same inputs; without it the chunk states are made again."""
+    packed = cu_seqlens is not None
+    prob = delta_problem(cfg, q, k, v, packed)
+    lead = _delta_check(cfg, prob, q, g, beta, s0, cu_seqlens)
+    _dense("dout", dout, lead + (prob.value_heads, prob.value_dim), v.dtype)
+    _dense("ds_final", ds_final, (prob.batch, prob.value_heads, prob.key_dim, prob.value_dim), torch.float32)
+    scale = cfg["key_dim"] ** -0.5 if scale is None else scale
+    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
+    out = {"dq": new(q), "dk": new(k), "dv": new(v), "dg": new(g), "dbeta": new(beta),
+           "ds0": None if s0 is None else new(s0)}
+    ws, n = workspace if workspace is not None else _delta_workspace(prob, True, stash is not None, v.device)
+    ssd_delta_backward(prob, dout, ds_final, q, k, v, g, beta, s0, cu_seqlens, scale, out["dq"], out["dk"], out["dv"],
+                       out["dg"], out["dbeta"], out["ds0"], stash, 0 if stash is None else stash.numel(), ws, n, stream)
+    return out
+
+
+def delta_step(cfg: dict, q, k, v, g, beta, state, slots=None, scale=None, stream=None):
+    """Allocate o and run ``ssd_delta_step``: seqlen steps of each sequence on its slot of ``state`` [slots, HV, K, V]
+    (fp32), which is updated in place; returns o."""
+    prob = delta_problem(cfg, q, k, v)
+    _delta_check(cfg, prob, q, g, beta, None, None)
+    _dense("state", state, (state.shape[0], prob.value_heads, prob.key_dim, prob.value_dim), torch.float32)
+    _dense("slots", slots, (prob.batch,), torch.int32)
+    scale = cfg["key_dim"] ** -0.5 if scale is None else scale
+    o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    ssd_delta_step(prob, q, k, v, g, beta, state, slots, state.shape[0], scale, o, stream)
+    return o
+
+
+# ------------------------------------------------------------- layer norm
+def _name(dtype) -> str:
+    for k, v in _TORCH_DTYPE.items():
+        if v == dtype:
+            return k
+    raise ValueError(f"{dtype}: float32 or bfloat16 expected")
+
+
+def norm_problem(x, weight=None) -> ssd_norm_problem:
+    """An ``ssd_norm_problem`` for x [.., D]: contiguous, or two-dimensional with a stride from row to row."""
+    dim = x.shape[-1]
+    wt = DTYPES[_name(weight.dtype)] if weight is not None else DTYPES["f32"]
+    stride = 0
+    if not x.is_contiguous():
+        if x.dim() != 2 or (dim > 1 and x.stride(1) != 1) or x.stride(0) < dim:
+            raise ValueError(f"x: strides {tuple(x.stride())}: rows have to be dense, at one stride")
+        stride = x.stride(0)
+    return ssd_norm_problem(DTYPES[_name(x.dtype)], wt, x.numel() // max(dim, 1), dim, stride)
+
+
+def ssd_norm_workspace_size(prob: ssd_norm_problem) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().ssd_norm_workspace_size(ctypes.byref(prob), ctypes.byref(out))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_norm_workspace_size")
+    return out.value
+
+
+def ssd_norm_forward(prob, x, weight, bias, eps, y, mean, rstd, stream=None) -> None:
+    st = load().ssd_norm_forward(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(mean),
+                                 _ptr(rstd), _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_norm_forward")
+
+
+def ssd_norm_backward(prob, dy, x, mean, rstd, weight, dx, dw, db, ws, ws_bytes, stream=None) -> None:
+    st = load().ssd_norm_backward(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),
+                                  _ptr(dw), _ptr(db), _ptr(ws), int(ws_bytes), _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_norm_backward")
+
+
+def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stream=None):
+    """Layer norm of x [.., D]; weight and bias [D] (either may be None) of one type.  Returns y (contiguous), mean and
+    rstd (fp32, one per row)."""
+    prob = norm_problem(x, weight if weight is not None else bias)
+    if weight is not None:
+        _dense("weight", weight, (prob.dim,), weight.dtype)
+    if bias is not None:
+        _dense("bias", bias, (prob.dim,), weight.dtype if weight is not None else bias.dtype)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    stats = torch.empty((2, -(-prob.rows // 4) * 4), dtype=torch.float32, device=x.device)
+    mean, rstd = (s[:prob.rows].view(x.shape[:-1]) for s in stats)
+    ssd_norm_forward(prob, x, weight, bias, eps, y, mean, rstd, stream)
+    return y, mean, rstd
+
+
+def norm_backward(dy, x, mean, rstd, weight=None, stream=None, workspace=None):
+    """The gradients of ``norm_forward``: dx (contiguous), and dw and db in the weight's type (fp32 without a
+    weight)."""
+    prob = norm_problem(x, weight)
+    if dy.dtype != x.dtype or dy.shape != x.shape or not dy.is_contiguous():
+        raise ValueError(f"dy: {dy.dtype} {tuple(dy.shape)}, expected contiguous {x.dtype} {tuple(x.shape)}")
+    if weight is not None:
+        _dense("weight", weight, (prob.dim,), weight.dtype)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    wt = torch.float32 if weight is None else weight.dtype
+    dw = torch.empty(prob.dim, dtype=wt, device=x.device)
+    db = torch.empty(prob.dim, dtype=wt, device=x.device)
+    if workspace is None:
+        n = ssd_norm_workspace_size(prob)
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device), n
+    ssd_norm_backward(prob, dy, x, mean, rstd, weight, dx, dw, db, workspace[0], workspace[1], stream)
+    return {"dx": dx, "dw": dw, "db": db}

@@ -39,6 +39,14 @@ KDA_CONFIGS = {
                      value_dim=128),
 }
 
+# The gated delta rule with one decay per head: the same sizes as the KDA workloads, on bf16 tensors.
+DELTA_CONFIGS = {
+    "delta_tiny_bf16": dict(dtype="bf16", gate_dtype="f32", batch=1, seqlen=16, nheads=2, value_heads=4, key_dim=8,
+                            value_dim=8),
+    "delta_bf16": dict(dtype="bf16", gate_dtype="f32", batch=2, seqlen=1024, nheads=8, value_heads=16, key_dim=128,
+                       value_dim=128),
+}
+
 
 def tokens(cfg: dict) -> int:
     """Tokens per forward+backward pair: batch x seqlen."""

@@ -1,0 +1,227 @@
+// Building blocks of the chunked delta rule: warp-level bf16 products whose operands come out of shared-memory tiles
+// (ldmatrix) or straight out of another product's accumulators, the split of an fp32 operand into two bf16 ones, and
+// the sizes, tiles and workspace records that its kernels share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ssd.h"
+#include "ssd_internal.h"
+
+namespace ssd {
+namespace delta {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kC = 64;              // steps of a chunk
+constexpr int kTP = kC + 8;         // shared-memory pitch of a [64][64] bf16 tile (16 bytes past a multiple of 128: ldmatrix without conflicts)
+constexpr int kGateRows = 5;        // per-step records of a chunk: e^G, e^{G_end - G}, beta, G (high), G (low)
+constexpr float kMinG = -1e4f;      // e^g of anything below is 0; keeps G - G' defined where g is -inf
+
+struct Dims {
+  int N, T, H, HV, G, K, V;          // sequences, steps (packed: of all), heads, value heads, HV / H, widths
+  int KP, VP;                        // K rounded up to 64 or 128, V rounded up to a multiple of 16
+  int nc;                            // chunks (packed: the most there can be, over all sequences)
+  bool packed, f32, gate_bf16;
+  long long qs, ks, vs;              // elements from a token to the next in q, k, v
+  bool qvec, kvec, vvec, ovec;       // rows of 16-byte pieces
+};
+
+// Where the sequences lie: sequence n has its steps at start[n] .. start[n] + len[n] - 1 of the token axis and its
+// chunks at chunk[n] .. chunk[n + 1] - 1 of the chunk axis.  Filled from cu_seqlens for a packed batch; computed
+// where it is read otherwise.
+struct Table {
+  int *start, *len, *chunk;
+};
+
+// One record per (chunk, value head), item = chunk * HV + head.
+struct Prep {
+  bf16* Thi;     // [item][64][64]: (I + A)^-1, rounded to bf16
+  bf16* Tlo;     // [item][64][64]: what that rounding left, rounded
+  bf16* P;       // [item][64][64]: e^{G_i - G_j} q_i . k_j (j <= i)
+  float* gates;  // [item][5][64]
+};
+
+// The sizes of a problem, or the error that it is refused with.
+ssd_status make_dims(const ssd_delta_problem* p, bool f32_ok, Dims* d);
+
+struct In {
+  const bf16 *q, *k, *v;
+  const void *g, *beta;
+  const float* s0;
+  float scale;
+};
+
+__device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+  const int n = ok ? 16 : 0;  // 0: the 16 bytes are filled with zeros and nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four 8x8 tiles; lane l gives the address of row l % 8 of tile l / 8.
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void stm4(uint32_t a, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ void stm4t(uint32_t a, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// c[16x8] += a[16x16] b[16x8], bf16 operands, fp32 sums.
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+
+// (x, y) = h + l with both in bf16: h rounds to 8 bits and l holds the next 8, so h + l is within 2^-17 of each.
+__device__ __forceinline__ void split(float x, float y, uint32_t& h, uint32_t& l) {
+  h = pack(x, y);
+  l = pack(x - lo_f(h), y - hi_f(h));
+}
+
+// Two neighbouring accumulator tiles [16x8] as one left operand [16x16]: the layouts are the same, so a product's
+// result feeds the next product without leaving the registers.
+__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&h)[4], uint32_t (&l)[4]) {
+  split(c0[0], c0[1], h[0], l[0]);
+  split(c0[2], c0[3], h[1], l[1]);
+  split(c1[0], c1[1], h[2], l[2]);
+  split(c1[2], c1[3], h[3], l[3]);
+}
+__device__ __forceinline__ void round_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&h)[4]) {
+  h[0] = pack(c0[0], c0[1]);
+  h[1] = pack(c0[2], c0[3]);
+  h[2] = pack(c1[0], c1[1]);
+  h[3] = pack(c1[2], c1[3]);
+}
+
+// Lane addresses into a tile of rows of `pitch` elements, for ldm4 / ldm4t / stm4 / stm4t of 16 x 16 elements at
+// (row, col).  by_row: tiles in the order (rows 0-7, cols 0-7), (rows 0-7, cols 8-15), (rows 8-15, cols 0-7), ...;
+// by_col: (0-7, 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15).
+__device__ __forceinline__ uint32_t by_row(uint32_t base, int pitch, int row, int col, int lane) {
+  return base + 2u * (uint32_t)((row + (lane & 7) + ((lane >> 4) << 3)) * pitch + col + (((lane >> 3) & 1) << 3));
+}
+__device__ __forceinline__ uint32_t by_col(uint32_t base, int pitch, int row, int col, int lane) {
+  return base + 2u * (uint32_t)((row + (lane & 7) + (((lane >> 3) & 1) << 3)) * pitch + col + ((lane >> 4) << 3));
+}
+
+// 64 rows of `width` (a multiple of 8) elements into a tile: row r from src + r * stride, zeros past `rows` and `cols`.
+// vec: every row starts on 16 bytes and cols is a multiple of 8 (asynchronous copies; the caller commits and waits);
+// otherwise element by element.
+__device__ __forceinline__ void load_rows(bf16* dst, int pitch, int width, const bf16* src, long long stride, int rows,
+                                          int cols, bool vec, int tid, int nthreads) {
+  if (vec) {
+    const int w8 = width >> 3;
+    const uint32_t d = su32(dst);
+    for (int i = tid; i < kC * w8; i += nthreads) {
+      const int r = i / w8, c = (i - r * w8) << 3;
+      const bool ok = r < rows && c < cols;
+      cp16(d + 2u * (uint32_t)(r * pitch + c), ok ? src + (long long)r * stride + c : src, ok);
+    }
+  } else {
+    for (int i = tid; i < kC * width; i += nthreads) {
+      const int r = i / width, c = i - r * width;
+      dst[r * pitch + c] = r < rows && c < cols ? src[(long long)r * stride + c] : __float2bfloat16_rn(0.f);
+    }
+  }
+}
+
+// `n16` 16-byte pieces of consecutive rows of `w8` pieces into a tile.
+__device__ __forceinline__ void load_dense(bf16* dst, int pitch, int w8, const bf16* src, int rows, int tid,
+                                           int nthreads) {
+  const uint32_t d = su32(dst);
+  for (int i = tid; i < rows * w8; i += nthreads) {
+    const int r = i / w8, c = (i - r * w8) << 3;
+    cp16(d + 2u * (uint32_t)(r * pitch + c), src + (size_t)i * 8, true);
+  }
+}
+
+__device__ __forceinline__ float gate(const void* p, size_t i, bool is_bf16) {
+  return is_bf16 ? __bfloat162float(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+struct Seq {
+  int start, len, chunk, nc;  // first step, steps, first chunk, chunks
+};
+__device__ __forceinline__ Seq sequence(const Dims& d, const Table& t, int n) {
+  Seq s;
+  if (d.packed) {
+    s.start = t.start[n];
+    s.len = t.len[n];
+    s.chunk = t.chunk[n];
+  } else {
+    s.start = n * d.T;
+    s.len = d.T;
+    s.chunk = n * ((d.T + kC - 1) / kC);
+  }
+  s.nc = (s.len + kC - 1) / kC;
+  return s;
+}
+
+// The sequence of chunk c, and how many steps of it the chunk holds (0: past the last chunk) from which step.
+struct Chunk {
+  int n, first, rows;
+};
+__device__ __forceinline__ Chunk chunk_of(const Dims& d, const Table& t, int c) {
+  Chunk r;
+  if (!d.packed) {
+    const int per = (d.T + kC - 1) / kC;
+    r.n = c / per;
+    const int at = (c - r.n * per) * kC;
+    r.first = r.n * d.T + at;
+    r.rows = min(kC, d.T - at);
+    return r;
+  }
+  r.n = 0;
+  r.first = 0;
+  r.rows = 0;
+  if (c >= t.chunk[d.N]) return r;
+  int lo = 0, hi = d.N - 1;  // the last n with chunk[n] <= c
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.chunk[mid] <= c)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int at = (c - t.chunk[lo]) * kC;
+  r.n = lo;
+  r.first = t.start[lo] + at;
+  r.rows = min(kC, t.len[lo] - at);
+  return r;
+}
+
+}  // namespace delta
+}  // namespace ssd

@@ -1,0 +1,448 @@
+// Layer norm over the last dimension, forward and backward, with the reductions of the weight's and the bias's
+// gradient.  Per row x of D values:
+//     mean = sum x / D,   var = sum (x - mean)^2 / D,   rstd = (var + eps)^-1/2,   h = (x - mean) rstd,   y = h w + b
+//     dx = rstd (w dy - mean(w dy) - h mean(w dy h)),   dw = sum over rows of dy h,   db = sum over rows of dy
+// Both passes are bound by memory: a row is read once and held in registers (the variance is summed from the
+// differences to the mean, in a second pass over the registers), sums are fp32.  The backward's blocks each take every
+// n-th row and keep their columns' dw and db in registers; one row of partial sums a block goes to the workspace and
+// k_norm_columns adds those in block order, so the result does not depend on timing.
+#include <initializer_list>
+
+#include "ssd.h"
+#include "ssd_internal.h"
+
+namespace ssd {
+namespace norm {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+struct Args {
+  long long rows, xs;  // rows; elements from a row of x to the next
+  int D;
+  bool wbf16;
+  float eps;
+};
+
+__device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float ld1(const float* p) { return *p; }
+__device__ __forceinline__ float ld1(const bf16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void st1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void st1(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
+template <typename T>
+struct Width;  // elements of a 16-byte piece
+template <>
+struct Width<float> {
+  static constexpr int n = 4;
+};
+template <>
+struct Width<bf16> {
+  static constexpr int n = 8;
+};
+__device__ __forceinline__ void ld16(const float* p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x;
+  x[1] = v.y;
+  x[2] = v.z;
+  x[3] = v.w;
+}
+__device__ __forceinline__ void ld16(const bf16* p, float (&x)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  x[0] = lo_f(v.x);
+  x[1] = hi_f(v.x);
+  x[2] = lo_f(v.y);
+  x[3] = hi_f(v.y);
+  x[4] = lo_f(v.z);
+  x[5] = hi_f(v.z);
+  x[6] = lo_f(v.w);
+  x[7] = hi_f(v.w);
+}
+__device__ __forceinline__ void st16(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void st16(bf16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
+}
+
+// A thread's E elements of a row held by TPR threads.  kVec: pieces of 16 bytes, piece i of thread t at column
+// (i TPR + t) W; otherwise single elements, element i at column i TPR + t.
+template <typename T, int TPR, int E, bool kVec>
+struct Row {
+  static constexpr int W = kVec ? Width<T>::n : 1;
+  static constexpr int NP = E / W;
+  static __device__ __forceinline__ int col(int i, int t) { return (i * TPR + t) * W; }
+  template <typename U>
+  static __device__ __forceinline__ void load(const U* p, int D, int t, float (&x)[E], float fill) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = col(i, t);
+      if constexpr (kVec && sizeof(U) == sizeof(T)) {
+        float y[Width<U>::n];
+#pragma unroll
+        for (int j = 0; j < W; ++j) y[j] = fill;
+        if (c < D) ld16(p + c, y);
+#pragma unroll
+        for (int j = 0; j < W; ++j) x[i * W + j] = y[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) x[i * W + j] = c + j < D ? ld1(p + c + j) : fill;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, int D, int t, const float (&x)[E]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = col(i, t);
+      if (c >= D) continue;
+      if constexpr (kVec) {
+        float y[Width<T>::n];
+#pragma unroll
+        for (int j = 0; j < W; ++j) y[j] = x[i * W + j];
+        st16(p + c, y);
+      } else {
+        st1(p + c, x[i]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void weights(const void* w, bool wbf16, int D, int t, float (&x)[E], float fill) {
+    if (!w) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] = fill;
+    } else if (wbf16) {
+      load(static_cast<const bf16*>(w), D, t, x, fill);
+    } else {
+      load(static_cast<const float*>(w), D, t, x, fill);
+    }
+  }
+  static __device__ __forceinline__ bool in(int e, int D, int t) { return col(e / W, t) + e % W < D; }
+};
+
+// Sums over the TPR threads of a row, in every one of them.  TPR > 32: `red` holds NV floats per warp of the row; two
+// barriers of the whole block, which every thread takes part in.
+template <int TPR, int NV>
+__device__ __forceinline__ void row_sum(float (&x)[NV], float* red, int t) {
+#pragma unroll
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < NV; ++j) x[j] += __shfl_xor_sync(0xffffffffu, x[j], o);
+  if (TPR > 32) {
+    __syncthreads();
+    if ((t & 31) == 0)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) red[(t >> 5) * NV + j] = x[j];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      x[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < (TPR + 31) / 32; ++i) x[j] += red[i * NV + j];
+    }
+  }
+}
+
+template <int TPR>
+constexpr int block_threads() {
+  return TPR < 256 ? 256 : TPR;
+}
+
+template <typename T, int TPR, int E, bool kVec>
+__global__ void __launch_bounds__(block_threads<TPR>())
+    k_norm_forward(Args a, const T* __restrict__ x, const void* w, const void* b, T* y, float* mean, float* rstd) {
+  using R = Row<T, TPR, E, kVec>;
+  constexpr int kGroups = block_threads<TPR>() / TPR;
+  __shared__ float red[kGroups][(TPR + 31) / 32];
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  const long long row = (long long)blockIdx.x * kGroups + grp;
+  const bool live = row < a.rows;
+  float v[E];
+  R::load(x + (live ? row : 0) * a.xs, live ? a.D : 0, t, v, 0.f);
+  float s[1] = {0.f};
+#pragma unroll
+  for (int e = 0; e < E; ++e) s[0] += v[e];
+  row_sum<TPR, 1>(s, red[grp], t);
+  const float inv = 1.f / (float)a.D, m = s[0] * inv;
+  s[0] = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    v[e] = R::in(e, a.D, t) ? v[e] - m : 0.f;
+    s[0] = fmaf(v[e], v[e], s[0]);
+  }
+  row_sum<TPR, 1>(s, red[grp], t);
+  const float r = rsqrtf(fmaf(s[0], inv, a.eps));
+  if (!live) return;
+  float wt[E], bt[E];
+  R::weights(w, a.wbf16, a.D, t, wt, 1.f);
+  R::weights(b, a.wbf16, a.D, t, bt, 0.f);
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = fmaf(v[e] * r, wt[e], bt[e]);
+  R::store(y + (size_t)row * a.D, a.D, t, v);
+  if (t == 0) {
+    if (mean) mean[row] = m;
+    if (rstd) rstd[row] = r;
+  }
+}
+
+template <typename T, int TPR, int E, bool kVec>
+__global__ void __launch_bounds__(block_threads<TPR>())
+    k_norm_backward(Args a, const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ mean,
+                    const float* __restrict__ rstd, const void* w, T* dx, float* part) {
+  using R = Row<T, TPR, E, kVec>;
+  constexpr int kGroups = block_threads<TPR>() / TPR;
+  __shared__ float red[kGroups][2 * ((TPR + 31) / 32)];
+  __shared__ float s_part[kGroups > 1 ? TPR * E : 1];
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  float wt[E], dw[E], db[E];
+  R::weights(w, a.wbf16, a.D, t, wt, 1.f);
+#pragma unroll
+  for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.f;
+  const float inv = 1.f / (float)a.D;
+  for (long long first = (long long)blockIdx.x * kGroups; first < a.rows; first += (long long)gridDim.x * kGroups) {
+    const long long row = first + grp;
+    const bool live = row < a.rows;
+    float h[E], g[E];
+    R::load(x + (live ? row : 0) * a.xs, live ? a.D : 0, t, h, 0.f);
+    R::load(dy + (live ? row : 0) * (long long)a.D, live ? a.D : 0, t, g, 0.f);
+    const float m = live ? mean[row] : 0.f, r = live ? rstd[row] : 0.f;
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      h[e] = R::in(e, a.D, t) ? (h[e] - m) * r : 0.f;
+      db[e] += g[e];
+      dw[e] = fmaf(g[e], h[e], dw[e]);
+      g[e] *= wt[e];
+      s[0] += g[e];
+      s[1] = fmaf(g[e], h[e], s[1]);
+    }
+    row_sum<TPR, 2>(s, red[grp], t);
+    const float s0 = s[0] * inv, s1 = s[1] * inv;
+#pragma unroll
+    for (int e = 0; e < E; ++e) g[e] = r * (g[e] - s0 - h[e] * s1);
+    if (live) R::store(dx + (size_t)row * a.D, a.D, t, g);
+  }
+  if (!part) return;
+  // this block's sums: its groups in order
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float(&acc)[E] = which ? db : dw;
+    if (kGroups > 1) {
+      for (int k = 1; k < kGroups; ++k) {
+        __syncthreads();
+        if (grp == k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) s_part[e * TPR + t] = acc[e];
+        __syncthreads();
+        if (grp == 0)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += s_part[e * TPR + t];
+      }
+    }
+    if (grp == 0) {
+      float* p = part + ((size_t)which * gridDim.x + blockIdx.x) * a.D;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = R::col(e / R::W, t) + e % R::W;
+        if (c < a.D) p[c] = acc[e];
+      }
+    }
+  }
+}
+
+// out[c] = sum over n blocks of part[.][c]: 32 columns a block, 32 rows at a time; blockIdx.y: dw, db.
+__global__ void __launch_bounds__(1024) k_norm_columns(const float* __restrict__ part, int n, int D, void* dw, void* db,
+                                                        bool wbf16) {
+  __shared__ float s[32][33];
+  void* out = blockIdx.y ? db : dw;
+  if (!out) return;
+  const float* p = part + (size_t)blockIdx.y * n * D;
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  float x = 0.f;
+  if (c < D)
+    for (int i = threadIdx.y; i < n; i += 32) x += p[(size_t)i * D + c];
+  s[threadIdx.y][threadIdx.x] = x;
+  __syncthreads();
+  x = s[threadIdx.x][threadIdx.y];  // one column a warp
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  const int col = blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && col < D) {
+    if (wbf16)
+      static_cast<bf16*>(out)[col] = __float2bfloat16_rn(x);
+    else
+      static_cast<float*>(out)[col] = x;
+  }
+}
+
+struct Call {
+  Args a;
+  const void *dy, *x, *w, *b;
+  void *y, *dx, *dw, *db;
+  float *mean, *rstd, *part;
+  bool backward;
+};
+
+// Blocks of the backward: two or four an SM of this GPU's 152, so that the loads of some cover the sums of others.
+// Narrow rows have the room for more.
+int backward_blocks(long long rows, int D) {
+  const long long groups = D <= 128 ? 16 : D <= 512 ? 8 : D <= 2048 ? 2 : 1;
+  const long long most = D <= 512 ? 608 : 304, want = (rows + groups - 1) / groups;
+  return (int)(want < most ? want : most);
+}
+
+template <typename T, int TPR, int E, bool kVec>
+void launch(const Call& c, cudaStream_t st) {
+  constexpr int kT = block_threads<TPR>(), kGroups = kT / TPR;
+  if (!c.backward) {
+    const unsigned grid = (unsigned)((c.a.rows + kGroups - 1) / kGroups);
+    SSD_LAUNCH("k_norm_forward", st,
+               k_norm_forward<T, TPR, E, kVec><<<grid, kT, 0, st>>>(c.a, (const T*)c.x, c.w, c.b, (T*)c.y, c.mean, c.rstd));
+    return;
+  }
+  const int nb = backward_blocks(c.a.rows, c.a.D);
+  SSD_LAUNCH("k_norm_backward", st,
+             k_norm_backward<T, TPR, E, kVec>
+             <<<nb, kT, 0, st>>>(c.a, (const T*)c.dy, (const T*)c.x, c.mean, c.rstd, c.w, (T*)c.dx, c.part));
+  if (c.part)
+    SSD_LAUNCH("k_norm_columns", st,
+               k_norm_columns<<<dim3((unsigned)((c.a.D + 31) / 32), 2), dim3(32, 32), 0, st>>>(c.part, nb, c.a.D, c.dw,
+                                                                                             c.db, c.a.wbf16));
+}
+
+// Threads a row and elements a thread: 16 elements (eight on narrow rows) leave the backward, which holds five values
+// for each, the registers for two blocks an SM; rows past 8192 take 32.
+template <typename T, bool kVec>
+void by_width(const Call& c, cudaStream_t st) {
+  const int D = c.a.D;
+  if (D <= 128)
+    launch<T, 16, 8, kVec>(c, st);
+  else if (D <= 256)
+    launch<T, 32, 8, kVec>(c, st);
+  else if (D <= 512)
+    launch<T, 32, 16, kVec>(c, st);
+  else if (D <= 1024)
+    launch<T, 128, 8, kVec>(c, st);
+  else if (D <= 2048)
+    launch<T, 128, 16, kVec>(c, st);
+  else if (D <= 4096)
+    launch<T, 256, 16, kVec>(c, st);
+  else if (D <= 8192)
+    launch<T, 512, 16, kVec>(c, st);
+  else
+    launch<T, 512, 32, kVec>(c, st);
+}
+void run(const Call& c, bool f32, cudaStream_t st) {
+  const int w = f32 ? 4 : 8;
+  const auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  const bool vec = c.a.D % w == 0 && c.a.xs % w == 0 && al(c.x);
+  if (f32)
+    vec ? by_width<float, true>(c, st) : by_width<float, false>(c, st);
+  else
+    vec ? by_width<bf16, true>(c, st) : by_width<bf16, false>(c, st);
+}
+
+ssd_status make(const ssd_norm_problem* p, Call* c, bool* f32) {
+  if (!p) return SSD_ERR_INVALID_ARG;
+  if ((p->io_dtype != SSD_F32 && p->io_dtype != SSD_BF16) || (p->weight_dtype != SSD_F32 && p->weight_dtype != SSD_BF16))
+    return SSD_ERR_INVALID_ARG;
+  if (p->rows < 1 || p->dim < 1 || p->x_stride < 0) return SSD_ERR_INVALID_ARG;
+  if (p->dim > 16384 || p->rows > 0x7fffffffll || (p->x_stride && p->x_stride < p->dim)) return SSD_ERR_SHAPE;
+  *c = Call{};
+  c->a.rows = p->rows;
+  c->a.D = (int)p->dim;
+  c->a.xs = p->x_stride ? p->x_stride : p->dim;
+  c->a.wbf16 = p->weight_dtype == SSD_BF16;
+  *f32 = p->io_dtype == SSD_F32;
+  return SSD_OK;
+}
+
+ssd_status check(std::initializer_list<const void*> req, std::initializer_list<const void*> opt) {
+  for (const void* p : req)
+    if (!p) return SSD_ERR_INVALID_ARG;
+  for (const void* p : req)
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return SSD_ERR_ALIGNMENT;
+  for (const void* p : opt)
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return SSD_ERR_ALIGNMENT;
+  return SSD_OK;
+}
+
+size_t workspace(const Call& c) {
+  Carver cv(nullptr);
+  cv.take<float>(2 * (size_t)backward_blocks(c.a.rows, c.a.D) * c.a.D);
+  return cv.off;
+}
+
+}  // namespace
+}  // namespace norm
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+ssd_status ssd_norm_workspace_size(const ssd_norm_problem* prob, size_t* bytes) {
+  if (!bytes) return SSD_ERR_INVALID_ARG;
+  norm::Call c;
+  bool f32;
+  const ssd_status s = norm::make(prob, &c, &f32);
+  if (s != SSD_OK) return s;
+  *bytes = norm::workspace(c);
+  return SSD_OK;
+}
+
+ssd_status ssd_norm_forward(const ssd_norm_problem* prob, const void* x, const void* weight, const void* bias, float eps,
+                            void* y, float* mean, float* rstd, void* cuda_stream) {
+  norm::Call c;
+  bool f32;
+  ssd_status s = norm::make(prob, &c, &f32);
+  if (s != SSD_OK) return s;
+  if ((s = norm::check({y}, {weight, bias, mean, rstd})) != SSD_OK) return s;
+  if (!x) return SSD_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(x) % (f32 ? 4 : 2)) return SSD_ERR_ALIGNMENT;
+  if (!(eps >= 0.f)) return SSD_ERR_INVALID_ARG;
+  c.a.eps = eps;
+  c.x = x;
+  c.w = weight;
+  c.b = bias;
+  c.y = y;
+  c.mean = mean;
+  c.rstd = rstd;
+  norm::run(c, f32, static_cast<cudaStream_t>(cuda_stream));
+  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status ssd_norm_backward(const ssd_norm_problem* prob, const void* dy, const void* x, const float* mean,
+                             const float* rstd, const void* weight, void* dx, void* dw, void* db, void* ws,
+                             size_t ws_bytes, void* cuda_stream) {
+  norm::Call c;
+  bool f32;
+  ssd_status s = norm::make(prob, &c, &f32);
+  if (s != SSD_OK) return s;
+  if ((s = norm::check({dy, mean, rstd, dx}, {weight, dw, db, ws})) != SSD_OK) return s;
+  if (!x) return SSD_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(x) % (f32 ? 4 : 2)) return SSD_ERR_ALIGNMENT;
+  if (dw || db) {
+    if (!ws) return SSD_ERR_INVALID_ARG;
+    if (ws_bytes < norm::workspace(c)) return SSD_ERR_WORKSPACE;
+    Carver cv(ws);
+    c.part = cv.take<float>(2 * (size_t)norm::backward_blocks(c.a.rows, c.a.D) * c.a.D);
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  c.dy = dy;
+  c.x = x;
+  c.mean = const_cast<float*>(mean);
+  c.rstd = const_cast<float*>(rstd);
+  c.w = weight;
+  c.dx = dx;
+  c.dw = dw;
+  c.db = db;
+  c.backward = true;
+  norm::run(c, f32, st);
+  return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+}  // extern "C"
