@@ -36,13 +36,13 @@ struct Table {
   int *start, *len, *chunk;
 };
 
-// One record per (chunk, value head), item = chunk * HV + head.
-struct Prep {
-  bf16* Thi;     // [item][64][64]: (I + A)^-1, rounded to bf16
-  bf16* Tlo;     // [item][64][64]: what that rounding left, rounded
-  bf16* P;       // [item][64][64]: e^{G_i - G_j} q_i . k_j (j <= i)
-  float* gates;  // [item][5][64]
-};
+// One record per (chunk, value head), item = chunk * HV + head, in one piece of memory that one bulk copy brings in:
+// four [64][64] bf16 tiles, swizzled as the tensor cores read them (element (i, j) at tile_off), and the decays.
+//   (I + A)^-1 rounded to bf16; what that rounding left, rounded; P_ij = e^{G_i - G_j} q_i . k_j (j <= i) in the same
+//   two parts (16-blocks above the diagonal are not written and not read); float [5][64] of kGateRows
+constexpr int kRecordGates = 4 * kC * kC * 2;
+constexpr int kRecordBytes = kRecordGates + kGateRows * kC * 4;
+__host__ __device__ constexpr int tile_off(int i, int j) { return i * 128 + (((j >> 3) ^ (i & 7)) << 4) + 2 * (j & 7); }
 
 // The sizes of a problem, or the error that it is refused with.
 ssd_status make_dims(const ssd_delta_problem* p, bool f32_ok, Dims* d);
@@ -53,6 +53,15 @@ struct In {
   const float* s0;
   float scale;
 };
+
+// The scans (ssd_delta_scan.cu).  S / R (null: not kept): the state entering each chunk and R, both bf16 and transposed
+// (S^T [VP][KP], R^T [VP][64]) and stored by 16-byte pieces of a row, [item][KP / 8][VP][8] and [item][8][VP][8], so that
+// the threads of neighbouring rows write neighbouring pieces.  o may be null (S and R only).  dS / dY of the reverse
+// scan: the gradient of the state leaving each chunk and dY, laid out like S and R.
+cudaError_t forward_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, bf16* o, float* s_final,
+                         bf16* S, bf16* R, int* status, cudaStream_t st);
+cudaError_t reverse_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const bf16* dout,
+                         const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status, cudaStream_t st);
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -79,16 +88,6 @@ __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t a) {
                : "r"(a)
                : "memory");
 }
-__device__ __forceinline__ void stm4(uint32_t a, const uint32_t (&r)[4]) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
-}
-__device__ __forceinline__ void stm4t(uint32_t a, const uint32_t (&r)[4]) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
-}
 
 // c[16x8] += a[16x16] b[16x8], bf16 operands, fp32 sums.
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -112,22 +111,7 @@ __device__ __forceinline__ void split(float x, float y, uint32_t& h, uint32_t& l
   l = pack(x - lo_f(h), y - hi_f(h));
 }
 
-// Two neighbouring accumulator tiles [16x8] as one left operand [16x16]: the layouts are the same, so a product's
-// result feeds the next product without leaving the registers.
-__device__ __forceinline__ void split_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&h)[4], uint32_t (&l)[4]) {
-  split(c0[0], c0[1], h[0], l[0]);
-  split(c0[2], c0[3], h[1], l[1]);
-  split(c1[0], c1[1], h[2], l[2]);
-  split(c1[2], c1[3], h[3], l[3]);
-}
-__device__ __forceinline__ void round_a(const float (&c0)[4], const float (&c1)[4], uint32_t (&h)[4]) {
-  h[0] = pack(c0[0], c0[1]);
-  h[1] = pack(c0[2], c0[3]);
-  h[2] = pack(c1[0], c1[1]);
-  h[3] = pack(c1[2], c1[3]);
-}
-
-// Lane addresses into a tile of rows of `pitch` elements, for ldm4 / ldm4t / stm4 / stm4t of 16 x 16 elements at
+// Lane addresses into a tile of rows of `pitch` elements, for ldm4 / ldm4t of 16 x 16 elements at
 // (row, col).  by_row: tiles in the order (rows 0-7, cols 0-7), (rows 0-7, cols 8-15), (rows 8-15, cols 0-7), ...;
 // by_col: (0-7, 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15).
 __device__ __forceinline__ uint32_t by_row(uint32_t base, int pitch, int row, int col, int lane) {
@@ -158,13 +142,13 @@ __device__ __forceinline__ void load_rows(bf16* dst, int pitch, int width, const
   }
 }
 
-// `n16` 16-byte pieces of consecutive rows of `w8` pieces into a tile.
-__device__ __forceinline__ void load_dense(bf16* dst, int pitch, int w8, const bf16* src, int rows, int tid,
-                                           int nthreads) {
+// Rows of `w8` 16-byte pieces, stored piece by piece ([w8][rows][8]), into a tile of rows.
+__device__ __forceinline__ void load_pieces(bf16* dst, int pitch, int w8, const bf16* src, int rows, int tid,
+                                            int nthreads) {
   const uint32_t d = su32(dst);
   for (int i = tid; i < rows * w8; i += nthreads) {
-    const int r = i / w8, c = (i - r * w8) << 3;
-    cp16(d + 2u * (uint32_t)(r * pitch + c), src + (size_t)i * 8, true);
+    const int j = i / rows, r = i - j * rows;
+    cp16(d + 2u * (uint32_t)(r * pitch + 8 * j), src + (size_t)i * 8, true);
   }
 }
 

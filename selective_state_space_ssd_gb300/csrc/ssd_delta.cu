@@ -141,12 +141,12 @@ __device__ __forceinline__ void put16(float* dst, const float (&c)[2][4], float 
 // forward substitution (a lane a column), then twice the block rule  [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']].
 // Substitution and block products stay small for strongly correlated keys, where a series in powers of A would not.
 template <int KP>
-__global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, Prep pr, int* status) {
+__global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, uint8_t* records, int* status) {
   constexpr int kP = KP + 8;
   extern __shared__ __align__(16) unsigned char smem[];
   bf16* Ks = reinterpret_cast<bf16*>(smem);
   bf16* Qs = Ks + kC * kP;
-  float* Af = reinterpret_cast<float*>(Qs + kC * kP);
+  float* Af = reinterpret_cast<float*>(smem);  // over K and Q, once their products are in registers
   float* Tf = Af + kC * kFP;
   float* Mf = Tf + kC * kFP;  // [32][kFP]
   __shared__ float s_hi[kC], s_lo[kC], s_beta[kC];
@@ -158,7 +158,6 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, Pre
   load_rows(Ks, kP, KP, in.k + (long long)ch.first * d.ks + (long long)hk * d.K, d.ks, ch.rows, d.K, d.kvec, tid, 128);
   load_rows(Qs, kP, KP, in.q + (long long)ch.first * d.qs + (long long)hk * d.K, d.qs, ch.rows, d.K, d.qvec, tid, 128);
   cp_commit();
-  for (int i = tid; i < kC * kFP; i += 128) Tf[i] = 0.f;
   cp_wait<0>();
   __syncthreads();
   const int r0 = 16 * w, g4 = lane >> 2, t2 = 2 * (lane & 3);
@@ -184,9 +183,11 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, Pre
       mma(qk[2 * jb + 1], aq, b[2], b[3]);
     }
   }
+  __syncthreads();
+  for (int i = tid; i < kC * kFP; i += 128) Tf[i] = 0.f;
   for (int gi = 0; gi < d.G; ++gi) {
     const int hv = hk * d.G + gi;
-    const size_t item = (size_t)c * d.HV + hv;
+    uint8_t* record = records + ((size_t)c * d.HV + hv) * kRecordBytes;
     if (w == 0) {  // G of two steps a lane; the sums in fp64, kept as a high and a low fp32 part
       double x[2];
 #pragma unroll
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, Pre
         if (lane >= o) sum += y;
       }
       const double end = __shfl_sync(0xffffffffu, sum, 31);
-      float* gr = pr.gates + item * (kGateRows * kC);
+      float* gr = reinterpret_cast<float*>(record + kRecordGates);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
@@ -225,7 +226,6 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, Pre
       }
     }
     __syncthreads();
-    uint32_t* P32 = reinterpret_cast<uint32_t*>(pr.P + item * (kC * kC));
 #pragma unroll
     for (int nt = 0; nt < 8; ++nt) {
       if (nt > 2 * w + 1) break;
@@ -241,7 +241,10 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, Pre
         }
         Af[i * kFP + j] = a[0];
         Af[i * kFP + j + 1] = a[1];
-        P32[(i * kC + j) >> 1] = pack(p[0], p[1]);
+        uint32_t ph, pl;
+        split(p[0], p[1], ph, pl);
+        *reinterpret_cast<uint32_t*>(record + 2 * 8192 + tile_off(i, j)) = ph;
+        *reinterpret_cast<uint32_t*>(record + 3 * 8192 + tile_off(i, j)) = pl;
       }
     }
     __syncwarp();
@@ -276,469 +279,18 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, Pre
     __syncthreads();
     {
       const int i = tid >> 1, j0 = 32 * (tid & 1);
-      uint4* dh = reinterpret_cast<uint4*>(pr.Thi + item * (kC * kC) + i * kC + j0);
-      uint4* dl = reinterpret_cast<uint4*>(pr.Tlo + item * (kC * kC) + i * kC + j0);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t h[4], l[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           split(Tf[i * kFP + j0 + 8 * q + 2 * e], Tf[i * kFP + j0 + 8 * q + 2 * e + 1], h[e], l[e]);
-        dh[q] = make_uint4(h[0], h[1], h[2], h[3]);
-        dl[q] = make_uint4(l[0], l[1], l[2], l[3]);
+        *reinterpret_cast<uint4*>(record + tile_off(i, j0 + 8 * q)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(record + 8192 + tile_off(i, j0 + 8 * q)) = make_uint4(l[0], l[1], l[2], l[3]);
       }
     }
     __syncthreads();
   }
-}
-
-// ---------------------------------------------------------------- the scans
-// Shared memory of one stage of a scan: K, Q, V (or dO), T high and low, P, the decays.
-template <int KP>
-struct Stage {
-  bf16 *K, *Q, *V, *Th, *Tl, *P;
-  float* gates;
-  static __host__ __device__ size_t bytes(int nw) {
-    return 2 * (size_t)(2 * kC * (KP + 8) + kC * (16 * nw + 8) + 3 * kC * kTP) + sizeof(float) * 3 * kC;
-  }
-  __device__ Stage(unsigned char* base, int nw) {
-    K = reinterpret_cast<bf16*>(base);
-    Q = K + kC * (KP + 8);
-    V = Q + kC * (KP + 8);
-    Th = V + kC * (16 * nw + 8);
-    Tl = Th + kC * kTP;
-    P = Tl + kC * kTP;
-    gates = reinterpret_cast<float*>(P + kC * kTP);
-  }
-};
-
-// `v`: the tensor whose columns the block's warps own (V forward, dO in reverse), `stride` elements from step to step.
-template <int KP>
-__device__ __forceinline__ void load_stage(const Stage<KP>& s, const Dims& d, const In& in, const Prep& pr,
-                                           const bf16* v, long long stride, bool vvec, int first, int rows, int hk,
-                                           int hv, size_t item, int v0, int nw) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  load_rows(s.K, KP + 8, KP, in.k + (long long)first * d.ks + (long long)hk * d.K, d.ks, rows, d.K, d.kvec, tid, nt);
-  load_rows(s.Q, KP + 8, KP, in.q + (long long)first * d.qs + (long long)hk * d.K, d.qs, rows, d.K, d.qvec, tid, nt);
-  load_rows(s.V, 16 * nw + 8, 16 * nw, v + (long long)first * stride + (long long)hv * d.V + v0, stride, rows,
-            d.V - v0, vvec, tid, nt);
-  load_dense(s.Th, kTP, kC / 8, pr.Thi + item * (kC * kC), kC, tid, nt);
-  load_dense(s.Tl, kTP, kC / 8, pr.Tlo + item * (kC * kC), kC, tid, nt);
-  load_dense(s.P, kTP, kC / 8, pr.P + item * (kC * kC), kC, tid, nt);
-  for (int i = tid; i < 3 * kC / 4; i += nt)
-    cp16(su32(s.gates + 4 * i), pr.gates + item * (kGateRows * kC) + 4 * i, true);
-}
-
-// The warp's 16 columns of a [64][..] tile in shared memory to rows of a tensor: row r to dst + r * stride.
-__device__ __forceinline__ void store_cols(const bf16* tile, int pitch, bf16* dst, long long stride, int rows, int cols,
-                                           bool vec, int lane) {
-  if (vec) {
-    const int c = 8 * (lane & 1);
-    if (c < cols)
-#pragma unroll
-      for (int r = lane >> 1; r < kC; r += 16)
-        if (r < rows)
-          *reinterpret_cast<uint4*>(dst + (long long)r * stride + c) =
-              *reinterpret_cast<const uint4*>(tile + r * pitch + c);
-  } else {
-    const int c = lane & 15;
-    if (c < cols)
-      for (int r = lane >> 4; r < rows; r += 2) dst[(long long)r * stride + c] = tile[r * pitch + c];
-  }
-}
-
-// The transposed accumulators [16 v][64 t] as bf16 into the warp's columns of a [64 t][v] tile.
-__device__ __forceinline__ void stage_t(bf16* tile, int pitch, const float (&x)[8][4], int lane) {
-#pragma unroll
-  for (int tb = 0; tb < 4; ++tb) {
-    uint32_t r[4];
-    round_a(x[2 * tb], x[2 * tb + 1], r);
-    stm4t(by_row(su32(tile), pitch, 16 * tb, 0, lane), r);
-  }
-}
-
-// The state accumulators [16 v][KP] as bf16 rows of dst (pitch KP), through a warp's own [16][KP + 8] buffer.
-template <int KP>
-__device__ __forceinline__ void store_state(bf16* buf, bf16* dst, const float (&S)[KP / 8][4], int lane) {
-  constexpr int kP = KP + 8;
-#pragma unroll
-  for (int kb = 0; kb < KP / 16; ++kb) {
-    uint32_t r[4];
-    round_a(S[2 * kb], S[2 * kb + 1], r);
-    stm4(by_col(su32(buf), kP, 0, 16 * kb, lane), r);
-  }
-  __syncwarp();
-#pragma unroll
-  for (int i = lane; i < 2 * KP; i += 32) {
-    const int r = i / (KP / 8), c = 8 * (i % (KP / 8));
-    *reinterpret_cast<uint4*>(dst + (size_t)r * KP + c) = *reinterpret_cast<const uint4*>(buf + r * kP + c);
-  }
-  __syncwarp();
-}
-
-// s [K, V] (fp32, row-major) to and from the accumulators of rows v0 .. v0 + 15 of its transpose.
-template <int KP>
-__device__ __forceinline__ void read_state(float (&S)[KP / 8][4], const float* s, int K, int V, int v0, int lane) {
-#pragma unroll
-  for (int nt = 0; nt < KP / 8; ++nt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = 8 * nt + 2 * (lane & 3) + (j & 1), v = v0 + (lane >> 2) + 8 * (j >> 1);
-      S[nt][j] = s && k < K && v < V ? s[(size_t)k * V + v] : 0.f;
-    }
-}
-template <int KP>
-__device__ __forceinline__ void write_state(float* s, const float (&S)[KP / 8][4], int K, int V, int v0, int lane) {
-#pragma unroll
-  for (int nt = 0; nt < KP / 8; ++nt)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = 8 * nt + 2 * (lane & 3) + (j & 1), v = v0 + (lane >> 2) + 8 * (j >> 1);
-      if (k < K && v < V) s[(size_t)k * V + v] = S[nt][j];
-    }
-}
-
-// One block of nw warps per (sequence, value head, 16 nw columns of V); two stages of tiles, the next chunk's copies in
-// flight while a chunk is computed.  Sout / Rout (either may be null): the state entering each chunk, bf16
-// [item][VP][KP], and R, bf16 [item][64][VP].
-template <int KP>
-__global__ void __launch_bounds__(256, 1)
-    k_delta_scan(Dims d, Table tb, In in, Prep pr, bf16* o, float* s_final, bf16* Sout, bf16* Rout) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int nw = blockDim.x >> 5, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int n = blockIdx.x / d.HV, hv = blockIdx.x - n * d.HV, hk = hv / d.G;
-  const int vb = 16 * nw * blockIdx.y, v0 = vb + 16 * w;  // the block's and the warp's first column
-  const bool live = v0 < d.VP;
-  const size_t sb = Stage<KP>::bytes(nw);
-  bf16* sbuf = reinterpret_cast<bf16*>(smem + 2 * sb) + w * 16 * (KP + 8);
-  const int vp = 16 * nw + 8;
-  const Seq sq = sequence(d, tb, n);
-  const size_t su = ((size_t)n * d.HV + hv) * d.K * d.V;
-  float S[KP / 8][4];
-  read_state<KP>(S, in.s0 ? in.s0 + su : nullptr, d.K, d.V, v0, lane);
-  if (sq.nc > 0) {
-    load_stage<KP>(Stage<KP>(smem + (0) * sb, nw), d, in, pr, in.v, d.vs, d.vvec, sq.start, min(kC, sq.len), hk, hv,
-                   (size_t)sq.chunk * d.HV + hv, vb, nw);
-  }
-  cp_commit();
-  const int t2 = 2 * (lane & 3);
-  for (int c = 0; c < sq.nc; ++c) {
-    const Stage<KP> cur(smem + (c & 1) * sb, nw);
-    const size_t item = (size_t)(sq.chunk + c) * d.HV + hv;
-    const int first = sq.start + c * kC, rows = min(kC, sq.len - c * kC);
-    if (c + 1 < sq.nc)
-      load_stage<KP>(Stage<KP>(smem + ((c + 1) & 1) * sb, nw), d, in, pr, in.v, d.vs, d.vvec, first + kC, min(kC, sq.len - (c + 1) * kC), hk,
-                     hv, item + d.HV, vb, nw);
-    cp_commit();
-    cp_wait<1>();
-    __syncthreads();
-    if (live) {
-      if (Sout) store_state<KP>(sbuf, Sout + (item * d.VP + v0) * KP, S, lane);
-      const float *eg = cur.gates, *ee = cur.gates + kC, *be = cur.gates + 2 * kC;
-      const uint32_t ka = su32(cur.K), qa = su32(cur.Q);
-      float X[8][4], O[8][4];  // (K S)^T, (Q S)^T: [16 v][64 t]
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) X[i][j] = O[i][j] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < KP / 16; ++kb) {
-        uint32_t h[4], l[4];
-        split_a(S[2 * kb], S[2 * kb + 1], h, l);
-#pragma unroll
-        for (int tb4 = 0; tb4 < 4; ++tb4) {
-          uint32_t b[4];
-          ldm4(b, by_row(ka, KP + 8, 16 * tb4, 16 * kb, lane));
-          mma(X[2 * tb4], h, b[0], b[1]);
-          mma(X[2 * tb4 + 1], h, b[2], b[3]);
-          mma(X[2 * tb4], l, b[0], b[1]);
-          mma(X[2 * tb4 + 1], l, b[2], b[3]);
-          if (o) {
-            ldm4(b, by_row(qa, KP + 8, 16 * tb4, 16 * kb, lane));
-            mma(O[2 * tb4], h, b[0], b[1]);
-            mma(O[2 * tb4 + 1], h, b[2], b[3]);
-            mma(O[2 * tb4], l, b[0], b[1]);
-            mma(O[2 * tb4 + 1], l, b[2], b[3]);
-          }
-        }
-      }
-      uint32_t yh[4][4], yl[4][4];
-      const uint32_t va = su32(cur.V) + 2u * (uint32_t)(16 * w);
-#pragma unroll
-      for (int tb4 = 0; tb4 < 4; ++tb4) {
-        uint32_t v[4];
-        ldm4t(v, by_row(va, vp, 16 * tb4, 0, lane));
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float(&x)[4] = X[2 * tb4 + half];
-          const int t = 16 * tb4 + 8 * half + t2;
-          const float2 e = *reinterpret_cast<const float2*>(eg + t), b = *reinterpret_cast<const float2*>(be + t);
-          x[0] = b.x * fmaf(-e.x, x[0], lo_f(v[2 * half]));
-          x[1] = b.y * fmaf(-e.y, x[1], hi_f(v[2 * half]));
-          x[2] = b.x * fmaf(-e.x, x[2], lo_f(v[2 * half + 1]));
-          x[3] = b.y * fmaf(-e.y, x[3], hi_f(v[2 * half + 1]));
-          float(&oo)[4] = O[2 * tb4 + half];
-          oo[0] *= e.x;
-          oo[1] *= e.y;
-          oo[2] *= e.x;
-          oo[3] *= e.y;
-        }
-        split_a(X[2 * tb4], X[2 * tb4 + 1], yh[tb4], yl[tb4]);
-      }
-      // R^T = Y^T T^T: step i takes from the steps j <= i
-      float(&R)[8][4] = X;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) R[i][j] = 0.f;
-      const uint32_t th = su32(cur.Th), tl = su32(cur.Tl), pa = su32(cur.P);
-#pragma unroll
-      for (int jb = 0; jb < 4; ++jb)
-#pragma unroll
-        for (int ib = jb; ib < 4; ++ib) {
-          uint32_t b[4];
-          ldm4(b, by_row(th, kTP, 16 * ib, 16 * jb, lane));
-          mma(R[2 * ib], yh[jb], b[0], b[1]);
-          mma(R[2 * ib + 1], yh[jb], b[2], b[3]);
-          mma(R[2 * ib], yl[jb], b[0], b[1]);
-          mma(R[2 * ib + 1], yl[jb], b[2], b[3]);
-          ldm4(b, by_row(tl, kTP, 16 * ib, 16 * jb, lane));
-          mma(R[2 * ib], yh[jb], b[0], b[1]);
-          mma(R[2 * ib + 1], yh[jb], b[2], b[3]);
-        }
-      bf16* own = cur.V + 16 * w;  // the warp's columns of the V tile, which only it reads: staging for R and o
-      if (Rout) {
-        __syncwarp();
-        stage_t(own, vp, R, lane);
-        __syncwarp();
-        store_cols(own, vp, Rout + item * kC * d.VP + v0, d.VP, kC, 16, true, lane);
-      }
-      if (o) {
-#pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-          uint32_t h[4], l[4];
-          split_a(R[2 * jb], R[2 * jb + 1], h, l);
-#pragma unroll
-          for (int ib = jb; ib < 4; ++ib) {
-            uint32_t b[4];
-            ldm4(b, by_row(pa, kTP, 16 * ib, 16 * jb, lane));
-            mma(O[2 * ib], h, b[0], b[1]);
-            mma(O[2 * ib + 1], h, b[2], b[3]);
-            mma(O[2 * ib], l, b[0], b[1]);
-            mma(O[2 * ib + 1], l, b[2], b[3]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) O[i][j] *= in.scale;
-        __syncwarp();
-        stage_t(own, vp, O, lane);
-        __syncwarp();
-        store_cols(own, vp, o + ((long long)first * d.HV + hv) * d.V + v0, (long long)d.HV * d.V, rows, d.V - v0,
-                   d.ovec, lane);
-      }
-      // S' = e^{G_end} S + K^T (e^{G_end - G} R)
-      const float keep = eg[kC - 1];
-#pragma unroll
-      for (int i = 0; i < KP / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) S[i][j] *= keep;
-#pragma unroll
-      for (int tb4 = 0; tb4 < 4; ++tb4) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float(&x)[4] = R[2 * tb4 + half];
-          const float2 e = *reinterpret_cast<const float2*>(ee + 16 * tb4 + 8 * half + t2);
-          x[0] *= e.x;
-          x[1] *= e.y;
-          x[2] *= e.x;
-          x[3] *= e.y;
-        }
-        uint32_t h[4], l[4];
-        split_a(R[2 * tb4], R[2 * tb4 + 1], h, l);
-#pragma unroll
-        for (int kb = 0; kb < KP / 16; ++kb) {
-          uint32_t b[4];
-          ldm4t(b, by_col(ka, KP + 8, 16 * tb4, 16 * kb, lane));
-          mma(S[2 * kb], h, b[0], b[1]);
-          mma(S[2 * kb + 1], h, b[2], b[3]);
-          mma(S[2 * kb], l, b[0], b[1]);
-          mma(S[2 * kb + 1], l, b[2], b[3]);
-        }
-      }
-    }
-    __syncthreads();
-  }
-  if (live && s_final) write_state<KP>(s_final + su, S, d.K, d.V, v0, lane);
-}
-
-// The reverse scan: dS^T [16 v][KP] a warp.  dSout: the gradient of the state leaving each chunk, bf16 [item][VP][KP];
-// dYout: bf16 [item][64][VP].
-template <int KP>
-__global__ void __launch_bounds__(256, 1) k_delta_rev(Dims d, Table tb, In in, Prep pr, const bf16* dout,
-                                                       bool dovec, const float* ds_final, bf16* dv, float* ds0,
-                                                       bf16* dSout, bf16* dYout) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int nw = blockDim.x >> 5, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int n = blockIdx.x / d.HV, hv = blockIdx.x - n * d.HV, hk = hv / d.G;
-  const int vb = 16 * nw * blockIdx.y, v0 = vb + 16 * w;
-  const bool live = v0 < d.VP;
-  const size_t sb = Stage<KP>::bytes(nw);
-  bf16* sbuf = reinterpret_cast<bf16*>(smem + 2 * sb) + w * 16 * (KP + 8);
-  const int vp = 16 * nw + 8;
-  const long long os = (long long)d.HV * d.V;
-  const Seq sq = sequence(d, tb, n);
-  const size_t su = ((size_t)n * d.HV + hv) * d.K * d.V;
-  float S[KP / 8][4];
-  read_state<KP>(S, ds_final ? ds_final + su : nullptr, d.K, d.V, v0, lane);
-  if (sq.nc > 0) {
-    const int c = sq.nc - 1;
-    load_stage<KP>(Stage<KP>(smem + (c & 1) * sb, nw), d, in, pr, dout, os, dovec, sq.start + c * kC, sq.len - c * kC, hk, hv,
-                   (size_t)(sq.chunk + c) * d.HV + hv, vb, nw);
-  }
-  cp_commit();
-  const int t2 = 2 * (lane & 3);
-  for (int c = sq.nc - 1; c >= 0; --c) {
-    const Stage<KP> cur(smem + (c & 1) * sb, nw);
-    const size_t item = (size_t)(sq.chunk + c) * d.HV + hv;
-    const int first = sq.start + c * kC, rows = min(kC, sq.len - c * kC);
-    if (c > 0)
-      load_stage<KP>(Stage<KP>(smem + ((c - 1) & 1) * sb, nw), d, in, pr, dout, os, dovec, first - kC, kC, hk, hv, item - d.HV, vb, nw);
-    cp_commit();
-    cp_wait<1>();
-    __syncthreads();
-    if (live) {
-      store_state<KP>(sbuf, dSout + (item * d.VP + v0) * KP, S, lane);
-      const float *eg = cur.gates, *ee = cur.gates + kC, *be = cur.gates + 2 * kC;
-      const uint32_t ka = su32(cur.K), qa = su32(cur.Q), th = su32(cur.Th), tl = su32(cur.Tl), pa = su32(cur.P);
-      const uint32_t da = su32(cur.V) + 2u * (uint32_t)(16 * w);
-      float X[8][4], U[8][4];  // (K dS')^T and (P^T dO)^T: [16 v][64 t]
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) X[i][j] = U[i][j] = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < KP / 16; ++kb) {
-        uint32_t h[4], l[4];
-        split_a(S[2 * kb], S[2 * kb + 1], h, l);
-#pragma unroll
-        for (int tb4 = 0; tb4 < 4; ++tb4) {
-          uint32_t b[4];
-          ldm4(b, by_row(ka, KP + 8, 16 * tb4, 16 * kb, lane));
-          mma(X[2 * tb4], h, b[0], b[1]);
-          mma(X[2 * tb4 + 1], h, b[2], b[3]);
-          mma(X[2 * tb4], l, b[0], b[1]);
-          mma(X[2 * tb4 + 1], l, b[2], b[3]);
-        }
-      }
-#pragma unroll
-      for (int ib = 0; ib < 4; ++ib) {
-        uint32_t a[4];
-        ldm4t(a, by_row(da, vp, 16 * ib, 0, lane));  // dO^T: rows v, columns i
-#pragma unroll
-        for (int tb4 = 0; tb4 <= ib; ++tb4) {
-          uint32_t b[4];
-          ldm4t(b, by_col(pa, kTP, 16 * ib, 16 * tb4, lane));
-          mma(U[2 * tb4], a, b[0], b[1]);
-          mma(U[2 * tb4 + 1], a, b[2], b[3]);
-        }
-      }
-      uint32_t rh[4][4], rl[4][4];  // dR
-#pragma unroll
-      for (int tb4 = 0; tb4 < 4; ++tb4) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float2 e = *reinterpret_cast<const float2*>(ee + 16 * tb4 + 8 * half + t2);
-          float(&x)[4] = X[2 * tb4 + half];
-          const float(&u)[4] = U[2 * tb4 + half];
-          x[0] = fmaf(in.scale, u[0], e.x * x[0]);
-          x[1] = fmaf(in.scale, u[1], e.y * x[1]);
-          x[2] = fmaf(in.scale, u[2], e.x * x[2]);
-          x[3] = fmaf(in.scale, u[3], e.y * x[3]);
-        }
-        split_a(X[2 * tb4], X[2 * tb4 + 1], rh[tb4], rl[tb4]);
-      }
-      // dY^T = dR^T T: step t takes from the steps i >= t
-      float(&Y)[8][4] = X;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) Y[i][j] = 0.f;
-#pragma unroll
-      for (int ib = 0; ib < 4; ++ib)
-#pragma unroll
-        for (int tb4 = 0; tb4 <= ib; ++tb4) {
-          uint32_t b[4];
-          ldm4t(b, by_col(th, kTP, 16 * ib, 16 * tb4, lane));
-          mma(Y[2 * tb4], rh[ib], b[0], b[1]);
-          mma(Y[2 * tb4 + 1], rh[ib], b[2], b[3]);
-          mma(Y[2 * tb4], rl[ib], b[0], b[1]);
-          mma(Y[2 * tb4 + 1], rl[ib], b[2], b[3]);
-          ldm4t(b, by_col(tl, kTP, 16 * ib, 16 * tb4, lane));
-          mma(Y[2 * tb4], rh[ib], b[0], b[1]);
-          mma(Y[2 * tb4 + 1], rh[ib], b[2], b[3]);
-        }
-      const float keep = eg[kC - 1];
-#pragma unroll
-      for (int i = 0; i < KP / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) S[i][j] *= keep;
-#pragma unroll
-      for (int tb4 = 0; tb4 < 4; ++tb4) {
-        uint32_t a[4], h[4], l[4], xh[4], xl[4];
-        ldm4t(a, by_row(da, vp, 16 * tb4, 0, lane));
-        float dx[2][4];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int t = 16 * tb4 + 8 * half + t2;
-          const float2 e = *reinterpret_cast<const float2*>(eg + t), b = *reinterpret_cast<const float2*>(be + t);
-          const float f0 = in.scale * e.x, f1 = in.scale * e.y;
-          split(f0 * lo_f(a[2 * half]), f1 * hi_f(a[2 * half]), h[2 * half], l[2 * half]);
-          split(f0 * lo_f(a[2 * half + 1]), f1 * hi_f(a[2 * half + 1]), h[2 * half + 1], l[2 * half + 1]);
-          const float(&y)[4] = Y[2 * tb4 + half];
-          dx[half][0] = -b.x * e.x * y[0];
-          dx[half][1] = -b.y * e.y * y[1];
-          dx[half][2] = -b.x * e.x * y[2];
-          dx[half][3] = -b.y * e.y * y[3];
-        }
-        split_a(dx[0], dx[1], xh, xl);
-#pragma unroll
-        for (int kb = 0; kb < KP / 16; ++kb) {
-          uint32_t b[4];
-          ldm4t(b, by_col(qa, KP + 8, 16 * tb4, 16 * kb, lane));
-          mma(S[2 * kb], h, b[0], b[1]);
-          mma(S[2 * kb + 1], h, b[2], b[3]);
-          mma(S[2 * kb], l, b[0], b[1]);
-          mma(S[2 * kb + 1], l, b[2], b[3]);
-          ldm4t(b, by_col(ka, KP + 8, 16 * tb4, 16 * kb, lane));
-          mma(S[2 * kb], xh, b[0], b[1]);
-          mma(S[2 * kb + 1], xh, b[2], b[3]);
-          mma(S[2 * kb], xl, b[0], b[1]);
-          mma(S[2 * kb + 1], xl, b[2], b[3]);
-        }
-      }
-      bf16* own = cur.V + 16 * w;  // dO has been read for the last time: staging for dY and dV
-      __syncwarp();
-      stage_t(own, vp, Y, lane);
-      __syncwarp();
-      store_cols(own, vp, dYout + item * kC * d.VP + v0, d.VP, kC, 16, true, lane);
-#pragma unroll
-      for (int nt = 0; nt < 8; ++nt) {
-        const float2 b = *reinterpret_cast<const float2*>(be + 8 * nt + t2);
-        Y[nt][0] *= b.x;
-        Y[nt][1] *= b.y;
-        Y[nt][2] *= b.x;
-        Y[nt][3] *= b.y;
-      }
-      __syncwarp();
-      stage_t(own, vp, Y, lane);
-      __syncwarp();
-      store_cols(own, vp, dv + ((long long)first * d.HV + hv) * d.V + v0, os, rows, d.V - v0, d.ovec, lane);
-    }
-    __syncthreads();
-  }
-  if (live && ds0) write_state<KP>(ds0 + su, S, d.K, d.V, v0, lane);
 }
 
 // ---------------------------------------------------------------- dQ, dK, dbeta, dg of a chunk
@@ -761,7 +313,7 @@ __device__ __forceinline__ float quad_sum(float x) {
 
 template <int KP>
 size_t grads_smem(int VP) {
-  return 2 * (size_t)(2 * kC * (KP + 8) + 3 * kC * (VP + 8) + 2 * VP * (KP + 8) + 2 * kC * kTP) +
+  return 2 * (size_t)(2 * kC * (KP + 8) + kC * (VP + 8) + 2 * VP * kTP + 2 * VP * (KP + 8) + 2 * kC * kTP) +
          sizeof(float) * kGateRows * kC;
 }
 
@@ -769,7 +321,7 @@ size_t grads_smem(int VP) {
 // half w / 4 of the columns of every product, and dQ, dK of the head stay in its accumulators (so the sum over the
 // value heads has one order).  Every factor of a decay is applied in fp32 to a product's result.
 template <int KP>
-__global__ void __launch_bounds__(256, 1) k_delta_grads(Dims d, Table tb, In in, Prep pr, const bf16* __restrict__ dout,
+__global__ void __launch_bounds__(256, 1) k_delta_grads(Dims d, Table tb, In in, const uint8_t* records, const bf16* __restrict__ dout,
                                                          bool dovec, const bf16* __restrict__ Sst,
                                                          const bf16* __restrict__ Rst, const bf16* __restrict__ dSst,
                                                          const bf16* __restrict__ dYst, GradOut out) {
@@ -779,9 +331,9 @@ __global__ void __launch_bounds__(256, 1) k_delta_grads(Dims d, Table tb, In in,
   bf16* Ks = reinterpret_cast<bf16*>(smem);
   bf16* Qs = Ks + kC * kP;
   bf16* Os = Qs + kC * kP;   // dO
-  bf16* Rs = Os + kC * vp;
-  bf16* Ys = Rs + kC * vp;   // dY
-  bf16* Ss = Ys + kC * vp;   // S^T [VP][KP]
+  bf16* Rs = Os + kC * vp;   // R^T [VP][64]
+  bf16* Ys = Rs + VP * kTP;  // dY^T
+  bf16* Ss = Ys + VP * kTP;  // S^T [VP][KP]
   bf16* Ds = Ss + VP * kP;   // dS'^T
   bf16* B1 = Ds + VP * kP;   // scale dO R^T . decay
   bf16* B2 = B1 + kC * kTP;  // -dY R^T . beta decay
@@ -812,12 +364,12 @@ __global__ void __launch_bounds__(256, 1) k_delta_grads(Dims d, Table tb, In in,
     const size_t item = (size_t)c * d.HV + hv;
     load_rows(Os, vp, VP, dout + ((long long)ch.first * d.HV + hv) * d.V, (long long)d.HV * d.V, ch.rows, d.V, dovec,
               tid, 256);
-    load_dense(Rs, vp, VP / 8, Rst + item * kC * VP, kC, tid, 256);
-    load_dense(Ys, vp, VP / 8, dYst + item * kC * VP, kC, tid, 256);
-    load_dense(Ss, kP, KP / 8, Sst + item * VP * KP, VP, tid, 256);
-    load_dense(Ds, kP, KP / 8, dSst + item * VP * KP, VP, tid, 256);
+    load_pieces(Rs, kTP, kC / 8, Rst + item * kC * VP, VP, tid, 256);
+    load_pieces(Ys, kTP, kC / 8, dYst + item * kC * VP, VP, tid, 256);
+    load_pieces(Ss, kP, KP / 8, Sst + item * VP * KP, VP, tid, 256);
+    load_pieces(Ds, kP, KP / 8, dSst + item * VP * KP, VP, tid, 256);
     for (int i = tid; i < kGateRows * kC / 4; i += 256)
-      cp16(su32(gt + 4 * i), pr.gates + item * (kGateRows * kC) + 4 * i, true);
+      cp16(su32(gt + 4 * i), records + item * kRecordBytes + kRecordGates + 16 * i, true);
     cp_commit();
     cp_wait<0>();
     __syncthreads();
@@ -849,11 +401,11 @@ __global__ void __launch_bounds__(256, 1) k_delta_grads(Dims d, Table tb, In in,
       for (int vb = 0; vb < VP; vb += 16) {
         uint32_t ao[4], ay[4];
         ldm4(ao, by_col(oa, vp, r0, vb, lane));
-        ldm4(ay, by_col(ya, vp, r0, vb, lane));
+        ldm4t(ay, by_row(ya, kTP, vb, r0, lane));
 #pragma unroll
         for (int jb = 0; jb < 2; ++jb) {
           uint32_t b[4];
-          ldm4(b, by_row(ra, vp, 32 * half + 16 * jb, vb, lane));
+          ldm4t(b, by_col(ra, kTP, vb, 32 * half + 16 * jb, lane));
           mma(m1[2 * jb], ao, b[0], b[1]);
           mma(m1[2 * jb + 1], ao, b[2], b[3]);
           mma(m2[2 * jb], ay, b[0], b[1]);
@@ -916,7 +468,10 @@ __global__ void __launch_bounds__(256, 1) k_delta_grads(Dims d, Table tb, In in,
         for (int j = 0; j < 4; ++j) z[i][j] = 0.f;
       for (int vb = 0; vb < VP; vb += 16) {
         uint32_t a[4];
-        ldm4(a, by_col(aa, vp, r0, vb, lane));
+        if (pass == 0)
+          ldm4(a, by_col(aa, vp, r0, vb, lane));
+        else
+          ldm4t(a, by_row(aa, kTP, vb, r0, lane));
 #pragma unroll
         for (int nb = 0; nb < kNT / 2; ++nb) {
           uint32_t b[4];
@@ -973,11 +528,11 @@ __global__ void __launch_bounds__(256, 1) k_delta_grads(Dims d, Table tb, In in,
               a[j] = pack(i + 2 * j < d.V ? __bfloat162float(vr[i + 2 * j]) : 0.f,
                           i + 2 * j + 1 < d.V ? __bfloat162float(vr[i + 2 * j + 1]) : 0.f);
           }
-          const uint4 b = *reinterpret_cast<const uint4*>(Ys + t * vp + i);
-          x = fmaf(lo_f(a[0]), lo_f(b.x), fmaf(hi_f(a[0]), hi_f(b.x), x));
-          x = fmaf(lo_f(a[1]), lo_f(b.y), fmaf(hi_f(a[1]), hi_f(b.y), x));
-          x = fmaf(lo_f(a[2]), lo_f(b.z), fmaf(hi_f(a[2]), hi_f(b.z), x));
-          x = fmaf(lo_f(a[3]), lo_f(b.w), fmaf(hi_f(a[3]), hi_f(b.w), x));
+          const bf16* y = Ys + i * kTP + t;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x = fmaf(lo_f(a[j]), __bfloat162float(y[2 * j * kTP]),
+                     fmaf(hi_f(a[j]), __bfloat162float(y[(2 * j + 1) * kTP]), x));
         }
       }
       x = quad_sum(x);
@@ -1083,22 +638,14 @@ bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // What a training forward keeps for its backward, and a backward without it makes again.
 struct Kept {
-  Prep prep;
+  uint8_t* records;
   bf16 *S, *R;
 };
-Prep carve_prep(const Dims& d, Carver& cv) {
-  const size_t items = (size_t)d.nc * d.HV;
-  Prep p;
-  p.Thi = cv.take<bf16>(items * kC * kC);
-  p.Tlo = cv.take<bf16>(items * kC * kC);
-  p.P = cv.take<bf16>(items * kC * kC);
-  p.gates = cv.take<float>(items * kGateRows * kC);
-  return p;
-}
+uint8_t* carve_records(const Dims& d, Carver& cv) { return cv.take<uint8_t>((size_t)d.nc * d.HV * kRecordBytes); }
 Kept carve_kept(const Dims& d, Carver& cv) {
   const size_t items = (size_t)d.nc * d.HV;
   Kept k;
-  k.prep = carve_prep(d, cv);
+  k.records = carve_records(d, cv);
   k.S = cv.take<bf16>(items * d.VP * d.KP);
   k.R = cv.take<bf16>(items * kC * d.VP);
   return k;
@@ -1131,7 +678,7 @@ size_t workspace(const Dims& d, bool backward, bool stashed) {
     if (backward)
       carve_kept(d, cv);
     else
-      carve_prep(d, cv);
+      carve_records(d, cv);
   }
   return cv.off;
 }
@@ -1154,76 +701,36 @@ ssd_status check_elem(std::initializer_list<const void*> req, unsigned bytes) {
   return SSD_OK;
 }
 
-cudaError_t sm_count(int* n) {
-  int dev;
-  cudaError_t e = cudaGetDevice(&dev);
-  return e == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) : e;
-}
-
-// Warps of a scan's block: a block has an SM to itself (its two stages take most of the shared memory), so the
-// fewest warps a block with which one wave of blocks holds them all, at most eight.
-cudaError_t scan_warps(const Dims& d, int* nw) {
-  int sms;
-  cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
-  const long long units = (long long)d.N * d.HV;
-  const int vt = d.VP / 16;
-  *nw = 1;
-  while (*nw < 8 && *nw < vt && units * ((vt + *nw - 1) / *nw) > sms) *nw *= 2;
-  return cudaSuccess;
-}
-template <int KP>
-size_t scan_smem(int nw) {
-  return 2 * Stage<KP>::bytes(nw) + 2 * (size_t)nw * 16 * (KP + 8);
-}
-
 template <typename F>
 cudaError_t allow_smem(F* f, size_t bytes) {
   return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 template <int KP>
-cudaError_t run_prep(const Dims& d, const Table& tb, const In& in, const Prep& pr, const int* cu, int* status,
+cudaError_t run_prep(const Dims& d, const Table& tb, const In& in, uint8_t* records, const int* cu, int* status,
                      cudaStream_t st) {
   if (d.packed) SSD_LAUNCH("k_delta_table", st, k_delta_table<<<1, 1024, 0, st>>>(cu, d.N, d.T, tb));
-  const size_t sm = 2 * (size_t)(2 * kC * (KP + 8)) + sizeof(float) * (2 * kC + 32) * kFP;
+  const size_t kq = 2 * (size_t)(2 * kC * (KP + 8)), at = sizeof(float) * (2 * kC + 32) * kFP, sm = kq > at ? kq : at;
   cudaError_t e = allow_smem(k_delta_prep<KP>, sm);
   if (e != cudaSuccess) return e;
   SSD_LAUNCH("k_delta_prep", st,
-             k_delta_prep<KP><<<dim3((unsigned)d.nc, (unsigned)d.H), 128, sm, st>>>(d, tb, in, pr, status));
+             k_delta_prep<KP><<<dim3((unsigned)d.nc, (unsigned)d.H), 128, sm, st>>>(d, tb, in, records, status));
   return cudaGetLastError();
 }
 
 template <int KP>
-cudaError_t run_scan(const Dims& d, const Table& tb, const In& in, const Prep& pr, bf16* o, float* s_final, bf16* S,
-                     bf16* R, cudaStream_t st) {
-  int nw;
-  cudaError_t e = scan_warps(d, &nw);
-  if (e == cudaSuccess) e = allow_smem(k_delta_scan<KP>, scan_smem<KP>(nw));
+cudaError_t run_grads(const Dims& d, const Table& tb, const In& in, const Kept& kept, const Grads& gr, const bf16* dout,
+                      const GradOut& out, cudaStream_t st) {
+  cudaError_t e = allow_smem(k_delta_grads<KP>, grads_smem<KP>(d.VP));
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(d.N * d.HV), (unsigned)((d.VP / 16 + nw - 1) / nw));
-  SSD_LAUNCH("k_delta_scan", st,
-             k_delta_scan<KP><<<grid, 32 * nw, scan_smem<KP>(nw), st>>>(d, tb, in, pr, o, s_final, S, R));
-  return cudaGetLastError();
-}
-
-template <int KP>
-cudaError_t run_backward(const Dims& d, const Table& tb, const In& in, const Kept& kept, const Grads& gr,
-                         const bf16* dout, const float* ds_final, const GradOut& out, bf16* dv, float* ds0,
-                         cudaStream_t st) {
-  int nw;
-  cudaError_t e = scan_warps(d, &nw);
-  if (e == cudaSuccess) e = allow_smem(k_delta_rev<KP>, scan_smem<KP>(nw));
-  if (e == cudaSuccess) e = allow_smem(k_delta_grads<KP>, grads_smem<KP>(d.VP));
-  if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(d.N * d.HV), (unsigned)((d.VP / 16 + nw - 1) / nw));
-  SSD_LAUNCH("k_delta_rev", st,
-             k_delta_rev<KP><<<grid, 32 * nw, scan_smem<KP>(nw), st>>>(d, tb, in, kept.prep, dout, d.ovec, ds_final, dv,
-                                                                       ds0, gr.dS, gr.dY));
   SSD_LAUNCH("k_delta_grads", st,
              k_delta_grads<KP><<<dim3((unsigned)d.nc, (unsigned)d.H), 256, grads_smem<KP>(d.VP), st>>>(
-                 d, tb, in, kept.prep, dout, d.ovec, kept.S, kept.R, gr.dS, gr.dY, out));
+                 d, tb, in, kept.records, dout, d.ovec, kept.S, kept.R, gr.dS, gr.dY, out));
   return cudaGetLastError();
+}
+cudaError_t prepare(const Dims& d, const Table& tb, const In& in, uint8_t* records, const int* cu, int* status,
+                    cudaStream_t st) {
+  return d.KP == 64 ? run_prep<64>(d, tb, in, records, cu, status, st) : run_prep<128>(d, tb, in, records, cu, status, st);
 }
 
 }  // namespace
@@ -1326,18 +833,12 @@ ssd_status ssd_delta_forward(const ssd_delta_problem* prob, const void* q, const
     Carver cs(stash);
     kept = carve_kept(d, cs);
   } else {
-    kept.prep = carve_prep(d, cv);
+    kept.records = carve_records(d, cv);
   }
   const In in{(const bf16*)q, (const bf16*)k, (const bf16*)v, g, beta, s0, scale};
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t e;
-  if (d.KP == 64) {
-    e = run_prep<64>(d, tb, in, kept.prep, cu_seqlens, (int*)ws, st);
-    if (e == cudaSuccess) e = run_scan<64>(d, tb, in, kept.prep, (bf16*)o, s_final, kept.S, kept.R, st);
-  } else {
-    e = run_prep<128>(d, tb, in, kept.prep, cu_seqlens, (int*)ws, st);
-    if (e == cudaSuccess) e = run_scan<128>(d, tb, in, kept.prep, (bf16*)o, s_final, kept.S, kept.R, st);
-  }
+  cudaError_t e = prepare(d, tb, in, kept.records, cu_seqlens, (int*)ws, st);
+  if (e == cudaSuccess) e = forward_scan(d, tb, in, kept.records, (bf16*)o, s_final, kept.S, kept.R, (int*)ws, st);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -1379,16 +880,15 @@ ssd_status ssd_delta_backward(const ssd_delta_problem* prob, const void* dout, c
   if (stash) {
     if (d.packed) SSD_LAUNCH("k_delta_table", st, k_delta_table<<<1, 1024, 0, st>>>(cu_seqlens, d.N, d.T, tb));
     e = cudaMemsetAsync(ws, 0, sizeof(int32_t), st);
-  } else if (d.KP == 64) {
-    e = run_prep<64>(d, tb, in, kept.prep, cu_seqlens, (int*)ws, st);
-    if (e == cudaSuccess) e = run_scan<64>(d, tb, in, kept.prep, nullptr, nullptr, kept.S, kept.R, st);
   } else {
-    e = run_prep<128>(d, tb, in, kept.prep, cu_seqlens, (int*)ws, st);
-    if (e == cudaSuccess) e = run_scan<128>(d, tb, in, kept.prep, nullptr, nullptr, kept.S, kept.R, st);
+    e = prepare(d, tb, in, kept.records, cu_seqlens, (int*)ws, st);
+    if (e == cudaSuccess) e = forward_scan(d, tb, in, kept.records, nullptr, nullptr, kept.S, kept.R, (int*)ws, st);
   }
   if (e == cudaSuccess)
-    e = d.KP == 64 ? run_backward<64>(d, tb, in, kept, gr, (const bf16*)dout, ds_final, out, (bf16*)dv, ds0, st)
-                   : run_backward<128>(d, tb, in, kept, gr, (const bf16*)dout, ds_final, out, (bf16*)dv, ds0, st);
+    e = reverse_scan(d, tb, in, kept.records, (const bf16*)dout, ds_final, (bf16*)dv, ds0, gr.dS, gr.dY, (int*)ws, st);
+  if (e == cudaSuccess)
+    e = d.KP == 64 ? run_grads<64>(d, tb, in, kept, gr, (const bf16*)dout, out, st)
+                   : run_grads<128>(d, tb, in, kept, gr, (const bf16*)dout, out, st);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

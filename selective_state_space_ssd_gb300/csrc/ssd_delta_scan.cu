@@ -1,0 +1,833 @@
+// The two sequential scans of the chunked delta rule on tcgen05: one block per (sequence, value head) walks its chunks
+// of 64 steps in order (k_delta_scan) or in reverse (k_delta_rev).  The formulas are in ssd_delta.cu.
+//
+// Everything is transposed: a TMEM lane (and the four threads that serve it) is a column v of V, so S^T [128 v][K] is
+// the left operand of every product and the results of one product, X^T = S^T K^T, R^T = Y^T T^T, S'^T += R^T K, are
+// the left operand of the next after a few elementwise operations.  tcgen05 takes the left operand from tensor memory:
+// the chain of a chunk never touches shared memory, which holds only the tiles that are read as right operands as they
+// lie in global memory (K and Q by rows for S^T K^T, the same bytes by columns for R^T K).
+//
+// Twenty-four warps:
+//   0-15   the chain: four warps a lane quadrant, each with a quarter of the columns; S stays in their registers (fp32)
+//   16-19  beside the chain: o and the stash forward; dS', dY, dV and the scaled dO^T operand in reverse
+//   20     issues every MMA
+//   21-23  copies of the next chunk's tiles (two stages; TMA where rows are whole 16-byte pieces)
+// Between two chunks lie three round trips through tensor memory (X, R, S'), which is what bounds the kernel: about
+// 105 cycles of latency for each group of MMAs, 32 cycles for each 128 x 64 x 16 one (A in TMEM; 57 with A in shared
+// memory), and the elementwise work of 128 x 64 and 128 x K values between them.
+#include "delta_common.cuh"
+#include "tc_common.cuh"
+
+namespace ssd {
+namespace delta {
+namespace {
+
+using namespace ssd::tc;
+
+constexpr int kChainWarps = 16, kSideWarps = 4, kLoadWarps = 3;
+constexpr int kMmaWarp = kChainWarps + kSideWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1 + kLoadWarps);
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSideBar = 1;  // named barrier of the side warps
+
+// A stage: [K; Q] rows as one 128-row K-major tile, V (or dO) [64][128], the chunk's record.  Beside the two stages: a
+// [64][128] tile through which o (dV) turns from columns into rows.
+template <int KP>
+struct Tiles {
+  static constexpr uint32_t kKQ = 128 * KP * 2, kV = kC * 128 * 2;
+  static constexpr uint32_t kRec = kKQ + kV;
+  static constexpr uint32_t kBytes = (kRec + kRecordBytes + 1023) / 1024 * 1024;
+};
+template <int KP>
+constexpr uint32_t scan_smem() {
+  return 2 * Tiles<KP>::kBytes + kC * 128 * 2 + 1024;  // 1024: the tiles' alignment
+}
+
+struct Bars {
+  uint64_t full[2], empty[2], tail, s, x, y, r, rp, ro, d, o, e1, e2, f, done;
+};
+struct Maps {
+  CUtensorMap k, q, v;  // v: V forward, dO in reverse
+};
+
+// D[tmem] (+)= A[tmem] B[smem]^T
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void st16u(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void st8u(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// A wait of a whole warp: every lane learns the same answer, so a bound that runs out stops the warp as one.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t phase, int* status, int code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, phase, status, code)) != 0;
+}
+// The warp's tensor-memory stores are done and visible to whoever waits on the barrier.
+__device__ __forceinline__ void signal_tmem(uint64_t* bar, int lane) {
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+// The warp has read what it needs (tensor or shared memory).
+__device__ __forceinline__ void signal_read(uint64_t* bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// 16 values as the bf16 operand columns [8] and what the rounding left [8], the two side by side in tensor memory.
+__device__ __forceinline__ void put_split(uint32_t addr, const float (&x)[16]) {
+  uint32_t h[8], l[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split(x[2 * i], x[2 * i + 1], h[i], l[i]);
+  st8u(addr, h);
+  st8u(addr + 8, l);
+}
+__device__ __forceinline__ void ld16(uint32_t addr, float (&x)[16]) {
+  uint32_t u[16];
+  tmem_ld16_nowait(addr, u);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void lds16(const float* p, float (&x)[16]) {  // the same 16 floats for every lane
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p + i);
+    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+  }
+}
+
+__device__ __forceinline__ uint32_t v_off(int t, int v) {  // element (t, v) of the V tile
+  return (uint32_t)((v >> 6) * (kC * 128)) + sw128_chunk(t, (v & 63) >> 3) + 2u * (v & 7);
+}
+
+// 64 rows of `cols` valid elements, zeros past `rows` and `cols`, into a 128-byte-swizzled tile whose 64-column atoms
+// hold R rows each, element by element (rows that are not whole 16-byte pieces): eight loads in flight a thread.
+__device__ __forceinline__ void load_elements(uint8_t* tile, int R, int width, const bf16* src, long long stride,
+                                              int rows, int cols, int tid) {
+  constexpr int kN = 32 * kLoadWarps, kBatch = 8;
+  const unsigned short* s = reinterpret_cast<const unsigned short*>(src);
+  for (int base = tid; base < kC * width; base += kN * kBatch) {
+    unsigned short x[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = base + j * kN, r = i / width, c = i - r * width;
+      x[j] = r < rows && c < cols ? s[(long long)r * stride + c] : (unsigned short)0;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = base + j * kN, r = i / width, c = i - r * width;
+      if (r < kC) *reinterpret_cast<unsigned short*>(tile + (c >> 6) * R * 128 + sw128_chunk(r, (c & 63) >> 3) + 2 * (c & 7)) = x[j];
+    }
+  }
+}
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int R, int atoms, int rows, int tid) {
+  for (int i = tid; i < (kC - rows) * atoms * 8; i += 32 * kLoadWarps) {
+    const int r = rows + i / (atoms * 8), j = i % (atoms * 8);
+    *reinterpret_cast<uint4*>(tile + (j >> 3) * R * 128 + r * 128 + (j & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// What the copy warps do for one chunk: its tiles into a stage and an arrival on the stage's barrier.  TMA copies and
+// the record arrive by themselves, but for a chunk of fewer than 64 steps: what a box brings in past its end belongs to
+// the next sequence and is overwritten with zeros first.
+template <int KP>
+struct Loader {
+  const Dims& d;
+  const In& in;
+  const Maps& maps;
+  const bf16* v;
+  long long vstride;
+  bool vvec, with_q;
+  int hk, hv;
+  uint64_t* tail;
+  uint32_t tails;  // chunks of fewer steps so far
+
+  __device__ bool operator()(uint8_t* st, uint64_t* full, const uint8_t* record, int first, int rows, int tid,
+                             int* status) {
+    const bool kt = d.kvec, qt = with_q && d.qvec, vt = vvec, cut = rows < kC;
+    uint8_t* vtile = st + Tiles<KP>::kKQ;
+    if (tid == 0) {
+      uint64_t* bar = cut ? tail : full;
+      const uint32_t rowsb = kC * 128;
+      mbar_expect_tx(bar, kRecordBytes + rowsb * ((kt ? KP / 64 : 0) + (qt ? KP / 64 : 0) + (vt ? 2 : 0)));
+      bulk_load(smem_u32(st + Tiles<KP>::kRec), record, kRecordBytes, bar);
+#pragma unroll
+      for (int a = 0; a < KP / 64; ++a) {
+        if (kt) tma_load_3d(st + a * 128 * 128, &maps.k, 64 * a, hk, first, bar);
+        if (qt) tma_load_3d(st + a * 128 * 128 + kC * 128, &maps.q, 64 * a, hk, first, bar);
+      }
+      if (vt)
+        for (int a = 0; a < 2; ++a) tma_load_3d(vtile + a * kC * 128, &maps.v, 64 * a, hv, first, bar);
+    }
+    if (!kt) load_elements(st, 128, KP, in.k + (long long)first * d.ks + (long long)hk * d.K, d.ks, rows, d.K, tid);
+    if (with_q && !qt)
+      load_elements(st + kC * 128, 128, KP, in.q + (long long)first * d.qs + (long long)hk * d.K, d.qs, rows, d.K, tid);
+    if (!vt) load_elements(vtile, kC, 128, v + (long long)first * vstride + (long long)hv * d.V, vstride, rows, d.V, tid);
+    bool ok = true;
+    if (cut) {
+      ok = wait_warp(tail, tails & 1, status, 43);
+      ++tails;
+      if (kt) zero_rows(st, 128, KP / 64, rows, tid);
+      if (qt) zero_rows(st + kC * 128, 128, KP / 64, rows, tid);
+      if (vt) zero_rows(vtile, kC, 2, rows, tid);
+    }
+    fence_proxy_async();  // the MMAs read these tiles
+    __syncwarp();
+    if ((tid & 31) == 0) mbar_arrive(full);
+    if (cut && tid == 0) mbar_arrive(full);  // in the place of the arrival that announced the bytes, on the other barrier
+    return ok;
+  }
+};
+
+// s [K, V] fp32 to and from a thread's keys k0 .. k0 + NK - 1 of lane v: neighbouring lanes are neighbouring columns.
+template <int NK>
+__device__ __forceinline__ void read_state(float (&S)[NK], const float* s, int K, int V, int k0, int v) {
+#pragma unroll
+  for (int i = 0; i < NK; ++i) S[i] = s && k0 + i < K && v < V ? s[(size_t)(k0 + i) * V + v] : 0.f;
+}
+template <int NK>
+__device__ __forceinline__ void write_state(float* s, const float (&S)[NK], int K, int V, int k0, int v) {
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+    if (k0 + i < K && v < V) s[(size_t)(k0 + i) * V + v] = S[i];
+}
+
+// Columns of tensor memory.  fp32 results: X (then Y high, low in place), QS (forward: (Q S)^T; reverse: U, then dY),
+// R (then R' high, low in place), O2 (forward: (P R)^T) or F (reverse: the scaled dO^T, high and low), D (the state's
+// update); the state's operand, high and low, and R's for o and the stash (over the low part of a full-width state,
+// which has been read by then).
+template <int KP>
+struct Cols {
+  static constexpr int X = 0, QS = 64, R = 128, O2 = 192, D = 256, Sh = 384, Sl = Sh + KP / 2, Ro = 448;
+};
+// Operand columns of the 16-value block kb: 8 high, 8 low, where its 16 fp32 values were.
+__device__ __forceinline__ constexpr int pair_col(int base, int kb, bool low) { return base + 16 * kb + (low ? 8 : 0); }
+
+struct Block {
+  int hv, hk;
+  Seq sq;
+  size_t su;
+};
+__device__ __forceinline__ Block block_of(const Dims& d, const Table& tb) {
+  Block b;
+  const int n = blockIdx.x / d.HV;
+  b.hv = blockIdx.x - n * d.HV;
+  b.hk = b.hv / d.G;
+  b.sq = sequence(d, tb, n);
+  b.su = ((size_t)n * d.HV + b.hv) * d.K * d.V;
+  return b;
+}
+
+__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* p) {
+  return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u);
+}
+
+__device__ __forceinline__ void init_bars(Bars* b) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&b->full[i], kLoadWarps + 1);
+    mbar_init(&b->empty[i], 1 + kChainWarps + kSideWarps);
+  }
+  mbar_init(&b->tail, 1);
+  mbar_init(&b->s, kChainWarps);
+  mbar_init(&b->x, 1);
+  mbar_init(&b->y, kChainWarps);
+  mbar_init(&b->r, 1);
+  mbar_init(&b->rp, kChainWarps);
+  mbar_init(&b->ro, kChainWarps);
+  mbar_init(&b->d, 1);
+  mbar_init(&b->o, 1);
+  mbar_init(&b->e1, kSideWarps);
+  mbar_init(&b->e2, kSideWarps);
+  mbar_init(&b->f, kSideWarps);
+  mbar_init(&b->done, 1);
+  mbar_init_fence();
+}
+
+// A chain thread's keys as operand columns: high parts into Sh, low parts into Sl.
+template <int KP>
+__device__ __forceinline__ void put_state(uint32_t tm, int lane0, int wg, const float (&S)[KP / 4]) {
+#pragma unroll
+  for (int b = 0; b < KP / 64; ++b) {
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split(S[16 * b + 2 * i], S[16 * b + 2 * i + 1], h[i], l[i]);
+    st8u(taddr(tm, lane0, Cols<KP>::Sh + wg * (KP / 8) + 8 * b), h);
+    st8u(taddr(tm, lane0, Cols<KP>::Sl + wg * (KP / 8) + 8 * b), l);
+  }
+}
+// S = keep S + D
+template <int KP>
+__device__ __forceinline__ void update_state(uint32_t tm, int lane0, int k0, float keep, float (&S)[KP / 4]) {
+#pragma unroll
+  for (int b = 0; b < KP / 64; ++b) {
+    float x[16];
+    ld16(taddr(tm, lane0, Cols<KP>::D + k0 + 16 * b), x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(keep, S[16 * b + i], x[i]);
+  }
+  tc_fence_before();
+}
+
+// The state's operand (its bf16 high part) of lane v: 16-byte pieces of eight keys, [KP / 8][VP] of them, so that the
+// lanes of a warp write consecutive pieces.
+template <int KP>
+__device__ __forceinline__ void keep_state(uint32_t tm, int lane0, bf16* dst, int VP, int v) {
+#pragma unroll
+  for (int b = 0; b < KP / 64; ++b) {
+    uint32_t u[32];
+    tmem_ld32_nowait(taddr(tm, lane0, Cols<KP>::Sh + 32 * b), u);
+    tmem_wait_ld();
+    if (v < VP) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(dst + ((size_t)(8 * b + j) * VP + v) * 8) =
+            make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+    }
+  }
+}
+
+// The [64][128] bf16 tile of the side warps to rows of a tensor, first step at dst.
+__device__ __forceinline__ void store_tile(const uint8_t* tile, bf16* dst, long long stride, int rows, int V, bool vec,
+                                           int tid) {
+  const bf16* t = reinterpret_cast<const bf16*>(tile);
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = (tid >> 4) + 8 * i, c = 8 * (tid & 15);
+      if (r < rows && c < V)
+        *reinterpret_cast<uint4*>(dst + (long long)r * stride + c) = *reinterpret_cast<const uint4*>(t + r * 128 + c);
+    }
+  } else {
+    for (int r = 0; r < rows; ++r)
+      if (tid < V) dst[(long long)r * stride + tid] = t[r * 128 + tid];
+  }
+}
+
+// ---------------------------------------------------------------- forward
+template <int KP>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_delta_scan(Dims d, Table tb, In in, const __grid_constant__ Maps maps, const uint8_t* records, bf16* o,
+                 float* s_final, bf16* Sout, bf16* Rout, int* status) {
+  using C = Cols<KP>;
+  extern __shared__ uint8_t raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t tslot;
+  uint8_t* smem = aligned_smem(raw);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  if (threadIdx.x == 0) init_bars(&bars);
+  if (w == kMmaWarp) tmem_alloc(&tslot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = tslot;
+  const Block blk = block_of(d, tb);
+  const int nc = blk.sq.nc;
+  const bool stash = Sout != nullptr;
+
+  if (w < kChainWarps) {
+    const int wg = w >> 2, lane0 = 32 * (w & 3), v = lane0 + lane, k0 = wg * (KP / 4);
+    float S[KP / 4];
+    read_state(S, in.s0 ? in.s0 + blk.su : nullptr, d.K, d.V, k0, v);
+    for (int c = 0; c < nc; ++c) {
+      const uint32_t ph = c & 1;
+      const uint8_t* st = smem + (c & 1) * Tiles<KP>::kBytes;
+      const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
+      if (c > 0) {  // the columns of the state's operand and of R's: read to the end by the chunk before?
+        if (stash && !wait_warp(&bars.e1, ph ^ 1, status, 11)) break;
+        if (o && !wait_warp(&bars.o, ph ^ 1, status, 12)) break;
+        tc_fence_after();
+      }
+      put_state<KP>(tm, lane0, wg, S);
+      signal_tmem(&bars.s, lane);
+      if (!wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 13)) break;
+      float x[16], a[16], b[16];
+      {
+        const uint8_t* vt = st + Tiles<KP>::kKQ;
+        lds16(gates + 2 * kC + 16 * wg, a);
+        lds16(gates + 16 * wg, b);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          b[i] *= -a[i];
+          a[i] *= __bfloat162float(*reinterpret_cast<const bf16*>(vt + v_off(16 * wg + i, v)));
+        }
+      }
+      if (!wait_warp(&bars.x, ph, status, 14)) break;
+      tc_fence_after();
+      ld16(taddr(tm, lane0, C::X + 16 * wg), x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = fmaf(b[i], x[i], a[i]);  // Y = beta V - beta e^G X
+      put_split(taddr(tm, lane0, C::X + 16 * wg), x);
+      signal_tmem(&bars.y, lane);
+      lds16(gates + kC + 16 * wg, a);
+      if (!wait_warp(&bars.r, ph, status, 15)) break;
+      tc_fence_after();
+      ld16(taddr(tm, lane0, C::R + 16 * wg), x);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a[i] *= x[i];  // R' = e^{G_end - G} R
+      put_split(taddr(tm, lane0, C::R + 16 * wg), a);
+      signal_tmem(&bars.rp, lane);
+      put_split(taddr(tm, lane0, C::Ro + 16 * wg), x);  // R itself, for o and the stash
+      const float keep = gates[kC - 1];
+      signal_tmem(&bars.ro, lane);
+      if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
+      if (!wait_warp(&bars.d, ph, status, 16)) break;
+      tc_fence_after();
+      update_state<KP>(tm, lane0, k0, keep, S);
+    }
+    if (s_final) write_state(s_final + blk.su, S, d.K, d.V, k0, v);
+  } else if (w < kMmaWarp) {
+    const int lane0 = 32 * (w & 3), v = lane0 + lane, tid = threadIdx.x - 32 * kChainWarps;
+    const long long os = (long long)d.HV * d.V;
+    bf16* tile = reinterpret_cast<bf16*>(smem + 2 * Tiles<KP>::kBytes);
+    bool ok = true;
+    for (int c = 0; c < nc && ok; ++c) {
+      const uint32_t ph = c & 1;
+      const float* gates =
+          reinterpret_cast<const float*>(smem + (c & 1) * Tiles<KP>::kBytes + Tiles<KP>::kRec + kRecordGates);
+      const size_t item = (size_t)(blk.sq.chunk + c) * d.HV + blk.hv;
+      if (stash) {  // the state entering the chunk, and R, both as the bf16 operands hold them
+        if (!(ok = wait_warp(&bars.s, ph, status, 21))) break;
+        tc_fence_after();
+        keep_state<KP>(tm, lane0, Sout + item * d.VP * KP, d.VP, v);
+        if (!(ok = wait_warp(&bars.ro, ph, status, 22))) break;
+        tc_fence_after();
+        uint32_t u[4][8];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld8_nowait(taddr(tm, lane0, C::Ro + 16 * b), u[b]);
+        tmem_wait_ld();
+        signal_read(&bars.e1, lane);
+        if (v < d.VP) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(Rout + item * d.VP * kC + ((size_t)j * d.VP + v) * 8) =
+                make_uint4(u[j >> 1][4 * (j & 1)], u[j >> 1][4 * (j & 1) + 1], u[j >> 1][4 * (j & 1) + 2], u[j >> 1][4 * (j & 1) + 3]);
+        }
+      }
+      if (o) {
+        ok = wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 23) && wait_warp(&bars.o, ph, status, 24);
+        // the tile's last rows have been stored, and all side warps go on together or not at all
+        if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t q[16], r[16];
+          tmem_ld16_nowait(taddr(tm, lane0, C::QS + 16 * b), q);
+          tmem_ld16_nowait(taddr(tm, lane0, C::O2 + 16 * b), r);
+          float e[16];
+          lds16(gates + 16 * b, e);
+          tmem_wait_ld();
+          if (b == 3) signal_read(&bars.e2, lane);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            tile[(16 * b + i) * 128 + v] =
+                __float2bfloat16_rn(in.scale * fmaf(e[i], __uint_as_float(q[i]), __uint_as_float(r[i])));
+        }
+        named_bar(kSideBar, 32 * kSideWarps);
+        store_tile(reinterpret_cast<const uint8_t*>(tile), o + ((long long)(blk.sq.start + c * kC) * d.HV + blk.hv) * d.V,
+                   os, min(kC, blk.sq.len - c * kC), d.V, d.ovec, tid);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
+    }
+  } else if (w == kMmaWarp) {
+    constexpr uint32_t n64 = idesc_bf16(128, 64, false, false), nk = idesc_bf16(128, KP, false, true);
+    for (int c = 0; c < nc; ++c) {
+      const uint32_t ph = c & 1;
+      const uint8_t* st = smem + (c & 1) * Tiles<KP>::kBytes;
+      const uint8_t* rc = st + Tiles<KP>::kRec;
+      const uint64_t kd = kdesc(st, 128, 0), qd = kdesc(st + kC * 128, 128, 0);
+      const uint64_t km = sdesc_sw128(smem_u32(st), 128 * 128, 1024);  // the same K rows as [step][key]
+      if (!wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 31)) break;
+      if (!wait_warp(&bars.s, ph, status, 32)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::X, tm + C::Sh + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, kb > 0);
+#pragma unroll
+        for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::X, tm + C::Sl + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, true);
+        mma_commit(&bars.x);
+      }
+      __syncwarp();
+      if (o) {
+        if (c > 0 && !wait_warp(&bars.e2, ph ^ 1, status, 33)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::QS, tm + C::Sh + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, kb > 0);
+#pragma unroll
+          for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::QS, tm + C::Sl + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, true);
+        }
+        __syncwarp();
+      }
+      if (!wait_warp(&bars.y, ph, status, 34)) break;
+      tc_fence_after();
+      if (elect_one()) {  // R^T = Y^T T^T: the steps of 16-block kb reach the steps i >= 16 kb
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          const uint32_t id = idesc_bf16(128, kC - 16 * kb, false, false);
+          const uint32_t yh = tm + pair_col(C::X, kb, false), yl = tm + pair_col(C::X, kb, true);
+          const uint64_t th = kdesc(rc + 16 * kb * 128, kC, 16 * kb), tl = kdesc(rc + 8192 + 16 * kb * 128, kC, 16 * kb);
+          mma_ts(tm + C::R + 16 * kb, yh, th, id, kb > 0);
+          mma_ts(tm + C::R + 16 * kb, yl, th, id, true);
+          mma_ts(tm + C::R + 16 * kb, yh, tl, id, true);
+        }
+        mma_commit(&bars.r);
+      }
+      __syncwarp();
+      if (!wait_warp(&bars.rp, ph, status, 35)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          mma_ts(tm + C::D, tm + pair_col(C::R, kb, false), km + mdesc_step(16 * kb), nk, kb > 0);
+          mma_ts(tm + C::D, tm + pair_col(C::R, kb, true), km + mdesc_step(16 * kb), nk, true);
+        }
+        mma_commit(&bars.d);
+      }
+      __syncwarp();
+      if (o) {
+        if (!wait_warp(&bars.ro, ph, status, 36)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kb = 0; kb < 4; ++kb) {
+            const uint32_t id = idesc_bf16(128, kC - 16 * kb, false, false);
+            const uint32_t rh = tm + pair_col(C::Ro, kb, false), rl = tm + pair_col(C::Ro, kb, true);
+            const uint64_t p0 = kdesc(rc + 2 * 8192 + 16 * kb * 128, kC, 16 * kb), p1 = kdesc(rc + 3 * 8192 + 16 * kb * 128, kC, 16 * kb);
+            mma_ts(tm + C::O2 + 16 * kb, rh, p0, id, kb > 0);
+            mma_ts(tm + C::O2 + 16 * kb, rl, p0, id, true);
+            mma_ts(tm + C::O2 + 16 * kb, rh, p1, id, true);
+          }
+          mma_commit(&bars.o);
+        }
+        __syncwarp();
+      }
+      if (elect_one()) mma_commit(&bars.empty[c & 1]);
+      __syncwarp();
+    }
+    if (elect_one()) mma_commit(&bars.done);  // every MMA has finished before the tensor memory is given back
+    __syncwarp();
+    wait_warp(&bars.done, 0, status, 37);
+  } else {
+    const int tid = threadIdx.x - 32 * (kMmaWarp + 1);
+    Loader<KP> ld{d, in, maps, in.v, d.vs, d.vvec, o != nullptr, blk.hk, blk.hv, &bars.tail, 0};
+    int loaded = -1;
+    for (int c = 0; c < nc; ++c) {
+      if (c >= 2 && !wait_warp(&bars.empty[c & 1], ((c >> 1) & 1) ^ 1, status, 41)) break;
+      const bool ok = ld(smem + (c & 1) * Tiles<KP>::kBytes, &bars.full[c & 1],
+                         records + ((size_t)(blk.sq.chunk + c) * d.HV + blk.hv) * kRecordBytes, blk.sq.start + c * kC,
+                         min(kC, blk.sq.len - c * kC), tid, status);
+      loaded = c;
+      if (!ok) break;
+    }
+    // no copy is in flight when the block ends, also where a wait above ran out
+    for (int c = max(loaded - 1, 0); c <= loaded; ++c) wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 42);
+  }
+  __syncthreads();
+  if (w == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tm, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- reverse
+template <int KP>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_delta_rev(Dims d, Table tb, In in, const __grid_constant__ Maps maps, const uint8_t* records, const bf16* dout,
+                const float* ds_final, bf16* dv, float* ds0, bf16* dSout, bf16* dYout, int* status) {
+  using C = Cols<KP>;
+  constexpr int U = C::QS, F = C::O2;
+  extern __shared__ uint8_t raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t tslot;
+  uint8_t* smem = aligned_smem(raw);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  if (threadIdx.x == 0) init_bars(&bars);
+  if (w == kMmaWarp) tmem_alloc(&tslot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = tslot;
+  const Block blk = block_of(d, tb);
+  const int nc = blk.sq.nc;
+  const long long os = (long long)d.HV * d.V;
+
+  // i counts the chunks in the order they are walked; chunk nc - 1 - i
+  if (w < kChainWarps) {
+    const int wg = w >> 2, lane0 = 32 * (w & 3), v = lane0 + lane, k0 = wg * (KP / 4);
+    float S[KP / 4];
+    read_state(S, ds_final ? ds_final + blk.su : nullptr, d.K, d.V, k0, v);
+    for (int i = 0; i < nc; ++i) {
+      const uint32_t ph = i & 1;
+      const uint8_t* st = smem + (i & 1) * Tiles<KP>::kBytes;
+      const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
+      if (i > 0) {
+        if (!wait_warp(&bars.e1, ph ^ 1, status, 51)) break;
+        tc_fence_after();
+      }
+      put_state<KP>(tm, lane0, wg, S);
+      signal_tmem(&bars.s, lane);
+      if (!wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 52)) break;
+      float x[16], a[16];
+      lds16(gates + kC + 16 * wg, a);
+      if (!wait_warp(&bars.x, ph, status, 53)) break;
+      tc_fence_after();
+      {  // dR = e^{G_end - G} X + scale U
+        uint32_t p[16], q[16];
+        tmem_ld16_nowait(taddr(tm, lane0, C::X + 16 * wg), p);
+        tmem_ld16_nowait(taddr(tm, lane0, U + 16 * wg), q);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = fmaf(in.scale, __uint_as_float(q[j]), a[j] * __uint_as_float(p[j]));
+      }
+      put_split(taddr(tm, lane0, C::X + 16 * wg), x);
+      signal_tmem(&bars.y, lane);
+      {
+        float b[16];
+        lds16(gates + 16 * wg, a);
+        lds16(gates + 2 * kC + 16 * wg, b);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) a[j] *= -b[j];
+      }
+      if (!wait_warp(&bars.r, ph, status, 54)) break;
+      tc_fence_after();
+      ld16(taddr(tm, lane0, C::R + 16 * wg), x);  // dY
+#pragma unroll
+      for (int j = 0; j < 16; ++j) a[j] *= x[j];  // dX = -beta e^G dY
+      put_split(taddr(tm, lane0, C::R + 16 * wg), a);
+      signal_tmem(&bars.rp, lane);
+      {  // dY for the side warps, over U
+        uint32_t u[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(x[j]);
+        st16u(taddr(tm, lane0, U + 16 * wg), u);
+      }
+      const float keep = gates[kC - 1];
+      signal_tmem(&bars.ro, lane);
+      if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
+      if (!wait_warp(&bars.d, ph, status, 55)) break;
+      tc_fence_after();
+      update_state<KP>(tm, lane0, k0, keep, S);
+    }
+    if (ds0) write_state(ds0 + blk.su, S, d.K, d.V, k0, v);
+  } else if (w < kMmaWarp) {
+    const int lane0 = 32 * (w & 3), v = lane0 + lane, tid = threadIdx.x - 32 * kChainWarps;
+    bf16* tile = reinterpret_cast<bf16*>(smem + 2 * Tiles<KP>::kBytes);
+    bool ok = true;
+    for (int i = 0; i < nc && ok; ++i) {
+      const uint32_t ph = i & 1;
+      const int c = nc - 1 - i;
+      const uint8_t* st = smem + (i & 1) * Tiles<KP>::kBytes;
+      const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
+      const size_t item = (size_t)(blk.sq.chunk + c) * d.HV + blk.hv;
+      if (!(ok = wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 61))) break;
+      if (i > 0 && !(ok = wait_warp(&bars.d, ph ^ 1, status, 62))) break;  // F of the chunk before has been read
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {  // F = scale e^G dO^T
+        float x[16];
+        lds16(gates + 16 * b, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          x[j] *= in.scale * __bfloat162float(*reinterpret_cast<const bf16*>(st + Tiles<KP>::kKQ + v_off(16 * b + j, v)));
+        put_split(taddr(tm, lane0, F + 16 * b), x);
+      }
+      signal_tmem(&bars.f, lane);
+      if (!(ok = wait_warp(&bars.s, ph, status, 63))) break;
+      tc_fence_after();
+      keep_state<KP>(tm, lane0, dSout + item * d.VP * KP, d.VP, v);
+      signal_read(&bars.e1, lane);
+      ok = wait_warp(&bars.ro, ph, status, 64);
+      if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float x[16], be[16];
+        lds16(gates + 2 * kC + 16 * b, be);
+        ld16(taddr(tm, lane0, U + 16 * b), x);
+        if (b == 3) signal_read(&bars.e2, lane);
+        if (v < d.VP) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<uint4*>(dYout + item * d.VP * kC + ((size_t)(2 * b + j) * d.VP + v) * 8) =
+                make_uint4(pack(x[8 * j], x[8 * j + 1]), pack(x[8 * j + 2], x[8 * j + 3]),
+                           pack(x[8 * j + 4], x[8 * j + 5]), pack(x[8 * j + 6], x[8 * j + 7]));
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) tile[(16 * b + j) * 128 + v] = __float2bfloat16_rn(be[j] * x[j]);
+      }
+      named_bar(kSideBar, 32 * kSideWarps);
+      if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
+      store_tile(reinterpret_cast<const uint8_t*>(tile), dv + ((long long)(blk.sq.start + c * kC) * d.HV + blk.hv) * d.V,
+                 os, min(kC, blk.sq.len - c * kC), d.V, d.ovec, tid);
+    }
+  } else if (w == kMmaWarp) {
+    constexpr uint32_t n64 = idesc_bf16(128, 64, false, false), nk = idesc_bf16(128, KP, false, true);
+    for (int i = 0; i < nc; ++i) {
+      const uint32_t ph = i & 1;
+      const uint8_t* st = smem + (i & 1) * Tiles<KP>::kBytes;
+      const uint8_t* rc = st + Tiles<KP>::kRec;
+      const uint64_t kd = kdesc(st, 128, 0);
+      const uint64_t km = sdesc_sw128(smem_u32(st), 128 * 128, 1024), qm = sdesc_sw128(smem_u32(st) + kC * 128, 128 * 128, 1024);
+      const uint64_t od = sdesc_sw128(smem_u32(st) + Tiles<KP>::kKQ, kC * 128, 1024);  // dO^T: [step][v]
+      if (!wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 71)) break;
+      if (i > 0 && !wait_warp(&bars.e2, ph ^ 1, status, 77)) break;
+      tc_fence_after();
+      if (elect_one()) {  // U^T = dO^T P: the steps of 16-block kb reach the steps t <= 16 kb + 15
+#pragma unroll
+        for (int kb = 3; kb >= 0; --kb) {
+          const uint32_t id = idesc_bf16(128, 16 * (kb + 1), true, true);
+          mma_bf16(tm + U, od + mdesc_step(16 * kb), mdesc(rc + 2 * 8192, kC, 16 * kb), id, kb < 3);
+          mma_bf16(tm + U, od + mdesc_step(16 * kb), mdesc(rc + 3 * 8192, kC, 16 * kb), id, true);
+        }
+      }
+      __syncwarp();
+      if (!wait_warp(&bars.s, ph, status, 72)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::X, tm + C::Sh + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, kb > 0);
+#pragma unroll
+        for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::X, tm + C::Sl + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, true);
+        mma_commit(&bars.x);
+      }
+      __syncwarp();
+      if (!wait_warp(&bars.f, ph, status, 73)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          mma_ts(tm + C::D, tm + pair_col(F, kb, false), qm + mdesc_step(16 * kb), nk, kb > 0);
+          mma_ts(tm + C::D, tm + pair_col(F, kb, true), qm + mdesc_step(16 * kb), nk, true);
+        }
+      }
+      __syncwarp();
+      if (!wait_warp(&bars.y, ph, status, 74)) break;
+      tc_fence_after();
+      if (elect_one()) {  // dY^T = dR^T T
+#pragma unroll
+        for (int kb = 3; kb >= 0; --kb) {
+          const uint32_t id = idesc_bf16(128, 16 * (kb + 1), false, true);
+          const uint32_t yh = tm + pair_col(C::X, kb, false), yl = tm + pair_col(C::X, kb, true);
+          const uint64_t th = mdesc(rc, kC, 16 * kb), tl = mdesc(rc + 8192, kC, 16 * kb);
+          mma_ts(tm + C::R, yh, th, id, kb < 3);
+          mma_ts(tm + C::R, yl, th, id, true);
+          mma_ts(tm + C::R, yh, tl, id, true);
+        }
+        mma_commit(&bars.r);
+      }
+      __syncwarp();
+      if (!wait_warp(&bars.rp, ph, status, 75)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {
+          mma_ts(tm + C::D, tm + pair_col(C::R, kb, false), km + mdesc_step(16 * kb), nk, true);
+          mma_ts(tm + C::D, tm + pair_col(C::R, kb, true), km + mdesc_step(16 * kb), nk, true);
+        }
+        mma_commit(&bars.d);
+        mma_commit(&bars.empty[i & 1]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) mma_commit(&bars.done);
+    __syncwarp();
+    wait_warp(&bars.done, 0, status, 76);
+  } else {
+    const int tid = threadIdx.x - 32 * (kMmaWarp + 1);
+    Loader<KP> ld{d, in, maps, dout, os, d.ovec, true, blk.hk, blk.hv, &bars.tail, 0};
+    int loaded = -1;
+    for (int i = 0; i < nc; ++i) {
+      const int c = nc - 1 - i;
+      if (i >= 2 && !wait_warp(&bars.empty[i & 1], ((i >> 1) & 1) ^ 1, status, 81)) break;
+      const bool ok = ld(smem + (i & 1) * Tiles<KP>::kBytes, &bars.full[i & 1],
+                         records + ((size_t)(blk.sq.chunk + c) * d.HV + blk.hv) * kRecordBytes, blk.sq.start + c * kC,
+                         min(kC, blk.sq.len - c * kC), tid, status);
+      loaded = i;
+      if (!ok) break;
+    }
+    for (int i = max(loaded - 1, 0); i <= loaded; ++i) wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 82);
+  }
+  __syncthreads();
+  if (w == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tm, kTmemCols);
+  }
+}
+
+template <typename F>
+cudaError_t allow_smem(F* f, uint32_t bytes) {
+  return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+cudaError_t make_maps(const Dims& d, const In& in, const bf16* v, long long vstride, bool vvec, Maps* m) {
+  const uint64_t steps = d.packed ? (uint64_t)d.T : (uint64_t)d.N * d.T;
+  cudaError_t e = cudaSuccess;
+  if (d.kvec) e = make_tmap_heads_bf16(&m->k, in.k, d.K, d.H, steps, d.ks);
+  if (e == cudaSuccess && d.qvec) e = make_tmap_heads_bf16(&m->q, in.q, d.K, d.H, steps, d.qs);
+  if (e == cudaSuccess && vvec) e = make_tmap_heads_bf16(&m->v, v, d.V, d.HV, steps, vstride);
+  return e;
+}
+
+template <int KP>
+cudaError_t run_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, bf16* o, float* s_final,
+                     bf16* S, bf16* R, int* status, cudaStream_t st) {
+  Maps maps = {};
+  cudaError_t e = make_maps(d, in, in.v, d.vs, d.vvec, &maps);
+  if (e == cudaSuccess) e = allow_smem(k_delta_scan<KP>, scan_smem<KP>());
+  if (e != cudaSuccess) return e;
+  SSD_LAUNCH("k_delta_scan", st,
+             k_delta_scan<KP><<<(unsigned)(d.N * d.HV), kThreads, scan_smem<KP>(), st>>>(d, tb, in, maps, records, o,
+                                                                                        s_final, S, R, status));
+  return cudaGetLastError();
+}
+template <int KP>
+cudaError_t run_rev(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const bf16* dout,
+                    const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status, cudaStream_t st) {
+  Maps maps = {};
+  cudaError_t e = make_maps(d, in, dout, (long long)d.HV * d.V, d.ovec, &maps);
+  if (e == cudaSuccess) e = allow_smem(k_delta_rev<KP>, scan_smem<KP>());
+  if (e != cudaSuccess) return e;
+  SSD_LAUNCH("k_delta_rev", st,
+             k_delta_rev<KP><<<(unsigned)(d.N * d.HV), kThreads, scan_smem<KP>(), st>>>(
+                 d, tb, in, maps, records, dout, ds_final, dv, ds0, dS, dY, status));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t forward_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, bf16* o, float* s_final,
+                         bf16* S, bf16* R, int* status, cudaStream_t st) {
+  return d.KP == 64 ? run_scan<64>(d, tb, in, records, o, s_final, S, R, status, st)
+                    : run_scan<128>(d, tb, in, records, o, s_final, S, R, status, st);
+}
+cudaError_t reverse_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const bf16* dout,
+                         const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status, cudaStream_t st) {
+  return d.KP == 64 ? run_rev<64>(d, tb, in, records, dout, ds_final, dv, ds0, dS, dY, status, st)
+                    : run_rev<128>(d, tb, in, records, dout, ds_final, dv, ds0, dS, dY, status, st);
+}
+
+}  // namespace delta
+}  // namespace ssd

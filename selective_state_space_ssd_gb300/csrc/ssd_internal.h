@@ -139,6 +139,10 @@ cudaError_t make_tmap_4d_bf16(CUtensorMap* m, const void* base, uint64_t d0, uin
 //   [b, T, G, N] bf16 (B, C): 64 x 1 x 64 x 1 boxes, coordinates (n, g, t, b).
 cudaError_t make_tmap_seq_bf16(CUtensorMap* m, const void* base, const Dims& d, uint64_t width);
 cudaError_t make_tmap_bc_bf16(CUtensorMap* m, const void* base, const Dims& d);
+// [steps, heads, width] bf16 with `stride` elements from a step to the next (a multiple of 8, as width): boxes of 64
+// steps of one head, 64 columns, coordinates (col, head, step).
+cudaError_t make_tmap_heads_bf16(CUtensorMap* m, const void* base, uint64_t width, uint64_t heads, uint64_t steps,
+                                 uint64_t stride);
 
 // Mamba-1 path (fp32).
 size_t m1_forward_ws(const Dims& d);

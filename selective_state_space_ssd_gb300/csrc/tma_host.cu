@@ -69,4 +69,12 @@ cudaError_t make_tmap_bc_bf16(CUtensorMap* m, const void* base, const Dims& d) {
   return make_tmap_4d_bf16(m, base, (uint64_t)d.N, (uint64_t)d.G, (uint64_t)d.T, (uint64_t)d.b, 64, 1, 64, 1);
 }
 
+cudaError_t make_tmap_heads_bf16(CUtensorMap* m, const void* base, uint64_t width, uint64_t heads, uint64_t steps,
+                                 uint64_t stride) {
+  const cuuint64_t dims[3] = {width, heads, steps};
+  const cuuint64_t strides[2] = {width * 2, stride * 2};
+  const cuuint32_t box[3] = {64, 1, 64};
+  return encode(m, base, 3, dims, strides, box);
+}
+
 }  // namespace ssd
