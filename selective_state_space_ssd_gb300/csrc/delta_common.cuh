@@ -54,14 +54,22 @@ struct In {
   float scale;
 };
 
-// The scans (ssd_delta_scan.cu).  S / R (null: not kept): the state entering each chunk and R, both bf16 and transposed
-// (S^T [VP][KP], R^T [VP][64]) and stored by 16-byte pieces of a row, [item][KP / 8][VP][8] and [item][8][VP][8], so that
-// the threads of neighbouring rows write neighbouring pieces.  o may be null (S and R only).  dS / dY of the reverse
-// scan: the gradient of the state leaving each chunk and dY, laid out like S and R.
+// The scans (ssd_delta_scan.cu).  S / R (null: not kept): the state entering each chunk and R, both bf16 and transposed,
+// as 128-byte-swizzled images: S^T [KP / 64][VP rows][64 keys], R^T [VP rows][64 steps].  o may be null (S and R only).
+// dS / dY of the reverse scan: the gradient of the state leaving each chunk, laid out like S, and dY by steps,
+// [ceil(VP / 64)][64 steps][64 columns].
 cudaError_t forward_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, bf16* o, float* s_final,
                          bf16* S, bf16* R, int* status, cudaStream_t st);
 cudaError_t reverse_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const bf16* dout,
                          const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status, cudaStream_t st);
+// dQ, dK, dbeta, dg of every chunk (ssd_delta_grads.cu).
+struct GradOut {
+  bf16 *dq, *dk;
+  void *dg, *dbeta;
+};
+cudaError_t chunk_grads(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const bf16* dout,
+                        const bf16* S, const bf16* R, const bf16* dS, const bf16* dY, const GradOut& out, int* status,
+                        cudaStream_t st);
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -142,15 +150,6 @@ __device__ __forceinline__ void load_rows(bf16* dst, int pitch, int width, const
   }
 }
 
-// Rows of `w8` 16-byte pieces, stored piece by piece ([w8][rows][8]), into a tile of rows.
-__device__ __forceinline__ void load_pieces(bf16* dst, int pitch, int w8, const bf16* src, int rows, int tid,
-                                            int nthreads) {
-  const uint32_t d = su32(dst);
-  for (int i = tid; i < rows * w8; i += nthreads) {
-    const int j = i / rows, r = i - j * rows;
-    cp16(d + 2u * (uint32_t)(r * pitch + 8 * j), src + (size_t)i * 8, true);
-  }
-}
 
 __device__ __forceinline__ float gate(const void* p, size_t i, bool is_bf16) {
   return is_bf16 ? __bfloat162float(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];

@@ -293,346 +293,6 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, uin
   }
 }
 
-// ---------------------------------------------------------------- dQ, dK, dbeta, dg of a chunk
-struct GradOut {
-  bf16 *dq, *dk;
-  void *dg, *dbeta;
-};
-
-__device__ __forceinline__ void put_gate(void* p, size_t i, float x, bool is_bf16) {
-  if (is_bf16)
-    static_cast<bf16*>(p)[i] = __float2bfloat16_rn(x);
-  else
-    static_cast<float*>(p)[i] = x;
-}
-
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
-}
-
-template <int KP>
-size_t grads_smem(int VP) {
-  return 2 * (size_t)(2 * kC * (KP + 8) + kC * (VP + 8) + 2 * VP * kTP + 2 * VP * (KP + 8) + 2 * kC * kTP) +
-         sizeof(float) * kGateRows * kC;
-}
-
-// Eight warps per (chunk, query/key head), its value heads one after another: warp w holds rows 16 (w % 4) .. + 15 and
-// half w / 4 of the columns of every product, and dQ, dK of the head stay in its accumulators (so the sum over the
-// value heads has one order).  Every factor of a decay is applied in fp32 to a product's result.
-template <int KP>
-__global__ void __launch_bounds__(256, 1) k_delta_grads(Dims d, Table tb, In in, const uint8_t* records, const bf16* __restrict__ dout,
-                                                         bool dovec, const bf16* __restrict__ Sst,
-                                                         const bf16* __restrict__ Rst, const bf16* __restrict__ dSst,
-                                                         const bf16* __restrict__ dYst, GradOut out) {
-  constexpr int kP = KP + 8, kNT = KP / 16;  // kNT: 8-column tiles of a warp's half of the key axis
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int VP = d.VP, vp = VP + 8;
-  bf16* Ks = reinterpret_cast<bf16*>(smem);
-  bf16* Qs = Ks + kC * kP;
-  bf16* Os = Qs + kC * kP;   // dO
-  bf16* Rs = Os + kC * vp;   // R^T [VP][64]
-  bf16* Ys = Rs + VP * kTP;  // dY^T
-  bf16* Ss = Ys + VP * kTP;  // S^T [VP][KP]
-  bf16* Ds = Ss + VP * kP;   // dS'^T
-  bf16* B1 = Ds + VP * kP;   // scale dO R^T . decay
-  bf16* B2 = B1 + kC * kTP;  // -dY R^T . beta decay
-  float* gt = reinterpret_cast<float*>(B2 + kC * kTP);
-  __shared__ float s_row[2][kC], s_col[4][kC], s_beta[2][kC], s_q[2][kC], s_z[2][kC], s_e[2][kC], s_yv[kC], s_ss[8];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int g4 = lane >> 2, t2 = 2 * (lane & 3);
-  const int r0 = 16 * (w & 3), half = w >> 2, rb = w & 3;
-  const int c = blockIdx.x, hk = blockIdx.y;
-  const Chunk ch = chunk_of(d, tb, c);
-  if (ch.rows == 0) return;
-  load_rows(Ks, kP, KP, in.k + (long long)ch.first * d.ks + (long long)hk * d.K, d.ks, ch.rows, d.K, d.kvec, tid, 256);
-  load_rows(Qs, kP, KP, in.q + (long long)ch.first * d.qs + (long long)hk * d.K, d.qs, ch.rows, d.K, d.qvec, tid, 256);
-  cp_commit();
-  const uint32_t ka = su32(Ks), qa = su32(Qs), oa = su32(Os), ra = su32(Rs), ya = su32(Ys), sa = su32(Ss),
-                 dsa = su32(Ds), b1a = su32(B1), b2a = su32(B2);
-  float kk[4][4], qk[4][4], dQ[kNT][4], dK[kNT][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) kk[i][j] = qk[i][j] = 0.f;
-#pragma unroll
-  for (int i = 0; i < kNT; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dQ[i][j] = dK[i][j] = 0.f;
-  for (int gi = 0; gi < d.G; ++gi) {
-    const int hv = hk * d.G + gi;
-    const size_t item = (size_t)c * d.HV + hv;
-    load_rows(Os, vp, VP, dout + ((long long)ch.first * d.HV + hv) * d.V, (long long)d.HV * d.V, ch.rows, d.V, dovec,
-              tid, 256);
-    load_pieces(Rs, kTP, kC / 8, Rst + item * kC * VP, VP, tid, 256);
-    load_pieces(Ys, kTP, kC / 8, dYst + item * kC * VP, VP, tid, 256);
-    load_pieces(Ss, kP, KP / 8, Sst + item * VP * KP, VP, tid, 256);
-    load_pieces(Ds, kP, KP / 8, dSst + item * VP * KP, VP, tid, 256);
-    for (int i = tid; i < kGateRows * kC / 4; i += 256)
-      cp16(su32(gt + 4 * i), records + item * kRecordBytes + kRecordGates + 16 * i, true);
-    cp_commit();
-    cp_wait<0>();
-    __syncthreads();
-    if (gi == 0) {
-#pragma unroll
-      for (int kb = 0; kb < KP / 16; ++kb) {
-        uint32_t ak[4], aq[4];
-        ldm4(ak, by_col(ka, kP, r0, 16 * kb, lane));
-        ldm4(aq, by_col(qa, kP, r0, 16 * kb, lane));
-#pragma unroll
-        for (int jb = 0; jb < 2; ++jb) {
-          uint32_t b[4];
-          ldm4(b, by_row(ka, kP, 32 * half + 16 * jb, 16 * kb, lane));
-          mma(kk[2 * jb], ak, b[0], b[1]);
-          mma(kk[2 * jb + 1], ak, b[2], b[3]);
-          mma(qk[2 * jb], aq, b[0], b[1]);
-          mma(qk[2 * jb + 1], aq, b[2], b[3]);
-        }
-      }
-    }
-    const float *eg = gt, *ee = gt + kC, *be = gt + 2 * kC, *gh = gt + 3 * kC, *gl = gt + 4 * kC;
-    // scores: rows i, columns j = 32 half ..
-    float m1[4][4], m2[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) m1[i][j] = m2[i][j] = 0.f;
-    if (32 * half <= r0 + 15)
-      for (int vb = 0; vb < VP; vb += 16) {
-        uint32_t ao[4], ay[4];
-        ldm4(ao, by_col(oa, vp, r0, vb, lane));
-        ldm4t(ay, by_row(ya, kTP, vb, r0, lane));
-#pragma unroll
-        for (int jb = 0; jb < 2; ++jb) {
-          uint32_t b[4];
-          ldm4t(b, by_col(ra, kTP, vb, 32 * half + 16 * jb, lane));
-          mma(m1[2 * jb], ao, b[0], b[1]);
-          mma(m1[2 * jb + 1], ao, b[2], b[3]);
-          mma(m2[2 * jb], ay, b[0], b[1]);
-          mma(m2[2 * jb + 1], ay, b[2], b[3]);
-        }
-      }
-    {
-      float rsum[2] = {0.f, 0.f}, bsum[2] = {0.f, 0.f};
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const int j = 32 * half + 8 * nt + t2;
-        float csum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int i = r0 + g4 + 8 * hh;
-          float p[2], a[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const bool le = j + e <= i, lt = j + e < i;
-            const float dec = le ? __expf((gh[i] - gh[j + e]) + (gl[i] - gl[j + e])) : 0.f;
-            const float dp = in.scale * m1[nt][2 * hh + e] * dec;   // d (q_i . k_j)
-            const float da = lt ? -m2[nt][2 * hh + e] * dec : 0.f;  // d (beta_i k_i . k_j)
-            p[e] = le ? dp : 0.f;
-            a[e] = be[i] * da;
-            const float kkv = kk[nt][2 * hh + e];
-            const float mm = p[e] * qk[nt][2 * hh + e] + a[e] * kkv;
-            rsum[hh] += mm;
-            csum[e] += mm;
-            bsum[hh] += da * kkv;
-          }
-          *reinterpret_cast<uint32_t*>(B1 + i * kTP + j) = pack(p[0], p[1]);
-          *reinterpret_cast<uint32_t*>(B2 + i * kTP + j) = pack(a[0], a[1]);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = csum[e];
-          x += __shfl_xor_sync(0xffffffffu, x, 4);
-          x += __shfl_xor_sync(0xffffffffu, x, 8);
-          x += __shfl_xor_sync(0xffffffffu, x, 16);
-          if (g4 == 0) s_col[rb][j + e] = x;
-        }
-      }
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const float x = quad_sum(rsum[hh]), y = quad_sum(bsum[hh]);
-        if ((lane & 3) == 0) {
-          s_row[half][r0 + g4 + 8 * hh] = x;
-          s_beta[half][r0 + g4 + 8 * hh] = y;
-        }
-      }
-    }
-    // the products with the states: rows t, columns key = half KP/2 ..
-#pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const uint32_t aa = pass == 0 ? oa : pass == 1 ? ya : ra, ba = pass == 2 ? dsa : sa;
-      float z[kNT][4];
-#pragma unroll
-      for (int i = 0; i < kNT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z[i][j] = 0.f;
-      for (int vb = 0; vb < VP; vb += 16) {
-        uint32_t a[4];
-        if (pass == 0)
-          ldm4(a, by_col(aa, vp, r0, vb, lane));
-        else
-          ldm4t(a, by_row(aa, kTP, vb, r0, lane));
-#pragma unroll
-        for (int nb = 0; nb < kNT / 2; ++nb) {
-          uint32_t b[4];
-          ldm4t(b, by_col(ba, kP, vb, half * (KP / 2) + 16 * nb, lane));
-          mma(z[2 * nb], a, b[0], b[1]);
-          mma(z[2 * nb + 1], a, b[2], b[3]);
-        }
-      }
-      float sum[2] = {0.f, 0.f};
-      const bf16* dotted = pass == 0 ? Qs : Ks;
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int t = r0 + g4 + 8 * hh;
-        const float f = pass == 0 ? in.scale * eg[t] : pass == 1 ? -be[t] * eg[t] : ee[t];
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-          const uint32_t x = *reinterpret_cast<const uint32_t*>(dotted + t * kP + half * (KP / 2) + 8 * nt + t2);
-          const float z0 = z[nt][2 * hh], z1 = z[nt][2 * hh + 1];
-          sum[hh] += z0 * lo_f(x) + z1 * hi_f(x);
-          float(&acc)[4] = pass == 0 ? dQ[nt] : dK[nt];
-          acc[2 * hh] = fmaf(f, z0, acc[2 * hh]);
-          acc[2 * hh + 1] = fmaf(f, z1, acc[2 * hh + 1]);
-        }
-        const float y = quad_sum(sum[hh]);
-        if ((lane & 3) == 0) (pass == 0 ? s_q : pass == 1 ? s_z : s_e)[half][t] = y;
-      }
-    }
-    {  // <dS', S>
-      float x = 0.f;
-      for (int i = tid; i < VP * KP / 8; i += 256) {
-        const int r = i / (KP / 8), cc = 8 * (i % (KP / 8));
-        const uint4 a = *reinterpret_cast<const uint4*>(Ss + r * kP + cc);
-        const uint4 b = *reinterpret_cast<const uint4*>(Ds + r * kP + cc);
-        x += lo_f(a.x) * lo_f(b.x) + hi_f(a.x) * hi_f(b.x) + lo_f(a.y) * lo_f(b.y) + hi_f(a.y) * hi_f(b.y) +
-             lo_f(a.z) * lo_f(b.z) + hi_f(a.z) * hi_f(b.z) + lo_f(a.w) * lo_f(b.w) + hi_f(a.w) * hi_f(b.w);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (lane == 0) s_ss[w] = x;
-    }
-    {  // dY . V of a row, four lanes each
-      const int t = tid >> 2;
-      float x = 0.f;
-      if (t < ch.rows) {
-        const bf16* vr = in.v + (long long)(ch.first + t) * d.vs + (long long)hv * d.V;
-        for (int i = 8 * (tid & 3); i < d.V; i += 32) {  // in one order, however V is read
-          uint32_t a[4];
-          if (d.vvec) {
-            const uint4 y = *reinterpret_cast<const uint4*>(vr + i);
-            a[0] = y.x, a[1] = y.y, a[2] = y.z, a[3] = y.w;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              a[j] = pack(i + 2 * j < d.V ? __bfloat162float(vr[i + 2 * j]) : 0.f,
-                          i + 2 * j + 1 < d.V ? __bfloat162float(vr[i + 2 * j + 1]) : 0.f);
-          }
-          const bf16* y = Ys + i * kTP + t;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            x = fmaf(lo_f(a[j]), __bfloat162float(y[2 * j * kTP]),
-                     fmaf(hi_f(a[j]), __bfloat162float(y[(2 * j + 1) * kTP]), x));
-        }
-      }
-      x = quad_sum(x);
-      if ((tid & 3) == 0) s_yv[t] = x;
-    }
-    __syncthreads();
-    // the score matrices times K and Q (below the diagonal: k-blocks up to rb; transposed: from rb)
-#pragma unroll
-    for (int jb = 0; jb < 4; ++jb) {
-      uint32_t a1[4], a2[4], a1t[4], a2t[4];
-      const bool lower = jb <= rb, upper = jb >= rb;
-      if (lower) {
-        ldm4(a1, by_col(b1a, kTP, r0, 16 * jb, lane));
-        ldm4(a2, by_col(b2a, kTP, r0, 16 * jb, lane));
-      }
-      if (upper) {
-        ldm4t(a1t, by_row(b1a, kTP, 16 * jb, r0, lane));
-        ldm4t(a2t, by_row(b2a, kTP, 16 * jb, r0, lane));
-      }
-#pragma unroll
-      for (int nb = 0; nb < kNT / 2; ++nb) {
-        uint32_t bk[4], bq[4];
-        ldm4t(bk, by_col(ka, kP, 16 * jb, half * (KP / 2) + 16 * nb, lane));
-        if (lower) {
-          mma(dQ[2 * nb], a1, bk[0], bk[1]);
-          mma(dQ[2 * nb + 1], a1, bk[2], bk[3]);
-          mma(dK[2 * nb], a2, bk[0], bk[1]);
-          mma(dK[2 * nb + 1], a2, bk[2], bk[3]);
-        }
-        if (upper) {
-          ldm4t(bq, by_col(qa, kP, 16 * jb, half * (KP / 2) + 16 * nb, lane));
-          mma(dK[2 * nb], a1t, bq[0], bq[1]);
-          mma(dK[2 * nb + 1], a1t, bq[2], bq[3]);
-          mma(dK[2 * nb], a2t, bk[0], bk[1]);
-          mma(dK[2 * nb + 1], a2t, bk[2], bk[3]);
-        }
-      }
-    }
-    if (w == 0) {  // dbeta, dG and its sums from the right, two steps a lane
-      float dG[2], e_all = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 2 * lane + i;
-        const float z = s_z[0][t] + s_z[1][t], e = ee[t] * (s_e[0][t] + s_e[1][t]);
-        const float col = (s_col[0][t] + s_col[1][t]) + (s_col[2][t] + s_col[3][t]);
-        dG[i] = (s_row[0][t] + s_row[1][t]) - col + in.scale * eg[t] * (s_q[0][t] + s_q[1][t]) - be[t] * eg[t] * z - e;
-        e_all += e;
-        if (t < ch.rows)
-          put_gate(out.dbeta, (size_t)(ch.first + t) * d.HV + hv,
-                   s_yv[t] - eg[t] * z + (s_beta[0][t] + s_beta[1][t]), d.gate_bf16);
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) e_all += __shfl_xor_sync(0xffffffffu, e_all, o);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += s_ss[i];
-      const float end = e_all + eg[kC - 1] * ss;
-      float sum = dG[0] + dG[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += y;
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 2 * lane + i;
-        if (t < ch.rows)
-          put_gate(out.dg, (size_t)(ch.first + t) * d.HV + hv, end + (i ? sum - dG[0] : sum), d.gate_bf16);
-      }
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int hh = 0; hh < 2; ++hh) {
-    const int t = r0 + g4 + 8 * hh;
-    if (t >= ch.rows) continue;
-    const size_t row = ((size_t)(ch.first + t) * d.H + hk) * d.K;
-#pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      const int k = half * (KP / 2) + 8 * nt + t2;
-      const float q0 = dQ[nt][2 * hh], q1 = dQ[nt][2 * hh + 1], k0 = dK[nt][2 * hh], k1 = dK[nt][2 * hh + 1];
-      if ((d.K & 1) == 0) {
-        if (k < d.K) {
-          *reinterpret_cast<uint32_t*>(out.dq + row + k) = pack(q0, q1);
-          *reinterpret_cast<uint32_t*>(out.dk + row + k) = pack(k0, k1);
-        }
-      } else {
-        if (k < d.K) {
-          out.dq[row + k] = __float2bfloat16_rn(q0);
-          out.dk[row + k] = __float2bfloat16_rn(k0);
-        }
-        if (k + 1 < d.K) {
-          out.dq[row + k + 1] = __float2bfloat16_rn(q1);
-          out.dk[row + k + 1] = __float2bfloat16_rn(k1);
-        }
-      }
-    }
-  }
-}
-
 // ---------------------------------------------------------------- host side
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -666,7 +326,7 @@ Grads carve_grads(const Dims& d, Carver& cv) {
   const size_t items = (size_t)d.nc * d.HV;
   Grads g;
   g.dS = cv.take<bf16>(items * d.VP * d.KP);
-  g.dY = cv.take<bf16>(items * kC * d.VP);
+  g.dY = cv.take<bf16>(items * kC * ((d.VP + 63) / 64 * 64));
   return g;
 }
 
@@ -718,16 +378,6 @@ cudaError_t run_prep(const Dims& d, const Table& tb, const In& in, uint8_t* reco
   return cudaGetLastError();
 }
 
-template <int KP>
-cudaError_t run_grads(const Dims& d, const Table& tb, const In& in, const Kept& kept, const Grads& gr, const bf16* dout,
-                      const GradOut& out, cudaStream_t st) {
-  cudaError_t e = allow_smem(k_delta_grads<KP>, grads_smem<KP>(d.VP));
-  if (e != cudaSuccess) return e;
-  SSD_LAUNCH("k_delta_grads", st,
-             k_delta_grads<KP><<<dim3((unsigned)d.nc, (unsigned)d.H), 256, grads_smem<KP>(d.VP), st>>>(
-                 d, tb, in, kept.records, dout, d.ovec, kept.S, kept.R, gr.dS, gr.dY, out));
-  return cudaGetLastError();
-}
 cudaError_t prepare(const Dims& d, const Table& tb, const In& in, uint8_t* records, const int* cu, int* status,
                     cudaStream_t st) {
   return d.KP == 64 ? run_prep<64>(d, tb, in, records, cu, status, st) : run_prep<128>(d, tb, in, records, cu, status, st);
@@ -887,8 +537,7 @@ ssd_status ssd_delta_backward(const ssd_delta_problem* prob, const void* dout, c
   if (e == cudaSuccess)
     e = reverse_scan(d, tb, in, kept.records, (const bf16*)dout, ds_final, (bf16*)dv, ds0, gr.dS, gr.dY, (int*)ws, st);
   if (e == cudaSuccess)
-    e = d.KP == 64 ? run_grads<64>(d, tb, in, kept, gr, (const bf16*)dout, out, st)
-                   : run_grads<128>(d, tb, in, kept, gr, (const bf16*)dout, out, st);
+    e = chunk_grads(d, tb, in, kept.records, (const bf16*)dout, kept.S, kept.R, gr.dS, gr.dY, out, (int*)ws, st);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

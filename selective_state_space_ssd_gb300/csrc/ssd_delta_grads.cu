@@ -1,0 +1,513 @@
+// dQ, dK, dbeta and dg of the chunked delta rule, every (chunk, query/key head) by itself, on tcgen05.  With S entering
+// the chunk, dS' the gradient of the state leaving it, E_t = e^{G_end - G_t}, D_ij = e^{G_i - G_j} (j <= i):
+//     B1_ij = scale D_ij (dO R^T)_ij  (j <= i)          the gradient of q_i . k_j
+//     B2_ij = -D_ij (dY R^T)_ij       (j < i)           the gradient of beta_i k_i . k_j, over beta_i
+//     dQ    = scale e^G dO S^T + B1 K
+//     H     = B2 K - e^G dY S^T,        dK = beta H + dK',    dK' = E R dS'^T + B1^T Q + (beta B2)^T K
+//     dbeta = k_t . H_t + dY_t . V_t
+// and the gradient of G without any further product: every term of the loss that holds e^{G_i} or D_ij holds q_i, k_i or
+// k_j once, so
+//     dG_t = q_t . dQ_t + beta_t k_t . H_t - k_t . dK'_t,     dG_end += sum_t E_t k_t . (R dS'^T)_t + e^{G_end} <dS', S>
+// and dg is its sum from the right.
+//
+// Results are transposed (a TMEM lane is a key): six groups of MMAs a value head, the two that read S and the two that
+// read [dO; dY] stacked on 128 rows.  The decays never touch an operand but B1, B2: everything else is scaled in fp32
+// where it leaves tensor memory.  What a head reads (144 KB for K = V = 128) comes by TMA and bulk copies while the head
+// before is in its second half; that traffic is what bounds the kernel.
+//
+// Sixteen warps: 0-7 the elementwise work, two a lane quadrant (halves of the columns); 8 the MMAs; 9-11 copies; 12-15 the
+// two sums that need no product (dY . V by rows, <dS', S>).
+#include "delta_tc.cuh"
+
+namespace ssd {
+namespace delta {
+namespace {
+
+constexpr int kWorkWarps = 8, kSumWarps = 4, kMmaWarp = kWorkWarps, kLoadWarp0 = kMmaWarp + 1,
+              kSumWarp0 = kLoadWarp0 + kLoadWarps;
+constexpr int kThreads = 32 * (kSumWarp0 + kSumWarps);
+constexpr int kWorkBar = 1;
+
+// Shared memory.  QK (two of them): [Q; K] rows of the head; OY: [dO; dY] rows; R^T, S^T, dS'^T images; B: [B1; B2] rows
+// and beta B2; Out: dQ or dK rows on their way out.
+constexpr uint32_t kQK = 32768, kOY = 32768, kRt = 16384, kSt = 32768, kB = 16384, kBb = 8192, kOutT = 16384;
+constexpr uint32_t oOY = 2 * kQK, oR = oOY + kOY, oS = oR + kRt, oD = oS + kSt, oB = oD + kSt, oBb = oB + kB,
+                   oOut = oBb + kBb, oGates = oOut + kOutT, kSmem = oGates + 2 * kGateRows * kC * 4 + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+
+// Columns of tensor memory: the scores [dO; dY] R^T, then dS'^T's product; S's two products; [B1; B2] K; dK' 's scores.
+constexpr int cM = 0, cZ3 = 64, cZ = 128, cW = 256, cD = 384;
+constexpr uint32_t kTmemCols = 512;
+
+struct Bars {
+  uint64_t qk[2], qk_free[2], full, empty, tail, m, z, b, w, free, sums, sums_read, done;
+};
+struct Maps {
+  CUtensorMap k, q, dout;
+};
+
+// The value heads of this block's (chunk, query/key head) units, one after another.
+struct Work {
+  const Dims& d;
+  const Table& tb;
+  int unit, gi, hk, c;
+  Chunk ch;
+  int step = 0, qkn = 0;  // value heads and units so far
+  __device__ Work(const Dims& dd, const Table& t) : d(dd), tb(t), unit(blockIdx.x), gi(0) { find(); }
+  __device__ void find() {  // the next unit that is a chunk of some sequence
+    const int units = d.nc * d.H;
+    for (; unit < units; unit += gridDim.x) {
+      c = unit / d.H;
+      hk = unit - c * d.H;
+      ch = chunk_of(d, tb, c);
+      if (ch.rows > 0) return;
+    }
+    unit = -1;
+  }
+  __device__ bool more() const { return unit >= 0; }
+  __device__ bool last() const { return gi + 1 == d.G; }
+  __device__ int hv() const { return hk * d.G + gi; }
+  __device__ size_t item() const { return (size_t)c * d.HV + hv(); }
+  __device__ void next() {
+    ++step;
+    if (++gi == d.G) {
+      gi = 0;
+      ++qkn;
+      unit += gridDim.x;
+      find();
+    }
+  }
+};
+
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float x) {
+  const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x = fmaf(lo_f(p[i]), lo_f(q[i]), fmaf(hi_f(p[i]), hi_f(q[i]), x));
+  return x;
+}
+
+// x[i] summed over the warp's lanes; lane l gets the sum of x[l % 8].
+__device__ __forceinline__ float lane_sums(float (&x)[8], int lane) {
+#pragma unroll
+  for (int o = 4; o; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float give = up ? x[i] : x[i + o], keep = up ? x[i + o] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  x[0] += __shfl_xor_sync(0xffffffffu, x[0], 8);
+  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
+}
+
+__device__ __forceinline__ void put_gate(void* p, size_t i, float x, bool is_bf16) {
+  if (is_bf16)
+    static_cast<bf16*>(p)[i] = __float2bfloat16_rn(x);
+  else
+    static_cast<float*>(p)[i] = x;
+}
+
+// The [64 steps][128 keys] tile to rows of dq or dk.
+__device__ __forceinline__ void store_rows(const bf16* tile, bf16* dst, long long stride, int rows, int K, int tid) {
+  if (K % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (tid >> 4) + 16 * i, c = 8 * (tid & 15);
+      if (r < rows && c < K)
+        *reinterpret_cast<uint4*>(dst + (long long)r * stride + c) = *reinterpret_cast<const uint4*>(tile + r * 128 + c);
+    }
+  } else {
+    for (int r = tid >> 7; r < rows; r += 2)
+      if ((tid & 127) < K) dst[(long long)r * stride + (tid & 127)] = tile[r * 128 + (tid & 127)];
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_delta_grads(Dims d, Table tb, In in, const __grid_constant__ Maps maps, const uint8_t* records, const bf16* dout,
+                  const bf16* Sst, const bf16* Rst, const bf16* dSst, const bf16* dYst, GradOut out, int* status) {
+  extern __shared__ uint8_t raw[];
+  __shared__ Bars bars;
+  __shared__ uint32_t tslot;
+  __shared__ float s_yv[kC], s_ss[kSumWarps], s_a[4][kC], s_h[4][kC], s_e[kWorkWarps];
+  uint8_t* smem = aligned_smem(raw);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.qk[i], kLoadWarps + 1);
+      mbar_init(&bars.qk_free[i], 1 + kWorkWarps);
+    }
+    mbar_init(&bars.full, kLoadWarps + 1);
+    mbar_init(&bars.empty, 1 + kSumWarps + kWorkWarps);
+    mbar_init(&bars.tail, 1);
+    mbar_init(&bars.m, 1);
+    mbar_init(&bars.z, 1);
+    mbar_init(&bars.b, kWorkWarps);
+    mbar_init(&bars.w, 1);
+    mbar_init(&bars.free, kWorkWarps);
+    mbar_init(&bars.sums, kSumWarps);
+    mbar_init(&bars.sums_read, kWorkWarps);
+    mbar_init(&bars.done, 1);
+    mbar_init_fence();
+  }
+  if (w == kMmaWarp) tmem_alloc(&tslot, kTmemCols);
+  if (d.KP == 64) {  // the key tiles' second atoms, which no copy writes
+    for (int i = threadIdx.x; i < 1024; i += kThreads) {
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      reinterpret_cast<uint4*>(smem + 16384)[i] = z;
+      reinterpret_cast<uint4*>(smem + kQK + 16384)[i] = z;
+      reinterpret_cast<uint4*>(smem + oS + 16384)[i] = z;
+      reinterpret_cast<uint4*>(smem + oD + 16384)[i] = z;
+    }
+  }
+  fence_proxy_async();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = tslot;
+  const uint32_t satom = d.KP == 64 ? 16384u : (uint32_t)d.VP * 128u;  // from one 64-key atom of S^T to the next
+  Work wk(d, tb);
+
+  if (w < kWorkWarps) {
+    const int lane0 = 32 * (w & 3), l = lane0 + lane, hf = w >> 2, tid = threadIdx.x;
+    const int i = l & 63;               // the scores' row; lanes 64 .. 127 hold dY's
+    const bool is_y = l >= 64;
+    bf16* tile = reinterpret_cast<bf16*>(smem + oOut);
+    float dQ[32], dK[32];  // key l, steps 32 hf ..
+#pragma unroll
+    for (int j = 0; j < 32; ++j) dQ[j] = dK[j] = 0.f;
+    for (; wk.more(); wk.next()) {
+      const uint32_t ph = wk.step & 1;
+      const float* gt = reinterpret_cast<const float*>(smem + oGates) + ph * kGateRows * kC;
+      const float *eg = gt, *ee = gt + kC, *be = gt + 2 * kC, *gh = gt + 3 * kC, *gl = gt + 4 * kC;
+      bool ok = wait_warp(&bars.full, ph, status, 101);
+      // (an arrival here keeps the copies within one phase of this wait)
+      if (lane == 0) mbar_arrive(&bars.empty);
+      ok = ok && wait_warp(&bars.m, ph, status, 102);
+      tc_fence_after();
+      {  // B1, B2, beta B2
+        const float hi = gh[i], lo = gl[i], bi = be[i], f = is_y ? -1.f : in.scale;
+        const int top = is_y ? i - 1 : i;  // the last column below the diagonal (dY) or on it (dO)
+        const bool some = 32 * hf <= (lane0 & 63) + 31;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float x[16];
+          uint32_t p[8], q[8];
+          if (some && ok) {
+            ld16(taddr(tm, lane0, cM + 32 * hf + 16 * b), x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int j = 32 * hf + 16 * b + e;
+              x[e] = j <= top ? f * x[e] * __expf((hi - gh[j]) + (lo - gl[j])) : 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            p[e] = pack(x[2 * e], x[2 * e + 1]);
+            q[e] = pack(bi * x[2 * e], bi * x[2 * e + 1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = 4 * hf + 2 * b + e;
+            *reinterpret_cast<uint4*>(smem + oB + sw128_chunk(l, j)) = make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
+            if (is_y)
+              *reinterpret_cast<uint4*>(smem + oBb + sw128_chunk(i, j)) = make_uint4(q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
+          }
+        }
+        fence_proxy_async();
+        signal_read(&bars.b, lane);
+      }
+      ok = ok && wait_warp(&bars.qk[wk.qkn & 1], (wk.qkn >> 1) & 1, status, 106) &&
+           wait_warp(&bars.z, ph, status, 103) && wait_warp(&bars.w, ph, status, 104);
+      tc_fence_after();
+      const uint8_t* qk = smem + (wk.qkn & 1) * kQK + (l >> 6) * 16384 + 2 * (l & 7);
+      float e_all = 0.f;  // this key's share of sum_t E_t k_t.(R dS'^T)_t
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float sa[8], sh[8];  // its shares of q.dQ - k.dK' and k.H of eight steps
+        uint32_t z[8], s[8];
+        tmem_ld8_nowait(taddr(tm, lane0, cZ + 32 * hf + 8 * b), z);
+        tmem_ld8_nowait(taddr(tm, lane0, cW + 32 * hf + 8 * b), s);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int t = 32 * hf + 8 * b + e;
+          const float q = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(t, (l & 63) >> 3)));
+          const float x = fmaf(in.scale * eg[t], __uint_as_float(z[e]), __uint_as_float(s[e]));
+          dQ[8 * b + e] += x;
+          sa[e] = q * x;
+        }
+        uint32_t y[8], u[8];
+        tmem_ld8_nowait(taddr(tm, lane0, cZ + 64 + 32 * hf + 8 * b), z);
+        tmem_ld8_nowait(taddr(tm, lane0, cW + 64 + 32 * hf + 8 * b), s);
+        tmem_ld8_nowait(taddr(tm, lane0, cZ3 + 32 * hf + 8 * b), y);
+        tmem_ld8_nowait(taddr(tm, lane0, cD + 32 * hf + 8 * b), u);
+        tmem_wait_ld();
+        if (b == 3) signal_read(&bars.free, lane);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int t = 32 * hf + 8 * b + e;
+          const float k = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(kC + t, (l & 63) >> 3)));
+          const float h = fmaf(-eg[t], __uint_as_float(z[e]), __uint_as_float(s[e]));
+          const float r = ee[t] * __uint_as_float(y[e]);
+          const float m = r + __uint_as_float(u[e]);
+          dK[8 * b + e] += fmaf(be[t], h, m);
+          sh[e] = k * h;
+          e_all = fmaf(k, r, e_all);
+          sa[e] = fmaf(-k, m, sa[e]);
+        }
+        const float a = lane_sums(sa, lane), h = lane_sums(sh, lane);
+        if (lane < 8) {
+          s_a[w & 3][32 * hf + 8 * b + lane] = a;
+          s_h[w & 3][32 * hf + 8 * b + lane] = h;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) e_all += __shfl_xor_sync(0xffffffffu, e_all, o);
+      if (lane == 0) {
+        s_e[w] = e_all;
+        if (wk.last()) mbar_arrive(&bars.qk_free[wk.qkn & 1]);
+      }
+      ok = ok && wait_warp(&bars.sums, ph, status, 105);
+      if (named_bar_or(kWorkBar, 32 * kWorkWarps, !ok)) break;
+      const Chunk ch = wk.ch;
+      const int hv = wk.hv();
+      if (w == 0) {  // two steps a lane
+        float dG[2], all = lane < kWorkWarps ? s_e[lane] : 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int t = 2 * lane + n;
+          const float a = (s_a[0][t] + s_a[1][t]) + (s_a[2][t] + s_a[3][t]);
+          const float h = (s_h[0][t] + s_h[1][t]) + (s_h[2][t] + s_h[3][t]);
+          dG[n] = fmaf(be[t], h, a);
+          if (t < ch.rows) put_gate(out.dbeta, (size_t)(ch.first + t) * d.HV + hv, h + s_yv[t], d.gate_bf16);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        const float end = fmaf(eg[kC - 1], (s_ss[0] + s_ss[1]) + (s_ss[2] + s_ss[3]), all);
+        float sum = dG[0] + dG[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float y = __shfl_down_sync(0xffffffffu, sum, o);
+          if (lane + o < 32) sum += y;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int t = 2 * lane + n;
+          if (t < ch.rows)
+            put_gate(out.dg, (size_t)(ch.first + t) * d.HV + hv, end + (n ? sum - dG[0] : sum), d.gate_bf16);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.sums_read);
+      if (wk.last()) {
+        const long long stride = (long long)d.H * d.K;
+        const size_t at = ((size_t)ch.first * d.H + wk.hk) * d.K;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          float(&x)[32] = which ? dK : dQ;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            tile[(32 * hf + j) * 128 + l] = __float2bfloat16_rn(x[j]);
+            x[j] = 0.f;
+          }
+          named_bar(kWorkBar, 32 * kWorkWarps);
+          store_rows(tile, (which ? out.dk : out.dq) + at, stride, ch.rows, d.K, tid);
+          named_bar(kWorkBar, 32 * kWorkWarps);
+        }
+      } else {
+        named_bar(kWorkBar, 32 * kWorkWarps);  // the sums have been read before the next head writes its own
+      }
+    }
+  } else if (w == kMmaWarp) {
+    constexpr uint32_t iM = idesc_bf16(128, 64, false, true), iZ = idesc_bf16(128, 128, true, false),
+                       iR = idesc_bf16(128, 64, true, true), iW = idesc_bf16(128, 128, true, false);
+    const int nv = d.VP / 16;
+    for (; wk.more(); wk.next()) {
+      const uint32_t ph = wk.step & 1;
+      const uint8_t* qk = smem + (wk.qkn & 1) * kQK;
+      if (!wait_warp(&bars.full, ph, status, 111)) break;
+      tc_fence_after();
+      const uint64_t oy = kdesc(smem + oOY, 128, 0), rt = mdesc(smem + oR, d.VP, 0);
+      const uint64_t sm = sdesc_sw128(smem_u32(smem + oS), satom, 1024), dm = sdesc_sw128(smem_u32(smem + oD), satom, 1024);
+      if (elect_one()) {
+        for (int vb = 0; vb < nv; ++vb) mma_bf16(tm + cM, oy + kdesc_step(128, 16 * vb), rt + mdesc_step(16 * vb), iM, vb > 0);
+        mma_commit(&bars.m);
+      }
+      __syncwarp();
+      if (wk.step > 0 && !wait_warp(&bars.free, ph ^ 1, status, 112)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        for (int vb = 0; vb < nv; ++vb) mma_bf16(tm + cZ, sm + mdesc_step(16 * vb), oy + kdesc_step(128, 16 * vb), iZ, vb > 0);
+        for (int vb = 0; vb < nv; ++vb) mma_bf16(tm + cZ3, dm + mdesc_step(16 * vb), rt + mdesc_step(16 * vb), iR, vb > 0);
+        mma_commit(&bars.z);
+        mma_commit(&bars.empty);
+      }
+      __syncwarp();
+      if (wk.gi == 0 && !wait_warp(&bars.qk[wk.qkn & 1], (wk.qkn >> 1) & 1, status, 113)) break;
+      if (!wait_warp(&bars.b, ph, status, 114)) break;
+      tc_fence_after();
+      const uint64_t qm = sdesc_sw128(smem_u32(qk), 16384, 1024), km = sdesc_sw128(smem_u32(qk) + kC * 128, 16384, 1024);
+      const uint64_t bk = kdesc(smem + oB, 128, 0);
+      if (elect_one()) {
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) mma_bf16(tm + cW, km + mdesc_step(16 * jb), bk + kdesc_step(128, 16 * jb), iW, jb > 0);
+        // the transposed scores: row block ib has columns j <= 16 ib + 15
+#pragma unroll
+        for (int ib = 3; ib >= 0; --ib) {
+          const uint32_t id = idesc_bf16(128, 16 * (ib + 1), true, true);
+          mma_bf16(tm + cD, qm + mdesc_step(16 * ib), mdesc(smem + oB, 128, 16 * ib), id, ib < 3);
+          mma_bf16(tm + cD, km + mdesc_step(16 * ib), mdesc(smem + oBb, kC, 16 * ib), id, true);
+        }
+        mma_commit(&bars.w);
+        if (wk.last()) mma_commit(&bars.qk_free[wk.qkn & 1]);
+      }
+      __syncwarp();
+    }
+    if (elect_one()) mma_commit(&bars.done);
+    __syncwarp();
+    wait_warp(&bars.done, 0, status, 115);
+  } else if (w < kSumWarp0) {
+    const int tid = threadIdx.x - 32 * kLoadWarp0;
+    uint32_t tails = 0;
+    bool ok = true;
+    int loaded = -1, units = -1;
+    const int na = d.KP / 64, va = (d.VP + 63) / 64;
+    for (; wk.more() && ok; wk.next()) {
+      const uint32_t ph = wk.step & 1;
+      const int first = wk.ch.first, rows = wk.ch.rows;
+      const bool cut = rows < kC;
+      if (wk.gi == 0) {
+        const int s = wk.qkn & 1;
+        if (wk.qkn >= 2 && !wait_warp(&bars.qk_free[s], ((wk.qkn >> 1) & 1) ^ 1, status, 121)) break;
+        uint8_t* qt = smem + s * kQK;
+        uint64_t* bar = cut ? &bars.tail : &bars.qk[s];
+        if (tid == 0) {
+          mbar_expect_tx(bar, kC * 128 * na * ((d.qvec ? 1 : 0) + (d.kvec ? 1 : 0)));
+          for (int a = 0; a < na; ++a) {
+            if (d.qvec) tma_load_3d(qt + a * 16384, &maps.q, 64 * a, wk.hk, first, bar);
+            if (d.kvec) tma_load_3d(qt + a * 16384 + kC * 128, &maps.k, 64 * a, wk.hk, first, bar);
+          }
+        }
+        if (!d.qvec) load_elements(qt, 128, d.KP, in.q + (long long)first * d.qs + (long long)wk.hk * d.K, d.qs, rows, d.K, tid);
+        if (!d.kvec) load_elements(qt + kC * 128, 128, d.KP, in.k + (long long)first * d.ks + (long long)wk.hk * d.K, d.ks, rows, d.K, tid);
+        if (cut) {
+          ok = wait_warp(&bars.tail, tails++ & 1, status, 122);
+          if (d.qvec) zero_rows(qt, 128, na, rows, tid);
+          if (d.kvec) zero_rows(qt + kC * 128, 128, na, rows, tid);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&bars.qk[s]);
+        if (cut && tid == 0) mbar_arrive(&bars.qk[s]);
+        units = wk.qkn;
+        if (!ok) break;
+      }
+      if (wk.step > 0 && !(ok = wait_warp(&bars.empty, ph ^ 1, status, 123))) break;
+      uint64_t* bar = cut ? &bars.tail : &bars.full;
+      const size_t item = wk.item();
+      if (tid == 0) {
+        const uint32_t sb = (uint32_t)d.VP * 128 * na, rb = (uint32_t)d.VP * 128, gb = kGateRows * kC * 4;
+        mbar_expect_tx(bar, 2 * sb + rb + gb + kC * 128 * va * (1 + (d.ovec ? 1 : 0)));
+        if (d.ovec)
+          for (int a = 0; a < va; ++a) tma_load_3d(smem + oOY + a * 16384, &maps.dout, 64 * a, wk.hv(), first, bar);
+        for (int a = 0; a < va; ++a)
+          bulk_load(smem_u32(smem + oOY) + a * 16384 + kC * 128, dYst + item * va * 64 * kC + a * 64 * kC, kC * 128, bar);
+        bulk_load(smem_u32(smem + oR), Rst + item * d.VP * kC, rb, bar);
+        bulk_load(smem_u32(smem + oGates) + ph * gb, records + item * kRecordBytes + kRecordGates, gb, bar);
+        bulk_load(smem_u32(smem + oS), Sst + item * d.VP * d.KP, sb, bar);
+        bulk_load(smem_u32(smem + oD), dSst + item * d.VP * d.KP, sb, bar);
+      }
+      if (!d.ovec)
+        load_elements(smem + oOY, 128, 64 * va, dout + ((long long)first * d.HV + wk.hv()) * d.V, (long long)d.HV * d.V, rows, d.V, tid);
+      if (cut) {
+        ok = wait_warp(&bars.tail, tails++ & 1, status, 124);
+        if (d.ovec) zero_rows(smem + oOY, 128, va, rows, tid);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if ((tid & 31) == 0) mbar_arrive(&bars.full);
+      if (cut && tid == 0) mbar_arrive(&bars.full);
+      loaded = wk.step;
+    }
+    // no copy is in flight when the block ends
+    if (loaded >= 0) wait_warp(&bars.full, loaded & 1, status, 125);
+    for (int u = max(units - 1, 0); u <= units; ++u) wait_warp(&bars.qk[u & 1], (u >> 1) & 1, status, 126);
+  } else {
+    const int tid = threadIdx.x - 32 * kSumWarp0;
+    for (; wk.more(); wk.next()) {
+      const uint32_t ph = wk.step & 1;
+      if (!wait_warp(&bars.full, ph, status, 131)) break;
+      const Chunk ch = wk.ch;
+      float x = 0.f;
+      const int t = tid >> 1;  // two lanes a row, every other piece of eight columns each
+      if (t < ch.rows) {
+        const bf16* vr = in.v + (long long)(ch.first + t) * d.vs + (long long)wk.hv() * d.V;
+        for (int j = tid & 1; 8 * j < d.V; j += 2) {
+          uint4 a;
+          if (d.vvec) {
+            a = *reinterpret_cast<const uint4*>(vr + 8 * j);
+          } else {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              p[e] = pack(8 * j + 2 * e < d.V ? __bfloat162float(vr[8 * j + 2 * e]) : 0.f,
+                          8 * j + 2 * e + 1 < d.V ? __bfloat162float(vr[8 * j + 2 * e + 1]) : 0.f);
+            a = make_uint4(p[0], p[1], p[2], p[3]);
+          }
+          x = dot8(a, *reinterpret_cast<const uint4*>(smem + oOY + (j >> 3) * 16384 + sw128_chunk(kC + t, j & 7)), x);
+        }
+      }
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      float y = 0.f;
+      const int n16 = d.VP * d.KP / 8;  // the two images have the same layout, whatever it is
+      for (int j = tid; j < n16; j += 32 * kSumWarps)
+        y = dot8(reinterpret_cast<const uint4*>(smem + oS)[j], reinterpret_cast<const uint4*>(smem + oD)[j], y);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+      // the head before has been finished: its sums have been read, and its decays, whose place the next copies take
+      if (wk.step > 0 && !wait_warp(&bars.sums_read, ph ^ 1, status, 132)) break;
+      if ((tid & 1) == 0) s_yv[t] = x;
+      if (lane == 0) s_ss[tid >> 5] = y;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bars.empty);
+        mbar_arrive(&bars.sums);
+      }
+    }
+  }
+  __syncthreads();
+  if (w == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tm, kTmemCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t chunk_grads(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const bf16* dout,
+                        const bf16* S, const bf16* R, const bf16* dS, const bf16* dY, const GradOut& out, int* status,
+                        cudaStream_t st) {
+  const uint64_t steps = d.packed ? (uint64_t)d.T : (uint64_t)d.N * d.T;
+  Maps maps = {};
+  cudaError_t e = cudaSuccess;
+  if (d.kvec) e = make_tmap_heads_bf16(&maps.k, in.k, d.K, d.H, steps, d.ks);
+  if (e == cudaSuccess && d.qvec) e = make_tmap_heads_bf16(&maps.q, in.q, d.K, d.H, steps, d.qs);
+  if (e == cudaSuccess && d.ovec) e = make_tmap_heads_bf16(&maps.dout, dout, d.V, d.HV, steps, (uint64_t)d.HV * d.V);
+  int dev, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_delta_grads, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  const long long units = (long long)d.nc * d.H;
+  SSD_LAUNCH("k_delta_grads", st,
+             k_delta_grads<<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, st>>>(
+                 d, tb, in, maps, records, dout, S, R, dS, dY, out, status));
+  return cudaGetLastError();
+}
+
+}  // namespace delta
+}  // namespace ssd

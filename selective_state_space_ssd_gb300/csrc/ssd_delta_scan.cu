@@ -15,23 +15,22 @@
 // Between two chunks lie three round trips through tensor memory (X, R, S'), which is what bounds the kernel: about
 // 105 cycles of latency for each group of MMAs, 32 cycles for each 128 x 64 x 16 one (A in TMEM; 57 with A in shared
 // memory), and the elementwise work of 128 x 64 and 128 x K values between them.
-#include "delta_common.cuh"
-#include "tc_common.cuh"
+#include "delta_tc.cuh"
 
 namespace ssd {
 namespace delta {
 namespace {
 
-using namespace ssd::tc;
-
-constexpr int kChainWarps = 16, kSideWarps = 4, kLoadWarps = 3;
+constexpr int kChainWarps = 16, kSideWarps = 4;
 constexpr int kMmaWarp = kChainWarps + kSideWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1 + kLoadWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSideBar = 1;  // named barrier of the side warps
+constexpr uint32_t kOut = 32768;
 
-// A stage: [K; Q] rows as one 128-row K-major tile, V (or dO) [64][128], the chunk's record.  Beside the two stages: a
-// [64][128] tile through which o (dV) turns from columns into rows.
+// A stage: [K; Q] rows as one 128-row K-major tile, V (or dO) [64][128], the chunk's record.  Beside the two stages: 32 KB
+// through which results leave: the kept state (all of it), then R or dY (first half) and o or dV (second half), the kept
+// ones as the images that the gradient kernel reads, with one bulk copy each.
 template <int KP>
 struct Tiles {
   static constexpr uint32_t kKQ = 128 * KP * 2, kV = kC * 128 * 2;
@@ -40,7 +39,7 @@ struct Tiles {
 };
 template <int KP>
 constexpr uint32_t scan_smem() {
-  return 2 * Tiles<KP>::kBytes + kC * 128 * 2 + 1024;  // 1024: the tiles' alignment
+  return 2 * Tiles<KP>::kBytes + kOut + 1024;  // 1024: the tiles' alignment
 }
 
 struct Bars {
@@ -50,51 +49,6 @@ struct Maps {
   CUtensorMap k, q, v;  // v: V forward, dO in reverse
 };
 
-// D[tmem] (+)= A[tmem] B[smem]^T
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-      : "memory");
-}
-__device__ __forceinline__ void st16u(uint32_t addr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          addr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-__device__ __forceinline__ void st8u(uint32_t addr, const uint32_t (&v)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
-// A wait of a whole warp: every lane learns the same answer, so a bound that runs out stops the warp as one.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t phase, int* status, int code) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, phase, status, code)) != 0;
-}
-// The warp's tensor-memory stores are done and visible to whoever waits on the barrier.
-__device__ __forceinline__ void signal_tmem(uint64_t* bar, int lane) {
-  tmem_wait_st();
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
-}
-// The warp has read what it needs (tensor or shared memory).
-__device__ __forceinline__ void signal_read(uint64_t* bar, int lane) {
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar);
-}
-
 // 16 values as the bf16 operand columns [8] and what the rounding left [8], the two side by side in tensor memory.
 __device__ __forceinline__ void put_split(uint32_t addr, const float (&x)[16]) {
   uint32_t h[8], l[8];
@@ -103,52 +57,6 @@ __device__ __forceinline__ void put_split(uint32_t addr, const float (&x)[16]) {
   st8u(addr, h);
   st8u(addr + 8, l);
 }
-__device__ __forceinline__ void ld16(uint32_t addr, float (&x)[16]) {
-  uint32_t u[16];
-  tmem_ld16_nowait(addr, u);
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(u[i]);
-}
-__device__ __forceinline__ void lds16(const float* p, float (&x)[16]) {  // the same 16 floats for every lane
-#pragma unroll
-  for (int i = 0; i < 16; i += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(p + i);
-    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-  }
-}
-
-__device__ __forceinline__ uint32_t v_off(int t, int v) {  // element (t, v) of the V tile
-  return (uint32_t)((v >> 6) * (kC * 128)) + sw128_chunk(t, (v & 63) >> 3) + 2u * (v & 7);
-}
-
-// 64 rows of `cols` valid elements, zeros past `rows` and `cols`, into a 128-byte-swizzled tile whose 64-column atoms
-// hold R rows each, element by element (rows that are not whole 16-byte pieces): eight loads in flight a thread.
-__device__ __forceinline__ void load_elements(uint8_t* tile, int R, int width, const bf16* src, long long stride,
-                                              int rows, int cols, int tid) {
-  constexpr int kN = 32 * kLoadWarps, kBatch = 8;
-  const unsigned short* s = reinterpret_cast<const unsigned short*>(src);
-  for (int base = tid; base < kC * width; base += kN * kBatch) {
-    unsigned short x[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = base + j * kN, r = i / width, c = i - r * width;
-      x[j] = r < rows && c < cols ? s[(long long)r * stride + c] : (unsigned short)0;
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = base + j * kN, r = i / width, c = i - r * width;
-      if (r < kC) *reinterpret_cast<unsigned short*>(tile + (c >> 6) * R * 128 + sw128_chunk(r, (c & 63) >> 3) + 2 * (c & 7)) = x[j];
-    }
-  }
-}
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int R, int atoms, int rows, int tid) {
-  for (int i = tid; i < (kC - rows) * atoms * 8; i += 32 * kLoadWarps) {
-    const int r = rows + i / (atoms * 8), j = i % (atoms * 8);
-    *reinterpret_cast<uint4*>(tile + (j >> 3) * R * 128 + r * 128 + (j & 7) * 16) = make_uint4(0, 0, 0, 0);
-  }
-}
-
 // What the copy warps do for one chunk: its tiles into a stage and an arrival on the stage's barrier.  TMA copies and
 // the record arrive by themselves, but for a chunk of fewer than 64 steps: what a box brings in past its end belongs to
 // the next sequence and is overwritten with zeros first.
@@ -240,10 +148,6 @@ __device__ __forceinline__ Block block_of(const Dims& d, const Table& tb) {
   return b;
 }
 
-__device__ __forceinline__ uint8_t* aligned_smem(uint8_t* p) {
-  return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u);
-}
-
 __device__ __forceinline__ void init_bars(Bars* b) {
   for (int i = 0; i < 2; ++i) {
     mbar_init(&b->full[i], kLoadWarps + 1);
@@ -290,10 +194,9 @@ __device__ __forceinline__ void update_state(uint32_t tm, int lane0, int k0, flo
   tc_fence_before();
 }
 
-// The state's operand (its bf16 high part) of lane v: 16-byte pieces of eight keys, [KP / 8][VP] of them, so that the
-// lanes of a warp write consecutive pieces.
+// The state's operand (its bf16 high part) of lane v as row v of the state's image.
 template <int KP>
-__device__ __forceinline__ void keep_state(uint32_t tm, int lane0, bf16* dst, int VP, int v) {
+__device__ __forceinline__ void stage_state(uint32_t tm, int lane0, uint8_t* out, int VP, int v) {
 #pragma unroll
   for (int b = 0; b < KP / 64; ++b) {
     uint32_t u[32];
@@ -302,10 +205,25 @@ __device__ __forceinline__ void keep_state(uint32_t tm, int lane0, bf16* dst, in
     if (v < VP) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4*>(dst + ((size_t)(8 * b + j) * VP + v) * 8) =
+        *reinterpret_cast<uint4*>(out + b * VP * 128 + sw128_chunk(v, j)) =
             make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
     }
   }
+}
+// The side warps have written a tile: one of them sends it off.  Every one of them calls this.
+__device__ __forceinline__ void send_tile(void* dst, const uint8_t* src, uint32_t bytes, int tid) {
+  fence_proxy_async();
+  named_bar(kSideBar, 32 * kSideWarps);
+  if (tid == 0) {
+    bulk_store(dst, src, bytes);
+    tma_store_commit();
+  }
+}
+// Tiles sent off have been read: they may be written again.  `fail`: a wait of this warp ran out; true where one of any
+// warp did, so that the side warps stop together.
+__device__ __forceinline__ bool tiles_free(int tid, bool fail) {
+  if (tid == 0) tma_store_wait_read0();
+  return named_bar_or(kSideBar, 32 * kSideWarps, fail);
 }
 
 // The [64][128] bf16 tile of the side warps to rows of a tensor, first step at dst.
@@ -400,18 +318,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (w < kMmaWarp) {
     const int lane0 = 32 * (w & 3), v = lane0 + lane, tid = threadIdx.x - 32 * kChainWarps;
     const long long os = (long long)d.HV * d.V;
-    bf16* tile = reinterpret_cast<bf16*>(smem + 2 * Tiles<KP>::kBytes);
-    bool ok = true;
-    for (int c = 0; c < nc && ok; ++c) {
+    uint8_t* out = smem + 2 * Tiles<KP>::kBytes;
+    bf16* tile = reinterpret_cast<bf16*>(out + kOut / 2);
+    for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
       const float* gates =
           reinterpret_cast<const float*>(smem + (c & 1) * Tiles<KP>::kBytes + Tiles<KP>::kRec + kRecordGates);
       const size_t item = (size_t)(blk.sq.chunk + c) * d.HV + blk.hv;
       if (stash) {  // the state entering the chunk, and R, both as the bf16 operands hold them
-        if (!(ok = wait_warp(&bars.s, ph, status, 21))) break;
+        if (tiles_free(tid, !wait_warp(&bars.s, ph, status, 21))) break;
         tc_fence_after();
-        keep_state<KP>(tm, lane0, Sout + item * d.VP * KP, d.VP, v);
-        if (!(ok = wait_warp(&bars.ro, ph, status, 22))) break;
+        stage_state<KP>(tm, lane0, out, d.VP, v);
+        send_tile(Sout + item * d.VP * KP, out, (uint32_t)(d.VP * KP * 2), tid);
+        if (tiles_free(tid, !wait_warp(&bars.ro, ph, status, 22))) break;
         tc_fence_after();
         uint32_t u[4][8];
 #pragma unroll
@@ -421,13 +340,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (v < d.VP) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(Rout + item * d.VP * kC + ((size_t)j * d.VP + v) * 8) =
+            *reinterpret_cast<uint4*>(out + sw128_chunk(v, j)) =
                 make_uint4(u[j >> 1][4 * (j & 1)], u[j >> 1][4 * (j & 1) + 1], u[j >> 1][4 * (j & 1) + 2], u[j >> 1][4 * (j & 1) + 3]);
         }
+        send_tile(Rout + item * d.VP * kC, out, (uint32_t)(d.VP * kC * 2), tid);
       }
       if (o) {
-        ok = wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 23) && wait_warp(&bars.o, ph, status, 24);
-        // the tile's last rows have been stored, and all side warps go on together or not at all
+        const bool ok = wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 23) && wait_warp(&bars.o, ph, status, 24);
+        // the tile's last rows have been stored
         if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;
         tc_fence_after();
 #pragma unroll
@@ -447,10 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar(kSideBar, 32 * kSideWarps);
         store_tile(reinterpret_cast<const uint8_t*>(tile), o + ((long long)(blk.sq.start + c * kC) * d.HV + blk.hv) * d.V,
                    os, min(kC, blk.sq.len - c * kC), d.V, d.ovec, tid);
+        if (stash) named_bar(kSideBar, 32 * kSideWarps);  // the next state's image covers this tile
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
     }
+    if (tid == 0) tma_store_wait0();
   } else if (w == kMmaWarp) {
     constexpr uint32_t n64 = idesc_bf16(128, 64, false, false), nk = idesc_bf16(128, KP, false, true);
     for (int c = 0; c < nc; ++c) {
@@ -634,16 +556,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ds0) write_state(ds0 + blk.su, S, d.K, d.V, k0, v);
   } else if (w < kMmaWarp) {
     const int lane0 = 32 * (w & 3), v = lane0 + lane, tid = threadIdx.x - 32 * kChainWarps;
-    bf16* tile = reinterpret_cast<bf16*>(smem + 2 * Tiles<KP>::kBytes);
-    bool ok = true;
-    for (int i = 0; i < nc && ok; ++i) {
+    uint8_t* out = smem + 2 * Tiles<KP>::kBytes;
+    bf16* tile = reinterpret_cast<bf16*>(out + kOut / 2);
+    const int va = (d.VP + 63) / 64;  // 64-column atoms of dY's image
+    for (int i = 0; i < nc; ++i) {
       const uint32_t ph = i & 1;
       const int c = nc - 1 - i;
       const uint8_t* st = smem + (i & 1) * Tiles<KP>::kBytes;
       const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
       const size_t item = (size_t)(blk.sq.chunk + c) * d.HV + blk.hv;
-      if (!(ok = wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 61))) break;
-      if (i > 0 && !(ok = wait_warp(&bars.d, ph ^ 1, status, 62))) break;  // F of the chunk before has been read
+      bool ok = wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 61);
+      ok = ok && (i == 0 || wait_warp(&bars.d, ph ^ 1, status, 62));  // F of the chunk before has been read
+      if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;  // (and the tile's last rows have been stored)
       tc_fence_after();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {  // F = scale e^G dO^T
@@ -655,12 +579,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         put_split(taddr(tm, lane0, F + 16 * b), x);
       }
       signal_tmem(&bars.f, lane);
-      if (!(ok = wait_warp(&bars.s, ph, status, 63))) break;
+      if (tiles_free(tid, !wait_warp(&bars.s, ph, status, 63))) break;
       tc_fence_after();
-      keep_state<KP>(tm, lane0, dSout + item * d.VP * KP, d.VP, v);
+      stage_state<KP>(tm, lane0, out, d.VP, v);
       signal_read(&bars.e1, lane);
-      ok = wait_warp(&bars.ro, ph, status, 64);
-      if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;
+      send_tile(dSout + item * d.VP * KP, out, (uint32_t)(d.VP * KP * 2), tid);
+      if (tiles_free(tid, !wait_warp(&bars.ro, ph, status, 64))) break;
       tc_fence_after();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -668,21 +592,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         lds16(gates + 2 * kC + 16 * b, be);
         ld16(taddr(tm, lane0, U + 16 * b), x);
         if (b == 3) signal_read(&bars.e2, lane);
-        if (v < d.VP) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<uint4*>(dYout + item * d.VP * kC + ((size_t)(2 * b + j) * d.VP + v) * 8) =
-                make_uint4(pack(x[8 * j], x[8 * j + 1]), pack(x[8 * j + 2], x[8 * j + 3]),
-                           pack(x[8 * j + 4], x[8 * j + 5]), pack(x[8 * j + 6], x[8 * j + 7]));
+        for (int j = 0; j < 16; ++j) {
+          *reinterpret_cast<bf16*>(out + v_off(16 * b + j, v)) = __float2bfloat16_rn(x[j]);
+          tile[(16 * b + j) * 128 + v] = __float2bfloat16_rn(be[j] * x[j]);
         }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) tile[(16 * b + j) * 128 + v] = __float2bfloat16_rn(be[j] * x[j]);
       }
-      named_bar(kSideBar, 32 * kSideWarps);
+      send_tile(dYout + item * va * 64 * kC, out, (uint32_t)(va * 64 * kC * 2), tid);
       if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
       store_tile(reinterpret_cast<const uint8_t*>(tile), dv + ((long long)(blk.sq.start + c * kC) * d.HV + blk.hv) * d.V,
                  os, min(kC, blk.sq.len - c * kC), d.V, d.ovec, tid);
     }
+    if (tid == 0) tma_store_wait0();
   } else if (w == kMmaWarp) {
     constexpr uint32_t n64 = idesc_bf16(128, 64, false, false), nk = idesc_bf16(128, KP, false, true);
     for (int i = 0; i < nc; ++i) {
