@@ -17,8 +17,8 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kC = 64;              // steps of a chunk
 constexpr int kTP = kC + 8;         // shared-memory pitch of a [64][64] bf16 tile (16 bytes past a multiple of 128: ldmatrix without conflicts)
-constexpr int kGateRows = 5;        // per-step records of a chunk: e^G, e^{G_end - G}, beta, G (high), G (low)
-constexpr float kMinG = -1e4f;      // e^g of anything below is 0; keeps G - G' defined where g is -inf
+constexpr int kGateRows = 5;        // per-step records of a chunk: e^G, e^{G_end - G}, beta, G / ln 2, scale e^G
+constexpr float kMinG = -200.f;     // e^g of anything below is 0; keeps G - G' defined where g is -inf
 
 struct Dims {
   int N, T, H, HV, G, K, V;          // sequences, steps (packed: of all), heads, value heads, HV / H, widths
@@ -38,7 +38,7 @@ struct Table {
 
 // One record per (chunk, value head), item = chunk * HV + head, in one piece of memory that one bulk copy brings in:
 // four [64][64] bf16 tiles, swizzled as the tensor cores read them (element (i, j) at tile_off), and the decays.
-//   (I + A)^-1 rounded to bf16; what that rounding left, rounded; P_ij = e^{G_i - G_j} q_i . k_j (j <= i) in the same
+//   (I + A)^-1 rounded to bf16; what that rounding left, rounded; P_ij = scale e^{G_i - G_j} q_i . k_j (j <= i) in the same
 //   two parts (16-blocks above the diagonal are not written and not read); float [5][64] of kGateRows
 constexpr int kRecordGates = 4 * kC * kC * 2;
 constexpr int kRecordBytes = kRecordGates + kGateRows * kC * 4;

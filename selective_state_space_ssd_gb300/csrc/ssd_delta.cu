@@ -221,8 +221,8 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, uin
         gr[t] = expf((float)gt);
         gr[kC + t] = expf((float)(end - gt));
         gr[2 * kC + t] = s_beta[t];
-        gr[3 * kC + t] = h;
-        gr[4 * kC + t] = l;
+        gr[3 * kC + t] = (float)(gt * 1.4426950408889634);
+        gr[4 * kC + t] = in.scale * expf((float)gt);
       }
     }
     __syncthreads();
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, uin
         for (int e = 0; e < 2; ++e) {
           const float dec = expf((s_hi[i] - s_hi[j + e]) + (s_lo[i] - s_lo[j + e]));
           a[e] = i > j + e ? s_beta[i] * dec * kk[nt][2 * half + e] : 0.f;
-          p[e] = i >= j + e ? dec * qk[nt][2 * half + e] : 0.f;
+          p[e] = i >= j + e ? in.scale * dec * qk[nt][2 * half + e] : 0.f;
         }
         Af[i * kFP + j] = a[0];
         Af[i * kFP + j + 1] = a[1];

@@ -15,32 +15,34 @@
 // where it leaves tensor memory.  What a head reads (144 KB for K = V = 128) comes by TMA and bulk copies while the head
 // before is in its second half; that traffic is what bounds the kernel.
 //
-// Sixteen warps: 0-7 the elementwise work, two a lane quadrant (halves of the columns); 8 the MMAs; 9-11 copies; 12-15 the
-// two sums that need no product (dY . V by rows, <dS', S>).
+// Twenty-four warps: 0-15 the elementwise work, four a lane quadrant (quarters of the columns); 16 the MMAs; 17-19 copies;
+// 20-23 the two sums that need no product (dY . V by rows, <dS', S>).
 #include "delta_tc.cuh"
 
 namespace ssd {
 namespace delta {
 namespace {
 
-constexpr int kWorkWarps = 8, kSumWarps = 4, kMmaWarp = kWorkWarps, kLoadWarp0 = kMmaWarp + 1,
+constexpr int kWorkWarps = 16, kSumWarps = 4, kMmaWarp = kWorkWarps, kLoadWarp0 = kMmaWarp + 1,
               kSumWarp0 = kLoadWarp0 + kLoadWarps;
 constexpr int kThreads = 32 * (kSumWarp0 + kSumWarps);
 constexpr int kWorkBar = 1;
 
-// Shared memory.  QK (two of them): [Q; K] rows of the head; OY: [dO; dY] rows; R^T, S^T, dS'^T images; B: [B1; B2] rows
-// and beta B2; Out: dQ or dK rows on their way out.
+// Shared memory.  QK: [Q; K] rows of the head; OY: [dO; dY] rows; R^T, S^T, dS'^T images; B: [B1; B2] rows and beta B2,
+// each rounded to bf16, and what that rounding left; Out: dQ rows on their way out (dK's
+// leave through B).
 constexpr uint32_t kQK = 32768, kOY = 32768, kRt = 16384, kSt = 32768, kB = 16384, kBb = 8192, kOutT = 16384;
-constexpr uint32_t oOY = 2 * kQK, oR = oOY + kOY, oS = oR + kRt, oD = oS + kSt, oB = oD + kSt, oBb = oB + kB,
-                   oOut = oBb + kBb, oGates = oOut + kOutT, kSmem = oGates + 2 * kGateRows * kC * 4 + 1024;
+constexpr uint32_t oOY = kQK, oR = oOY + kOY, oS = oR + kRt, oD = oS + kSt, oB = oD + kSt, oBl = oB + kB, oBb = oBl + kB,
+                   oBbl = oBb + kBb, oOut = oBbl + kBb, oGates = oOut + kOutT, kSmem = oGates + 2 * kGateRows * kC * 4 + 1024;
 static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 
-// Columns of tensor memory: the scores [dO; dY] R^T, then dS'^T's product; S's two products; [B1; B2] K; dK' 's scores.
-constexpr int cM = 0, cZ3 = 64, cZ = 128, cW = 256, cD = 384;
+// Columns of tensor memory: the scores [dO; dY] R^T, and over them, once they have been read, the scores' part of dK';
+// dS' 's product; S's two products; [B1; B2] K; dQ and dK summed over the value heads so far.
+constexpr int cM = 0, cD = 0, cZ3 = 64, cZ = 128, cW = 256, cSum = 384;
 constexpr uint32_t kTmemCols = 512;
 
 struct Bars {
-  uint64_t qk[2], qk_free[2], full, empty, tail, m, z, b, w, free, sums, sums_read, done;
+  uint64_t qk, qk_free, full, empty, tail, m, z, b, w, free, sums, sums_read, done;
 };
 struct Maps {
   CUtensorMap k, q, dout;
@@ -112,13 +114,13 @@ __device__ __forceinline__ void put_gate(void* p, size_t i, float x, bool is_bf1
 __device__ __forceinline__ void store_rows(const bf16* tile, bf16* dst, long long stride, int rows, int K, int tid) {
   if (K % 8 == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = (tid >> 4) + 16 * i, c = 8 * (tid & 15);
+    for (int i = 0; i < 2; ++i) {
+      const int r = (tid >> 4) + 32 * i, c = 8 * (tid & 15);
       if (r < rows && c < K)
         *reinterpret_cast<uint4*>(dst + (long long)r * stride + c) = *reinterpret_cast<const uint4*>(tile + r * 128 + c);
     }
   } else {
-    for (int r = tid >> 7; r < rows; r += 2)
+    for (int r = tid >> 7; r < rows; r += 4)
       if ((tid & 127) < K) dst[(long long)r * stride + (tid & 127)] = tile[r * 128 + (tid & 127)];
   }
 }
@@ -133,10 +135,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = aligned_smem(raw);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.qk[i], kLoadWarps + 1);
-      mbar_init(&bars.qk_free[i], 1 + kWorkWarps);
-    }
+    mbar_init(&bars.qk, kLoadWarps + 1);
+    mbar_init(&bars.qk_free, 1 + kWorkWarps);
     mbar_init(&bars.full, kLoadWarps + 1);
     mbar_init(&bars.empty, 1 + kSumWarps + kWorkWarps);
     mbar_init(&bars.tail, 1);
@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = threadIdx.x; i < 1024; i += kThreads) {
       const uint4 z = make_uint4(0, 0, 0, 0);
       reinterpret_cast<uint4*>(smem + 16384)[i] = z;
-      reinterpret_cast<uint4*>(smem + kQK + 16384)[i] = z;
       reinterpret_cast<uint4*>(smem + oS + 16384)[i] = z;
       reinterpret_cast<uint4*>(smem + oD + 16384)[i] = z;
     }
@@ -169,107 +168,131 @@ __global__ void __launch_bounds__(kThreads, 1)
   Work wk(d, tb);
 
   if (w < kWorkWarps) {
-    const int lane0 = 32 * (w & 3), l = lane0 + lane, hf = w >> 2, tid = threadIdx.x;
-    const int i = l & 63;               // the scores' row; lanes 64 .. 127 hold dY's
-    const bool is_y = l >= 64;
-    bf16* tile = reinterpret_cast<bf16*>(smem + oOut);
-    float dQ[32], dK[32];  // key l, steps 32 hf ..
-#pragma unroll
-    for (int j = 0; j < 32; ++j) dQ[j] = dK[j] = 0.f;
+    const int lane0 = 32 * (w & 3), l = lane0 + lane, wg = w >> 2, tid = threadIdx.x;
+    const int i = l & 63;             // the scores' row
+    const bool is_y = (w & 3) >= 2;   // lanes 64 .. 127 hold dY's
+    bf16 *tq = reinterpret_cast<bf16*>(smem + oOut), *tk = reinterpret_cast<bf16*>(smem + oB);
     for (; wk.more(); wk.next()) {
       const uint32_t ph = wk.step & 1;
       const float* gt = reinterpret_cast<const float*>(smem + oGates) + ph * kGateRows * kC;
-      const float *eg = gt, *ee = gt + kC, *be = gt + 2 * kC, *gh = gt + 3 * kC, *gl = gt + 4 * kC;
+      const float *eg = gt, *be = gt + 2 * kC;
       bool ok = wait_warp(&bars.full, ph, status, 101);
       // (an arrival here keeps the copies within one phase of this wait)
       if (lane == 0) mbar_arrive(&bars.empty);
       ok = ok && wait_warp(&bars.m, ph, status, 102);
       tc_fence_after();
       {  // B1, B2, beta B2
-        const float hi = gh[i], lo = gl[i], bi = be[i], f = is_y ? -1.f : in.scale;
-        const int top = is_y ? i - 1 : i;  // the last column below the diagonal (dY) or on it (dO)
-        const bool some = 32 * hf <= (lane0 & 63) + 31;
+        float x[16];
+        if (16 * wg <= (lane0 & 63) + 31 && ok) {
+          float gj[16];
+          lds16(gt + 3 * kC + 16 * wg, gj);
+          const float gi = gt[3 * kC + i], f = is_y ? -1.f : in.scale;
+          const int top = is_y ? i - 1 : i;  // the last column below the diagonal (dY) or on it (dO)
+          ld16(taddr(tm, lane0, cM + 16 * wg), x);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          float x[16];
-          uint32_t p[8], q[8];
-          if (some && ok) {
-            ld16(taddr(tm, lane0, cM + 32 * hf + 16 * b), x);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int j = 32 * hf + 16 * b + e;
-              x[e] = j <= top ? f * x[e] * __expf((hi - gh[j]) + (lo - gl[j])) : 0.f;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = 0.f;
+          for (int e = 0; e < 16; ++e) {
+            float dec;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(dec) : "f"(gi - gj[e]));
+            x[e] = 16 * wg + e <= top ? f * x[e] * dec : 0.f;
           }
+        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            p[e] = pack(x[2 * e], x[2 * e + 1]);
-            q[e] = pack(bi * x[2 * e], bi * x[2 * e + 1]);
-          }
+          for (int e = 0; e < 16; ++e) x[e] = 0.f;
+        }
+        const auto put = [&](uint32_t hi, uint32_t lo, int r) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int j = 4 * hf + 2 * b + e;
-            *reinterpret_cast<uint4*>(smem + oB + sw128_chunk(l, j)) = make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]);
-            if (is_y)
-              *reinterpret_cast<uint4*>(smem + oBb + sw128_chunk(i, j)) = make_uint4(q[4 * e], q[4 * e + 1], q[4 * e + 2], q[4 * e + 3]);
+            uint32_t p[4], q[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) split(x[8 * e + 2 * n], x[8 * e + 2 * n + 1], p[n], q[n]);
+            *reinterpret_cast<uint4*>(smem + hi + sw128_chunk(r, 2 * wg + e)) = make_uint4(p[0], p[1], p[2], p[3]);
+            *reinterpret_cast<uint4*>(smem + lo + sw128_chunk(r, 2 * wg + e)) = make_uint4(q[0], q[1], q[2], q[3]);
           }
+        };
+        put(oB, oBl, l);
+        if (is_y) {
+          const float bi = be[i];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] *= bi;
+          put(oBb, oBbl, i);
         }
         fence_proxy_async();
         signal_read(&bars.b, lane);
       }
-      ok = ok && wait_warp(&bars.qk[wk.qkn & 1], (wk.qkn >> 1) & 1, status, 106) &&
-           wait_warp(&bars.z, ph, status, 103) && wait_warp(&bars.w, ph, status, 104);
+      ok = ok && wait_warp(&bars.qk, wk.qkn & 1, status, 106) && wait_warp(&bars.z, ph, status, 103) &&
+           wait_warp(&bars.w, ph, status, 104);
       tc_fence_after();
-      const uint8_t* qk = smem + (wk.qkn & 1) * kQK + (l >> 6) * 16384 + 2 * (l & 7);
+      const uint8_t* qk = smem + (l >> 6) * 16384 + 2 * (l & 7);
+      // eight steps of dQ or dK: added to the sum of the value heads before, and kept there or sent out
+      const auto emit = [&](bf16* tile, int col, int t0, float(&x)[8]) {
+        uint32_t u[8];
+        if (wk.gi > 0) {
+          tmem_ld8_nowait(taddr(tm, lane0, col), u);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] += __uint_as_float(u[e]);
+        }
+        if (wk.last()) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) tile[(t0 + e) * 128 + l] = __float2bfloat16_rn(x[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[e] = __float_as_uint(x[e]);
+          st8u(taddr(tm, lane0, col), u);
+          tmem_wait_st();
+        }
+      };
       float e_all = 0.f;  // this key's share of sum_t E_t k_t.(R dS'^T)_t
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        float sa[8], sh[8];  // its shares of q.dQ - k.dK' and k.H of eight steps
+      for (int b = 0; b < 2; ++b) {
+        const int t0 = 16 * wg + 8 * b;
+        float sa[8], sh[8], g[8];  // this key's shares of q.dQ - k.dK' and k.H of eight steps
         uint32_t z[8], s[8];
-        tmem_ld8_nowait(taddr(tm, lane0, cZ + 32 * hf + 8 * b), z);
-        tmem_ld8_nowait(taddr(tm, lane0, cW + 32 * hf + 8 * b), s);
+        tmem_ld8_nowait(taddr(tm, lane0, cZ + t0), z);
+        tmem_ld8_nowait(taddr(tm, lane0, cW + t0), s);
+        lds8(gt + 4 * kC + t0, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          sa[e] = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(t0 + e, (l & 63) >> 3)));
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int t = 32 * hf + 8 * b + e;
-          const float q = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(t, (l & 63) >> 3)));
-          const float x = fmaf(in.scale * eg[t], __uint_as_float(z[e]), __uint_as_float(s[e]));
-          dQ[8 * b + e] += x;
-          sa[e] = q * x;
+          g[e] = fmaf(g[e], __uint_as_float(z[e]), __uint_as_float(s[e]));
+          sa[e] *= g[e];
         }
-        uint32_t y[8], u[8];
-        tmem_ld8_nowait(taddr(tm, lane0, cZ + 64 + 32 * hf + 8 * b), z);
-        tmem_ld8_nowait(taddr(tm, lane0, cW + 64 + 32 * hf + 8 * b), s);
-        tmem_ld8_nowait(taddr(tm, lane0, cZ3 + 32 * hf + 8 * b), y);
-        tmem_ld8_nowait(taddr(tm, lane0, cD + 32 * hf + 8 * b), u);
+        emit(tq, cSum + t0, t0, g);
+        tmem_ld8_nowait(taddr(tm, lane0, cZ + 64 + t0), z);
+        tmem_ld8_nowait(taddr(tm, lane0, cW + 64 + t0), s);
+        lds8(eg + t0, g);
         tmem_wait_ld();
-        if (b == 3) signal_read(&bars.free, lane);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sh[e] = fmaf(-g[e], __uint_as_float(z[e]), __uint_as_float(s[e]));  // H
+        tmem_ld8_nowait(taddr(tm, lane0, cZ3 + t0), z);
+        tmem_ld8_nowait(taddr(tm, lane0, cD + t0), s);
+        lds8(gt + kC + t0, g);
+        tmem_wait_ld();
+        if (b == 1) signal_read(&bars.free, lane);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int t = 32 * hf + 8 * b + e;
-          const float k = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(kC + t, (l & 63) >> 3)));
-          const float h = fmaf(-eg[t], __uint_as_float(z[e]), __uint_as_float(s[e]));
-          const float r = ee[t] * __uint_as_float(y[e]);
-          const float m = r + __uint_as_float(u[e]);
-          dK[8 * b + e] += fmaf(be[t], h, m);
-          sh[e] = k * h;
+          const float k = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(kC + t0 + e, (l & 63) >> 3)));
+          const float r = g[e] * __uint_as_float(z[e]), m = r + __uint_as_float(s[e]);
           e_all = fmaf(k, r, e_all);
           sa[e] = fmaf(-k, m, sa[e]);
+          g[e] = fmaf(be[t0 + e], sh[e], m);
+          sh[e] *= k;
         }
+        emit(tk, cSum + 64 + t0, t0, g);
         const float a = lane_sums(sa, lane), h = lane_sums(sh, lane);
         if (lane < 8) {
-          s_a[w & 3][32 * hf + 8 * b + lane] = a;
-          s_h[w & 3][32 * hf + 8 * b + lane] = h;
+          s_a[w & 3][t0 + lane] = a;
+          s_h[w & 3][t0 + lane] = h;
         }
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) e_all += __shfl_xor_sync(0xffffffffu, e_all, o);
       if (lane == 0) {
         s_e[w] = e_all;
-        if (wk.last()) mbar_arrive(&bars.qk_free[wk.qkn & 1]);
+        if (wk.last()) mbar_arrive(&bars.qk_free);
       }
       ok = ok && wait_warp(&bars.sums, ph, status, 105);
       if (named_bar_or(kWorkBar, 32 * kWorkWarps, !ok)) break;
@@ -306,21 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (wk.last()) {
         const long long stride = (long long)d.H * d.K;
         const size_t at = ((size_t)ch.first * d.H + wk.hk) * d.K;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          float(&x)[32] = which ? dK : dQ;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            tile[(32 * hf + j) * 128 + l] = __float2bfloat16_rn(x[j]);
-            x[j] = 0.f;
-          }
-          named_bar(kWorkBar, 32 * kWorkWarps);
-          store_rows(tile, (which ? out.dk : out.dq) + at, stride, ch.rows, d.K, tid);
-          named_bar(kWorkBar, 32 * kWorkWarps);
-        }
-      } else {
-        named_bar(kWorkBar, 32 * kWorkWarps);  // the sums have been read before the next head writes its own
+        store_rows(tq, out.dq + at, stride, ch.rows, d.K, tid);
+        store_rows(tk, out.dk + at, stride, ch.rows, d.K, tid);
       }
+      named_bar(kWorkBar, 32 * kWorkWarps);  // sums and tiles have been read before the next head writes its own
     }
   } else if (w == kMmaWarp) {
     constexpr uint32_t iM = idesc_bf16(128, 64, false, true), iZ = idesc_bf16(128, 128, true, false),
@@ -328,18 +340,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nv = d.VP / 16;
     for (; wk.more(); wk.next()) {
       const uint32_t ph = wk.step & 1;
-      const uint8_t* qk = smem + (wk.qkn & 1) * kQK;
       if (!wait_warp(&bars.full, ph, status, 111)) break;
       tc_fence_after();
       const uint64_t oy = kdesc(smem + oOY, 128, 0), rt = mdesc(smem + oR, d.VP, 0);
       const uint64_t sm = sdesc_sw128(smem_u32(smem + oS), satom, 1024), dm = sdesc_sw128(smem_u32(smem + oD), satom, 1024);
+      if (wk.step > 0 && !wait_warp(&bars.free, ph ^ 1, status, 112)) break;
+      tc_fence_after();
       if (elect_one()) {
         for (int vb = 0; vb < nv; ++vb) mma_bf16(tm + cM, oy + kdesc_step(128, 16 * vb), rt + mdesc_step(16 * vb), iM, vb > 0);
         mma_commit(&bars.m);
       }
       __syncwarp();
-      if (wk.step > 0 && !wait_warp(&bars.free, ph ^ 1, status, 112)) break;
-      tc_fence_after();
       if (elect_one()) {
         for (int vb = 0; vb < nv; ++vb) mma_bf16(tm + cZ, sm + mdesc_step(16 * vb), oy + kdesc_step(128, 16 * vb), iZ, vb > 0);
         for (int vb = 0; vb < nv; ++vb) mma_bf16(tm + cZ3, dm + mdesc_step(16 * vb), rt + mdesc_step(16 * vb), iR, vb > 0);
@@ -347,23 +358,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&bars.empty);
       }
       __syncwarp();
-      if (wk.gi == 0 && !wait_warp(&bars.qk[wk.qkn & 1], (wk.qkn >> 1) & 1, status, 113)) break;
+      if (wk.gi == 0 && !wait_warp(&bars.qk, wk.qkn & 1, status, 113)) break;
       if (!wait_warp(&bars.b, ph, status, 114)) break;
       tc_fence_after();
-      const uint64_t qm = sdesc_sw128(smem_u32(qk), 16384, 1024), km = sdesc_sw128(smem_u32(qk) + kC * 128, 16384, 1024);
-      const uint64_t bk = kdesc(smem + oB, 128, 0);
+      const uint64_t qm = sdesc_sw128(smem_u32(smem), 16384, 1024), km = sdesc_sw128(smem_u32(smem) + kC * 128, 16384, 1024);
+      const uint64_t bk = kdesc(smem + oB, 128, 0), bkl = kdesc(smem + oBl, 128, 0);
       if (elect_one()) {
 #pragma unroll
-        for (int jb = 0; jb < 4; ++jb) mma_bf16(tm + cW, km + mdesc_step(16 * jb), bk + kdesc_step(128, 16 * jb), iW, jb > 0);
+        for (int jb = 0; jb < 4; ++jb) {
+          mma_bf16(tm + cW, km + mdesc_step(16 * jb), bk + kdesc_step(128, 16 * jb), iW, jb > 0);
+          mma_bf16(tm + cW, km + mdesc_step(16 * jb), bkl + kdesc_step(128, 16 * jb), iW, true);
+        }
         // the transposed scores: row block ib has columns j <= 16 ib + 15
 #pragma unroll
         for (int ib = 3; ib >= 0; --ib) {
           const uint32_t id = idesc_bf16(128, 16 * (ib + 1), true, true);
           mma_bf16(tm + cD, qm + mdesc_step(16 * ib), mdesc(smem + oB, 128, 16 * ib), id, ib < 3);
+          mma_bf16(tm + cD, qm + mdesc_step(16 * ib), mdesc(smem + oBl, 128, 16 * ib), id, true);
           mma_bf16(tm + cD, km + mdesc_step(16 * ib), mdesc(smem + oBb, kC, 16 * ib), id, true);
+          mma_bf16(tm + cD, km + mdesc_step(16 * ib), mdesc(smem + oBbl, kC, 16 * ib), id, true);
         }
         mma_commit(&bars.w);
-        if (wk.last()) mma_commit(&bars.qk_free[wk.qkn & 1]);
+        if (wk.last()) mma_commit(&bars.qk_free);
       }
       __syncwarp();
     }
@@ -381,10 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = wk.ch.first, rows = wk.ch.rows;
       const bool cut = rows < kC;
       if (wk.gi == 0) {
-        const int s = wk.qkn & 1;
-        if (wk.qkn >= 2 && !wait_warp(&bars.qk_free[s], ((wk.qkn >> 1) & 1) ^ 1, status, 121)) break;
-        uint8_t* qt = smem + s * kQK;
-        uint64_t* bar = cut ? &bars.tail : &bars.qk[s];
+        if (wk.qkn > 0 && !wait_warp(&bars.qk_free, (wk.qkn & 1) ^ 1, status, 121)) break;
+        uint8_t* qt = smem;
+        uint64_t* bar = cut ? &bars.tail : &bars.qk;
         if (tid == 0) {
           mbar_expect_tx(bar, kC * 128 * na * ((d.qvec ? 1 : 0) + (d.kvec ? 1 : 0)));
           for (int a = 0; a < na; ++a) {
@@ -401,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async();
         __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(&bars.qk[s]);
-        if (cut && tid == 0) mbar_arrive(&bars.qk[s]);
+        if ((tid & 31) == 0) mbar_arrive(&bars.qk);
+        if (cut && tid == 0) mbar_arrive(&bars.qk);
         units = wk.qkn;
         if (!ok) break;
       }
@@ -435,37 +450,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // no copy is in flight when the block ends
     if (loaded >= 0) wait_warp(&bars.full, loaded & 1, status, 125);
-    for (int u = max(units - 1, 0); u <= units; ++u) wait_warp(&bars.qk[u & 1], (u >> 1) & 1, status, 126);
+    if (units >= 0) wait_warp(&bars.qk, units & 1, status, 126);
   } else {
-    const int tid = threadIdx.x - 32 * kSumWarp0;
+    const int tid = threadIdx.x - 32 * kSumWarp0, t = tid >> 1;  // two lanes a row, every other piece of eight columns each
     for (; wk.more(); wk.next()) {
       const uint32_t ph = wk.step & 1;
-      if (!wait_warp(&bars.full, ph, status, 131)) break;
       const Chunk ch = wk.ch;
-      float x = 0.f;
-      const int t = tid >> 1;  // two lanes a row, every other piece of eight columns each
-      if (t < ch.rows) {
+      uint4 a[8];  // V, before the wait
+      {
         const bf16* vr = in.v + (long long)(ch.first + t) * d.vs + (long long)wk.hv() * d.V;
-        for (int j = tid & 1; 8 * j < d.V; j += 2) {
-          uint4 a;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int j = 2 * n + (tid & 1);
+          a[n] = make_uint4(0, 0, 0, 0);
+          if (t >= ch.rows || 8 * j >= d.V) continue;
           if (d.vvec) {
-            a = *reinterpret_cast<const uint4*>(vr + 8 * j);
+            a[n] = *reinterpret_cast<const uint4*>(vr + 8 * j);
           } else {
             uint32_t p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               p[e] = pack(8 * j + 2 * e < d.V ? __bfloat162float(vr[8 * j + 2 * e]) : 0.f,
                           8 * j + 2 * e + 1 < d.V ? __bfloat162float(vr[8 * j + 2 * e + 1]) : 0.f);
-            a = make_uint4(p[0], p[1], p[2], p[3]);
+            a[n] = make_uint4(p[0], p[1], p[2], p[3]);
           }
-          x = dot8(a, *reinterpret_cast<const uint4*>(smem + oOY + (j >> 3) * 16384 + sw128_chunk(kC + t, j & 7)), x);
         }
       }
+      if (!wait_warp(&bars.full, ph, status, 131)) break;
+      float x = 0.f;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int j = 2 * n + (tid & 1);
+        if (8 * j < d.V)
+          x = dot8(a[n], *reinterpret_cast<const uint4*>(smem + oOY + (j >> 3) * 16384 + sw128_chunk(kC + t, j & 7)), x);
+      }
       x += __shfl_xor_sync(0xffffffffu, x, 1);
-      float y = 0.f;
+      float y4[4] = {0.f, 0.f, 0.f, 0.f};
       const int n16 = d.VP * d.KP / 8;  // the two images have the same layout, whatever it is
-      for (int j = tid; j < n16; j += 32 * kSumWarps)
-        y = dot8(reinterpret_cast<const uint4*>(smem + oS)[j], reinterpret_cast<const uint4*>(smem + oD)[j], y);
+      for (int j = tid; j < n16; j += 128 * kSumWarps) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int m = j + 32 * kSumWarps * n;
+          if (m < n16)
+            y4[n] = dot8(reinterpret_cast<const uint4*>(smem + oS)[m], reinterpret_cast<const uint4*>(smem + oD)[m], y4[n]);
+        }
+      }
+      float y = (y4[0] + y4[1]) + (y4[2] + y4[3]);
 #pragma unroll
       for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
       // the head before has been finished: its sums have been read, and its decays, whose place the next copies take

@@ -11,7 +11,7 @@
 //   0-15   the chain: four warps a lane quadrant, each with a quarter of the columns; S stays in their registers (fp32)
 //   16-19  beside the chain: o and the stash forward; dS', dY, dV and the scaled dO^T operand in reverse
 //   20     issues every MMA
-//   21-23  copies of the next chunk's tiles (two stages; TMA where rows are whole 16-byte pieces)
+//   21-23  copy the next chunk's tiles (two stages; TMA where rows are whole 16-byte pieces)
 // Between two chunks lie three round trips through tensor memory (X, R, S'), which is what bounds the kernel: about
 // 105 cycles of latency for each group of MMAs, 32 cycles for each 128 x 64 x 16 one (A in TMEM; 57 with A in shared
 // memory), and the elementwise work of 128 x 64 and 128 x K values between them.
@@ -198,14 +198,14 @@ __device__ __forceinline__ void update_state(uint32_t tm, int lane0, int k0, flo
 template <int KP>
 __device__ __forceinline__ void stage_state(uint32_t tm, int lane0, uint8_t* out, int VP, int v) {
 #pragma unroll
-  for (int b = 0; b < KP / 64; ++b) {
-    uint32_t u[32];
-    tmem_ld32_nowait(taddr(tm, lane0, Cols<KP>::Sh + 32 * b), u);
+  for (int b = 0; b < KP / 32; ++b) {
+    uint32_t u[16];
+    tmem_ld16_nowait(taddr(tm, lane0, Cols<KP>::Sh + 16 * b), u);
     tmem_wait_ld();
     if (v < VP) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4*>(out + b * VP * 128 + sw128_chunk(v, j)) =
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(out + (b >> 1) * VP * 128 + sw128_chunk(v, 4 * (b & 1) + j)) =
             make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
     }
   }
@@ -280,28 +280,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       put_state<KP>(tm, lane0, wg, S);
       signal_tmem(&bars.s, lane);
       if (!wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 13)) break;
-      float x[16], a[16], b[16];
-      {
-        const uint8_t* vt = st + Tiles<KP>::kKQ;
-        lds16(gates + 2 * kC + 16 * wg, a);
-        lds16(gates + 16 * wg, b);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          b[i] *= -a[i];
-          a[i] *= __bfloat162float(*reinterpret_cast<const bf16*>(vt + v_off(16 * wg + i, v)));
-        }
-      }
       if (!wait_warp(&bars.x, ph, status, 14)) break;
       tc_fence_after();
+      float x[16];
       ld16(taddr(tm, lane0, C::X + 16 * wg), x);
+      {
+        const uint8_t* vt = st + Tiles<KP>::kKQ;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = fmaf(b[i], x[i], a[i]);  // Y = beta V - beta e^G X
+        for (int b = 0; b < 16; b += 8) {  // Y = beta (V - e^G X)
+          float e[8], be[8];
+          lds8(gates + 16 * wg + b, e);
+          lds8(gates + 2 * kC + 16 * wg + b, be);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            x[b + i] = be[i] * fmaf(-e[i], x[b + i],
+                                    __bfloat162float(*reinterpret_cast<const bf16*>(vt + v_off(16 * wg + b + i, v))));
+        }
+      }
       put_split(taddr(tm, lane0, C::X + 16 * wg), x);
       signal_tmem(&bars.y, lane);
-      lds16(gates + kC + 16 * wg, a);
       if (!wait_warp(&bars.r, ph, status, 15)) break;
       tc_fence_after();
       ld16(taddr(tm, lane0, C::R + 16 * wg), x);
+      float a[16];
+      lds16(gates + kC + 16 * wg, a);
 #pragma unroll
       for (int i = 0; i < 16; ++i) a[i] *= x[i];  // R' = e^{G_end - G} R
       put_split(taddr(tm, lane0, C::R + 16 * wg), a);
@@ -332,16 +334,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         send_tile(Sout + item * d.VP * KP, out, (uint32_t)(d.VP * KP * 2), tid);
         if (tiles_free(tid, !wait_warp(&bars.ro, ph, status, 22))) break;
         tc_fence_after();
-        uint32_t u[4][8];
 #pragma unroll
-        for (int b = 0; b < 4; ++b) tmem_ld8_nowait(taddr(tm, lane0, C::Ro + 16 * b), u[b]);
-        tmem_wait_ld();
-        signal_read(&bars.e1, lane);
-        if (v < d.VP) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(out + sw128_chunk(v, j)) =
-                make_uint4(u[j >> 1][4 * (j & 1)], u[j >> 1][4 * (j & 1) + 1], u[j >> 1][4 * (j & 1) + 2], u[j >> 1][4 * (j & 1) + 3]);
+        for (int b = 0; b < 4; ++b) {
+          uint32_t u[8];
+          tmem_ld8_nowait(taddr(tm, lane0, C::Ro + 16 * b), u);
+          tmem_wait_ld();
+          if (b == 3) signal_read(&bars.e1, lane);
+          if (v < d.VP) {
+            *reinterpret_cast<uint4*>(out + sw128_chunk(v, 2 * b)) = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(out + sw128_chunk(v, 2 * b + 1)) = make_uint4(u[4], u[5], u[6], u[7]);
+          }
         }
         send_tile(Rout + item * d.VP * kC, out, (uint32_t)(d.VP * kC * 2), tid);
       }
@@ -351,18 +353,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;
         tc_fence_after();
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t q[16], r[16];
-          tmem_ld16_nowait(taddr(tm, lane0, C::QS + 16 * b), q);
-          tmem_ld16_nowait(taddr(tm, lane0, C::O2 + 16 * b), r);
-          float e[16];
-          lds16(gates + 16 * b, e);
+        for (int b = 0; b < 8; ++b) {
+          uint32_t q[8], r[8];
+          tmem_ld8_nowait(taddr(tm, lane0, C::QS + 8 * b), q);
+          tmem_ld8_nowait(taddr(tm, lane0, C::O2 + 8 * b), r);
+          float e[8];
+          lds8(gates + 4 * kC + 8 * b, e);
           tmem_wait_ld();
-          if (b == 3) signal_read(&bars.e2, lane);
+          if (b == 7) signal_read(&bars.e2, lane);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            tile[(16 * b + i) * 128 + v] =
-                __float2bfloat16_rn(in.scale * fmaf(e[i], __uint_as_float(q[i]), __uint_as_float(r[i])));
+          for (int i = 0; i < 8; ++i)
+            tile[(8 * b + i) * 128 + v] =
+                __float2bfloat16_rn(fmaf(e[i], __uint_as_float(q[i]), __uint_as_float(r[i])));
         }
         named_bar(kSideBar, 32 * kSideWarps);
         store_tile(reinterpret_cast<const uint8_t*>(tile), o + ((long long)(blk.sq.start + c * kC) * d.HV + blk.hv) * d.V,
@@ -512,33 +514,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       put_state<KP>(tm, lane0, wg, S);
       signal_tmem(&bars.s, lane);
       if (!wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 52)) break;
-      float x[16], a[16];
-      lds16(gates + kC + 16 * wg, a);
       if (!wait_warp(&bars.x, ph, status, 53)) break;
       tc_fence_after();
-      {  // dR = e^{G_end - G} X + scale U
-        uint32_t p[16], q[16];
-        tmem_ld16_nowait(taddr(tm, lane0, C::X + 16 * wg), p);
-        tmem_ld16_nowait(taddr(tm, lane0, U + 16 * wg), q);
+      float x[16];
+#pragma unroll
+      for (int b = 0; b < 16; b += 8) {  // dR = e^{G_end - G} X + U (the scores hold the scale)
+        uint32_t p[8], q[8];
+        float e[8];
+        tmem_ld8_nowait(taddr(tm, lane0, C::X + 16 * wg + b), p);
+        tmem_ld8_nowait(taddr(tm, lane0, U + 16 * wg + b), q);
+        lds8(gates + kC + 16 * wg + b, e);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = fmaf(in.scale, __uint_as_float(q[j]), a[j] * __uint_as_float(p[j]));
+        for (int j = 0; j < 8; ++j) x[b + j] = fmaf(e[j], __uint_as_float(p[j]), __uint_as_float(q[j]));
       }
       put_split(taddr(tm, lane0, C::X + 16 * wg), x);
       signal_tmem(&bars.y, lane);
-      {
-        float b[16];
-        lds16(gates + 16 * wg, a);
-        lds16(gates + 2 * kC + 16 * wg, b);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) a[j] *= -b[j];
-      }
       if (!wait_warp(&bars.r, ph, status, 54)) break;
       tc_fence_after();
       ld16(taddr(tm, lane0, C::R + 16 * wg), x);  // dY
+      {
+        float a[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) a[j] *= x[j];  // dX = -beta e^G dY
-      put_split(taddr(tm, lane0, C::R + 16 * wg), a);
+        for (int b = 0; b < 16; b += 8) {  // dX = -beta e^G dY
+          float e[8], be[8];
+          lds8(gates + 16 * wg + b, e);
+          lds8(gates + 2 * kC + 16 * wg + b, be);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) a[b + j] = -be[j] * e[j] * x[b + j];
+        }
+        put_split(taddr(tm, lane0, C::R + 16 * wg), a);
+      }
       signal_tmem(&bars.rp, lane);
       {  // dY for the side warps, over U
         uint32_t u[16];
@@ -570,13 +576,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;  // (and the tile's last rows have been stored)
       tc_fence_after();
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {  // F = scale e^G dO^T
-        float x[16];
-        lds16(gates + 16 * b, x);
+      for (int b = 0; b < 8; ++b) {  // F = scale e^G dO^T
+        float x[8];
+        uint32_t h[4], l[4];
+        lds8(gates + 4 * kC + 8 * b, x);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          x[j] *= in.scale * __bfloat162float(*reinterpret_cast<const bf16*>(st + Tiles<KP>::kKQ + v_off(16 * b + j, v)));
-        put_split(taddr(tm, lane0, F + 16 * b), x);
+        for (int j = 0; j < 8; ++j)
+          x[j] *= __bfloat162float(*reinterpret_cast<const bf16*>(st + Tiles<KP>::kKQ + v_off(8 * b + j, v)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split(x[2 * j], x[2 * j + 1], h[j], l[j]);
+        st4u(taddr(tm, lane0, F + 16 * (b >> 1) + 4 * (b & 1)), h);
+        st4u(taddr(tm, lane0, F + 16 * (b >> 1) + 4 * (b & 1) + 8), l);
       }
       signal_tmem(&bars.f, lane);
       if (tiles_free(tid, !wait_warp(&bars.s, ph, status, 63))) break;
@@ -587,15 +597,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tiles_free(tid, !wait_warp(&bars.ro, ph, status, 64))) break;
       tc_fence_after();
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        float x[16], be[16];
-        lds16(gates + 2 * kC + 16 * b, be);
-        ld16(taddr(tm, lane0, U + 16 * b), x);
-        if (b == 3) signal_read(&bars.e2, lane);
+      for (int b = 0; b < 8; ++b) {
+        uint32_t x[8];
+        float be[8];
+        tmem_ld8_nowait(taddr(tm, lane0, U + 8 * b), x);
+        lds8(gates + 2 * kC + 8 * b, be);
+        tmem_wait_ld();
+        if (b == 7) signal_read(&bars.e2, lane);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          *reinterpret_cast<bf16*>(out + v_off(16 * b + j, v)) = __float2bfloat16_rn(x[j]);
-          tile[(16 * b + j) * 128 + v] = __float2bfloat16_rn(be[j] * x[j]);
+        for (int j = 0; j < 8; ++j) {
+          *reinterpret_cast<bf16*>(out + v_off(8 * b + j, v)) = __float2bfloat16_rn(__uint_as_float(x[j]));
+          tile[(8 * b + j) * 128 + v] = __float2bfloat16_rn(be[j] * __uint_as_float(x[j]));
         }
       }
       send_tile(dYout + item * va * 64 * kC, out, (uint32_t)(va * 64 * kC * 2), tid);
