@@ -402,7 +402,7 @@ ssd_status ssd_kda_backward(const ssd_kda_problem* prob, const float* dout, cons
  *               0 .. seqlen and to ascending order; steps that belong to no
  *               sequence are not written.  ssd_delta_step takes packed = 0.
  *   batch, seqlen, nheads (H), value_heads (HV, a multiple of H), key_dim (K),
- *   value_dim (V): >= 1.  Limits of this build: K, V <= 128, H <= 65535, steps
+ *   value_dim (V): >= 1.  Limits of this build: K, V <= 128, HV <= 65535, steps
  *               and b*HV below 2^31 (SSD_ERR_SHAPE).
  *   q_stride, k_stride, v_stride: elements from a step to the next, for
  *               tensors that lie inside wider ones; 0 = dense (H*K, H*K,

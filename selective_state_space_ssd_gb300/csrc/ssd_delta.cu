@@ -136,28 +136,73 @@ __device__ __forceinline__ void put16(float* dst, const float (&c)[2][4], float 
     for (int j = 0; j < 4; ++j) dst[(g + 8 * (j >> 1)) * kFP + 8 * h + 2 * t + (j & 1)] = sign * c[h][j];
 }
 
-// Four warps per (chunk, query/key head); warp w holds rows 16 w .. 16 w + 15 of K K^T and Q K^T, which the head's
-// value heads share, and multiplies them by each head's decays.  (I + A)^-1: the four 16-blocks of the diagonal by
-// forward substitution (a lane a column), then twice the block rule  [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']].
+// Four warps per (chunk, value head); warp w holds rows 16 w .. 16 w + 15 of K K^T and Q K^T, up to the diagonal, and
+// multiplies them by the decays.  (I + A)^-1 in the place of A: the four 16-blocks of the diagonal by forward
+// substitution (a lane a column), then twice the block rule  [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']].
 // Substitution and block products stay small for strongly correlated keys, where a series in powers of A would not.
+// Latency-bound (a chain of small steps): five blocks an SM, at 96 registers, hide one another's.
 template <int KP>
-__global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, uint8_t* records, int* status) {
+__global__ void __launch_bounds__(128, 5) k_delta_prep(Dims d, Table tb, In in, uint8_t* records, int* status) {
   constexpr int kP = KP + 8;
   extern __shared__ __align__(16) unsigned char smem[];
   bf16* Ks = reinterpret_cast<bf16*>(smem);
   bf16* Qs = Ks + kC * kP;
   float* Af = reinterpret_cast<float*>(smem);  // over K and Q, once their products are in registers
-  float* Tf = Af + kC * kFP;
-  float* Mf = Tf + kC * kFP;  // [32][kFP]
+  float* Pf = Af + kC * kFP;
+  float* Mf = Pf + kC * kFP;  // [32][kFP]
   __shared__ float s_hi[kC], s_lo[kC], s_beta[kC];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int c = blockIdx.x, hk = blockIdx.y;
-  if (c == 0 && hk == 0 && tid == 0) *status = 0;
+  const int c = blockIdx.x, hv = blockIdx.y, hk = hv / d.G;
+  if (c == 0 && hv == 0 && tid == 0) *status = 0;
   const Chunk ch = chunk_of(d, tb, c);
   if (ch.rows == 0) return;
   load_rows(Ks, kP, KP, in.k + (long long)ch.first * d.ks + (long long)hk * d.K, d.ks, ch.rows, d.K, d.kvec, tid, 128);
   load_rows(Qs, kP, KP, in.q + (long long)ch.first * d.qs + (long long)hk * d.K, d.qs, ch.rows, d.K, d.qvec, tid, 128);
   cp_commit();
+  uint8_t* record = records + ((size_t)c * d.HV + hv) * kRecordBytes;
+  if (w == 0) {  // G of two steps a lane; the sums in fp64, in units of log 2 as a high and a low fp32 part
+    double x[2];
+    float b[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * lane + i;
+      float v = 0.f;
+      b[i] = 0.f;
+      if (t < ch.rows) {
+        const size_t at = (size_t)(ch.first + t) * d.HV + hv;
+        v = gate(in.g, at, d.gate_bf16);
+        b[i] = gate(in.beta, at, d.gate_bf16);
+        v = v < kMinG ? kMinG : v;
+      }
+      x[i] = (double)v * 1.4426950408889634;
+    }
+    double sum = x[0] + x[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const double end = __shfl_sync(0xffffffffu, sum, 31);
+    float2* gr = reinterpret_cast<float2*>(record + kRecordGates) + lane;
+    float eg[2], ee[2], g2[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = 2 * lane + i;
+      const double gt = i ? sum : sum - x[1];
+      const float h = (float)gt;
+      s_hi[t] = h;
+      s_lo[t] = (float)(gt - (double)h);
+      s_beta[t] = b[i];
+      eg[i] = exp2f(h);
+      ee[i] = exp2f((float)(end - gt));
+      g2[i] = h;
+    }
+    gr[0] = make_float2(eg[0], eg[1]);
+    gr[kC / 2] = make_float2(ee[0], ee[1]);
+    gr[kC] = make_float2(b[0], b[1]);
+    gr[3 * kC / 2] = make_float2(g2[0], g2[1]);
+    gr[2 * kC] = make_float2(in.scale * eg[0], in.scale * eg[1]);
+  }
   cp_wait<0>();
   __syncthreads();
   const int r0 = 16 * w, g4 = lane >> 2, t2 = 2 * (lane & 3);
@@ -184,112 +229,85 @@ __global__ void __launch_bounds__(128) k_delta_prep(Dims d, Table tb, In in, uin
     }
   }
   __syncthreads();
-  for (int i = tid; i < kC * kFP; i += 128) Tf[i] = 0.f;
-  for (int gi = 0; gi < d.G; ++gi) {
-    const int hv = hk * d.G + gi;
-    uint8_t* record = records + ((size_t)c * d.HV + hv) * kRecordBytes;
-    if (w == 0) {  // G of two steps a lane; the sums in fp64, kept as a high and a low fp32 part
-      double x[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 2 * lane + i;
-        float v = 0.f, b = 0.f;
-        if (t < ch.rows) {
-          const size_t at = (size_t)(ch.first + t) * d.HV + hv;
-          v = gate(in.g, at, d.gate_bf16);
-          b = gate(in.beta, at, d.gate_bf16);
-          v = v < kMinG ? kMinG : v;
-        }
-        x[i] = v;
-        s_beta[t] = b;
-      }
-      double sum = x[0] + x[1];
+  for (int nt = 0; nt < 8; ++nt) {
+    if (nt > 2 * w + 1) break;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const double end = __shfl_sync(0xffffffffu, sum, 31);
-      float* gr = reinterpret_cast<float*>(record + kRecordGates);
+    for (int half = 0; half < 2; ++half) {
+      const int i = r0 + g4 + 8 * half, j = 8 * nt + t2;
+      float a[2], p[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 2 * lane + i;
-        const double gt = i ? sum : sum - x[1];
-        const float h = (float)gt, l = (float)(gt - (double)h);
-        s_hi[t] = h;
-        s_lo[t] = l;
-        gr[t] = expf((float)gt);
-        gr[kC + t] = expf((float)(end - gt));
-        gr[2 * kC + t] = s_beta[t];
-        gr[3 * kC + t] = (float)(gt * 1.4426950408889634);
-        gr[4 * kC + t] = in.scale * expf((float)gt);
+      for (int e = 0; e < 2; ++e) {
+        float dec;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(dec) : "f"((s_hi[i] - s_hi[j + e]) + (s_lo[i] - s_lo[j + e])));
+        a[e] = i > j + e ? s_beta[i] * dec * kk[nt][2 * half + e] : 0.f;
+        p[e] = i >= j + e ? in.scale * dec * qk[nt][2 * half + e] : 0.f;
       }
+      *reinterpret_cast<float2*>(Af + i * kFP + j) = make_float2(a[0], a[1]);
+      *reinterpret_cast<float2*>(Pf + i * kFP + j) = make_float2(p[0], p[1]);
     }
-    __syncthreads();
+  }
+  __syncwarp();
+  {  // the diagonal block of this warp, column lane % 16
+    float x[16];
 #pragma unroll
-    for (int nt = 0; nt < 8; ++nt) {
-      if (nt > 2 * w + 1) break;
+    for (int i = 0; i < 16; ++i) {
+      float s = i == (lane & 15) ? 1.f : 0.f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int i = r0 + g4 + 8 * half, j = 8 * nt + t2;
-        float a[2], p[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float dec = expf((s_hi[i] - s_hi[j + e]) + (s_lo[i] - s_lo[j + e]));
-          a[e] = i > j + e ? s_beta[i] * dec * kk[nt][2 * half + e] : 0.f;
-          p[e] = i >= j + e ? in.scale * dec * qk[nt][2 * half + e] : 0.f;
-        }
-        Af[i * kFP + j] = a[0];
-        Af[i * kFP + j + 1] = a[1];
-        uint32_t ph, pl;
-        split(p[0], p[1], ph, pl);
-        *reinterpret_cast<uint32_t*>(record + 2 * 8192 + tile_off(i, j)) = ph;
-        *reinterpret_cast<uint32_t*>(record + 3 * 8192 + tile_off(i, j)) = pl;
+      for (int j = 0; j < i; j += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(Af + (r0 + i) * kFP + r0 + j);
+        s = fmaf(-a.x, x[j], s);
+        if (j + 1 < i) s = fmaf(-a.y, x[j + 1], s);
+        if (j + 2 < i) s = fmaf(-a.z, x[j + 2], s);
+        if (j + 3 < i) s = fmaf(-a.w, x[j + 3], s);
       }
+      x[i] = s;
     }
     __syncwarp();
-    if (lane < 16) {  // the diagonal block of this warp, column `lane`
-      float x[16];
+    if (lane < 16)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float s = i == lane ? 1.f : 0.f;
+      for (int i = 0; i < 16; ++i) Af[(r0 + i) * kFP + r0 + lane] = x[i];
+  }
+  __syncthreads();
+  float m[2][4];
+  if ((w & 1) == 0) {  // rows 16 .. 31 (warp 0) and 48 .. 63 (warp 2): -b' c a'
+    const int a0 = 16 * w, b0 = a0 + 16;
+    mul16(m, Af + b0 * kFP + a0, Af + a0 * kFP + a0, 16, lane);
+    put16(Mf + w * 8 * kFP, m, 1.f, lane);
+    __syncwarp();
+    mul16(m, Af + b0 * kFP + b0, Mf + w * 8 * kFP, 16, lane);
+    put16(Af + b0 * kFP + a0, m, -1.f, lane);
+  } else {  // the blocks above the diagonal that the next products read
+    const int a0 = 16 * (w - 1);
+    for (int i = lane; i < 64; i += 32)
+      *reinterpret_cast<float4*>(Af + (a0 + (i >> 2)) * kFP + a0 + 16 + 4 * (i & 3)) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  const int br = 16 * (w >> 1), bc = 16 * (w & 1);  // one 16-block of the 32 x 32 product a warp
+  mul16(m, Af + (32 + br) * kFP, Af + bc, 32, lane);
+  put16(Mf + br * kFP + bc, m, 1.f, lane);
+  __syncthreads();
+  mul16(m, Af + (32 + br) * kFP + 32, Mf + bc, 32, lane);
+  put16(Af + (32 + br) * kFP + bc, m, -1.f, lane);
+  __syncthreads();
+  // 16-byte pieces of the four tiles in the order of memory, up to the diagonal's blocks
 #pragma unroll
-        for (int j = 0; j < i; ++j) s = fmaf(-Af[(r0 + i) * kFP + r0 + j], x[j], s);
-        x[i] = s;
-        Tf[(r0 + i) * kFP + r0 + lane] = s;
-      }
+  for (int n = 0; n < 4; ++n) {
+    const int i = (tid >> 3) + 16 * n, j = (tid & 7) ^ (i & 7);
+    if (8 * j >= 16 * (n + 1)) continue;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const float* f = (which ? Pf : Af) + i * kFP + 8 * j;
+      const float4 x = *reinterpret_cast<const float4*>(f), y = *reinterpret_cast<const float4*>(f + 4);
+      uint32_t h[4], l[4];
+      split(x.x, x.y, h[0], l[0]);
+      split(x.z, x.w, h[1], l[1]);
+      split(y.x, y.y, h[2], l[2]);
+      split(y.z, y.w, h[3], l[3]);
+      uint4* dst = reinterpret_cast<uint4*>(record + which * 16384 + tile_off(i, 8 * j));
+      dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+      dst[512] = make_uint4(l[0], l[1], l[2], l[3]);
     }
-    __syncthreads();
-    float m[2][4];
-    if ((w & 1) == 0) {  // rows 16 .. 31 (warp 0) and 48 .. 63 (warp 2): -b' c a'
-      const int a0 = 16 * w, b0 = a0 + 16;
-      mul16(m, Af + b0 * kFP + a0, Tf + a0 * kFP + a0, 16, lane);
-      put16(Mf + w * 8 * kFP, m, 1.f, lane);
-      __syncwarp();
-      mul16(m, Tf + b0 * kFP + b0, Mf + w * 8 * kFP, 16, lane);
-      put16(Tf + b0 * kFP + a0, m, -1.f, lane);
-    }
-    __syncthreads();
-    const int br = 16 * (w >> 1), bc = 16 * (w & 1);  // one 16-block of the 32 x 32 product a warp
-    mul16(m, Af + (32 + br) * kFP, Tf + bc, 32, lane);
-    put16(Mf + br * kFP + bc, m, 1.f, lane);
-    __syncthreads();
-    mul16(m, Tf + (32 + br) * kFP + 32, Mf + bc, 32, lane);
-    put16(Tf + (32 + br) * kFP + bc, m, -1.f, lane);
-    __syncthreads();
-    {
-      const int i = tid >> 1, j0 = 32 * (tid & 1);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          split(Tf[i * kFP + j0 + 8 * q + 2 * e], Tf[i * kFP + j0 + 8 * q + 2 * e + 1], h[e], l[e]);
-        *reinterpret_cast<uint4*>(record + tile_off(i, j0 + 8 * q)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(record + 8192 + tile_off(i, j0 + 8 * q)) = make_uint4(l[0], l[1], l[2], l[3]);
-      }
-    }
-    __syncthreads();
   }
 }
 
@@ -374,7 +392,7 @@ cudaError_t run_prep(const Dims& d, const Table& tb, const In& in, uint8_t* reco
   cudaError_t e = allow_smem(k_delta_prep<KP>, sm);
   if (e != cudaSuccess) return e;
   SSD_LAUNCH("k_delta_prep", st,
-             k_delta_prep<KP><<<dim3((unsigned)d.nc, (unsigned)d.H), 128, sm, st>>>(d, tb, in, records, status));
+             k_delta_prep<KP><<<dim3((unsigned)d.nc, (unsigned)d.HV), 128, sm, st>>>(d, tb, in, records, status));
   return cudaGetLastError();
 }
 
@@ -395,7 +413,7 @@ ssd_status make_dims(const ssd_delta_problem* p, bool f32_ok, Dims* d) {
   if (p->q_stride < 0 || p->k_stride < 0 || p->v_stride < 0) return SSD_ERR_INVALID_ARG;
   if (p->io_dtype == SSD_F32 && !f32_ok) return SSD_ERR_DTYPE;
   if (p->value_heads % p->nheads) return SSD_ERR_SHAPE;
-  if (p->key_dim > 128 || p->value_dim > 128 || p->nheads > 65535) return SSD_ERR_SHAPE;
+  if (p->key_dim > 128 || p->value_dim > 128 || p->value_heads > 65535) return SSD_ERR_SHAPE;
   constexpr long long kInt = 0x7fffffffll;
   if (p->batch > kInt || p->seqlen > kInt || p->value_heads > kInt) return SSD_ERR_SHAPE;
   const long long tokens = p->packed ? p->seqlen : p->batch * p->seqlen;

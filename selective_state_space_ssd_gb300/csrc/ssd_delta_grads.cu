@@ -396,31 +396,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ph = wk.step & 1;
       const int first = wk.ch.first, rows = wk.ch.rows;
       const bool cut = rows < kC;
-      if (wk.gi == 0) {
-        if (wk.qkn > 0 && !wait_warp(&bars.qk_free, (wk.qkn & 1) ^ 1, status, 121)) break;
-        uint8_t* qt = smem;
-        uint64_t* bar = cut ? &bars.tail : &bars.qk;
-        if (tid == 0) {
-          mbar_expect_tx(bar, kC * 128 * na * ((d.qvec ? 1 : 0) + (d.kvec ? 1 : 0)));
-          for (int a = 0; a < na; ++a) {
-            if (d.qvec) tma_load_3d(qt + a * 16384, &maps.q, 64 * a, wk.hk, first, bar);
-            if (d.kvec) tma_load_3d(qt + a * 16384 + kC * 128, &maps.k, 64 * a, wk.hk, first, bar);
-          }
-        }
-        if (!d.qvec) load_elements(qt, 128, d.KP, in.q + (long long)first * d.qs + (long long)wk.hk * d.K, d.qs, rows, d.K, tid);
-        if (!d.kvec) load_elements(qt + kC * 128, 128, d.KP, in.k + (long long)first * d.ks + (long long)wk.hk * d.K, d.ks, rows, d.K, tid);
-        if (cut) {
-          ok = wait_warp(&bars.tail, tails++ & 1, status, 122);
-          if (d.qvec) zero_rows(qt, 128, na, rows, tid);
-          if (d.kvec) zero_rows(qt + kC * 128, 128, na, rows, tid);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if ((tid & 31) == 0) mbar_arrive(&bars.qk);
-        if (cut && tid == 0) mbar_arrive(&bars.qk);
-        units = wk.qkn;
-        if (!ok) break;
-      }
       if (wk.step > 0 && !(ok = wait_warp(&bars.empty, ph ^ 1, status, 123))) break;
       uint64_t* bar = cut ? &bars.tail : &bars.full;
       const size_t item = wk.item();
@@ -447,6 +422,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((tid & 31) == 0) mbar_arrive(&bars.full);
       if (cut && tid == 0) mbar_arrive(&bars.full);
       loaded = wk.step;
+      if (wk.gi == 0) {
+        if (wk.qkn > 0 && !wait_warp(&bars.qk_free, (wk.qkn & 1) ^ 1, status, 121)) break;
+        uint8_t* qt = smem;
+        uint64_t* bar = cut ? &bars.tail : &bars.qk;
+        if (tid == 0) {
+          mbar_expect_tx(bar, kC * 128 * na * ((d.qvec ? 1 : 0) + (d.kvec ? 1 : 0)));
+          for (int a = 0; a < na; ++a) {
+            if (d.qvec) tma_load_3d(qt + a * 16384, &maps.q, 64 * a, wk.hk, first, bar);
+            if (d.kvec) tma_load_3d(qt + a * 16384 + kC * 128, &maps.k, 64 * a, wk.hk, first, bar);
+          }
+        }
+        if (!d.qvec) load_elements(qt, 128, d.KP, in.q + (long long)first * d.qs + (long long)wk.hk * d.K, d.qs, rows, d.K, tid);
+        if (!d.kvec) load_elements(qt + kC * 128, 128, d.KP, in.k + (long long)first * d.ks + (long long)wk.hk * d.K, d.ks, rows, d.K, tid);
+        if (cut) {
+          ok = wait_warp(&bars.tail, tails++ & 1, status, 122);
+          if (d.qvec) zero_rows(qt, 128, na, rows, tid);
+          if (d.kvec) zero_rows(qt + kC * 128, 128, na, rows, tid);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&bars.qk);
+        if (cut && tid == 0) mbar_arrive(&bars.qk);
+        units = wk.qkn;
+      }
     }
     // no copy is in flight when the block ends
     if (loaded >= 0) wait_warp(&bars.full, loaded & 1, status, 125);
@@ -485,17 +484,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           x = dot8(a[n], *reinterpret_cast<const uint4*>(smem + oOY + (j >> 3) * 16384 + sw128_chunk(kC + t, j & 7)), x);
       }
       x += __shfl_xor_sync(0xffffffffu, x, 1);
-      float y4[4] = {0.f, 0.f, 0.f, 0.f};
-      const int n16 = d.VP * d.KP / 8;  // the two images have the same layout, whatever it is
-      for (int j = tid; j < n16; j += 128 * kSumWarps) {
+      // <dS', S>: eight rows of both images as the operands of a small product, of which the diagonal is wanted; each
+      // lane's rows of the images have one layout, so one address serves both
+      float c4[4] = {0.f, 0.f, 0.f, 0.f};
+      const int sw = tid >> 5, groups = d.VP / 8;
+      const uint32_t sa = smem_u32(smem + oS), da = smem_u32(smem + oD);
+      for (int g = sw; g < groups * (d.KP / 64); g += kSumWarps) {
+        const int atom = g / groups, r = 8 * (g - atom * groups) + (lane & 7);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int m = j + 32 * kSumWarps * n;
-          if (m < n16)
-            y4[n] = dot8(reinterpret_cast<const uint4*>(smem + oS)[m], reinterpret_cast<const uint4*>(smem + oD)[m], y4[n]);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t at = (uint32_t)(atom * d.VP * 128) + sw128_chunk(r, 4 * h + (lane >> 3));
+          uint32_t m[4], n[4];
+          ldm4(m, sa + at);
+          ldm4(n, da + at);
+          const uint32_t a0[4] = {m[0], 0u, m[1], 0u}, a1[4] = {m[2], 0u, m[3], 0u};
+          mma(c4, a0, n[0], n[1]);
+          mma(c4, a1, n[2], n[3]);
         }
       }
-      float y = (y4[0] + y4[1]) + (y4[2] + y4[3]);
+      float y = (lane >> 2) == 2 * (lane & 3) ? c4[0] : (lane >> 2) == 2 * (lane & 3) + 1 ? c4[1] : 0.f;
 #pragma unroll
       for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
       // the head before has been finished: its sums have been read, and its decays, whose place the next copies take
