@@ -489,8 +489,9 @@ ssd_status ssd_delta_step(const ssd_delta_problem* prob, const void* q, const vo
  * ssd_norm_problem: io_dtype of x, y, dy, dx and weight_dtype of weight, bias,
  * dw, db (SSD_F32 or SSD_BF16 each; sums are fp32); rows >= 1 (< 2^31), dim
  * 1 .. 16384 (SSD_ERR_SHAPE), x_stride: elements from a row of x to the next
- * (0 = dense).  y, dy, dx are dense [rows, dim]; mean, rstd fp32 [rows].  x
- * needs the alignment of its type, every other pointer 16 bytes.
+ * (0 = dense).  y, dy, dx are dense [rows, dim]; mean, rstd fp32 [rows].  x,
+ * mean and rstd need the alignment of their type, every other pointer 16
+ * bytes.
  *
  * ssd_norm_forward: y, and mean and rstd unless NULL.  weight NULL: ones, bias
  *   NULL: zeros; eps >= 0.

@@ -168,8 +168,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, device=None):
+    """The ``cudaStream_t`` of a call.  With the index of the tensors' device the current stream's handle is looked up
+    without making a stream object, which a call of a few microseconds notices."""
     if stream is None:
+        if device is not None and _raw_stream is not None:
+            return _raw_stream(device)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -457,25 +464,52 @@ def kda_backward(cfg: dict, dout, ds_final, q, k, v, g, beta, s0=None, scale=Non
 
 
 # ------------------------------------------------------------- gated delta rule, one decay per head
+# The conveniences below are called once a token: what they look up by a call's sizes is kept (a few hundred
+# problem descriptions and sizes, by value), and the checks take the common case first.
+_kept: dict = {}
+
+
+def _keep(key, make):
+    got = _kept.get(key)
+    if got is None:
+        if len(_kept) >= 512:
+            _kept.clear()
+        got = _kept[key] = make()
+    return got
+
+
+def _delta_key(cfg: dict, packed: bool, qs: int, ks: int, vs: int) -> tuple:
+    return ("delta", cfg["dtype"], cfg.get("gate_dtype", "f32"), packed, cfg["batch"], cfg["seqlen"], cfg["nheads"],
+            cfg["value_heads"], cfg["key_dim"], cfg["value_dim"], qs, ks, vs)
+
+
+def _delta_struct(key: tuple) -> ssd_delta_problem:
+    return ssd_delta_problem(DTYPES[key[1]], DTYPES[key[2]], int(key[3]), 0, *key[4:])
+
+
 def delta_problem(cfg: dict, q=None, k=None, v=None, packed: bool = False) -> ssd_delta_problem:
     """An ``ssd_delta_problem`` from a config dict (``configs.DELTA_CONFIGS``); q, k, v (if given) set the strides from
     step to step and are checked against the sizes."""
-    p = ssd_delta_problem(DTYPES[cfg["dtype"]], DTYPES[cfg.get("gate_dtype", "f32")], int(packed), 0, cfg["batch"],
-                          cfg["seqlen"], cfg["nheads"], cfg["value_heads"], cfg["key_dim"], cfg["value_dim"], 0, 0, 0)
-    lead = (1 if packed else p.batch, p.seqlen)
-    for name, t, heads, dim in (("q", q, p.nheads, p.key_dim), ("k", k, p.nheads, p.key_dim),
-                                ("v", v, p.value_heads, p.value_dim)):
-        if t is not None:
-            setattr(p, name + "_stride", _step_stride(name, t, lead + (heads, dim), cfg["dtype"]))
-    return p
+    return _delta_struct(_delta_of(cfg, q, k, v, packed))
 
 
-def _step_stride(name: str, t, shape: tuple, dtype: str) -> int:
+def _delta_of(cfg: dict, q, k, v, packed: bool) -> tuple:
+    """The key of a call's problem, from its q, k, v."""
+    lead = (1 if packed else cfg["batch"], cfg["seqlen"])
+    h, hv, kd, vd = cfg["nheads"], cfg["value_heads"], cfg["key_dim"], cfg["value_dim"]
+    dt = _TORCH_DTYPE[cfg["dtype"]]
+    return _delta_key(cfg, packed, 0 if q is None else _step_stride("q", q, lead + (h, kd), dt),
+                      0 if k is None else _step_stride("k", k, lead + (h, kd), dt),
+                      0 if v is None else _step_stride("v", v, lead + (hv, vd), dt))
+
+
+def _step_stride(name: str, t, shape: tuple, dtype) -> int:
     """Elements from a step to the next of a tensor [b, T, heads, dim] whose heads are dense and whose batches follow
-    one another at T steps; raises ValueError for any other tensor."""
-    if t.dtype != _TORCH_DTYPE[dtype]:
-        raise ValueError(f"{name}: {t.dtype}, expected {_TORCH_DTYPE[dtype]}")
-    got, (b, steps, heads, dim) = tuple(t.shape), shape
+    one another at T steps (0: dense); raises ValueError for any other tensor."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    got = tuple(t.shape)
+    b, steps, heads, dim = shape
     if got != shape and not (b == 1 and got == shape[1:]):
         raise ValueError(f"{name}: shape {got}, expected {shape}")
     if t.is_contiguous():
@@ -489,11 +523,11 @@ def _step_stride(name: str, t, shape: tuple, dtype: str) -> int:
 
 
 def _dense(name: str, t, shape: tuple, dtype) -> None:
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype == dtype and t.is_contiguous()):
         return
-    if t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) not in (tuple(shape), tuple(shape[1:]) if shape[0] == 1 else ()):
+    if t.dtype != dtype or not t.is_contiguous() or not (shape[0] == 1 and tuple(t.shape) == shape[1:]):
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} (contiguous: {t.is_contiguous()}), expected contiguous "
-                         f"{dtype} {tuple(shape)}")
+                         f"{dtype} {shape}")
 
 
 def ssd_delta_workspace_size(prob: ssd_delta_problem, backward: bool, stashed: bool = False) -> int:
@@ -514,49 +548,59 @@ def ssd_delta_stash_size(prob: ssd_delta_problem) -> int:
 
 def ssd_delta_forward(prob, q, k, v, g, beta, s0, cu_seqlens, scale, o, s_final, stash, stash_bytes, ws, ws_bytes,
                       stream=None) -> None:
-    st = load().ssd_delta_forward(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(s0),
-                                  _ptr(cu_seqlens), float(scale), _ptr(o), _ptr(s_final), _ptr(stash),
-                                  int(stash_bytes), _ptr(ws), int(ws_bytes), _stream(stream))
+    st = (_lib or load()).ssd_delta_forward(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                            _ptr(s0), _ptr(cu_seqlens), scale, _ptr(o), _ptr(s_final), _ptr(stash),
+                                            stash_bytes, _ptr(ws), ws_bytes, _stream(stream))
     if st != SSD_OK:
         raise SSDError(st, "ssd_delta_forward")
 
 
 def ssd_delta_backward(prob, dout, ds_final, q, k, v, g, beta, s0, cu_seqlens, scale, dq, dk, dv, dg, dbeta, ds0, stash,
                        stash_bytes, ws, ws_bytes, stream=None) -> None:
-    st = load().ssd_delta_backward(ctypes.byref(prob), _ptr(dout), _ptr(ds_final), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                   _ptr(beta), _ptr(s0), _ptr(cu_seqlens), float(scale), _ptr(dq), _ptr(dk), _ptr(dv),
-                                   _ptr(dg), _ptr(dbeta), _ptr(ds0), _ptr(stash), int(stash_bytes), _ptr(ws),
-                                   int(ws_bytes), _stream(stream))
+    st = (_lib or load()).ssd_delta_backward(ctypes.byref(prob), _ptr(dout), _ptr(ds_final), _ptr(q), _ptr(k), _ptr(v),
+                                             _ptr(g), _ptr(beta), _ptr(s0), _ptr(cu_seqlens), scale, _ptr(dq),
+                                             _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta), _ptr(ds0), _ptr(stash),
+                                             stash_bytes, _ptr(ws), ws_bytes, _stream(stream))
     if st != SSD_OK:
         raise SSDError(st, "ssd_delta_backward")
 
 
 def ssd_delta_step(prob, q, k, v, g, beta, state, slots, num_slots, scale, o, stream=None) -> None:
-    st = load().ssd_delta_step(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state),
-                               _ptr(slots), int(num_slots), float(scale), _ptr(o), _stream(stream))
+    st = (_lib or load()).ssd_delta_step(ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                         _ptr(state), _ptr(slots), num_slots, scale, _ptr(o), _stream(stream))
     if st != SSD_OK:
         raise SSDError(st, "ssd_delta_step")
 
 
-def _delta_check(cfg, prob, q, g, beta, s0, cu_seqlens):
-    lead = (1 if prob.packed else prob.batch, prob.seqlen)
-    gt = _TORCH_DTYPE[cfg.get("gate_dtype", "f32")]
-    _dense("g", g, lead + (prob.value_heads,), gt)
-    _dense("beta", beta, lead + (prob.value_heads,), gt)
-    _dense("s0", s0, (prob.batch, prob.value_heads, prob.key_dim, prob.value_dim), torch.float32)
-    _dense("cu_seqlens", cu_seqlens, (prob.batch + 1,), torch.int32)
+def _delta_check(key, g, beta, s0, cu_seqlens):
+    _, _, gdt, packed, b, t, _, hv, kd, vd = key[:10]
+    lead = (1 if packed else b, t)
+    gt = _TORCH_DTYPE[gdt]
+    _dense("g", g, lead + (hv,), gt)
+    _dense("beta", beta, lead + (hv,), gt)
+    if s0 is not None:
+        _dense("s0", s0, (b, hv, kd, vd), torch.float32)
+    if cu_seqlens is not None:
+        _dense("cu_seqlens", cu_seqlens, (b + 1,), torch.int32)
     return lead
+
+
+def _like(t):
+    """An uninitialised dense tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def delta_stash(cfg: dict, device="cuda", packed: bool = False):
     """A buffer for what ``delta_forward`` keeps for ``delta_backward`` (uint8)."""
-    n = ssd_delta_stash_size(delta_problem(cfg, packed=packed))
+    key = _delta_key(cfg, packed, 0, 0, 0)
+    n = _keep(key + ("stash",), lambda: ssd_delta_stash_size(_delta_struct(key)))
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _delta_workspace(prob, backward, stashed, device):
-    n = ssd_delta_workspace_size(prob, backward, stashed)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device), n
+def _delta_workspace(key, backward, stashed, device):
+    n = _keep(key + (backward, stashed),
+              lambda: max(ssd_delta_workspace_size(_delta_struct(key), backward, stashed), 256))
+    return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
 def delta_forward(cfg: dict, q, k, v, g, beta, s0=None, scale=None, cu_seqlens=None, stash=None, stream=None,
@@ -564,16 +608,16 @@ def delta_forward(cfg: dict, q, k, v, g, beta, s0=None, scale=None, cu_seqlens=N
     """Allocate o and s_final, run ``ssd_delta_forward``; returns (o, s_final).  With ``cu_seqlens`` (int32,
     [batch + 1]) the sequences are packed on one axis of seqlen steps; ``stash`` (``delta_stash``) is filled for
     ``delta_backward``; scale defaults to key_dim^-1/2."""
-    packed = cu_seqlens is not None
-    prob = delta_problem(cfg, q, k, v, packed)
-    _delta_check(cfg, prob, q, g, beta, s0, cu_seqlens)
+    key = _delta_of(cfg, q, k, v, cu_seqlens is not None)
+    prob = _keep(key, lambda: _delta_struct(key))
+    _delta_check(key, g, beta, s0, cu_seqlens)
     scale = cfg["key_dim"] ** -0.5 if scale is None else scale
-    o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    s_final = torch.empty((cfg["batch"], cfg["value_heads"], cfg["key_dim"], cfg["value_dim"]), dtype=torch.float32,
-                          device=v.device)
-    ws, n = workspace if workspace is not None else _delta_workspace(prob, False, stash is not None, v.device)
+    dev = v.device
+    o = _like(v)
+    s_final = torch.empty((key[4], key[7], key[8], key[9]), dtype=torch.float32, device=dev)
+    ws, n = workspace if workspace is not None else _delta_workspace(key, False, stash is not None, dev)
     ssd_delta_forward(prob, q, k, v, g, beta, s0, cu_seqlens, scale, o, s_final, stash,
-                      0 if stash is None else stash.numel(), ws, n, stream)
+                      0 if stash is None else stash.numel(), ws, n, _stream(stream, dev.index))
     return o, s_final
 
 
@@ -581,31 +625,35 @@ def delta_backward(cfg: dict, dout, q, k, v, g, beta, ds_final=None, s0=None, sc
                    stream=None, workspace=None):
     """Allocate the gradients and run ``ssd_delta_backward``; returns dq, dk, dv, dg, dbeta and ds0 (None where s0 is
     None).  ``stash``: what ``delta_forward`` filled on the same inputs; without it the chunk states are made again."""
-    packed = cu_seqlens is not None
-    prob = delta_problem(cfg, q, k, v, packed)
-    lead = _delta_check(cfg, prob, q, g, beta, s0, cu_seqlens)
-    _dense("dout", dout, lead + (prob.value_heads, prob.value_dim), v.dtype)
-    _dense("ds_final", ds_final, (prob.batch, prob.value_heads, prob.key_dim, prob.value_dim), torch.float32)
+    key = _delta_of(cfg, q, k, v, cu_seqlens is not None)
+    prob = _keep(key, lambda: _delta_struct(key))
+    lead = _delta_check(key, g, beta, s0, cu_seqlens)
+    _dense("dout", dout, lead + (key[7], key[9]), v.dtype)
+    if ds_final is not None:
+        _dense("ds_final", ds_final, (key[4], key[7], key[8], key[9]), torch.float32)
     scale = cfg["key_dim"] ** -0.5 if scale is None else scale
-    new = lambda t: torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
-    out = {"dq": new(q), "dk": new(k), "dv": new(v), "dg": new(g), "dbeta": new(beta),
-           "ds0": None if s0 is None else new(s0)}
-    ws, n = workspace if workspace is not None else _delta_workspace(prob, True, stash is not None, v.device)
+    dev = v.device
+    out = {"dq": _like(q), "dk": _like(k), "dv": _like(v), "dg": _like(g), "dbeta": _like(beta),
+           "ds0": None if s0 is None else _like(s0)}
+    ws, n = workspace if workspace is not None else _delta_workspace(key, True, stash is not None, dev)
     ssd_delta_backward(prob, dout, ds_final, q, k, v, g, beta, s0, cu_seqlens, scale, out["dq"], out["dk"], out["dv"],
-                       out["dg"], out["dbeta"], out["ds0"], stash, 0 if stash is None else stash.numel(), ws, n, stream)
+                       out["dg"], out["dbeta"], out["ds0"], stash, 0 if stash is None else stash.numel(), ws, n,
+                       _stream(stream, dev.index))
     return out
 
 
 def delta_step(cfg: dict, q, k, v, g, beta, state, slots=None, scale=None, stream=None):
     """Allocate o and run ``ssd_delta_step``: seqlen steps of each sequence on its slot of ``state`` [slots, HV, K, V]
     (fp32), which is updated in place; returns o."""
-    prob = delta_problem(cfg, q, k, v)
-    _delta_check(cfg, prob, q, g, beta, None, None)
-    _dense("state", state, (state.shape[0], prob.value_heads, prob.key_dim, prob.value_dim), torch.float32)
-    _dense("slots", slots, (prob.batch,), torch.int32)
+    key = _delta_of(cfg, q, k, v, False)
+    prob = _keep(key, lambda: _delta_struct(key))
+    _delta_check(key, g, beta, None, None)
+    ns = state.shape[0]
+    _dense("state", state, (ns, key[7], key[8], key[9]), torch.float32)
+    _dense("slots", slots, (key[4],), torch.int32)
     scale = cfg["key_dim"] ** -0.5 if scale is None else scale
-    o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    ssd_delta_step(prob, q, k, v, g, beta, state, slots, state.shape[0], scale, o, stream)
+    o = _like(v)
+    ssd_delta_step(prob, q, k, v, g, beta, state, slots, ns, scale, o, _stream(stream, v.device.index))
     return o
 
 
@@ -617,16 +665,24 @@ def _name(dtype) -> str:
     raise ValueError(f"{dtype}: float32 or bfloat16 expected")
 
 
-def norm_problem(x, weight=None) -> ssd_norm_problem:
-    """An ``ssd_norm_problem`` for x [.., D]: contiguous, or two-dimensional with a stride from row to row."""
+def _norm_of(x, weight) -> tuple:
+    """The key of a call's problem: (type, weight's type, rows, dim, stride)."""
     dim = x.shape[-1]
-    wt = DTYPES[_name(weight.dtype)] if weight is not None else DTYPES["f32"]
     stride = 0
     if not x.is_contiguous():
         if x.dim() != 2 or (dim > 1 and x.stride(1) != 1) or x.stride(0) < dim:
             raise ValueError(f"x: strides {tuple(x.stride())}: rows have to be dense, at one stride")
         stride = x.stride(0)
-    return ssd_norm_problem(DTYPES[_name(x.dtype)], wt, x.numel() // max(dim, 1), dim, stride)
+    return x.dtype, torch.float32 if weight is None else weight.dtype, x.numel() // max(dim, 1), dim, stride
+
+
+def _norm_struct(key: tuple) -> ssd_norm_problem:
+    return ssd_norm_problem(DTYPES[_name(key[0])], DTYPES[_name(key[1])], *key[2:])
+
+
+def norm_problem(x, weight=None) -> ssd_norm_problem:
+    """An ``ssd_norm_problem`` for x [.., D]: contiguous, or two-dimensional with a stride from row to row."""
+    return _norm_struct(_norm_of(x, weight))
 
 
 def ssd_norm_workspace_size(prob: ssd_norm_problem) -> int:
@@ -638,15 +694,15 @@ def ssd_norm_workspace_size(prob: ssd_norm_problem) -> int:
 
 
 def ssd_norm_forward(prob, x, weight, bias, eps, y, mean, rstd, stream=None) -> None:
-    st = load().ssd_norm_forward(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), float(eps), _ptr(y), _ptr(mean),
-                                 _ptr(rstd), _stream(stream))
+    st = (_lib or load()).ssd_norm_forward(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), eps, _ptr(y),
+                                           _ptr(mean), _ptr(rstd), _stream(stream))
     if st != SSD_OK:
         raise SSDError(st, "ssd_norm_forward")
 
 
 def ssd_norm_backward(prob, dy, x, mean, rstd, weight, dx, dw, db, ws, ws_bytes, stream=None) -> None:
-    st = load().ssd_norm_backward(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),
-                                  _ptr(dw), _ptr(db), _ptr(ws), int(ws_bytes), _stream(stream))
+    st = (_lib or load()).ssd_norm_backward(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight),
+                                            _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws_bytes, _stream(stream))
     if st != SSD_OK:
         raise SSDError(st, "ssd_norm_backward")
 
@@ -654,32 +710,38 @@ def ssd_norm_backward(prob, dy, x, mean, rstd, weight, dx, dw, db, ws, ws_bytes,
 def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stream=None):
     """Layer norm of x [.., D]; weight and bias [D] (either may be None) of one type.  Returns y (contiguous), mean and
     rstd (fp32, one per row)."""
-    prob = norm_problem(x, weight if weight is not None else bias)
+    key = _norm_of(x, weight if weight is not None else bias)
+    prob = _keep(key, lambda: _norm_struct(key))
     if weight is not None:
-        _dense("weight", weight, (prob.dim,), weight.dtype)
+        _dense("weight", weight, (key[3],), key[1])
     if bias is not None:
-        _dense("bias", bias, (prob.dim,), weight.dtype if weight is not None else bias.dtype)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    stats = torch.empty((2, -(-prob.rows // 4) * 4), dtype=torch.float32, device=x.device)
-    mean, rstd = (s[:prob.rows].view(x.shape[:-1]) for s in stats)
-    ssd_norm_forward(prob, x, weight, bias, eps, y, mean, rstd, stream)
+        _dense("bias", bias, (key[3],), key[1])
+    y = _like(x)
+    dev = x.device
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty_like(mean)
+    ssd_norm_forward(prob, x, weight, bias, eps, y, mean, rstd, _stream(stream, dev.index))
     return y, mean, rstd
 
 
 def norm_backward(dy, x, mean, rstd, weight=None, stream=None, workspace=None):
     """The gradients of ``norm_forward``: dx (contiguous), and dw and db in the weight's type (fp32 without a
     weight)."""
-    prob = norm_problem(x, weight)
+    key = _norm_of(x, weight)
+    prob = _keep(key, lambda: _norm_struct(key))
     if dy.dtype != x.dtype or dy.shape != x.shape or not dy.is_contiguous():
         raise ValueError(f"dy: {dy.dtype} {tuple(dy.shape)}, expected contiguous {x.dtype} {tuple(x.shape)}")
     if weight is not None:
-        _dense("weight", weight, (prob.dim,), weight.dtype)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    wt = torch.float32 if weight is None else weight.dtype
-    dw = torch.empty(prob.dim, dtype=wt, device=x.device)
-    db = torch.empty(prob.dim, dtype=wt, device=x.device)
+        _dense("weight", weight, (key[3],), key[1])
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t.dtype != torch.float32 or t.numel() != key[2] or not t.is_contiguous():
+            raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous float32, one per row")
+    dx = _like(x)
+    dev = x.device
+    dw, db = torch.empty(key[3], dtype=key[1], device=dev), torch.empty(key[3], dtype=key[1], device=dev)
     if workspace is None:
-        n = ssd_norm_workspace_size(prob)
-        workspace = torch.empty(n, dtype=torch.uint8, device=x.device), n
-    ssd_norm_backward(prob, dy, x, mean, rstd, weight, dx, dw, db, workspace[0], workspace[1], stream)
+        n = _keep(key + ("ws",), lambda: ssd_norm_workspace_size(prob))
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev), n
+    ssd_norm_backward(prob, dy, x, mean, rstd, weight, dx, dw, db, workspace[0], workspace[1],
+                      _stream(stream, dev.index))
     return {"dx": dx, "dw": dw, "db": db}

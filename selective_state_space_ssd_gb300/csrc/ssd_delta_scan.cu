@@ -122,8 +122,8 @@ __device__ __forceinline__ void write_state(float* s, const float (&S)[NK], int 
     if (k0 + i < K && v < V) s[(size_t)(k0 + i) * V + v] = S[i];
 }
 
-// Columns of tensor memory.  fp32 results: X (then Y high, low in place), QS (forward: (Q S)^T; reverse: U, then dY),
-// R (then R' high, low in place), O2 (forward: (P R)^T) or F (reverse: the scaled dO^T, high and low), D (the state's
+// Columns of tensor memory.  fp32 results: X (then Y high, low in place; reverse: then dY), QS (forward: (Q S)^T; reverse:
+// U), R (then R' high, low in place), O2 (forward: (P R)^T) or F (reverse: the scaled dO^T, high and low), D (the state's
 // update); the state's operand, high and low, and R's for o and the stash (over the low part of a full-width state,
 // which has been read by then).
 template <int KP>
@@ -546,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         put_split(taddr(tm, lane0, C::R + 16 * wg), a);
       }
       signal_tmem(&bars.rp, lane);
-      {  // dY for the side warps, over U
+      {  // dY for the side warps, over X
         uint32_t u[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(x[j]);
-        st16u(taddr(tm, lane0, U + 16 * wg), u);
+        st16u(taddr(tm, lane0, C::X + 16 * wg), u);
       }
       const float keep = gates[kC - 1];
       signal_tmem(&bars.ro, lane);
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < 8; ++b) {
         uint32_t x[8];
         float be[8];
-        tmem_ld8_nowait(taddr(tm, lane0, U + 8 * b), x);
+        tmem_ld8_nowait(taddr(tm, lane0, C::X + 8 * b), x);
         lds8(gates + 2 * kC + 8 * b, be);
         tmem_wait_ld();
         if (b == 7) signal_read(&bars.e2, lane);
@@ -626,7 +626,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t km = sdesc_sw128(smem_u32(st), 128 * 128, 1024), qm = sdesc_sw128(smem_u32(st) + kC * 128, 128 * 128, 1024);
       const uint64_t od = sdesc_sw128(smem_u32(st) + Tiles<KP>::kKQ, kC * 128, 1024);  // dO^T: [step][v]
       if (!wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 71)) break;
-      if (i > 0 && !wait_warp(&bars.e2, ph ^ 1, status, 77)) break;
       tc_fence_after();
       if (elect_one()) {  // U^T = dO^T P: the steps of 16-block kb reach the steps t <= 16 kb + 15
 #pragma unroll
@@ -637,6 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
+      if (i > 0 && !wait_warp(&bars.e2, ph ^ 1, status, 77)) break;  // the side warps have dY of the chunk before
       if (!wait_warp(&bars.s, ph, status, 72)) break;
       tc_fence_after();
       if (elect_one()) {

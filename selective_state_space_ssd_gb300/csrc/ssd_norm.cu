@@ -82,13 +82,16 @@ struct Row {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int c = col(i, t);
-      if constexpr (kVec && sizeof(U) == sizeof(T)) {
-        float y[Width<U>::n];
+      if constexpr (kVec && W >= Width<U>::n) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) y[j] = fill;
-        if (c < D) ld16(p + c, y);
+        for (int k = 0; k < W; k += Width<U>::n) {
+          float y[Width<U>::n];
 #pragma unroll
-        for (int j = 0; j < W; ++j) x[i * W + j] = y[j];
+          for (int j = 0; j < Width<U>::n; ++j) y[j] = fill;
+          if (c < D) ld16(p + c + k, y);
+#pragma unroll
+          for (int j = 0; j < Width<U>::n; ++j) x[i * W + k + j] = y[j];
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < W; ++j) x[i * W + j] = c + j < D ? ld1(p + c + j) : fill;
@@ -148,7 +151,14 @@ __device__ __forceinline__ void row_sum(float (&x)[NV], float* red, int t) {
 
 template <int TPR>
 constexpr int block_threads() {
-  return TPR < 256 ? 256 : TPR;
+  return TPR < 128 ? 128 : TPR;
+}
+// Registers of the backward: five values an element, and the rest.
+template <int TPR, int E>
+constexpr int backward_blocks_per_sm() {
+  return 65536 / (block_threads<TPR>() * (5 * E + 48 < 255 ? 5 * E + 48 : 255)) > 0
+             ? 65536 / (block_threads<TPR>() * (5 * E + 48 < 255 ? 5 * E + 48 : 255))
+             : 1;
 }
 
 template <typename T, int TPR, int E, bool kVec>
@@ -189,7 +199,7 @@ __global__ void __launch_bounds__(block_threads<TPR>())
 }
 
 template <typename T, int TPR, int E, bool kVec>
-__global__ void __launch_bounds__(block_threads<TPR>())
+__global__ void __launch_bounds__(block_threads<TPR>(), backward_blocks_per_sm<TPR, E>())
     k_norm_backward(Args a, const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ mean,
                     const float* __restrict__ rstd, const void* w, T* dx, float* part) {
   using R = Row<T, TPR, E, kVec>;
@@ -262,8 +272,10 @@ __global__ void __launch_bounds__(1024) k_norm_columns(const float* __restrict__
   const float* p = part + (size_t)blockIdx.y * n * D;
   const int c = blockIdx.x * 32 + threadIdx.x;
   float x = 0.f;
-  if (c < D)
+  if (c < D) {
+#pragma unroll 8
     for (int i = threadIdx.y; i < n; i += 32) x += p[(size_t)i * D + c];
+  }
   s[threadIdx.y][threadIdx.x] = x;
   __syncthreads();
   x = s[threadIdx.x][threadIdx.y];  // one column a warp
@@ -286,11 +298,27 @@ struct Call {
   bool backward;
 };
 
-// Blocks of the backward: two or four an SM of this GPU's 152, so that the loads of some cover the sums of others.
-// Narrow rows have the room for more.
+// Threads a row and elements a thread: the fewest threads, from 8 to 512, with at most 24 elements each, in eights (a
+// row of 2560 is 128 threads of 24, 83% of them used; a head's 128 values are eight threads of 16).  More elements a
+// thread mean fewer steps of the sums across threads, fewer leave the backward room for several blocks an SM.
+struct Shape {
+  int tpr, e;
+};
+constexpr Shape shape_of(int D) {
+  int t = 8;
+  while (t < 512 && t * 24 < D) t *= 2;
+  int e = (D + 8 * t - 1) / (8 * t) * 8;
+  return Shape{t, e};
+}
+
+// Blocks of the backward, each with a row of partial sums: as many as this GPU's 152 SMs hold at once, four an SM at
+// most.
 int backward_blocks(long long rows, int D) {
-  const long long groups = D <= 128 ? 16 : D <= 512 ? 8 : D <= 2048 ? 2 : 1;
-  const long long most = D <= 512 ? 608 : 304, want = (rows + groups - 1) / groups;
+  const Shape s = shape_of(D);
+  const int threads = s.tpr < 128 ? 128 : s.tpr, regs = 5 * s.e + 48 < 255 ? 5 * s.e + 48 : 255;
+  int per = 65536 / (threads * regs);
+  per = per < 1 ? 1 : per > 4 ? 4 : per;
+  const long long groups = threads / s.tpr, want = (rows + groups - 1) / groups, most = 152 * per;
   return (int)(want < most ? want : most);
 }
 
@@ -313,27 +341,29 @@ void launch(const Call& c, cudaStream_t st) {
                                                                                              c.db, c.a.wbf16));
 }
 
-// Threads a row and elements a thread: 16 elements (eight on narrow rows) leave the backward, which holds five values
-// for each, the registers for two blocks an SM; rows past 8192 take 32.
+template <typename T, int TPR, bool kVec>
+void by_elements(const Call& c, int e, cudaStream_t st) {
+  if constexpr (TPR == 8)
+    if (e == 8) return launch<T, TPR, 8, kVec>(c, st);
+  if constexpr (TPR == 512)
+    if (e == 32) return launch<T, TPR, 32, kVec>(c, st);
+  if (e == 16)
+    launch<T, TPR, 16, kVec>(c, st);
+  else
+    launch<T, TPR, 24, kVec>(c, st);
+}
 template <typename T, bool kVec>
 void by_width(const Call& c, cudaStream_t st) {
-  const int D = c.a.D;
-  if (D <= 128)
-    launch<T, 16, 8, kVec>(c, st);
-  else if (D <= 256)
-    launch<T, 32, 8, kVec>(c, st);
-  else if (D <= 512)
-    launch<T, 32, 16, kVec>(c, st);
-  else if (D <= 1024)
-    launch<T, 128, 8, kVec>(c, st);
-  else if (D <= 2048)
-    launch<T, 128, 16, kVec>(c, st);
-  else if (D <= 4096)
-    launch<T, 256, 16, kVec>(c, st);
-  else if (D <= 8192)
-    launch<T, 512, 16, kVec>(c, st);
-  else
-    launch<T, 512, 32, kVec>(c, st);
+  const Shape s = shape_of(c.a.D);
+  switch (s.tpr) {
+    case 8: return by_elements<T, 8, kVec>(c, s.e, st);
+    case 16: return by_elements<T, 16, kVec>(c, s.e, st);
+    case 32: return by_elements<T, 32, kVec>(c, s.e, st);
+    case 64: return by_elements<T, 64, kVec>(c, s.e, st);
+    case 128: return by_elements<T, 128, kVec>(c, s.e, st);
+    case 256: return by_elements<T, 256, kVec>(c, s.e, st);
+    default: return by_elements<T, 512, kVec>(c, s.e, st);
+  }
 }
 void run(const Call& c, bool f32, cudaStream_t st) {
   const int w = f32 ? 4 : 8;
@@ -400,9 +430,11 @@ ssd_status ssd_norm_forward(const ssd_norm_problem* prob, const void* x, const v
   bool f32;
   ssd_status s = norm::make(prob, &c, &f32);
   if (s != SSD_OK) return s;
-  if ((s = norm::check({y}, {weight, bias, mean, rstd})) != SSD_OK) return s;
+  if ((s = norm::check({y}, {weight, bias})) != SSD_OK) return s;
   if (!x) return SSD_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(x) % (f32 ? 4 : 2)) return SSD_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(x) % (f32 ? 4 : 2) || reinterpret_cast<uintptr_t>(mean) % 4 ||
+      reinterpret_cast<uintptr_t>(rstd) % 4)
+    return SSD_ERR_ALIGNMENT;
   if (!(eps >= 0.f)) return SSD_ERR_INVALID_ARG;
   c.a.eps = eps;
   c.x = x;
@@ -422,9 +454,11 @@ ssd_status ssd_norm_backward(const ssd_norm_problem* prob, const void* dy, const
   bool f32;
   ssd_status s = norm::make(prob, &c, &f32);
   if (s != SSD_OK) return s;
-  if ((s = norm::check({dy, mean, rstd, dx}, {weight, dw, db, ws})) != SSD_OK) return s;
-  if (!x) return SSD_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(x) % (f32 ? 4 : 2)) return SSD_ERR_ALIGNMENT;
+  if ((s = norm::check({dy, dx}, {weight, dw, db, ws})) != SSD_OK) return s;
+  if (!x || !mean || !rstd) return SSD_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(x) % (f32 ? 4 : 2) || reinterpret_cast<uintptr_t>(mean) % 4 ||
+      reinterpret_cast<uintptr_t>(rstd) % 4)
+    return SSD_ERR_ALIGNMENT;
   if (dw || db) {
     if (!ws) return SSD_ERR_INVALID_ARG;
     if (ws_bytes < norm::workspace(c)) return SSD_ERR_WORKSPACE;
