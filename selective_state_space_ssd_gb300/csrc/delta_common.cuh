@@ -54,14 +54,27 @@ struct In {
   float scale;
 };
 
+// A long sequence of few heads in parts.  The chunks of every sequence are cut into `parts` runs of the same number; a
+// chunk's step is affine in the state, S_out = M S_in + B, so a first launch walks the runs but the last from a zero
+// state (B; the first run from s0) and, with V = 0, from the identity (M), k_delta_join goes through the runs
+// (S_in of run i + 1 = M_i S_in_i + B_i), and the scan proper walks all runs at once.  The reverse scan is affine in the
+// gradient of the state that leaves a chunk and is split the same way, from the last run on.
+struct Split {
+  int parts;      // 1: none
+  float* states;  // [N * HV][parts - 1][K][V]: B, then S_in of the run after it
+  float* maps;    // [N * HV][parts - 2][KP][KP]: M of runs 1 .., zeros around it
+};
+
 // The scans (ssd_delta_scan.cu).  S / R (null: not kept): the state entering each chunk and R, both bf16 and transposed,
 // as 128-byte-swizzled images: S^T [KP / 64][VP rows][64 keys], R^T [VP rows][64 steps].  o may be null (S and R only).
 // dS / dY of the reverse scan: the gradient of the state leaving each chunk, laid out like S, and dY by steps,
 // [ceil(VP / 64)][64 steps][64 columns].
-cudaError_t forward_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, bf16* o, float* s_final,
-                         bf16* S, bf16* R, int* status, cudaStream_t st);
-cudaError_t reverse_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const bf16* dout,
-                         const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status, cudaStream_t st);
+cudaError_t forward_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const Split& split,
+                         bf16* o, float* s_final, bf16* S, bf16* R, int* status, cudaStream_t st);
+cudaError_t reverse_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const Split& split,
+                         const bf16* dout, const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status,
+                         cudaStream_t st);
+int scan_parts(const Dims& d);
 // dQ, dK, dbeta, dg of every chunk (ssd_delta_grads.cu).
 struct GradOut {
   bf16 *dq, *dk;

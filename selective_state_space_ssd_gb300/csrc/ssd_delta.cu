@@ -337,6 +337,15 @@ Table carve_table(const Dims& d, Carver& cv) {
   }
   return t;
 }
+Split carve_split(const Dims& d, Carver& cv) {
+  Split sp = {scan_parts(d), nullptr, nullptr};
+  const size_t units = (size_t)d.N * d.HV;
+  if (sp.parts > 1) {
+    sp.states = cv.take<float>(units * (sp.parts - 1) * d.K * d.V);
+    sp.maps = cv.take<float>(units * (sp.parts - 2) * d.KP * d.KP);
+  }
+  return sp;
+}
 struct Grads {
   bf16 *dS, *dY;
 };
@@ -352,6 +361,7 @@ size_t workspace(const Dims& d, bool backward, bool stashed) {
   Carver cv(nullptr);
   carve_table(d, cv);
   if (backward) carve_grads(d, cv);
+  carve_split(d, cv);
   if (!stashed) {
     if (backward)
       carve_kept(d, cv);
@@ -496,6 +506,7 @@ ssd_status ssd_delta_forward(const ssd_delta_problem* prob, const void* q, const
   d.vvec = d.vvec && al16(v);
   Carver cv(ws);
   const Table tb = carve_table(d, cv);
+  const Split split = carve_split(d, cv);
   Kept kept = {};
   if (stash) {
     Carver cs(stash);
@@ -506,7 +517,7 @@ ssd_status ssd_delta_forward(const ssd_delta_problem* prob, const void* q, const
   const In in{(const bf16*)q, (const bf16*)k, (const bf16*)v, g, beta, s0, scale};
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = prepare(d, tb, in, kept.records, cu_seqlens, (int*)ws, st);
-  if (e == cudaSuccess) e = forward_scan(d, tb, in, kept.records, (bf16*)o, s_final, kept.S, kept.R, (int*)ws, st);
+  if (e == cudaSuccess) e = forward_scan(d, tb, in, kept.records, split, (bf16*)o, s_final, kept.S, kept.R, (int*)ws, st);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -534,6 +545,7 @@ ssd_status ssd_delta_backward(const ssd_delta_problem* prob, const void* dout, c
   Carver cv(ws);
   const Table tb = carve_table(d, cv);
   const Grads gr = carve_grads(d, cv);
+  const Split split = carve_split(d, cv);
   Kept kept;
   if (stash) {
     Carver cs(const_cast<void*>(stash));
@@ -550,10 +562,10 @@ ssd_status ssd_delta_backward(const ssd_delta_problem* prob, const void* dout, c
     e = cudaMemsetAsync(ws, 0, sizeof(int32_t), st);
   } else {
     e = prepare(d, tb, in, kept.records, cu_seqlens, (int*)ws, st);
-    if (e == cudaSuccess) e = forward_scan(d, tb, in, kept.records, nullptr, nullptr, kept.S, kept.R, (int*)ws, st);
+    if (e == cudaSuccess) e = forward_scan(d, tb, in, kept.records, split, nullptr, nullptr, kept.S, kept.R, (int*)ws, st);
   }
   if (e == cudaSuccess)
-    e = reverse_scan(d, tb, in, kept.records, (const bf16*)dout, ds_final, (bf16*)dv, ds0, gr.dS, gr.dY, (int*)ws, st);
+    e = reverse_scan(d, tb, in, kept.records, split, (const bf16*)dout, ds_final, (bf16*)dv, ds0, gr.dS, gr.dY, (int*)ws, st);
   if (e == cudaSuccess)
     e = chunk_grads(d, tb, in, kept.records, (const bf16*)dout, kept.S, kept.R, gr.dS, gr.dY, out, (int*)ws, st);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;

@@ -65,7 +65,7 @@ struct Loader {
   const Dims& d;
   const In& in;
   const Maps& maps;
-  const bf16* v;
+  const bf16* v;  // null: zeros
   long long vstride;
   bool vvec, with_q;
   int hk, hv;
@@ -74,7 +74,7 @@ struct Loader {
 
   __device__ bool operator()(uint8_t* st, uint64_t* full, const uint8_t* record, int first, int rows, int tid,
                              int* status) {
-    const bool kt = d.kvec, qt = with_q && d.qvec, vt = vvec, cut = rows < kC;
+    const bool kt = d.kvec, qt = with_q && d.qvec, vt = vvec && v, cut = rows < kC;
     uint8_t* vtile = st + Tiles<KP>::kKQ;
     if (tid == 0) {
       uint64_t* bar = cut ? tail : full;
@@ -92,7 +92,10 @@ struct Loader {
     if (!kt) load_elements(st, 128, KP, in.k + (long long)first * d.ks + (long long)hk * d.K, d.ks, rows, d.K, tid);
     if (with_q && !qt)
       load_elements(st + kC * 128, 128, KP, in.q + (long long)first * d.qs + (long long)hk * d.K, d.qs, rows, d.K, tid);
-    if (!vt) load_elements(vtile, kC, 128, v + (long long)first * vstride + (long long)hv * d.V, vstride, rows, d.V, tid);
+    if (!v)
+      zero_rows(vtile, kC, 2, 0, tid);
+    else if (!vt)
+      load_elements(vtile, kC, 128, v + (long long)first * vstride + (long long)hv * d.V, vstride, rows, d.V, tid);
     bool ok = true;
     if (cut) {
       ok = wait_warp(tail, tails & 1, status, 43);
@@ -136,16 +139,46 @@ __device__ __forceinline__ constexpr int pair_col(int base, int kb, bool low) { 
 struct Block {
   int hv, hk;
   Seq sq;
-  size_t su;
+  size_t unit, su;  // sequence and value head; its state's offset
 };
-__device__ __forceinline__ Block block_of(const Dims& d, const Table& tb) {
+__device__ __forceinline__ Block block_of(const Dims& d, const Table& tb, int unit) {
   Block b;
-  const int n = blockIdx.x / d.HV;
-  b.hv = blockIdx.x - n * d.HV;
+  const int n = unit / d.HV;
+  b.hv = unit - n * d.HV;
   b.hk = b.hv / d.G;
   b.sq = sequence(d, tb, n);
-  b.su = ((size_t)n * d.HV + b.hv) * d.K * d.V;
+  b.unit = (size_t)unit;
+  b.su = b.unit * d.K * d.V;
   return b;
+}
+// The chunks c0 .. c1 - 1 of a block's sequence that it walks, from where to where its state goes, and whether it is a
+// map (an identity to start from, no V).
+struct Run {
+  int c0, c1;
+  const float* from;
+  float* to;
+  int rows, columns;  // of the state at `to`
+  bool map;
+};
+// part: in the order of the walk, `back`: from the last chunk on.
+__device__ __forceinline__ Run run_of(const Dims& d, const Split& sp, const Block& b, int part, bool back, bool map,
+                                      bool first_pass, const float* s0, float* s_final) {
+  Run r;
+  const int nc = b.sq.nc, per = (nc + sp.parts - 1) / sp.parts;
+  r.c0 = min(nc, (back ? sp.parts - 1 - part : part) * per);
+  r.c1 = min(nc, r.c0 + per);
+  float* states = sp.states + (b.unit * (sp.parts - 1) + part) * d.K * d.V;
+  r.map = map;
+  r.rows = map ? d.KP : d.K;
+  r.columns = map ? d.KP : d.V;
+  if (first_pass) {
+    r.from = part == 0 && s0 ? s0 + b.su : nullptr;
+    r.to = map ? sp.maps + (b.unit * (sp.parts - 2) + part - 1) * d.KP * d.KP : states;
+  } else {
+    r.from = part > 0 ? states - d.K * d.V : s0 ? s0 + b.su : nullptr;
+    r.to = part == sp.parts - 1 && s_final ? s_final + b.su : nullptr;
+  }
+  return r;
 }
 
 __device__ __forceinline__ void init_bars(Bars* b) {
@@ -246,28 +279,42 @@ __device__ __forceinline__ void store_tile(const uint8_t* tile, bf16* dst, long 
 // ---------------------------------------------------------------- forward
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_delta_scan(Dims d, Table tb, In in, const __grid_constant__ Maps maps, const uint8_t* records, bf16* o,
-                 float* s_final, bf16* Sout, bf16* Rout, int* status) {
+    k_delta_scan(Dims d, Table tb, In in, const __grid_constant__ Maps maps, const uint8_t* records, Split sp,
+                 bool first_pass, bf16* o, float* s_final, bf16* Sout, bf16* Rout, int* status) {
   using C = Cols<KP>;
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
   __shared__ uint32_t tslot;
+  __shared__ Block s_blk;  // (kept here: the chain has no registers to spare)
+  __shared__ Run s_run;
   uint8_t* smem = aligned_smem(raw);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  if (threadIdx.x == 0) init_bars(&bars);
+  if (threadIdx.x == 0) {
+    init_bars(&bars);
+    const int per_unit = first_pass ? 2 * sp.parts - 3 : sp.parts, unit = blockIdx.x / per_unit, r = blockIdx.x - unit * per_unit;
+    s_blk = block_of(d, tb, unit);
+    s_run = run_of(d, sp, s_blk, first_pass ? (r + 1) >> 1 : r, false, first_pass && r > 0 && !(r & 1), first_pass,
+                           in.s0, s_final);
+  }
   if (w == kMmaWarp) tmem_alloc(&tslot, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tslot;
-  const Block blk = block_of(d, tb);
-  const int nc = blk.sq.nc;
+  // blocks of a sequence and value head: its runs; of the first pass: run 0, then the runs 1 .. and their maps in turn
+  const Block& blk = s_blk;
+  const Run& run = s_run;
+  const int nc = run.c1 - run.c0, chunk0 = blk.sq.chunk + run.c0, step0 = blk.sq.start + run.c0 * kC,
+            steps = blk.sq.len - run.c0 * kC;
   const bool stash = Sout != nullptr;
 
   if (w < kChainWarps) {
     const int wg = w >> 2, lane0 = 32 * (w & 3), v = lane0 + lane, k0 = wg * (KP / 4);
     float S[KP / 4];
-    read_state(S, in.s0 ? in.s0 + blk.su : nullptr, d.K, d.V, k0, v);
+    read_state(S, run.from, d.K, d.V, k0, v);
+    if (run.map)
+#pragma unroll
+      for (int j = 0; j < KP / 4; ++j) S[j] = k0 + j == v && v < d.K ? 1.f : 0.f;
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
       const uint8_t* st = smem + (c & 1) * Tiles<KP>::kBytes;
@@ -308,15 +355,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 16; ++i) a[i] *= x[i];  // R' = e^{G_end - G} R
       put_split(taddr(tm, lane0, C::R + 16 * wg), a);
       signal_tmem(&bars.rp, lane);
-      put_split(taddr(tm, lane0, C::Ro + 16 * wg), x);  // R itself, for o and the stash
       const float keep = gates[kC - 1];
-      signal_tmem(&bars.ro, lane);
+      if (o || stash) {
+        put_split(taddr(tm, lane0, C::Ro + 16 * wg), x);  // R itself
+        signal_tmem(&bars.ro, lane);
+      }
+      __syncwarp();
       if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
       if (!wait_warp(&bars.d, ph, status, 16)) break;
       tc_fence_after();
       update_state<KP>(tm, lane0, k0, keep, S);
     }
-    if (s_final) write_state(s_final + blk.su, S, d.K, d.V, k0, v);
+    if (run.to) write_state(run.to, S, run.rows, run.columns, k0, v);
   } else if (w < kMmaWarp) {
     const int lane0 = 32 * (w & 3), v = lane0 + lane, tid = threadIdx.x - 32 * kChainWarps;
     const long long os = (long long)d.HV * d.V;
@@ -326,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ph = c & 1;
       const float* gates =
           reinterpret_cast<const float*>(smem + (c & 1) * Tiles<KP>::kBytes + Tiles<KP>::kRec + kRecordGates);
-      const size_t item = (size_t)(blk.sq.chunk + c) * d.HV + blk.hv;
+      const size_t item = (size_t)(chunk0 + c) * d.HV + blk.hv;
       if (stash) {  // the state entering the chunk, and R, both as the bf16 operands hold them
         if (tiles_free(tid, !wait_warp(&bars.s, ph, status, 21))) break;
         tc_fence_after();
@@ -367,10 +417,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __float2bfloat16_rn(fmaf(e[i], __uint_as_float(q[i]), __uint_as_float(r[i])));
         }
         named_bar(kSideBar, 32 * kSideWarps);
-        store_tile(reinterpret_cast<const uint8_t*>(tile), o + ((long long)(blk.sq.start + c * kC) * d.HV + blk.hv) * d.V,
-                   os, min(kC, blk.sq.len - c * kC), d.V, d.ovec, tid);
+        store_tile(reinterpret_cast<const uint8_t*>(tile), o + ((long long)(step0 + c * kC) * d.HV + blk.hv) * d.V,
+                   os, min(kC, steps - c * kC), d.V, d.ovec, tid);
         if (stash) named_bar(kSideBar, 32 * kSideWarps);  // the next state's image covers this tile
       }
+      // (a wait, so that no warp is a phase ahead)
+      if (!o && !stash && !wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 25)) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
     }
@@ -456,13 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait_warp(&bars.done, 0, status, 37);
   } else {
     const int tid = threadIdx.x - 32 * (kMmaWarp + 1);
-    Loader<KP> ld{d, in, maps, in.v, d.vs, d.vvec, o != nullptr, blk.hk, blk.hv, &bars.tail, 0};
+    Loader<KP> ld{d, in, maps, run.map ? nullptr : in.v, d.vs, d.vvec, o != nullptr, blk.hk, blk.hv, &bars.tail, 0};
     int loaded = -1;
     for (int c = 0; c < nc; ++c) {
       if (c >= 2 && !wait_warp(&bars.empty[c & 1], ((c >> 1) & 1) ^ 1, status, 41)) break;
       const bool ok = ld(smem + (c & 1) * Tiles<KP>::kBytes, &bars.full[c & 1],
-                         records + ((size_t)(blk.sq.chunk + c) * d.HV + blk.hv) * kRecordBytes, blk.sq.start + c * kC,
-                         min(kC, blk.sq.len - c * kC), tid, status);
+                         records + ((size_t)(chunk0 + c) * d.HV + blk.hv) * kRecordBytes, step0 + c * kC,
+                         min(kC, steps - c * kC), tid, status);
       loaded = c;
       if (!ok) break;
     }
@@ -479,35 +531,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---------------------------------------------------------------- reverse
 template <int KP>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_delta_rev(Dims d, Table tb, In in, const __grid_constant__ Maps maps, const uint8_t* records, const bf16* dout,
-                const float* ds_final, bf16* dv, float* ds0, bf16* dSout, bf16* dYout, int* status) {
+    k_delta_rev(Dims d, Table tb, In in, const __grid_constant__ Maps maps, const uint8_t* records, Split sp,
+                bool first_pass, const bf16* dout, const float* ds_final, bf16* dv, float* ds0, bf16* dSout, bf16* dYout, int* status) {
   using C = Cols<KP>;
   constexpr int U = C::QS, F = C::O2;
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
   __shared__ uint32_t tslot;
+  __shared__ Block s_blk;  // (kept here: the chain has no registers to spare)
+  __shared__ Run s_run;
   uint8_t* smem = aligned_smem(raw);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  if (threadIdx.x == 0) init_bars(&bars);
+  if (threadIdx.x == 0) {
+    init_bars(&bars);
+    const int per_unit = first_pass ? 2 * sp.parts - 3 : sp.parts, unit = blockIdx.x / per_unit, r = blockIdx.x - unit * per_unit;
+    s_blk = block_of(d, tb, unit);
+    s_run = run_of(d, sp, s_blk, first_pass ? (r + 1) >> 1 : r, true, first_pass && r > 0 && !(r & 1), first_pass,
+                           ds_final, ds0);
+  }
   if (w == kMmaWarp) tmem_alloc(&tslot, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tslot;
-  const Block blk = block_of(d, tb);
-  const int nc = blk.sq.nc;
+  const Block& blk = s_blk;
+  const Run& run = s_run;
+  const int nc = run.c1 - run.c0, chunk0 = blk.sq.chunk + run.c0, step0 = blk.sq.start + run.c0 * kC,
+            steps = blk.sq.len - run.c0 * kC;
   const long long os = (long long)d.HV * d.V;
 
   // i counts the chunks in the order they are walked; chunk nc - 1 - i
   if (w < kChainWarps) {
     const int wg = w >> 2, lane0 = 32 * (w & 3), v = lane0 + lane, k0 = wg * (KP / 4);
     float S[KP / 4];
-    read_state(S, ds_final ? ds_final + blk.su : nullptr, d.K, d.V, k0, v);
+    read_state(S, run.from, d.K, d.V, k0, v);
+    if (run.map)
+#pragma unroll
+      for (int j = 0; j < KP / 4; ++j) S[j] = k0 + j == v && v < d.K ? 1.f : 0.f;
     for (int i = 0; i < nc; ++i) {
       const uint32_t ph = i & 1;
       const uint8_t* st = smem + (i & 1) * Tiles<KP>::kBytes;
       const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
-      if (i > 0) {
+      if (i > 0 && !first_pass) {
         if (!wait_warp(&bars.e1, ph ^ 1, status, 51)) break;
         tc_fence_after();
       }
@@ -546,20 +611,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         put_split(taddr(tm, lane0, C::R + 16 * wg), a);
       }
       signal_tmem(&bars.rp, lane);
-      {  // dY for the side warps, over X
+      const float keep = gates[kC - 1];
+      if (!first_pass) {  // dY for the side warps, over X
         uint32_t u[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(x[j]);
         st16u(taddr(tm, lane0, C::X + 16 * wg), u);
+        signal_tmem(&bars.ro, lane);
       }
-      const float keep = gates[kC - 1];
-      signal_tmem(&bars.ro, lane);
+      __syncwarp();
       if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
       if (!wait_warp(&bars.d, ph, status, 55)) break;
       tc_fence_after();
       update_state<KP>(tm, lane0, k0, keep, S);
     }
-    if (ds0) write_state(ds0 + blk.su, S, d.K, d.V, k0, v);
+    if (run.to) write_state(run.to, S, run.rows, run.columns, k0, v);
   } else if (w < kMmaWarp) {
     const int lane0 = 32 * (w & 3), v = lane0 + lane, tid = threadIdx.x - 32 * kChainWarps;
     uint8_t* out = smem + 2 * Tiles<KP>::kBytes;
@@ -570,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c = nc - 1 - i;
       const uint8_t* st = smem + (i & 1) * Tiles<KP>::kBytes;
       const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
-      const size_t item = (size_t)(blk.sq.chunk + c) * d.HV + blk.hv;
+      const size_t item = (size_t)(chunk0 + c) * d.HV + blk.hv;
       bool ok = wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 61);
       ok = ok && (i == 0 || wait_warp(&bars.d, ph ^ 1, status, 62));  // F of the chunk before has been read
       if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;  // (and the tile's last rows have been stored)
@@ -589,6 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         st4u(taddr(tm, lane0, F + 16 * (b >> 1) + 4 * (b & 1) + 8), l);
       }
       signal_tmem(&bars.f, lane);
+      if (first_pass) {
+        if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
+        continue;
+      }
       if (tiles_free(tid, !wait_warp(&bars.s, ph, status, 63))) break;
       tc_fence_after();
       stage_state<KP>(tm, lane0, out, d.VP, v);
@@ -612,8 +682,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       send_tile(dYout + item * va * 64 * kC, out, (uint32_t)(va * 64 * kC * 2), tid);
       if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
-      store_tile(reinterpret_cast<const uint8_t*>(tile), dv + ((long long)(blk.sq.start + c * kC) * d.HV + blk.hv) * d.V,
-                 os, min(kC, blk.sq.len - c * kC), d.V, d.ovec, tid);
+      store_tile(reinterpret_cast<const uint8_t*>(tile), dv + ((long long)(step0 + c * kC) * d.HV + blk.hv) * d.V,
+                 os, min(kC, steps - c * kC), d.V, d.ovec, tid);
     }
     if (tid == 0) tma_store_wait0();
   } else if (w == kMmaWarp) {
@@ -636,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (i > 0 && !wait_warp(&bars.e2, ph ^ 1, status, 77)) break;  // the side warps have dY of the chunk before
+      if (i > 0 && !first_pass && !wait_warp(&bars.e2, ph ^ 1, status, 77)) break;  // the side warps have dY of the chunk before
       if (!wait_warp(&bars.s, ph, status, 72)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -690,14 +760,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     wait_warp(&bars.done, 0, status, 76);
   } else {
     const int tid = threadIdx.x - 32 * (kMmaWarp + 1);
-    Loader<KP> ld{d, in, maps, dout, os, d.ovec, true, blk.hk, blk.hv, &bars.tail, 0};
+    Loader<KP> ld{d, in, maps, run.map ? nullptr : dout, os, d.ovec, true, blk.hk, blk.hv, &bars.tail, 0};
     int loaded = -1;
     for (int i = 0; i < nc; ++i) {
       const int c = nc - 1 - i;
       if (i >= 2 && !wait_warp(&bars.empty[i & 1], ((i >> 1) & 1) ^ 1, status, 81)) break;
       const bool ok = ld(smem + (i & 1) * Tiles<KP>::kBytes, &bars.full[i & 1],
-                         records + ((size_t)(blk.sq.chunk + c) * d.HV + blk.hv) * kRecordBytes, blk.sq.start + c * kC,
-                         min(kC, blk.sq.len - c * kC), tid, status);
+                         records + ((size_t)(chunk0 + c) * d.HV + blk.hv) * kRecordBytes, step0 + c * kC,
+                         min(kC, steps - c * kC), tid, status);
       loaded = i;
       if (!ok) break;
     }
@@ -724,42 +794,157 @@ cudaError_t make_maps(const Dims& d, const In& in, const bf16* v, long long vstr
   return e;
 }
 
+// S_in of the runs of a split scan: S_in of run 1 is there (the first run's result), S_in of run i + 1 is M_i S_in_i + B_i
+// in the place of B_i.  A block per (sequence, value head) and 16 columns; a thread four rows and four columns.  fp32; the
+// next map's copy is in flight while a product is computed.
+constexpr int kMapPitch = 132;
+__global__ void __launch_bounds__(128) k_delta_join(Split sp, int K, int KP, int V) {
+  extern __shared__ __align__(16) float sm[];  // two maps [KP][kMapPitch], the state's columns [KP][16]
+  float* cols = sm + 2 * KP * kMapPitch;
+  const int tid = threadIdx.x, r0 = 4 * (tid >> 2), c0 = 4 * (tid & 3), v0 = blockIdx.y * 16 + c0;
+  float* st = sp.states + (size_t)blockIdx.x * (sp.parts - 1) * K * V;
+  const float* maps = sp.maps + (size_t)blockIdx.x * (sp.parts - 2) * KP * KP;
+  const auto fetch = [&](int i) {
+    const float* m = maps + (size_t)(i - 1) * KP * KP;
+    const uint32_t dst = su32(sm + (i & 1) * KP * kMapPitch);
+    for (int j = tid; j < KP * KP / 4; j += 128) {
+      const int r = j / (KP / 4), c = 4 * (j - r * (KP / 4));
+      cp16(dst + 4u * (uint32_t)(r * kMapPitch + c), m + r * KP + c, true);
+    }
+    cp_commit();
+  };
+  fetch(1);
+  const bool on = r0 < KP;
+  if (on)
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        cols[(r0 + a) * 16 + c0 + b] = r0 + a < K && v0 + b < V ? st[(size_t)(r0 + a) * V + v0 + b] : 0.f;
+  for (int i = 1; i < sp.parts - 1; ++i) {
+    float* out = st + (size_t)i * K * V;
+    float x[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) x[a][b] = r0 + a < K && v0 + b < V ? out[(size_t)(r0 + a) * V + v0 + b] : 0.f;
+    if (i + 1 < sp.parts - 1) fetch(i + 1);
+    else cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    if (on) {
+      const float* m = sm + (i & 1) * KP * kMapPitch + r0 * kMapPitch;
+      for (int k = 0; k < KP; k += 4) {
+        float4 s[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = *reinterpret_cast<const float4*>(cols + (k + e) * 16 + c0);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const float4 y = *reinterpret_cast<const float4*>(m + a * kMapPitch + k);
+          const float ya[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[a][0] = fmaf(ya[e], s[e].x, x[a][0]);
+            x[a][1] = fmaf(ya[e], s[e].y, x[a][1]);
+            x[a][2] = fmaf(ya[e], s[e].z, x[a][2]);
+            x[a][3] = fmaf(ya[e], s[e].w, x[a][3]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (on)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        *reinterpret_cast<float4*>(cols + (r0 + a) * 16 + c0) = make_float4(x[a][0], x[a][1], x[a][2], x[a][3]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (r0 + a < K && v0 + b < V) out[(size_t)(r0 + a) * V + v0 + b] = x[a][b];
+      }
+  }
+}
+
+cudaError_t join(const Dims& d, const Split& split, cudaStream_t st) {
+  if (split.parts <= 2) return cudaSuccess;
+  const uint32_t smem = 4 * (uint32_t)(2 * d.KP * kMapPitch + 16 * d.KP);
+  const cudaError_t e = allow_smem(k_delta_join, smem);
+  if (e != cudaSuccess) return e;
+  SSD_LAUNCH("k_delta_join", st,
+             k_delta_join<<<dim3((unsigned)(d.N * d.HV), (unsigned)((d.V + 15) / 16)), 128, smem, st>>>(split, d.K, d.KP, d.V));
+  return cudaGetLastError();
+}
+
 template <int KP>
-cudaError_t run_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, bf16* o, float* s_final,
-                     bf16* S, bf16* R, int* status, cudaStream_t st) {
+cudaError_t run_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const Split& split, bf16* o,
+                     float* s_final, bf16* S, bf16* R, int* status, cudaStream_t st) {
   Maps maps = {};
   cudaError_t e = make_maps(d, in, in.v, d.vs, d.vvec, &maps);
   if (e == cudaSuccess) e = allow_smem(k_delta_scan<KP>, scan_smem<KP>());
   if (e != cudaSuccess) return e;
+  const unsigned units = (unsigned)(d.N * d.HV);
+  if (split.parts > 1) {
+    SSD_LAUNCH("k_delta_maps", st,
+               k_delta_scan<KP><<<units * (2 * split.parts - 3), kThreads, scan_smem<KP>(), st>>>(
+                   d, tb, in, maps, records, split, true, nullptr, nullptr, nullptr, nullptr, status));
+    if ((e = join(d, split, st)) != cudaSuccess) return e;
+  }
   SSD_LAUNCH("k_delta_scan", st,
-             k_delta_scan<KP><<<(unsigned)(d.N * d.HV), kThreads, scan_smem<KP>(), st>>>(d, tb, in, maps, records, o,
-                                                                                        s_final, S, R, status));
+             k_delta_scan<KP><<<units * split.parts, kThreads, scan_smem<KP>(), st>>>(
+                 d, tb, in, maps, records, split, false, o, s_final, S, R, status));
   return cudaGetLastError();
 }
 template <int KP>
-cudaError_t run_rev(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const bf16* dout,
-                    const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status, cudaStream_t st) {
+cudaError_t run_rev(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const Split& split,
+                    const bf16* dout, const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status,
+                    cudaStream_t st) {
   Maps maps = {};
   cudaError_t e = make_maps(d, in, dout, (long long)d.HV * d.V, d.ovec, &maps);
   if (e == cudaSuccess) e = allow_smem(k_delta_rev<KP>, scan_smem<KP>());
   if (e != cudaSuccess) return e;
+  const unsigned units = (unsigned)(d.N * d.HV);
+  if (split.parts > 1) {
+    SSD_LAUNCH("k_delta_rev_maps", st,
+               k_delta_rev<KP><<<units * (2 * split.parts - 3), kThreads, scan_smem<KP>(), st>>>(
+                   d, tb, in, maps, records, split, true, dout, ds_final, nullptr, nullptr, nullptr, nullptr, status));
+    if ((e = join(d, split, st)) != cudaSuccess) return e;
+  }
   SSD_LAUNCH("k_delta_rev", st,
-             k_delta_rev<KP><<<(unsigned)(d.N * d.HV), kThreads, scan_smem<KP>(), st>>>(
-                 d, tb, in, maps, records, dout, ds_final, dv, ds0, dS, dY, status));
+             k_delta_rev<KP><<<units * split.parts, kThreads, scan_smem<KP>(), st>>>(
+                 d, tb, in, maps, records, split, false, dout, ds_final, dv, ds0, dS, dY, status));
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t forward_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, bf16* o, float* s_final,
-                         bf16* S, bf16* R, int* status, cudaStream_t st) {
-  return d.KP == 64 ? run_scan<64>(d, tb, in, records, o, s_final, S, R, status, st)
-                    : run_scan<128>(d, tb, in, records, o, s_final, S, R, status, st);
+// Runs of a scan, by the number of chunk steps that its launches take one after another: a block an SM, 152 of
+// them; a step of the first pass (no o) is about three quarters of one with o, and the two further launches cost about
+// eight.  16 heads of 256 chunks: 256 steps in one run, 80 in nine.  A packed batch is taken at its mean length.
+int scan_parts(const Dims& d) {
+  const long long units = (long long)d.N * d.HV, nc = d.nc / d.N;
+  const auto waves = [](long long blocks) { return (blocks + 151) / 152; };
+  int best = 1;
+  double least = 0.8 * (double)(waves(units) * nc);  // a split has to be worth it
+  for (int s = 2; s <= 16 && units * s <= 2 * 152; ++s) {
+    const long long per = (nc + s - 1) / s;
+    const double t = 0.75 * (double)(waves(units * (2 * s - 3)) * per) + (double)(waves(units * s) * per) + 8.0;
+    if (t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
 }
-cudaError_t reverse_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const bf16* dout,
-                         const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status, cudaStream_t st) {
-  return d.KP == 64 ? run_rev<64>(d, tb, in, records, dout, ds_final, dv, ds0, dS, dY, status, st)
-                    : run_rev<128>(d, tb, in, records, dout, ds_final, dv, ds0, dS, dY, status, st);
+
+cudaError_t forward_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const Split& split,
+                         bf16* o, float* s_final, bf16* S, bf16* R, int* status, cudaStream_t st) {
+  return d.KP == 64 ? run_scan<64>(d, tb, in, records, split, o, s_final, S, R, status, st)
+                    : run_scan<128>(d, tb, in, records, split, o, s_final, S, R, status, st);
+}
+cudaError_t reverse_scan(const Dims& d, const Table& tb, const In& in, const uint8_t* records, const Split& split,
+                         const bf16* dout, const float* ds_final, bf16* dv, float* ds0, bf16* dS, bf16* dY, int* status,
+                         cudaStream_t st) {
+  return d.KP == 64 ? run_rev<64>(d, tb, in, records, split, dout, ds_final, dv, ds0, dS, dY, status, st)
+                    : run_rev<128>(d, tb, in, records, split, dout, ds_final, dv, ds0, dS, dY, status, st);
 }
 
 }  // namespace delta

@@ -106,6 +106,42 @@ CASES = {
     "dim128": cfg_of(b=2, T=300, H=2, HV=4, K=128, V=128, gates="bf16"),
 }
 
+# chunk counts at which a scan of few heads is cut into runs, and at which a block takes several chunks in turn
+LONG = {
+    "few_heads": cfg_of(T=64 * 40 + 7, H=1, HV=2, K=40, V=72),
+    "one_head": cfg_of(T=64 * 33, H=1, HV=1, K=128, V=128, gates="bf16"),
+    "unaligned": cfg_of(b=2, T=64 * 24 + 1, H=1, HV=1, K=33, V=17),
+    "many_chunks": cfg_of(b=3, T=64 * 20 + 5, H=3, HV=9, K=16, V=16),
+}
+
+
+@pytest.mark.parametrize("name", sorted(LONG))
+def test_long_sequences_match_the_oracle(name):
+    cfg = LONG[name]
+    cpu = make(cfg, 14, decay=0.01)
+    got = run(cfg, cuda(cpu))
+    check(got, oracle(cfg, cpu, cfg["key_dim"] ** -0.5), {**TOL_F, **TOL_B})
+    again = run(cfg, cuda(cpu), stash=binding.delta_stash(cfg))
+    for k in got:
+        assert torch.equal(got[k], again[k]), k
+
+
+def test_long_packed_sequences_match_the_oracle():
+    """Two long sequences, short ones and empty ones in one batch, cut into runs by their mean length."""
+    lengths = [64 * 37 + 3, 0, 64 * 70, 5, 0]
+    cfg = cfg_of(b=5, T=sum(lengths), H=1, HV=1, K=32, V=24)
+    cpu = make(cfg, 15, packed=True, decay=0.01)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32)
+    got = run(cfg, cuda(cpu), cu=cu.cuda())
+    for i, (a, length) in enumerate(zip(cu[:-1].tolist(), lengths)):
+        if not length:
+            assert torch.equal(got["s_final"][i].cpu(), cpu["s0"][i]) and torch.equal(got["ds0"][i].cpu(), cpu["ds_final"][i])
+            continue
+        one = {k: (x[i:i + 1] if k in ("s0", "ds_final") else x[:, a:a + length]) for k, x in cpu.items()}
+        ref = oracle(dict(cfg, batch=1, seqlen=length), one, 32 ** -0.5)
+        part = {k: (x[i:i + 1] if k in ("s_final", "ds0") else x[:, a:a + length]) for k, x in got.items()}
+        check(part, ref, {**TOL_F, **TOL_B})
+
 
 @pytest.mark.parametrize("name", sorted(CASES))
 def test_matches_the_oracle(name):
