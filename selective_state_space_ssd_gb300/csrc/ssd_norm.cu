@@ -7,6 +7,7 @@
 // n-th row and keep their columns' dw and db in registers; one row of partial sums a block goes to the workspace and
 // k_norm_columns adds those in block order, so the result does not depend on timing.
 #include <initializer_list>
+#include <type_traits>
 
 #include "ssd.h"
 #include "ssd_internal.h"
@@ -45,15 +46,13 @@ template <>
 struct Width<bf16> {
   static constexpr int n = 8;
 };
-__device__ __forceinline__ void ld16(const float* p, float (&x)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  x[0] = v.x;
-  x[1] = v.y;
-  x[2] = v.z;
-  x[3] = v.w;
+__device__ __forceinline__ void as_floats(const uint4& v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x);
+  x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z);
+  x[3] = __uint_as_float(v.w);
 }
-__device__ __forceinline__ void ld16(const bf16* p, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void as_floats(const uint4& v, float (&x)[8]) {
   x[0] = lo_f(v.x);
   x[1] = hi_f(v.x);
   x[2] = lo_f(v.y);
@@ -62,6 +61,10 @@ __device__ __forceinline__ void ld16(const bf16* p, float (&x)[8]) {
   x[5] = hi_f(v.z);
   x[6] = lo_f(v.w);
   x[7] = hi_f(v.w);
+}
+template <typename T, int N>
+__device__ __forceinline__ void ld16(const T* p, float (&x)[N]) {
+  as_floats(*reinterpret_cast<const uint4*>(p), x);
 }
 __device__ __forceinline__ void st16(float* p, const float (&x)[4]) {
   *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -98,6 +101,29 @@ struct Row {
       }
     }
   }
+  // The elements as they lie in memory, for a row that is wanted later.
+  using Piece = typename std::conditional<kVec, uint4, T>::type;
+  static __device__ __forceinline__ void fetch(const T* p, int D, int t, Piece (&r)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int c = col(i, t);
+      r[i] = Piece{};
+      if (c < D) r[i] = *reinterpret_cast<const Piece*>(p + c);
+    }
+  }
+  static __device__ __forceinline__ void unpack(const Piece (&r)[NP], float (&x)[E]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      if constexpr (kVec) {
+        float y[Width<T>::n];
+        as_floats(r[i], y);
+#pragma unroll
+        for (int j = 0; j < W; ++j) x[i * W + j] = y[j];
+      } else {
+        x[i] = ld1(&r[i]);
+      }
+    }
+  }
   static __device__ __forceinline__ void store(T* p, int D, int t, const float (&x)[E]) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
@@ -123,7 +149,7 @@ struct Row {
       load(static_cast<const float*>(w), D, t, x, fill);
     }
   }
-  static __device__ __forceinline__ bool in(int e, int D, int t) { return col(e / W, t) + e % W < D; }
+  static __device__ __forceinline__ bool in(int i, int D, int t) { return col(i, t) < D; }  // piece i: all of it or none
 };
 
 // Sums over the TPR threads of a row, in every one of them.  TPR > 32: `red` holds NV floats per warp of the row; two
@@ -153,53 +179,68 @@ template <int TPR>
 constexpr int block_threads() {
   return TPR < 128 ? 128 : TPR;
 }
-// Registers of the backward: five values an element, and the rest.
-template <int TPR, int E>
-constexpr int backward_blocks_per_sm() {
-  return 65536 / (block_threads<TPR>() * (5 * E + 48 < 255 ? 5 * E + 48 : 255)) > 0
-             ? 65536 / (block_threads<TPR>() * (5 * E + 48 < 255 ? 5 * E + 48 : 255))
-             : 1;
+// Blocks an SM: by their registers, five values an element backward (two rows as they lie in memory, h, dw, db), three
+// forward.
+template <int TPR, int E, bool kBack>
+constexpr int blocks_per_sm() {
+  const int regs = kBack ? (5 * E + 48 < 255 ? 5 * E + 48 : 255) : 3 * E + 32;
+  const int n = 65536 / (block_threads<TPR>() * regs);
+  return n < 1 ? 1 : n;
 }
 
+// The groups of a block take every n-th row each; a group's next row is on its way while it sums the one before.
 template <typename T, int TPR, int E, bool kVec>
-__global__ void __launch_bounds__(block_threads<TPR>())
+__global__ void __launch_bounds__(block_threads<TPR>(), blocks_per_sm<TPR, E, false>())
     k_norm_forward(Args a, const T* __restrict__ x, const void* w, const void* b, T* y, float* mean, float* rstd) {
   using R = Row<T, TPR, E, kVec>;
   constexpr int kGroups = block_threads<TPR>() / TPR;
   __shared__ float red[kGroups][(TPR + 31) / 32];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-  const long long row = (long long)blockIdx.x * kGroups + grp;
-  const bool live = row < a.rows;
-  float v[E];
-  R::load(x + (live ? row : 0) * a.xs, live ? a.D : 0, t, v, 0.f);
-  float s[1] = {0.f};
+  const long long step = (long long)gridDim.x * kGroups;
+  const float inv = 1.f / (float)a.D;
+  typename R::Piece next[R::NP];
+  const auto fetch = [&](long long row) { R::fetch(x + (row < a.rows ? row : 0) * a.xs, row < a.rows ? a.D : 0, t, next); };
+  long long row = (long long)blockIdx.x * kGroups + grp;
+  fetch(row);
+  for (long long first = (long long)blockIdx.x * kGroups; first < a.rows; first += step, row += step) {
+    const bool live = row < a.rows;
+    float v[E];
+    R::unpack(next, v);
+    fetch(row + step);
+    float s[1] = {0.f};
 #pragma unroll
-  for (int e = 0; e < E; ++e) s[0] += v[e];
-  row_sum<TPR, 1>(s, red[grp], t);
-  const float inv = 1.f / (float)a.D, m = s[0] * inv;
-  s[0] = 0.f;
+    for (int e = 0; e < E; ++e) s[0] += v[e];
+    row_sum<TPR, 1>(s, red[grp], t);
+    const float m = s[0] * inv;
+    s[0] = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    v[e] = R::in(e, a.D, t) ? v[e] - m : 0.f;
-    s[0] = fmaf(v[e], v[e], s[0]);
-  }
-  row_sum<TPR, 1>(s, red[grp], t);
-  const float r = rsqrtf(fmaf(s[0], inv, a.eps));
-  if (!live) return;
-  float wt[E], bt[E];
-  R::weights(w, a.wbf16, a.D, t, wt, 1.f);
-  R::weights(b, a.wbf16, a.D, t, bt, 0.f);
+    for (int i = 0; i < R::NP; ++i)
+      if (R::in(i, a.D, t))
 #pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = fmaf(v[e] * r, wt[e], bt[e]);
-  R::store(y + (size_t)row * a.D, a.D, t, v);
-  if (t == 0) {
-    if (mean) mean[row] = m;
-    if (rstd) rstd[row] = r;
+        for (int e = i * R::W; e < (i + 1) * R::W; ++e) {
+          v[e] -= m;
+          s[0] = fmaf(v[e], v[e], s[0]);
+        }
+    row_sum<TPR, 1>(s, red[grp], t);
+    const float r = rsqrtf(fmaf(s[0], inv, a.eps));
+    if (!live) continue;
+    float wt[E];
+    R::weights(w, a.wbf16, a.D, t, wt, 1.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = v[e] * r * wt[e];
+    R::weights(b, a.wbf16, a.D, t, wt, 0.f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += wt[e];
+    R::store(y + (size_t)row * a.D, a.D, t, v);
+    if (t == 0) {
+      if (mean) mean[row] = m;
+      if (rstd) rstd[row] = r;
+    }
   }
 }
 
 template <typename T, int TPR, int E, bool kVec>
-__global__ void __launch_bounds__(block_threads<TPR>(), backward_blocks_per_sm<TPR, E>())
+__global__ void __launch_bounds__(block_threads<TPR>(), blocks_per_sm<TPR, E, true>())
     k_norm_backward(Args a, const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ mean,
                     const float* __restrict__ rstd, const void* w, T* dx, float* part) {
   using R = Row<T, TPR, E, kVec>;
@@ -207,22 +248,35 @@ __global__ void __launch_bounds__(block_threads<TPR>(), backward_blocks_per_sm<T
   __shared__ float red[kGroups][2 * ((TPR + 31) / 32)];
   __shared__ float s_part[kGroups > 1 ? TPR * E : 1];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-  float wt[E], dw[E], db[E];
-  R::weights(w, a.wbf16, a.D, t, wt, 1.f);
+  float dw[E], db[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.f;
   const float inv = 1.f / (float)a.D;
-  for (long long first = (long long)blockIdx.x * kGroups; first < a.rows; first += (long long)gridDim.x * kGroups) {
-    const long long row = first + grp;
+  const long long step = (long long)gridDim.x * kGroups;
+  typename R::Piece nx[R::NP], ng[R::NP];
+  float nm = 0.f, nr = 0.f;
+  const auto fetch = [&](long long row) {
     const bool live = row < a.rows;
+    R::fetch(x + (live ? row : 0) * a.xs, live ? a.D : 0, t, nx);
+    R::fetch(dy + (live ? row : 0) * (long long)a.D, live ? a.D : 0, t, ng);
+    nm = live ? mean[row] : 0.f;
+    nr = live ? rstd[row] : 0.f;
+  };
+  long long row = (long long)blockIdx.x * kGroups + grp;
+  fetch(row);
+  for (long long first = (long long)blockIdx.x * kGroups; first < a.rows; first += step, row += step) {
     float h[E], g[E];
-    R::load(x + (live ? row : 0) * a.xs, live ? a.D : 0, t, h, 0.f);
-    R::load(dy + (live ? row : 0) * (long long)a.D, live ? a.D : 0, t, g, 0.f);
-    const float m = live ? mean[row] : 0.f, r = live ? rstd[row] : 0.f;
+    R::unpack(nx, h);
+    R::unpack(ng, g);
+    const float m = nm, r = nr;
+    fetch(row + step);
     float s[2] = {0.f, 0.f};
+    float wt[E];
+    R::weights(w, a.wbf16, a.D, t, wt, 1.f);
+    // (past the row's end the upstream gradient is zero: nothing is added there, and nothing stored)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      h[e] = R::in(e, a.D, t) ? (h[e] - m) * r : 0.f;
+      h[e] = (h[e] - m) * r;
       db[e] += g[e];
       dw[e] = fmaf(g[e], h[e], dw[e]);
       g[e] *= wt[e];
@@ -231,9 +285,10 @@ __global__ void __launch_bounds__(block_threads<TPR>(), backward_blocks_per_sm<T
     }
     row_sum<TPR, 2>(s, red[grp], t);
     const float s0 = s[0] * inv, s1 = s[1] * inv;
+    const float a0 = -r * s0, a1 = -r * s1;
 #pragma unroll
-    for (int e = 0; e < E; ++e) g[e] = r * (g[e] - s0 - h[e] * s1);
-    if (live) R::store(dx + (size_t)row * a.D, a.D, t, g);
+    for (int e = 0; e < E; ++e) g[e] = fmaf(r, g[e], fmaf(a1, h[e], a0));
+    if (row < a.rows) R::store(dx + (size_t)row * a.D, a.D, t, g);
   }
   if (!part) return;
   // this block's sums: its groups in order
@@ -326,7 +381,9 @@ template <typename T, int TPR, int E, bool kVec>
 void launch(const Call& c, cudaStream_t st) {
   constexpr int kT = block_threads<TPR>(), kGroups = kT / TPR;
   if (!c.backward) {
-    const unsigned grid = (unsigned)((c.a.rows + kGroups - 1) / kGroups);
+    constexpr long long kMost = 152 * blocks_per_sm<TPR, E, false>();  // as many as this GPU's 152 SMs hold at once
+    const long long want = (c.a.rows + kGroups - 1) / kGroups;
+    const unsigned grid = (unsigned)(want < kMost ? want : kMost);
     SSD_LAUNCH("k_norm_forward", st,
                k_norm_forward<T, TPR, E, kVec><<<grid, kT, 0, st>>>(c.a, (const T*)c.x, c.w, c.b, (T*)c.y, c.mean, c.rstd));
     return;
