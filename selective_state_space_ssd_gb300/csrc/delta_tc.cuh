@@ -10,7 +10,7 @@ namespace delta {
 
 using namespace ssd::tc;
 
-constexpr int kLoadWarps = 3, kLoadThreads = 32 * kLoadWarps;
+constexpr int kLoadWarps = 2, kLoadThreads = 32 * kLoadWarps;
 
 // D[tmem] (+)= A[tmem] B[smem]^T
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -89,6 +89,13 @@ __device__ __forceinline__ void lds8(const float* p, float (&x)[8]) {
     const float4 v = *reinterpret_cast<const float4*>(p + i);
     x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
   }
+}
+
+// A value that the compiler takes for a new one: what is computed from it stays where it is used, and is not kept in
+// registers around a loop that has none to spare.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
 }
 
 __device__ __forceinline__ uint32_t v_off(int t, int v) {  // element (t, v) of the V tile

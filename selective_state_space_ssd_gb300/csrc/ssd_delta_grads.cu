@@ -15,8 +15,8 @@
 // where it leaves tensor memory.  What a head reads (144 KB for K = V = 128) comes by TMA and bulk copies while the head
 // before is in its second half; that traffic is what bounds the kernel.
 //
-// Twenty-four warps: 0-15 the elementwise work, four a lane quadrant (quarters of the columns); 16 the MMAs; 17-19 copies;
-// 20-23 the two sums that need no product (dY . V by rows, <dS', S>).
+// Twenty-three warps: 0-15 the elementwise work, four a lane quadrant (quarters of the columns); 16 the MMAs; 17-18 copies;
+// 19-22 the two sums that need no product (dY . V by rows, <dS', S>).
 #include "delta_tc.cuh"
 
 namespace ssd {
@@ -24,7 +24,7 @@ namespace delta {
 namespace {
 
 constexpr int kWorkWarps = 16, kSumWarps = 4, kMmaWarp = kWorkWarps, kLoadWarp0 = kMmaWarp + 1,
-              kSumWarp0 = kLoadWarp0 + kLoadWarps;
+              kSumWarp0 = kLoadWarp0 + kLoadWarps;  // (the sums read no tensor memory: any warps will do)
 constexpr int kThreads = 32 * (kSumWarp0 + kSumWarps);
 constexpr int kWorkBar = 1;
 

@@ -9,12 +9,16 @@
 //
 // Twenty-four warps:
 //   0-15   the chain: four warps a lane quadrant, each with a quarter of the columns; S stays in their registers (fp32)
-//   16-19  beside the chain: o and the stash forward; dS', dY, dV and the scaled dO^T operand in reverse
+//   16-19  beside the chain: o forward; dV and the scaled dO^T operand in reverse
 //   20     issues every MMA
-//   21-23  copy the next chunk's tiles (two stages; TMA where rows are whole 16-byte pieces)
+//   21-22  copy the next chunk's tiles (two stages; TMA where rows are whole 16-byte pieces)
+//   23     sends off what is kept: the chain's warps leave S and R (dS' and dY) as tiles of shared memory while they wait
+//          for MMAs, one bulk copy each
 // Between two chunks lie three round trips through tensor memory (X, R, S'), which is what bounds the kernel: about
 // 105 cycles of latency for each group of MMAs, 32 cycles for each 128 x 64 x 16 one (A in TMEM; 57 with A in shared
-// memory), and the elementwise work of 128 x 64 and 128 x K values between them.
+// memory), and the elementwise work of 128 x 64 and 128 x K values between them.  So the chain goes in two halves, warps
+// 0-7 with the steps 0-31 and the first half of the keys and warps 8-15 with the others: while one half is at its
+// elementwise work the MMAs run that need only the other's (X's first keys, R's first steps, the state's first half).
 #include "delta_tc.cuh"
 
 namespace ssd {
@@ -23,14 +27,15 @@ namespace {
 
 constexpr int kChainWarps = 16, kSideWarps = 4;
 constexpr int kMmaWarp = kChainWarps + kSideWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1 + kLoadWarps);
+constexpr int kLoadWarp0 = kMmaWarp + 1, kSendWarp = kLoadWarp0 + kLoadWarps;
+constexpr int kThreads = 32 * (kSendWarp + 1);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSideBar = 1;  // named barrier of the side warps
-constexpr uint32_t kOut = 32768;
+constexpr uint32_t kKeep = 32768, kOut = 16384;
 
-// A stage: [K; Q] rows as one 128-row K-major tile, V (or dO) [64][128], the chunk's record.  Beside the two stages: 32 KB
-// through which results leave: the kept state (all of it), then R or dY (first half) and o or dV (second half), the kept
-// ones as the images that the gradient kernel reads, with one bulk copy each.
+// A stage: [K; Q] rows as one 128-row K-major tile, V (or dO) [64][128], the chunk's record.  Beside the two stages the
+// tiles through which results leave: the kept state, and after it in the same place R or dY, as the images that the
+// gradient kernel reads; o or dV.
 template <int KP>
 struct Tiles {
   static constexpr uint32_t kKQ = 128 * KP * 2, kV = kC * 128 * 2;
@@ -39,11 +44,12 @@ struct Tiles {
 };
 template <int KP>
 constexpr uint32_t scan_smem() {
-  return 2 * Tiles<KP>::kBytes + kOut + 1024;  // 1024: the tiles' alignment
+  return 2 * Tiles<KP>::kBytes + kKeep + kOut + 1024;  // 1024: the tiles' alignment
 }
 
 struct Bars {
-  uint64_t full[2], empty[2], tail, s, x, y, r, rp, ro, d, o, e1, e2, f, done;
+  uint64_t full[2], empty[2], tail, s[2], x[2], y[2], r[2], rp[2], ro, d[2], q, o, e2, f, kept, sent, dv, dv_sent,
+      done;  // [2]: stages, halves
 };
 struct Maps {
   CUtensorMap k, q, v;  // v: V forward, dO in reverse
@@ -125,8 +131,7 @@ __device__ __forceinline__ void write_state(float* s, const float (&S)[NK], int 
     if (k0 + i < K && v < V) s[(size_t)(k0 + i) * V + v] = S[i];
 }
 
-// Columns of tensor memory.  fp32 results: X (then Y high, low in place; reverse: then dY), QS (forward: (Q S)^T; reverse:
-// U), R (then R' high, low in place), O2 (forward: (P R)^T) or F (reverse: the scaled dO^T, high and low), D (the state's
+// Columns of tensor memory.  fp32 results: X (then Y high, low in place), QS (forward: (Q S)^T; reverse: U), R (then R' high, low in place), O2 (forward: (P R)^T) or F (reverse: the scaled dO^T, high and low), D (the state's
 // update); the state's operand, high and low, and R's for o and the stash (over the low part of a full-width state,
 // which has been read by then).
 template <int KP>
@@ -187,17 +192,23 @@ __device__ __forceinline__ void init_bars(Bars* b) {
     mbar_init(&b->empty[i], 1 + kChainWarps + kSideWarps);
   }
   mbar_init(&b->tail, 1);
-  mbar_init(&b->s, kChainWarps);
-  mbar_init(&b->x, 1);
-  mbar_init(&b->y, kChainWarps);
-  mbar_init(&b->r, 1);
-  mbar_init(&b->rp, kChainWarps);
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&b->s[i], kChainWarps / 2);
+    mbar_init(&b->x[i], 1);
+    mbar_init(&b->y[i], kChainWarps / 2);
+    mbar_init(&b->r[i], 1);
+    mbar_init(&b->rp[i], kChainWarps / 2);
+    mbar_init(&b->d[i], 1);
+  }
   mbar_init(&b->ro, kChainWarps);
-  mbar_init(&b->d, 1);
+  mbar_init(&b->q, 1);
   mbar_init(&b->o, 1);
-  mbar_init(&b->e1, kSideWarps);
   mbar_init(&b->e2, kSideWarps);
   mbar_init(&b->f, kSideWarps);
+  mbar_init(&b->kept, kChainWarps);
+  mbar_init(&b->sent, 1);
+  mbar_init(&b->dv, kChainWarps);
+  mbar_init(&b->dv_sent, kSideWarps);
   mbar_init(&b->done, 1);
   mbar_init_fence();
 }
@@ -214,6 +225,22 @@ __device__ __forceinline__ void put_state(uint32_t tm, int lane0, int wg, const 
     st8u(taddr(tm, lane0, Cols<KP>::Sl + wg * (KP / 8) + 8 * b), l);
   }
 }
+// The high parts as their pieces of row v of the state's image.
+template <int KP>
+__device__ __forceinline__ void keep_state(uint8_t* tile, int VP, int v, int k0, const float (&S)[KP / 4]) {
+  if (v < VP)
+#pragma unroll
+    for (int j = 0; j < KP / 32; ++j)
+      *reinterpret_cast<uint4*>(tile + (k0 >> 6) * VP * 128 + sw128_chunk(v, ((k0 & 63) >> 3) + j)) =
+          make_uint4(pack(S[8 * j], S[8 * j + 1]), pack(S[8 * j + 2], S[8 * j + 3]), pack(S[8 * j + 4], S[8 * j + 5]),
+                     pack(S[8 * j + 6], S[8 * j + 7]));
+}
+// The warp's part of a tile that is sent off has been written.
+__device__ __forceinline__ void signal_tile(uint64_t* bar, int lane) {
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
 // S = keep S + D
 template <int KP>
 __device__ __forceinline__ void update_state(uint32_t tm, int lane0, int k0, float keep, float (&S)[KP / 4]) {
@@ -227,36 +254,22 @@ __device__ __forceinline__ void update_state(uint32_t tm, int lane0, int k0, flo
   tc_fence_before();
 }
 
-// The state's operand (its bf16 high part) of lane v as row v of the state's image.
-template <int KP>
-__device__ __forceinline__ void stage_state(uint32_t tm, int lane0, uint8_t* out, int VP, int v) {
-#pragma unroll
-  for (int b = 0; b < KP / 32; ++b) {
-    uint32_t u[16];
-    tmem_ld16_nowait(taddr(tm, lane0, Cols<KP>::Sh + 16 * b), u);
-    tmem_wait_ld();
-    if (v < VP) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(out + (b >> 1) * VP * 128 + sw128_chunk(v, 4 * (b & 1) + j)) =
-            make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+// The sending warp: two tiles a chunk out of one place, each free again once its copy has read it.
+__device__ __forceinline__ void send_kept(Bars& bars, const uint8_t* tile, uint8_t* first, size_t step1, uint32_t bytes1,
+                                          uint8_t* second, size_t step2, uint32_t bytes2, long long stride, int n, int lane,
+                                          int* status) {
+  for (int i = 0; i < 2 * n; ++i) {
+    if (!wait_warp(&bars.kept, i & 1, status, 91)) break;
+    if (lane == 0) {
+      uint8_t* dst = i & 1 ? second + (long long)step2 * stride * (i >> 1) : first + (long long)step1 * stride * (i >> 1);
+      bulk_store(dst, tile, i & 1 ? bytes2 : bytes1);
+      tma_store_commit();
+      tma_store_wait_read0();
+      mbar_arrive(&bars.sent);
     }
+    __syncwarp();
   }
-}
-// The side warps have written a tile: one of them sends it off.  Every one of them calls this.
-__device__ __forceinline__ void send_tile(void* dst, const uint8_t* src, uint32_t bytes, int tid) {
-  fence_proxy_async();
-  named_bar(kSideBar, 32 * kSideWarps);
-  if (tid == 0) {
-    bulk_store(dst, src, bytes);
-    tma_store_commit();
-  }
-}
-// Tiles sent off have been read: they may be written again.  `fail`: a wait of this warp ran out; true where one of any
-// warp did, so that the side warps stop together.
-__device__ __forceinline__ bool tiles_free(int tid, bool fail) {
-  if (tid == 0) tma_store_wait_read0();
-  return named_bar_or(kSideBar, 32 * kSideWarps, fail);
+  if (lane == 0) tma_store_wait0();
 }
 
 // The [64][128] bf16 tile of the side warps to rows of a tensor, first step at dst.
@@ -307,9 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nc = run.c1 - run.c0, chunk0 = blk.sq.chunk + run.c0, step0 = blk.sq.start + run.c0 * kC,
             steps = blk.sq.len - run.c0 * kC;
   const bool stash = Sout != nullptr;
+  uint8_t* keep_tile = smem + 2 * Tiles<KP>::kBytes;
 
   if (w < kChainWarps) {
-    const int wg = w >> 2, lane0 = 32 * (w & 3), v = lane0 + lane, k0 = wg * (KP / 4);
+    const int wg = w >> 2, half = wg >> 1, lane0 = 32 * (w & 3), v = lane0 + lane, k0 = wg * (KP / 4);
     float S[KP / 4];
     read_state(S, run.from, d.K, d.V, k0, v);
     if (run.map)
@@ -319,20 +333,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ph = c & 1;
       const uint8_t* st = smem + (c & 1) * Tiles<KP>::kBytes;
       const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
-      if (c > 0) {  // the columns of the state's operand and of R's: read to the end by the chunk before?
-        if (stash && !wait_warp(&bars.e1, ph ^ 1, status, 11)) break;
-        if (o && !wait_warp(&bars.o, ph ^ 1, status, 12)) break;
+      if (c > 0 && o) {  // R of the chunk before, whose columns the low part takes, has been read
+        if (!wait_warp(&bars.o, ph ^ 1, status, 12)) break;
         tc_fence_after();
       }
       put_state<KP>(tm, lane0, wg, S);
-      signal_tmem(&bars.s, lane);
+      signal_tmem(&bars.s[half], lane);
+      if (stash) {
+        if (c > 0 && !wait_warp(&bars.sent, 1, status, 11)) break;
+        keep_state<KP>(keep_tile, d.VP, fresh(v), k0, S);
+        signal_tile(&bars.kept, lane);
+      }
       if (!wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 13)) break;
-      if (!wait_warp(&bars.x, ph, status, 14)) break;
+      if (!wait_warp(&bars.x[half], ph, status, 14)) break;
       tc_fence_after();
       float x[16];
       ld16(taddr(tm, lane0, C::X + 16 * wg), x);
       {
-        const uint8_t* vt = st + Tiles<KP>::kKQ;
+        const uint8_t* vt = st + Tiles<KP>::kKQ + 16 * wg * 128;
+        const int vf = fresh(v);
 #pragma unroll
         for (int b = 0; b < 16; b += 8) {  // Y = beta (V - e^G X)
           float e[8], be[8];
@@ -341,12 +360,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             x[b + i] = be[i] * fmaf(-e[i], x[b + i],
-                                    __bfloat162float(*reinterpret_cast<const bf16*>(vt + v_off(16 * wg + b + i, v))));
+                                    __bfloat162float(*reinterpret_cast<const bf16*>(vt + v_off(b + i, vf))));
         }
       }
       put_split(taddr(tm, lane0, C::X + 16 * wg), x);
-      signal_tmem(&bars.y, lane);
-      if (!wait_warp(&bars.r, ph, status, 15)) break;
+      signal_tmem(&bars.y[half], lane);
+      if (!wait_warp(&bars.r[half], ph, status, 15)) break;
       tc_fence_after();
       ld16(taddr(tm, lane0, C::R + 16 * wg), x);
       float a[16];
@@ -354,15 +373,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i) a[i] *= x[i];  // R' = e^{G_end - G} R
       put_split(taddr(tm, lane0, C::R + 16 * wg), a);
-      signal_tmem(&bars.rp, lane);
+      signal_tmem(&bars.rp[half], lane);
       const float keep = gates[kC - 1];
-      if (o || stash) {
+      if (o) {
+        if (!wait_warp(&bars.q, ph, status, 17)) break;  // the state's low part, whose columns these are, has been read
+        tc_fence_after();
         put_split(taddr(tm, lane0, C::Ro + 16 * wg), x);  // R itself
         signal_tmem(&bars.ro, lane);
       }
+      if (stash) {
+        if (!wait_warp(&bars.sent, 0, status, 18)) break;
+        const int vf = fresh(v);
+        if (vf < d.VP) {
+          *reinterpret_cast<uint4*>(keep_tile + sw128_chunk(vf, 2 * wg)) =
+              make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
+          *reinterpret_cast<uint4*>(keep_tile + sw128_chunk(vf, 2 * wg + 1)) =
+              make_uint4(pack(x[8], x[9]), pack(x[10], x[11]), pack(x[12], x[13]), pack(x[14], x[15]));
+        }
+        signal_tile(&bars.kept, lane);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
-      if (!wait_warp(&bars.d, ph, status, 16)) break;
+      if (!wait_warp(&bars.d[half], ph, status, 16)) break;
       tc_fence_after();
       update_state<KP>(tm, lane0, k0, keep, S);
     }
@@ -370,36 +402,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (w < kMmaWarp) {
     const int lane0 = 32 * (w & 3), v = lane0 + lane, tid = threadIdx.x - 32 * kChainWarps;
     const long long os = (long long)d.HV * d.V;
-    uint8_t* out = smem + 2 * Tiles<KP>::kBytes;
-    bf16* tile = reinterpret_cast<bf16*>(out + kOut / 2);
+    bf16* tile = reinterpret_cast<bf16*>(keep_tile + kKeep);
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
       const float* gates =
           reinterpret_cast<const float*>(smem + (c & 1) * Tiles<KP>::kBytes + Tiles<KP>::kRec + kRecordGates);
-      const size_t item = (size_t)(chunk0 + c) * d.HV + blk.hv;
-      if (stash) {  // the state entering the chunk, and R, both as the bf16 operands hold them
-        if (tiles_free(tid, !wait_warp(&bars.s, ph, status, 21))) break;
-        tc_fence_after();
-        stage_state<KP>(tm, lane0, out, d.VP, v);
-        send_tile(Sout + item * d.VP * KP, out, (uint32_t)(d.VP * KP * 2), tid);
-        if (tiles_free(tid, !wait_warp(&bars.ro, ph, status, 22))) break;
-        tc_fence_after();
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t u[8];
-          tmem_ld8_nowait(taddr(tm, lane0, C::Ro + 16 * b), u);
-          tmem_wait_ld();
-          if (b == 3) signal_read(&bars.e1, lane);
-          if (v < d.VP) {
-            *reinterpret_cast<uint4*>(out + sw128_chunk(v, 2 * b)) = make_uint4(u[0], u[1], u[2], u[3]);
-            *reinterpret_cast<uint4*>(out + sw128_chunk(v, 2 * b + 1)) = make_uint4(u[4], u[5], u[6], u[7]);
-          }
-        }
-        send_tile(Rout + item * d.VP * kC, out, (uint32_t)(d.VP * kC * 2), tid);
-      }
+      bool ok = wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 23);
       if (o) {
-        const bool ok = wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 23) && wait_warp(&bars.o, ph, status, 24);
-        // the tile's last rows have been stored
+        ok = ok && wait_warp(&bars.o, ph, status, 24);
+        // the tile's last rows have been stored; all side warps go on together or not at all
         if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;
         tc_fence_after();
 #pragma unroll
@@ -413,37 +424,52 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (b == 7) signal_read(&bars.e2, lane);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            tile[(8 * b + i) * 128 + v] =
-                __float2bfloat16_rn(fmaf(e[i], __uint_as_float(q[i]), __uint_as_float(r[i])));
+            tile[(8 * b + i) * 128 + v] = __float2bfloat16_rn(fmaf(e[i], __uint_as_float(q[i]), __uint_as_float(r[i])));
         }
+        if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
         named_bar(kSideBar, 32 * kSideWarps);
-        store_tile(reinterpret_cast<const uint8_t*>(tile), o + ((long long)(step0 + c * kC) * d.HV + blk.hv) * d.V,
-                   os, min(kC, steps - c * kC), d.V, d.ovec, tid);
-        if (stash) named_bar(kSideBar, 32 * kSideWarps);  // the next state's image covers this tile
+        store_tile(reinterpret_cast<const uint8_t*>(tile), o + ((long long)(step0 + c * kC) * d.HV + blk.hv) * d.V, os,
+                   min(kC, steps - c * kC), d.V, d.ovec, tid);
+      } else {
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&bars.empty[c & 1]);  // (after a wait for the stage, so that no warp is a phase ahead)
       }
-      // (a wait, so that no warp is a phase ahead)
-      if (!o && !stash && !wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 25)) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
     }
-    if (tid == 0) tma_store_wait0();
   } else if (w == kMmaWarp) {
-    constexpr uint32_t n64 = idesc_bf16(128, 64, false, false), nk = idesc_bf16(128, KP, false, true);
+    constexpr uint32_t n64 = idesc_bf16(128, 64, false, false), n32 = idesc_bf16(128, 32, false, false),
+                       nk = idesc_bf16(128, KP, false, true), n64k = idesc_bf16(128, 64, false, true);
+    constexpr int kH = KP / 32;  // 16-key blocks of a half of the state
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
       const uint8_t* st = smem + (c & 1) * Tiles<KP>::kBytes;
       const uint8_t* rc = st + Tiles<KP>::kRec;
-      const uint64_t kd = kdesc(st, 128, 0), qd = kdesc(st + kC * 128, 128, 0);
-      const uint64_t km = sdesc_sw128(smem_u32(st), 128 * 128, 1024);  // the same K rows as [step][key]
+      const uint64_t kd = kdesc(st, 128, 0), qd = kdesc(st + kC * 128, 128, 0), kd1 = kdesc(st + 32 * 128, 128, 0);
+      // the same K rows as [step][key], all keys and the second half of them
+      const uint64_t km = sdesc_sw128(smem_u32(st), 128 * 128, 1024);
+      const uint64_t km1 = sdesc_sw128(smem_u32(st) + 128 * 128, 128 * 128, 1024);
       if (!wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 31)) break;
-      if (!wait_warp(&bars.s, ph, status, 32)) break;
+      if (!wait_warp(&bars.s[0], ph, status, 32)) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::X, tm + C::Sh + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, kb > 0);
+        for (int kb = 0; kb < kH; ++kb) {
+          mma_ts(tm + C::X, tm + C::Sh + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, kb > 0);
+          mma_ts(tm + C::X, tm + C::Sl + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, true);
+        }
+      }
+      __syncwarp();
+      if (!wait_warp(&bars.s[1], ph, status, 38)) break;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-        for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::X, tm + C::Sl + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, true);
-        mma_commit(&bars.x);
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int kb = kH; kb < 2 * kH; ++kb) {
+            mma_ts(tm + C::X + 32 * h, tm + C::Sh + 8 * kb, (h ? kd1 : kd) + kdesc_step(128, 16 * kb), n32, true);
+            mma_ts(tm + C::X + 32 * h, tm + C::Sl + 8 * kb, (h ? kd1 : kd) + kdesc_step(128, 16 * kb), n32, true);
+          }
+          mma_commit(&bars.x[h]);
+        }
       }
       __syncwarp();
       if (o) {
@@ -452,35 +478,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
 #pragma unroll
           for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::QS, tm + C::Sh + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, kb > 0);
-#pragma unroll
-          for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::QS, tm + C::Sl + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, true);
         }
         __syncwarp();
       }
-      if (!wait_warp(&bars.y, ph, status, 34)) break;
-      tc_fence_after();
-      if (elect_one()) {  // R^T = Y^T T^T: the steps of 16-block kb reach the steps i >= 16 kb
+      // R^T = Y^T T^T: the steps of 16-block kb reach the steps i >= 16 kb
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-          const uint32_t id = idesc_bf16(128, kC - 16 * kb, false, false);
-          const uint32_t yh = tm + pair_col(C::X, kb, false), yl = tm + pair_col(C::X, kb, true);
-          const uint64_t th = kdesc(rc + 16 * kb * 128, kC, 16 * kb), tl = kdesc(rc + 8192 + 16 * kb * 128, kC, 16 * kb);
-          mma_ts(tm + C::R + 16 * kb, yh, th, id, kb > 0);
-          mma_ts(tm + C::R + 16 * kb, yl, th, id, true);
-          mma_ts(tm + C::R + 16 * kb, yh, tl, id, true);
+      for (int h = 0; h < 2; ++h) {
+        if (!wait_warp(&bars.y[h], ph, status, 34)) goto end;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kb = 2 * h; kb < 2 * h + 2; ++kb) {
+            const uint32_t id = idesc_bf16(128, kC - 16 * kb, false, false);
+            const uint32_t yh = tm + pair_col(C::X, kb, false), yl = tm + pair_col(C::X, kb, true);
+            const uint64_t th = kdesc(rc + 16 * kb * 128, kC, 16 * kb), tl = kdesc(rc + 8192 + 16 * kb * 128, kC, 16 * kb);
+            mma_ts(tm + C::R + 16 * kb, yh, th, id, kb > 0);
+            mma_ts(tm + C::R + 16 * kb, yl, th, id, true);
+            mma_ts(tm + C::R + 16 * kb, yh, tl, id, true);
+          }
+          mma_commit(&bars.r[h]);
+          if (h == 1 && o) {
+#pragma unroll
+            for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::QS, tm + C::Sl + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, true);
+            mma_commit(&bars.q);
+          }
         }
-        mma_commit(&bars.r);
+        __syncwarp();
       }
-      __syncwarp();
-      if (!wait_warp(&bars.rp, ph, status, 35)) break;
+      if (!wait_warp(&bars.rp[0], ph, status, 35)) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
+        for (int kb = 0; kb < 2; ++kb) {
           mma_ts(tm + C::D, tm + pair_col(C::R, kb, false), km + mdesc_step(16 * kb), nk, kb > 0);
           mma_ts(tm + C::D, tm + pair_col(C::R, kb, true), km + mdesc_step(16 * kb), nk, true);
         }
-        mma_commit(&bars.d);
+      }
+      __syncwarp();
+      if (!wait_warp(&bars.rp[1], ph, status, 39)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          // (64 keys are one atom of the tile, which is not cut: all of it before the first half's signal)
+          if (KP == 128 || h == 0)
+#pragma unroll
+            for (int kb = 2; kb < 4; ++kb) {
+              mma_ts(tm + C::D + 64 * h, tm + pair_col(C::R, kb, false), (h ? km1 : km) + mdesc_step(16 * kb), n64k, true);
+              mma_ts(tm + C::D + 64 * h, tm + pair_col(C::R, kb, true), (h ? km1 : km) + mdesc_step(16 * kb), n64k, true);
+            }
+          mma_commit(&bars.d[h]);
+        }
       }
       __syncwarp();
       if (o) {
@@ -503,11 +551,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) mma_commit(&bars.empty[c & 1]);
       __syncwarp();
     }
+  end:
     if (elect_one()) mma_commit(&bars.done);  // every MMA has finished before the tensor memory is given back
     __syncwarp();
     wait_warp(&bars.done, 0, status, 37);
+  } else if (w == kSendWarp) {
+    if (stash) {
+      const size_t item = (size_t)chunk0 * d.HV + blk.hv;
+      send_kept(bars, keep_tile, reinterpret_cast<uint8_t*>(Sout + item * d.VP * KP), (size_t)d.VP * KP * 2,
+                (uint32_t)(d.VP * KP * 2), reinterpret_cast<uint8_t*>(Rout + item * d.VP * kC), (size_t)d.VP * kC * 2,
+                (uint32_t)(d.VP * kC * 2), d.HV, nc, lane, status);
+    }
   } else {
-    const int tid = threadIdx.x - 32 * (kMmaWarp + 1);
+    const int tid = threadIdx.x - 32 * kLoadWarp0;
     Loader<KP> ld{d, in, maps, run.map ? nullptr : in.v, d.vs, d.vvec, o != nullptr, blk.hk, blk.hv, &bars.tail, 0};
     int loaded = -1;
     for (int c = 0; c < nc; ++c) {
@@ -559,10 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nc = run.c1 - run.c0, chunk0 = blk.sq.chunk + run.c0, step0 = blk.sq.start + run.c0 * kC,
             steps = blk.sq.len - run.c0 * kC;
   const long long os = (long long)d.HV * d.V;
+  uint8_t* keep_tile = smem + 2 * Tiles<KP>::kBytes;
+  const int dyw = (d.VP + 63) / 64 * 64;  // columns of dY's image
 
   // i counts the chunks in the order they are walked; chunk nc - 1 - i
   if (w < kChainWarps) {
-    const int wg = w >> 2, lane0 = 32 * (w & 3), v = lane0 + lane, k0 = wg * (KP / 4);
+    const int wg = w >> 2, half = wg >> 1, lane0 = 32 * (w & 3), v = lane0 + lane, k0 = wg * (KP / 4);
     float S[KP / 4];
     read_state(S, run.from, d.K, d.V, k0, v);
     if (run.map)
@@ -572,14 +630,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ph = i & 1;
       const uint8_t* st = smem + (i & 1) * Tiles<KP>::kBytes;
       const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
-      if (i > 0 && !first_pass) {
-        if (!wait_warp(&bars.e1, ph ^ 1, status, 51)) break;
-        tc_fence_after();
-      }
       put_state<KP>(tm, lane0, wg, S);
-      signal_tmem(&bars.s, lane);
+      signal_tmem(&bars.s[half], lane);
+      if (!first_pass) {
+        if (i > 0 && !wait_warp(&bars.sent, 1, status, 51)) break;
+        keep_state<KP>(keep_tile, d.VP, fresh(v), k0, S);
+        signal_tile(&bars.kept, lane);
+      }
       if (!wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 52)) break;
-      if (!wait_warp(&bars.x, ph, status, 53)) break;
+      if (!wait_warp(&bars.x[half], ph, status, 53)) break;
       tc_fence_after();
       float x[16];
 #pragma unroll
@@ -594,8 +653,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 8; ++j) x[b + j] = fmaf(e[j], __uint_as_float(p[j]), __uint_as_float(q[j]));
       }
       put_split(taddr(tm, lane0, C::X + 16 * wg), x);
-      signal_tmem(&bars.y, lane);
-      if (!wait_warp(&bars.r, ph, status, 54)) break;
+      signal_tmem(&bars.y[half], lane);
+      if (!wait_warp(&bars.r[half], ph, status, 54)) break;
       tc_fence_after();
       ld16(taddr(tm, lane0, C::R + 16 * wg), x);  // dY
       {
@@ -610,36 +669,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         put_split(taddr(tm, lane0, C::R + 16 * wg), a);
       }
-      signal_tmem(&bars.rp, lane);
+      signal_tmem(&bars.rp[half], lane);
       const float keep = gates[kC - 1];
-      if (!first_pass) {  // dY for the side warps, over X
-        uint32_t u[16];
+      if (!first_pass) {  // dY and dV = beta dY on their way out
+        if (!wait_warp(&bars.sent, 0, status, 56)) break;
+        if (i > 0 && !wait_warp(&bars.dv_sent, ph ^ 1, status, 57)) break;
+        const int vf = fresh(v);
+        uint8_t* yt = keep_tile + 16 * wg * 128;
+        bf16* tile = reinterpret_cast<bf16*>(keep_tile + kKeep) + 16 * wg * 128 + vf;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(x[j]);
-        st16u(taddr(tm, lane0, C::X + 16 * wg), u);
-        signal_tmem(&bars.ro, lane);
+        for (int b = 0; b < 16; b += 8) {
+          float be[8];
+          lds8(gates + 2 * kC + 16 * wg + b, be);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (vf < dyw) *reinterpret_cast<bf16*>(yt + v_off(b + j, vf)) = __float2bfloat16_rn(x[b + j]);
+            tile[(b + j) * 128] = __float2bfloat16_rn(be[j] * x[b + j]);
+          }
+        }
+        signal_tile(&bars.kept, lane);
+        if (lane == 0) mbar_arrive(&bars.dv);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
-      if (!wait_warp(&bars.d, ph, status, 55)) break;
+      if (!wait_warp(&bars.d[half], ph, status, 55)) break;
       tc_fence_after();
       update_state<KP>(tm, lane0, k0, keep, S);
     }
     if (run.to) write_state(run.to, S, run.rows, run.columns, k0, v);
   } else if (w < kMmaWarp) {
     const int lane0 = 32 * (w & 3), v = lane0 + lane, tid = threadIdx.x - 32 * kChainWarps;
-    uint8_t* out = smem + 2 * Tiles<KP>::kBytes;
-    bf16* tile = reinterpret_cast<bf16*>(out + kOut / 2);
-    const int va = (d.VP + 63) / 64;  // 64-column atoms of dY's image
     for (int i = 0; i < nc; ++i) {
       const uint32_t ph = i & 1;
       const int c = nc - 1 - i;
       const uint8_t* st = smem + (i & 1) * Tiles<KP>::kBytes;
       const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
-      const size_t item = (size_t)(chunk0 + c) * d.HV + blk.hv;
-      bool ok = wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 61);
-      ok = ok && (i == 0 || wait_warp(&bars.d, ph ^ 1, status, 62));  // F of the chunk before has been read
-      if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;  // (and the tile's last rows have been stored)
+      if (!wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 61)) break;
+      if (i > 0 && !wait_warp(&bars.d[0], ph ^ 1, status, 62)) break;  // F of the chunk before has been read
       tc_fence_after();
 #pragma unroll
       for (int b = 0; b < 8; ++b) {  // F = scale e^G dO^T
@@ -655,45 +721,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         st4u(taddr(tm, lane0, F + 16 * (b >> 1) + 4 * (b & 1) + 8), l);
       }
       signal_tmem(&bars.f, lane);
-      if (first_pass) {
-        if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
-        continue;
-      }
-      if (tiles_free(tid, !wait_warp(&bars.s, ph, status, 63))) break;
-      tc_fence_after();
-      stage_state<KP>(tm, lane0, out, d.VP, v);
-      signal_read(&bars.e1, lane);
-      send_tile(dSout + item * d.VP * KP, out, (uint32_t)(d.VP * KP * 2), tid);
-      if (tiles_free(tid, !wait_warp(&bars.ro, ph, status, 64))) break;
-      tc_fence_after();
-#pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        uint32_t x[8];
-        float be[8];
-        tmem_ld8_nowait(taddr(tm, lane0, C::X + 8 * b), x);
-        lds8(gates + 2 * kC + 8 * b, be);
-        tmem_wait_ld();
-        if (b == 7) signal_read(&bars.e2, lane);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          *reinterpret_cast<bf16*>(out + v_off(8 * b + j, v)) = __float2bfloat16_rn(__uint_as_float(x[j]));
-          tile[(8 * b + j) * 128 + v] = __float2bfloat16_rn(be[j] * __uint_as_float(x[j]));
-        }
-      }
-      send_tile(dYout + item * va * 64 * kC, out, (uint32_t)(va * 64 * kC * 2), tid);
       if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
-      store_tile(reinterpret_cast<const uint8_t*>(tile), dv + ((long long)(step0 + c * kC) * d.HV + blk.hv) * d.V,
-                 os, min(kC, steps - c * kC), d.V, d.ovec, tid);
+      if (first_pass) continue;
+      if (!wait_warp(&bars.dv, ph, status, 64)) break;
+      store_tile(keep_tile + kKeep, dv + ((long long)(step0 + c * kC) * d.HV + blk.hv) * d.V, os,
+                 min(kC, steps - c * kC), d.V, d.ovec, tid);
+      signal_read(&bars.dv_sent, lane);
     }
-    if (tid == 0) tma_store_wait0();
   } else if (w == kMmaWarp) {
-    constexpr uint32_t n64 = idesc_bf16(128, 64, false, false), nk = idesc_bf16(128, KP, false, true);
+    constexpr uint32_t n64 = idesc_bf16(128, 64, false, false), n32 = idesc_bf16(128, 32, false, false),
+                       nk = idesc_bf16(128, KP, false, true), n64k = idesc_bf16(128, 64, false, true);
+    constexpr int kH = KP / 32;
     for (int i = 0; i < nc; ++i) {
       const uint32_t ph = i & 1;
       const uint8_t* st = smem + (i & 1) * Tiles<KP>::kBytes;
       const uint8_t* rc = st + Tiles<KP>::kRec;
-      const uint64_t kd = kdesc(st, 128, 0);
-      const uint64_t km = sdesc_sw128(smem_u32(st), 128 * 128, 1024), qm = sdesc_sw128(smem_u32(st) + kC * 128, 128 * 128, 1024);
+      const uint64_t kd = kdesc(st, 128, 0), kd1 = kdesc(st + 32 * 128, 128, 0);
+      const uint64_t km = sdesc_sw128(smem_u32(st), 128 * 128, 1024), qm = sdesc_sw128(smem_u32(st) + kC * 128, 128 * 128, 1024),
+                     km1 = sdesc_sw128(smem_u32(st) + 128 * 128, 128 * 128, 1024);
       const uint64_t od = sdesc_sw128(smem_u32(st) + Tiles<KP>::kKQ, kC * 128, 1024);  // dO^T: [step][v]
       if (!wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 71)) break;
       tc_fence_after();
@@ -706,17 +751,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (i > 0 && !first_pass && !wait_warp(&bars.e2, ph ^ 1, status, 77)) break;  // the side warps have dY of the chunk before
-      if (!wait_warp(&bars.s, ph, status, 72)) break;
+      // the second half leads: dY goes from the last step back
+      if (!wait_warp(&bars.s[1], ph, status, 72)) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::X, tm + C::Sh + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, kb > 0);
-#pragma unroll
-        for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::X, tm + C::Sl + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, true);
-        mma_commit(&bars.x);
+        for (int kb = kH; kb < 2 * kH; ++kb) {
+          mma_ts(tm + C::X, tm + C::Sh + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, kb > kH);
+          mma_ts(tm + C::X, tm + C::Sl + 8 * kb, kd + kdesc_step(128, 16 * kb), n64, true);
+        }
       }
       __syncwarp();
+      if (!wait_warp(&bars.s[0], ph, status, 78)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+#pragma unroll
+          for (int kb = 0; kb < kH; ++kb) {
+            mma_ts(tm + C::X + 32 * h, tm + C::Sh + 8 * kb, (h ? kd1 : kd) + kdesc_step(128, 16 * kb), n32, true);
+            mma_ts(tm + C::X + 32 * h, tm + C::Sl + 8 * kb, (h ? kd1 : kd) + kdesc_step(128, 16 * kb), n32, true);
+          }
+          mma_commit(&bars.x[h]);
+        }
+      }
+      __syncwarp();
+      // dY^T = dR^T T: the steps of 16-block kb reach the steps t <= 16 kb + 15
+#pragma unroll
+      for (int h = 1; h >= 0; --h) {
+        if (!wait_warp(&bars.y[h], ph, status, 74)) goto end;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kb = 2 * h + 1; kb >= 2 * h; --kb) {
+            const uint32_t id = idesc_bf16(128, 16 * (kb + 1), false, true);
+            const uint32_t yh = tm + pair_col(C::X, kb, false), yl = tm + pair_col(C::X, kb, true);
+            const uint64_t th = mdesc(rc, kC, 16 * kb), tl = mdesc(rc + 8192, kC, 16 * kb);
+            mma_ts(tm + C::R, yh, th, id, kb < 3);
+            mma_ts(tm + C::R, yl, th, id, true);
+            mma_ts(tm + C::R, yh, tl, id, true);
+          }
+          mma_commit(&bars.r[h]);
+        }
+        __syncwarp();
+      }
       if (!wait_warp(&bars.f, ph, status, 73)) break;
       tc_fence_after();
       if (elect_one()) {
@@ -727,39 +805,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (!wait_warp(&bars.y, ph, status, 74)) break;
-      tc_fence_after();
-      if (elect_one()) {  // dY^T = dR^T T
-#pragma unroll
-        for (int kb = 3; kb >= 0; --kb) {
-          const uint32_t id = idesc_bf16(128, 16 * (kb + 1), false, true);
-          const uint32_t yh = tm + pair_col(C::X, kb, false), yl = tm + pair_col(C::X, kb, true);
-          const uint64_t th = mdesc(rc, kC, 16 * kb), tl = mdesc(rc + 8192, kC, 16 * kb);
-          mma_ts(tm + C::R, yh, th, id, kb < 3);
-          mma_ts(tm + C::R, yl, th, id, true);
-          mma_ts(tm + C::R, yh, tl, id, true);
-        }
-        mma_commit(&bars.r);
-      }
-      __syncwarp();
-      if (!wait_warp(&bars.rp, ph, status, 75)) break;
+      if (!wait_warp(&bars.rp[1], ph, status, 75)) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
+        for (int kb = 2; kb < 4; ++kb) {
           mma_ts(tm + C::D, tm + pair_col(C::R, kb, false), km + mdesc_step(16 * kb), nk, true);
           mma_ts(tm + C::D, tm + pair_col(C::R, kb, true), km + mdesc_step(16 * kb), nk, true);
         }
-        mma_commit(&bars.d);
+      }
+      __syncwarp();
+      if (!wait_warp(&bars.rp[0], ph, status, 79)) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {
+          // (64 keys are one atom of the tile, which is not cut: all of it before the first half's signal)
+          if (KP == 128 || h == 1) {
+            const int at = KP == 128 ? h : 0;
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+              mma_ts(tm + C::D + 64 * at, tm + pair_col(C::R, kb, false), (at ? km1 : km) + mdesc_step(16 * kb), n64k, true);
+              mma_ts(tm + C::D + 64 * at, tm + pair_col(C::R, kb, true), (at ? km1 : km) + mdesc_step(16 * kb), n64k, true);
+            }
+          }
+          mma_commit(&bars.d[h]);
+        }
         mma_commit(&bars.empty[i & 1]);
       }
       __syncwarp();
     }
+  end:
     if (elect_one()) mma_commit(&bars.done);
     __syncwarp();
     wait_warp(&bars.done, 0, status, 76);
+  } else if (w == kSendWarp) {
+    if (!first_pass && nc > 0) {
+      const size_t item = (size_t)(chunk0 + nc - 1) * d.HV + blk.hv;
+      send_kept(bars, keep_tile, reinterpret_cast<uint8_t*>(dSout + item * d.VP * KP), (size_t)d.VP * KP * 2,
+                (uint32_t)(d.VP * KP * 2), reinterpret_cast<uint8_t*>(dYout + item * dyw * kC), (size_t)dyw * kC * 2,
+                (uint32_t)(dyw * kC * 2), -(long long)d.HV, nc, lane, status);
+    }
   } else {
-    const int tid = threadIdx.x - 32 * (kMmaWarp + 1);
+    const int tid = threadIdx.x - 32 * kLoadWarp0;
     Loader<KP> ld{d, in, maps, run.map ? nullptr : dout, os, d.ovec, true, blk.hk, blk.hv, &bars.tail, 0};
     int loaded = -1;
     for (int i = 0; i < nc; ++i) {
