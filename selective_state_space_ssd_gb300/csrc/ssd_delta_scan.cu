@@ -48,7 +48,7 @@ constexpr uint32_t scan_smem() {
 }
 
 struct Bars {
-  uint64_t full[2], empty[2], tail, s[2], x[2], y[2], r[2], rp[2], ro, d[2], q, o, e2, f, kept, sent, dv, dv_sent,
+  uint64_t full[2], empty[2], tail, s[2], x[2], y[2], r[2], rp[2], ro, d[2], o, e2, f, kept, sent, dv, dv_sent,
       done;  // [2]: stages, halves
 };
 struct Maps {
@@ -132,11 +132,10 @@ __device__ __forceinline__ void write_state(float* s, const float (&S)[NK], int 
 }
 
 // Columns of tensor memory.  fp32 results: X (then Y high, low in place), QS (forward: (Q S)^T; reverse: U), R (then R' high, low in place), O2 (forward: (P R)^T) or F (reverse: the scaled dO^T, high and low), D (the state's
-// update); the state's operand, high and low, and R's for o and the stash (over the low part of a full-width state,
-// which has been read by then).
+// update); the state's operand, high and low.  R's operand for o lies over X.
 template <int KP>
 struct Cols {
-  static constexpr int X = 0, QS = 64, R = 128, O2 = 192, D = 256, Sh = 384, Sl = Sh + KP / 2, Ro = 448;
+  static constexpr int X = 0, QS = 64, R = 128, O2 = 192, D = 256, Sh = 384, Sl = Sh + KP / 2, Ro = X;
 };
 // Operand columns of the 16-value block kb: 8 high, 8 low, where its 16 fp32 values were.
 __device__ __forceinline__ constexpr int pair_col(int base, int kb, bool low) { return base + 16 * kb + (low ? 8 : 0); }
@@ -201,7 +200,6 @@ __device__ __forceinline__ void init_bars(Bars* b) {
     mbar_init(&b->d[i], 1);
   }
   mbar_init(&b->ro, kChainWarps);
-  mbar_init(&b->q, 1);
   mbar_init(&b->o, 1);
   mbar_init(&b->e2, kSideWarps);
   mbar_init(&b->f, kSideWarps);
@@ -224,6 +222,14 @@ __device__ __forceinline__ void put_state(uint32_t tm, int lane0, int wg, const 
     st8u(taddr(tm, lane0, Cols<KP>::Sh + wg * (KP / 8) + 8 * b), h);
     st8u(taddr(tm, lane0, Cols<KP>::Sl + wg * (KP / 8) + 8 * b), l);
   }
+}
+// Values b .. b + 7 (b = 0, 8) of the same layout as put_split's.
+__device__ __forceinline__ void put_split8(uint32_t addr, int b, const float (&x)[8]) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split(x[2 * i], x[2 * i + 1], h[i], l[i]);
+  st4u(addr + b / 2, h);
+  st4u(addr + b / 2 + 8, l);
 }
 // The high parts as their pieces of row v of the state's image.
 template <int KP>
@@ -333,10 +339,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ph = c & 1;
       const uint8_t* st = smem + (c & 1) * Tiles<KP>::kBytes;
       const float* gates = reinterpret_cast<const float*>(st + Tiles<KP>::kRec + kRecordGates);
-      if (c > 0 && o) {  // R of the chunk before, whose columns the low part takes, has been read
-        if (!wait_warp(&bars.o, ph ^ 1, status, 12)) break;
-        tc_fence_after();
-      }
       put_state<KP>(tm, lane0, wg, S);
       signal_tmem(&bars.s[half], lane);
       if (stash) {
@@ -368,16 +370,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_warp(&bars.r[half], ph, status, 15)) break;
       tc_fence_after();
       ld16(taddr(tm, lane0, C::R + 16 * wg), x);
-      float a[16];
-      lds16(gates + kC + 16 * wg, a);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) a[i] *= x[i];  // R' = e^{G_end - G} R
-      put_split(taddr(tm, lane0, C::R + 16 * wg), a);
+      for (int b = 0; b < 16; b += 8) {  // R' = e^{G_end - G} R
+        float a[8];
+        lds8(gates + kC + 16 * wg + b, a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] *= x[b + i];
+        put_split8(taddr(tm, lane0, C::R + 16 * wg), b, a);
+      }
       signal_tmem(&bars.rp[half], lane);
       const float keep = gates[kC - 1];
       if (o) {
-        if (!wait_warp(&bars.q, ph, status, 17)) break;  // the state's low part, whose columns these are, has been read
-        tc_fence_after();
         put_split(taddr(tm, lane0, C::Ro + 16 * wg), x);  // R itself
         signal_tmem(&bars.ro, lane);
       }
@@ -447,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the same K rows as [step][key], all keys and the second half of them
       const uint64_t km = sdesc_sw128(smem_u32(st), 128 * 128, 1024);
       const uint64_t km1 = sdesc_sw128(smem_u32(st) + 128 * 128, 128 * 128, 1024);
+      if (o && c > 0 && !wait_warp(&bars.o, ph ^ 1, status, 30)) break;  // (what X is written over)
       if (!wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 31)) break;
       if (!wait_warp(&bars.s[0], ph, status, 32)) break;
       tc_fence_after();
@@ -472,15 +476,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      if (o) {
-        if (c > 0 && !wait_warp(&bars.e2, ph ^ 1, status, 33)) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::QS, tm + C::Sh + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, kb > 0);
-        }
-        __syncwarp();
-      }
       // R^T = Y^T T^T: the steps of 16-block kb reach the steps i >= 16 kb
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -497,10 +492,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ts(tm + C::R + 16 * kb, yh, tl, id, true);
           }
           mma_commit(&bars.r[h]);
-          if (h == 1 && o) {
+        }
+        __syncwarp();
+      }
+      // (Q S)^T, of no hurry, while R' is made
+      if (o) {
+        if (c > 0 && !wait_warp(&bars.e2, ph ^ 1, status, 33)) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-            for (int kb = 0; kb < KP / 16; ++kb) mma_ts(tm + C::QS, tm + C::Sl + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, true);
-            mma_commit(&bars.q);
+          for (int kb = 0; kb < KP / 16; ++kb) {
+            mma_ts(tm + C::QS, tm + C::Sh + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, kb > 0);
+            mma_ts(tm + C::QS, tm + C::Sl + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, true);
           }
         }
         __syncwarp();
@@ -658,16 +661,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       ld16(taddr(tm, lane0, C::R + 16 * wg), x);  // dY
       {
-        float a[16];
 #pragma unroll
         for (int b = 0; b < 16; b += 8) {  // dX = -beta e^G dY
           float e[8], be[8];
           lds8(gates + 16 * wg + b, e);
           lds8(gates + 2 * kC + 16 * wg + b, be);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) a[b + j] = -be[j] * e[j] * x[b + j];
+          for (int j = 0; j < 8; ++j) e[j] *= -be[j] * x[b + j];
+          put_split8(taddr(tm, lane0, C::R + 16 * wg), b, e);
         }
-        put_split(taddr(tm, lane0, C::R + 16 * wg), a);
       }
       signal_tmem(&bars.rp[half], lane);
       const float keep = gates[kC - 1];
@@ -710,15 +712,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int b = 0; b < 8; ++b) {  // F = scale e^G dO^T
         float x[8];
-        uint32_t h[4], l[4];
         lds8(gates + 4 * kC + 8 * b, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           x[j] *= __bfloat162float(*reinterpret_cast<const bf16*>(st + Tiles<KP>::kKQ + v_off(8 * b + j, v)));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) split(x[2 * j], x[2 * j + 1], h[j], l[j]);
-        st4u(taddr(tm, lane0, F + 16 * (b >> 1) + 4 * (b & 1)), h);
-        st4u(taddr(tm, lane0, F + 16 * (b >> 1) + 4 * (b & 1) + 8), l);
+        put_split8(taddr(tm, lane0, F + 16 * (b >> 1)), 8 * (b & 1), x);
       }
       signal_tmem(&bars.f, lane);
       if (lane == 0) mbar_arrive(&bars.empty[i & 1]);
