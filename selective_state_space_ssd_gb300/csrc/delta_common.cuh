@@ -126,10 +126,26 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
 
+// Two fp32 operations in one instruction: (d0, d1) = (a0, a1) (b0, b1) + (c0, c1), and without the sum.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 c, a, b, c; mov.b64 {%0, %1}, c; }"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5};\n"
+      "mul.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 // (x, y) = h + l with both in bf16: h rounds to 8 bits and l holds the next 8, so h + l is within 2^-17 of each.
 __device__ __forceinline__ void split(float x, float y, uint32_t& h, uint32_t& l) {
   h = pack(x, y);
-  l = pack(x - lo_f(h), y - hi_f(h));
+  float a, b;
+  fma2(a, b, lo_f(h), hi_f(h), -1.f, -1.f, x, y);
+  l = pack(a, b);
 }
 
 // Lane addresses into a tile of rows of `pitch` elements, for ldm4 / ldm4t of 16 x 16 elements at

@@ -255,7 +255,8 @@ __device__ __forceinline__ void update_state(uint32_t tm, int lane0, int k0, flo
     float x[16];
     ld16(taddr(tm, lane0, Cols<KP>::D + k0 + 16 * b), x);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(keep, S[16 * b + i], x[i]);
+    for (int i = 0; i < 16; i += 2)
+      fma2(S[16 * b + i], S[16 * b + i + 1], keep, keep, S[16 * b + i], S[16 * b + i + 1], x[i], x[i + 1]);
   }
   tc_fence_before();
 }
@@ -360,9 +361,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           lds8(gates + 16 * wg + b, e);
           lds8(gates + 2 * kC + 16 * wg + b, be);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            x[b + i] = be[i] * fmaf(-e[i], x[b + i],
-                                    __bfloat162float(*reinterpret_cast<const bf16*>(vt + v_off(b + i, vf))));
+          for (int i = 0; i < 8; i += 2) {
+            float a0, a1;
+            fma2(a0, a1, -e[i], -e[i + 1], x[b + i], x[b + i + 1],
+                 __bfloat162float(*reinterpret_cast<const bf16*>(vt + v_off(b + i, vf))),
+                 __bfloat162float(*reinterpret_cast<const bf16*>(vt + v_off(b + i + 1, vf))));
+            mul2(x[b + i], x[b + i + 1], be[i], be[i + 1], a0, a1);
+          }
         }
       }
       put_split(taddr(tm, lane0, C::X + 16 * wg), x);
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float a[8];
         lds8(gates + kC + 16 * wg + b, a);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] *= x[b + i];
+        for (int i = 0; i < 8; i += 2) mul2(a[i], a[i + 1], a[i], a[i + 1], x[b + i], x[b + i + 1]);
         put_split8(taddr(tm, lane0, C::R + 16 * wg), b, a);
       }
       signal_tmem(&bars.rp[half], lane);
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (w < kMmaWarp) {
     const int lane0 = 32 * (w & 3), v = lane0 + lane, tid = threadIdx.x - 32 * kChainWarps;
     const long long os = (long long)d.HV * d.V;
-    bf16* tile = reinterpret_cast<bf16*>(keep_tile + kKeep);
+    unsigned short* tile = reinterpret_cast<unsigned short*>(keep_tile + kKeep);
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
       const float* gates =
@@ -416,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the tile's last rows have been stored; all side warps go on together or not at all
         if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 2
         for (int b = 0; b < 8; ++b) {
           uint32_t q[8], r[8];
           tmem_ld8_nowait(taddr(tm, lane0, C::QS + 8 * b), q);
@@ -426,8 +431,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           if (b == 7) signal_read(&bars.e2, lane);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            tile[(8 * b + i) * 128 + v] = __float2bfloat16_rn(fmaf(e[i], __uint_as_float(q[i]), __uint_as_float(r[i])));
+          for (int i = 0; i < 8; i += 2) {
+            float a0, a1;
+            fma2(a0, a1, e[i], e[i + 1], __uint_as_float(q[i]), __uint_as_float(q[i + 1]), __uint_as_float(r[i]),
+                 __uint_as_float(r[i + 1]));
+            const uint32_t y = pack(a0, a1);
+            tile[(8 * b + i) * 128 + v] = (unsigned short)y;
+            tile[(8 * b + i + 1) * 128 + v] = (unsigned short)(y >> 16);
+          }
         }
         if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
         named_bar(kSideBar, 32 * kSideWarps);
@@ -476,6 +487,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
+      // (Q S)^T, of no hurry, while Y is made
+      if (o) {
+        if (c > 0 && !wait_warp(&bars.e2, ph ^ 1, status, 33)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kb = 0; kb < KP / 16; ++kb) {
+            mma_ts(tm + C::QS, tm + C::Sh + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, kb > 0);
+            mma_ts(tm + C::QS, tm + C::Sl + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, true);
+          }
+        }
+        __syncwarp();
+      }
       // R^T = Y^T T^T: the steps of 16-block kb reach the steps i >= 16 kb
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -492,19 +516,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_ts(tm + C::R + 16 * kb, yh, tl, id, true);
           }
           mma_commit(&bars.r[h]);
-        }
-        __syncwarp();
-      }
-      // (Q S)^T, of no hurry, while R' is made
-      if (o) {
-        if (c > 0 && !wait_warp(&bars.e2, ph ^ 1, status, 33)) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kb = 0; kb < KP / 16; ++kb) {
-            mma_ts(tm + C::QS, tm + C::Sh + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, kb > 0);
-            mma_ts(tm + C::QS, tm + C::Sl + 8 * kb, qd + kdesc_step(128, 16 * kb), n64, true);
-          }
         }
         __syncwarp();
       }
@@ -653,7 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         lds8(gates + kC + 16 * wg + b, e);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[b + j] = fmaf(e[j], __uint_as_float(p[j]), __uint_as_float(q[j]));
+        for (int j = 0; j < 8; j += 2)
+          fma2(x[b + j], x[b + j + 1], e[j], e[j + 1], __uint_as_float(p[j]), __uint_as_float(p[j + 1]),
+               __uint_as_float(q[j]), __uint_as_float(q[j + 1]));
       }
       put_split(taddr(tm, lane0, C::X + 16 * wg), x);
       signal_tmem(&bars.y[half], lane);
@@ -667,7 +680,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           lds8(gates + 16 * wg + b, e);
           lds8(gates + 2 * kC + 16 * wg + b, be);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] *= -be[j] * x[b + j];
+          for (int j = 0; j < 8; j += 2) {
+            mul2(e[j], e[j + 1], e[j], e[j + 1], -be[j], -be[j + 1]);
+            mul2(e[j], e[j + 1], e[j], e[j + 1], x[b + j], x[b + j + 1]);
+          }
           put_split8(taddr(tm, lane0, C::R + 16 * wg), b, e);
         }
       }
@@ -678,15 +694,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i > 0 && !wait_warp(&bars.dv_sent, ph ^ 1, status, 57)) break;
         const int vf = fresh(v);
         uint8_t* yt = keep_tile + 16 * wg * 128;
-        bf16* tile = reinterpret_cast<bf16*>(keep_tile + kKeep) + 16 * wg * 128 + vf;
+        unsigned short* tile = reinterpret_cast<unsigned short*>(keep_tile + kKeep) + 16 * wg * 128 + vf;
 #pragma unroll
         for (int b = 0; b < 16; b += 8) {
           float be[8];
           lds8(gates + 2 * kC + 16 * wg + b, be);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (vf < dyw) *reinterpret_cast<bf16*>(yt + v_off(b + j, vf)) = __float2bfloat16_rn(x[b + j]);
-            tile[(b + j) * 128] = __float2bfloat16_rn(be[j] * x[b + j]);
+          for (int j = 0; j < 8; j += 2) {
+            const uint32_t y = pack(x[b + j], x[b + j + 1]);
+            if (vf < dyw) {
+              *reinterpret_cast<unsigned short*>(yt + v_off(b + j, vf)) = (unsigned short)y;
+              *reinterpret_cast<unsigned short*>(yt + v_off(b + j + 1, vf)) = (unsigned short)(y >> 16);
+            }
+            float a0, a1;
+            mul2(a0, a1, be[j], be[j + 1], x[b + j], x[b + j + 1]);
+            const uint32_t z = pack(a0, a1);
+            tile[(b + j) * 128] = (unsigned short)z;
+            tile[(b + j + 1) * 128] = (unsigned short)(z >> 16);
           }
         }
         signal_tile(&bars.kept, lane);
@@ -709,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_warp(&bars.full[i & 1], (i >> 1) & 1, status, 61)) break;
       if (i > 0 && !wait_warp(&bars.d[0], ph ^ 1, status, 62)) break;  // F of the chunk before has been read
       tc_fence_after();
-#pragma unroll
+#pragma unroll 2
       for (int b = 0; b < 8; ++b) {  // F = scale e^G dO^T
         float x[8];
         lds8(gates + 4 * kC + 8 * b, x);
