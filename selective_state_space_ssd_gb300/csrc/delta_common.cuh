@@ -158,27 +158,31 @@ __device__ __forceinline__ uint32_t by_col(uint32_t base, int pitch, int row, in
   return base + 2u * (uint32_t)((row + (lane & 7) + (((lane >> 3) & 1) << 3)) * pitch + col + ((lane >> 4) << 3));
 }
 
-// 64 rows of `width` (a multiple of 8) elements into a tile: row r from src + r * stride, zeros past `rows` and `cols`.
+// 64 rows of W (64 or 128) elements into a tile by NT threads: row r from src + r * stride, zeros past `rows` and `cols`.
 // vec: every row starts on 16 bytes and cols is a multiple of 8 (asynchronous copies; the caller commits and waits);
 // otherwise element by element.
-__device__ __forceinline__ void load_rows(bf16* dst, int pitch, int width, const bf16* src, long long stride, int rows,
-                                          int cols, bool vec, int tid, int nthreads) {
+template <int W, int NT>
+__device__ __forceinline__ void load_rows(bf16* dst, int pitch, const bf16* src, long long stride, int rows, int cols,
+                                          bool vec, int tid) {
+  constexpr int w8 = W / 8, kStep = NT / w8;
+  static_assert(NT % w8 == 0, "whole rows a step");
   if (vec) {
-    const int w8 = width >> 3;
-    const uint32_t d = su32(dst);
-    for (int i = tid; i < kC * w8; i += nthreads) {
-      const int r = i / w8, c = (i - r * w8) << 3;
+    const int r0 = tid / w8, c = 8 * (tid % w8);
+    const bf16* s = src + (long long)r0 * stride + c;
+    uint32_t a = su32(dst) + 2u * (uint32_t)(r0 * pitch + c);
+    for (int r = r0; r < kC; r += kStep) {
       const bool ok = r < rows && c < cols;
-      cp16(d + 2u * (uint32_t)(r * pitch + c), ok ? src + (long long)r * stride + c : src, ok);
+      cp16(a, ok ? s : src, ok);
+      s += kStep * stride;
+      a += 2u * (uint32_t)(kStep * pitch);
     }
   } else {
-    for (int i = tid; i < kC * width; i += nthreads) {
-      const int r = i / width, c = i - r * width;
+    for (int i = tid; i < kC * W; i += NT) {
+      const int r = i / W, c = i - r * W;
       dst[r * pitch + c] = r < rows && c < cols ? src[(long long)r * stride + c] : __float2bfloat16_rn(0.f);
     }
   }
 }
-
 
 __device__ __forceinline__ float gate(const void* p, size_t i, bool is_bf16) {
   return is_bf16 ? __bfloat162float(static_cast<const bf16*>(p)[i]) : static_cast<const float*>(p)[i];

@@ -156,9 +156,6 @@ __global__ void __launch_bounds__(128, 5) k_delta_prep(Dims d, Table tb, In in, 
   if (c == 0 && hv == 0 && tid == 0) *status = 0;
   const Chunk ch = chunk_of(d, tb, c);
   if (ch.rows == 0) return;
-  load_rows(Ks, kP, KP, in.k + (long long)ch.first * d.ks + (long long)hk * d.K, d.ks, ch.rows, d.K, d.kvec, tid, 128);
-  load_rows(Qs, kP, KP, in.q + (long long)ch.first * d.qs + (long long)hk * d.K, d.qs, ch.rows, d.K, d.qvec, tid, 128);
-  cp_commit();
   uint8_t* record = records + ((size_t)c * d.HV + hv) * kRecordBytes;
   if (w == 0) {  // G of two steps a lane; the sums in fp64, in units of log 2 as a high and a low fp32 part
     double x[2];
@@ -202,6 +199,10 @@ __global__ void __launch_bounds__(128, 5) k_delta_prep(Dims d, Table tb, In in, 
     gr[kC] = make_float2(b[0], b[1]);
     gr[3 * kC / 2] = make_float2(g2[0], g2[1]);
     gr[2 * kC] = make_float2(in.scale * eg[0], in.scale * eg[1]);
+  } else {  // the other warps copy the tiles meanwhile
+    load_rows<KP, 96>(Ks, kP, in.k + (long long)ch.first * d.ks + (long long)hk * d.K, d.ks, ch.rows, d.K, d.kvec, tid - 32);
+    load_rows<KP, 96>(Qs, kP, in.q + (long long)ch.first * d.qs + (long long)hk * d.K, d.qs, ch.rows, d.K, d.qvec, tid - 32);
+    cp_commit();
   }
   cp_wait<0>();
   __syncthreads();
@@ -229,22 +230,39 @@ __global__ void __launch_bounds__(128, 5) k_delta_prep(Dims d, Table tb, In in, 
     }
   }
   __syncthreads();
+  {
+    const float2 hi = make_float2(s_hi[r0 + g4], s_hi[r0 + g4 + 8]), lo = make_float2(s_lo[r0 + g4], s_lo[r0 + g4 + 8]),
+                 be = make_float2(s_beta[r0 + g4], s_beta[r0 + g4 + 8]);
 #pragma unroll
-  for (int nt = 0; nt < 8; ++nt) {
-    if (nt > 2 * w + 1) break;
+    for (int nt = 0; nt < 8; ++nt) {
+      if (nt > 2 * w + 1) break;
+      const int j = 8 * nt + t2;
+      const float2 hj = *reinterpret_cast<const float2*>(s_hi + j), lj = *reinterpret_cast<const float2*>(s_lo + j);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int i = r0 + g4 + 8 * half, j = 8 * nt + t2;
-      float a[2], p[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float dec;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(dec) : "f"((s_hi[i] - s_hi[j + e]) + (s_lo[i] - s_lo[j + e])));
-        a[e] = i > j + e ? s_beta[i] * dec * kk[nt][2 * half + e] : 0.f;
-        p[e] = i >= j + e ? in.scale * dec * qk[nt][2 * half + e] : 0.f;
+      for (int half = 0; half < 2; ++half) {
+        const int i = r0 + g4 + 8 * half;
+        const float h = half ? hi.y : hi.x, l = half ? lo.y : lo.x, b = half ? be.y : be.x;
+        float x0, x1, y0, y1;  // e^{G_i - G_j}, from its exponent's two parts
+        fma2(x0, x1, hj.x, hj.y, -1.f, -1.f, h, h);
+        fma2(y0, y1, lj.x, lj.y, -1.f, -1.f, l, l);
+        fma2(x0, x1, x0, x1, 1.f, 1.f, y0, y1);
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x0) : "f"(x0));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x1) : "f"(x1));
+        if (nt >= 2 * w) {  // the diagonal's blocks
+          x0 = i >= j ? x0 : 0.f;
+          x1 = i >= j + 1 ? x1 : 0.f;
+        }
+        mul2(y0, y1, x0, x1, in.scale, in.scale);
+        mul2(y0, y1, y0, y1, qk[nt][2 * half], qk[nt][2 * half + 1]);
+        *reinterpret_cast<float2*>(Pf + i * kFP + j) = make_float2(y0, y1);
+        mul2(x0, x1, x0, x1, b, b);
+        mul2(x0, x1, x0, x1, kk[nt][2 * half], kk[nt][2 * half + 1]);
+        if (nt >= 2 * w) {
+          x0 = i > j ? x0 : 0.f;
+          x1 = i > j + 1 ? x1 : 0.f;
+        }
+        *reinterpret_cast<float2*>(Af + i * kFP + j) = make_float2(x0, x1);
       }
-      *reinterpret_cast<float2*>(Af + i * kFP + j) = make_float2(a[0], a[1]);
-      *reinterpret_cast<float2*>(Pf + i * kFP + j) = make_float2(p[0], p[1]);
     }
   }
   __syncwarp();

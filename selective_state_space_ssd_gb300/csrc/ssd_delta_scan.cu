@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tslot;
   __shared__ Block s_blk;  // (kept here: the chain has no registers to spare)
   __shared__ Run s_run;
+  __shared__ __align__(16) float s_eg[2][kC];
   uint8_t* smem = aligned_smem(raw);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -415,39 +416,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t ph = c & 1;
       const float* gates =
           reinterpret_cast<const float*>(smem + (c & 1) * Tiles<KP>::kBytes + Tiles<KP>::kRec + kRecordGates);
+      // the decays that o needs, so that the stage is not held until o is there (and a wait for the stage in any case, so
+      // that no warp is a phase ahead)
       bool ok = wait_warp(&bars.full[c & 1], (c >> 1) & 1, status, 23);
-      if (o) {
-        ok = ok && wait_warp(&bars.o, ph, status, 24);
-        // the tile's last rows have been stored; all side warps go on together or not at all
-        if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;
-        tc_fence_after();
-#pragma unroll 2
-        for (int b = 0; b < 8; ++b) {
-          uint32_t q[8], r[8];
-          tmem_ld8_nowait(taddr(tm, lane0, C::QS + 8 * b), q);
-          tmem_ld8_nowait(taddr(tm, lane0, C::O2 + 8 * b), r);
-          float e[8];
-          lds8(gates + 4 * kC + 8 * b, e);
-          tmem_wait_ld();
-          if (b == 7) signal_read(&bars.e2, lane);
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            float a0, a1;
-            fma2(a0, a1, e[i], e[i + 1], __uint_as_float(q[i]), __uint_as_float(q[i + 1]), __uint_as_float(r[i]),
-                 __uint_as_float(r[i + 1]));
-            const uint32_t y = pack(a0, a1);
-            tile[(8 * b + i) * 128 + v] = (unsigned short)y;
-            tile[(8 * b + i + 1) * 128 + v] = (unsigned short)(y >> 16);
-          }
-        }
-        if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
-        named_bar(kSideBar, 32 * kSideWarps);
-        store_tile(reinterpret_cast<const uint8_t*>(tile), o + ((long long)(step0 + c * kC) * d.HV + blk.hv) * d.V, os,
-                   min(kC, steps - c * kC), d.V, d.ovec, tid);
-      } else {
+      if (lane < 16) s_eg[ph][16 * (w & 3) + lane] = gates[4 * kC + 16 * (w & 3) + lane];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.empty[c & 1]);
+      if (!o) {
         if (!ok) break;
-        if (lane == 0) mbar_arrive(&bars.empty[c & 1]);  // (after a wait for the stage, so that no warp is a phase ahead)
+        continue;
       }
+      ok = ok && wait_warp(&bars.o, ph, status, 24);
+      // the tile's last rows have been stored; all side warps go on together or not at all
+      if (named_bar_or(kSideBar, 32 * kSideWarps, !ok)) break;
+      tc_fence_after();
+#pragma unroll 2
+      for (int b = 0; b < 8; ++b) {
+        uint32_t q[8], r[8];
+        tmem_ld8_nowait(taddr(tm, lane0, C::QS + 8 * b), q);
+        tmem_ld8_nowait(taddr(tm, lane0, C::O2 + 8 * b), r);
+        float e[8];
+        lds8(s_eg[ph] + 8 * b, e);
+        tmem_wait_ld();
+        if (b == 7) signal_read(&bars.e2, lane);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          float a0, a1;
+          fma2(a0, a1, e[i], e[i + 1], __uint_as_float(q[i]), __uint_as_float(q[i + 1]), __uint_as_float(r[i]),
+               __uint_as_float(r[i + 1]));
+          const uint32_t y = pack(a0, a1);
+          tile[(8 * b + i) * 128 + v] = (unsigned short)y;
+          tile[(8 * b + i + 1) * 128 + v] = (unsigned short)(y >> 16);
+        }
+      }
+      named_bar(kSideBar, 32 * kSideWarps);
+      store_tile(reinterpret_cast<const uint8_t*>(tile), o + ((long long)(step0 + c * kC) * d.HV + blk.hv) * d.V, os,
+                 min(kC, steps - c * kC), d.V, d.ovec, tid);
     }
   } else if (w == kMmaWarp) {
     constexpr uint32_t n64 = idesc_bf16(128, 64, false, false), n32 = idesc_bf16(128, 32, false, false),
