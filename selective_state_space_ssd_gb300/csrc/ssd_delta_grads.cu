@@ -16,7 +16,7 @@
 // before is in its second half; that traffic is what bounds the kernel.
 //
 // Twenty-three warps: 0-15 the elementwise work, four a lane quadrant (quarters of the columns); 16 the MMAs; 17-18 copies;
-// 19-22 the two sums that need no product (dY . V by rows, <dS', S>).
+// 19-22 the two sums that need no product (dY . V by rows, <dS', S>), and from all sums dbeta and dg.
 #include "delta_tc.cuh"
 
 namespace ssd {
@@ -26,7 +26,7 @@ namespace {
 constexpr int kWorkWarps = 16, kSumWarps = 4, kMmaWarp = kWorkWarps, kLoadWarp0 = kMmaWarp + 1,
               kSumWarp0 = kLoadWarp0 + kLoadWarps;  // (the sums read no tensor memory: any warps will do)
 constexpr int kThreads = 32 * (kSumWarp0 + kSumWarps);
-constexpr int kWorkBar = 1;
+constexpr int kWorkBar = 1, kSumBar = 2;
 
 // Shared memory.  QK: [Q; K] rows of the head; OY: [dO; dY] rows; R^T, S^T, dS'^T images; B: [B1; B2] rows and beta B2,
 // each rounded to bf16, and what that rounding left; Out: dQ rows on their way out (dK's
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
   __shared__ uint32_t tslot;
-  __shared__ float s_yv[kC], s_ss[kSumWarps], s_a[4][kC], s_h[4][kC], s_e[kWorkWarps];
+  __shared__ float s_yv[kC], s_ss[kSumWarps], s_a[2][4][kC], s_h[2][4][kC], s_e[2][kWorkWarps];
   uint8_t* smem = aligned_smem(raw);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -145,8 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars.b, kWorkWarps);
     mbar_init(&bars.w, 1);
     mbar_init(&bars.free, kWorkWarps);
-    mbar_init(&bars.sums, kSumWarps);
-    mbar_init(&bars.sums_read, kWorkWarps);
+    mbar_init(&bars.sums, kWorkWarps);
+    mbar_init(&bars.sums_read, 1);
     mbar_init(&bars.done, 1);
     mbar_init_fence();
   }
@@ -256,9 +256,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           sa[e] = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(t0 + e, (l & 63) >> 3)));
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          g[e] = fmaf(g[e], __uint_as_float(z[e]), __uint_as_float(s[e]));
-          sa[e] *= g[e];
+        for (int e = 0; e < 8; e += 2) {
+          fma2(g[e], g[e + 1], g[e], g[e + 1], __uint_as_float(z[e]), __uint_as_float(z[e + 1]), __uint_as_float(s[e]),
+               __uint_as_float(s[e + 1]));
+          mul2(sa[e], sa[e + 1], sa[e], sa[e + 1], g[e], g[e + 1]);
         }
         emit(tq, cSum + t0, t0, g);
         tmem_ld8_nowait(taddr(tm, lane0, cZ + 64 + t0), z);
@@ -266,73 +267,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         lds8(eg + t0, g);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sh[e] = fmaf(-g[e], __uint_as_float(z[e]), __uint_as_float(s[e]));  // H
+        for (int e = 0; e < 8; e += 2)  // H
+          fma2(sh[e], sh[e + 1], -g[e], -g[e + 1], __uint_as_float(z[e]), __uint_as_float(z[e + 1]), __uint_as_float(s[e]),
+               __uint_as_float(s[e + 1]));
         tmem_ld8_nowait(taddr(tm, lane0, cZ3 + t0), z);
         tmem_ld8_nowait(taddr(tm, lane0, cD + t0), s);
         lds8(gt + kC + t0, g);
         tmem_wait_ld();
         if (b == 1) signal_read(&bars.free, lane);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float k = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(kC + t0 + e, (l & 63) >> 3)));
-          const float r = g[e] * __uint_as_float(z[e]), m = r + __uint_as_float(s[e]);
-          e_all = fmaf(k, r, e_all);
-          sa[e] = fmaf(-k, m, sa[e]);
-          g[e] = fmaf(be[t0 + e], sh[e], m);
-          sh[e] *= k;
+        for (int e = 0; e < 8; e += 2) {
+          const float k0 = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(kC + t0 + e, (l & 63) >> 3)));
+          const float k1 = __bfloat162float(*reinterpret_cast<const bf16*>(qk + sw128_chunk(kC + t0 + e + 1, (l & 63) >> 3)));
+          float r0, r1, m0, m1;
+          mul2(r0, r1, g[e], g[e + 1], __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+          fma2(m0, m1, r0, r1, 1.f, 1.f, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          e_all = fmaf(k1, r1, fmaf(k0, r0, e_all));
+          fma2(sa[e], sa[e + 1], -k0, -k1, m0, m1, sa[e], sa[e + 1]);
+          fma2(g[e], g[e + 1], be[t0 + e], be[t0 + e + 1], sh[e], sh[e + 1], m0, m1);
+          mul2(sh[e], sh[e + 1], sh[e], sh[e + 1], k0, k1);
         }
         emit(tk, cSum + 64 + t0, t0, g);
         const float a = lane_sums(sa, lane), h = lane_sums(sh, lane);
+        // (the sums of the head before have been read, so that no warp is a phase ahead)
+        if (b == 0 && wk.step > 0) ok = wait_warp(&bars.sums_read, ph ^ 1, status, 105) && ok;
         if (lane < 8) {
-          s_a[w & 3][t0 + lane] = a;
-          s_h[w & 3][t0 + lane] = h;
+          s_a[ph][w & 3][t0 + lane] = a;
+          s_h[ph][w & 3][t0 + lane] = h;
         }
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) e_all += __shfl_xor_sync(0xffffffffu, e_all, o);
+      if (lane == 0) s_e[ph][w] = e_all;
+      __syncwarp();
       if (lane == 0) {
-        s_e[w] = e_all;
+        mbar_arrive(&bars.sums);
         if (wk.last()) mbar_arrive(&bars.qk_free);
       }
-      ok = ok && wait_warp(&bars.sums, ph, status, 105);
       if (named_bar_or(kWorkBar, 32 * kWorkWarps, !ok)) break;
-      const Chunk ch = wk.ch;
-      const int hv = wk.hv();
-      if (w == 0) {  // two steps a lane
-        float dG[2], all = lane < kWorkWarps ? s_e[lane] : 0.f;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int t = 2 * lane + n;
-          const float a = (s_a[0][t] + s_a[1][t]) + (s_a[2][t] + s_a[3][t]);
-          const float h = (s_h[0][t] + s_h[1][t]) + (s_h[2][t] + s_h[3][t]);
-          dG[n] = fmaf(be[t], h, a);
-          if (t < ch.rows) put_gate(out.dbeta, (size_t)(ch.first + t) * d.HV + hv, h + s_yv[t], d.gate_bf16);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        const float end = fmaf(eg[kC - 1], (s_ss[0] + s_ss[1]) + (s_ss[2] + s_ss[3]), all);
-        float sum = dG[0] + dG[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float y = __shfl_down_sync(0xffffffffu, sum, o);
-          if (lane + o < 32) sum += y;
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int t = 2 * lane + n;
-          if (t < ch.rows)
-            put_gate(out.dg, (size_t)(ch.first + t) * d.HV + hv, end + (n ? sum - dG[0] : sum), d.gate_bf16);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.sums_read);
       if (wk.last()) {
         const long long stride = (long long)d.H * d.K;
-        const size_t at = ((size_t)ch.first * d.H + wk.hk) * d.K;
-        store_rows(tq, out.dq + at, stride, ch.rows, d.K, tid);
-        store_rows(tk, out.dk + at, stride, ch.rows, d.K, tid);
+        const size_t at = ((size_t)wk.ch.first * d.H + wk.hk) * d.K;
+        store_rows(tq, out.dq + at, stride, wk.ch.rows, d.K, tid);
+        store_rows(tk, out.dk + at, stride, wk.ch.rows, d.K, tid);
+        named_bar(kWorkBar, 32 * kWorkWarps);  // the tiles have been read: the next head writes B over one
       }
-      named_bar(kWorkBar, 32 * kWorkWarps);  // sums and tiles have been read before the next head writes its own
     }
   } else if (w == kMmaWarp) {
     constexpr uint32_t iM = idesc_bf16(128, 64, false, true), iZ = idesc_bf16(128, 128, true, false),
@@ -475,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!wait_warp(&bars.full, ph, status, 131)) break;
+      bool ok = wait_warp(&bars.full, ph, status, 131);  // (all sum warps stop together, below)
       float x = 0.f;
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
@@ -505,15 +484,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       float y = (lane >> 2) == 2 * (lane & 3) ? c4[0] : (lane >> 2) == 2 * (lane & 3) + 1 ? c4[1] : 0.f;
 #pragma unroll
       for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-      // the head before has been finished: its sums have been read, and its decays, whose place the next copies take
-      if (wk.step > 0 && !wait_warp(&bars.sums_read, ph ^ 1, status, 132)) break;
       if ((tid & 1) == 0) s_yv[t] = x;
-      if (lane == 0) s_ss[tid >> 5] = y;
-      __syncwarp();
       if (lane == 0) {
+        s_ss[tid >> 5] = y;
         mbar_arrive(&bars.empty);
-        mbar_arrive(&bars.sums);
       }
+      // dbeta, and dG with its sums from the right, once the work warps' shares are there: two steps a lane of one warp.
+      // (The decays' place is free for the head after the next only when this warp arrives for the next.)
+      if (w == kSumWarp0) ok = ok && wait_warp(&bars.sums, ph, status, 132);
+      if (named_bar_or(kSumBar, 32 * kSumWarps, !ok)) break;
+      if (w == kSumWarp0) {
+        const float* gt = reinterpret_cast<const float*>(smem + oGates) + ph * kGateRows * kC;
+        const float *eg = gt, *be = gt + 2 * kC;
+        const int hv = wk.hv();
+        float dG[2], all = lane < kWorkWarps ? s_e[ph][lane] : 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int u = 2 * lane + n;
+          const float a0 = (s_a[ph][0][u] + s_a[ph][1][u]) + (s_a[ph][2][u] + s_a[ph][3][u]);
+          const float h = (s_h[ph][0][u] + s_h[ph][1][u]) + (s_h[ph][2][u] + s_h[ph][3][u]);
+          dG[n] = fmaf(be[u], h, a0);
+          if (u < ch.rows) put_gate(out.dbeta, (size_t)(ch.first + u) * d.HV + hv, h + s_yv[u], d.gate_bf16);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        const float end = fmaf(eg[kC - 1], (s_ss[0] + s_ss[1]) + (s_ss[2] + s_ss[3]), all);
+        float sum = dG[0] + dG[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const float z = __shfl_down_sync(0xffffffffu, sum, o);
+          if (lane + o < 32) sum += z;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int u = 2 * lane + n;
+          if (u < ch.rows)
+            put_gate(out.dg, (size_t)(ch.first + u) * d.HV + hv, end + (n ? sum - dG[0] : sum), d.gate_bf16);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.sums_read);
+      }
+      named_bar(kSumBar, 32 * kSumWarps);  // (s_yv and s_ss are written again)
     }
   }
   __syncthreads();
