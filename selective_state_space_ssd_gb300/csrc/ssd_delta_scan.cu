@@ -909,72 +909,68 @@ cudaError_t make_maps(const Dims& d, const In& in, const bf16* v, long long vstr
 }
 
 // S_in of the runs of a split scan: S_in of run 1 is there (the first run's result), S_in of run i + 1 is M_i S_in_i + B_i
-// in the place of B_i.  A block per (sequence, value head) and 16 columns; a thread four rows and four columns.  fp32; the
+// in the place of B_i.  A block per (sequence, value head) and 16 columns; a thread four rows and two columns.  fp32; the
 // next map's copy is in flight while a product is computed.
-constexpr int kMapPitch = 132;
-__global__ void __launch_bounds__(128) k_delta_join(Split sp, int K, int KP, int V) {
+constexpr int kMapPitch = 132, kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) k_delta_join(Split sp, int K, int KP, int V) {
   extern __shared__ __align__(16) float sm[];  // two maps [KP][kMapPitch], the state's columns [KP][16]
   float* cols = sm + 2 * KP * kMapPitch;
-  const int tid = threadIdx.x, r0 = 4 * (tid >> 2), c0 = 4 * (tid & 3), v0 = blockIdx.y * 16 + c0;
+  const int tid = threadIdx.x, r0 = 4 * (tid >> 3), c0 = 2 * (tid & 7), v0 = blockIdx.y * 16 + c0;
   float* st = sp.states + (size_t)blockIdx.x * (sp.parts - 1) * K * V;
   const float* maps = sp.maps + (size_t)blockIdx.x * (sp.parts - 2) * KP * KP;
   const auto fetch = [&](int i) {
     const float* m = maps + (size_t)(i - 1) * KP * KP;
     const uint32_t dst = su32(sm + (i & 1) * KP * kMapPitch);
-    for (int j = tid; j < KP * KP / 4; j += 128) {
+    for (int j = tid; j < KP * KP / 4; j += kJoinThreads) {
       const int r = j / (KP / 4), c = 4 * (j - r * (KP / 4));
       cp16(dst + 4u * (uint32_t)(r * kMapPitch + c), m + r * KP + c, true);
     }
     cp_commit();
   };
-  fetch(1);
   const bool on = r0 < KP;
-  if (on)
+  const auto mine = [&](const float* p, float (&x)[4][2]) {  // this thread's part of a state
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        cols[(r0 + a) * 16 + c0 + b] = r0 + a < K && v0 + b < V ? st[(size_t)(r0 + a) * V + v0 + b] : 0.f;
+      for (int b = 0; b < 2; ++b) x[a][b] = on && r0 + a < K && v0 + b < V ? p[(size_t)(r0 + a) * V + v0 + b] : 0.f;
+  };
+  float x[4][2];
+  fetch(1);
+  mine(st, x);
   for (int i = 1; i < sp.parts - 1; ++i) {
     float* out = st + (size_t)i * K * V;
-    float x[4][4];
+    if (on)
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) x[a][b] = r0 + a < K && v0 + b < V ? out[(size_t)(r0 + a) * V + v0 + b] : 0.f;
-    if (i + 1 < sp.parts - 1) fetch(i + 1);
-    else cp_commit();
+      for (int a = 0; a < 4; ++a) *reinterpret_cast<float2*>(cols + (r0 + a) * 16 + c0) = make_float2(x[a][0], x[a][1]);
+    mine(out, x);
+    if (i + 1 < sp.parts - 1)
+      fetch(i + 1);
+    else
+      cp_commit();
     cp_wait<1>();
     __syncthreads();
     if (on) {
       const float* m = sm + (i & 1) * KP * kMapPitch + r0 * kMapPitch;
+#pragma unroll 4
       for (int k = 0; k < KP; k += 4) {
-        float4 s[4];
+        float2 s[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = *reinterpret_cast<const float4*>(cols + (k + e) * 16 + c0);
+        for (int e = 0; e < 4; ++e) s[e] = *reinterpret_cast<const float2*>(cols + (k + e) * 16 + c0);
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
           const float4 y = *reinterpret_cast<const float4*>(m + a * kMapPitch + k);
           const float ya[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[a][0] = fmaf(ya[e], s[e].x, x[a][0]);
-            x[a][1] = fmaf(ya[e], s[e].y, x[a][1]);
-            x[a][2] = fmaf(ya[e], s[e].z, x[a][2]);
-            x[a][3] = fmaf(ya[e], s[e].w, x[a][3]);
-          }
+          for (int e = 0; e < 4; ++e) fma2(x[a][0], x[a][1], ya[e], ya[e], s[e].x, s[e].y, x[a][0], x[a][1]);
         }
       }
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          if (r0 + a < K && v0 + b < V) out[(size_t)(r0 + a) * V + v0 + b] = x[a][b];
     }
     __syncthreads();
-    if (on)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        *reinterpret_cast<float4*>(cols + (r0 + a) * 16 + c0) = make_float4(x[a][0], x[a][1], x[a][2], x[a][3]);
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (r0 + a < K && v0 + b < V) out[(size_t)(r0 + a) * V + v0 + b] = x[a][b];
-      }
   }
 }
 
@@ -984,7 +980,7 @@ cudaError_t join(const Dims& d, const Split& split, cudaStream_t st) {
   const cudaError_t e = allow_smem(k_delta_join, smem);
   if (e != cudaSuccess) return e;
   SSD_LAUNCH("k_delta_join", st,
-             k_delta_join<<<dim3((unsigned)(d.N * d.HV), (unsigned)((d.V + 15) / 16)), 128, smem, st>>>(split, d.K, d.KP, d.V));
+             k_delta_join<<<dim3((unsigned)(d.N * d.HV), (unsigned)((d.V + 15) / 16)), kJoinThreads, smem, st>>>(split, d.K, d.KP, d.V));
   return cudaGetLastError();
 }
 
