@@ -416,11 +416,11 @@ ssd_status ssd_kda_backward(const ssd_kda_problem* prob, const float* dout, cons
  *
  * Precision.  The state is fp32 over any length: what the chunk products read
  * of it enters the tensor cores as two bf16 numbers, so s_final (and ds0) are
- * good to about 1e-5 of their size, and o is rounded once to bf16.  The other
- * gradients are sums of products of bf16-rounded tiles: their relative error
- * is about 2^-8 whatever type they are stored in.  A NaN or infinity in q, k,
- * v, g or beta may reach every step of its chunk of 64 steps and every later
- * one of its sequence; other sequences and steps past a sequence's end take
+ * good to about 1e-5 of their size, and o and dv are rounded once to
+ * bf16.  The other gradients are sums of products of bf16-rounded tiles: their
+ * relative error is about 2^-8 whatever type they are stored in.  A NaN or
+ * infinity in q, k, v, g or beta may reach every step of its chunk of 64 steps
+ * and every later one of its sequence; other sequences and steps past a sequence's end take
  * nothing from it.
  *
  * ssd_delta_workspace_size: device workspace of ssd_delta_forward (backward ==
@@ -431,7 +431,7 @@ ssd_status ssd_kda_backward(const ssd_kda_problem* prob, const float* dout, cons
  *   for its backward: per chunk and value head the bf16 state that enters it
  *   (V16*KP*2 bytes, V16 = V rounded up to 16, KP = K rounded up to 64 or
  *   128), the written rows r (64*V16*2) and the chunk's triangular inverse,
- *   scores and decays (25.25 KiB).  Host-only.
+ *   scores and decays (33.25 KiB).  Host-only.
  * ssd_delta_forward: o, and s_final unless it is NULL, from s0 (NULL: zeros).
  *   stash NULL, or a device buffer (16-byte aligned) that is filled.
  * ssd_delta_backward: dq, dk, dv, dg, dbeta and (unless NULL) ds0 of <do, o> +

@@ -1,6 +1,6 @@
-// Building blocks of the chunked delta rule: warp-level bf16 products whose operands come out of shared-memory tiles
-// (ldmatrix) or straight out of another product's accumulators, the split of an fp32 operand into two bf16 ones, and
-// the sizes, tiles and workspace records that its kernels share.
+// Building blocks of the delta rule: its sizes and where its sequences lie, the records and kept tiles that its kernels
+// hand to one another, warp-level bf16 products out of shared-memory tiles, and the split of an fp32 operand into two
+// bf16 ones.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -16,7 +16,6 @@ namespace delta {
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 64;              // steps of a chunk
-constexpr int kTP = kC + 8;         // shared-memory pitch of a [64][64] bf16 tile (16 bytes past a multiple of 128: ldmatrix without conflicts)
 constexpr int kGateRows = 5;        // per-step records of a chunk: e^G, e^{G_end - G}, beta, G / ln 2, scale e^G
 constexpr float kMinG = -200.f;     // e^g of anything below is 0; keeps G - G' defined where g is -inf
 

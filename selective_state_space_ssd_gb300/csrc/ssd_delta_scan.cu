@@ -19,6 +19,8 @@
 // memory), and the elementwise work of 128 x 64 and 128 x K values between them.  So the chain goes in two halves, warps
 // 0-7 with the steps 0-31 and the first half of the keys and warps 8-15 with the others: while one half is at its
 // elementwise work the MMAs run that need only the other's (X's first keys, R's first steps, the state's first half).
+// Measured at K = V = 128, 128 heads of 64 chunks at once: 205 us forward with the stash, 3.2 us a chunk (1.08 GB moved,
+// 5.2 TB/s: four fifths of a plain copy's rate), 201 us in reverse.
 #include "delta_tc.cuh"
 
 namespace ssd {

