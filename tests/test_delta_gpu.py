@@ -332,6 +332,26 @@ def test_on_a_side_stream():
         assert torch.equal(ref[k], got[k]), k
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements of v and o: the last chunks are those of a short run (the state is empty until then)."""
+    hv, tail, T = 64, 100, 64 * 4099 + 1
+    cfg = cfg_of(T=T, H=1, HV=hv, K=16, V=128)
+    assert T * hv * 128 > 1 << 31
+    short = cuda(make(cfg_of(T=tail, H=1, HV=hv, K=16, V=128), 16))
+    x = dict(q=torch.zeros((1, T, 1, 16), dtype=torch.bfloat16, device="cuda"))
+    x["k"] = torch.zeros_like(x["q"])
+    x["v"] = torch.zeros((1, T, hv, 128), dtype=torch.bfloat16, device="cuda")
+    x["g"] = torch.zeros((1, T, hv), device="cuda")
+    x["beta"] = torch.zeros_like(x["g"])
+    for n in x:
+        x[n][:, -tail:] = short[n]
+    o, sf = binding.delta_forward(cfg, *x.values())
+    want_o, want_sf = binding.delta_forward(dict(cfg, seqlen=tail), *(short[n] for n in x))
+    assert (o[:, :-tail] == 0).all()
+    assert rel(o[:, -tail:], want_o.double().cpu().numpy()) <= 8e-3  # (other chunk bounds, other roundings)
+    assert rel(sf, want_sf.double().cpu().numpy()) <= 6e-5
+
+
 # ---------------------------------------------------------------- the step form
 STEP_CASES = {
     "one": (cfg_of(b=1, T=1, H=1, HV=2, K=128, V=128), 1),
@@ -361,6 +381,20 @@ def test_step_matches_the_oracle(name):
     assert rel(state[at.long().cuda()], ref["s_final"]) <= 1e-5
     rest = [i for i in range(slots) if i not in at.tolist()]
     assert torch.equal(state[rest].cpu(), cache[rest])  # the other slots are untouched
+
+
+def test_step_slots_past_32_bits():
+    """A cache of more than 2^31 elements: the last slots are the sequences' own."""
+    cfg = cfg_of(b=2, T=2, H=8, HV=32, K=128, V=128)
+    dev = cuda(make(cfg, 26))
+    x = tuple(dev[n] for n in ("q", "k", "v", "g", "beta"))
+    slots = (1 << 31) // (32 * 128 * 128) + 3
+    state = torch.empty((slots, 32, 128, 128), device="cuda")
+    at = torch.tensor([slots - 1, slots - 2], dtype=torch.int32, device="cuda")
+    state[at.long()] = dev["s0"]
+    o = binding.delta_step(cfg, *x, state, at)
+    want = dev["s0"].clone()
+    assert torch.equal(o, binding.delta_step(cfg, *x, want)) and torch.equal(state[at.long()], want)
 
 
 def test_step_places_without_a_sequence():

@@ -131,6 +131,18 @@ def test_rows_take_nothing_from_a_nan_row_and_calls_repeat():
     assert y2[7].isnan().all()
 
 
+def test_offsets_past_32_bits():
+    rows, dim = (1 << 31) // 8192 + 5, 8192
+    x = torch.zeros((rows, dim), dtype=torch.bfloat16, device="cuda")
+    c = make(3, dim, "bf16", "f32", 6)
+    d = {k: t.cuda() for k, t in c.items()}
+    x[-3:] = d["x"]
+    y, mean, rstd = binding.norm_forward(x, d["w"], d["b"])
+    ref = reference(c, 1e-5)
+    for n, t in dict(y=y, mean=mean, rstd=rstd).items():
+        check(n, t[-3:], ref[n])
+
+
 def test_gradients_against_differences():
     c = make(6, 40, "f32", "f32", 5)
     d = {k: t.cuda() for k, t in c.items()}
