@@ -13,11 +13,15 @@
 // Results are transposed (a TMEM lane is a key): six groups of MMAs a value head, the two that read S and the two that
 // read [dO; dY] stacked on 128 rows.  The decays never touch an operand but B1, B2: everything else is scaled in fp32
 // where it leaves tensor memory.  What a head reads (144 KB for K = V = 128) comes by TMA and bulk copies while the head
-// before is in its second half.  8192 chunks and heads: 336 us, 4.0 TB/s (1.34 GB); the elementwise work between the
-// products bounds it, at 1.7 times the time of the traffic alone.
+// before is in its second half, S and dS' last: the scores do not wait for them.  8192 chunks and heads:
+// 269 us, 5.0 TB/s (1.34 GB); the elementwise work between the products bounds it, at 1.3 times the time of the traffic
+// alone.
 //
 // Twenty-three warps: 0-15 the elementwise work, four a lane quadrant (quarters of the columns); 16 the MMAs; 17-18 copies;
-// 19-22 the two sums that need no product (dY . V by rows, <dS', S>), and from all sums dbeta and dg.
+// 19-22 the two sums that need no product (dY . V by rows, <dS', S>); 23 dbeta and dg from all sums.  The two sums hold the
+// tiles longer than the MMAs do, and the next head's copies with them: fused operations on bf16 pairs took 277 us,
+// fp32 ones after a conversion 283, mma.sync (of which the diagonal is wanted) 293, each before the scores stopped waiting
+// for S and dS'.
 #include "delta_tc.cuh"
 
 namespace ssd {
@@ -25,9 +29,10 @@ namespace delta {
 namespace {
 
 constexpr int kWorkWarps = 16, kSumWarps = 4, kMmaWarp = kWorkWarps, kLoadWarp0 = kMmaWarp + 1,
-              kSumWarp0 = kLoadWarp0 + kLoadWarps;  // (the sums read no tensor memory: any warps will do)
-constexpr int kThreads = 32 * (kSumWarp0 + kSumWarps);
-constexpr int kWorkBar = 1, kSumBar = 2;
+              kSumWarp0 = kLoadWarp0 + kLoadWarps,  // (the sums read no tensor memory: any warps will do)
+              kGateWarp = kSumWarp0 + kSumWarps;
+constexpr int kThreads = 32 * (kGateWarp + 1);
+constexpr int kWorkBar = 1;
 
 // Shared memory.  QK: [Q; K] rows of the head; OY: [dO; dY] rows; R^T, S^T, dS'^T images; B: [B1; B2] rows and beta B2,
 // each rounded to bf16, and what that rounding left; Out: dQ rows on their way out (dK's
@@ -43,7 +48,7 @@ constexpr int cM = 0, cD = 0, cZ3 = 64, cZ = 128, cW = 256, cSum = 384;
 constexpr uint32_t kTmemCols = 512;
 
 struct Bars {
-  uint64_t qk, qk_free, full, empty, tail, m, z, b, w, free, sums, sums_read, done;
+  uint64_t qk, qk_free, full, states, empty, tail, m, z, b, w, dk, free, sums, sums_read, done;
 };
 struct Maps {
   CUtensorMap k, q, dout;
@@ -82,10 +87,20 @@ struct Work {
   }
 };
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+// a . b + x: bf16 pairs multiplied into fp32, without a conversion of their own.
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float x) {
   const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x = fmaf(lo_f(p[i]), lo_f(q[i]), fmaf(hi_f(p[i]), hi_f(q[i]), x));
+  for (int i = 0; i < 4; ++i)
+    asm("{\n.reg .b16 a, b, c, d;\nmov.b32 {a, b}, %1;\nmov.b32 {c, d}, %2;\n"
+        "fma.rn.f32.bf16 %0, a, c, %0;\nfma.rn.f32.bf16 %0, b, d, %0;\n}"
+        : "+f"(x)
+        : "r"(p[i]), "r"(q[i]));
   return x;
 }
 
@@ -132,21 +147,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
   __shared__ uint32_t tslot;
-  __shared__ float s_yv[kC], s_ss[kSumWarps], s_a[2][4][kC], s_h[2][4][kC], s_e[2][kWorkWarps];
+  __shared__ float s_yv[2][kC], s_ss[2][kSumWarps], s_a[2][4][kC], s_h[2][4][kC], s_e[2][kWorkWarps];
   uint8_t* smem = aligned_smem(raw);
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     mbar_init(&bars.qk, kLoadWarps + 1);
     mbar_init(&bars.qk_free, 1 + kWorkWarps);
     mbar_init(&bars.full, kLoadWarps + 1);
-    mbar_init(&bars.empty, 1 + kSumWarps + kWorkWarps);
+    mbar_init(&bars.states, 1);
+    mbar_init(&bars.empty, 1 + kSumWarps + kWorkWarps + 1);
     mbar_init(&bars.tail, 1);
     mbar_init(&bars.m, 1);
     mbar_init(&bars.z, 1);
     mbar_init(&bars.b, kWorkWarps);
     mbar_init(&bars.w, 1);
+    mbar_init(&bars.dk, 1);
     mbar_init(&bars.free, kWorkWarps);
-    mbar_init(&bars.sums, kWorkWarps);
+    mbar_init(&bars.sums, kWorkWarps + kSumWarps);
     mbar_init(&bars.sums_read, 1);
     mbar_init(&bars.done, 1);
     mbar_init_fence();
@@ -271,6 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 8; e += 2)  // H
           fma2(sh[e], sh[e + 1], -g[e], -g[e + 1], __uint_as_float(z[e]), __uint_as_float(z[e + 1]), __uint_as_float(s[e]),
                __uint_as_float(s[e + 1]));
+        if (b == 0) {
+          ok = wait_warp(&bars.dk, ph, status, 107) && ok;
+          tc_fence_after();
+        }
         tmem_ld8_nowait(taddr(tm, lane0, cZ3 + t0), z);
         tmem_ld8_nowait(taddr(tm, lane0, cD + t0), s);
         lds8(gt + kC + t0, g);
@@ -331,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&bars.m);
       }
       __syncwarp();
+      if (!wait_warp(&bars.states, ph, status, 116)) break;
       if (elect_one()) {
         for (int vb = 0; vb < nv; ++vb) mma_bf16(tm + cZ, sm + mdesc_step(16 * vb), oy + kdesc_step(128, 16 * vb), iZ, vb > 0);
         for (int vb = 0; vb < nv; ++vb) mma_bf16(tm + cZ3, dm + mdesc_step(16 * vb), rt + mdesc_step(16 * vb), iR, vb > 0);
@@ -349,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_bf16(tm + cW, km + mdesc_step(16 * jb), bk + kdesc_step(128, 16 * jb), iW, jb > 0);
           mma_bf16(tm + cW, km + mdesc_step(16 * jb), bkl + kdesc_step(128, 16 * jb), iW, true);
         }
+        mma_commit(&bars.w);
         // the transposed scores: row block ib has columns j <= 16 ib + 15
 #pragma unroll
         for (int ib = 3; ib >= 0; --ib) {
@@ -358,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_bf16(tm + cD, km + mdesc_step(16 * ib), mdesc(smem + oBb, kC, 16 * ib), id, true);
           mma_bf16(tm + cD, km + mdesc_step(16 * ib), mdesc(smem + oBbl, kC, 16 * ib), id, true);
         }
-        mma_commit(&bars.w);
+        mma_commit(&bars.dk);
         if (wk.last()) mma_commit(&bars.qk_free);
       }
       __syncwarp();
@@ -381,15 +404,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t item = wk.item();
       if (tid == 0) {
         const uint32_t sb = (uint32_t)d.VP * 128 * na, rb = (uint32_t)d.VP * 128, gb = kGateRows * kC * 4;
-        mbar_expect_tx(bar, 2 * sb + rb + gb + kC * 128 * va * (1 + (d.ovec ? 1 : 0)));
+        mbar_expect_tx(bar, rb + gb + kC * 128 * va * (1 + (d.ovec ? 1 : 0)));
         if (d.ovec)
           for (int a = 0; a < va; ++a) tma_load_3d(smem + oOY + a * 16384, &maps.dout, 64 * a, wk.hv(), first, bar);
         for (int a = 0; a < va; ++a)
           bulk_load(smem_u32(smem + oOY) + a * 16384 + kC * 128, dYst + item * va * 64 * kC + a * 64 * kC, kC * 128, bar);
         bulk_load(smem_u32(smem + oR), Rst + item * d.VP * kC, rb, bar);
         bulk_load(smem_u32(smem + oGates) + ph * gb, records + item * kRecordBytes + kRecordGates, gb, bar);
-        bulk_load(smem_u32(smem + oS), Sst + item * d.VP * d.KP, sb, bar);
-        bulk_load(smem_u32(smem + oD), dSst + item * d.VP * d.KP, sb, bar);
+        mbar_expect_tx(&bars.states, 2 * sb);
+        bulk_load(smem_u32(smem + oS), Sst + item * d.VP * d.KP, sb, &bars.states);
+        bulk_load(smem_u32(smem + oD), dSst + item * d.VP * d.KP, sb, &bars.states);
       }
       if (!d.ovec)
         load_elements(smem + oOY, 128, 64 * va, dout + ((long long)first * d.HV + wk.hv()) * d.V, (long long)d.HV * d.V, rows, d.V, tid);
@@ -428,104 +452,122 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // no copy is in flight when the block ends
-    if (loaded >= 0) wait_warp(&bars.full, loaded & 1, status, 125);
+    if (loaded >= 0) {
+      wait_warp(&bars.full, loaded & 1, status, 125);
+      wait_warp(&bars.states, loaded & 1, status, 127);
+    }
     if (units >= 0) wait_warp(&bars.qk, units & 1, status, 126);
-  } else {
-    const int tid = threadIdx.x - 32 * kSumWarp0, t = tid >> 1;  // two lanes a row, every other piece of eight columns each
-    for (; wk.more(); wk.next()) {
-      const uint32_t ph = wk.step & 1;
-      const Chunk ch = wk.ch;
-      uint4 a[8];  // V, before the wait
-      {
-        const bf16* vr = in.v + (long long)(ch.first + t) * d.vs + (long long)wk.hv() * d.V;
+  } else if (w < kGateWarp) {
+    const int sw = w - kSumWarp0, g = lane >> 2, q4 = lane & 3;
+    uint4 v[2][4];  // V, rows 16 sw + g and + 8, pieces of eight columns 4 n + q4: read before the wait
+    const auto fetch = [&] {
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          const int j = 2 * n + (tid & 1);
-          a[n] = make_uint4(0, 0, 0, 0);
-          if (t >= ch.rows || 8 * j >= d.V) continue;
+      for (int h = 0; h < 2; ++h) {
+        const int t = 16 * sw + 8 * h + g;
+        const bf16* vr = in.v + (long long)(wk.ch.first + t) * d.vs + (long long)wk.hv() * d.V;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int c = 32 * n + 8 * q4;
+          v[h][n] = make_uint4(0, 0, 0, 0);
+          if (t >= wk.ch.rows || c >= d.V) continue;
           if (d.vvec) {
-            a[n] = *reinterpret_cast<const uint4*>(vr + 8 * j);
+            v[h][n] = *reinterpret_cast<const uint4*>(vr + c);
           } else {
             uint32_t p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              p[e] = pack(8 * j + 2 * e < d.V ? __bfloat162float(vr[8 * j + 2 * e]) : 0.f,
-                          8 * j + 2 * e + 1 < d.V ? __bfloat162float(vr[8 * j + 2 * e + 1]) : 0.f);
-            a[n] = make_uint4(p[0], p[1], p[2], p[3]);
+              p[e] = pack(c + 2 * e < d.V ? __bfloat162float(vr[c + 2 * e]) : 0.f,
+                          c + 2 * e + 1 < d.V ? __bfloat162float(vr[c + 2 * e + 1]) : 0.f);
+            v[h][n] = make_uint4(p[0], p[1], p[2], p[3]);
           }
         }
       }
-      bool ok = wait_warp(&bars.full, ph, status, 131);  // (all sum warps stop together, below)
-      float x = 0.f;
+    };
+    for (; wk.more(); wk.next()) {
+      const uint32_t ph = wk.step & 1;
+      fetch();
+      bool ok = wait_warp(&bars.full, ph, status, 131);
+      const uint32_t oa = smem_u32(smem + oOY) + (kC + 16 * sw + g) * 128;
+      float yv[2] = {0.f, 0.f}, ss[2] = {0.f, 0.f};
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        const int j = 2 * n + (tid & 1);
-        if (8 * j < d.V)
-          x = dot8(a[n], *reinterpret_cast<const uint4*>(smem + oOY + (j >> 3) * 16384 + sw128_chunk(kC + t, j & 7)), x);
-      }
-      x += __shfl_xor_sync(0xffffffffu, x, 1);
-      // <dS', S>: eight rows of both images as the operands of a small product, of which the diagonal is wanted; each
-      // lane's rows of the images have one layout, so one address serves both
-      float c4[4] = {0.f, 0.f, 0.f, 0.f};
-      const int sw = tid >> 5, groups = d.VP / 8;
-      const uint32_t sa = smem_u32(smem + oS), da = smem_u32(smem + oD);
-      for (int g = sw; g < groups * (d.KP / 64); g += kSumWarps) {
-        const int atom = g / groups, r = 8 * (g - atom * groups) + (lane & 7);
+      for (int n = 0; n < 4; ++n) {
+        if (32 * n >= d.V) break;
+        const int j = 4 * n + q4;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t at = (uint32_t)(atom * d.VP * 128) + sw128_chunk(r, 4 * h + (lane >> 3));
-          uint32_t m[4], n[4];
-          ldm4(m, sa + at);
-          ldm4(n, da + at);
-          const uint32_t a0[4] = {m[0], 0u, m[1], 0u}, a1[4] = {m[2], 0u, m[3], 0u};
-          mma(c4, a0, n[0], n[1]);
-          mma(c4, a1, n[2], n[3]);
-        }
+        for (int h = 0; h < 2; ++h)
+          if (8 * j < d.V) yv[h] = dot8(v[h][n], lds128(oa + (n >> 1) * 16384 + h * 1024 + (((j & 7) ^ g) << 4)), yv[h]);
       }
-      float y = (lane >> 2) == 2 * (lane & 3) ? c4[0] : (lane >> 2) == 2 * (lane & 3) + 1 ? c4[1] : 0.f;
+      const uint32_t at = smem_u32(smem) + (uint32_t)(sw * 1024 + lane * 16);
+      ok = ok && wait_warp(&bars.states, ph, status, 135);
+#pragma unroll 2
+      for (int i = sw; i < d.VP * d.KP / 512; i += kSumWarps) {  // a kilobyte of both images
+        const uint32_t p = at + (i - sw) * 1024;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) ss[h] = dot8(lds128(p + 512 * h + oS), lds128(p + 512 * h + oD), ss[h]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.empty);  // (the tiles have been read)
+      float y = ss[0] + ss[1];
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) yv[h] += __shfl_xor_sync(0xffffffffu, yv[h], o);
+      const float y0 = yv[0], y1 = yv[1];
 #pragma unroll
       for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-      if ((tid & 1) == 0) s_yv[t] = x;
+      // (the sums of the head before have been read, so that no warp is a phase ahead)
+      if (wk.step > 0) ok = wait_warp(&bars.sums_read, ph ^ 1, status, 132) && ok;
+      if (q4 == 0) {
+        s_yv[ph][16 * sw + g] = y0;
+        s_yv[ph][16 * sw + 8 + g] = y1;
+      }
+      if (lane == 0) s_ss[ph][sw] = y;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.sums);
+      if (!ok) break;
+    }
+  } else {
+    // dbeta, and dG with its sums from the right, once all shares are there: two steps a lane.  The decays' place is free
+    // for the head after the next only when this warp has arrived for the next.
+    if (lane == 0) mbar_arrive(&bars.empty);
+    for (; wk.more(); wk.next()) {
+      const uint32_t ph = wk.step & 1;
+      const Chunk ch = wk.ch;
+      if (!wait_warp(&bars.sums, ph, status, 133) || !wait_warp(&bars.empty, ph, status, 134)) break;
+      const float* gt = reinterpret_cast<const float*>(smem + oGates) + ph * kGateRows * kC;
+      const float *eg = gt, *be = gt + 2 * kC;
+      const int hv = wk.hv();
+      float dG[2], db[2], all = lane < kWorkWarps ? s_e[ph][lane] : 0.f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int u = 2 * lane + n;
+        const float a0 = (s_a[ph][0][u] + s_a[ph][1][u]) + (s_a[ph][2][u] + s_a[ph][3][u]);
+        const float h = (s_h[ph][0][u] + s_h[ph][1][u]) + (s_h[ph][2][u] + s_h[ph][3][u]);
+        dG[n] = fmaf(be[u], h, a0);
+        db[n] = h + s_yv[ph][u];
+      }
+      const float ss = (s_ss[ph][0] + s_ss[ph][1]) + (s_ss[ph][2] + s_ss[ph][3]), decay = eg[kC - 1];
+      __syncwarp();
       if (lane == 0) {
-        s_ss[tid >> 5] = y;
+        mbar_arrive(&bars.sums_read);
         mbar_arrive(&bars.empty);
       }
-      // dbeta, and dG with its sums from the right, once the work warps' shares are there: two steps a lane of one warp.
-      // (The decays' place is free for the head after the next only when this warp arrives for the next.)
-      if (w == kSumWarp0) ok = ok && wait_warp(&bars.sums, ph, status, 132);
-      if (named_bar_or(kSumBar, 32 * kSumWarps, !ok)) break;
-      if (w == kSumWarp0) {
-        const float* gt = reinterpret_cast<const float*>(smem + oGates) + ph * kGateRows * kC;
-        const float *eg = gt, *be = gt + 2 * kC;
-        const int hv = wk.hv();
-        float dG[2], all = lane < kWorkWarps ? s_e[ph][lane] : 0.f;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int u = 2 * lane + n;
-          const float a0 = (s_a[ph][0][u] + s_a[ph][1][u]) + (s_a[ph][2][u] + s_a[ph][3][u]);
-          const float h = (s_h[ph][0][u] + s_h[ph][1][u]) + (s_h[ph][2][u] + s_h[ph][3][u]);
-          dG[n] = fmaf(be[u], h, a0);
-          if (u < ch.rows) put_gate(out.dbeta, (size_t)(ch.first + u) * d.HV + hv, h + s_yv[u], d.gate_bf16);
-        }
+      for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      const float end = fmaf(decay, ss, all);
+      float sum = dG[0] + dG[1];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        const float end = fmaf(eg[kC - 1], (s_ss[0] + s_ss[1]) + (s_ss[2] + s_ss[3]), all);
-        float sum = dG[0] + dG[1];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float z = __shfl_down_sync(0xffffffffu, sum, o);
-          if (lane + o < 32) sum += z;
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int u = 2 * lane + n;
-          if (u < ch.rows)
-            put_gate(out.dg, (size_t)(ch.first + u) * d.HV + hv, end + (n ? sum - dG[0] : sum), d.gate_bf16);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.sums_read);
+      for (int o = 1; o < 32; o <<= 1) {
+        const float z = __shfl_down_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) sum += z;
       }
-      named_bar(kSumBar, 32 * kSumWarps);  // (s_yv and s_ss are written again)
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const int u = 2 * lane + n;
+        if (u >= ch.rows) continue;
+        put_gate(out.dbeta, (size_t)(ch.first + u) * d.HV + hv, db[n], d.gate_bf16);
+        put_gate(out.dg, (size_t)(ch.first + u) * d.HV + hv, end + (n ? sum - dG[0] : sum), d.gate_bf16);
+      }
     }
   }
   __syncthreads();
