@@ -585,6 +585,26 @@ def _delta_check(key, g, beta, s0, cu_seqlens):
     return lead
 
 
+def _device(first, *others) -> int:
+    """The index of the CUDA device that all tensors of a call are on (None is passed over)."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one CUDA device expected")
+    if dev < 0:
+        raise ValueError(f"tensors on {first.device}: a CUDA device expected")
+    return dev
+
+
+def _on(stream, device):
+    """The context of a call on a stream of the caller's (a torch stream or a ``cudaStream_t``): what the call allocates
+    belongs to that stream, as a workspace that is freed on return has to."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
 def _like(t):
     """An uninitialised dense tensor of t's shape and type."""
     return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
@@ -607,17 +627,21 @@ def delta_forward(cfg: dict, q, k, v, g, beta, s0=None, scale=None, cu_seqlens=N
                   workspace=None):
     """Allocate o and s_final, run ``ssd_delta_forward``; returns (o, s_final).  With ``cu_seqlens`` (int32,
     [batch + 1]) the sequences are packed on one axis of seqlen steps; ``stash`` (``delta_stash``) is filled for
-    ``delta_backward``; scale defaults to key_dim^-1/2."""
+    ``delta_backward``; scale defaults to key_dim^-1/2.  On ``stream``, the outputs belong to it."""
+    if stream is not None:
+        with _on(stream, v.device):
+            return delta_forward(cfg, q, k, v, g, beta, s0, scale, cu_seqlens, stash, None, workspace)
     key = _delta_of(cfg, q, k, v, cu_seqlens is not None)
     prob = _keep(key, lambda: _delta_struct(key))
     _delta_check(key, g, beta, s0, cu_seqlens)
     scale = cfg["key_dim"] ** -0.5 if scale is None else scale
+    at = _device(v, q, k, g, beta, s0, cu_seqlens, stash, workspace and workspace[0])
     dev = v.device
     o = _like(v)
     s_final = torch.empty((key[4], key[7], key[8], key[9]), dtype=torch.float32, device=dev)
     ws, n = workspace if workspace is not None else _delta_workspace(key, False, stash is not None, dev)
     ssd_delta_forward(prob, q, k, v, g, beta, s0, cu_seqlens, scale, o, s_final, stash,
-                      0 if stash is None else stash.numel(), ws, n, _stream(stream, dev.index))
+                      0 if stash is None else stash.numel(), ws, n, _stream(None, at))
     return o, s_final
 
 
@@ -625,6 +649,9 @@ def delta_backward(cfg: dict, dout, q, k, v, g, beta, ds_final=None, s0=None, sc
                    stream=None, workspace=None):
     """Allocate the gradients and run ``ssd_delta_backward``; returns dq, dk, dv, dg, dbeta and ds0 (None where s0 is
     None).  ``stash``: what ``delta_forward`` filled on the same inputs; without it the chunk states are made again."""
+    if stream is not None:
+        with _on(stream, v.device):
+            return delta_backward(cfg, dout, q, k, v, g, beta, ds_final, s0, scale, cu_seqlens, stash, None, workspace)
     key = _delta_of(cfg, q, k, v, cu_seqlens is not None)
     prob = _keep(key, lambda: _delta_struct(key))
     lead = _delta_check(key, g, beta, s0, cu_seqlens)
@@ -632,19 +659,23 @@ def delta_backward(cfg: dict, dout, q, k, v, g, beta, ds_final=None, s0=None, sc
     if ds_final is not None:
         _dense("ds_final", ds_final, (key[4], key[7], key[8], key[9]), torch.float32)
     scale = cfg["key_dim"] ** -0.5 if scale is None else scale
+    at = _device(v, q, k, g, beta, dout, ds_final, s0, cu_seqlens, stash, workspace and workspace[0])
     dev = v.device
     out = {"dq": _like(q), "dk": _like(k), "dv": _like(v), "dg": _like(g), "dbeta": _like(beta),
            "ds0": None if s0 is None else _like(s0)}
     ws, n = workspace if workspace is not None else _delta_workspace(key, True, stash is not None, dev)
     ssd_delta_backward(prob, dout, ds_final, q, k, v, g, beta, s0, cu_seqlens, scale, out["dq"], out["dk"], out["dv"],
                        out["dg"], out["dbeta"], out["ds0"], stash, 0 if stash is None else stash.numel(), ws, n,
-                       _stream(stream, dev.index))
+                       _stream(None, at))
     return out
 
 
 def delta_step(cfg: dict, q, k, v, g, beta, state, slots=None, scale=None, stream=None):
     """Allocate o and run ``ssd_delta_step``: seqlen steps of each sequence on its slot of ``state`` [slots, HV, K, V]
     (fp32), which is updated in place; returns o."""
+    if stream is not None:
+        with _on(stream, v.device):
+            return delta_step(cfg, q, k, v, g, beta, state, slots, scale)
     key = _delta_of(cfg, q, k, v, False)
     prob = _keep(key, lambda: _delta_struct(key))
     _delta_check(key, g, beta, None, None)
@@ -652,8 +683,9 @@ def delta_step(cfg: dict, q, k, v, g, beta, state, slots=None, scale=None, strea
     _dense("state", state, (ns, key[7], key[8], key[9]), torch.float32)
     _dense("slots", slots, (key[4],), torch.int32)
     scale = cfg["key_dim"] ** -0.5 if scale is None else scale
+    at = _device(v, q, k, g, beta, state, slots)
     o = _like(v)
-    ssd_delta_step(prob, q, k, v, g, beta, state, slots, ns, scale, o, _stream(stream, v.device.index))
+    ssd_delta_step(prob, q, k, v, g, beta, state, slots, ns, scale, o, _stream(None, at))
     return o
 
 
@@ -710,23 +742,30 @@ def ssd_norm_backward(prob, dy, x, mean, rstd, weight, dx, dw, db, ws, ws_bytes,
 def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stream=None):
     """Layer norm of x [.., D]; weight and bias [D] (either may be None) of one type.  Returns y (contiguous), mean and
     rstd (fp32, one per row)."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return norm_forward(x, weight, bias, eps)
     key = _norm_of(x, weight if weight is not None else bias)
     prob = _keep(key, lambda: _norm_struct(key))
     if weight is not None:
         _dense("weight", weight, (key[3],), key[1])
     if bias is not None:
         _dense("bias", bias, (key[3],), key[1])
+    at = _device(x, weight, bias)
     y = _like(x)
     dev = x.device
     mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
     rstd = torch.empty_like(mean)
-    ssd_norm_forward(prob, x, weight, bias, eps, y, mean, rstd, _stream(stream, dev.index))
+    ssd_norm_forward(prob, x, weight, bias, eps, y, mean, rstd, _stream(None, at))
     return y, mean, rstd
 
 
 def norm_backward(dy, x, mean, rstd, weight=None, stream=None, workspace=None):
     """The gradients of ``norm_forward``: dx (contiguous), and dw and db in the weight's type (fp32 without a
     weight)."""
+    if stream is not None:
+        with _on(stream, x.device):
+            return norm_backward(dy, x, mean, rstd, weight, None, workspace)
     key = _norm_of(x, weight)
     prob = _keep(key, lambda: _norm_struct(key))
     if dy.dtype != x.dtype or dy.shape != x.shape or not dy.is_contiguous():
@@ -736,6 +775,7 @@ def norm_backward(dy, x, mean, rstd, weight=None, stream=None, workspace=None):
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t.dtype != torch.float32 or t.numel() != key[2] or not t.is_contiguous():
             raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected contiguous float32, one per row")
+    at = _device(x, dy, mean, rstd, weight, workspace and workspace[0])
     dx = _like(x)
     dev = x.device
     dw, db = torch.empty(key[3], dtype=key[1], device=dev), torch.empty(key[3], dtype=key[1], device=dev)
@@ -743,5 +783,5 @@ def norm_backward(dy, x, mean, rstd, weight=None, stream=None, workspace=None):
         n = _keep(key + ("ws",), lambda: ssd_norm_workspace_size(prob))
         workspace = torch.empty(n, dtype=torch.uint8, device=dev), n
     ssd_norm_backward(prob, dy, x, mean, rstd, weight, dx, dw, db, workspace[0], workspace[1],
-                      _stream(stream, dev.index))
+                      _stream(None, at))
     return {"dx": dx, "dw": dw, "db": db}

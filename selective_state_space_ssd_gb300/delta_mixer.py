@@ -79,7 +79,7 @@ class DeltaMixer:
         q, k, v, a, b = (h @ self.p["w_in"].T).split(self.parts, dim=-1)
         unit = lambda x: torch.nn.functional.normalize(x.unflatten(-1, (self.h, self.kd)).float(), dim=-1).to(x.dtype)  # noqa: E731
         g = -torch.exp(self.p["log_a"]) * torch.nn.functional.softplus(a.float() + self.p["dt_bias"])
-        return unit(q), unit(k), v.unflatten(-1, (self.hv, self.vd)), g, torch.sigmoid(b.float())
+        return unit(q), unit(k), v.unflatten(-1, (self.hv, self.vd)), g.contiguous(), torch.sigmoid(b.float()).contiguous()
 
     def output(self, x, o, norm):
         o = norm(o, self.p["head_w"], self.p["head_b"], 1e-5)
@@ -99,7 +99,7 @@ class DeltaMixer:
         norm = lambda *a: binding.norm_forward(*a)[0]  # noqa: E731
         h = norm(x, self.p["norm_w"], self.p["norm_b"], 1e-5)
         q, k, v, g, beta = self.inputs(h[None])
-        o, final = binding.delta_forward(self.cfg(slots.numel(), x.shape[0]), q, k, v, g.contiguous(), beta.contiguous(),
+        o, final = binding.delta_forward(self.cfg(slots.numel(), x.shape[0]), q, k, v, g, beta,
                                          cu_seqlens=cu_seqlens)  # (v as the projection left it: a slice of wider rows)
         state[slots.long()] = final
         return self.output(x, o[0], norm)
@@ -110,7 +110,7 @@ class DeltaMixer:
         norm = lambda *a: binding.norm_forward(*a)[0]  # noqa: E731
         h = norm(x, self.p["norm_w"], self.p["norm_b"], 1e-5)
         q, k, v, g, beta = self.inputs(h)
-        o = binding.delta_step(self.cfg(x.shape[0], x.shape[1]), q, k, v, g.contiguous(), beta.contiguous(), state, slots)
+        o = binding.delta_step(self.cfg(x.shape[0], x.shape[1]), q, k, v, g, beta, state, slots)
         return self.output(x, o, norm)
 
 

@@ -1,0 +1,75 @@
+"""Calls on a stream of the caller's: what a call allocates and frees must not be handed to the current stream's work while
+the kernels on the other stream still use it.  And tensors that are not on one CUDA device are refused."""
+import pytest
+import torch
+
+from selective_state_space_ssd_gb300 import binding
+from selective_state_space_ssd_gb300.configs import DELTA_CONFIGS
+
+pytestmark = pytest.mark.gpu
+CFG = dict(DELTA_CONFIGS["delta_bf16"], batch=1, seqlen=200, nheads=2, value_heads=4, key_dim=64, value_dim=64)
+
+
+def tensors(device="cuda"):
+    gen = torch.Generator().manual_seed(7)
+    rn = lambda *s: torch.randn(s, generator=gen)  # noqa: E731
+    x = dict(q=rn(1, 200, 2, 64) / 8, k=rn(1, 200, 2, 64) / 8, v=rn(1, 200, 4, 64), dout=rn(1, 200, 4, 64))
+    x = {n: t.to(torch.bfloat16) for n, t in x.items()}
+    x.update(g=-torch.rand((1, 200, 4), generator=gen), beta=torch.rand((1, 200, 4), generator=gen))
+    return {n: t.to(device) for n, t in x.items()}
+
+
+def calls(x):
+    ins = tuple(x[n] for n in ("q", "k", "v", "g", "beta"))
+    rows = x["v"].reshape(-1, 64)
+    w = torch.ones(64, device="cuda")
+    _, mean, rstd = binding.norm_forward(rows, w, w)
+    torch.cuda.synchronize()
+    return {"delta_forward": lambda s: binding.delta_forward(CFG, *ins, stream=s),
+            "delta_backward": lambda s: tuple(t for t in binding.delta_backward(CFG, x["dout"], *ins, stream=s).values()
+                                              if t is not None),
+            "norm_forward": lambda s: binding.norm_forward(rows, w, w, stream=s),
+            "norm_backward": lambda s: tuple(binding.norm_backward(rows, rows, mean, rstd, w, stream=s).values())}
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", ["delta_forward", "delta_backward", "norm_forward", "norm_backward"])
+def test_call_on_another_stream(name, raw):
+    call = calls(tensors())[name]
+    want = call(None)
+    side = torch.cuda.Stream()
+    call(side)  # the first use of the stream and its memory
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some ten milliseconds
+    got = call(side.cuda_stream if raw else side)
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (1 << 9, 1 << 14, 1 << 18, 1 << 20, 3 << 20)
+            for _ in range(8)]  # the current stream's work meanwhile, on memory that is free there
+    torch.cuda.synchronize()
+    assert len(junk) == 40 and torch.cuda.current_stream() != side
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_tensors_off_the_device_are_refused():
+    x, host = tensors(), tensors("cpu")
+    names = ("q", "k", "v", "g", "beta")
+    for n in names:
+        with pytest.raises(ValueError):
+            binding.delta_forward(CFG, *(host[m] if m == n else x[m] for m in names))
+        with pytest.raises(ValueError):
+            binding.delta_step(CFG, *(host[m] if m == n else x[m] for m in names), torch.zeros((1, 4, 64, 64), device="cuda"))
+    with pytest.raises(ValueError):
+        binding.delta_forward(CFG, *(host[m] for m in names))
+    with pytest.raises(ValueError):
+        binding.delta_backward(CFG, host["dout"], *(x[m] for m in names))
+    with pytest.raises(ValueError):
+        binding.delta_step(CFG, *(x[m] for m in names), torch.zeros((1, 4, 64, 64)))
+    rows = x["v"].reshape(-1, 64)
+    with pytest.raises(ValueError):
+        binding.norm_forward(rows.cpu())
+    with pytest.raises(ValueError):
+        binding.norm_forward(rows, torch.ones(64))
+    y, mean, rstd = binding.norm_forward(rows)
+    with pytest.raises(ValueError):
+        binding.norm_backward(y, rows, mean.cpu(), rstd)
