@@ -73,3 +73,24 @@ def test_tensors_off_the_device_are_refused():
     y, mean, rstd = binding.norm_forward(rows)
     with pytest.raises(ValueError):
         binding.norm_backward(y, rows, mean.cpu(), rstd)
+
+
+@pytest.mark.parametrize("name", ["delta_forward", "delta_backward", "norm_backward"])
+def test_workspace_stays_with_the_callers_stream(name, monkeypatch):
+    """While the other stream is busy, the current stream is not given the block that the call took as its workspace."""
+    call, taken = calls(tensors())[name], []
+    launch = getattr(binding, "ssd_" + name)
+
+    def spy(*args):
+        taken.append((args[-3].data_ptr(), args[-3].numel()))
+        launch(*args)
+
+    monkeypatch.setattr(binding, "ssd_" + name, spy)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    call(side)
+    at, n = taken[0]
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(not (b.data_ptr() < at + n and at < b.data_ptr() + n) for b in blocks)
