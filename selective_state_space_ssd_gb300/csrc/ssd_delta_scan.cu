@@ -911,13 +911,16 @@ cudaError_t make_maps(const Dims& d, const In& in, const bf16* v, long long vstr
 }
 
 // S_in of the runs of a split scan: S_in of run 1 is there (the first run's result), S_in of run i + 1 is M_i S_in_i + B_i
-// in the place of B_i.  A block per (sequence, value head) and 16 columns; a thread four rows and two columns.  fp32; the
-// next map's copy is in flight while a product is computed.
+// in the place of B_i.  A block per (sequence, value head) and 16 columns; a thread two columns of every 32nd row.  fp32; the
+// next map's copy is in flight while a product is computed.  16 heads of 128 x 128 at 16384 steps: 28.5 us, bound by the
+// latency of its steps (33 us with four neighbouring rows a thread, whose reads meet half of the banks; 31 us with the keys
+// summed by two halves of twice the threads).
 constexpr int kMapPitch = 132, kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) k_delta_join(Split sp, int K, int KP, int V) {
+template <int KP>
+__global__ void __launch_bounds__(kJoinThreads) k_delta_join(Split sp, int K, int V) {
   extern __shared__ __align__(16) float sm[];  // two maps [KP][kMapPitch], the state's columns [KP][16]
   float* cols = sm + 2 * KP * kMapPitch;
-  const int tid = threadIdx.x, r0 = 4 * (tid >> 3), c0 = 2 * (tid & 7), v0 = blockIdx.y * 16 + c0;
+  const int tid = threadIdx.x, r0 = tid >> 3, c0 = 2 * (tid & 7), v0 = blockIdx.y * 16 + c0;
   float* st = sp.states + (size_t)blockIdx.x * (sp.parts - 1) * K * V;
   const float* maps = sp.maps + (size_t)blockIdx.x * (sp.parts - 2) * KP * KP;
   const auto fetch = [&](int i) {
@@ -929,21 +932,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(Split sp, int K, in
     }
     cp_commit();
   };
-  const bool on = r0 < KP;
   const auto mine = [&](const float* p, float (&x)[4][2]) {  // this thread's part of a state
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) x[a][b] = on && r0 + a < K && v0 + b < V ? p[(size_t)(r0 + a) * V + v0 + b] : 0.f;
+      for (int b = 0; b < 2; ++b) x[a][b] = r0 + 32 * a < K && v0 + b < V ? p[(size_t)(r0 + 32 * a) * V + v0 + b] : 0.f;
   };
   float x[4][2];
   fetch(1);
   mine(st, x);
   for (int i = 1; i < sp.parts - 1; ++i) {
     float* out = st + (size_t)i * K * V;
-    if (on)
 #pragma unroll
-      for (int a = 0; a < 4; ++a) *reinterpret_cast<float2*>(cols + (r0 + a) * 16 + c0) = make_float2(x[a][0], x[a][1]);
+    for (int a = 0; a < 4; ++a)
+      if (32 * a < KP) *reinterpret_cast<float2*>(cols + (r0 + 32 * a) * 16 + c0) = make_float2(x[a][0], x[a][1]);
     mine(out, x);
     if (i + 1 < sp.parts - 1)
       fetch(i + 1);
@@ -951,7 +953,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(Split sp, int K, in
       cp_commit();
     cp_wait<1>();
     __syncthreads();
-    if (on) {
+    {
       const float* m = sm + (i & 1) * KP * kMapPitch + r0 * kMapPitch;
 #pragma unroll 4
       for (int k = 0; k < KP; k += 4) {
@@ -960,7 +962,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(Split sp, int K, in
         for (int e = 0; e < 4; ++e) s[e] = *reinterpret_cast<const float2*>(cols + (k + e) * 16 + c0);
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
-          const float4 y = *reinterpret_cast<const float4*>(m + a * kMapPitch + k);
+          if (32 * a >= KP) break;
+          const float4 y = *reinterpret_cast<const float4*>(m + 32 * a * kMapPitch + k);
           const float ya[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) fma2(x[a][0], x[a][1], ya[e], ya[e], s[e].x, s[e].y, x[a][0], x[a][1]);
@@ -970,19 +973,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_delta_join(Split sp, int K, in
       for (int a = 0; a < 4; ++a)
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-          if (r0 + a < K && v0 + b < V) out[(size_t)(r0 + a) * V + v0 + b] = x[a][b];
+          if (r0 + 32 * a < K && v0 + b < V) out[(size_t)(r0 + 32 * a) * V + v0 + b] = x[a][b];
     }
     __syncthreads();
   }
 }
 
+template <int KP>
 cudaError_t join(const Dims& d, const Split& split, cudaStream_t st) {
   if (split.parts <= 2) return cudaSuccess;
-  const uint32_t smem = 4 * (uint32_t)(2 * d.KP * kMapPitch + 16 * d.KP);
-  const cudaError_t e = allow_smem(k_delta_join, smem);
+  const uint32_t smem = 4 * (uint32_t)(2 * KP * kMapPitch + 16 * KP);
+  const cudaError_t e = allow_smem(k_delta_join<KP>, smem);
   if (e != cudaSuccess) return e;
   SSD_LAUNCH("k_delta_join", st,
-             k_delta_join<<<dim3((unsigned)(d.N * d.HV), (unsigned)((d.V + 15) / 16)), kJoinThreads, smem, st>>>(split, d.K, d.KP, d.V));
+             k_delta_join<KP><<<dim3((unsigned)(d.N * d.HV), (unsigned)((d.V + 15) / 16)), kJoinThreads, smem, st>>>(split, d.K, d.V));
   return cudaGetLastError();
 }
 
@@ -998,7 +1002,7 @@ cudaError_t run_scan(const Dims& d, const Table& tb, const In& in, const uint8_t
     SSD_LAUNCH("k_delta_maps", st,
                k_delta_scan<KP><<<units * (2 * split.parts - 3), kThreads, scan_smem<KP>(), st>>>(
                    d, tb, in, maps, records, split, true, nullptr, nullptr, nullptr, nullptr, status));
-    if ((e = join(d, split, st)) != cudaSuccess) return e;
+    if ((e = join<KP>(d, split, st)) != cudaSuccess) return e;
   }
   SSD_LAUNCH("k_delta_scan", st,
              k_delta_scan<KP><<<units * split.parts, kThreads, scan_smem<KP>(), st>>>(
@@ -1018,7 +1022,7 @@ cudaError_t run_rev(const Dims& d, const Table& tb, const In& in, const uint8_t*
     SSD_LAUNCH("k_delta_rev_maps", st,
                k_delta_rev<KP><<<units * (2 * split.parts - 3), kThreads, scan_smem<KP>(), st>>>(
                    d, tb, in, maps, records, split, true, dout, ds_final, nullptr, nullptr, nullptr, nullptr, status));
-    if ((e = join(d, split, st)) != cudaSuccess) return e;
+    if ((e = join<KP>(d, split, st)) != cudaSuccess) return e;
   }
   SSD_LAUNCH("k_delta_rev", st,
              k_delta_rev<KP><<<units * split.parts, kThreads, scan_smem<KP>(), st>>>(
