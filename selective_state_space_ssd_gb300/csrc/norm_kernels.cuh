@@ -6,7 +6,7 @@
 // differences to the mean, in a second pass over the registers), sums are fp32.  The backward's blocks each take every
 // n-th row and keep their columns' dw and db in registers; one row of partial sums a block goes to the workspace and
 // k_norm_columns adds those in block order, so the result does not depend on timing.  Measured: 16384 rows of 2560 bf16
-// values with fp32 weights 44 us forward and 64 us backward (3.8 and 4.0 TB/s), 8 us for k_norm_columns; 262144 rows of
+// values with fp32 weights 45 us forward and 59 us backward (3.7 and 4.3 TB/s), 8 us for k_norm_columns; 262144 rows of
 // 128 30 us (4.5 TB/s).
 #pragma once
 
@@ -181,6 +181,35 @@ constexpr int blocks_per_sm() {
   return n < 1 ? 1 : n;
 }
 
+// Backward, rows of x and dy that are on their way to shared memory at a time: as many as 40 KB a block take, four at most (0:
+// one row, in registers).  A thread copies the 16-byte pieces that it reads itself, so no barrier stands between.  16384
+// rows of 2560: 59 us, with the next row in registers 64; forward the same took 49 us in place of 45, so there the next
+// row stays in registers.
+template <typename T, int TPR, int E, bool kVec>
+constexpr int ring_stages() {
+  const int n = 40960 / (block_threads<TPR>() * E * (int)sizeof(T) * 2);
+  return !kVec ? 0 : n < 4 ? n : 4;
+}
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
+  const int n = ok ? 16 : 0;  // 0: zeros, and nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void copies_wait() {  // all but the last kN groups have arrived
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+template <typename R, int kT, typename T>
+__device__ __forceinline__ void copy_row(uint4* slot, const T* p, bool live, int D, int t) {
+#pragma unroll
+  for (int i = 0; i < R::NP; ++i) {
+    const bool ok = live && R::in(i, D, t);
+    copy16(slot + i * kT, ok ? p + R::col(i, t) : p, ok);
+  }
+}
+
 // The groups of a block take every n-th row each; a group's next row is on its way while it sums the one before.
 template <typename T, int TPR, int E, bool kVec>
 __global__ void __launch_bounds__(block_threads<TPR>(), blocks_per_sm<T, TPR, E, kVec, false>())
@@ -239,30 +268,54 @@ __global__ void __launch_bounds__(block_threads<TPR>(), blocks_per_sm<T, TPR, E,
   using R = Row<T, TPR, E, kVec>;
   constexpr int kGroups = block_threads<TPR>() / TPR;
   __shared__ float red[kGroups][2 * ((TPR + 31) / 32)];
-  __shared__ float s_part[kGroups > 1 ? TPR * E : 1];
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   float dw[E], db[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.f;
   const float inv = 1.f / (float)a.D;
   const long long step = (long long)gridDim.x * kGroups;
+  constexpr int kS = ring_stages<T, TPR, E, kVec>(), kT = block_threads<TPR>();
+  __shared__ uint4 ring[kS ? 2 * kS * R::NP * kT : kGroups > 1 ? TPR * E / 4 : 1];
   typename R::Piece nx[R::NP], ng[R::NP];
   float nm = 0.f, nr = 0.f;
+  int slot = 0;
   const auto fetch = [&](long long row) {
     const bool live = row < a.rows;
-    R::fetch(x + (live ? row : 0) * a.xs, live ? a.D : 0, t, nx);
-    R::fetch(dy + (live ? row : 0) * (long long)a.D, live ? a.D : 0, t, ng);
-    nm = live ? mean[row] : 0.f;
-    nr = live ? rstd[row] : 0.f;
+    const T *px = x + (live ? row : 0) * a.xs, *pg = dy + (live ? row : 0) * (long long)a.D;
+    if constexpr (kS > 0) {
+      uint4* to = ring + 2 * slot * R::NP * kT + threadIdx.x;
+      copy_row<R, kT>(to, px, live, a.D, t);
+      copy_row<R, kT>(to + R::NP * kT, pg, live, a.D, t);
+      copies_commit();
+      slot = slot + 1 == kS ? 0 : slot + 1;
+    } else {
+      R::fetch(px, live ? a.D : 0, t, nx);
+      R::fetch(pg, live ? a.D : 0, t, ng);
+    }
+  };
+  const auto stats = [&](long long row) {
+    nm = row < a.rows ? mean[row] : 0.f;
+    nr = row < a.rows ? rstd[row] : 0.f;
   };
   long long row = (long long)blockIdx.x * kGroups + grp;
-  fetch(row);
+  for (int i = 0; i < (kS ? kS : 1); ++i) fetch(row + i * step);
+  stats(row);
   for (long long first = (long long)blockIdx.x * kGroups; first < a.rows; first += step, row += step) {
     float h[E], g[E];
+    if constexpr (kS > 0) {
+      copies_wait<(kS ? kS - 1 : 0)>();
+      const uint4* from = ring + 2 * slot * R::NP * kT + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < R::NP; ++i) {
+        nx[i] = from[i * kT];
+        ng[i] = from[(R::NP + i) * kT];
+      }
+    }
     R::unpack(nx, h);
     R::unpack(ng, g);
     const float m = nm, r = nr;
-    fetch(row + step);
+    stats(row + step);
+    if (kS == 0) fetch(row + step);
     float s[2] = {0.f, 0.f};
     float wt[E];
     R::weights(w, a.wbf16, a.D, t, wt, 1.f);
@@ -277,14 +330,17 @@ __global__ void __launch_bounds__(block_threads<TPR>(), blocks_per_sm<T, TPR, E,
       s[1] = fmaf(g[e], h[e], s[1]);
     }
     row_sum<TPR, 2>(s, red[grp], t);
+    if (kS > 0) fetch(row + kS * step);  // (what the slot held has been summed)
     const float s0 = s[0] * inv, s1 = s[1] * inv;
     const float a0 = -r * s0, a1 = -r * s1;
 #pragma unroll
     for (int e = 0; e < E; ++e) g[e] = fmaf(r, g[e], fmaf(a1, h[e], a0));
     if (row < a.rows) R::store(dx + (size_t)row * a.D, a.D, t, g);
   }
+  if constexpr (kS > 0) copies_wait<0>();
   if (!part) return;
-  // this block's sums: its groups in order
+  // this block's sums: its groups in order, over the ring
+  float* s_part = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     float(&acc)[E] = which ? db : dw;
