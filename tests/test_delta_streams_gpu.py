@@ -94,3 +94,58 @@ def test_workspace_stays_with_the_callers_stream(name, monkeypatch):
     blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
     torch.cuda.synchronize()
     assert all(not (b.data_ptr() < at + n and at < b.data_ptr() + n) for b in blocks)
+
+
+def test_calls_in_a_graph():
+    """A server's step and its norm captured once and replayed: the state moves on with every replay."""
+    x = tensors()
+    step = dict(CFG, seqlen=1, batch=3)
+    q, k, v = (torch.empty((3, 1) + x[n].shape[2:], dtype=torch.bfloat16, device="cuda") for n in ("q", "k", "v"))
+    g, beta = (torch.empty((3, 1, 4), device="cuda") for _ in range(2))
+    state, w = torch.zeros((3, 4, 64, 64), device="cuda"), torch.ones(64, device="cuda")
+
+    def at(t):
+        for buf, n in ((q, "q"), (k, "k"), (v, "v"), (g, "g"), (beta, "beta")):
+            buf.copy_(x[n][0, 3 * t:3 * t + 3][:, None])
+
+    def run():
+        return binding.norm_forward(binding.delta_step(step, q, k, v, g, beta, state), w, w)[0]
+
+    want, expect = state.clone(), []
+    at(0)
+    run()  # (the first call of a size loads its kernels)
+    state.zero_()
+    for t in range(5):
+        at(t)
+        expect.append(run())
+    want.copy_(state)
+    state.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run()
+    state.zero_()
+    for t in range(5):
+        at(t)
+        graph.replay()
+        assert torch.equal(y, expect[t])
+    assert torch.equal(state, want)
+
+
+def test_training_step_in_a_graph():
+    x = tensors()
+    ins = tuple(x[n] for n in ("q", "k", "v", "g", "beta"))
+    stash = binding.delta_stash(CFG)
+
+    def run():
+        o, sf = binding.delta_forward(CFG, *ins, stash=stash)
+        return (o, sf) + tuple(t for t in binding.delta_backward(CFG, x["dout"], *ins, stash=stash).values() if t is not None)
+
+    want = [t.clone() for t in run()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(2):
+        for t in got:
+            t.fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
