@@ -31,8 +31,10 @@ struct Dims {
 // Where the sequences lie: sequence n has its steps at start[n] .. start[n] + len[n] - 1 of the token axis and its
 // chunks at chunk[n] .. chunk[n + 1] - 1 of the chunk axis.  Filled from cu_seqlens for a packed batch; computed
 // where it is read otherwise.
+constexpr int kRanked = 1024;  // a packed batch of more sequences keeps their order: its many blocks even out by themselves
 struct Table {
   int *start, *len, *chunk;
+  int* order;  // the sequences, those with the most chunks first (up to kRanked of them)
 };
 
 // One record per (chunk, value head), item = chunk * HV + head, in one piece of memory that one bulk copy brings in:

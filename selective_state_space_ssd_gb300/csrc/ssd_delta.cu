@@ -32,7 +32,7 @@ namespace delta {
 namespace {
 
 // ---------------------------------------------------------------- packed sequences
-// cu_seqlens -> start, length and first chunk of every sequence.  One block.  Bounds that leave the token axis or
+// cu_seqlens -> start, length and first chunk of every sequence, and their order by length.  One block.  Bounds that leave the token axis or
 // run backwards are pulled in (a running maximum), so no later kernel can leave its buffers whatever the values are.
 __global__ void __launch_bounds__(1024) k_delta_table(const int* __restrict__ cu, int N, int T, Table tb) {
   __shared__ int s_max[1024], s_sum[1024];
@@ -70,6 +70,13 @@ __global__ void __launch_bounds__(1024) k_delta_table(const int* __restrict__ cu
       tb.chunk[n] = carry_chunk + s_sum[tid] - nc;
     }
     __syncthreads();
+    if (N <= kRanked) {  // (one pass of this loop)
+      s_max[tid] = nc;
+      __syncthreads();
+      int rank = 0;
+      for (int m = 0; m < N; ++m) rank += s_max[m] > nc || (s_max[m] == nc && m < n);
+      if (n < N) tb.order[rank] = n;
+    }
     if (tid == 1023) {
       carry_end = end;
       carry_chunk += s_sum[tid];
@@ -346,11 +353,12 @@ Kept carve_kept(const Dims& d, Carver& cv) {
   return k;
 }
 Table carve_table(const Dims& d, Carver& cv) {
-  Table t = {nullptr, nullptr, nullptr};
+  Table t = {nullptr, nullptr, nullptr, nullptr};
   if (d.packed) {
     t.start = cv.take<int>(d.N);
     t.len = cv.take<int>(d.N);
     t.chunk = cv.take<int>((size_t)d.N + 1);
+    t.order = cv.take<int>(d.N);
   }
   return t;
 }

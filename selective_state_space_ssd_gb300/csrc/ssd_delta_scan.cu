@@ -147,6 +147,13 @@ struct Block {
   Seq sq;
   size_t unit, su;  // sequence and value head; its state's offset
 };
+// The (sequence, value head) of a place in the grid.  Packed: the longest sequences first, so that what runs last is
+// short: 24 sequences of 20011 steps and 32 heads of 128 x 96 take 222 us, in their own order 253.
+__device__ __forceinline__ int unit_of(const Dims& d, const Table& tb, int place) {
+  if (!d.packed || d.N > kRanked) return place;
+  const int n = place / d.HV;
+  return tb.order[n] * d.HV + (place - n * d.HV);
+}
 __device__ __forceinline__ Block block_of(const Dims& d, const Table& tb, int unit) {
   Block b;
   const int n = unit / d.HV;
@@ -314,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     init_bars(&bars);
-    const int per_unit = first_pass ? 2 * sp.parts - 3 : sp.parts, unit = blockIdx.x / per_unit, r = blockIdx.x - unit * per_unit;
-    s_blk = block_of(d, tb, unit);
+    const int per_unit = first_pass ? 2 * sp.parts - 3 : sp.parts, place = blockIdx.x / per_unit, r = blockIdx.x - place * per_unit;
+    s_blk = block_of(d, tb, unit_of(d, tb, place));
     s_run = run_of(d, sp, s_blk, first_pass ? (r + 1) >> 1 : r, false, first_pass && r > 0 && !(r & 1), first_pass,
                            in.s0, s_final);
   }
@@ -620,8 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     init_bars(&bars);
-    const int per_unit = first_pass ? 2 * sp.parts - 3 : sp.parts, unit = blockIdx.x / per_unit, r = blockIdx.x - unit * per_unit;
-    s_blk = block_of(d, tb, unit);
+    const int per_unit = first_pass ? 2 * sp.parts - 3 : sp.parts, place = blockIdx.x / per_unit, r = blockIdx.x - place * per_unit;
+    s_blk = block_of(d, tb, unit_of(d, tb, place));
     s_run = run_of(d, sp, s_blk, first_pass ? (r + 1) >> 1 : r, true, first_pass && r > 0 && !(r & 1), first_pass,
                            ds_final, ds0);
   }

@@ -143,6 +143,21 @@ def test_long_packed_sequences_match_the_oracle():
         check(part, ref, {**TOL_F, **TOL_B})
 
 
+def test_more_sequences_than_are_ranked():
+    """Up to 1024 packed sequences are taken by length, more in their order: the same results bit for bit."""
+    lengths = [(7 * i) % 5 + 70 * (i % 11 == 3) for i in range(1300)]
+    cfg = cfg_of(b=1300, T=sum(lengths), H=1, HV=2, K=16, V=16)
+    dev = cuda(make(cfg, 17, packed=True))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32)
+    got = run(cfg, dev, cu=cu.cuda())
+    for a, b in ((0, 1024), (900, 1300)):
+        t0, t1 = int(cu[a]), int(cu[b])
+        part = {k: (x[a:b] if k in ("s0", "ds_final") else x[:, t0:t1]).contiguous() for k, x in dev.items()}
+        alone = run(dict(cfg, batch=b - a, seqlen=t1 - t0), part, cu=(cu[a:b + 1] - t0).cuda())
+        for k, x in alone.items():
+            assert torch.equal(x, got[k][a:b] if k in ("s_final", "ds0") else got[k][:, t0:t1]), k
+
+
 @pytest.mark.parametrize("name", sorted(CASES))
 def test_matches_the_oracle(name):
     cfg = CASES[name]
