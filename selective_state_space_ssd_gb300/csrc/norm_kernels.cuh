@@ -172,8 +172,8 @@ template <int TPR>
 constexpr int block_threads() {
   return TPR < 128 ? 128 : TPR;
 }
-// Blocks an SM, by their registers: an element backward takes four values (h, the gradient, dw, db) and its two in the
-// next row as they lie in memory, one to four bytes each; forward three in all.
+// Blocks an SM, by their registers: an element backward takes four values (h, the gradient, dw, db) and its two as
+// they lie in memory, two or four bytes each; forward three in all, the next row's among them.
 template <typename T, int TPR, int E, bool kVec, bool kBack>
 constexpr int blocks_per_sm() {
   const int regs = kBack ? (kVec && sizeof(T) == 2 ? 5 : 6) * E + 48 : 3 * E + 40;
