@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars.full, kLoadWarps + 1);
     mbar_init(&bars.states, 1);
     mbar_init(&bars.empty, 1 + kSumWarps + kWorkWarps + 1);
-    mbar_init(&bars.tail, 1);
+    mbar_init(&bars.tail, kLoadWarps + 1);
     mbar_init(&bars.m, 1);
     mbar_init(&bars.z, 1);
     mbar_init(&bars.b, kWorkWarps);
@@ -393,6 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x - 32 * kLoadWarp0;
     uint32_t tails = 0;
     bool ok = true;
+    // The copies of a cut chunk have arrived.  Each copy warp arrives here as well, so that a phase cannot end, and the next
+    // one neither, before both warps have come to wait for it.
+    const auto wait_tail = [&](int code) {
+      if (lane == 0) mbar_arrive(&bars.tail);
+      return wait_warp(&bars.tail, tails++ & 1, status, code);
+    };
     int loaded = -1, units = -1;
     const int na = d.KP / 64, va = (d.VP + 63) / 64;
     for (; wk.more() && ok; wk.next()) {
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!d.ovec)
         load_elements(smem + oOY, 128, 64 * va, dout + ((long long)first * d.HV + wk.hv()) * d.V, (long long)d.HV * d.V, rows, d.V, tid);
       if (cut) {
-        ok = wait_warp(&bars.tail, tails++ & 1, status, 124);
+        ok = wait_tail(124);
         if (d.ovec) zero_rows(smem + oOY, 128, va, rows, tid);
       }
       fence_proxy_async();
@@ -440,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!d.qvec) load_elements(qt, 128, d.KP, in.q + (long long)first * d.qs + (long long)wk.hk * d.K, d.qs, rows, d.K, tid);
         if (!d.kvec) load_elements(qt + kC * 128, 128, d.KP, in.k + (long long)first * d.ks + (long long)wk.hk * d.K, d.ks, rows, d.K, tid);
         if (cut) {
-          ok = wait_warp(&bars.tail, tails++ & 1, status, 122);
+          ok = wait_tail(122) && ok;
           if (d.qvec) zero_rows(qt, 128, na, rows, tid);
           if (d.kvec) zero_rows(qt + kC * 128, 128, na, rows, tid);
         }
