@@ -586,13 +586,17 @@ def _delta_check(key, g, beta, s0, cu_seqlens):
 
 
 def _device(first, *others) -> int:
-    """The index of the CUDA device that all tensors of a call are on (None is passed over)."""
+    """The index of the CUDA device that all tensors of a call are on (None is passed over).  It has to be the current
+    one: the library launches there, whatever device a stream's handle or a pointer belongs to."""
     dev = first.get_device()
     for t in others:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"tensors on {first.device} and {t.device}: one CUDA device expected")
     if dev < 0:
         raise ValueError(f"tensors on {first.device}: a CUDA device expected")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on {first.device}, but the current device (or that of the stream given) is "
+                         f"cuda:{torch.cuda.current_device()}: make theirs current first")
     return dev
 
 
