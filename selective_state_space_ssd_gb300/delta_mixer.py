@@ -19,6 +19,24 @@ import torch
 from . import binding
 
 
+class FirstOrder(torch.autograd.Function):
+    """Hands on the first `n` tensors, gradients that the library's kernels computed out of the others, and raises where
+    they would be differentiated in their turn: taken for constants, they would drop terms without a word."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the library's gradients have no second derivative")
+
+
+def first_order(grads, *of):
+    """`grads` as a backward function returns them; a graph of them (create_graph) refuses to be used."""
+    return FirstOrder.apply(len(grads), *grads, *of) if torch.is_grad_enabled() else grads
+
+
 class LayerNorm(torch.autograd.Function):
     """``binding.norm_forward`` / ``binding.norm_backward`` on rows of the last dimension."""
 
@@ -32,7 +50,7 @@ class LayerNorm(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         g = binding.norm_backward(dy.contiguous(), x, mean, rstd, weight)
-        return g["dx"], g["dw"], g["db"], None
+        return *first_order((g["dx"], g["dw"], g["db"]), dy, x, weight), None
 
 
 class DeltaRule(torch.autograd.Function):
@@ -50,7 +68,7 @@ class DeltaRule(torch.autograd.Function):
     def backward(ctx, do):
         q, k, v, g, beta, stash = ctx.saved_tensors
         d = binding.delta_backward(ctx.cfg, do.contiguous(), q, k, v, g, beta, stash=stash)
-        return None, d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"]
+        return None, *first_order((d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"]), do, q, k, v, g, beta)
 
 
 class DeltaMixer:
