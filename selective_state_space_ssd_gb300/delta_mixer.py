@@ -113,13 +113,18 @@ class DeltaMixer:
     @torch.no_grad()
     def prefill(self, x, cu_seqlens, state, slots):
         """Packed prompts x [tokens, width] with bounds cu_seqlens (int32) to y; prompt n's final state goes to
-        state[slots[n]] of the cache [slots, HV, K, V]."""
+        state[slots[n]] of the cache [slots, HV, K, V], or nowhere if slots[n] is none of its slots."""
         norm = lambda *a: binding.norm_forward(*a)[0]  # noqa: E731
         h = norm(x, self.p["norm_w"], self.p["norm_b"], 1e-5)
         q, k, v, g, beta = self.inputs(h[None])
         o, final = binding.delta_forward(self.cfg(slots.numel(), x.shape[0]), q, k, v, g, beta,
                                          cu_seqlens=cu_seqlens)  # (v as the projection left it: a slice of wider rows)
-        state[slots.long()] = final
+        # A place without a slot writes what another place writes too (the cache's own content where no place has a slot),
+        # so that nothing waits for the device to count them.
+        held = (slots >= 0) & (slots < state.shape[0])
+        place = torch.where(held, torch.arange(slots.numel(), device=slots.device), held.int().argmax())
+        slot = slots[place].long().clamp(0, state.shape[0] - 1)
+        state[slot] = torch.where(held.any(), final[place], state[slot])
         return self.output(x, o[0], norm)
 
     @torch.no_grad()
