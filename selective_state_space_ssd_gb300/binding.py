@@ -24,7 +24,7 @@ VARIANTS = {"mamba2": 0, "mamba1": 1, "mimo": 2}
 DTYPES = {"f32": 0, "bf16": 1}
 _TORCH_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16}
 
-SSD_OK = 0
+SSD_OK, SSD_ERR_TIMEOUT = 0, 7
 
 
 class SSDError(RuntimeError):
@@ -627,43 +627,68 @@ def _delta_workspace(key, backward, stashed, device):
     return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
+def delta_status(device="cuda"):
+    """A tensor for the ``status`` of ``delta_forward`` and ``delta_backward``: the device status words of the calls that
+    it is handed to end up in it (the largest; 0: every wait of their kernels ended in time).  ``check_status`` reads it."""
+    return torch.zeros(1, dtype=torch.int32, device=device)
+
+
+def check_status(status) -> None:
+    """Waits for the work that `status` stands for and raises SSDError if a kernel's wait gave up, and with it results."""
+    code = int(status)
+    if code:
+        raise SSDError(SSD_ERR_TIMEOUT, f"delta rule (device status word {code})")
+
+
+def _join_status(status, ws) -> None:
+    """The status word of a call, the first 4 bytes of its workspace, into the caller's tensor, on the call's stream."""
+    torch.maximum(status, ws.view(torch.uint8)[:4].view(torch.int32), out=status)
+
+
 def delta_forward(cfg: dict, q, k, v, g, beta, s0=None, scale=None, cu_seqlens=None, stash=None, stream=None,
-                  workspace=None):
+                  workspace=None, status=None):
     """Allocate o and s_final, run ``ssd_delta_forward``; returns (o, s_final).  With ``cu_seqlens`` (int32,
     [batch + 1]) the sequences are packed on one axis of seqlen steps; ``stash`` (``delta_stash``) is filled for
-    ``delta_backward``; scale defaults to key_dim^-1/2.  On ``stream``, the outputs belong to it."""
+    ``delta_backward``; scale defaults to key_dim^-1/2.  On ``stream``, the outputs belong to it.  ``status``
+    (``delta_status``): where to leave the device status word, which is gone with the workspace otherwise."""
     if stream is not None:
         with _on(stream, v.device):
-            return delta_forward(cfg, q, k, v, g, beta, s0, scale, cu_seqlens, stash, None, workspace)
+            return delta_forward(cfg, q, k, v, g, beta, s0, scale, cu_seqlens, stash, None, workspace, status)
     key = _delta_of(cfg, q, k, v, cu_seqlens is not None)
     prob = _keep(key, lambda: _delta_struct(key))
     _delta_check(key, g, beta, s0, cu_seqlens)
+    _dense("status", status, (1,), torch.int32)
     scale = cfg["key_dim"] ** -0.5 if scale is None else scale
-    at = _device(v, q, k, g, beta, s0, cu_seqlens, stash, workspace and workspace[0])
+    at = _device(v, q, k, g, beta, s0, cu_seqlens, stash, status, workspace and workspace[0])
     dev = v.device
     o = _like(v)
     s_final = torch.empty((key[4], key[7], key[8], key[9]), dtype=torch.float32, device=dev)
     ws, n = workspace if workspace is not None else _delta_workspace(key, False, stash is not None, dev)
     ssd_delta_forward(prob, q, k, v, g, beta, s0, cu_seqlens, scale, o, s_final, stash,
                       0 if stash is None else stash.numel(), ws, n, _stream(None, at))
+    if status is not None:
+        _join_status(status, ws)
     return o, s_final
 
 
 def delta_backward(cfg: dict, dout, q, k, v, g, beta, ds_final=None, s0=None, scale=None, cu_seqlens=None, stash=None,
-                   stream=None, workspace=None):
+                   stream=None, workspace=None, status=None):
     """Allocate the gradients and run ``ssd_delta_backward``; returns dq, dk, dv, dg, dbeta and ds0 (None where s0 is
-    None).  ``stash``: what ``delta_forward`` filled on the same inputs; without it the chunk states are made again."""
+    None).  ``stash``: what ``delta_forward`` filled on the same inputs; without it the chunk states are made again.
+    ``status``: as for ``delta_forward``."""
     if stream is not None:
         with _on(stream, v.device):
-            return delta_backward(cfg, dout, q, k, v, g, beta, ds_final, s0, scale, cu_seqlens, stash, None, workspace)
+            return delta_backward(cfg, dout, q, k, v, g, beta, ds_final, s0, scale, cu_seqlens, stash, None, workspace,
+                                  status)
     key = _delta_of(cfg, q, k, v, cu_seqlens is not None)
     prob = _keep(key, lambda: _delta_struct(key))
     lead = _delta_check(key, g, beta, s0, cu_seqlens)
     _dense("dout", dout, lead + (key[7], key[9]), v.dtype)
     if ds_final is not None:
         _dense("ds_final", ds_final, (key[4], key[7], key[8], key[9]), torch.float32)
+    _dense("status", status, (1,), torch.int32)
     scale = cfg["key_dim"] ** -0.5 if scale is None else scale
-    at = _device(v, q, k, g, beta, dout, ds_final, s0, cu_seqlens, stash, workspace and workspace[0])
+    at = _device(v, q, k, g, beta, dout, ds_final, s0, cu_seqlens, stash, status, workspace and workspace[0])
     dev = v.device
     out = {"dq": _like(q), "dk": _like(k), "dv": _like(v), "dg": _like(g), "dbeta": _like(beta),
            "ds0": None if s0 is None else _like(s0)}
@@ -671,6 +696,8 @@ def delta_backward(cfg: dict, dout, q, k, v, g, beta, ds_final=None, s0=None, sc
     ssd_delta_backward(prob, dout, ds_final, q, k, v, g, beta, s0, cu_seqlens, scale, out["dq"], out["dk"], out["dv"],
                        out["dg"], out["dbeta"], out["ds0"], stash, 0 if stash is None else stash.numel(), ws, n,
                        _stream(None, at))
+    if status is not None:
+        _join_status(status, ws)
     return out
 
 

@@ -54,21 +54,22 @@ class LayerNorm(torch.autograd.Function):
 
 
 class DeltaRule(torch.autograd.Function):
-    """``binding.delta_forward`` with its stash / ``binding.delta_backward``, from an empty first state."""
+    """``binding.delta_forward`` with its stash / ``binding.delta_backward``, from an empty first state.  ``status``: where
+    both leave their device status word."""
 
     @staticmethod
-    def forward(ctx, cfg, q, k, v, g, beta):
+    def forward(ctx, cfg, q, k, v, g, beta, status=None):
         stash = binding.delta_stash(cfg, q.device)
-        o, _ = binding.delta_forward(cfg, q, k, v, g, beta, stash=stash)
+        o, _ = binding.delta_forward(cfg, q, k, v, g, beta, stash=stash, status=status)
         ctx.save_for_backward(q, k, v, g, beta, stash)
-        ctx.cfg = cfg
+        ctx.cfg, ctx.status = cfg, status
         return o
 
     @staticmethod
     def backward(ctx, do):
         q, k, v, g, beta, stash = ctx.saved_tensors
-        d = binding.delta_backward(ctx.cfg, do.contiguous(), q, k, v, g, beta, stash=stash)
-        return None, *first_order((d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"]), do, q, k, v, g, beta)
+        d = binding.delta_backward(ctx.cfg, do.contiguous(), q, k, v, g, beta, stash=stash, status=ctx.status)
+        return None, *first_order((d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"]), do, q, k, v, g, beta), None
 
 
 class DeltaMixer:
@@ -87,6 +88,15 @@ class DeltaMixer:
                  head_b=torch.zeros(value_dim), log_a=torch.rand(value_heads, generator=gen) * 2.0,
                  dt_bias=rn(value_heads) - 3.0)
         self.p = {n: t.to(device).requires_grad_() for n, t in p.items()}
+        self.status = binding.delta_status(device)
+
+    def check(self) -> None:
+        """Waits for the block's calls so far and raises SSDError if a kernel of theirs gave up; a program does so where it
+        waits for the GPU anyhow, once in so many steps."""
+        try:
+            binding.check_status(self.status)
+        finally:
+            self.status.zero_()
 
     def cfg(self, batch: int, seqlen: int) -> dict:
         return dict(dtype="bf16", gate_dtype="f32", batch=batch, seqlen=seqlen, nheads=self.h, value_heads=self.hv,
@@ -107,7 +117,7 @@ class DeltaMixer:
         """x [b, T, width] (bf16) to y, with gradients of x and of the weights."""
         h = LayerNorm.apply(x, self.p["norm_w"], self.p["norm_b"], 1e-5)
         q, k, v, g, beta = self.inputs(h)
-        o = DeltaRule.apply(self.cfg(x.shape[0], x.shape[1]), q, k, v.contiguous(), g, beta)
+        o = DeltaRule.apply(self.cfg(x.shape[0], x.shape[1]), q, k, v.contiguous(), g, beta, self.status)
         return self.output(x, o, LayerNorm.apply)
 
     @torch.no_grad()
@@ -117,8 +127,9 @@ class DeltaMixer:
         norm = lambda *a: binding.norm_forward(*a)[0]  # noqa: E731
         h = norm(x, self.p["norm_w"], self.p["norm_b"], 1e-5)
         q, k, v, g, beta = self.inputs(h[None])
-        o, final = binding.delta_forward(self.cfg(slots.numel(), x.shape[0]), q, k, v, g, beta,
-                                         cu_seqlens=cu_seqlens)  # (v as the projection left it: a slice of wider rows)
+        # (v as the projection left it: a slice of wider rows)
+        o, final = binding.delta_forward(self.cfg(slots.numel(), x.shape[0]), q, k, v, g, beta, cu_seqlens=cu_seqlens,
+                                         status=self.status)
         # A place without a slot writes what another place writes too (the cache's own content where no place has a slot),
         # so that nothing waits for the device to count them.
         held = (slots >= 0) & (slots < state.shape[0])
@@ -155,6 +166,7 @@ def main() -> None:
         token = mixer.decode(token, state, slots)
     print("prompts of", lengths, "tokens, four more tokens each: y", tuple(token.shape), "finite:",
           bool(token.isfinite().all()))
+    mixer.check()
 
 
 if __name__ == "__main__":
