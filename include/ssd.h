@@ -399,8 +399,10 @@ ssd_status ssd_kda_backward(const ssd_kda_problem* prob, const float* dout, cons
  *               on; the call's cu_seqlens (device, int32 [batch + 1], 4-byte
  *               aligned) holds 0, the ends of the first sequences, seqlen.
  *               Empty sequences are allowed.  The kernels clamp its values to
- *               0 .. seqlen and to ascending order; steps that belong to no
- *               sequence are not written.  ssd_delta_step takes packed = 0.
+ *               0 .. seqlen and to ascending order.  Steps that belong to no
+ *               sequence (before the first value, past the last one of an axis
+ *               that is padded) take no part; o and the gradients are zero
+ *               there.  ssd_delta_step takes packed = 0.
  *   batch, seqlen, nheads (H), value_heads (HV, a multiple of H), key_dim (K),
  *   value_dim (V): >= 1.  Limits of this build: K, V <= 128, HV <= 65535, steps
  *               and b*HV below 2^31 (SSD_ERR_SHAPE).

@@ -648,8 +648,8 @@ def _join_status(status, ws) -> None:
 def delta_forward(cfg: dict, q, k, v, g, beta, s0=None, scale=None, cu_seqlens=None, stash=None, stream=None,
                   workspace=None, status=None):
     """Allocate o and s_final, run ``ssd_delta_forward``; returns (o, s_final).  With ``cu_seqlens`` (int32,
-    [batch + 1]) the sequences are packed on one axis of seqlen steps; ``stash`` (``delta_stash``) is filled for
-    ``delta_backward``; scale defaults to key_dim^-1/2.  On ``stream``, the outputs belong to it.  ``status``
+    [batch + 1]) the sequences are packed on one axis of seqlen steps (steps of no sequence are zero in o and in the
+    gradients); ``stash`` (``delta_stash``) is filled for ``delta_backward``; scale defaults to key_dim^-1/2.  On ``stream``, the outputs belong to it.  ``status``
     (``delta_status``): where to leave the device status word, which is gone with the workspace otherwise."""
     if stream is not None:
         with _on(stream, v.device):

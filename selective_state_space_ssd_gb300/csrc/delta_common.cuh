@@ -37,6 +37,14 @@ struct Table {
   int* order;  // the sequences, those with the most chunks first (up to kRanked of them)
 };
 
+// Outputs that hold one row a step (null: not there) and the bytes of a row, an even number: where a step of a packed axis
+// belongs to no sequence they get zeros.
+constexpr int kStepOutputs = 5;
+struct StepRows {
+  void* p[kStepOutputs];
+  int bytes[kStepOutputs];
+};
+
 // One record per (chunk, value head), item = chunk * HV + head, in one piece of memory that one bulk copy brings in:
 // four [64][64] bf16 tiles, swizzled as the tensor cores read them (element (i, j) at tile_off), and the decays.
 //   (I + A)^-1 rounded to bf16; what that rounding left, rounded; P_ij = scale e^{G_i - G_j} q_i . k_j (j <= i) in the same

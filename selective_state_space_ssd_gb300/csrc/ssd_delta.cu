@@ -32,12 +32,44 @@ namespace delta {
 namespace {
 
 // ---------------------------------------------------------------- packed sequences
-// cu_seqlens -> start, length and first chunk of every sequence, and their order by length.  One block.  Bounds that leave the token axis or
-// run backwards are pulled in (a running maximum), so no later kernel can leave its buffers whatever the values are.
-__global__ void __launch_bounds__(1024) k_delta_table(const int* __restrict__ cu, int N, int T, Table tb) {
+// Zeros into bytes a .. b - 1 (both even) of p (16-byte aligned) by `threads` threads, of which this is number t.
+__device__ void zero_bytes(void* p, long long a, long long b, int t, int threads) {
+  for (long long at = a / 16 * 16 + 16ll * t; at < b; at += 16ll * threads) {
+    unsigned char* q = static_cast<unsigned char*>(p) + at;
+    if (at >= a && at + 16 <= b) {
+      *reinterpret_cast<uint4*>(q) = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int i = 0; i < 16; i += 2)
+        if (at + i >= a && at + i < b) *reinterpret_cast<unsigned short*>(q + i) = 0;
+    }
+  }
+}
+
+// cu_seqlens -> start, length and first chunk of every sequence, and their order by length, by the first block.  Bounds that
+// leave the token axis or run backwards are pulled in (a running maximum), so no later kernel can leave its buffers whatever
+// the values are.  The other blocks meanwhile write the outputs' rows of the steps that belong to no sequence: those before
+// the first bound and those past the largest, on an axis that is padded.
+constexpr int kTableBlocks = 64;
+__global__ void __launch_bounds__(1024) k_delta_table(const int* __restrict__ cu, int N, int T, Table tb, StepRows rows) {
   __shared__ int s_max[1024], s_sum[1024];
   __shared__ int carry_end, carry_chunk;
   const int tid = threadIdx.x;
+  if (blockIdx.x > 0) {
+    int end = 0;
+    for (int n = tid; n <= N; n += 1024) end = max(end, min(max(cu[n], 0), T));
+    end = __reduce_max_sync(0xffffffffu, end);
+    if ((tid & 31) == 0) s_max[tid >> 5] = end;
+    __syncthreads();
+    end = __reduce_max_sync(0xffffffffu, s_max[tid & 31]);
+    const long long start = min(max(cu[0], 0), T);
+    const int t = ((int)blockIdx.x - 1) * 1024 + tid, threads = (kTableBlocks - 1) * 1024;
+    for (int i = 0; i < kStepOutputs; ++i) {
+      if (!rows.p[i]) continue;
+      zero_bytes(rows.p[i], 0, start * rows.bytes[i], t, threads);
+      zero_bytes(rows.p[i], (long long)end * rows.bytes[i], (long long)T * rows.bytes[i], t, threads);
+    }
+    return;
+  }
   if (tid == 0) {
     carry_end = min(max(cu[0], 0), T);
     carry_chunk = 0;
@@ -419,10 +451,12 @@ cudaError_t allow_smem(F* f, size_t bytes) {
   return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+void run_table(const Dims& d, const Table& tb, const int* cu, const StepRows& rows, cudaStream_t st) {
+  if (d.packed) SSD_LAUNCH("k_delta_table", st, k_delta_table<<<kTableBlocks, 1024, 0, st>>>(cu, d.N, d.T, tb, rows));
+}
+
 template <int KP>
-cudaError_t run_prep(const Dims& d, const Table& tb, const In& in, uint8_t* records, const int* cu, int* status,
-                     cudaStream_t st) {
-  if (d.packed) SSD_LAUNCH("k_delta_table", st, k_delta_table<<<1, 1024, 0, st>>>(cu, d.N, d.T, tb));
+cudaError_t run_prep(const Dims& d, const Table& tb, const In& in, uint8_t* records, int* status, cudaStream_t st) {
   const size_t kq = 2 * (size_t)(2 * kC * (KP + 8)), at = sizeof(float) * (2 * kC + 32) * kFP, sm = kq > at ? kq : at;
   cudaError_t e = allow_smem(k_delta_prep<KP>, sm);
   if (e != cudaSuccess) return e;
@@ -431,9 +465,8 @@ cudaError_t run_prep(const Dims& d, const Table& tb, const In& in, uint8_t* reco
   return cudaGetLastError();
 }
 
-cudaError_t prepare(const Dims& d, const Table& tb, const In& in, uint8_t* records, const int* cu, int* status,
-                    cudaStream_t st) {
-  return d.KP == 64 ? run_prep<64>(d, tb, in, records, cu, status, st) : run_prep<128>(d, tb, in, records, cu, status, st);
+cudaError_t prepare(const Dims& d, const Table& tb, const In& in, uint8_t* records, int* status, cudaStream_t st) {
+  return d.KP == 64 ? run_prep<64>(d, tb, in, records, status, st) : run_prep<128>(d, tb, in, records, status, st);
 }
 
 }  // namespace
@@ -541,7 +574,8 @@ ssd_status ssd_delta_forward(const ssd_delta_problem* prob, const void* q, const
   }
   const In in{(const bf16*)q, (const bf16*)k, (const bf16*)v, g, beta, s0, scale};
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t e = prepare(d, tb, in, kept.records, cu_seqlens, (int*)ws, st);
+  run_table(d, tb, cu_seqlens, StepRows{{o}, {d.HV * d.V * 2}}, st);
+  cudaError_t e = prepare(d, tb, in, kept.records, (int*)ws, st);
   if (e == cudaSuccess) e = forward_scan(d, tb, in, kept.records, split, (bf16*)o, s_final, kept.S, kept.R, (int*)ws, st);
   return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
@@ -581,12 +615,13 @@ ssd_status ssd_delta_backward(const ssd_delta_problem* prob, const void* dout, c
   const In in{(const bf16*)q, (const bf16*)k, (const bf16*)v, g, beta, s0, scale};
   const GradOut out{(bf16*)dq, (bf16*)dk, dg, dbeta};
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  const int qk = d.H * d.K * 2, gate = d.HV * (d.gate_bf16 ? 2 : 4);
+  run_table(d, tb, cu_seqlens, StepRows{{dq, dk, dv, dg, dbeta}, {qk, qk, d.HV * d.V * 2, gate, gate}}, st);
   cudaError_t e = cudaSuccess;
   if (stash) {
-    if (d.packed) SSD_LAUNCH("k_delta_table", st, k_delta_table<<<1, 1024, 0, st>>>(cu_seqlens, d.N, d.T, tb));
     e = cudaMemsetAsync(ws, 0, sizeof(int32_t), st);
   } else {
-    e = prepare(d, tb, in, kept.records, cu_seqlens, (int*)ws, st);
+    e = prepare(d, tb, in, kept.records, (int*)ws, st);
     if (e == cudaSuccess) e = forward_scan(d, tb, in, kept.records, split, nullptr, nullptr, kept.S, kept.R, (int*)ws, st);
   }
   if (e == cudaSuccess)
