@@ -384,6 +384,8 @@ void launch(const Call& c, cudaStream_t st) {
              <<<nb, kT, 0, st>>>(c.a, (const T*)c.dy, (const T*)c.x, c.mean, c.rstd, c.w, (T*)c.dx, c.part));
 }
 
+// The elements a thread that shape_of gives for TPR threads a row, and no others: 8 and 16 only at the fewest threads (16
+// in fp32 at any), 32 in bf16 or at the most threads, 40 in bf16 below those.
 template <typename T, int TPR, bool kVec>
 void by_elements(const Call& c, int e, cudaStream_t st) {
   if constexpr (TPR == 8)
@@ -392,7 +394,7 @@ void by_elements(const Call& c, int e, cudaStream_t st) {
     if (e == 16) return launch<T, TPR, 16, kVec>(c, st);
   if constexpr (TPR == 512 || sizeof(T) == 2)
     if (e == 32) return launch<T, TPR, 32, kVec>(c, st);
-  if constexpr (sizeof(T) == 2)
+  if constexpr (sizeof(T) == 2 && TPR < 512)
     if (e == 40) return launch<T, TPR, 40, kVec>(c, st);
   launch<T, TPR, 24, kVec>(c, st);
 }
