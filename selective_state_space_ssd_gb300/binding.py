@@ -600,12 +600,17 @@ def _device(first, *others) -> int:
     return dev
 
 
-def _on(stream, device):
+def _on(stream, device, *tensors):
     """The context of a call on a stream of the caller's (a torch stream or a ``cudaStream_t``): what the call allocates
-    belongs to that stream, as a workspace that is freed on return has to."""
+    belongs to that stream, as a workspace that is freed on return has to.  The call's own tensors, which may belong to
+    another, stay until a torch stream has come to their use; a handle's owner keeps them, since it may end before they do."""
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream(stream)
         stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    else:
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -649,10 +654,12 @@ def delta_forward(cfg: dict, q, k, v, g, beta, s0=None, scale=None, cu_seqlens=N
                   workspace=None, status=None):
     """Allocate o and s_final, run ``ssd_delta_forward``; returns (o, s_final).  With ``cu_seqlens`` (int32,
     [batch + 1]) the sequences are packed on one axis of seqlen steps (steps of no sequence are zero in o and in the
-    gradients); ``stash`` (``delta_stash``) is filled for ``delta_backward``; scale defaults to key_dim^-1/2.  On ``stream``, the outputs belong to it.  ``status``
-    (``delta_status``): where to leave the device status word, which is gone with the workspace otherwise."""
+    gradients); ``stash`` (``delta_stash``) is filled for ``delta_backward``; scale defaults to key_dim^-1/2.  On
+    ``stream`` (a torch stream, or a ``cudaStream_t`` whose owner keeps the tensors until it has used them), the outputs
+    belong to it.  ``status`` (``delta_status``): where to leave the device status word, which is gone with the
+    workspace otherwise."""
     if stream is not None:
-        with _on(stream, v.device):
+        with _on(stream, v.device, q, k, v, g, beta, s0, cu_seqlens, stash, workspace and workspace[0], status):
             return delta_forward(cfg, q, k, v, g, beta, s0, scale, cu_seqlens, stash, None, workspace, status)
     key = _delta_of(cfg, q, k, v, cu_seqlens is not None)
     prob = _keep(key, lambda: _delta_struct(key))
@@ -677,7 +684,8 @@ def delta_backward(cfg: dict, dout, q, k, v, g, beta, ds_final=None, s0=None, sc
     None).  ``stash``: what ``delta_forward`` filled on the same inputs; without it the chunk states are made again.
     ``status``: as for ``delta_forward``."""
     if stream is not None:
-        with _on(stream, v.device):
+        with _on(stream, v.device, dout, q, k, v, g, beta, ds_final, s0, cu_seqlens, stash, workspace and workspace[0],
+                 status):
             return delta_backward(cfg, dout, q, k, v, g, beta, ds_final, s0, scale, cu_seqlens, stash, None, workspace,
                                   status)
     key = _delta_of(cfg, q, k, v, cu_seqlens is not None)
@@ -705,7 +713,7 @@ def delta_step(cfg: dict, q, k, v, g, beta, state, slots=None, scale=None, strea
     """Allocate o and run ``ssd_delta_step``: seqlen steps of each sequence on its slot of ``state`` [slots, HV, K, V]
     (fp32), which is updated in place; returns o."""
     if stream is not None:
-        with _on(stream, v.device):
+        with _on(stream, v.device, q, k, v, g, beta, state, slots):
             return delta_step(cfg, q, k, v, g, beta, state, slots, scale)
     key = _delta_of(cfg, q, k, v, False)
     prob = _keep(key, lambda: _delta_struct(key))
@@ -774,7 +782,7 @@ def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, stream=None):
     """Layer norm of x [.., D]; weight and bias [D] (either may be None) of one type.  Returns y (contiguous), mean and
     rstd (fp32, one per row)."""
     if stream is not None:
-        with _on(stream, x.device):
+        with _on(stream, x.device, x, weight, bias):
             return norm_forward(x, weight, bias, eps)
     key = _norm_of(x, weight if weight is not None else bias)
     prob = _keep(key, lambda: _norm_struct(key))
@@ -795,7 +803,7 @@ def norm_backward(dy, x, mean, rstd, weight=None, stream=None, workspace=None):
     """The gradients of ``norm_forward``: dx (contiguous), and dw and db in the weight's type (fp32 without a
     weight)."""
     if stream is not None:
-        with _on(stream, x.device):
+        with _on(stream, x.device, dy, x, mean, rstd, weight, workspace and workspace[0]):
             return norm_backward(dy, x, mean, rstd, weight, None, workspace)
     key = _norm_of(x, weight)
     prob = _keep(key, lambda: _norm_struct(key))
