@@ -416,11 +416,14 @@ ssd_status ssd_kda_backward(const ssd_kda_problem* prob, const float* dout, cons
  * start on 16 bytes are read faster); every other pointer of the chunked calls
  * is 16-byte aligned.
  *
- * Precision.  The state is fp32 over any length: what the chunk products read
- * of it enters the tensor cores as two bf16 numbers, so s_final (and ds0) are
- * good to about 1e-5 of their size, and o and dv are rounded once to
- * bf16.  The other gradients are sums of products of bf16-rounded tiles: their
- * relative error is about 2^-8 whatever type they are stored in.  A NaN or
+ * Precision.  The state is held and summed in fp32 over any length, and what
+ * the chunk products read of it enters the tensor cores as two bf16 numbers,
+ * which keep 16 bits: s_final and ds0 are good to about 1e-5 of the terms that
+ * they are sums of (some 4e-6 of their own size as a rule, where fp32 products
+ * would give 3e-7; 7e-5 was seen of ds0 at one key a head, whose terms cancel),
+ * and o and dv are rounded once to bf16.  The other gradients are sums of
+ * products of bf16-rounded tiles: their relative error is about 2^-8 whatever
+ * type they are stored in, also for fp32 gates.  A NaN or
  * infinity in q, k, v, g or beta may reach every step of its chunk of 64 steps
  * and every later one of its sequence; other sequences and steps past a sequence's end take
  * nothing from it.
