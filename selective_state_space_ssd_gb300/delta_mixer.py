@@ -50,7 +50,9 @@ class LayerNorm(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, mean, rstd = ctx.saved_tensors
         g = binding.norm_backward(dy.contiguous(), x, mean, rstd, weight)
-        return *first_order((g["dx"], g["dw"], g["db"]), dy, x, weight), None
+        of = (dy, x) if weight is None else (dy, x, weight)
+        grads = first_order((g["dx"], g["dw"], g["db"]), *of)
+        return *(t if need else None for t, need in zip(grads, ctx.needs_input_grad)), None
 
 
 class DeltaRule(torch.autograd.Function):

@@ -74,3 +74,19 @@ def test_first_derivatives_are_the_same_with_and_without_a_graph(calls, kind):
         want = torch.autograd.grad((torch.nn.functional.layer_norm(x, (5,), w, None, 1e-5) * c).sum(), (x, w))
         for a, b in zip(plain, want):
             assert torch.allclose(a, b, rtol=1e-10, atol=1e-12)
+
+
+@pytest.mark.parametrize("weight,bias", [(False, False), (True, False), (False, True)])
+def test_norm_without_a_weight_or_a_bias(calls, monkeypatch, weight, bias):
+    one, zero = torch.ones(5, dtype=torch.float64), torch.zeros(5, dtype=torch.float64)
+    monkeypatch.setattr(binding, "norm_forward", lambda x, w, b, eps: norm_forward(x, one if w is None else w,
+                                                                                  zero if b is None else b, eps))
+    monkeypatch.setattr(binding, "norm_backward", lambda dy, x, m, r, w: norm_backward(dy, x, m, r, one if w is None else w))
+    gen = torch.Generator().manual_seed(2)
+    x, w, b, c = (torch.randn(s, generator=gen, dtype=torch.float64).requires_grad_() for s in ((3, 5), (5,), (5,), (3, 5)))
+    w, b = w if weight else None, b if bias else None
+    leaves = [t for t in (x, w, b) if t is not None]
+    got = torch.autograd.grad((LayerNorm.apply(x, w, b, 1e-5) * c).sum(), leaves)
+    want = torch.autograd.grad((torch.nn.functional.layer_norm(x, (5,), w, b, 1e-5) * c).sum(), leaves)
+    for g, r in zip(got, want):
+        assert torch.allclose(g, r, rtol=1e-10, atol=1e-12)
