@@ -639,7 +639,8 @@ def delta_status(device="cuda"):
 
 
 def check_status(status) -> None:
-    """Waits for the work that `status` stands for and raises SSDError if a kernel's wait gave up, and with it results."""
+    """Reads `status` on the current stream (made to come after the calls' stream by the caller, where that is another),
+    waiting for it, and raises SSDError if a kernel's wait gave up: results of those calls are missing or wrong."""
     code = int(status)
     if code:
         raise SSDError(SSD_ERR_TIMEOUT, f"delta rule (device status word {code})")
@@ -647,7 +648,7 @@ def check_status(status) -> None:
 
 def _join_status(status, ws) -> None:
     """The status word of a call, the first 4 bytes of its workspace, into the caller's tensor, on the call's stream."""
-    torch.maximum(status, ws.view(torch.uint8)[:4].view(torch.int32), out=status)
+    torch.maximum(status, ws.view(torch.uint8)[:4].view(torch.int32).view(status.shape), out=status)
 
 
 def delta_forward(cfg: dict, q, k, v, g, beta, s0=None, scale=None, cu_seqlens=None, stash=None, stream=None,

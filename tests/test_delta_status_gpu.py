@@ -74,6 +74,15 @@ def test_refusals():
             binding.delta_backward(cfg, x[2], *x, status=bad)
 
 
+def test_a_number_without_dimensions(codes):
+    cfg = cfg_of(T=8)
+    x = tuple(cuda(make(cfg, 54))[n] for n in NAMES)
+    status = torch.zeros((), dtype=torch.int32, device="cuda")
+    codes["ssd_delta_forward"] = 9
+    binding.delta_forward(cfg, *x, status=status)
+    assert status.shape == () and int(status) == 9
+
+
 def test_in_a_graph(codes):
     cfg = cfg_of(T=40, K=16, V=16)
     x = tuple(cuda(make(cfg, 53))[n] for n in NAMES)
