@@ -16,7 +16,10 @@ namespace delta {
 using bf16 = __nv_bfloat16;
 
 constexpr int kC = 64;              // steps of a chunk
-constexpr int kGateRows = 5;        // per-step records of a chunk: e^G, e^{G_end - G}, beta, G / ln 2, scale e^G
+// Per-step records of a chunk: e^G, e^{G_end - G}, beta, G / ln 2, scale e^G.  G / ln 2 is one fp32 number: the gradients'
+// decays e^{G_i - G_j} come from it alone and are good to 2^-24 |G|, 1e-3 at the steepest sum of 64 steps that kMinG
+// allows and 1e-5 at a decay of e^-2 a step; the forward's (k_delta_prep) come from two.
+constexpr int kGateRows = 5;
 constexpr float kMinG = -200.f;     // e^g of anything below is 0; keeps G - G' defined where g is -inf
 
 struct Dims {

@@ -17,11 +17,14 @@
 //
 // Precision.  q, k, v, dO are bf16 as given.  What a scan computes in fp32 and has to multiply again (S, Y, T, P, R and
 // their gradients) enters the tensor cores as two bf16 numbers, high and low, so a product of two such is three
-// products; what is dropped is 2^-17 of each factor.  The state therefore keeps fp32 accuracy over any length (relative
-// error 3e-6 to 4e-6 against 64 bits), which single bf16 operands would not give: a state that is read for thousands of
-// steps would carry 2^-9.  The gradients' last products (k_delta_grads) take S, dS', R and dY rounded to bf16, as the
-// stash holds them: their results are gradients of bf16 inputs (relative error 2.5e-3 for dq, dk, dbeta, 3e-3 to 3.5e-3
-// for dg; 1.7e-3 for o and dv, which is the rounding of a bf16 result).
+// products; what is dropped is 2^-17 of each factor.  The state itself is held and summed in fp32 over any length; with
+// 16-bit factors it comes out at a relative error of 3e-6 to 4e-6 against 64 bits, where fp32 products give 1e-7 to 3e-7,
+// and single bf16 operands would carry 2^-9 through thousands of steps.  The gradients' last products (k_delta_grads) take
+// S, dS', R and dY rounded to bf16, as the stash holds them: their results are gradients of bf16 inputs (relative error
+// 2.5e-3 for dq and dk; dg 2.5e-3 and dbeta 1.8e-3 in fp32, 2.9e-3 and 2.4e-3 in bf16; 1.7e-3 for o and dv, which is the
+// rounding of a bf16 result).  Two parts there would leave only that rounding, and double the 0.8 GB that those four
+// tensors are written and then read with in a training step of 8192 chunks and heads; the kernel's shared memory has no
+// room for them.
 #include <initializer_list>
 
 #include "delta_common.cuh"

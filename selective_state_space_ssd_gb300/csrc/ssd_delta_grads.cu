@@ -14,10 +14,10 @@
 // read [dO; dY] stacked on 128 rows.  The decays never touch an operand but B1, B2: everything else is scaled in fp32
 // where it leaves tensor memory.  What a head reads (144 KB for K = V = 128) comes by TMA and bulk copies while the head
 // before is in its second half, S and dS' last: the scores do not wait for them.  8192 chunks and heads:
-// 269 us, 5.0 TB/s (1.34 GB); the elementwise work between the products bounds it, at 1.3 times the time of the traffic
+// 268 us, 5.0 TB/s (1.34 GB); the elementwise work between the products bounds it, at 1.3 times the time of the traffic
 // alone.
 //
-// Twenty-three warps: 0-15 the elementwise work, four a lane quadrant (quarters of the columns); 16 the MMAs; 17-18 copies;
+// Twenty-four warps: 0-15 the elementwise work, four a lane quadrant (quarters of the columns); 16 the MMAs; 17-18 copies;
 // 19-22 the two sums that need no product (dY . V by rows, <dS', S>); 23 dbeta and dg from all sums.  The two sums hold the
 // tiles longer than the MMAs do, and the next head's copies with them: fused operations on bf16 pairs took 277 us,
 // fp32 ones after a conversion 283, mma.sync (of which the diagonal is wanted) 293, each before the scores stopped waiting

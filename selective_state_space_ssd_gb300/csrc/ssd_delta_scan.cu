@@ -77,7 +77,7 @@ struct Loader {
   long long vstride;
   bool vvec, with_q;
   int hk, hv;
-  uint64_t* tail;
+  uint64_t* tail;  // (completes once a block: a run has one cut chunk at most, so no warp can miss a phase)
   uint32_t tails;  // chunks of fewer steps so far
 
   __device__ bool operator()(uint8_t* st, uint64_t* full, const uint8_t* record, int first, int rows, int tid,
