@@ -521,6 +521,135 @@ ssd_status ssd_norm_backward(const ssd_norm_problem* prob, const void* dy, const
                              size_t ws_bytes, void* cuda_stream);
 
 /*
+ * The gated linear recurrence with one decay per channel: whole sequences with
+ * gradients, packed prompts, and single steps on a cache of states.  Per
+ * sequence and channel, with s the sigmoid:
+ *     g_t = -scale softplus(lam) s(r_t),   a_t = exp(g_t)
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) s(i_t) x_t,   y_t = h_t
+ *
+ * ssd_glr_problem:
+ *   io_dtype    of x, r, i, y and their gradients: SSD_F32 or SSD_BF16.  lam,
+ *               states and their gradients are fp32, as all arithmetic.
+ *   packed      0: batch sequences of seqlen steps each, x [b,T,D].  1: batch
+ *               sequences one after another on one axis of seqlen steps, x
+ *               [T,D], with cu_seqlens as for the delta rule above (ascending;
+ *               values are clamped to 0 .. seqlen; empty sequences are allowed:
+ *               their h_final is their h0).  y and the gradients are zero at
+ *               steps of no sequence.  ssd_glr_step takes packed = 0.
+ *   batch, seqlen, dim (D): >= 1.  Limits of this build (SSD_ERR_SHAPE): steps
+ *               below 2^31 - 4095, batch below 2^29, and up to 65535 where
+ *               sequences are not packed.
+ *   x_stride, r_stride, i_stride: elements from a step to the next, for
+ *               tensors that lie inside wider ones; 0 = dense.  Batches follow
+ *               one another at T strides.  Everything else is dense.
+ * Layouts: x, r, i, y, dy, dx, dr, di [b,T,D]; lam, dlam [D]; h0, h_final,
+ * dh_final, dh0 [b,D] fp32.  x, r, i, dy and fp32 arrays need the alignment of
+ * their type (rows of whole 16-byte pieces that start on 16 bytes are read
+ * faster), y, dx, dr, di, the stash and the workspace 16 bytes.  Outputs must
+ * not overlap inputs.
+ *
+ * A NaN or infinity reaches the later steps of its channel and sequence only
+ * (the earlier ones' gradients); other sequences take nothing from it.
+ *
+ * ssd_glr_stash_size: bytes of the stash a training forward may keep for its
+ *   backward: the fp32 state that enters every 32nd step.  Host-only.
+ * ssd_glr_workspace_size: device workspace of ssd_glr_backward (the forward
+ *   needs none); stashed != 0: of the call with a stash.  Host-only.
+ * ssd_glr_forward: y, and h_final unless NULL, from h0 (NULL: zeros); the stash
+ *   is filled unless NULL.  scale >= 0.
+ * ssd_glr_backward: dx, dr, di, dlam and (unless NULL) dh0 of <dy, y> +
+ *   <dh_final, h_final> (dh_final NULL: zeros) from the leaf inputs, as passed
+ *   to the forward.  Without the stash of a forward of the same problem and
+ *   inputs the states are made again; the results are the same bit for bit.
+ * ssd_glr_step: seqlen >= 1 steps of each of batch sequences on `state`
+ *   [num_slots,D] (fp32), updated in place; slots as for ssd_delta_step.
+ * Errors as for ssd_forward; every error is returned before anything is
+ * enqueued.  Results are bitwise reproducible.
+ */
+typedef struct {
+  int32_t io_dtype;
+  int32_t packed;
+  int64_t batch;
+  int64_t seqlen;
+  int64_t dim;
+  int64_t x_stride;
+  int64_t r_stride;
+  int64_t i_stride;
+} ssd_glr_problem;
+
+ssd_status ssd_glr_stash_size(const ssd_glr_problem* prob, size_t* bytes);
+ssd_status ssd_glr_workspace_size(const ssd_glr_problem* prob, int stashed, size_t* bytes);
+ssd_status ssd_glr_forward(const ssd_glr_problem* prob, const void* x, const void* r, const void* i, const float* lam,
+                           const float* h0, const int32_t* cu_seqlens, float scale, void* y, float* h_final, void* stash,
+                           size_t stash_bytes, void* cuda_stream);
+ssd_status ssd_glr_backward(const ssd_glr_problem* prob, const void* dy, const float* dh_final, const void* x, const void* r,
+                            const void* i, const float* lam, const float* h0, const int32_t* cu_seqlens, float scale,
+                            void* dx, void* dr, void* di, float* dlam, float* dh0, const void* stash, size_t stash_bytes,
+                            void* ws, size_t ws_bytes, void* cuda_stream);
+ssd_status ssd_glr_step(const ssd_glr_problem* prob, const void* x, const void* r, const void* i, const float* lam,
+                        float* state, const int32_t* slots, int64_t num_slots, float scale, void* y, void* cuda_stream);
+
+/*
+ * The causal short convolution of each channel (depthwise) with bias and
+ * activation: whole sequences with gradients, packed prompts, and single steps
+ * on a cache of inputs.  Per sequence and channel
+ *     z_t = bias + sum over j < K of weight[K-1-j] x_{t-j},   y = z s(z) or z
+ * where x before the first step is the sequence's taps: the last K - 1 inputs
+ * of what came before it, oldest first (NULL: zeros).
+ *
+ * ssd_conv_problem:
+ *   io_dtype     of x, y, the taps and their gradients; weight_dtype of weight,
+ *                bias, dw, db (SSD_F32 or SSD_BF16 each; arithmetic is fp32).
+ *   packed       0: x [b,T,D]; 1: x [T,D] and cu_seqlens, as for ssd_glr_forward.
+ *                ssd_conv_step takes packed = 0.
+ *   activation   SSD_ACT_NONE or SSD_ACT_SILU.
+ *   batch, seqlen, dim (D), taps (K): >= 1.  Limits of this build
+ *                (SSD_ERR_SHAPE): K 2 .. 4, D up to 2^20, steps below 2^31 -
+ *                4095, batch below 2^29, and up to 65535 where not packed.
+ *   x_stride     elements from a step of x to the next (0: dense); batches
+ *                follow one another at T strides.  Everything else is dense.
+ * Layouts: x, y, dy, dx [b,T,D]; weight, dw [D,K]; bias, db [D]; taps,
+ * taps_final, dtaps [b,K-1,D].  Pointers need the alignment of their type, the
+ * workspace 16 bytes; where D and the stride are multiples of four and every
+ * pointer starts on four elements four channels are taken at a time.  Outputs
+ * must not overlap inputs.
+ *
+ * ssd_conv_workspace_size: device workspace of ssd_conv_backward (the others
+ *   need none).  Host-only.
+ * ssd_conv_forward: y, and taps_final unless NULL (where a sequence has fewer
+ *   than K - 1 steps, what is left of its taps comes first).  bias NULL: zeros.
+ * ssd_conv_backward: dx, and dw, db (summed in a fixed order) and dtaps unless
+ *   NULL, of <dy, y>.  taps_final hands on inputs: its gradient is the caller's.
+ * ssd_conv_step: seqlen >= 1 steps of each of batch sequences on `state`
+ *   [num_slots,K-1,D] (io_dtype), updated in place; slots as for
+ *   ssd_delta_step.
+ * Errors as for ssd_forward; every error is returned before anything is
+ * enqueued.  Results are bitwise reproducible.
+ */
+typedef enum { SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GELU = 2 } ssd_activation;
+
+typedef struct {
+  int32_t io_dtype;
+  int32_t weight_dtype;
+  int32_t packed;
+  int32_t activation;
+  int64_t batch;
+  int64_t seqlen;
+  int64_t dim;
+  int64_t taps;
+  int64_t x_stride;
+} ssd_conv_problem;
+
+ssd_status ssd_conv_workspace_size(const ssd_conv_problem* prob, size_t* bytes);
+ssd_status ssd_conv_forward(const ssd_conv_problem* prob, const void* x, const void* weight, const void* bias, const void* taps,
+                            const int32_t* cu_seqlens, void* y, void* taps_final, void* cuda_stream);
+ssd_status ssd_conv_backward(const ssd_conv_problem* prob, const void* dy, const void* x, const void* weight, const void* bias,
+                             const void* taps, const int32_t* cu_seqlens, void* dx, void* dw, void* db, void* dtaps, void* ws,
+                             size_t ws_bytes, void* cuda_stream);
+ssd_status ssd_conv_step(const ssd_conv_problem* prob, const void* x, const void* weight, const void* bias, void* state,
+                         const int32_t* slots, int64_t num_slots, void* y, void* cuda_stream);
+
+/*
  * Per-launch timing, for diagnostics and roofline measurement.
  *
  * ssd_profile_start(capacity): every later ssd_forward / ssd_backward call

@@ -46,7 +46,9 @@ EXPORTS = ("ssd_workspace_size", "ssd_forward", "ssd_backward", "ssd_forward_sta
            "ssd_checkpoints_size", "ssd_forward_checkpointed", "ssd_backward_checkpointed",
            "ssd_kda_workspace_size", "ssd_kda_forward", "ssd_kda_backward", "ssd_delta_workspace_size",
            "ssd_delta_stash_size", "ssd_delta_forward", "ssd_delta_backward", "ssd_delta_step",
-           "ssd_norm_workspace_size", "ssd_norm_forward", "ssd_norm_backward")
+           "ssd_norm_workspace_size", "ssd_norm_forward", "ssd_norm_backward", "ssd_glr_workspace_size",
+           "ssd_glr_stash_size", "ssd_glr_forward", "ssd_glr_backward", "ssd_glr_step", "ssd_conv_workspace_size",
+           "ssd_conv_forward", "ssd_conv_backward", "ssd_conv_step")
 
 
 class ssd_kda_problem(ctypes.Structure):
@@ -65,6 +67,18 @@ class ssd_delta_problem(ctypes.Structure):
 class ssd_norm_problem(ctypes.Structure):
     _fields_ = [("io_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("rows", ctypes.c_int64),
                 ("dim", ctypes.c_int64), ("x_stride", ctypes.c_int64)]
+
+
+class ssd_glr_problem(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("packed", ctypes.c_int32), ("batch", ctypes.c_int64),
+                ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("r_stride", ctypes.c_int64), ("i_stride", ctypes.c_int64)]
+
+
+class ssd_conv_problem(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("packed", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("taps", ctypes.c_int64), ("x_stride", ctypes.c_int64)]
 
 
 class ssd_kernel_time(ctypes.Structure):
@@ -150,6 +164,26 @@ def load(path: str | None = None):
         lib.ssd_norm_forward.restype = i32
         lib.ssd_norm_backward.argtypes = [np_] + [vp] * 9 + [sz, vp]
         lib.ssd_norm_backward.restype = i32
+        gp = ctypes.POINTER(ssd_glr_problem)
+        lib.ssd_glr_workspace_size.argtypes = [gp, i32, ctypes.POINTER(sz)]
+        lib.ssd_glr_workspace_size.restype = i32
+        lib.ssd_glr_stash_size.argtypes = [gp, ctypes.POINTER(sz)]
+        lib.ssd_glr_stash_size.restype = i32
+        lib.ssd_glr_forward.argtypes = [gp] + [vp] * 6 + [f32, vp, vp, vp, sz, vp]
+        lib.ssd_glr_forward.restype = i32
+        lib.ssd_glr_backward.argtypes = [gp] + [vp] * 8 + [f32] + [vp] * 5 + [vp, sz, vp, sz, vp]
+        lib.ssd_glr_backward.restype = i32
+        lib.ssd_glr_step.argtypes = [gp] + [vp] * 6 + [i64, f32, vp, vp]
+        lib.ssd_glr_step.restype = i32
+        cp = ctypes.POINTER(ssd_conv_problem)
+        lib.ssd_conv_workspace_size.argtypes = [cp, ctypes.POINTER(sz)]
+        lib.ssd_conv_workspace_size.restype = i32
+        lib.ssd_conv_forward.argtypes = [cp] + [vp] * 8
+        lib.ssd_conv_forward.restype = i32
+        lib.ssd_conv_backward.argtypes = [cp] + [vp] * 11 + [sz, vp]
+        lib.ssd_conv_backward.restype = i32
+        lib.ssd_conv_step.argtypes = [cp] + [vp] * 5 + [i64, vp, vp]
+        lib.ssd_conv_step.restype = i32
         _lib = lib
         return lib
 
@@ -825,3 +859,289 @@ def norm_backward(dy, x, mean, rstd, weight=None, stream=None, workspace=None):
     ssd_norm_backward(prob, dy, x, mean, rstd, weight, dx, dw, db, workspace[0], workspace[1],
                       _stream(None, at))
     return {"dx": dx, "dw": dw, "db": db}
+
+
+# ------------------------------------------------------------- sequences of channels: recurrence and convolution
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _act(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation {name!r}: one of {sorted(ACTIVATIONS)} expected")
+    return ACTIVATIONS[name]
+
+
+def _axes(x, cu_seqlens=None) -> tuple:
+    """(sequences, steps, channels, leading shape) of x [b, T, D], of one sequence [T, D], or of a packed axis ([T, D] or
+    [1, T, D]) with cu_seqlens [sequences + 1]."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [T, D] or [b, T, D]")
+    b = x.shape[0] if x.dim() == 3 else 1
+    if cu_seqlens is None:
+        return b, x.shape[-2], x.shape[-1]
+    if b != 1:
+        raise ValueError(f"x: shape {tuple(x.shape)}: packed sequences lie on one axis")
+    if cu_seqlens.dim() != 1 or cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 2:
+        raise ValueError(f"cu_seqlens: {cu_seqlens.dtype} {tuple(cu_seqlens.shape)}, expected contiguous int32 "
+                         f"[sequences + 1]")
+    return cu_seqlens.numel() - 1, x.shape[-2], x.shape[-1]
+
+
+def _row_stride(name: str, t, like) -> int:
+    """Elements from a step to the next of a tensor of `like`'s shape and type whose rows are dense and whose batches follow
+    one another (0: dense); raises ValueError for any other tensor."""
+    if t.dtype != like.dtype or t.shape != like.shape:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {like.dtype} {tuple(like.shape)}")
+    if t.is_contiguous():
+        return 0
+    steps, dim = t.shape[-2:]
+    b = t.shape[0] if t.dim() == 3 else 1
+    st = t.stride(-2)
+    if steps == 1:  # one step a batch: the batches are the steps
+        st = t.stride(0) if b > 1 else dim
+    if (dim > 1 and t.stride(-1) != 1) or (b > 1 and t.stride(0) != steps * st) or st < dim:
+        raise ValueError(f"{name}: strides {t.stride()}: rows have to be dense and batches follow one another")
+    return st
+
+
+def _same(name: str, t, like) -> None:
+    if t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous():
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} (contiguous: {t.is_contiguous()}), expected contiguous "
+                         f"{like.dtype} {tuple(like.shape)}")
+
+
+# ------------------------------------------------------------- gated linear recurrence, one decay per channel
+def _glr_of(x, r, i, cu_seqlens=None) -> tuple:
+    """The key of a call's problem: (kind, type, packed, sequences, steps, channels, strides)."""
+    n, steps, dim = _axes(x, cu_seqlens)
+    return ("glr", x.dtype, cu_seqlens is not None, n, steps, dim, _row_stride("x", x, x), _row_stride("r", r, x),
+            _row_stride("i", i, x))
+
+
+def _glr_struct(key: tuple) -> ssd_glr_problem:
+    return ssd_glr_problem(DTYPES[_name(key[1])], int(key[2]), *key[3:])
+
+
+def glr_problem(x, r=None, i=None, cu_seqlens=None) -> ssd_glr_problem:
+    """An ``ssd_glr_problem`` for x, r, i [b, T, D] (or [T, D]): dense, or rows at one stride."""
+    return _glr_struct(_glr_of(x, x if r is None else r, x if i is None else i, cu_seqlens))
+
+
+def ssd_glr_workspace_size(prob: ssd_glr_problem, stashed: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().ssd_glr_workspace_size(ctypes.byref(prob), int(bool(stashed)), ctypes.byref(out))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_glr_workspace_size")
+    return out.value
+
+
+def ssd_glr_stash_size(prob: ssd_glr_problem) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().ssd_glr_stash_size(ctypes.byref(prob), ctypes.byref(out))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_glr_stash_size")
+    return out.value
+
+
+def ssd_glr_forward(prob, x, r, i, lam, h0, cu_seqlens, scale, y, h_final, stash, stash_bytes, stream=None) -> None:
+    st = (_lib or load()).ssd_glr_forward(ctypes.byref(prob), _ptr(x), _ptr(r), _ptr(i), _ptr(lam), _ptr(h0),
+                                          _ptr(cu_seqlens), scale, _ptr(y), _ptr(h_final), _ptr(stash), stash_bytes,
+                                          _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_glr_forward")
+
+
+def ssd_glr_backward(prob, dy, dh_final, x, r, i, lam, h0, cu_seqlens, scale, dx, dr, di, dlam, dh0, stash, stash_bytes, ws,
+                     ws_bytes, stream=None) -> None:
+    st = (_lib or load()).ssd_glr_backward(ctypes.byref(prob), _ptr(dy), _ptr(dh_final), _ptr(x), _ptr(r), _ptr(i),
+                                           _ptr(lam), _ptr(h0), _ptr(cu_seqlens), scale, _ptr(dx), _ptr(dr), _ptr(di),
+                                           _ptr(dlam), _ptr(dh0), _ptr(stash), stash_bytes, _ptr(ws), ws_bytes,
+                                           _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_glr_backward")
+
+
+def ssd_glr_step(prob, x, r, i, lam, state, slots, num_slots, scale, y, stream=None) -> None:
+    st = (_lib or load()).ssd_glr_step(ctypes.byref(prob), _ptr(x), _ptr(r), _ptr(i), _ptr(lam), _ptr(state), _ptr(slots),
+                                       num_slots, scale, _ptr(y), _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_glr_step")
+
+
+def glr_stash(x):
+    """A buffer for what ``glr_forward`` keeps of x's sequences for ``glr_backward`` (uint8)."""
+    b, steps, dim = _axes(x)
+    key = ("glr", x.dtype, False, b, steps, dim, 0, 0, 0)
+    n = _keep(key + ("stash",), lambda: ssd_glr_stash_size(_glr_struct(key)))
+    return torch.empty(n, dtype=torch.uint8, device=x.device)
+
+
+def glr_forward(x, r, i, lam, h0=None, scale: float = 8.0, cu_seqlens=None, stash=None, stream=None):
+    """Gated linear recurrence over whole sequences: x and the gates' inputs r, i [b, T, D] (or [T, D]), lam [D] (fp32), h0
+    [b, D] (fp32; None: zeros).  Returns (y, h_final).  With ``cu_seqlens`` (int32, [sequences + 1]) the sequences are packed
+    on one axis (steps of no sequence are zero in y and in the gradients); ``stash`` (``glr_stash``) is filled for
+    ``glr_backward``.  ``stream``: as for ``delta_forward``."""
+    if stream is not None:
+        with _on(stream, x.device, x, r, i, lam, h0, cu_seqlens, stash):
+            return glr_forward(x, r, i, lam, h0, scale, cu_seqlens, stash)
+    key = _glr_of(x, r, i, cu_seqlens)
+    prob = _keep(key, lambda: _glr_struct(key))
+    _dense("lam", lam, (key[5],), torch.float32)
+    _dense("h0", h0, (key[3], key[5]), torch.float32)
+    at = _device(x, r, i, lam, h0, cu_seqlens, stash)
+    y = _like(x)
+    h_final = torch.empty((key[3], key[5]), dtype=torch.float32, device=x.device)
+    ssd_glr_forward(prob, x, r, i, lam, h0, cu_seqlens, scale, y, h_final, stash, 0 if stash is None else stash.numel(),
+                    _stream(None, at))
+    return y, h_final
+
+
+def glr_backward(dy, x, r, i, lam, dh_final=None, h0=None, scale: float = 8.0, cu_seqlens=None, stash=None, stream=None,
+                 workspace=None):
+    """The gradients of ``glr_forward``: a dict with dx, dr, di, dlam and dh0 (None where h0 is None).  ``stash``: what
+    ``glr_forward`` filled on the same inputs; without it the states are made again."""
+    if stream is not None:
+        with _on(stream, x.device, dy, x, r, i, lam, dh_final, h0, cu_seqlens, stash, workspace and workspace[0]):
+            return glr_backward(dy, x, r, i, lam, dh_final, h0, scale, cu_seqlens, stash, None, workspace)
+    key = _glr_of(x, r, i, cu_seqlens)
+    prob = _keep(key, lambda: _glr_struct(key))
+    _same("dy", dy, x)
+    _dense("lam", lam, (key[5],), torch.float32)
+    _dense("h0", h0, (key[3], key[5]), torch.float32)
+    _dense("dh_final", dh_final, (key[3], key[5]), torch.float32)
+    at = _device(x, dy, r, i, lam, dh_final, h0, cu_seqlens, stash, workspace and workspace[0])
+    out = {"dx": _like(x), "dr": _like(r), "di": _like(i), "dlam": _like(lam), "dh0": None if h0 is None else _like(h0)}
+    if workspace is None:
+        n = _keep(key + ("ws", stash is None), lambda: ssd_glr_workspace_size(prob, stash is not None))
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device), n
+    ssd_glr_backward(prob, dy, dh_final, x, r, i, lam, h0, cu_seqlens, scale, out["dx"], out["dr"], out["di"], out["dlam"],
+                     out["dh0"], stash, 0 if stash is None else stash.numel(), workspace[0], workspace[1],
+                     _stream(None, at))
+    return out
+
+
+def glr_step(x, r, i, lam, state, slots=None, scale: float = 8.0, stream=None):
+    """The steps x, r, i [b, T, D] of each of b sequences on its slot of ``state`` [slots, D] (fp32), which is updated in
+    place; returns y.  ``slots`` (int32, [b]; None: slot n for sequence n): a number that is no slot marks a place without
+    a sequence, whose y is zero."""
+    if stream is not None:
+        with _on(stream, x.device, x, r, i, lam, state, slots):
+            return glr_step(x, r, i, lam, state, slots, scale)
+    key = _glr_of(x, r, i)
+    prob = _keep(key, lambda: _glr_struct(key))
+    _dense("lam", lam, (key[5],), torch.float32)
+    ns = state.shape[0]
+    _dense("state", state, (ns, key[5]), torch.float32)
+    _dense("slots", slots, (key[3],), torch.int32)
+    at = _device(x, r, i, lam, state, slots)
+    y = _like(x)
+    ssd_glr_step(prob, x, r, i, lam, state, slots, ns, scale, y, _stream(None, at))
+    return y
+
+
+# ------------------------------------------------------------- causal short convolution
+def _conv_of(x, weight, activation, cu_seqlens=None) -> tuple:
+    """The key of a call's problem: (kind, type, weight's type, packed, activation, sequences, steps, channels, taps, stride)."""
+    n, steps, dim = _axes(x, cu_seqlens)
+    if weight.dim() != 2 or weight.shape[0] != dim or not weight.is_contiguous():
+        raise ValueError(f"weight: shape {tuple(weight.shape)} (contiguous: {weight.is_contiguous()}), expected contiguous "
+                         f"[{dim}, taps]")
+    return ("conv", x.dtype, weight.dtype, cu_seqlens is not None, _act(activation), n, steps, dim, weight.shape[1],
+            _row_stride("x", x, x))
+
+
+def _conv_struct(key: tuple) -> ssd_conv_problem:
+    return ssd_conv_problem(DTYPES[_name(key[1])], DTYPES[_name(key[2])], int(key[3]), *key[4:])
+
+
+def conv_problem(x, weight, activation: str = "silu", cu_seqlens=None) -> ssd_conv_problem:
+    """An ``ssd_conv_problem`` for x [b, T, D] (or [T, D]; dense, or rows at one stride) and weight [D, K]."""
+    return _conv_struct(_conv_of(x, weight, activation, cu_seqlens))
+
+
+def ssd_conv_workspace_size(prob: ssd_conv_problem) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().ssd_conv_workspace_size(ctypes.byref(prob), ctypes.byref(out))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_conv_workspace_size")
+    return out.value
+
+
+def ssd_conv_forward(prob, x, weight, bias, taps, cu_seqlens, y, taps_final, stream=None) -> None:
+    st = (_lib or load()).ssd_conv_forward(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), _ptr(taps),
+                                           _ptr(cu_seqlens), _ptr(y), _ptr(taps_final), _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_conv_forward")
+
+
+def ssd_conv_backward(prob, dy, x, weight, bias, taps, cu_seqlens, dx, dw, db, dtaps, ws, ws_bytes, stream=None) -> None:
+    st = (_lib or load()).ssd_conv_backward(ctypes.byref(prob), _ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(taps),
+                                            _ptr(cu_seqlens), _ptr(dx), _ptr(dw), _ptr(db), _ptr(dtaps), _ptr(ws), ws_bytes,
+                                            _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_conv_backward")
+
+
+def ssd_conv_step(prob, x, weight, bias, state, slots, num_slots, y, stream=None) -> None:
+    st = (_lib or load()).ssd_conv_step(ctypes.byref(prob), _ptr(x), _ptr(weight), _ptr(bias), _ptr(state), _ptr(slots),
+                                        num_slots, _ptr(y), _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_conv_step")
+
+
+def conv_forward(x, weight, bias=None, activation: str = "silu", taps=None, cu_seqlens=None, stream=None):
+    """Causal short convolution of each channel of x [b, T, D] (or [T, D]): weight [D, K] with the present step's tap last,
+    bias [D] of its type or None, activation "silu" or "none"; ``taps`` [b, K - 1, D]: the inputs before the first step,
+    oldest first (None: zeros).  Returns (y, the taps that follow each sequence).  ``cu_seqlens``: packed sequences;
+    ``stream``: as for ``delta_forward``."""
+    if stream is not None:
+        with _on(stream, x.device, x, weight, bias, taps, cu_seqlens):
+            return conv_forward(x, weight, bias, activation, taps, cu_seqlens)
+    key = _conv_of(x, weight, activation, cu_seqlens)
+    prob = _keep(key, lambda: _conv_struct(key))
+    _dense("bias", bias, (key[7],), weight.dtype)
+    _dense("taps", taps, (key[5], key[8] - 1, key[7]), x.dtype)
+    at = _device(x, weight, bias, taps, cu_seqlens)
+    y = _like(x)
+    last = torch.empty((key[5], max(key[8] - 1, 0), key[7]), dtype=x.dtype, device=x.device)
+    ssd_conv_forward(prob, x, weight, bias, taps, cu_seqlens, y, last, _stream(None, at))
+    return y, last
+
+
+def conv_backward(dy, x, weight, bias=None, activation: str = "silu", taps=None, cu_seqlens=None, stream=None, workspace=None):
+    """The gradients of ``conv_forward``'s y: a dict with dx, dw, db (None without a bias) and dtaps (None without taps)."""
+    if stream is not None:
+        with _on(stream, x.device, dy, x, weight, bias, taps, cu_seqlens, workspace and workspace[0]):
+            return conv_backward(dy, x, weight, bias, activation, taps, cu_seqlens, None, workspace)
+    key = _conv_of(x, weight, activation, cu_seqlens)
+    prob = _keep(key, lambda: _conv_struct(key))
+    _same("dy", dy, x)
+    _dense("bias", bias, (key[7],), weight.dtype)
+    _dense("taps", taps, (key[5], key[8] - 1, key[7]), x.dtype)
+    at = _device(x, dy, weight, bias, taps, cu_seqlens, workspace and workspace[0])
+    out = {"dx": _like(x), "dw": _like(weight), "db": None if bias is None else _like(bias),
+           "dtaps": None if taps is None else _like(taps)}
+    if workspace is None:
+        n = _keep(key + ("ws",), lambda: ssd_conv_workspace_size(prob))
+        workspace = torch.empty(n, dtype=torch.uint8, device=x.device), n
+    ssd_conv_backward(prob, dy, x, weight, bias, taps, cu_seqlens, out["dx"], out["dw"], out["db"], out["dtaps"],
+                      workspace[0], workspace[1], _stream(None, at))
+    return out
+
+
+def conv_step(x, weight, bias, state, slots=None, activation: str = "silu", stream=None):
+    """The steps x [b, T, D] of each of b sequences on its slot of ``state`` [slots, K - 1, D] (x's type: the last inputs,
+    oldest first), which is updated in place; returns y.  ``slots``: as for ``glr_step``."""
+    if stream is not None:
+        with _on(stream, x.device, x, weight, bias, state, slots):
+            return conv_step(x, weight, bias, state, slots, activation)
+    key = _conv_of(x, weight, activation)
+    prob = _keep(key, lambda: _conv_struct(key))
+    _dense("bias", bias, (key[7],), weight.dtype)
+    ns = state.shape[0]
+    _dense("state", state, (ns, key[8] - 1, key[7]), x.dtype)
+    _dense("slots", slots, (key[5],), torch.int32)
+    at = _device(x, weight, bias, state, slots)
+    y = _like(x)
+    ssd_conv_step(prob, x, weight, bias, state, slots, ns, y, _stream(None, at))
+    return y
