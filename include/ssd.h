@@ -650,6 +650,61 @@ ssd_status ssd_conv_step(const ssd_conv_problem* prob, const void* x, const void
                          const int32_t* slots, int64_t num_slots, void* y, void* cuda_stream);
 
 /*
+ * The gated feed-forward: both projections, the activation and the product in
+ * one pass, and its gradients.
+ *     G = x Wg^T,   U = x Wu^T,   h = act(G) U
+ * with act SiLU (G s(G)) or GELU in its tanh form.
+ *
+ * ssd_ffn_problem:
+ *   io_dtype    of every tensor: SSD_BF16 (SSD_F32 returns SSD_ERR_DTYPE).
+ *               Products are summed in fp32.
+ *   activation  SSD_ACT_SILU or SSD_ACT_GELU.
+ *   rows (M), dim (D), hidden (F): >= 1.  Limits of this build (SSD_ERR_SHAPE):
+ *               D and F multiples of 8 up to 2^20, M up to 2^24.
+ *   x_stride    elements from a row of x to the next, a multiple of 8 (0:
+ *               dense).  Everything else is dense.
+ * Layouts: x, dx [M,D]; w_gate, w_up, dw_gate, dw_up [F,D]; h, dh [M,F].
+ * Every pointer is 16-byte aligned.  Outputs must not overlap inputs.
+ *
+ * Precision.  h is rounded once.  The stash holds G and U in bf16, and the
+ * backward's products read dG and dU in bf16: each of these roundings is at
+ * most 2^-9 of a value, so the gradients are good to some 2^-8 of the sums'
+ * size, as those of a layer whose tensors are bf16.  A NaN or infinity reaches
+ * its own row of h and dx, and every element of the weights' gradients that
+ * sums over that row.
+ *
+ * ssd_ffn_stash_size: bytes of the stash that a training forward may keep for
+ *   its backward (4 F bytes for each of M rows, M rounded up to 128).
+ *   Host-only.
+ * ssd_ffn_workspace_size: device workspace of ssd_ffn_forward (backward == 0) or
+ *   ssd_ffn_backward; stashed != 0: of the call with a stash, which needs less.
+ *   Host-only.  Its first 4 bytes are the device status word, as for
+ *   ssd_forward.
+ * ssd_ffn_forward: h; the stash is filled unless NULL.
+ * ssd_ffn_backward: dx, dw_gate and dw_up of <dh, h> from the leaf inputs, as
+ *   passed to the forward.  Without the stash of a forward of the same problem
+ *   and inputs G and U are made again; the results are the same bit for bit.
+ * Errors as for ssd_forward; every error is returned before anything is
+ * enqueued.  Results are bitwise reproducible.
+ */
+typedef struct {
+  int32_t io_dtype;
+  int32_t activation;
+  int64_t rows;
+  int64_t dim;
+  int64_t hidden;
+  int64_t x_stride;
+} ssd_ffn_problem;
+
+ssd_status ssd_ffn_stash_size(const ssd_ffn_problem* prob, size_t* bytes);
+ssd_status ssd_ffn_workspace_size(const ssd_ffn_problem* prob, int backward, int stashed, size_t* bytes);
+ssd_status ssd_ffn_forward(const ssd_ffn_problem* prob, const void* x, const void* w_gate, const void* w_up, void* h,
+                           void* stash, size_t stash_bytes, void* ws, size_t ws_bytes, void* cuda_stream);
+ssd_status ssd_ffn_backward(const ssd_ffn_problem* prob, const void* dh, const void* x, const void* w_gate, const void* w_up,
+                            void* dx, void* dw_gate, void* dw_up, const void* stash, size_t stash_bytes, void* ws,
+                            size_t ws_bytes, void* cuda_stream);
+
+/*
  * Per-launch timing, for diagnostics and roofline measurement.
  *
  * ssd_profile_start(capacity): every later ssd_forward / ssd_backward call

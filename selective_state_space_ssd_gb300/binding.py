@@ -48,7 +48,8 @@ EXPORTS = ("ssd_workspace_size", "ssd_forward", "ssd_backward", "ssd_forward_sta
            "ssd_delta_stash_size", "ssd_delta_forward", "ssd_delta_backward", "ssd_delta_step",
            "ssd_norm_workspace_size", "ssd_norm_forward", "ssd_norm_backward", "ssd_glr_workspace_size",
            "ssd_glr_stash_size", "ssd_glr_forward", "ssd_glr_backward", "ssd_glr_step", "ssd_conv_workspace_size",
-           "ssd_conv_forward", "ssd_conv_backward", "ssd_conv_step")
+           "ssd_conv_forward", "ssd_conv_backward", "ssd_conv_step", "ssd_ffn_workspace_size", "ssd_ffn_stash_size",
+           "ssd_ffn_forward", "ssd_ffn_backward")
 
 
 class ssd_kda_problem(ctypes.Structure):
@@ -79,6 +80,11 @@ class ssd_conv_problem(ctypes.Structure):
     _fields_ = [("io_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("packed", ctypes.c_int32),
                 ("activation", ctypes.c_int32), ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("dim", ctypes.c_int64), ("taps", ctypes.c_int64), ("x_stride", ctypes.c_int64)]
+
+
+class ssd_ffn_problem(ctypes.Structure):
+    _fields_ = [("io_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("hidden", ctypes.c_int64), ("x_stride", ctypes.c_int64)]
 
 
 class ssd_kernel_time(ctypes.Structure):
@@ -184,6 +190,15 @@ def load(path: str | None = None):
         lib.ssd_conv_backward.restype = i32
         lib.ssd_conv_step.argtypes = [cp] + [vp] * 5 + [i64, vp, vp]
         lib.ssd_conv_step.restype = i32
+        fp = ctypes.POINTER(ssd_ffn_problem)
+        lib.ssd_ffn_workspace_size.argtypes = [fp, i32, i32, ctypes.POINTER(sz)]
+        lib.ssd_ffn_workspace_size.restype = i32
+        lib.ssd_ffn_stash_size.argtypes = [fp, ctypes.POINTER(sz)]
+        lib.ssd_ffn_stash_size.restype = i32
+        lib.ssd_ffn_forward.argtypes = [fp] + [vp] * 5 + [sz, vp, sz, vp]
+        lib.ssd_ffn_forward.restype = i32
+        lib.ssd_ffn_backward.argtypes = [fp] + [vp] * 8 + [sz, vp, sz, vp]
+        lib.ssd_ffn_backward.restype = i32
         _lib = lib
         return lib
 
@@ -677,7 +692,7 @@ def check_status(status) -> None:
     waiting for it, and raises SSDError if a kernel's wait gave up: results of those calls are missing or wrong."""
     code = int(status)
     if code:
-        raise SSDError(SSD_ERR_TIMEOUT, f"delta rule (device status word {code})")
+        raise SSDError(SSD_ERR_TIMEOUT, f"device status word {code}")
 
 
 def _join_status(status, ws) -> None:
@@ -1145,3 +1160,116 @@ def conv_step(x, weight, bias, state, slots=None, activation: str = "silu", stre
     y = _like(x)
     ssd_conv_step(prob, x, weight, bias, state, slots, ns, y, _stream(None, at))
     return y
+
+
+# ------------------------------------------------------------- gated feed-forward
+def _ffn_of(x, w_gate, activation) -> tuple:
+    """The key of a call's problem: (kind, type, activation, rows, width, hidden width, stride)."""
+    dim = x.shape[-1]
+    if w_gate.dim() != 2 or w_gate.shape[1] != dim:
+        raise ValueError(f"w_gate: shape {tuple(w_gate.shape)}, expected [hidden, {dim}]")
+    stride = 0
+    if not x.is_contiguous():
+        if x.dim() != 2 or (dim > 1 and x.stride(1) != 1) or x.stride(0) < dim:
+            raise ValueError(f"x: strides {tuple(x.stride())}: rows have to be dense, at one stride")
+        stride = x.stride(0)
+    return "ffn", x.dtype, _act(activation), x.numel() // max(dim, 1), dim, w_gate.shape[0], stride
+
+
+def _ffn_struct(key: tuple) -> ssd_ffn_problem:
+    return ssd_ffn_problem(DTYPES[_name(key[1])], *key[2:])
+
+
+def ffn_problem(x, w_gate, activation: str = "silu") -> ssd_ffn_problem:
+    """An ``ssd_ffn_problem`` for x [.., D] (contiguous, or two-dimensional with a stride from row to row) and w_gate [F, D]."""
+    return _ffn_struct(_ffn_of(x, w_gate, activation))
+
+
+def ssd_ffn_workspace_size(prob: ssd_ffn_problem, backward: bool, stashed: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().ssd_ffn_workspace_size(ctypes.byref(prob), int(bool(backward)), int(bool(stashed)), ctypes.byref(out))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_ffn_workspace_size")
+    return out.value
+
+
+def ssd_ffn_stash_size(prob: ssd_ffn_problem) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().ssd_ffn_stash_size(ctypes.byref(prob), ctypes.byref(out))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_ffn_stash_size")
+    return out.value
+
+
+def ssd_ffn_forward(prob, x, w_gate, w_up, h, stash, stash_bytes, ws, ws_bytes, stream=None) -> None:
+    st = (_lib or load()).ssd_ffn_forward(ctypes.byref(prob), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(h), _ptr(stash),
+                                          stash_bytes, _ptr(ws), ws_bytes, _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_ffn_forward")
+
+
+def ssd_ffn_backward(prob, dh, x, w_gate, w_up, dx, dw_gate, dw_up, stash, stash_bytes, ws, ws_bytes, stream=None) -> None:
+    st = (_lib or load()).ssd_ffn_backward(ctypes.byref(prob), _ptr(dh), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(dx),
+                                           _ptr(dw_gate), _ptr(dw_up), _ptr(stash), stash_bytes, _ptr(ws), ws_bytes,
+                                           _stream(stream))
+    if st != SSD_OK:
+        raise SSDError(st, "ssd_ffn_backward")
+
+
+def ffn_stash(x, w_gate):
+    """A buffer for what ``ffn_forward`` keeps for ``ffn_backward`` (uint8)."""
+    key = _ffn_of(x, w_gate, "silu")
+    n = _keep(key + ("stash",), lambda: ssd_ffn_stash_size(_ffn_struct(key)))
+    return torch.empty(n, dtype=torch.uint8, device=x.device)
+
+
+def _ffn_workspace(key, prob, backward, stashed, device):
+    n = _keep(key + (backward, stashed), lambda: ssd_ffn_workspace_size(prob, backward, stashed))
+    return torch.empty(n, dtype=torch.uint8, device=device), n
+
+
+def _ffn_check(key, x, w_gate, w_up, status):
+    shape = (key[5], key[4])
+    _dense("w_gate", w_gate, shape, x.dtype)
+    _dense("w_up", w_up, shape, x.dtype)
+    _dense("status", status, (1,), torch.int32)
+
+
+def ffn_forward(x, w_gate, w_up, activation: str = "silu", stash=None, stream=None, workspace=None, status=None):
+    """h = act(x w_gate^T) (x w_up^T) of x [.., D] (bf16) and w_gate, w_up [F, D]; activation "silu" or "gelu" (tanh form).
+    Returns h [.., F].  ``stash`` (``ffn_stash``) is filled for ``ffn_backward``; ``stream`` and ``status``: as for
+    ``delta_forward``."""
+    if stream is not None:
+        with _on(stream, x.device, x, w_gate, w_up, stash, workspace and workspace[0], status):
+            return ffn_forward(x, w_gate, w_up, activation, stash, None, workspace, status)
+    key = _ffn_of(x, w_gate, activation)
+    prob = _keep(key, lambda: _ffn_struct(key))
+    _ffn_check(key, x, w_gate, w_up, status)
+    at = _device(x, w_gate, w_up, stash, status, workspace and workspace[0])
+    h = torch.empty(x.shape[:-1] + (key[5],), dtype=x.dtype, device=x.device)
+    ws, n = workspace if workspace is not None else _ffn_workspace(key, prob, False, stash is not None, x.device)
+    ssd_ffn_forward(prob, x, w_gate, w_up, h, stash, 0 if stash is None else stash.numel(), ws, n, _stream(None, at))
+    if status is not None:
+        _join_status(status, ws)
+    return h
+
+
+def ffn_backward(dh, x, w_gate, w_up, activation: str = "silu", stash=None, stream=None, workspace=None, status=None):
+    """The gradients of ``ffn_forward``: a dict with dx (contiguous), dwg and dwu.  ``stash``: what ``ffn_forward`` filled on
+    the same inputs; without it both projections are made again.  ``status``: as for ``delta_forward``."""
+    if stream is not None:
+        with _on(stream, x.device, dh, x, w_gate, w_up, stash, workspace and workspace[0], status):
+            return ffn_backward(dh, x, w_gate, w_up, activation, stash, None, workspace, status)
+    key = _ffn_of(x, w_gate, activation)
+    prob = _keep(key, lambda: _ffn_struct(key))
+    _ffn_check(key, x, w_gate, w_up, status)
+    if dh.dtype != x.dtype or dh.shape != x.shape[:-1] + (key[5],) or not dh.is_contiguous():
+        raise ValueError(f"dh: {dh.dtype} {tuple(dh.shape)}, expected contiguous {x.dtype} {tuple(x.shape[:-1]) + (key[5],)}")
+    at = _device(x, dh, w_gate, w_up, stash, status, workspace and workspace[0])
+    out = {"dx": _like(x), "dwg": _like(w_gate), "dwu": _like(w_up)}
+    ws, n = workspace if workspace is not None else _ffn_workspace(key, prob, True, stash is not None, x.device)
+    ssd_ffn_backward(prob, dh, x, w_gate, w_up, out["dx"], out["dwg"], out["dwu"], stash,
+                     0 if stash is None else stash.numel(), ws, n, _stream(None, at))
+    if status is not None:
+        _join_status(status, ws)
+    return out

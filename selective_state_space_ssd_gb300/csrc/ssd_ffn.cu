@@ -1,0 +1,453 @@
+// The gated feed-forward: h = act(G) U with G = x Wg^T and U = x Wu^T, and its gradients
+//     dU = dh act(G),  dG = dh U act'(G),  dx = dG Wg + dU Wu,  dWg = dG^T x,  dWu = dU^T x
+// in four kernels: forward (both projections, the activation and the product), the elementwise dG and dU, dx, and both
+// weights' gradients.  The three products run on the tensor cores: bf16 operands by TMA into 128-byte swizzled tiles, fp32
+// accumulators in tensor memory.
+//
+// One kernel for the three, k_ffn_product: output tiles of 128 x 256, one block an SM that walks over tiles; a warp issues
+// the copies, one the products, four turn accumulators into results while the next tile is under way (two accumulators of
+// 256 columns).  In the forward's tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets both.
+//
+// The training forward keeps G and U, rounded to bf16, for the backward (their rounding is that of the tensors a training
+// step holds anyway; dG and dU are rounded to bf16 too, as operands of the tensor cores have to be).  The stash lies in
+// pieces of eight columns by 128 rows, as the forward's threads write them: [row tile][F / 8][128][8], G first, then U.
+#include <initializer_list>
+
+#include "ssd.h"
+#include "ssd_device.cuh"
+#include "ssd_internal.h"
+#include "tc_common.cuh"
+#include "vec_io.cuh"
+
+namespace ssd {
+namespace ffn {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int kStages = 4, kThreads = 256, kSMs = 152;
+constexpr int kBytesA = BM * BK * 2, kBytesB = BN * BK * 2, kBytesStage = kBytesA + kBytesB;
+constexpr int kBytesOut = 2 * BM * 64 * 2;  // two tiles of 64 columns on their way out
+constexpr int kSmem = kStages * kBytesStage + kBytesOut + 1024 + 256;
+constexpr int kGroup = 16;  // row tiles that are walked over together, so that their operands stay in L2
+
+enum Kind { kForward, kDx, kDw };
+
+struct Args {
+  int M, D, F;
+  bool gelu;
+  long long xs;
+};
+
+// Operands a (rows of the result), b (its columns), results o; two of each where the call has two matrices.
+struct Maps {
+  CUtensorMap a[2], b[2], o[2];
+};
+struct Plan {
+  int m_tiles, n_tiles, steps;  // steps of BK
+  int half;                     // kDx: steps of the first matrix pair; kDw: row tiles of the first matrix
+};
+
+__device__ __forceinline__ void act_and_slope(float g, bool gelu, float& a, float& s) {
+  if (gelu) {
+    // tanh form: g s(2 z) with z = sqrt(2 / pi) (g + 0.044715 g^3)
+    const float c = 1.5957691216057308f, e = __expf(fminf(-c * fmaf(0.044715f * g * g, g, g), 80.f));
+    const float q = __fdividef(1.f, 1.f + e);
+    a = g * q;
+    s = fmaf(g * q * (e * q), c * fmaf(3.f * 0.044715f * g, g, 1.f), q);
+  } else {
+    const float e = __expf(fminf(-g, 80.f)), q = __fdividef(1.f, 1.f + e);
+    a = g * q;
+    s = q * fmaf(g, e * q, 1.f);
+  }
+}
+
+__device__ __forceinline__ void tile_of(const Plan& p, int t, int& m, int& n) {
+  const int per = kGroup * p.n_tiles, g = t / per, m0 = g * kGroup, gm = min(kGroup, p.m_tiles - m0), r = t - g * per;
+  m = m0 + r % gm;
+  n = r / gm;
+}
+
+// Registers of a tcgen05.ld after its wait: nothing that reads them may be moved in front of this.
+__device__ __forceinline__ void settled(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+template <int kKind>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_ffn_product(const __grid_constant__ Maps maps, Plan plan, Args args, bf16* stash, int* status) {
+  constexpr bool kAmn = kKind == kDw, kBmn = kKind != kForward;
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+  uint8_t* out = smem + kStages * kBytesStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(out + kBytesOut);
+  uint64_t *full = bars, *empty = bars + kStages, *tfull = bars + 2 * kStages, *tempty = tfull + 2;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    for (int s = 0; s < 2; ++s) mbar_init(tfull + s, 1), mbar_init(tempty + s, 4);
+    mbar_init_fence();
+    if (kKind == kForward && blockIdx.x == 0) *status = 0;
+  }
+  if (warp == 2) tmem_alloc(slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *slot;
+  const int tiles = plan.m_tiles * plan.n_tiles;
+
+  if (warp == 0) {  // copies
+    const auto load = [&](int s, int m, int n, int k) {
+      uint8_t *a = smem + s * kBytesStage, *b = a + kBytesA;
+      mbar_expect_tx(full + s, kBytesStage);
+      if (kKind == kForward) {
+        tma_load_2d(a, &maps.a[0], k * BK, m * BM, full + s);
+        tma_load_2d(b, &maps.b[0], k * BK, n * 128, full + s);
+        tma_load_2d(b + kBytesB / 2, &maps.b[1], k * BK, n * 128, full + s);
+      } else if (kKind == kDx) {
+        const int which = k >= plan.half, kk = (k - (which ? plan.half : 0)) * BK;
+        tma_load_2d(a, &maps.a[which], kk, m * BM, full + s);
+#pragma unroll
+        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.b[which], n * BN + j * 64, kk, full + s);
+      } else {
+        const int which = m >= plan.half, row = (m - (which ? plan.half : 0)) * BM;
+#pragma unroll
+        for (int j = 0; j < BM / 64; ++j) tma_load_2d(a + j * 8192, &maps.a[which], row + j * 64, k * BK, full + s);
+#pragma unroll
+        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.b[0], n * BN + j * 64, k * BK, full + s);
+      }
+    };
+    int it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      int m, n;
+      tile_of(plan, t, m, n);
+      for (int k = 0; k < plan.steps; ++k, ++it) {
+        const int s = it % kStages;
+        if (it >= kStages && !(ok = mbar_wait(empty + s, (it / kStages - 1) & 1, status, 1))) break;
+        if (elect_one()) load(s, m, n, k);
+        __syncwarp();
+      }
+    }
+    // what is still on its way has to arrive before the block may end
+    for (int j = max(0, it - kStages); j < it; ++j) mbar_wait(full + j % kStages, (j / kStages) & 1, status, 2);
+  } else if (warp == 1) {  // products
+    constexpr uint32_t idesc = idesc_bf16(BM, BN, kAmn, kBmn);
+    int it = 0, done = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++done) {
+      const int acc = done & 1;
+      if (done >= 2 && !(ok = mbar_wait(tempty + acc, (done / 2 - 1) & 1, status, 3))) break;
+      tc_fence_after();
+      for (int k = 0; k < plan.steps; ++k, ++it) {
+        const int s = it % kStages;
+        if (!(ok = mbar_wait(full + s, (it / kStages) & 1, status, 4))) break;
+        tc_fence_after();
+        uint8_t *a = smem + s * kBytesStage, *b = a + kBytesA;
+        const uint64_t da = kAmn ? mdesc(a, BK, 0) : kdesc(a, BM, 0), db = kBmn ? mdesc(b, BK, 0) : kdesc(b, BN, 0);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < BK; kk += 16)
+            mma_bf16(tmem + acc * BN, da + (kAmn ? mdesc_step(kk) : kdesc_step(BM, kk)),
+                     db + (kBmn ? mdesc_step(kk) : kdesc_step(BN, kk)), idesc, k > 0 || kk > 0);
+          mma_commit(empty + s);
+        }
+        __syncwarp();
+      }
+      if (elect_one()) mma_commit(tfull + acc);
+      __syncwarp();
+    }
+    // the last products have to end before the tensor memory is given back
+    for (int d = max(0, done - 2); ok && d < done; ++d) mbar_wait(tfull + (d & 1), (d / 2) & 1, status, 5);
+  } else if (warp >= 4) {  // results
+    const int q = warp & 3, row = q * 32 + lane;
+    int done = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++done) {
+      int m, n;
+      tile_of(plan, t, m, n);
+      const int acc = done & 1;
+      const bool ok = mbar_wait(tfull + acc, (done / 2) & 1, status, 6);
+      if (named_bar_or(1, 128, !ok)) break;
+      tc_fence_after();
+      const uint32_t base = taddr(tmem, q * 32, acc * BN);
+      if (kKind == kForward) {
+        if (q == 0 && lane == 0) tma_store_wait_read0();
+        named_bar(1, 128);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t g[32], u[32];
+          tmem_ld32_nowait(base + c * 32, g);
+          tmem_ld32_nowait(base + 128 + c * 32, u);
+          tmem_wait_ld();
+          settled(g), settled(u);
+          float h[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float a, s;
+            act_and_slope(__uint_as_float(g[e]), args.gelu, a, s);
+            h[e] = a * __uint_as_float(u[e]);
+          }
+          store_row_bf16(out + (c >> 1) * (BM * 128), row, (c & 1) * 4, h, 4);
+          if (stash) {
+            const size_t half = (size_t)plan.m_tiles * BM * args.F;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int f = n * 128 + c * 32 + j * 8;
+              if (f >= args.F) break;
+              bf16* to = stash + (((size_t)m * (args.F / 8) + f / 8) * BM + row) * 8;
+              const auto word = [](const uint32_t* v) { return pack_bf16(__uint_as_float(v[0]), __uint_as_float(v[1])); };
+              *reinterpret_cast<uint4*>(to) =
+                  make_uint4(word(g + 8 * j), word(g + 8 * j + 2), word(g + 8 * j + 4), word(g + 8 * j + 6));
+              *reinterpret_cast<uint4*>(to + half) =
+                  make_uint4(word(u + 8 * j), word(u + 8 * j + 2), word(u + 8 * j + 4), word(u + 8 * j + 6));
+            }
+          }
+        }
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(tempty + acc);
+        fence_proxy_async();
+        named_bar(1, 128);
+        if (q == 0 && lane == 0) {
+          tma_store_2d(&maps.o[0], out, n * 128, m * BM);
+          if (n * 128 + 64 < args.F) tma_store_2d(&maps.o[0], out + BM * 128, n * 128 + 64, m * BM);
+          tma_store_commit();
+        }
+      } else {
+        const int which = kKind == kDw && m >= plan.half, row0 = (m - (which ? plan.half : 0)) * BM;
+#pragma unroll 1
+        for (int p = 0; p < BN / 64; ++p) {
+          uint32_t v[2][32];
+          tmem_ld32_nowait(base + p * 64, v[0]);
+          tmem_ld32_nowait(base + p * 64 + 32, v[1]);
+          if (q == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          tmem_wait_ld();
+          settled(v[0]), settled(v[1]);
+          named_bar(1, 128);
+          uint8_t* to = out + (p & 1) * (BM * 128);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float f[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[c][e]);
+            store_row_bf16(to, row, c * 4, f, 4);
+          }
+          fence_proxy_async();
+          named_bar(1, 128);
+          if (q == 0 && lane == 0) {
+            if (n * BN + p * 64 < args.D) tma_store_2d(&maps.o[which], to, n * BN + p * 64, row0);
+            tma_store_commit();
+          }
+        }
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(tempty + acc);
+      }
+    }
+    if (q == 0 && lane == 0) tma_store_wait0();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// dG and dU of the stashed G and U: a warp has eight rows of four pieces of eight columns.  status: cleared, where this is
+// a call's first kernel (the forward's product clears it where that is).
+__global__ void __launch_bounds__(256)
+    k_ffn_gates(Args a, const bf16* __restrict__ stash, const bf16* __restrict__ dh, bf16* dg, bf16* du, int* status) {
+  if (status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int f = (blockIdx.y * 32 + warp * 4 + (lane & 3)) * 8;
+  const int row = blockIdx.x * 8 + (lane >> 2);
+  if (row >= a.M || f >= a.F) return;
+  const size_t half = (size_t)((a.M + BM - 1) / BM) * BM * a.F;
+  const bf16* from = stash + (((size_t)(row / BM) * (a.F / 8) + f / 8) * BM + row % BM) * 8;
+  const uint4 g4 = *reinterpret_cast<const uint4*>(from), u4 = *reinterpret_cast<const uint4*>(from + half);
+  const uint4 d4 = *reinterpret_cast<const uint4*>(dh + (size_t)row * a.F + f);
+  const uint32_t g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
+  uint32_t og[4], ou[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float gv[2], uv[2], dv[2], x[2], y[2];
+    unpack(g[e], gv);
+    unpack(u[e], uv);
+    unpack(d[e], dv);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float act, slope;
+      act_and_slope(gv[k], a.gelu, act, slope);
+      x[k] = dv[k] * uv[k] * slope;
+      y[k] = dv[k] * act;
+    }
+    og[e] = pack2(x[0], x[1]);
+    ou[e] = pack2(y[0], y[1]);
+  }
+  *reinterpret_cast<uint4*>(dg + (size_t)row * a.F + f) = make_uint4(og[0], og[1], og[2], og[3]);
+  *reinterpret_cast<uint4*>(du + (size_t)row * a.F + f) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+}
+
+struct Call {
+  Args a;
+  const void *x, *wg, *wu, *dh;
+  void *h, *dx, *dwg, *dwu;
+  bf16 *stash, *dg, *du;
+  int* status;
+};
+
+cudaError_t map(CUtensorMap* m, const void* p, int cols, int rows, long long stride, int box_cols, int box_rows) {
+  return make_tmap_rows_bf16(m, p, cols, rows, stride, box_cols, box_rows);
+}
+
+template <int kKind>
+cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const Call& c, cudaStream_t st) {
+  const auto kernel = k_ffn_product<kKind>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  const int tiles = plan.m_tiles * plan.n_tiles;
+  SSD_LAUNCH(name, st,
+             kernel<<<tiles < kSMs ? tiles : kSMs, kThreads, kSmem, st>>>(maps, plan, c.a, kKind == kForward ? c.stash : nullptr,
+                                                                          c.status));
+  return cudaGetLastError();
+}
+
+int up(long long a, int b) { return (int)((a + b - 1) / b); }
+
+cudaError_t forward(const Call& c, cudaStream_t st) {
+  Maps maps;
+  cudaError_t e = map(&maps.a[0], c.x, c.a.D, c.a.M, c.a.xs, BK, BM);
+  if (e == cudaSuccess) e = map(&maps.b[0], c.wg, c.a.D, c.a.F, c.a.D, BK, 128);
+  if (e == cudaSuccess) e = map(&maps.b[1], c.wu, c.a.D, c.a.F, c.a.D, BK, 128);
+  if (e == cudaSuccess) e = map(&maps.o[0], c.h, c.a.F, c.a.M, c.a.F, 64, BM);
+  if (e != cudaSuccess) return e;
+  maps.a[1] = maps.a[0], maps.o[1] = maps.o[0];
+  return launch<kForward>("k_ffn_forward", maps, Plan{up(c.a.M, BM), up(c.a.F, 128), up(c.a.D, BK), 0}, c, st);
+}
+
+cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
+  const Args& a = c.a;
+  SSD_LAUNCH("k_ffn_gates", st,
+             k_ffn_gates<<<dim3(up(a.M, 8), up(a.F, 256)), 256, 0, st>>>(a, c.stash, (const bf16*)c.dh, c.dg, c.du,
+                                                                     first ? c.status : nullptr));
+  cudaError_t e = cudaGetLastError();
+  Maps maps;
+  if (e == cudaSuccess) e = map(&maps.a[0], c.dg, a.F, a.M, a.F, BK, BM);
+  if (e == cudaSuccess) e = map(&maps.a[1], c.du, a.F, a.M, a.F, BK, BM);
+  if (e == cudaSuccess) e = map(&maps.b[0], c.wg, a.D, a.F, a.D, 64, BK);
+  if (e == cudaSuccess) e = map(&maps.b[1], c.wu, a.D, a.F, a.D, 64, BK);
+  if (e == cudaSuccess) e = map(&maps.o[0], c.dx, a.D, a.M, a.D, 64, BM);
+  if (e != cudaSuccess) return e;
+  maps.o[1] = maps.o[0];
+  e = launch<kDx>("k_ffn_dx", maps, Plan{up(a.M, BM), up(a.D, BN), 2 * up(a.F, BK), up(a.F, BK)}, c, st);
+  if (e == cudaSuccess) e = map(&maps.a[0], c.dg, a.F, a.M, a.F, 64, BK);
+  if (e == cudaSuccess) e = map(&maps.a[1], c.du, a.F, a.M, a.F, 64, BK);
+  if (e == cudaSuccess) e = map(&maps.b[0], c.x, a.D, a.M, a.xs, 64, BK);
+  if (e == cudaSuccess) e = map(&maps.o[0], c.dwg, a.D, a.F, a.D, 64, BM);
+  if (e == cudaSuccess) e = map(&maps.o[1], c.dwu, a.D, a.F, a.D, 64, BM);
+  if (e != cudaSuccess) return e;
+  maps.b[1] = maps.b[0];
+  return launch<kDw>("k_ffn_dw", maps, Plan{2 * up(a.F, BM), up(a.D, BN), up(a.M, BK), up(a.F, BM)}, c, st);
+}
+
+ssd_status make_args(const ssd_ffn_problem* p, Args* a) {
+  if (!p) return SSD_ERR_INVALID_ARG;
+  if (p->io_dtype != SSD_F32 && p->io_dtype != SSD_BF16) return SSD_ERR_INVALID_ARG;
+  if (p->activation != SSD_ACT_SILU && p->activation != SSD_ACT_GELU) return SSD_ERR_INVALID_ARG;
+  if (p->rows < 1 || p->dim < 1 || p->hidden < 1 || p->x_stride < 0) return SSD_ERR_INVALID_ARG;
+  if (p->io_dtype != SSD_BF16) return SSD_ERR_DTYPE;
+  const int64_t most = 1 << 20;
+  if (p->dim > most || p->hidden > most || p->rows > (1 << 24) || p->dim % 8 || p->hidden % 8 || p->x_stride % 8 ||
+      (p->x_stride && p->x_stride < p->dim) || p->x_stride >= (1ll << 38))
+    return SSD_ERR_SHAPE;
+  *a = Args{(int)p->rows, (int)p->dim, (int)p->hidden, p->activation == SSD_ACT_GELU, p->x_stride ? p->x_stride : p->dim};
+  return SSD_OK;
+}
+
+size_t stash_elems(const Args& a) { return 2 * (size_t)up(a.M, BM) * BM * a.F; }
+
+size_t workspace(Call* c, bool back, bool stashed, void* ws) {
+  Carver cv(ws);
+  c->status = static_cast<int*>(ws);
+  if (back) {
+    c->dg = cv.take<bf16>((size_t)c->a.M * c->a.F);
+    c->du = cv.take<bf16>((size_t)c->a.M * c->a.F);
+    if (!stashed) {
+      c->stash = cv.take<bf16>(stash_elems(c->a));
+      c->h = cv.take<bf16>((size_t)c->a.M * c->a.F);  // of the forward that is made again
+    }
+  }
+  return cv.off;
+}
+
+ssd_status check(std::initializer_list<const void*> req, const void* stash) {
+  for (const void* p : req)
+    if (!p) return SSD_ERR_INVALID_ARG;
+  for (const void* p : req)
+    if (off(p, 16)) return SSD_ERR_ALIGNMENT;
+  return off(stash, 16) ? SSD_ERR_ALIGNMENT : SSD_OK;
+}
+
+}  // namespace
+}  // namespace ffn
+}  // namespace ssd
+
+using namespace ssd;
+
+extern "C" {
+
+ssd_status ssd_ffn_stash_size(const ssd_ffn_problem* prob, size_t* bytes) {
+  ffn::Args a;
+  if (!bytes) return SSD_ERR_INVALID_ARG;
+  const ssd_status s = ffn::make_args(prob, &a);
+  if (s != SSD_OK) return s;
+  *bytes = ffn::stash_elems(a) * 2;
+  return SSD_OK;
+}
+
+ssd_status ssd_ffn_workspace_size(const ssd_ffn_problem* prob, int backward, int stashed, size_t* bytes) {
+  ffn::Call c = {};
+  if (!bytes) return SSD_ERR_INVALID_ARG;
+  const ssd_status s = ffn::make_args(prob, &c.a);
+  if (s != SSD_OK) return s;
+  *bytes = ffn::workspace(&c, backward != 0, stashed != 0, nullptr);
+  return SSD_OK;
+}
+
+ssd_status ssd_ffn_forward(const ssd_ffn_problem* prob, const void* x, const void* w_gate, const void* w_up, void* h,
+                           void* stash, size_t stash_bytes, void* ws, size_t ws_bytes, void* cuda_stream) {
+  ffn::Call c = {};
+  ssd_status s = ffn::make_args(prob, &c.a);
+  if (s != SSD_OK) return s;
+  if ((s = ffn::check({x, w_gate, w_up, h, ws}, stash)) != SSD_OK) return s;
+  if (stash && stash_bytes < ffn::stash_elems(c.a) * 2) return SSD_ERR_WORKSPACE;
+  if (ws_bytes < ffn::workspace(&c, false, stash != nullptr, nullptr)) return SSD_ERR_WORKSPACE;
+  ffn::workspace(&c, false, stash != nullptr, ws);
+  c.x = x, c.wg = w_gate, c.wu = w_up, c.h = h, c.stash = static_cast<bf16*>(stash);
+  return ffn::forward(c, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+ssd_status ssd_ffn_backward(const ssd_ffn_problem* prob, const void* dh, const void* x, const void* w_gate, const void* w_up,
+                            void* dx, void* dw_gate, void* dw_up, const void* stash, size_t stash_bytes, void* ws,
+                            size_t ws_bytes, void* cuda_stream) {
+  ffn::Call c = {};
+  ssd_status s = ffn::make_args(prob, &c.a);
+  if (s != SSD_OK) return s;
+  if ((s = ffn::check({dh, x, w_gate, w_up, dx, dw_gate, dw_up, ws}, stash)) != SSD_OK) return s;
+  if (stash && stash_bytes < ffn::stash_elems(c.a) * 2) return SSD_ERR_WORKSPACE;
+  if (ws_bytes < ffn::workspace(&c, true, stash != nullptr, nullptr)) return SSD_ERR_WORKSPACE;
+  ffn::workspace(&c, true, stash != nullptr, ws);
+  c.x = x, c.wg = w_gate, c.wu = w_up, c.dh = dh, c.dx = dx, c.dwg = dw_gate, c.dwu = dw_up;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e = cudaSuccess;
+  if (stash)
+    c.stash = static_cast<bf16*>(const_cast<void*>(stash));
+  else
+    e = ffn::forward(c, st);
+  if (e == cudaSuccess) e = ffn::backward(c, stash != nullptr, st);
+  return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -143,6 +143,9 @@ cudaError_t make_tmap_bc_bf16(CUtensorMap* m, const void* base, const Dims& d);
 // steps of one head, 64 columns, coordinates (col, head, step).
 cudaError_t make_tmap_heads_bf16(CUtensorMap* m, const void* base, uint64_t width, uint64_t heads, uint64_t steps,
                                  uint64_t stride);
+// [rows, cols] bf16 with `stride` elements from a row to the next (a multiple of 8).
+cudaError_t make_tmap_rows_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t stride,
+                                uint32_t box_cols, uint32_t box_rows);
 
 // Mamba-1 path (fp32).
 size_t m1_forward_ws(const Dims& d);

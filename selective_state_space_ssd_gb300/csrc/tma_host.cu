@@ -77,4 +77,12 @@ cudaError_t make_tmap_heads_bf16(CUtensorMap* m, const void* base, uint64_t widt
   return encode(m, base, 3, dims, strides, box);
 }
 
+cudaError_t make_tmap_rows_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t stride,
+                                uint32_t box_cols, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {stride * 2};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  return encode(m, base, 2, dims, strides, box);
+}
+
 }  // namespace ssd
