@@ -1,0 +1,272 @@
+// The gradients of the gated linear recurrence (the split: glr_common.cuh).  With dh_t = dy_t + D_{t+1}, D_t = a_t dh_t:
+//     dx = dh m s(i),   di = dh m u (1 - s(i)),   q = dL/dn n = dh (a n) (a u / m - h_{t-1}),   dr = q (1 - s(r)),
+//     dlam = s(lam) / softplus(lam) sum of q,   dh0 = D_0
+// n / m goes to 0 with n, so a gate that is shut has finite gradients.
+#include <type_traits>
+
+#include "glr_common.cuh"
+
+namespace ssd {
+namespace glr {
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps, L = kMark, kRun = L / kWarps;
+template <typename T>
+constexpr int stages_of() {  // tiles in shared memory or on their way there: two blocks an SM
+  return sizeof(T) == 2 ? 3 : 2;
+}
+// (a tile begins where the stash holds a state)
+
+// Tile by tile from the end.  The states of a tile are made again from its mark, and the upstream gradients' maps D -> a D +
+// a dy are joined as the states' are, in the other direction; the states are made while a cluster's barrier is under way.
+// part [axes kMostShare, D]: the sums of q, and zeros where fewer blocks share.
+template <typename T, bool kVec, bool kPacked>
+__global__ void __launch_bounds__(kThreads, 2)
+    k_glr_backward(Args a, const T* __restrict__ dy, const float* __restrict__ dh_final, const T* __restrict__ x,
+                   const T* __restrict__ r, const T* __restrict__ i, const float* __restrict__ lam,
+                   const float* __restrict__ h0, const int* __restrict__ cu, const float* __restrict__ marks, T* dx, T* dr,
+                   T* di, float* dh0, float* part) {
+  constexpr int kStages = stages_of<T>();
+  using Tile = Tiles<T, kVec, kWarps, kRun, 4>;
+  using Word = typename Words<T>::Word;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ Map fwd[2][kWarps][32], rev[2][kWarps][32];
+  __shared__ Map xchg[2][kMostShare][32];
+  __shared__ int code[3][kPacked ? L : 1];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int share = a.share, rank = blockIdx.x % share;
+  const int c0 = (int)(blockIdx.x / share) * kWidth, c = c0 + lane * 2, axis = blockIdx.y;
+  const size_t row0 = (size_t)axis * a.T;
+  const T* const from[4] = {x + row0 * a.xs, r + row0 * a.rs, i + row0 * a.is, dy + row0 * a.D};
+  const uint32_t step[4] = {(uint32_t)a.xs, (uint32_t)a.rs, (uint32_t)a.is, (uint32_t)a.D};
+  const int nt = (a.T + L - 1) / L, rounds = (nt + share - 1) / share;
+  Tile tiles(from, step, c0, a.D, a.T, (nt - 1 - rank) * L, -share);
+  const auto bring = [&](int stage) {
+    tiles.bring(ring + stage * Tile::kBytes);
+    copies_commit();
+  };
+  // (below 0: there is no such tile)
+  const auto codes = [&](int j, int place) {
+    if (kPacked && threadIdx.x < L)
+      code[place][threadIdx.x] = code_of(cu, a.N, a.T, (nt - 1 - (j * share + rank)) * L + (int)threadIdx.x);
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) bring(s);
+  codes(0, 0);
+  const P rate = load_rate(lam, c, a.D, a.scale);
+  const bool far = any_far(rate), second = c + 1 < a.D;
+  P back = !kPacked && dh_final ? load_two(dh_final + (size_t)axis * a.D, c, a.D) : both(0.f);  // D behind the round
+  P qsum = both(0.f);
+  if (kPacked && dh0 && rank == 0) empty_sequences(cu, a, c0, dh_final, dh0);
+  copies_wait<kStages - 1>();
+  __syncthreads();
+  if (share > 1) {  // (the other blocks of the cluster have begun before anything is written to them)
+    cluster_arrive_relaxed();
+    cluster_wait();
+  }
+  const uint32_t o0 = (uint32_t)(w * kRun) * a.D + c;  // from a tile's first step
+  Ring<kStages> sg;
+  Ring<3> cd;
+  for (int j = 0; j < rounds; ++j, sg.next(), cd.next()) {
+    const int tile = nt - 1 - (j * share + rank), t0 = tile < 0 ? a.T : tile * L + w * kRun;
+    const Word* stage = reinterpret_cast<const Word*>(ring + sg.at * Tile::kBytes) + w * kRun * 32 + lane;
+    // per step: a, the state's increment b, a n, a u / m, dx / dh, di / dh, 1 - s(r), dy
+    P av[kRun], bv[kRun], an[kRun], um[kRun], mi[kRun], ki[kRun], r1[kRun], up[kRun];
+    P h = tile >= 0 ? load_two(marks + ((size_t)axis * nt + tile) * a.D, c, a.D) : both(0.f);
+    const auto maps_of_steps = [&](auto is_far) {
+#pragma unroll
+      for (int s = 0; s < kRun; ++s) {
+        const auto most = [](float v) { return min_nan(v, 1e30f); };
+        const P xv = Words<T>::open(stage[s * 32]);
+        const P er = each(exp_neg(Words<T>::open(stage[(L + s) * 32])), most), sr = inv_one_more(er);
+        const P ei = each(exp_neg(Words<T>::open(stage[(2 * L + s) * 32])), most), si = inv_one_more(ei);
+        up[s] = Words<T>::open(stage[(3 * L + s) * 32]);
+        const P n = rate * sr, o = one_minus_exp<decltype(is_far)::value>(n);
+        r1[s] = er * sr;
+        av[s] = one_less(o);
+        const P m2 = o * one_more(av[s]);
+        const P rm = each(m2, [](float v) { return rsqrt_f(fmaxf(v, 1e-37f)); });  // (m2 = 0: n is 0 too)
+        const P sm = si * rm;
+        mi[s] = m2 * sm;
+        bv[s] = mi[s] * xv;
+        ki[s] = bv[s] * (ei * si);
+        an[s] = av[s] * n;
+        um[s] = av[s] * (sm * xv);
+      }
+    };
+    if (far)
+      maps_of_steps(std::true_type());
+    else
+      maps_of_steps(std::false_type());
+    const Bits bits = bits_of<kPacked, kRun>(&code[cd.at][kPacked ? w * kRun : 0], t0, a.T, lane);
+    if (bits.first | bits.none | (kPacked ? bits.last : 0)) {
+#pragma unroll
+      for (int s = 0; s < kRun; ++s) {
+        if (bits.none >> s & 1) {
+          av[s] = both(1.f), bv[s] = up[s] = both(0.f);
+          continue;
+        }
+        if (!kPacked) continue;
+        const size_t at = (size_t)(code[cd.at][w * kRun + s] & kSeq) * a.D;
+        if ((bits.last >> s & 1) && dh_final) up[s] = up[s] + load_two(dh_final + at, c, a.D);
+        if ((bits.first >> s & 1) && h0) bv[s] = fma(av[s], load_two(h0 + at, c, a.D), bv[s]);
+      }
+    }
+    Map f, b;
+    if (kPacked && bits.first) {
+      f = Map{both(1.f), both(0.f)};
+      b = f;
+#pragma unroll
+      for (int s = 0; s < kRun; ++s) f = after<true>(f, Map{bits.first >> s & 1 ? anew() : av[s], bv[s]});
+#pragma unroll
+      for (int s = kRun - 1; s >= 0; --s)  // (what a first step hands on goes to dh0, not to the step before it)
+        b = bits.first >> s & 1 ? Map{anew(), both(0.f)} : after<true>(b, Map{av[s], av[s] * up[s]});
+    } else {
+      f = Map{av[0], bv[0]};
+#pragma unroll
+      for (int s = 1; s < kRun; ++s) f = Map{f.a * av[s], fma(av[s], f.b, bv[s])};
+      b = Map{f.a, av[kRun - 1] * up[kRun - 1]};
+#pragma unroll
+      for (int s = kRun - 2; s >= 0; --s) b.b = av[s] * (up[s] + b.b);
+    }
+    fwd[j & 1][w][lane] = f;
+    rev[j & 1][w][lane] = b;
+    codes(j + 1, cd.at == 2 ? 0 : cd.at + 1);
+    // the runs' maps are there, the next tile has come, and this one's stage is free
+    copies_wait<kStages - 2>();
+    const bool resets = kPacked && __syncthreads_or(bits.first != 0);
+    if (!kPacked) __syncthreads();
+    if (share > 1) {
+      if (w == kWarps - 1) {
+        b = rev[j & 1][kWarps - 1][lane];
+#pragma unroll
+        for (int v = kWarps - 2; v >= 0; --v) b = after<kPacked>(b, rev[j & 1][v][lane]);
+        for (int k = 0; k < share; ++k) store_to(&xchg[j & 1][rank][lane], k, b);
+        cluster_arrive();
+      } else {
+        cluster_arrive_relaxed();
+      }
+    }
+    bring(sg.at);
+    // the states before each step; from here on an holds a n (a u / m - h_{t-1})
+    const auto join = [&](auto anew_too) {
+#pragma unroll
+      for (int v = 0; v < kWarps - 1; ++v)
+        if (v < w) h = through<decltype(anew_too)::value>(fwd[j & 1][v][lane], h);
+    };
+    if (kPacked && resets)
+      join(std::true_type());
+    else
+      join(std::false_type());
+#pragma unroll
+    for (int s = 0; s < kRun; ++s) {
+      const bool start = kPacked && (bits.first >> s & 1);
+      if (start)
+        h = h0 && !(bits.none >> s & 1) ? load_two(h0 + (size_t)(code[cd.at][w * kRun + s] & kSeq) * a.D, c, a.D) : both(0.f);
+      an[s] = an[s] * less(um[s], h);
+      h = start ? bv[s] : fma(av[s], h, bv[s]);
+    }
+    P d = back;  // D of the step behind this thread's
+    if (share > 1) {
+      cluster_wait();
+#pragma unroll
+      for (int v = 0; v < kMostShare; ++v) {
+        if (v == share) break;
+        if (v == rank) d = back;
+        back = through<kPacked>(xchg[j & 1][v][lane], back);
+      }
+    }
+    const auto join_back = [&](auto anew_too) {
+      constexpr bool kAnew = decltype(anew_too)::value;
+#pragma unroll
+      for (int v = kWarps - 1; v > 0; --v)
+        if (v > w) d = through<kAnew>(rev[j & 1][v][lane], d);
+      if (share == 1) {
+        back = d;
+#pragma unroll
+        for (int v = kWarps - 1; v >= 0; --v)
+          if (v <= w) back = through<kAnew>(rev[j & 1][v][lane], back);
+      }
+    };
+    if (kPacked && resets)
+      join_back(std::true_type());
+    else
+      join_back(std::false_type());
+    if (t0 >= a.T) continue;
+    const size_t at = (row0 + (size_t)tile * L) * a.D;
+    T *px = dx + at, *pr = dr + at, *pi = di + at;
+    if (!(bits.first | bits.none) && (kPacked || t0 > 0)) {
+      P q[kRun];
+#pragma unroll
+      for (int s = kRun - 1; s >= 0; --s) {
+        const P dh = up[s] + d;
+        d = av[s] * dh;
+        q[s] = dh * an[s];
+        qsum = qsum + q[s];
+        mi[s] = dh * mi[s], ki[s] = dh * ki[s];
+      }
+      if (c < a.D) {
+#pragma unroll
+        for (int s = 0; s < kRun; ++s) {
+          const uint32_t o = o0 + s * (uint32_t)a.D;
+          store_row<T, kVec>(px + o, second, mi[s]);
+          store_row<T, kVec>(pr + o, second, q[s] * r1[s]);
+          store_row<T, kVec>(pi + o, second, ki[s]);
+        }
+      }
+      continue;
+    }
+#pragma unroll
+    for (int s = kRun - 1; s >= 0; --s) {
+      const P dh = up[s] + d;
+      d = av[s] * dh;
+      P q = dh * an[s], vx = dh * mi[s], vi = dh * ki[s], vr = q * r1[s];
+      if (bits.none >> s & 1) q = vx = vi = vr = both(0.f);
+      if (dh0 && (kPacked ? (bits.first & ~bits.none) >> s & 1 : t0 + s == 0))
+        store_two(dh0 + (size_t)(kPacked ? code[cd.at][w * kRun + s] & kSeq : axis) * a.D, c, a.D, d);
+      if (kPacked && (bits.first >> s & 1)) d = both(0.f);
+      if (t0 + s >= a.T) continue;
+      qsum = qsum + q;
+      if (c < a.D) {
+        const uint32_t o = o0 + s * (uint32_t)a.D;
+        store_row<T, kVec>(px + o, second, vx);
+        store_row<T, kVec>(pr + o, second, vr);
+        store_row<T, kVec>(pi + o, second, vi);
+      }
+    }
+  }
+  copies_wait<0>();
+  // the warps' sums of q, in order
+  __syncthreads();
+  fwd[0][w][lane].a = qsum;
+  __syncthreads();
+  if (w == 0) {
+    P s = fwd[0][0][lane].a;
+#pragma unroll
+    for (int v = 1; v < kWarps; ++v) s = s + fwd[0][v][lane].a;
+    for (int k = rank; k < kMostShare; k += share)
+      store_two(part + ((size_t)axis * kMostShare + k) * a.D, c, a.D, k == rank ? s : both(0.f));
+  }
+}
+
+template <typename T, bool kVec, bool kPacked>
+cudaError_t run(const Call& c, cudaStream_t st) {
+  auto* kernel = &k_glr_backward<T, kVec, kPacked>;
+  constexpr int smem = stages_of<T>() * Tiles<T, kVec, kWarps, kRun, 4>::kBytes;
+  static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
+  return launch_cluster("k_glr_backward", kernel, fit, c.a, L, kThreads, smem, st, (const T*)c.dy, c.dh_final, (const T*)c.x,
+                        (const T*)c.r, (const T*)c.i, c.lam, c.h0, c.cu, (const float*)c.marks, (T*)c.dx, (T*)c.dr, (T*)c.di,
+                        c.dh0, c.part);
+}
+template <typename T>
+cudaError_t by_type(const Call& c, cudaStream_t st) {
+  if (whole(c, true)) return c.a.packed ? run<T, true, true>(c, st) : run<T, true, false>(c, st);
+  return c.a.packed ? run<T, false, true>(c, st) : run<T, false, false>(c, st);
+}
+
+}  // namespace
+
+cudaError_t backward(const Call& c, cudaStream_t st) { return c.a.f32 ? by_type<float>(c, st) : by_type<bf16>(c, st); }
+
+}  // namespace glr
+}  // namespace ssd

@@ -1,0 +1,190 @@
+// The gated linear recurrence over whole sequences, forward (formulas and the split: glr_common.cuh).
+#include <type_traits>
+
+#include "glr_common.cuh"
+
+namespace ssd {
+namespace glr {
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kStages = 2;  // tiles in shared memory or on their way there: 48 KiB a block, three blocks an SM
+template <typename T>
+constexpr int run_of() {  // steps a thread has of a tile
+  return sizeof(T) == 2 ? 8 : 4;
+}
+
+// y, the final states and the marks (the states that enter every kMark-th step).  Grid: (64-channel slabs x a.share,
+// sequences; one for a packed batch).  Tile j share + k of a sequence is block k's of its cluster.  One warp joins the
+// runs' maps of each tile to one that goes to all blocks of the cluster; one barrier of the cluster later each of them has
+// the state that enters its tile.
+template <typename T, bool kVec, bool kPacked>
+__global__ void __launch_bounds__(kThreads, 3)
+    k_glr_forward(Args a, const T* __restrict__ x, const T* __restrict__ r, const T* __restrict__ i,
+                  const float* __restrict__ lam, const float* __restrict__ h0, const int* __restrict__ cu, T* y,
+                  float* h_final, float* marks) {
+  constexpr int kRun = run_of<T>(), L = kRun * kWarps;
+  static_assert(L % kMark == 0 && kMark % kRun == 0, "states are kept where runs begin");
+  using Tile = Tiles<T, kVec, kWarps, kRun, 3>;
+  using Word = typename Words<T>::Word;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ Map maps[2][kWarps][32];
+  __shared__ Map xchg[2][kMostShare][32];
+  __shared__ int code[3][kPacked ? L : 1];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int share = a.share, rank = blockIdx.x % share;
+  const int c0 = (int)(blockIdx.x / share) * kWidth, c = c0 + lane * 2, axis = blockIdx.y;
+  const size_t row0 = (size_t)axis * a.T;
+  const T* const from[3] = {x + row0 * a.xs, r + row0 * a.rs, i + row0 * a.is};
+  const uint32_t step[3] = {(uint32_t)a.xs, (uint32_t)a.rs, (uint32_t)a.is};
+  Tile tiles(from, step, c0, a.D, a.T, rank * L, share);
+  const int nt = (a.T + L - 1) / L, rounds = (nt + share - 1) / share, nm = (a.T + kMark - 1) / kMark;
+  const auto bring = [&](int stage) {
+    tiles.bring(ring + stage * Tile::kBytes);
+    copies_commit();
+  };
+  const auto codes = [&](int j, int place) {
+    if (kPacked && threadIdx.x < L) code[place][threadIdx.x] = code_of(cu, a.N, a.T, (j * share + rank) * L + threadIdx.x);
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) bring(s);
+  codes(0, 0);
+  const P rate = load_rate(lam, c, a.D, a.scale);
+  const bool far = any_far(rate), second = c + 1 < a.D;
+  P carry = !kPacked && h0 ? load_two(h0 + (size_t)axis * a.D, c, a.D) : both(0.f);  // the state that enters the round
+  if (kPacked && h_final && rank == 0) empty_sequences(cu, a, c0, h0, h_final);
+  copies_wait<kStages - 1>();
+  __syncthreads();
+  if (share > 1) {  // (the other blocks of the cluster have begun before anything is written to them)
+    cluster_arrive_relaxed();
+    cluster_wait();
+  }
+  int t0 = rank * L + w * kRun;
+  T* ty = y + (row0 + rank * L) * a.D;  // the tile's first step
+  const uint32_t oy = (uint32_t)(w * kRun) * a.D + c;
+  Ring<kStages> sg;
+  Ring<3> cd;
+  for (int j = 0; j < rounds; ++j, t0 += share * L, ty += (long long)(share * L) * a.D, sg.next(), cd.next()) {
+    const Word* stage = reinterpret_cast<const Word*>(ring + sg.at * Tile::kBytes) + w * kRun * 32 + lane;
+    P av[kRun], bv[kRun];
+    const auto maps_of_steps = [&](auto is_far) {
+#pragma unroll
+      for (int s = 0; s < kRun; ++s) {
+        const P o = one_minus_exp<decltype(is_far)::value>(rate * sigmoid(Words<T>::open(stage[(L + s) * 32])));
+        av[s] = one_less(o);
+        const P m = each(o * one_more(av[s]), [](float v) { return sqrt_f(v); });
+        bv[s] = m * (sigmoid(Words<T>::open(stage[(2 * L + s) * 32])) * Words<T>::open(stage[s * 32]));
+      }
+    };
+    if (far)
+      maps_of_steps(std::true_type());
+    else
+      maps_of_steps(std::false_type());
+    const Bits bits = bits_of<kPacked, kRun>(&code[cd.at][kPacked ? w * kRun : 0], t0, a.T, lane);
+    if (bits.first | bits.none) {
+#pragma unroll
+      for (int s = 0; s < kRun; ++s) {
+        if (bits.none >> s & 1) {
+          av[s] = kPacked ? anew() : both(1.f), bv[s] = both(0.f);
+        } else if (kPacked && (bits.first >> s & 1)) {
+          if (h0) bv[s] = fma(av[s], load_two(h0 + (size_t)(code[cd.at][w * kRun + s] & kSeq) * a.D, c, a.D), bv[s]);
+          av[s] = anew();
+        }
+      }
+    }
+    Map m = {av[0], bv[0]};
+    if (kPacked && bits.first) {
+#pragma unroll
+      for (int s = 1; s < kRun; ++s) m = after<true>(m, Map{av[s], bv[s]});
+    } else {
+#pragma unroll
+      for (int s = 1; s < kRun; ++s) m = Map{m.a * av[s], fma(av[s], m.b, bv[s])};
+    }
+    maps[j & 1][w][lane] = m;
+    codes(j + 1, cd.at == 2 ? 0 : cd.at + 1);
+    // the runs' maps are there, the next tile has come, and this one's stage is free
+    copies_wait<kStages - 2>();
+    const bool resets = kPacked && __syncthreads_or(bits.first != 0);
+    if (!kPacked) __syncthreads();
+    if (share > 1) {
+      if (w == kWarps - 1) {
+        m = maps[j & 1][0][lane];
+#pragma unroll
+        for (int v = 1; v < kWarps; ++v) m = after<kPacked>(m, maps[j & 1][v][lane]);
+        for (int k = 0; k < share; ++k) store_to(&xchg[j & 1][rank][lane], k, m);
+        cluster_arrive();
+      } else {
+        cluster_arrive_relaxed();
+      }
+    }
+    bring(sg.at);
+    P h = carry;
+    if (share > 1) {
+      cluster_wait();
+#pragma unroll
+      for (int v = 0; v < kMostShare; ++v) {
+        if (v == share) break;
+        if (v == rank) h = carry;
+        carry = through<kPacked>(xchg[j & 1][v][lane], carry);
+      }
+    }
+    const auto join = [&](auto anew_too) {
+      constexpr bool kAnew = decltype(anew_too)::value;
+#pragma unroll
+      for (int v = 0; v < kWarps - 1; ++v)
+        if (v < w) h = through<kAnew>(maps[j & 1][v][lane], h);
+      if (share == 1) {
+        carry = h;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v)
+          if (v >= w) carry = through<kAnew>(maps[j & 1][v][lane], carry);
+      }
+    };
+    if (kPacked && resets)
+      join(std::true_type());
+    else
+      join(std::false_type());
+    if (t0 >= a.T) continue;
+    if (marks && t0 % kMark == 0) store_two(marks + ((size_t)axis * nm + t0 / kMark) * a.D, c, a.D, h);
+    if (bits.first | bits.last | bits.none) {
+#pragma unroll
+      for (int s = 0; s < kRun; ++s) {
+        h = through<kPacked>(Map{av[s], bv[s]}, h);
+        if (t0 + s >= a.T) continue;
+        if (y && c < a.D) store_row<T, kVec>(ty + (oy + s * (uint32_t)a.D), second, h);
+        if (h_final && (bits.last >> s & 1)) {
+          const int n = kPacked ? code[cd.at][w * kRun + s] & kSeq : axis;
+          store_two(h_final + (size_t)n * a.D, c, a.D, h);
+        }
+      }
+    } else if (y && c < a.D) {
+#pragma unroll
+      for (int s = 0; s < kRun; ++s) {
+        h = fma(av[s], h, bv[s]);
+        store_row<T, kVec>(ty + (oy + s * (uint32_t)a.D), second, h);
+      }
+    }
+  }
+  copies_wait<0>();
+}
+
+template <typename T, bool kVec, bool kPacked>
+cudaError_t run(const Call& c, cudaStream_t st) {
+  auto* kernel = &k_glr_forward<T, kVec, kPacked>;
+  constexpr int smem = kStages * Tiles<T, kVec, kWarps, run_of<T>(), 3>::kBytes;
+  static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
+  return launch_cluster("k_glr_forward", kernel, fit, c.a, run_of<T>() * kWarps, kThreads, smem, st, (const T*)c.x, (const T*)c.r, (const T*)c.i,
+                        c.lam, c.h0, c.cu, (T*)c.y, c.h_final, c.marks);
+}
+template <typename T>
+cudaError_t by_type(const Call& c, cudaStream_t st) {
+  if (whole(c, false)) return c.a.packed ? run<T, true, true>(c, st) : run<T, true, false>(c, st);
+  return c.a.packed ? run<T, false, true>(c, st) : run<T, false, false>(c, st);
+}
+
+}  // namespace
+
+cudaError_t forward(const Call& c, cudaStream_t st) { return c.a.f32 ? by_type<float>(c, st) : by_type<bf16>(c, st); }
+
+}  // namespace glr
+}  // namespace ssd

@@ -7,24 +7,29 @@ namespace ssd {
 namespace glr {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kStepThreads = 128;
 
 // kW = 4: rows of whole four-element pieces, aligned; 1: any.
 template <typename T, int kW>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kStepThreads)
     k_glr_step(Args a, const T* __restrict__ x, const T* __restrict__ r, const T* __restrict__ i,
                const float* __restrict__ lam, float* state, const int* __restrict__ slots, long long num_slots, T* y) {
-  const int c = (blockIdx.x * kThreads + threadIdx.x) * kW;
+  const int c = (blockIdx.x * kStepThreads + threadIdx.x) * kW;
   if (c >= a.D) return;
   for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
     const long long slot = slots ? slots[n] : n;
     const bool held = slot >= 0 && slot < num_slots;  // else: a place without a sequence, y = 0
     float* s = state + (held ? (size_t)slot * a.D : 0) + c;
-    float h[kW], ksp[kW];
-    load<float, kW>(lam + c, ksp);
+    constexpr int kP = (kW + 1) / 2;
+    const auto two = [](const float(&v)[kW], int p) { return pair(v[2 * p], kW > 1 ? v[(2 * p + 1) % kW] : 0.f); };
+    float h[kW] = {}, l[kW];
+    load<float, kW>(lam + c, l);
     if (held) load<float, kW>(s, h);
+    P rate[kP];
 #pragma unroll
-    for (int k = 0; k < kW; ++k) ksp[k] = -a.scale * softplus_f(ksp[k]);
+    for (int p = 0; p < kP; ++p) {
+      rate[p] = each(two(l, p), [&](float v) { return a.scale * softplus_f(v); });
+    }
     for (int t = 0; t < a.T; ++t) {
       const size_t at = (size_t)n * a.T + t;
       if (held) {
@@ -33,14 +38,15 @@ __global__ void __launch_bounds__(kThreads)
         load<T, kW>(r + at * a.rs + c, rv);
         load<T, kW>(i + at * a.is + c, iv);
 #pragma unroll
-        for (int k = 0; k < kW; ++k) {
-          float av, m;
-          gates<T>(rv[k], ksp[k], av, m);
-          h[k] = fmaf(av, h[k], m * (sigmoid<T>(iv[k]) * xv[k]));
+        for (int p = 0; p < kP; ++p) {
+          const P o = one_minus_exp<true>(rate[p] * sigmoid(two(rv, p))), av = one_less(o);
+          const P m = each(o * one_more(av), [](float v) { return sqrt_f(v); });
+          const P hn = fma(av, two(h, p), m * (sigmoid(two(iv, p)) * two(xv, p)));
+          float h0, h1;
+          split(hn, h0, h1);
+          h[2 * p] = h0;
+          if (kW > 1) h[(2 * p + 1) % kW] = h1;
         }
-      } else {
-#pragma unroll
-        for (int k = 0; k < kW; ++k) h[k] = 0.f;
       }
       save<T, kW>(y + at * a.D + c, h);
     }
@@ -55,14 +61,14 @@ void launch(const Args& a, const void* x, const void* r, const void* i, const fl
   const bool whole = !(a.D % 4 || a.xs % 4 || a.rs % 4 || a.is % 4 || off(x, piece) || off(r, piece) || off(i, piece) ||
                        off(y, piece) || off(lam, 16) || off(state, 16));
   const int w = whole ? 4 : 1, groups = (a.D + w - 1) / w;
-  const dim3 grid((groups + kThreads - 1) / kThreads, a.N < 65535 ? a.N : 65535);
+  const dim3 grid((groups + kStepThreads - 1) / kStepThreads, a.N < 65535 ? a.N : 65535);
   if (whole)
     SSD_LAUNCH("k_glr_step", st,
-               k_glr_step<T, 4><<<grid, kThreads, 0, st>>>(a, (const T*)x, (const T*)r, (const T*)i, lam, state, slots,
+               k_glr_step<T, 4><<<grid, kStepThreads, 0, st>>>(a, (const T*)x, (const T*)r, (const T*)i, lam, state, slots,
                                                            num_slots, (T*)y));
   else
     SSD_LAUNCH("k_glr_step", st,
-               k_glr_step<T, 1><<<grid, kThreads, 0, st>>>(a, (const T*)x, (const T*)r, (const T*)i, lam, state, slots,
+               k_glr_step<T, 1><<<grid, kStepThreads, 0, st>>>(a, (const T*)x, (const T*)r, (const T*)i, lam, state, slots,
                                                            num_slots, (T*)y));
 }
 
