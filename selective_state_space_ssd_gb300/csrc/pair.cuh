@@ -1,0 +1,85 @@
+// Two fp32 numbers in one register pair, and operations on both at once.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ssd {
+
+struct P {
+  unsigned long long v;
+};
+__device__ __forceinline__ P pair(float x, float y) {
+  P p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ P both(float x) { return pair(x, x); }
+__device__ __forceinline__ void split(P p, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.v)); }
+__device__ __forceinline__ float low(P p) {
+  float x, y;
+  split(p, x, y);
+  return x;
+}
+__device__ __forceinline__ P fma(P a, P b, P c) {
+  P d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+__device__ __forceinline__ P operator*(P a, P b) {
+  P d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ P operator+(P a, P b) {
+  P d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ P less(P a, P b) { return fma(b, pair(-1.f, -1.f), a); }  // a - b
+template <typename F>
+__device__ __forceinline__ P each(P p, const F& f) {
+  float x, y;
+  split(p, x, y);
+  return pair(f(x), f(y));
+}
+
+__device__ __forceinline__ float exp2_f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float inv_f(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sqrt_f(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rsqrt_f(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The smaller one; NaN if one is.
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float z;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ P exp_neg(P z) {  // e^-z (infinity from about -88 on, where s is 0)
+  return each(z * both(-kLog2e), [](float x) { return exp2_f(x); });
+}
+__device__ __forceinline__ P inv_one_more(P x) {
+  return each(x + both(1.f), [](float v) { return inv_f(v); });
+}
+__device__ __forceinline__ P sigmoid(P z) { return inv_one_more(exp_neg(z)); }
+__device__ __forceinline__ P one_less(P x) { return fma(x, both(-1.f), both(1.f)); }
+__device__ __forceinline__ P one_more(P x) { return x + both(1.f); }
+
+}  // namespace ssd

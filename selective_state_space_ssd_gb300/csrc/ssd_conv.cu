@@ -4,7 +4,7 @@
 // where the steps are those of one sequence and x before its first one is its K - 1 taps (or zeros).
 // All of it is bound by memory.  A warp takes kW channels a lane and a run of steps, and holds what the taps reach back to
 // (and, backward, the K - 1 gradients that still miss terms) in registers, so a run reads K - 1 steps more than its own.
-// Eight steps are loaded before the first is used.  The weight's gradient is summed by a thread over its run, by a block
+// Steps are loaded well before they are used.  The weight's gradient is summed by a thread over its run, by a block
 // over its eight runs in order, and over blocks in order by k_conv_sums: nothing depends on timing.
 #include <initializer_list>
 #include <type_traits>
@@ -12,6 +12,7 @@
 #include "ssd.h"
 #include "ssd_device.cuh"
 #include "ssd_internal.h"
+#include "pair.cuh"
 #include "vec_io.cuh"
 
 namespace ssd {
@@ -19,7 +20,12 @@ namespace conv {
 namespace {
 
 constexpr int kThreads = 256, kWarps = 8;
-constexpr int kAhead = 8;  // steps loaded at a time
+// Steps loaded ahead, channels a thread has (where rows are whole pieces of them) and blocks an SM.  Measured at 4 x 4096
+// steps of 5120 channels: forward 61 us with eight steps, 3 blocks (four steps 65, 2 blocks 71; two channels a thread 69),
+// backward 128 us with four channels, four steps and 2 blocks (two channels 157 to 163; without the next steps on their way
+// 140).
+constexpr int kAhead = 8, kFwdBlocks = 3, kWide = 4;
+constexpr int kBack = 4, kBackBlocks = 2;
 
 struct Args {
   int N, T, D, K;
@@ -55,103 +61,151 @@ __device__ __forceinline__ Seq locate(const int* cu, int N, int T, int t) {
   return Seq{hi, clamp_cu(cu, hi, T), clamp_cu(cu, hi + 1, T)};
 }
 
-// kW channels' weights, w[tap][channel], and bias.
-template <int K, int kW>
-__device__ __forceinline__ void load_weights(const void* w, const void* b, bool wbf16, int c, float (&wt)[K][kW],
-                                             float (&bias)[kW]) {
-  float flat[K * kW];
+// kW channels (four, two or one) as pairs; of one channel the second number is idle.
+template <int kW>
+struct Chan {
+  static constexpr int kP = (kW + 1) / 2;
+  P p[kP];
+};
+template <int kW>
+__device__ __forceinline__ Chan<kW> chan(const float (&v)[kW]) {
+  Chan<kW> c;
 #pragma unroll
-  for (int i = 0; i < K; ++i) {
-    float v[kW];
-    if (wbf16)
-      load<bf16, kW>(static_cast<const bf16*>(w) + (size_t)c * K + i * kW, v);
-    else
-      load<float, kW>(static_cast<const float*>(w) + (size_t)c * K + i * kW, v);
-#pragma unroll
-    for (int k = 0; k < kW; ++k) flat[i * kW + k] = v[k];
-  }
-#pragma unroll
-  for (int j = 0; j < K; ++j)
-#pragma unroll
-    for (int k = 0; k < kW; ++k) wt[j][k] = flat[k * K + j];
-#pragma unroll
-  for (int k = 0; k < kW; ++k) bias[k] = 0.f;
-  if (b) {
-    if (wbf16)
-      load<bf16, kW>(static_cast<const bf16*>(b) + c, bias);
-    else
-      load<float, kW>(static_cast<const float*>(b) + c, bias);
-  }
+  for (int i = 0; i < Chan<kW>::kP; ++i) c.p[i] = pair(v[2 * i], kW > 1 ? v[(2 * i + 1) % kW] : 0.f);
+  return c;
 }
+template <int kW>
+__device__ __forceinline__ Chan<kW> none() {
+  Chan<kW> c;
+#pragma unroll
+  for (int i = 0; i < Chan<kW>::kP; ++i) c.p[i] = both(0.f);
+  return c;
+}
+template <typename T, int kW>
+__device__ __forceinline__ Chan<kW> get(const T* p) {
+  float v[kW];
+  load<T, kW>(p, v);
+  return chan<kW>(v);
+}
+template <typename T, int kW>
+__device__ __forceinline__ void put(T* p, const Chan<kW>& c) {
+  float v[kW + 1];
+#pragma unroll
+  for (int i = 0; i < Chan<kW>::kP; ++i) split(c.p[i], v[2 * i], v[2 * i + 1]);
+  float o[kW];
+#pragma unroll
+  for (int k = 0; k < kW; ++k) o[k] = v[k];
+  save<T, kW>(p, o);
+}
+// As they lie in memory, for steps that are loaded ahead.
+template <int kBytes>
+struct RawOf;
+template <>
+struct RawOf<2> {
+  using Type = uint16_t;
+};
+template <>
+struct RawOf<4> {
+  using Type = uint32_t;
+};
+template <>
+struct RawOf<8> {
+  using Type = uint2;
+};
+template <>
+struct RawOf<16> {
+  using Type = uint4;
+};
+template <typename T, int kW>
+using Raw = typename RawOf<kW * sizeof(T)>::Type;
+template <typename T, int kW>
+__device__ __forceinline__ Raw<T, kW> raw(const T* p) {
+  return *reinterpret_cast<const Raw<T, kW>*>(p);
+}
+__device__ __forceinline__ P two(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+__device__ __forceinline__ P two(uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); }
+template <typename T, int kW>
+__device__ __forceinline__ Chan<kW> open(const Raw<T, kW>& r) {
+  Chan<kW> c;
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (kW == 1) c.p[0] = two((uint32_t)r << 16, 0u);
+    if constexpr (kW == 2) c.p[0] = two(r);
+    if constexpr (kW == 4) c.p[0] = two(r.x), c.p[1] = two(r.y);
+  } else {
+    if constexpr (kW == 1) c.p[0] = two(r, 0u);
+    if constexpr (kW == 2) c.p[0] = two(r.x, r.y);
+    if constexpr (kW == 4) c.p[0] = two(r.x, r.y), c.p[1] = two(r.z, r.w);
+  }
+  return c;
+}
+
+template <int K, int kW>
+struct Weights {
+  Chan<kW> w[K], b;
+  __device__ __forceinline__ Weights(const void* wp, const void* bp, bool wbf16, int c) {
+    float flat[K * kW];
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      float v[kW];
+      if (wbf16)
+        load<bf16, kW>(static_cast<const bf16*>(wp) + (size_t)c * K + i * kW, v);
+      else
+        load<float, kW>(static_cast<const float*>(wp) + (size_t)c * K + i * kW, v);
+#pragma unroll
+      for (int k = 0; k < kW; ++k) flat[i * kW + k] = v[k];
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      float v[kW];
+#pragma unroll
+      for (int k = 0; k < kW; ++k) v[k] = flat[k * K + j];
+      w[j] = chan<kW>(v);
+    }
+    b = none<kW>();
+    if (bp) b = wbf16 ? get<bf16, kW>(static_cast<const bf16*>(bp) + c) : get<float, kW>(static_cast<const float*>(bp) + c);
+  }
+};
 
 // win[j] = x_{t-1-j}: steps of the sequence, before its first one its taps.
 template <typename T, int K, int kW>
 __device__ __forceinline__ void load_window(const T* x, long long xs, const T* taps, int D, const Seq& q, int t,
-                                            float (&win)[K - 1][kW]) {
+                                            Chan<kW> (&win)[K - 1]) {
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
     const int at = t - 1 - j;
-#pragma unroll
-    for (int k = 0; k < kW; ++k) win[j][k] = 0.f;
+    win[j] = none<kW>();
     if (q.n < 0) continue;
     if (at >= q.begin)
-      load<T, kW>(x + (long long)at * xs, win[j]);
+      win[j] = get<T, kW>(x + (long long)at * xs);
     else if (taps)
-      load<T, kW>(taps + ((size_t)q.n * (K - 1) + (K - 1 + at - q.begin)) * D, win[j]);
+      win[j] = get<T, kW>(taps + ((size_t)q.n * (K - 1) + (K - 1 + at - q.begin)) * D);
   }
 }
 template <int K, int kW>
-__device__ __forceinline__ void shift(float (&win)[K - 1][kW], const float (&x)[kW]) {
+__device__ __forceinline__ void shift(Chan<kW> (&win)[K - 1], const Chan<kW>& x) {
 #pragma unroll
-  for (int j = K - 2; j > 0; --j)
-#pragma unroll
-    for (int k = 0; k < kW; ++k) win[j][k] = win[j - 1][k];
-#pragma unroll
-  for (int k = 0; k < kW; ++k) win[0][k] = x[k];
+  for (int j = K - 2; j > 0; --j) win[j] = win[j - 1];
+  win[0] = x;
 }
 template <int K, int kW>
-__device__ __forceinline__ float product(const float (&wt)[K][kW], const float (&bias)[kW], const float (&win)[K - 1][kW],
-                                         const float (&x)[kW], int k) {
-  float z = fmaf(wt[K - 1][k], x[k], bias[k]);
+__device__ __forceinline__ P product(const Weights<K, kW>& wt, const Chan<kW> (&win)[K - 1], const Chan<kW>& x, int i) {
+  P z = fma(wt.w[K - 1].p[i], x.p[i], wt.b.p[i]);
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) z = fmaf(wt[K - 2 - j][k], win[j][k], z);
+  for (int j = 0; j < K - 1; ++j) z = fma(wt.w[K - 2 - j].p[i], win[j].p[i], z);
   return z;
 }
-template <typename T>
-__device__ __forceinline__ float exp_minus(float z) {  // e^-z, at most e^80
-  const float e = z < -80.f ? 80.f : -z;
-  return sizeof(T) == 4 ? expf(e) : __expf(e);
-}
-template <typename T>
-__device__ __forceinline__ float act(float z, bool silu) {
-  return silu ? __fdividef(z, 1.f + exp_minus<T>(z)) : z;
-}
-template <typename T>
-__device__ __forceinline__ float slope(float z, bool silu) {  // s (1 + z (1 - s))
-  const float e = exp_minus<T>(z), s = __fdividef(1.f, 1.f + e);
-  return silu ? s * fmaf(z, e * s, 1.f) : 1.f;
-}
-
-// Elements as they lie in memory, loaded ahead of their use.
-template <typename T, int kW>
-struct __align__(kW * sizeof(T)) RawVec {
-  T v[kW];
-};
-template <typename T, int kW>
-__device__ __forceinline__ void widen(const RawVec<T, kW>& r, float (&v)[kW]) {
-#pragma unroll
-  for (int k = 0; k < kW; ++k) v[k] = (float)r.v[k];
-}
-template <typename T, int kW>
-__device__ __forceinline__ RawVec<T, kW> raw(const T* p) {
-  return *reinterpret_cast<const RawVec<T, kW>*>(p);
+__device__ __forceinline__ P act(P z, bool silu) { return silu ? z * sigmoid(z) : z; }
+__device__ __forceinline__ P slope(P z, bool silu) {  // s (1 + z (1 - s))
+  const P s = sigmoid(z);
+  return silu ? s * fma(z, one_less(s), both(1.f)) : both(1.f);
 }
 
 // A block: 32 kW channels, eight runs of steps one after another.  Grid: (chunks of eight runs x channel slabs, sequences).
 template <typename T, int K, int kW>
-__global__ void __launch_bounds__(kThreads) k_conv_forward(Args a, const T* __restrict__ x, const void* __restrict__ w,
+__global__ void __launch_bounds__(kThreads, kFwdBlocks) k_conv_forward(Args a, const T* __restrict__ x, const void* __restrict__ w,
                                                            const void* __restrict__ b, const T* __restrict__ taps,
                                                            const int* __restrict__ cu, T* y, T* taps_out, int slabs) {
+  constexpr int kP = Chan<kW>::kP;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, axis = blockIdx.y;
   const int chunk = blockIdx.x / slabs, c = ((blockIdx.x - chunk * slabs) * 32 + lane) * kW;
   if (c >= a.D) return;
@@ -159,125 +213,195 @@ __global__ void __launch_bounds__(kThreads) k_conv_forward(Args a, const T* __re
     for (int n = warp; n < a.N; n += kWarps)
       if (clamp_cu(cu, n + 1, a.T) <= clamp_cu(cu, n, a.T))
         for (int p = 0; p < K - 1; ++p) {
-          float v[kW] = {};
           const size_t at = ((size_t)n * (K - 1) + p) * a.D + c;
-          if (taps) load<T, kW>(taps + at, v);
-          save<T, kW>(taps_out + at, v);
+          put<T, kW>(taps_out + at, taps ? get<T, kW>(taps + at) : none<kW>());
         }
   const long long first = ((long long)chunk * kWarps + warp) * a.run;
   if (first >= a.T) return;
   const int t0 = (int)first, t1 = (int)(first + a.run < a.T ? first + a.run : a.T);
-  const T* px = x + (size_t)axis * a.T * a.xs + c;
-  T* py = y + (size_t)axis * a.T * a.D + c;
-  const T* pt = taps ? taps + c : nullptr;
-  float wt[K][kW], bias[kW], win[K - 1][kW];
-  load_weights<K, kW>(w, b, a.wbf16, c, wt, bias);
+  const T* px = x + ((size_t)axis * a.T + t0) * a.xs + c;
+  T* py = y + ((size_t)axis * a.T + t0) * a.D + c;
+  const T *x0 = x + (size_t)axis * a.T * a.xs + c, *pt = taps ? taps + c : nullptr;
   Seq q = a.packed ? locate(cu, a.N, a.T, t0) : Seq{axis, 0, a.T};
-  load_window<T, K, kW>(px, a.xs, pt, a.D, q, t0, win);
+  Raw<T, kW> next[kAhead];
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s)
+    if (t0 + s < t1) next[s] = raw<T, kW>(px + s * a.xs);
+  const Weights<K, kW> wt(w, b, a.wbf16, c);
+  Chan<kW> win[K - 1];
+  load_window<T, K, kW>(x0, a.xs, pt, a.D, q, t0, win);
   for (int t = t0; t < t1; t += kAhead) {
-    RawVec<T, kW> next[kAhead];
+    Raw<T, kW> now[kAhead];
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s)
-      if (t + s < t1) next[s] = raw<T, kW>(px + (long long)(t + s) * a.xs);
+    for (int s = 0; s < kAhead; ++s) now[s] = next[s];
+    px += kAhead * a.xs;
+    if (t + 2 * kAhead <= t1) {
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) {
-      if (t + s >= t1) break;
-      if (t + s >= q.end) {
-        q = locate(cu, a.N, a.T, t + s);
-        load_window<T, K, kW>(px, a.xs, pt, a.D, q, t + s, win);
+      for (int s = 0; s < kAhead; ++s) next[s] = raw<T, kW>(px + s * a.xs);
+    } else {
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s)
+        if (t + kAhead + s < t1) next[s] = raw<T, kW>(px + s * a.xs);
+    }
+    if (t + kAhead <= t1 && t + kAhead < q.end && q.n >= 0) {  // eight steps of one sequence, not its last ones
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        const Chan<kW> v = open<T, kW>(now[s]);
+        Chan<kW> o;
+#pragma unroll
+        for (int i = 0; i < kP; ++i) o.p[i] = act(product<K, kW>(wt, win, v, i), a.silu);
+        put<T, kW>(py + s * (long long)a.D, o);
+        shift<K, kW>(win, v);
       }
-      float v[kW], o[kW];
-      widen(next[s], v);
+    } else {
 #pragma unroll
-      for (int k = 0; k < kW; ++k) {
-        o[k] = act<T>(product<K, kW>(wt, bias, win, v, k), a.silu);
-        if (q.n < 0) o[k] = 0.f;
-      }
-      save<T, kW>(py + (size_t)(t + s) * a.D, o);
-      shift<K, kW>(win, v);
-      if (taps_out && t + s == q.end - 1 && q.n >= 0) {
+      for (int s = 0; s < kAhead; ++s) {
+        if (t + s >= t1) break;
+        if (t + s >= q.end) {
+          q = locate(cu, a.N, a.T, t + s);
+          load_window<T, K, kW>(x0, a.xs, pt, a.D, q, t + s, win);
+        }
+        const Chan<kW> v = open<T, kW>(now[s]);
+        Chan<kW> o = none<kW>();
+        if (q.n >= 0) {
 #pragma unroll
-        for (int p = 0; p < K - 1; ++p) save<T, kW>(taps_out + ((size_t)q.n * (K - 1) + p) * a.D + c, win[K - 2 - p]);
+          for (int i = 0; i < kP; ++i) o.p[i] = act(product<K, kW>(wt, win, v, i), a.silu);
+        }
+        put<T, kW>(py + s * (long long)a.D, o);
+        shift<K, kW>(win, v);
+        if (taps_out && t + s == q.end - 1 && q.n >= 0) {
+#pragma unroll
+          for (int p = 0; p < K - 1; ++p)
+            put<T, kW>(taps_out + ((size_t)q.n * (K - 1) + p) * a.D + c, win[K - 2 - p]);
+        }
       }
     }
+    py += kAhead * (long long)a.D;
   }
 }
 
 template <typename T, int K, int kW>
-__global__ void __launch_bounds__(kThreads) k_conv_backward(Args a, const T* __restrict__ dy, const T* __restrict__ x,
-                                                            const void* __restrict__ w, const void* __restrict__ b,
-                                                            const T* __restrict__ taps, const int* __restrict__ cu, T* dx,
-                                                            float* part, int slabs) {
+__global__ void __launch_bounds__(kThreads, kBackBlocks)
+    k_conv_backward(Args a, const T* __restrict__ dy, const T* __restrict__ x, const void* __restrict__ w,
+                    const void* __restrict__ b, const T* __restrict__ taps, const int* __restrict__ cu, T* dx, float* part,
+                    int slabs) {
+  constexpr int kP = Chan<kW>::kP;
   __shared__ float red[kWarps][(K + 1) * kW][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, axis = blockIdx.y;
   const int chunk = blockIdx.x / slabs, c = ((blockIdx.x - chunk * slabs) * 32 + lane) * kW;
   const long long first = ((long long)chunk * kWarps + warp) * a.run;
-  float sum[K + 1][kW] = {};  // dw by tap, dbias
+  Chan<kW> sum[K + 1];  // dw by tap, dbias
+#pragma unroll
+  for (int j = 0; j <= K; ++j) sum[j] = none<kW>();
   if (c < a.D && first < a.T) {
     const int t0 = (int)first, t1 = (int)(first + a.run < a.T ? first + a.run : a.T);
-    const T* px = x + (size_t)axis * a.T * a.xs + c;
-    const T* pg = dy + (size_t)axis * a.T * a.D + c;
+    const T *x0 = x + (size_t)axis * a.T * a.xs + c, *pt = taps ? taps + c : nullptr;
+    const T* px = x0 + (long long)t0 * a.xs;
+    const T* pg = dy + ((size_t)axis * a.T + t0) * a.D + c;
     T* pd = dx + (size_t)axis * a.T * a.D + c;
-    const T* pt = taps ? taps + c : nullptr;
-    float wt[K][kW], bias[kW], win[K - 1][kW], acc[K - 1][kW] = {};  // acc[j]: dx of step t - 1 - j so far
-    load_weights<K, kW>(w, b, a.wbf16, c, wt, bias);
-    Seq q = a.packed ? locate(cu, a.N, a.T, t0) : Seq{axis, 0, a.T};
-    load_window<T, K, kW>(px, a.xs, pt, a.D, q, t0, win);
-    for (int t = t0; t < t1 + K - 1; t += kAhead) {
-      RawVec<T, kW> nx[kAhead], ng[kAhead];
+    const Weights<K, kW> wt(w, b, a.wbf16, c);
+    Chan<kW> win[K - 1], acc[K - 1];  // acc[j]: dx of step t - 1 - j so far
 #pragma unroll
-      for (int s = 0; s < kAhead; ++s)
-        if (t + s < t1 + K - 1 && t + s < a.T) {
-          nx[s] = raw<T, kW>(px + (long long)(t + s) * a.xs);
-          ng[s] = raw<T, kW>(pg + (size_t)(t + s) * a.D);
+    for (int j = 0; j < K - 1; ++j) acc[j] = none<kW>();
+    Seq q = a.packed ? locate(cu, a.N, a.T, t0) : Seq{axis, 0, a.T};
+    load_window<T, K, kW>(x0, a.xs, pt, a.D, q, t0, win);
+    // A step's dz into the sums and into dx of the steps before it; what is complete by it.
+    const auto spread = [&](const Chan<kW>& v, const Chan<kW>& dz, int back, bool own) {
+      if (own) {
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          sum[K].p[i] = sum[K].p[i] + dz.p[i];
+          sum[K - 1].p[i] = fma(dz.p[i], v.p[i], sum[K - 1].p[i]);
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j) sum[K - 2 - j].p[i] = fma(dz.p[i], win[j].p[i], sum[K - 2 - j].p[i]);
+        }
+      }
+      Chan<kW> out;
+#pragma unroll
+      for (int j = K - 2; j >= 0; --j)
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+          // (back: steps of the sequence that lie before this one)
+          const P more = j < back ? fma(wt.w[K - 2 - j].p[i], dz.p[i], acc[j].p[i]) : acc[j].p[i];
+          if (j == K - 2)
+            out.p[i] = more;
+          else
+            acc[j + 1].p[i] = more;
         }
 #pragma unroll
-      for (int s = 0; s < kAhead; ++s) {
+      for (int i = 0; i < kP; ++i) acc[0].p[i] = wt.w[K - 1].p[i] * dz.p[i];
+      shift<K, kW>(win, v);
+      return out;
+    };
+    const int last = t1 + K - 1 < a.T ? t1 + K - 1 : a.T;  // of the steps that are read
+    Raw<T, kW> nx[kBack], ng[kBack];
+#pragma unroll
+    for (int s = 0; s < kBack; ++s)
+      if (t0 + s < last) {
+        nx[s] = raw<T, kW>(px + s * a.xs);
+        ng[s] = raw<T, kW>(pg + s * (long long)a.D);
+      }
+    for (int t = t0; t < t1 + K - 1; t += kBack) {
+      Raw<T, kW> rx[kBack], rg[kBack];
+#pragma unroll
+      for (int s = 0; s < kBack; ++s) rx[s] = nx[s], rg[s] = ng[s];
+      px += kBack * a.xs, pg += kBack * (long long)a.D;
+      if (t + 2 * kBack <= last) {
+#pragma unroll
+        for (int s = 0; s < kBack; ++s) {
+          nx[s] = raw<T, kW>(px + s * a.xs);
+          ng[s] = raw<T, kW>(pg + s * (long long)a.D);
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < kBack; ++s)
+          if (t + kBack + s < last) {
+            nx[s] = raw<T, kW>(px + s * a.xs);
+            ng[s] = raw<T, kW>(pg + s * (long long)a.D);
+          }
+      }
+      const bool all = t + kBack <= t1;
+      if (all && t + kBack <= q.end && q.n >= 0 && t - q.begin >= K - 1) {
+        const bool later = t != t0;  // (of the first steps' terms, those for steps before the run are another warp's)
+#pragma unroll
+        for (int s = 0; s < kBack; ++s) {
+          const Chan<kW> v = open<T, kW>(rx[s]), g = open<T, kW>(rg[s]);
+          Chan<kW> dz;
+#pragma unroll
+          for (int i = 0; i < kP; ++i) dz.p[i] = g.p[i] * slope(product<K, kW>(wt, win, v, i), a.silu);
+          const Chan<kW> out = spread(v, dz, K, true);
+          if (later || s >= K - 1) put<T, kW>(pd + (size_t)(t + s - (K - 1)) * a.D, out);
+        }
+        continue;
+      }
+#pragma unroll
+      for (int s = 0; s < kBack; ++s) {
         if (t + s >= t1 + K - 1) break;
         const bool real = t + s < a.T;
         if (real && t + s >= q.end) {
           q = locate(cu, a.N, a.T, t + s);
-          load_window<T, K, kW>(px, a.xs, pt, a.D, q, t + s, win);
+          load_window<T, K, kW>(x0, a.xs, pt, a.D, q, t + s, win);
         }
-        float v[kW] = {}, dz[kW] = {};
+        Chan<kW> v = none<kW>(), dz = none<kW>();
         if (real && q.n >= 0) {
-          float g[kW];
-          widen(nx[s], v);
-          widen(ng[s], g);
+          v = open<T, kW>(rx[s]);
+          const Chan<kW> g = open<T, kW>(rg[s]);
 #pragma unroll
-          for (int k = 0; k < kW; ++k) {
-            dz[k] = g[k] * slope<T>(product<K, kW>(wt, bias, win, v, k), a.silu);
-            if (t + s < t1) {
-              sum[K][k] += dz[k];
-              sum[K - 1][k] = fmaf(dz[k], v[k], sum[K - 1][k]);
-#pragma unroll
-              for (int j = 0; j < K - 1; ++j) sum[K - 2 - j][k] = fmaf(dz[k], win[j][k], sum[K - 2 - j][k]);
-            }
-          }
+          for (int i = 0; i < kP; ++i) dz.p[i] = g.p[i] * slope(product<K, kW>(wt, win, v, i), a.silu);
         }
-        // terms of dz for the steps before it, as far back as the sequence goes
-        float out[kW];
-#pragma unroll
-        for (int j = K - 2; j >= 0; --j)
-#pragma unroll
-          for (int k = 0; k < kW; ++k) {
-            const float more = t + s - 1 - j >= q.begin ? fmaf(wt[K - 2 - j][k], dz[k], acc[j][k]) : acc[j][k];
-            if (j == K - 2)
-              out[k] = more;
-            else
-              acc[j + 1][k] = more;
-          }
-#pragma unroll
-        for (int k = 0; k < kW; ++k) acc[0][k] = wt[K - 1][k] * dz[k];
-        if (t + s - (K - 1) >= t0) save<T, kW>(pd + (size_t)(t + s - (K - 1)) * a.D, out);
-        shift<K, kW>(win, v);
+        const Chan<kW> out = spread(v, dz, t + s - q.begin, real && q.n >= 0 && t + s < t1);
+        if (t + s - (K - 1) >= t0) put<T, kW>(pd + (size_t)(t + s - (K - 1)) * a.D, out);
       }
     }
   }
 #pragma unroll
-  for (int j = 0; j <= K; ++j)
+  for (int j = 0; j <= K; ++j) {
+    float v[2 * kP];
 #pragma unroll
-    for (int k = 0; k < kW; ++k) red[warp][j * kW + k][lane] = sum[j][k];
+    for (int i = 0; i < kP; ++i) split(sum[j].p[i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+    for (int k = 0; k < kW; ++k) red[warp][j * kW + k][lane] = v[k];
+  }
   __syncthreads();
   // part [rows, K + 1, D]
   float* to = part + ((size_t)axis * (gridDim.x / slabs) + chunk) * (K + 1) * a.D;
@@ -324,29 +448,25 @@ __global__ void __launch_bounds__(kThreads) k_conv_dtaps(Args a, const T* __rest
                                                          const T* __restrict__ taps, const int* __restrict__ cu, T* dtaps) {
   const int c = blockIdx.x * kThreads + threadIdx.x;
   if (c >= a.D) return;
-  float wt[K][1], bias[1];
-  load_weights<K, 1>(w, b, a.wbf16, c, wt, bias);
+  const Weights<K, 1> wt(w, b, a.wbf16, c);
   for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
     const size_t row0 = a.packed ? 0 : (size_t)n * a.T;
     const Seq q = a.packed ? Seq{n, clamp_cu(cu, n, a.T), clamp_cu(cu, n + 1, a.T)} : Seq{n, 0, a.T};
-    float win[K - 1][1], out[K - 1] = {};
+    Chan<1> win[K - 1], out[K - 1];
+#pragma unroll
+    for (int p = 0; p < K - 1; ++p) out[p] = none<1>();
     load_window<T, K, 1>(x + row0 * a.xs + c, a.xs, taps ? taps + c : nullptr, a.D, q, q.begin, win);
 #pragma unroll
     for (int t = 0; t < K - 1; ++t) {
       if (q.begin + t >= q.end) break;
-      float v[1], g[1];
-      load<T, 1>(x + (row0 + q.begin + t) * a.xs + c, v);
-      load<T, 1>(dy + (row0 + q.begin + t) * a.D + c, g);
-      const float dz = g[0] * slope<T>(product<K, 1>(wt, bias, win, v, 0), a.silu);
+      const Chan<1> v = get<T, 1>(x + (row0 + q.begin + t) * a.xs + c);
+      const P dz = get<T, 1>(dy + (row0 + q.begin + t) * a.D + c).p[0] * slope(product<K, 1>(wt, win, v, 0), a.silu);
 #pragma unroll
-      for (int j = t + 1; j < K; ++j) out[K - 1 + t - j] = fmaf(wt[K - 1 - j][0], dz, out[K - 1 + t - j]);
+      for (int j = t + 1; j < K; ++j) out[K - 1 + t - j].p[0] = fma(wt.w[K - 1 - j].p[0], dz, out[K - 1 + t - j].p[0]);
       shift<K, 1>(win, v);
     }
 #pragma unroll
-    for (int p = 0; p < K - 1; ++p) {
-      const float o[1] = {out[p]};
-      save<T, 1>(dtaps + ((size_t)n * (K - 1) + p) * a.D + c, o);
-    }
+    for (int p = 0; p < K - 1; ++p) put<T, 1>(dtaps + ((size_t)n * (K - 1) + p) * a.D + c, out[p]);
   }
 }
 
@@ -357,31 +477,28 @@ __global__ void __launch_bounds__(128) k_conv_step(Args a, const T* __restrict__
                                                    long long num_slots, T* y) {
   const int c = (blockIdx.x * 128 + threadIdx.x) * kW;
   if (c >= a.D) return;
-  float wt[K][kW], bias[kW];
-  load_weights<K, kW>(w, b, a.wbf16, c, wt, bias);
+  const Weights<K, kW> wt(w, b, a.wbf16, c);
   for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
     const long long slot = slots ? slots[n] : n;
     const bool held = slot >= 0 && slot < num_slots;  // else: a place without a sequence, y = 0
     T* s = state + (held ? (size_t)slot * (K - 1) * a.D : 0) + c;
-    float win[K - 1][kW] = {};
-    if (held) {
+    Chan<kW> win[K - 1];
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) load<T, kW>(s + (size_t)(K - 2 - j) * a.D, win[j]);
-    }
+    for (int j = 0; j < K - 1; ++j) win[j] = held ? get<T, kW>(s + (size_t)(K - 2 - j) * a.D) : none<kW>();
     for (int t = 0; t < a.T; ++t) {
       const size_t at = (size_t)n * a.T + t;
-      float v[kW] = {}, o[kW] = {};
+      Chan<kW> o = none<kW>();
       if (held) {
-        load<T, kW>(x + at * a.xs + c, v);
+        const Chan<kW> v = get<T, kW>(x + at * a.xs + c);
 #pragma unroll
-        for (int k = 0; k < kW; ++k) o[k] = act<T>(product<K, kW>(wt, bias, win, v, k), a.silu);
+        for (int i = 0; i < Chan<kW>::kP; ++i) o.p[i] = act(product<K, kW>(wt, win, v, i), a.silu);
         shift<K, kW>(win, v);
       }
-      save<T, kW>(y + at * a.D + c, o);
+      put<T, kW>(y + at * a.D + c, o);
     }
     if (held) {
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) save<T, kW>(s + (size_t)(K - 2 - j) * a.D, win[j]);
+      for (int j = 0; j < K - 1; ++j) put<T, kW>(s + (size_t)(K - 2 - j) * a.D, win[j]);
     }
   }
 }
@@ -422,12 +539,12 @@ void step_of(const Call& c, void* state, const int32_t* slots, long long num_slo
                  c.a, (const T*)c.x, c.w, c.b, (T*)state, slots, num_slots, (T*)c.y));
 }
 
-// Runs f<T, K, kW> for a call's type, taps and width: four channels a thread where every row is whole, aligned pieces.
+// Runs f<T, K, kW> for a call's type, taps and width: kWide channels a thread where every row is whole, aligned pieces.
 template <typename F>
 void by_shape(const Call& c, bool whole, const F& f) {
   const auto width = [&](auto t, auto k) {
     if (whole)
-      f(t, k, std::integral_constant<int, 4>());
+      f(t, k, std::integral_constant<int, kWide>());
     else
       f(t, k, std::integral_constant<int, 1>());
   };

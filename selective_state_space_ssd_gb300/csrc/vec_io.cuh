@@ -36,7 +36,7 @@ __device__ __forceinline__ void copies_wait() {  // all but the last kN groups h
   asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
 }
 
-// kW elements as fp32: 1, or 4 at an address that is a multiple of their size.
+// kW elements as fp32: 1, or 2 or 4 at an address that is a multiple of their size.
 template <typename T, int kW>
 __device__ __forceinline__ void load(const T* p, float (&v)[kW]) {
   if constexpr (kW == 1) {
@@ -44,6 +44,13 @@ __device__ __forceinline__ void load(const T* p, float (&v)[kW]) {
       v[0] = *p;
     else
       v[0] = __bfloat162float(*p);
+  } else if constexpr (kW == 2) {
+    if constexpr (sizeof(T) == 4) {
+      const float2 q = *reinterpret_cast<const float2*>(p);
+      v[0] = q.x, v[1] = q.y;
+    } else {
+      unpack(*reinterpret_cast<const uint32_t*>(p), v);
+    }
   } else if constexpr (sizeof(T) == 4) {
     const float4 q = *reinterpret_cast<const float4*>(p);
     v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
@@ -60,6 +67,11 @@ __device__ __forceinline__ void save(T* p, const float (&v)[kW]) {
       *p = v[0];
     else
       *p = __float2bfloat16_rn(v[0]);
+  } else if constexpr (kW == 2) {
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
+    else
+      *reinterpret_cast<uint32_t*>(p) = pack2(v[0], v[1]);
   } else if constexpr (sizeof(T) == 4) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
