@@ -666,15 +666,14 @@ ssd_status ssd_conv_step(const ssd_conv_problem* prob, const void* x, const void
  * Layouts: x, dx [M,D]; w_gate, w_up, dw_gate, dw_up [F,D]; h, dh [M,F].
  * Every pointer is 16-byte aligned.  Outputs must not overlap inputs.
  *
- * Precision.  h is rounded once.  The stash holds G and U in bf16, and the
- * backward's products read dG and dU in bf16: each of these roundings is at
- * most 2^-9 of a value, so the gradients are good to some 2^-8 of the sums'
- * size, as those of a layer whose tensors are bf16.  A NaN or infinity reaches
- * its own row of h and dx, and every element of the weights' gradients that
- * sums over that row.
+ * Precision.  h is rounded once.  The stash holds 24 bits of each number of G
+ * and U, and the backward's products read dG and dU rounded to bf16: 2^-8 of
+ * each term at most, so the gradients are good to that of their terms' size and
+ * rounded once more.  A NaN or infinity reaches its own row of h and dx, and
+ * every element of the weights' gradients that sums over that row.
  *
  * ssd_ffn_stash_size: bytes of the stash that a training forward may keep for
- *   its backward (4 F bytes for each of M rows, M rounded up to 128).
+ *   its backward (6 F bytes for each of M rows, M rounded up to 128).
  *   Host-only.
  * ssd_ffn_workspace_size: device workspace of ssd_ffn_forward (backward == 0) or
  *   ssd_ffn_backward; stashed != 0: of the call with a stash, which needs less.

@@ -8,9 +8,8 @@
 // the copies, one the products, four turn accumulators into results while the next tile is under way (two accumulators of
 // 256 columns).  In the forward's tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets both.
 //
-// The training forward keeps G and U, rounded to bf16, for the backward (their rounding is that of the tensors a training
-// step holds anyway; dG and dU are rounded to bf16 too, as operands of the tensor cores have to be).  The stash lies in
-// pieces of eight columns by 128 rows, as the forward's threads write them: [row tile][F / 8][128][8], G first, then U.
+// The training forward keeps G and U for the backward.  dG and dU are rounded to bf16, as operands of the tensor cores have
+// to be: the one rounding of the backward before its results'.
 #include <initializer_list>
 
 #include "ssd.h"
@@ -25,12 +24,21 @@ namespace {
 
 using namespace tc;
 
-constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int kStages = 4, kThreads = 256, kSMs = 152;
-constexpr int kBytesA = BM * BK * 2, kBytesB = BN * BK * 2, kBytesStage = kBytesA + kBytesB;
+constexpr int BM = 128, BK = 64;
+constexpr int kThreads = 256, kSMs = 152;
+constexpr int kBytesA = BM * BK * 2;
 constexpr int kBytesOut = 2 * BM * 64 * 2;  // two tiles of 64 columns on their way out
-constexpr int kSmem = kStages * kBytesStage + kBytesOut + 1024 + 256;
 constexpr int kGroup = 16;  // row tiles that are walked over together, so that their operands stay in L2
+constexpr int kMostSmem = 232448;
+
+// Stages of a result's tile of BN columns: as many as shared memory holds.
+template <int BN>
+struct Stages {
+  static constexpr int kBytesB = BN * BK * 2, kBytes = kBytesA + kBytesB;
+  static constexpr int kN = BN == 256 ? 4 : 6;
+  static constexpr int kSmem = kN * kBytes + kBytesOut + 1024 + 256;
+  static_assert(kSmem <= kMostSmem, "");
+};
 
 enum Kind { kForward, kDx, kDw };
 
@@ -63,6 +71,41 @@ __device__ __forceinline__ void act_and_slope(float g, bool gelu, float& a, floa
   }
 }
 
+// The stash: G and U with 24 bits of each number (their last eight are cut off: less than 2^-15 of a value, where bf16
+// would leave 2^-8 in every factor of dG and dU), as the upper 16 and the next 8 bits in planes of their own.  A piece is
+// eight columns of a row; pieces of 128 rows follow one another, as the forward's threads write them.
+struct Kept {
+  uint4* hi;
+  uint2* lo;
+};
+__host__ __device__ __forceinline__ size_t kept_pieces(const Args& a) { return (size_t)((a.M + BM - 1) / BM) * BM * (a.F / 8); }
+__device__ __forceinline__ Kept kept(uint8_t* stash, const Args& a, int row, int f, int which) {
+  const size_t n = kept_pieces(a), at = ((size_t)(row / BM) * (a.F / 8) + f / 8) * BM + row % BM;
+  return Kept{reinterpret_cast<uint4*>(stash) + which * n + at, reinterpret_cast<uint2*>(stash + 2 * n * 16) + which * n + at};
+}
+__device__ __forceinline__ void keep_one(const Kept& k, const uint32_t* v) {
+  const auto hi = [](uint32_t x, uint32_t y) { return __byte_perm(x, y, 0x7632); };
+  const auto lo = [](const uint32_t* x) {
+    return __byte_perm(__byte_perm(x[0], x[1], 0x0051), __byte_perm(x[2], x[3], 0x0051), 0x5410);
+  };
+  *k.hi = make_uint4(hi(v[0], v[1]), hi(v[2], v[3]), hi(v[4], v[5]), hi(v[6], v[7]));
+  *k.lo = make_uint2(lo(v), lo(v + 4));
+}
+__device__ __forceinline__ void keep(uint8_t* stash, const Args& a, int row, int f, const uint32_t* g, const uint32_t* u) {
+  keep_one(kept(stash, a, row, f, 0), g);
+  keep_one(kept(stash, a, row, f, 1), u);
+}
+__device__ __forceinline__ void kept_values(const Kept& k, float (&v)[8]) {
+  const uint4 h = *k.hi;
+  const uint2 l = *k.lo;
+  const uint32_t hi[4] = {h.x, h.y, h.z, h.w}, lo[2] = {l.x, l.y};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t low = lo[e / 4] >> (8 * (e % 4)) & 0xffu;
+    v[e] = __uint_as_float((e % 2 ? hi[e / 2] & 0xffff0000u : hi[e / 2] << 16) | low << 8);
+  }
+}
+
 __device__ __forceinline__ void tile_of(const Plan& p, int t, int& m, int& n) {
   const int per = kGroup * p.n_tiles, g = t / per, m0 = g * kGroup, gm = min(kGroup, p.m_tiles - m0), r = t - g * per;
   m = m0 + r % gm;
@@ -75,10 +118,12 @@ __device__ __forceinline__ void settled(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-template <int kKind>
+template <int kKind, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_ffn_product(const __grid_constant__ Maps maps, Plan plan, Args args, bf16* stash, int* status) {
+    k_ffn_product(const __grid_constant__ Maps maps, Plan plan, Args args, uint8_t* stash, int* status) {
   constexpr bool kAmn = kKind == kDw, kBmn = kKind != kForward;
+  constexpr int kStages = Stages<BN>::kN, kBytesStage = Stages<BN>::kBytes, kBytesB = Stages<BN>::kBytesB;
+  static_assert(kKind != kForward || BN == 256, "128 columns of G and of U");
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
   uint8_t* out = smem + kStages * kBytesStage;
@@ -92,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init_fence();
     if (kKind == kForward && blockIdx.x == 0) *status = 0;
   }
-  if (warp == 2) tmem_alloc(slot, 512);
+  if (warp == 2) tmem_alloc(slot, 2 * BN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -161,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     // the last products have to end before the tensor memory is given back
-    for (int d = max(0, done - 2); ok && d < done; ++d) mbar_wait(tfull + (d & 1), (d / 2) & 1, status, 5);
+    for (int d = max(0, done - 2); d < done; ++d) mbar_wait(tfull + (d & 1), (d / 2) & 1, status, 5);
   } else if (warp >= 4) {  // results
     const int q = warp & 3, row = q * 32 + lane;
     int done = 0;
@@ -192,18 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           store_row_bf16(out + (c >> 1) * (BM * 128), row, (c & 1) * 4, h, 4);
           if (stash) {
-            const size_t half = (size_t)plan.m_tiles * BM * args.F;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int f = n * 128 + c * 32 + j * 8;
-              if (f >= args.F) break;
-              bf16* to = stash + (((size_t)m * (args.F / 8) + f / 8) * BM + row) * 8;
-              const auto word = [](const uint32_t* v) { return pack_bf16(__uint_as_float(v[0]), __uint_as_float(v[1])); };
-              *reinterpret_cast<uint4*>(to) =
-                  make_uint4(word(g + 8 * j), word(g + 8 * j + 2), word(g + 8 * j + 4), word(g + 8 * j + 6));
-              *reinterpret_cast<uint4*>(to + half) =
-                  make_uint4(word(u + 8 * j), word(u + 8 * j + 2), word(u + 8 * j + 4), word(u + 8 * j + 6));
-            }
+            for (int j = 0; j < 4; ++j)
+              if (n * 128 + c * 32 + j * 8 < args.F)
+                keep(stash, args, m * BM + row, n * 128 + c * 32 + j * 8, g + 8 * j, u + 8 * j);
           }
         }
         tc_fence_before();
@@ -251,36 +288,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 2 * BN);
   }
 }
 
 // dG and dU of the stashed G and U: a warp has eight rows of four pieces of eight columns.  status: cleared, where this is
 // a call's first kernel (the forward's product clears it where that is).
 __global__ void __launch_bounds__(256)
-    k_ffn_gates(Args a, const bf16* __restrict__ stash, const bf16* __restrict__ dh, bf16* dg, bf16* du, int* status) {
+    k_ffn_gates(Args a, uint8_t* stash, const bf16* __restrict__ dh, bf16* dg, bf16* du, int* status) {
   if (status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int f = (blockIdx.y * 32 + warp * 4 + (lane & 3)) * 8;
   const int row = blockIdx.x * 8 + (lane >> 2);
   if (row >= a.M || f >= a.F) return;
-  const size_t half = (size_t)((a.M + BM - 1) / BM) * BM * a.F;
-  const bf16* from = stash + (((size_t)(row / BM) * (a.F / 8) + f / 8) * BM + row % BM) * 8;
-  const uint4 g4 = *reinterpret_cast<const uint4*>(from), u4 = *reinterpret_cast<const uint4*>(from + half);
+  float g[8], u[8];
   const uint4 d4 = *reinterpret_cast<const uint4*>(dh + (size_t)row * a.F + f);
-  const uint32_t g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
+  kept_values(kept(stash, a, row, f, 0), g);
+  kept_values(kept(stash, a, row, f, 1), u);
+  const uint32_t d[4] = {d4.x, d4.y, d4.z, d4.w};
   uint32_t og[4], ou[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float gv[2], uv[2], dv[2], x[2], y[2];
-    unpack(g[e], gv);
-    unpack(u[e], uv);
+    float dv[2], x[2], y[2];
     unpack(d[e], dv);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       float act, slope;
-      act_and_slope(gv[k], a.gelu, act, slope);
-      x[k] = dv[k] * uv[k] * slope;
+      act_and_slope(g[2 * e + k], a.gelu, act, slope);
+      x[k] = dv[k] * u[2 * e + k] * slope;
       y[k] = dv[k] * act;
     }
     og[e] = pack2(x[0], x[1]);
@@ -290,11 +325,108 @@ __global__ void __launch_bounds__(256)
   *reinterpret_cast<uint4*>(du + (size_t)row * a.F + f) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
 }
 
+// The forward with few rows, where all that counts is how fast the weights come in: one tile a block, of up to 128 rows and
+// as many features (`wide`, of G and of U) as give every SM a block; stages of just the rows that there are.  (The products
+// take 128 rows of what lies there; results of those behind the last row go nowhere.)
+struct Few {
+  int rows, wide, stages, m_tiles;  // rows and wide: multiples of 8
+};
+constexpr int kFewThreads = 192, kFewStages = 16;
+__global__ void __launch_bounds__(kFewThreads, 1)
+    k_ffn_few(const __grid_constant__ Maps maps, Few few, Args args, bf16* h, uint8_t* stash, int* status) {
+  extern __shared__ uint8_t raw_smem[];
+  __shared__ uint64_t full[kFewStages], empty[kFewStages], done;
+  __shared__ uint32_t slot;
+  uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m = blockIdx.x % few.m_tiles, n = blockIdx.x / few.m_tiles, steps = (args.D + BK - 1) / BK;
+  const int bytes_a = few.rows * 128, bytes_b = few.wide * 128, bytes = bytes_a + 2 * bytes_b;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < few.stages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    mbar_init(&done, 1);
+    mbar_init_fence();
+    if (blockIdx.x == 0) *status = 0;
+  }
+  if (warp == 1) tmem_alloc(&slot, 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = slot;
+  if (warp == 0) {  // copies
+    int k = 0;
+    for (int s = 0, turn = 0; k < steps; ++k) {
+      if (turn > 0 && !mbar_wait(empty + s, (turn - 1) & 1, status, 1)) break;
+      if (elect_one()) {
+        uint8_t *a = smem + s * bytes, *b = a + bytes_a;
+        mbar_expect_tx(full + s, bytes);
+        tma_load_2d(b, &maps.b[0], k * BK, n * few.wide, full + s);
+        tma_load_2d(b + bytes_b, &maps.b[1], k * BK, n * few.wide, full + s);
+        tma_load_2d(a, &maps.a[0], k * BK, m * few.rows, full + s);
+      }
+      __syncwarp();
+      if (++s == few.stages) s = 0, ++turn;
+    }
+    // what is still on its way has to arrive before the block may end
+    for (int j = max(0, k - few.stages); j < k; ++j) mbar_wait(full + j % few.stages, (j / few.stages) & 1, status, 2);
+  } else if (warp == 1) {  // products
+    const uint32_t idesc = idesc_bf16(BM, 2 * few.wide, false, false);
+    for (int k = 0, s = 0, turn = 0; k < steps; ++k) {
+      if (!mbar_wait(full + s, turn & 1, status, 3)) break;
+      tc_fence_after();
+      const uint64_t da = kdesc(smem + s * bytes, BM, 0), db = kdesc(smem + s * bytes + bytes_a, 2 * few.wide, 0);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < BK; kk += 16)
+          mma_bf16(tmem, da + kdesc_step(BM, kk), db + kdesc_step(BM, kk), idesc, k > 0 || kk > 0);
+        mma_commit(empty + s);
+      }
+      __syncwarp();
+      if (++s == few.stages) s = 0, ++turn;
+    }
+    if (elect_one()) mma_commit(&done);
+    __syncwarp();
+  } else {  // results
+    const int q = warp & 3, r = q * 32 + lane, row = m * few.rows + r;
+    const bool live = r < few.rows && row < args.M;
+    // (every thread waits: the products end before the tensor memory is given back)
+    if (mbar_wait(&done, 0, status, 4) && q * 32 < few.rows) {
+      tc_fence_after();
+      for (int j = 0; j < few.wide; j += 8) {
+        uint32_t g[8], u[8];
+        tmem_ld8_nowait(taddr(tmem, q * 32, j), g);
+        tmem_ld8_nowait(taddr(tmem, q * 32, few.wide + j), u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) asm volatile("" : "+r"(g[e]), "+r"(u[e]));
+        const int f = n * few.wide + j;
+        if (!live || f >= args.F) continue;
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float act, slope;
+          act_and_slope(__uint_as_float(g[e]), args.gelu, act, slope);
+          o[e] = act * __uint_as_float(u[e]);
+        }
+        *reinterpret_cast<uint4*>(h + (size_t)row * args.F + f) =
+            make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+        if (stash) keep(stash, args, row, f, g, u);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
 struct Call {
   Args a;
   const void *x, *wg, *wu, *dh;
   void *h, *dx, *dwg, *dwu;
-  bf16 *stash, *dg, *du;
+  uint8_t* stash;
+  bf16 *dg, *du;
   int* status;
 };
 
@@ -302,29 +434,65 @@ cudaError_t map(CUtensorMap* m, const void* p, int cols, int rows, long long str
   return make_tmap_rows_bf16(m, p, cols, rows, stride, box_cols, box_rows);
 }
 
-template <int kKind>
+template <int kKind, int BN>
 cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const Call& c, cudaStream_t st) {
-  const auto kernel = k_ffn_product<kKind>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const auto kernel = k_ffn_product<kKind, BN>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Stages<BN>::kSmem);
   if (e != cudaSuccess) return e;
   const int tiles = plan.m_tiles * plan.n_tiles;
   SSD_LAUNCH(name, st,
-             kernel<<<tiles < kSMs ? tiles : kSMs, kThreads, kSmem, st>>>(maps, plan, c.a, kKind == kForward ? c.stash : nullptr,
-                                                                          c.status));
+             kernel<<<tiles < kSMs ? tiles : kSMs, kThreads, Stages<BN>::kSmem, st>>>(
+                 maps, plan, c.a, kKind == kForward ? c.stash : nullptr, c.status));
   return cudaGetLastError();
+}
+// Results of m_tiles row tiles and D columns: tiles of 256 columns, or of 128 where that still is one tile an SM at most
+// (they wait for their operands, and twice the blocks have twice as many on their way: 1501 x 776 out of 2 x 2056 columns
+// takes 34 us in 48 tiles, 22 us in 84).
+template <int kKind>
+cudaError_t launch_wide(const char* name, const Maps& maps, Plan plan, const Call& c, cudaStream_t st) {
+  plan.n_tiles = (c.a.D + 127) / 128;
+  if ((long long)plan.m_tiles * plan.n_tiles <= kSMs) return launch<kKind, 128>(name, maps, plan, c, st);
+  plan.n_tiles = (c.a.D + 255) / 256;
+  return launch<kKind, 256>(name, maps, plan, c, st);
 }
 
 int up(long long a, int b) { return (int)((a + b - 1) / b); }
 
+// Few rows: where tiles of 128 rows and 128 features leave SMs without one.
+bool few_rows(const Args& a, Few* few) {
+  const int mt = up(a.M, BM);
+  if ((long long)mt * up(a.F, 128) > kSMs) return false;
+  few->m_tiles = mt;
+  few->rows = up(up(a.M, mt), 8) * 8;
+  few->wide = up(up(a.F, kSMs / mt), 8) * 8;
+  const int stage = (few->rows + 2 * few->wide) * 128, room = kMostSmem - 2048 - kBytesA;
+  few->stages = room / stage < kFewStages ? room / stage : kFewStages;
+  return true;
+}
+
 cudaError_t forward(const Call& c, cudaStream_t st) {
   Maps maps;
-  cudaError_t e = map(&maps.a[0], c.x, c.a.D, c.a.M, c.a.xs, BK, BM);
-  if (e == cudaSuccess) e = map(&maps.b[0], c.wg, c.a.D, c.a.F, c.a.D, BK, 128);
-  if (e == cudaSuccess) e = map(&maps.b[1], c.wu, c.a.D, c.a.F, c.a.D, BK, 128);
-  if (e == cudaSuccess) e = map(&maps.o[0], c.h, c.a.F, c.a.M, c.a.F, 64, BM);
+  Few few;
+  const bool is_few = few_rows(c.a, &few);
+  const int wide = is_few ? few.wide : 128;
+  cudaError_t e = map(&maps.a[0], c.x, c.a.D, c.a.M, c.a.xs, BK, is_few ? few.rows : BM);
+  if (e == cudaSuccess) e = map(&maps.b[0], c.wg, c.a.D, c.a.F, c.a.D, BK, wide);
+  if (e == cudaSuccess) e = map(&maps.b[1], c.wu, c.a.D, c.a.F, c.a.D, BK, wide);
+  if (e == cudaSuccess && !is_few) e = map(&maps.o[0], c.h, c.a.F, c.a.M, c.a.F, 64, BM);
   if (e != cudaSuccess) return e;
-  maps.a[1] = maps.a[0], maps.o[1] = maps.o[0];
-  return launch<kForward>("k_ffn_forward", maps, Plan{up(c.a.M, BM), up(c.a.F, 128), up(c.a.D, BK), 0}, c, st);
+  maps.a[1] = maps.a[0];
+  if (!is_few) {
+    maps.o[1] = maps.o[0];
+    return launch<kForward, 256>("k_ffn_forward", maps, Plan{up(c.a.M, BM), up(c.a.F, 128), up(c.a.D, BK), 0}, c, st);
+  }
+  maps.o[0] = maps.o[1] = maps.a[0];
+  // (behind the last stage's rows the products still read what 128 rows would take)
+  const int smem = few.stages * (few.rows + 2 * few.wide) * 128 + kBytesA + 1024;
+  if ((e = cudaFuncSetAttribute(k_ffn_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+  SSD_LAUNCH("k_ffn_few", st,
+             k_ffn_few<<<few.m_tiles * up(c.a.F, few.wide), kFewThreads, smem, st>>>(maps, few, c.a, (bf16*)c.h, c.stash,
+                                                                                     c.status));
+  return cudaGetLastError();
 }
 
 cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
@@ -341,7 +509,7 @@ cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
   if (e == cudaSuccess) e = map(&maps.o[0], c.dx, a.D, a.M, a.D, 64, BM);
   if (e != cudaSuccess) return e;
   maps.o[1] = maps.o[0];
-  e = launch<kDx>("k_ffn_dx", maps, Plan{up(a.M, BM), up(a.D, BN), 2 * up(a.F, BK), up(a.F, BK)}, c, st);
+  e = launch_wide<kDx>("k_ffn_dx", maps, Plan{up(a.M, BM), 0, 2 * up(a.F, BK), up(a.F, BK)}, c, st);
   if (e == cudaSuccess) e = map(&maps.a[0], c.dg, a.F, a.M, a.F, 64, BK);
   if (e == cudaSuccess) e = map(&maps.a[1], c.du, a.F, a.M, a.F, 64, BK);
   if (e == cudaSuccess) e = map(&maps.b[0], c.x, a.D, a.M, a.xs, 64, BK);
@@ -349,7 +517,7 @@ cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
   if (e == cudaSuccess) e = map(&maps.o[1], c.dwu, a.D, a.F, a.D, 64, BM);
   if (e != cudaSuccess) return e;
   maps.b[1] = maps.b[0];
-  return launch<kDw>("k_ffn_dw", maps, Plan{2 * up(a.F, BM), up(a.D, BN), up(a.M, BK), up(a.F, BM)}, c, st);
+  return launch_wide<kDw>("k_ffn_dw", maps, Plan{2 * up(a.F, BM), 0, up(a.M, BK), up(a.F, BM)}, c, st);
 }
 
 ssd_status make_args(const ssd_ffn_problem* p, Args* a) {
@@ -366,7 +534,7 @@ ssd_status make_args(const ssd_ffn_problem* p, Args* a) {
   return SSD_OK;
 }
 
-size_t stash_elems(const Args& a) { return 2 * (size_t)up(a.M, BM) * BM * a.F; }
+size_t stash_bytes_of(const Args& a) { return kept_pieces(a) * 2 * 24; }
 
 size_t workspace(Call* c, bool back, bool stashed, void* ws) {
   Carver cv(ws);
@@ -375,7 +543,7 @@ size_t workspace(Call* c, bool back, bool stashed, void* ws) {
     c->dg = cv.take<bf16>((size_t)c->a.M * c->a.F);
     c->du = cv.take<bf16>((size_t)c->a.M * c->a.F);
     if (!stashed) {
-      c->stash = cv.take<bf16>(stash_elems(c->a));
+      c->stash = cv.take<uint8_t>(stash_bytes_of(c->a));
       c->h = cv.take<bf16>((size_t)c->a.M * c->a.F);  // of the forward that is made again
     }
   }
@@ -403,7 +571,7 @@ ssd_status ssd_ffn_stash_size(const ssd_ffn_problem* prob, size_t* bytes) {
   if (!bytes) return SSD_ERR_INVALID_ARG;
   const ssd_status s = ffn::make_args(prob, &a);
   if (s != SSD_OK) return s;
-  *bytes = ffn::stash_elems(a) * 2;
+  *bytes = ffn::stash_bytes_of(a);
   return SSD_OK;
 }
 
@@ -422,10 +590,10 @@ ssd_status ssd_ffn_forward(const ssd_ffn_problem* prob, const void* x, const voi
   ssd_status s = ffn::make_args(prob, &c.a);
   if (s != SSD_OK) return s;
   if ((s = ffn::check({x, w_gate, w_up, h, ws}, stash)) != SSD_OK) return s;
-  if (stash && stash_bytes < ffn::stash_elems(c.a) * 2) return SSD_ERR_WORKSPACE;
+  if (stash && stash_bytes < ffn::stash_bytes_of(c.a)) return SSD_ERR_WORKSPACE;
   if (ws_bytes < ffn::workspace(&c, false, stash != nullptr, nullptr)) return SSD_ERR_WORKSPACE;
   ffn::workspace(&c, false, stash != nullptr, ws);
-  c.x = x, c.wg = w_gate, c.wu = w_up, c.h = h, c.stash = static_cast<bf16*>(stash);
+  c.x = x, c.wg = w_gate, c.wu = w_up, c.h = h, c.stash = static_cast<uint8_t*>(stash);
   return ffn::forward(c, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -436,14 +604,14 @@ ssd_status ssd_ffn_backward(const ssd_ffn_problem* prob, const void* dh, const v
   ssd_status s = ffn::make_args(prob, &c.a);
   if (s != SSD_OK) return s;
   if ((s = ffn::check({dh, x, w_gate, w_up, dx, dw_gate, dw_up, ws}, stash)) != SSD_OK) return s;
-  if (stash && stash_bytes < ffn::stash_elems(c.a) * 2) return SSD_ERR_WORKSPACE;
+  if (stash && stash_bytes < ffn::stash_bytes_of(c.a)) return SSD_ERR_WORKSPACE;
   if (ws_bytes < ffn::workspace(&c, true, stash != nullptr, nullptr)) return SSD_ERR_WORKSPACE;
   ffn::workspace(&c, true, stash != nullptr, ws);
   c.x = x, c.wg = w_gate, c.wu = w_up, c.dh = dh, c.dx = dx, c.dwg = dw_gate, c.dwu = dw_up;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaSuccess;
   if (stash)
-    c.stash = static_cast<bf16*>(const_cast<void*>(stash));
+    c.stash = static_cast<uint8_t*>(const_cast<void*>(stash));
   else
     e = ffn::forward(c, st);
   if (e == cudaSuccess) e = ffn::backward(c, stash != nullptr, st);

@@ -1,10 +1,9 @@
 """GPU parity of the gated feed-forward (through the C ABI) with the formulas in float64.
 
 Bounds, set before the first run.  h: fp32 sums over D (below 1e-5 of the sum's size at these sizes) rounded once to bf16,
-half a step of 2^-8 of the value: max|gpu - ref| / max|ref| <= 4e-3.  The gradients are sums over terms of which each has
-been rounded to bf16 up to twice before (G and U in the stash, which dG and dU take their factors from, and dG and dU
-themselves: at most 2^-9 each of three factors' worth, 2^-7.4 of a term) and are rounded once more: of the sum's size at
-worst where all roundings of a term agree, and a term of a sum of one is the sum: 2^-7.4 + 2^-9 = 8e-3."""
+half a step of 2^-7 of the value: max|gpu - ref| / max|ref| <= 4e-3.  The gradients are sums over terms with a factor dG or
+dU that has been rounded to bf16 (2^-8 of each at most; the stash's 24 bits add 2^-15 to each of two factors) and are rounded
+once more: 2^-7 of the sum's size where all roundings agree, as they can where the sum has one term: 8e-3."""
 import numpy as np
 import pytest
 import torch
