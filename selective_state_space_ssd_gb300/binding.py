@@ -919,6 +919,11 @@ def _row_stride(name: str, t, like) -> int:
     return st
 
 
+def _of(t):
+    """What a call's checks go by: type, shape and strides of a tensor."""
+    return None if t is None else (t.dtype, t.shape, t.stride())
+
+
 def _same(name: str, t, like) -> None:
     if t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous():
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} (contiguous: {t.is_contiguous()}), expected contiguous "
@@ -940,6 +945,21 @@ def _glr_struct(key: tuple) -> ssd_glr_problem:
 def glr_problem(x, r=None, i=None, cu_seqlens=None) -> ssd_glr_problem:
     """An ``ssd_glr_problem`` for x, r, i [b, T, D] (or [T, D]): dense, or rows at one stride."""
     return _glr_struct(_glr_of(x, x if r is None else r, x if i is None else i, cu_seqlens))
+
+
+def _glr_plan(x, r, i, lam, h0=None, cu_seqlens=None, dy=None, dh_final=None, state=None, slots=None) -> tuple:
+    """(problem, key) of a call whose tensors fit one another; raises ValueError otherwise.  A call with tensors of the same
+    types, shapes and strides finds it by these."""
+    key = _glr_of(x, r, i, cu_seqlens)
+    _dense("lam", lam, (key[5],), torch.float32)
+    _dense("h0", h0, (key[3], key[5]), torch.float32)
+    if dy is not None:
+        _same("dy", dy, x)
+    _dense("dh_final", dh_final, (key[3], key[5]), torch.float32)
+    if state is not None:
+        _dense("state", state, (state.shape[0], key[5]), torch.float32)
+    _dense("slots", slots, (key[3],), torch.int32)
+    return _glr_struct(key), key
 
 
 def ssd_glr_workspace_size(prob: ssd_glr_problem, stashed: bool = False) -> int:
@@ -999,10 +1019,8 @@ def glr_forward(x, r, i, lam, h0=None, scale: float = 8.0, cu_seqlens=None, stas
     if stream is not None:
         with _on(stream, x.device, x, r, i, lam, h0, cu_seqlens, stash):
             return glr_forward(x, r, i, lam, h0, scale, cu_seqlens, stash)
-    key = _glr_of(x, r, i, cu_seqlens)
-    prob = _keep(key, lambda: _glr_struct(key))
-    _dense("lam", lam, (key[5],), torch.float32)
-    _dense("h0", h0, (key[3], key[5]), torch.float32)
+    prob, key = _keep(("glr forward", _of(x), _of(r), _of(i), _of(lam), _of(h0), _of(cu_seqlens)),
+                      lambda: _glr_plan(x, r, i, lam, h0, cu_seqlens))
     at = _device(x, r, i, lam, h0, cu_seqlens, stash)
     y = _like(x)
     h_final = torch.empty((key[3], key[5]), dtype=torch.float32, device=x.device)
@@ -1018,12 +1036,8 @@ def glr_backward(dy, x, r, i, lam, dh_final=None, h0=None, scale: float = 8.0, c
     if stream is not None:
         with _on(stream, x.device, dy, x, r, i, lam, dh_final, h0, cu_seqlens, stash, workspace and workspace[0]):
             return glr_backward(dy, x, r, i, lam, dh_final, h0, scale, cu_seqlens, stash, None, workspace)
-    key = _glr_of(x, r, i, cu_seqlens)
-    prob = _keep(key, lambda: _glr_struct(key))
-    _same("dy", dy, x)
-    _dense("lam", lam, (key[5],), torch.float32)
-    _dense("h0", h0, (key[3], key[5]), torch.float32)
-    _dense("dh_final", dh_final, (key[3], key[5]), torch.float32)
+    prob, key = _keep(("glr backward", _of(x), _of(r), _of(i), _of(lam), _of(h0), _of(cu_seqlens), _of(dy), _of(dh_final)),
+                      lambda: _glr_plan(x, r, i, lam, h0, cu_seqlens, dy, dh_final))
     at = _device(x, dy, r, i, lam, dh_final, h0, cu_seqlens, stash, workspace and workspace[0])
     out = {"dx": _like(x), "dr": _like(r), "di": _like(i), "dlam": _like(lam), "dh0": None if h0 is None else _like(h0)}
     if workspace is None:
@@ -1042,15 +1056,11 @@ def glr_step(x, r, i, lam, state, slots=None, scale: float = 8.0, stream=None):
     if stream is not None:
         with _on(stream, x.device, x, r, i, lam, state, slots):
             return glr_step(x, r, i, lam, state, slots, scale)
-    key = _glr_of(x, r, i)
-    prob = _keep(key, lambda: _glr_struct(key))
-    _dense("lam", lam, (key[5],), torch.float32)
-    ns = state.shape[0]
-    _dense("state", state, (ns, key[5]), torch.float32)
-    _dense("slots", slots, (key[3],), torch.int32)
+    prob, key = _keep(("glr step", _of(x), _of(r), _of(i), _of(lam), _of(state), _of(slots)),
+                      lambda: _glr_plan(x, r, i, lam, state=state, slots=slots))
     at = _device(x, r, i, lam, state, slots)
     y = _like(x)
-    ssd_glr_step(prob, x, r, i, lam, state, slots, ns, scale, y, _stream(None, at))
+    ssd_glr_step(prob, x, r, i, lam, state, slots, state.shape[0], scale, y, _stream(None, at))
     return y
 
 
@@ -1072,6 +1082,19 @@ def _conv_struct(key: tuple) -> ssd_conv_problem:
 def conv_problem(x, weight, activation: str = "silu", cu_seqlens=None) -> ssd_conv_problem:
     """An ``ssd_conv_problem`` for x [b, T, D] (or [T, D]; dense, or rows at one stride) and weight [D, K]."""
     return _conv_struct(_conv_of(x, weight, activation, cu_seqlens))
+
+
+def _conv_plan(x, weight, bias, activation, taps=None, cu_seqlens=None, dy=None, state=None, slots=None) -> tuple:
+    """(problem, key) of a call whose tensors fit one another, as ``_glr_plan``."""
+    key = _conv_of(x, weight, activation, cu_seqlens)
+    _dense("bias", bias, (key[7],), weight.dtype)
+    _dense("taps", taps, (key[5], key[8] - 1, key[7]), x.dtype)
+    if dy is not None:
+        _same("dy", dy, x)
+    if state is not None:
+        _dense("state", state, (state.shape[0], key[8] - 1, key[7]), x.dtype)
+    _dense("slots", slots, (key[5],), torch.int32)
+    return _conv_struct(key), key
 
 
 def ssd_conv_workspace_size(prob: ssd_conv_problem) -> int:
@@ -1112,10 +1135,8 @@ def conv_forward(x, weight, bias=None, activation: str = "silu", taps=None, cu_s
     if stream is not None:
         with _on(stream, x.device, x, weight, bias, taps, cu_seqlens):
             return conv_forward(x, weight, bias, activation, taps, cu_seqlens)
-    key = _conv_of(x, weight, activation, cu_seqlens)
-    prob = _keep(key, lambda: _conv_struct(key))
-    _dense("bias", bias, (key[7],), weight.dtype)
-    _dense("taps", taps, (key[5], key[8] - 1, key[7]), x.dtype)
+    prob, key = _keep(("conv forward", activation, _of(x), _of(weight), _of(bias), _of(taps), _of(cu_seqlens)),
+                      lambda: _conv_plan(x, weight, bias, activation, taps, cu_seqlens))
     at = _device(x, weight, bias, taps, cu_seqlens)
     y = _like(x)
     last = torch.empty((key[5], max(key[8] - 1, 0), key[7]), dtype=x.dtype, device=x.device)
@@ -1128,11 +1149,8 @@ def conv_backward(dy, x, weight, bias=None, activation: str = "silu", taps=None,
     if stream is not None:
         with _on(stream, x.device, dy, x, weight, bias, taps, cu_seqlens, workspace and workspace[0]):
             return conv_backward(dy, x, weight, bias, activation, taps, cu_seqlens, None, workspace)
-    key = _conv_of(x, weight, activation, cu_seqlens)
-    prob = _keep(key, lambda: _conv_struct(key))
-    _same("dy", dy, x)
-    _dense("bias", bias, (key[7],), weight.dtype)
-    _dense("taps", taps, (key[5], key[8] - 1, key[7]), x.dtype)
+    prob, key = _keep(("conv backward", activation, _of(x), _of(weight), _of(bias), _of(taps), _of(cu_seqlens), _of(dy)),
+                      lambda: _conv_plan(x, weight, bias, activation, taps, cu_seqlens, dy))
     at = _device(x, dy, weight, bias, taps, cu_seqlens, workspace and workspace[0])
     out = {"dx": _like(x), "dw": _like(weight), "db": None if bias is None else _like(bias),
            "dtaps": None if taps is None else _like(taps)}
@@ -1150,15 +1168,11 @@ def conv_step(x, weight, bias, state, slots=None, activation: str = "silu", stre
     if stream is not None:
         with _on(stream, x.device, x, weight, bias, state, slots):
             return conv_step(x, weight, bias, state, slots, activation)
-    key = _conv_of(x, weight, activation)
-    prob = _keep(key, lambda: _conv_struct(key))
-    _dense("bias", bias, (key[7],), weight.dtype)
-    ns = state.shape[0]
-    _dense("state", state, (ns, key[8] - 1, key[7]), x.dtype)
-    _dense("slots", slots, (key[5],), torch.int32)
+    prob, key = _keep(("conv step", activation, _of(x), _of(weight), _of(bias), _of(state), _of(slots)),
+                      lambda: _conv_plan(x, weight, bias, activation, state=state, slots=slots))
     at = _device(x, weight, bias, state, slots)
     y = _like(x)
-    ssd_conv_step(prob, x, weight, bias, state, slots, ns, y, _stream(None, at))
+    ssd_conv_step(prob, x, weight, bias, state, slots, state.shape[0], y, _stream(None, at))
     return y
 
 
@@ -1228,11 +1242,16 @@ def _ffn_workspace(key, prob, backward, stashed, device):
     return torch.empty(n, dtype=torch.uint8, device=device), n
 
 
-def _ffn_check(key, x, w_gate, w_up, status):
+def _ffn_plan(x, w_gate, w_up, activation, status=None, dh=None) -> tuple:
+    """(problem, key) of a call whose tensors fit one another, as ``_glr_plan``."""
+    key = _ffn_of(x, w_gate, activation)
     shape = (key[5], key[4])
     _dense("w_gate", w_gate, shape, x.dtype)
     _dense("w_up", w_up, shape, x.dtype)
     _dense("status", status, (1,), torch.int32)
+    if dh is not None and (dh.dtype != x.dtype or dh.shape != x.shape[:-1] + (key[5],) or not dh.is_contiguous()):
+        raise ValueError(f"dh: {dh.dtype} {tuple(dh.shape)}, expected contiguous {x.dtype} {tuple(x.shape[:-1]) + (key[5],)}")
+    return _ffn_struct(key), key
 
 
 def ffn_forward(x, w_gate, w_up, activation: str = "silu", stash=None, stream=None, workspace=None, status=None):
@@ -1242,9 +1261,8 @@ def ffn_forward(x, w_gate, w_up, activation: str = "silu", stash=None, stream=No
     if stream is not None:
         with _on(stream, x.device, x, w_gate, w_up, stash, workspace and workspace[0], status):
             return ffn_forward(x, w_gate, w_up, activation, stash, None, workspace, status)
-    key = _ffn_of(x, w_gate, activation)
-    prob = _keep(key, lambda: _ffn_struct(key))
-    _ffn_check(key, x, w_gate, w_up, status)
+    prob, key = _keep(("ffn forward", activation, _of(x), _of(w_gate), _of(w_up), _of(status)),
+                      lambda: _ffn_plan(x, w_gate, w_up, activation, status))
     at = _device(x, w_gate, w_up, stash, status, workspace and workspace[0])
     h = torch.empty(x.shape[:-1] + (key[5],), dtype=x.dtype, device=x.device)
     ws, n = workspace if workspace is not None else _ffn_workspace(key, prob, False, stash is not None, x.device)
@@ -1260,11 +1278,8 @@ def ffn_backward(dh, x, w_gate, w_up, activation: str = "silu", stash=None, stre
     if stream is not None:
         with _on(stream, x.device, dh, x, w_gate, w_up, stash, workspace and workspace[0], status):
             return ffn_backward(dh, x, w_gate, w_up, activation, stash, None, workspace, status)
-    key = _ffn_of(x, w_gate, activation)
-    prob = _keep(key, lambda: _ffn_struct(key))
-    _ffn_check(key, x, w_gate, w_up, status)
-    if dh.dtype != x.dtype or dh.shape != x.shape[:-1] + (key[5],) or not dh.is_contiguous():
-        raise ValueError(f"dh: {dh.dtype} {tuple(dh.shape)}, expected contiguous {x.dtype} {tuple(x.shape[:-1]) + (key[5],)}")
+    prob, key = _keep(("ffn backward", activation, _of(x), _of(w_gate), _of(w_up), _of(status), _of(dh)),
+                      lambda: _ffn_plan(x, w_gate, w_up, activation, status, dh))
     at = _device(x, dh, w_gate, w_up, stash, status, workspace and workspace[0])
     out = {"dx": _like(x), "dwg": _like(w_gate), "dwu": _like(w_up)}
     ws, n = workspace if workspace is not None else _ffn_workspace(key, prob, True, stash is not None, x.device)

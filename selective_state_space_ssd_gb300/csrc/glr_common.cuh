@@ -294,6 +294,7 @@ template <typename Kernel>
 struct Fit {  // of one kernel: clusters of 1 .. kMostShare blocks that fit at once
   int clusters[kMostShare + 1] = {};
   cudaError_t error = cudaSuccess;
+  mutable std::atomic<unsigned long long> allowed{0};
   Fit(Kernel kernel, int threads, int smem) {
     error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     for (int s = 1; s <= kMostShare && error == cudaSuccess; ++s) {
@@ -312,8 +313,7 @@ struct Fit {  // of one kernel: clusters of 1 .. kMostShare blocks that fit at o
 template <typename Kernel, typename... Args_>
 cudaError_t launch_cluster(const char* name, Kernel kernel, const Fit<Kernel>& fit, Args a, int L, int threads, int smem,
                            cudaStream_t st, Args_... args) {
-  // (on each call: the device may be another one than on the last)
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, fit.allowed);
   if (e == cudaSuccess) e = fit.error;
   if (e != cudaSuccess) return e;
   a.share = fit.sharers(a, L);

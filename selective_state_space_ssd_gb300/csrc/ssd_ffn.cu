@@ -437,7 +437,8 @@ cudaError_t map(CUtensorMap* m, const void* p, int cols, int rows, long long str
 template <int kKind, int BN>
 cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const Call& c, cudaStream_t st) {
   const auto kernel = k_ffn_product<kKind, BN>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Stages<BN>::kSmem);
+  static std::atomic<unsigned long long> allowed{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Stages<BN>::kSmem, allowed);
   if (e != cudaSuccess) return e;
   const int tiles = plan.m_tiles * plan.n_tiles;
   SSD_LAUNCH(name, st,
@@ -488,7 +489,8 @@ cudaError_t forward(const Call& c, cudaStream_t st) {
   maps.o[0] = maps.o[1] = maps.a[0];
   // (behind the last stage's rows the products still read what 128 rows would take)
   const int smem = few.stages * (few.rows + 2 * few.wide) * 128 + kBytesA + 1024;
-  if ((e = cudaFuncSetAttribute(k_ffn_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+  static std::atomic<unsigned long long> allowed{0};
+  if ((e = allow_smem(reinterpret_cast<const void*>(k_ffn_few), kMostSmem - 1024, allowed)) != cudaSuccess) return e;
   SSD_LAUNCH("k_ffn_few", st,
              k_ffn_few<<<few.m_tiles * up(c.a.F, few.wide), kFewThreads, smem, st>>>(maps, few, c.a, (bf16*)c.h, c.stash,
                                                                                      c.status));
