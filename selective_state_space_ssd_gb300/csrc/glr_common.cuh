@@ -27,7 +27,7 @@ namespace glr {
 constexpr int kMark = 32;     // the stash holds the state that enters every 32nd step
 constexpr int kWidth = 64;    // channels of a block
 constexpr int kMostShare = 8;   // blocks that share a sequence, at most
-constexpr long long kMostStride = 1 << 24;  // elements from a step to the next: those of a tile's 64 steps fit 32 bits
+constexpr long long kMostStride = 1 << 24;  // elements from a step to the next: those of a tile's 128 steps fit 32 bits
 
 struct Args {
   int N, T, D;  // sequences, steps (of each, or of the packed axis), channels
@@ -162,18 +162,31 @@ __device__ __forceinline__ void store_to(Map* p, int rank, const Map& m) {
 // A step's sequence, with whether it is its first or last one; -1: of no sequence.
 constexpr int kFirst = 1 << 30, kLast = 1 << 29, kSeq = kLast - 1;
 __device__ __forceinline__ int clamp_cu(const int* cu, int n, int T) { return min(max(cu[n], 0), T); }
-__device__ __forceinline__ int code_of(const int* cu, int N, int T, int t) {
+// n: where to look first (the sequence of a step not far from this one), and what was found.
+__device__ __forceinline__ int code_of(const int* cu, int N, int T, int t, int& n) {
   if (t < 0 || t >= T) return -1;
-  int lo = 0, hi = N;  // the last n with cu[n] <= t, or -1
-  while (lo <= hi) {
-    const int mid = (lo + hi) >> 1;
-    if (clamp_cu(cu, mid, T) <= t)
-      lo = mid + 1;
-    else
-      hi = mid - 1;
+  int begin = clamp_cu(cu, n, T), end = clamp_cu(cu, n + 1, T);
+  if (t < begin || t >= end) {
+    int lo = 0, hi = N;  // the last n with cu[n] <= t, or -1
+    while (lo <= hi) {
+      const int mid = (lo + hi) >> 1;
+      if (clamp_cu(cu, mid, T) <= t)
+        lo = mid + 1;
+      else
+        hi = mid - 1;
+    }
+    if (hi < 0 || hi >= N) return -1;
+    n = hi;
+    begin = clamp_cu(cu, n, T), end = clamp_cu(cu, n + 1, T);
   }
-  if (hi < 0 || hi >= N) return -1;
-  return hi | (clamp_cu(cu, hi, T) == t ? kFirst : 0) | (clamp_cu(cu, hi + 1, T) == t + 1 ? kLast : 0);
+  return n | (begin == t ? kFirst : 0) | (end == t + 1 ? kLast : 0);
+}
+// Brings 64 channels of a sequence's state near, for a tile that will read it soon.
+__device__ __forceinline__ void prefetch_state(const float* p, int code, int c0, int D) {
+  const float* at = p + (size_t)(code & kSeq) * D + c0;
+#pragma unroll
+  for (int c = 0; c < kWidth; c += 32)
+    if (c0 + c < D) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + c));
 }
 // What sequences without steps leave behind: their first state (the backward: the last state's gradient), or zeros.
 __device__ __forceinline__ void empty_sequences(const int* cu, const Args& a, int c0, const float* from, float* to) {

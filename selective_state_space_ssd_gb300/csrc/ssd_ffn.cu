@@ -1,10 +1,10 @@
 // The gated feed-forward: h = act(G) U with G = x Wg^T and U = x Wu^T, and its gradients
 //     dU = dh act(G),  dG = dh U act'(G),  dx = dG Wg + dU Wu,  dWg = dG^T x,  dWu = dU^T x
-// in four kernels: forward (both projections, the activation and the product), the elementwise dG and dU, dx, and both
-// weights' gradients.  The three products run on the tensor cores: bf16 operands by TMA into 128-byte swizzled tiles, fp32
+// in three kernels: forward (both projections, the activation and the product), the elementwise dG and dU, and dx with both
+// weights' gradients.  The products run on the tensor cores: bf16 operands by TMA into 128-byte swizzled tiles, fp32
 // accumulators in tensor memory.
 //
-// One kernel for the three, k_ffn_product: output tiles of 128 x 256, one block an SM that walks over tiles; a warp issues
+// One kernel for all of them, k_ffn_product: output tiles of 128 x 256, one block an SM that walks over tiles; a warp issues
 // the copies, one the products, four turn accumulators into results while the next tile is under way (two accumulators of
 // 256 columns).  In the forward's tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets both.
 //
@@ -30,6 +30,9 @@ constexpr int kBytesA = BM * BK * 2;
 constexpr int kBytesOut = 2 * BM * 64 * 2;  // two tiles of 64 columns on their way out
 constexpr int kGroup = 16;  // row tiles that are walked over together, so that their operands stay in L2
 constexpr int kMostSmem = 232448;
+#ifndef FFN_NARROW
+#define FFN_NARROW 2
+#endif
 
 // Stages of a result's tile of BN columns: as many as shared memory holds.
 template <int BN>
@@ -40,7 +43,7 @@ struct Stages {
   static_assert(kSmem <= kMostSmem, "");
 };
 
-enum Kind { kForward, kDx, kDw };
+enum Kind { kForward, kGrads };
 
 struct Args {
   int M, D, F;
@@ -48,14 +51,35 @@ struct Args {
   long long xs;
 };
 
-// Operands a (rows of the result), b (its columns), results o; two of each where the call has two matrices.
+// Operands a (rows of the result), b (its columns), results o; of the forward's product (or dx) and of the weights'
+// gradients, two of each where there are two matrices.
 struct Maps {
-  CUtensorMap a[2], b[2], o[2];
+  CUtensorMap a[2], b[2], o[2], wa[2], wb, wo[2];
 };
 struct Plan {
-  int m_tiles, n_tiles, steps;  // steps of BK
-  int half;                     // kDx: steps of the first matrix pair; kDw: row tiles of the first matrix
+  int m_tiles, n_tiles, steps, half;      // tiles and steps of BK; dx: half of the steps are of the first pair of matrices
+  int w_m_tiles, w_n_tiles, w_steps, w_half;  // the weights' gradients; half of the row tiles are of the first matrix
+  int both;                                   // of those, tiles that every block has
 };
+// The n-th tile of a block.  The forward's go round the blocks.  dx's do too, and the first of them leave some blocks with
+// one more; the weights' gradients' follow, `both` for every block and the others for those with fewer of dx's, as many as
+// end the two kinds of blocks about together (balance()).
+struct Item {
+  bool weights;
+  int t;
+};
+template <int kKind>
+__device__ __forceinline__ bool item_of(const Plan& p, int n, Item& it) {
+  const int blocks = gridDim.x, i = blockIdx.x, tiles = p.m_tiles * p.n_tiles;
+  it.weights = false;
+  it.t = n * blocks + i;
+  if (it.t < tiles) return true;
+  if (kKind == kForward) return false;
+  const int more = tiles % blocks, k = n - (tiles / blocks + (i < more));  // blocks that have one more of dx's: 0 .. more - 1
+  it.weights = true;
+  it.t = k < p.both ? k * blocks + i : p.both * blocks + (k - p.both) * (blocks - more) + i - more;
+  return (k < p.both || i >= more) && it.t < p.w_m_tiles * p.w_n_tiles;
+}
 
 __device__ __forceinline__ void act_and_slope(float g, bool gelu, float& a, float& s) {
   if (gelu) {
@@ -106,8 +130,8 @@ __device__ __forceinline__ void kept_values(const Kept& k, float (&v)[8]) {
   }
 }
 
-__device__ __forceinline__ void tile_of(const Plan& p, int t, int& m, int& n) {
-  const int per = kGroup * p.n_tiles, g = t / per, m0 = g * kGroup, gm = min(kGroup, p.m_tiles - m0), r = t - g * per;
+__device__ __forceinline__ void tile_of(int m_tiles, int n_tiles, int t, int& m, int& n) {
+  const int per = kGroup * n_tiles, g = t / per, m0 = g * kGroup, gm = min(kGroup, m_tiles - m0), r = t - g * per;
   m = m0 + r % gm;
   n = r / gm;
 }
@@ -121,7 +145,6 @@ __device__ __forceinline__ void settled(uint32_t (&r)[32]) {
 template <int kKind, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_ffn_product(const __grid_constant__ Maps maps, Plan plan, Args args, uint8_t* stash, int* status) {
-  constexpr bool kAmn = kKind == kDw, kBmn = kKind != kForward;
   constexpr int kStages = Stages<BN>::kN, kBytesStage = Stages<BN>::kBytes, kBytesB = Stages<BN>::kBytesB;
   static_assert(kKind != kForward || BN == 256, "128 columns of G and of U");
   extern __shared__ uint8_t raw_smem[];
@@ -142,62 +165,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const int tiles = plan.m_tiles * plan.n_tiles;
 
   if (warp == 0) {  // copies
-    const auto load = [&](int s, int m, int n, int k) {
+    const auto load = [&](int s, bool weights, int m, int n, int k) {
       uint8_t *a = smem + s * kBytesStage, *b = a + kBytesA;
       mbar_expect_tx(full + s, kBytesStage);
       if (kKind == kForward) {
         tma_load_2d(a, &maps.a[0], k * BK, m * BM, full + s);
         tma_load_2d(b, &maps.b[0], k * BK, n * 128, full + s);
         tma_load_2d(b + kBytesB / 2, &maps.b[1], k * BK, n * 128, full + s);
-      } else if (kKind == kDx) {
+      } else if (!weights) {
         const int which = k >= plan.half, kk = (k - (which ? plan.half : 0)) * BK;
         tma_load_2d(a, &maps.a[which], kk, m * BM, full + s);
 #pragma unroll
         for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.b[which], n * BN + j * 64, kk, full + s);
       } else {
-        const int which = m >= plan.half, row = (m - (which ? plan.half : 0)) * BM;
+        const int which = m >= plan.w_half, row = (m - (which ? plan.w_half : 0)) * BM;
 #pragma unroll
-        for (int j = 0; j < BM / 64; ++j) tma_load_2d(a + j * 8192, &maps.a[which], row + j * 64, k * BK, full + s);
+        for (int j = 0; j < BM / 64; ++j) tma_load_2d(a + j * 8192, &maps.wa[which], row + j * 64, k * BK, full + s);
 #pragma unroll
-        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.b[0], n * BN + j * 64, k * BK, full + s);
+        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.wb, n * BN + j * 64, k * BK, full + s);
       }
     };
     int it = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    Item tile;
+    for (int i = 0; ok && item_of<kKind>(plan, i, tile); ++i) {
+      const int m_tiles = tile.weights ? plan.w_m_tiles : plan.m_tiles, n_tiles = tile.weights ? plan.w_n_tiles : plan.n_tiles;
+      const int steps = tile.weights ? plan.w_steps : plan.steps;
       int m, n;
-      tile_of(plan, t, m, n);
-      for (int k = 0; k < plan.steps; ++k, ++it) {
+      tile_of(m_tiles, n_tiles, tile.t, m, n);
+      for (int k = 0; k < steps; ++k, ++it) {
         const int s = it % kStages;
         if (it >= kStages && !(ok = mbar_wait(empty + s, (it / kStages - 1) & 1, status, 1))) break;
-        if (elect_one()) load(s, m, n, k);
+        if (elect_one()) load(s, tile.weights, m, n, k);
         __syncwarp();
       }
     }
     // what is still on its way has to arrive before the block may end
     for (int j = max(0, it - kStages); j < it; ++j) mbar_wait(full + j % kStages, (j / kStages) & 1, status, 2);
   } else if (warp == 1) {  // products
-    constexpr uint32_t idesc = idesc_bf16(BM, BN, kAmn, kBmn);
     int it = 0, done = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++done) {
-      const int acc = done & 1;
+    Item tile;
+    for (int i = 0; ok && item_of<kKind>(plan, i, tile); ++i, ++done) {
+      // the forward's operands lie along the sum; dx's right one across it, the weights' gradients' both
+      const bool a_mn = kKind == kGrads && tile.weights;
+      constexpr bool kBmn = kKind == kGrads;
+      const uint32_t idesc = idesc_bf16(BM, BN, a_mn, kBmn);
+      const int steps = tile.weights ? plan.w_steps : plan.steps, acc = done & 1;
+      const uint64_t step_a = a_mn ? mdesc_step(16) : kdesc_step(BM, 16);
       if (done >= 2 && !(ok = mbar_wait(tempty + acc, (done / 2 - 1) & 1, status, 3))) break;
       tc_fence_after();
-      for (int k = 0; k < plan.steps; ++k, ++it) {
+      for (int k = 0; k < steps; ++k, ++it) {
         const int s = it % kStages;
         if (!(ok = mbar_wait(full + s, (it / kStages) & 1, status, 4))) break;
         tc_fence_after();
         uint8_t *a = smem + s * kBytesStage, *b = a + kBytesA;
-        const uint64_t da = kAmn ? mdesc(a, BK, 0) : kdesc(a, BM, 0), db = kBmn ? mdesc(b, BK, 0) : kdesc(b, BN, 0);
+        const uint64_t da = a_mn ? mdesc(a, BK, 0) : kdesc(a, BM, 0), db = kBmn ? mdesc(b, BK, 0) : kdesc(b, BN, 0);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < BK; kk += 16)
-            mma_bf16(tmem + acc * BN, da + (kAmn ? mdesc_step(kk) : kdesc_step(BM, kk)),
-                     db + (kBmn ? mdesc_step(kk) : kdesc_step(BN, kk)), idesc, k > 0 || kk > 0);
+            mma_bf16(tmem + acc * BN, da + (kk / 16) * step_a, db + (kBmn ? mdesc_step(kk) : kdesc_step(BN, kk)), idesc,
+                     k > 0 || kk > 0);
           mma_commit(empty + s);
         }
         __syncwarp();
@@ -210,9 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {  // results
     const int q = warp & 3, row = q * 32 + lane;
     int done = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++done) {
+    Item tile;
+    for (; item_of<kKind>(plan, done, tile); ++done) {
       int m, n;
-      tile_of(plan, t, m, n);
+      tile_of(tile.weights ? plan.w_m_tiles : plan.m_tiles, tile.weights ? plan.w_n_tiles : plan.n_tiles, tile.t, m, n);
       const int acc = done & 1;
       const bool ok = mbar_wait(tfull + acc, (done / 2) & 1, status, 6);
       if (named_bar_or(1, 128, !ok)) break;
@@ -253,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_store_commit();
         }
       } else {
-        const int which = kKind == kDw && m >= plan.half, row0 = (m - (which ? plan.half : 0)) * BM;
+        const int which = tile.weights && m >= plan.w_half, row0 = (m - (which ? plan.w_half : 0)) * BM;
+        const CUtensorMap* to_map = tile.weights ? &maps.wo[which] : &maps.o[0];
 #pragma unroll 1
         for (int p = 0; p < BN / 64; ++p) {
           uint32_t v[2][32];
@@ -274,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async();
           named_bar(1, 128);
           if (q == 0 && lane == 0) {
-            if (n * BN + p * 64 < args.D) tma_store_2d(&maps.o[which], to, n * BN + p * 64, row0);
+            if (n * BN + p * 64 < args.D) tma_store_2d(to_map, to, n * BN + p * 64, row0);
             tma_store_commit();
           }
         }
@@ -440,21 +472,28 @@ cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const C
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Stages<BN>::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  const int tiles = plan.m_tiles * plan.n_tiles;
+  const int tiles = plan.m_tiles * plan.n_tiles + (kKind == kGrads ? plan.w_m_tiles * plan.w_n_tiles : 0);
   SSD_LAUNCH(name, st,
              kernel<<<tiles < kSMs ? tiles : kSMs, kThreads, Stages<BN>::kSmem, st>>>(
                  maps, plan, c.a, kKind == kForward ? c.stash : nullptr, c.status));
   return cudaGetLastError();
 }
-// Results of m_tiles row tiles and D columns: tiles of 256 columns, or of 128 where that still is one tile an SM at most
-// (they wait for their operands, and twice the blocks have twice as many on their way: 1501 x 776 out of 2 x 2056 columns
-// takes 34 us in 48 tiles, 22 us in 84).
-template <int kKind>
-cudaError_t launch_wide(const char* name, const Maps& maps, Plan plan, const Call& c, cudaStream_t st) {
-  plan.n_tiles = (c.a.D + 127) / 128;
-  if ((long long)plan.m_tiles * plan.n_tiles <= kSMs) return launch<kKind, 128>(name, maps, plan, c, st);
-  plan.n_tiles = (c.a.D + 255) / 256;
-  return launch<kKind, 256>(name, maps, plan, c, st);
+// dx and the weights' gradients in one launch: how many of the latter's tiles every block takes, so that the last block
+// ends soonest (steps of a block with one more of dx's tiles, and of the others).  8192 rows of 2560 and 7680: 640 tiles of
+// 240 steps and 1200 of 128 on 152 blocks end after 2112 steps, one after the other they would after 2224.
+void balance(Plan* p) {
+  const int tiles = p->m_tiles * p->n_tiles, w_tiles = p->w_m_tiles * p->w_n_tiles;
+  const int blocks = tiles + w_tiles < kSMs ? tiles + w_tiles : kSMs;
+  const int more = tiles % blocks, each = tiles / blocks, others = blocks - more;
+  long long best = -1;
+  const int least = w_tiles / blocks - p->steps / p->w_steps - 2;  // (with fewer, the others would end later than the first)
+  for (int both = least > 0 ? least : 0; both <= (w_tiles + blocks - 1) / blocks; ++both) {
+    const int left = w_tiles - both * blocks > 0 ? w_tiles - both * blocks : 0;
+    const long long first = more ? (each + 1ll) * p->steps + (long long)both * p->w_steps : 0;
+    const long long second = (long long)each * p->steps + (both + (left + others - 1) / others) * (long long)p->w_steps;
+    const long long end = first > second ? first : second;
+    if (best < 0 || end < best) best = end, p->both = both;
+  }
 }
 
 int up(long long a, int b) { return (int)((a + b - 1) / b); }
@@ -483,10 +522,10 @@ cudaError_t forward(const Call& c, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   maps.a[1] = maps.a[0];
   if (!is_few) {
-    maps.o[1] = maps.o[0];
-    return launch<kForward, 256>("k_ffn_forward", maps, Plan{up(c.a.M, BM), up(c.a.F, 128), up(c.a.D, BK), 0}, c, st);
+    maps.o[1] = maps.o[0], maps.wa[0] = maps.wa[1] = maps.wb = maps.wo[0] = maps.wo[1] = maps.a[0];
+    return launch<kForward, 256>("k_ffn_forward", maps, Plan{up(c.a.M, BM), up(c.a.F, 128), up(c.a.D, BK)}, c, st);
   }
-  maps.o[0] = maps.o[1] = maps.a[0];
+  maps.o[0] = maps.o[1] = maps.wa[0] = maps.wa[1] = maps.wb = maps.wo[0] = maps.wo[1] = maps.a[0];
   // (behind the last stage's rows the products still read what 128 rows would take)
   const int smem = few.stages * (few.rows + 2 * few.wide) * 128 + kBytesA + 1024;
   static std::atomic<unsigned long long> allowed{0};
@@ -509,17 +548,20 @@ cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
   if (e == cudaSuccess) e = map(&maps.b[0], c.wg, a.D, a.F, a.D, 64, BK);
   if (e == cudaSuccess) e = map(&maps.b[1], c.wu, a.D, a.F, a.D, 64, BK);
   if (e == cudaSuccess) e = map(&maps.o[0], c.dx, a.D, a.M, a.D, 64, BM);
+  if (e == cudaSuccess) e = map(&maps.wa[0], c.dg, a.F, a.M, a.F, 64, BK);
+  if (e == cudaSuccess) e = map(&maps.wa[1], c.du, a.F, a.M, a.F, 64, BK);
+  if (e == cudaSuccess) e = map(&maps.wb, c.x, a.D, a.M, a.xs, 64, BK);
+  if (e == cudaSuccess) e = map(&maps.wo[0], c.dwg, a.D, a.F, a.D, 64, BM);
+  if (e == cudaSuccess) e = map(&maps.wo[1], c.dwu, a.D, a.F, a.D, 64, BM);
   if (e != cudaSuccess) return e;
   maps.o[1] = maps.o[0];
-  e = launch_wide<kDx>("k_ffn_dx", maps, Plan{up(a.M, BM), 0, 2 * up(a.F, BK), up(a.F, BK)}, c, st);
-  if (e == cudaSuccess) e = map(&maps.a[0], c.dg, a.F, a.M, a.F, 64, BK);
-  if (e == cudaSuccess) e = map(&maps.a[1], c.du, a.F, a.M, a.F, 64, BK);
-  if (e == cudaSuccess) e = map(&maps.b[0], c.x, a.D, a.M, a.xs, 64, BK);
-  if (e == cudaSuccess) e = map(&maps.o[0], c.dwg, a.D, a.F, a.D, 64, BM);
-  if (e == cudaSuccess) e = map(&maps.o[1], c.dwu, a.D, a.F, a.D, 64, BM);
-  if (e != cudaSuccess) return e;
-  maps.b[1] = maps.b[0];
-  return launch_wide<kDw>("k_ffn_dw", maps, Plan{2 * up(a.F, BM), 0, up(a.M, BK), up(a.F, BM)}, c, st);
+  // Tiles of 128 columns where that still is two tiles an SM at most: they wait for their operands, and twice the blocks
+  // have twice as many on their way.
+  Plan p = {up(a.M, BM), up(a.D, 128), 2 * up(a.F, BK), up(a.F, BK), 2 * up(a.F, BM), up(a.D, 128), up(a.M, BK), up(a.F, BM), 0};
+  const bool narrow = ((long long)p.m_tiles + p.w_m_tiles) * p.n_tiles <= FFN_NARROW * kSMs;
+  if (!narrow) p.n_tiles = p.w_n_tiles = up(a.D, 256);
+  balance(&p);
+  return narrow ? launch<kGrads, 128>("k_ffn_grads", maps, p, c, st) : launch<kGrads, 256>("k_ffn_grads", maps, p, c, st);
 }
 
 ssd_status make_args(const ssd_ffn_problem* p, Args* a) {

@@ -45,10 +45,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     tiles.bring(ring + stage * Tile::kBytes);
     copies_commit();
   };
+  int near = 0;
   // (below 0: there is no such tile)
   const auto codes = [&](int j, int place) {
-    if (kPacked && threadIdx.x < L)
-      code[place][threadIdx.x] = code_of(cu, a.N, a.T, (nt - 1 - (j * share + rank)) * L + (int)threadIdx.x);
+    if (!kPacked || threadIdx.x >= L) return;
+    const int found = code_of(cu, a.N, a.T, (nt - 1 - (j * share + rank)) * L + (int)threadIdx.x, near);
+    code[place][threadIdx.x] = found;
+    if (h0 && found >= 0 && (found & kFirst)) prefetch_state(h0, found, c0, a.D);
+    if (dh_final && found >= 0 && (found & kLast)) prefetch_state(dh_final, found, c0, a.D);
   };
 #pragma unroll
   for (int s = 0; s < kStages; ++s) bring(s);

@@ -8,10 +8,18 @@ namespace glr {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStages = 2;  // tiles in shared memory or on their way there: 48 KiB a block, three blocks an SM
-template <typename T>
-constexpr int run_of() {  // steps a thread has of a tile
-  return sizeof(T) == 2 ? 8 : 4;
+constexpr int kStages = 2;  // tiles in shared memory or on their way there
+// Steps a thread has of a tile, and blocks an SM.  Long runs share the joining of their maps and the cluster's barriers: one
+// sequence of 16384 steps of 2560 channels takes 91 us in runs of 16 (two blocks an SM), 106 us in runs of 8 (three).  The
+// packed form's code for sequences' ends does not fit the registers with runs of 16 (24 sequences of 20011 steps: 202 us
+// against 171 us).
+template <typename T, bool kPacked>
+constexpr int run_of() {
+  return sizeof(T) == 4 ? 4 : kPacked ? 8 : 16;
+}
+template <typename T, bool kPacked>
+constexpr int blocks_of() {
+  return run_of<T, kPacked>() == 16 ? 2 : 3;
 }
 
 // y, the final states and the marks (the states that enter every kMark-th step).  Grid: (64-channel slabs x a.share,
@@ -19,11 +27,11 @@ constexpr int run_of() {  // steps a thread has of a tile
 // runs' maps of each tile to one that goes to all blocks of the cluster; one barrier of the cluster later each of them has
 // the state that enters its tile.
 template <typename T, bool kVec, bool kPacked>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
     k_glr_forward(Args a, const T* __restrict__ x, const T* __restrict__ r, const T* __restrict__ i,
                   const float* __restrict__ lam, const float* __restrict__ h0, const int* __restrict__ cu, T* y,
                   float* h_final, float* marks) {
-  constexpr int kRun = run_of<T>(), L = kRun * kWarps;
+  constexpr int kRun = run_of<T, kPacked>(), L = kRun * kWarps;
   static_assert(L % kMark == 0 && kMark % kRun == 0, "states are kept where runs begin");
   using Tile = Tiles<T, kVec, kWarps, kRun, 3>;
   using Word = typename Words<T>::Word;
@@ -43,8 +51,12 @@ __global__ void __launch_bounds__(kThreads, 3)
     tiles.bring(ring + stage * Tile::kBytes);
     copies_commit();
   };
+  int near = 0;
   const auto codes = [&](int j, int place) {
-    if (kPacked && threadIdx.x < L) code[place][threadIdx.x] = code_of(cu, a.N, a.T, (j * share + rank) * L + threadIdx.x);
+    if (!kPacked || threadIdx.x >= L) return;
+    const int found = code_of(cu, a.N, a.T, (j * share + rank) * L + threadIdx.x, near);
+    code[place][threadIdx.x] = found;
+    if (h0 && found >= 0 && (found & kFirst)) prefetch_state(h0, found, c0, a.D);
   };
 #pragma unroll
   for (int s = 0; s < kStages; ++s) bring(s);
@@ -171,9 +183,9 @@ __global__ void __launch_bounds__(kThreads, 3)
 template <typename T, bool kVec, bool kPacked>
 cudaError_t run(const Call& c, cudaStream_t st) {
   auto* kernel = &k_glr_forward<T, kVec, kPacked>;
-  constexpr int smem = kStages * Tiles<T, kVec, kWarps, run_of<T>(), 3>::kBytes;
+  constexpr int smem = kStages * Tiles<T, kVec, kWarps, run_of<T, kPacked>(), 3>::kBytes;
   static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
-  return launch_cluster("k_glr_forward", kernel, fit, c.a, run_of<T>() * kWarps, kThreads, smem, st, (const T*)c.x, (const T*)c.r, (const T*)c.i,
+  return launch_cluster("k_glr_forward", kernel, fit, c.a, run_of<T, kPacked>() * kWarps, kThreads, smem, st, (const T*)c.x, (const T*)c.r, (const T*)c.i,
                         c.lam, c.h0, c.cu, (T*)c.y, c.h_final, c.marks);
 }
 template <typename T>
