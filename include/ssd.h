@@ -552,7 +552,8 @@ ssd_status ssd_norm_backward(const ssd_norm_problem* prob, const void* dy, const
  * (the earlier ones' gradients); other sequences take nothing from it.
  *
  * ssd_glr_stash_size: bytes of the stash a training forward may keep for its
- *   backward: the fp32 state that enters every 32nd step.  Host-only.
+ *   backward: the fp32 state that enters every eighth step (bf16), or every
+ *   fourth (fp32).  Host-only.
  * ssd_glr_workspace_size: device workspace of ssd_glr_backward (the forward
  *   needs none); stashed != 0: of the call with a stash.  Host-only.
  * ssd_glr_forward: y, and h_final unless NULL, from h0 (NULL: zeros); the stash

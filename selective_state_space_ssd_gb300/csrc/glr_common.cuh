@@ -24,7 +24,8 @@
 namespace ssd {
 namespace glr {
 
-constexpr int kMark = 32;     // the stash holds the state that enters every 32nd step
+// The stash holds the state that enters every so many steps: each run of the backward's threads.
+constexpr int mark_of(bool f32) { return f32 ? 4 : 8; }
 constexpr int kWidth = 64;    // channels of a block
 constexpr int kMostShare = 8;   // blocks that share a sequence, at most
 constexpr long long kMostStride = 1 << 24;  // elements from a step to the next: those of a tile's 128 steps fit 32 bits
@@ -155,7 +156,9 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 __device__ __forceinline__ void store_to(Map* p, int rank, const Map& m) {
   uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(at), "l"(m.a.v), "l"(m.b.v) : "memory");
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(m.a.v.x), "f"(m.a.v.y), "f"(m.b.v.x),
+               "f"(m.b.v.y)
+               : "memory");
 }
 
 // ------------------------------------------------------------ steps of a packed axis

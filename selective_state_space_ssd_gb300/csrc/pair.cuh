@@ -7,36 +7,16 @@
 namespace ssd {
 
 struct P {
-  unsigned long long v;
+  float2 v;
 };
-__device__ __forceinline__ P pair(float x, float y) {
-  P p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p.v) : "f"(x), "f"(y));
-  return p;
-}
+__device__ __forceinline__ P pair(float x, float y) { return P{make_float2(x, y)}; }
 __device__ __forceinline__ P both(float x) { return pair(x, x); }
-__device__ __forceinline__ void split(P p, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p.v)); }
-__device__ __forceinline__ float low(P p) {
-  float x, y;
-  split(p, x, y);
-  return x;
-}
-__device__ __forceinline__ P fma(P a, P b, P c) {
-  P d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return d;
-}
-__device__ __forceinline__ P operator*(P a, P b) {
-  P d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
-__device__ __forceinline__ P operator+(P a, P b) {
-  P d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
-  return d;
-}
-__device__ __forceinline__ P less(P a, P b) { return fma(b, pair(-1.f, -1.f), a); }  // a - b
+__device__ __forceinline__ void split(P p, float& x, float& y) { x = p.v.x, y = p.v.y; }
+__device__ __forceinline__ float low(P p) { return p.v.x; }
+__device__ __forceinline__ P fma(P a, P b, P c) { return P{__ffma2_rn(a.v, b.v, c.v)}; }
+__device__ __forceinline__ P operator*(P a, P b) { return P{__fmul2_rn(a.v, b.v)}; }
+__device__ __forceinline__ P operator+(P a, P b) { return P{__fadd2_rn(a.v, b.v)}; }
+__device__ __forceinline__ P less(P a, P b) { return fma(b, both(-1.f), a); }  // a - b
 template <typename F>
 __device__ __forceinline__ P each(P p, const F& f) {
   float x, y;

@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(1024) k_glr_lam(const float* __restrict__ part
   }
 }
 
-long long mark_count(const Args& a) { return (long long)axes(a) * ((a.T + kMark - 1) / kMark) * a.D; }
+long long mark_count(const Args& a) { return (long long)axes(a) * ((a.T + mark_of(a.f32) - 1) / mark_of(a.f32)) * a.D; }
 
 // The workspace of a call: the backward's partial sums, and the marks where no stash is given.
 size_t workspace(Call* c, bool stashed, void* ws) {

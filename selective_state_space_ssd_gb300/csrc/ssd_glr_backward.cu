@@ -10,36 +10,36 @@ namespace ssd {
 namespace glr {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps, L = kMark, kRun = L / kWarps;
-template <typename T>
-constexpr int stages_of() {  // tiles in shared memory or on their way there: two blocks an SM
-  return sizeof(T) == 2 ? 3 : 2;
-}
-// (a tile begins where the stash holds a state)
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kStages = 2;  // tiles in shared memory or on their way there
 
-// Tile by tile from the end.  The states of a tile are made again from its mark, and the upstream gradients' maps D -> a D +
-// a dy are joined as the states' are, in the other direction; the states are made while a cluster's barrier is under way.
-// part [axes kMostShare, D]: the sums of q, and zeros where fewer blocks share.
+// Tile by tile from the end.  The stash holds the state that enters each thread's run, so a run's states and all factors of
+// its gradients come without a word from other warps; only the upstream gradients' maps D -> a D + a dy are joined as the
+// states are forward, in the other direction.  The factors of a run's first steps wait for that in shared memory (eight
+// numbers a step and lane, written and read by the same thread), those of its last four in registers: runs of eight steps
+// halve the barriers that runs of four would take.  part [axes kMostShare, D]: the sums of q, and zeros where fewer blocks
+// share.
 template <typename T, bool kVec, bool kPacked>
 __global__ void __launch_bounds__(kThreads, 2)
     k_glr_backward(Args a, const T* __restrict__ dy, const float* __restrict__ dh_final, const T* __restrict__ x,
                    const T* __restrict__ r, const T* __restrict__ i, const float* __restrict__ lam,
                    const float* __restrict__ h0, const int* __restrict__ cu, const float* __restrict__ marks, T* dx, T* dr,
                    T* di, float* dh0, float* part) {
-  constexpr int kStages = stages_of<T>();
+  constexpr int kRun = mark_of(sizeof(T) == 4), L = kRun * kWarps, kAside = kRun - 4;
   using Tile = Tiles<T, kVec, kWarps, kRun, 4>;
   using Word = typename Words<T>::Word;
   extern __shared__ __align__(16) uint8_t ring[];
-  __shared__ Map fwd[2][kWarps][32], rev[2][kWarps][32];
+  __shared__ Map rev[2][kWarps][32];
   __shared__ Map xchg[2][kMostShare][32];
   __shared__ int code[3][kPacked ? L : 1];
+  Map* aside = reinterpret_cast<Map*>(ring + kStages * Tile::kBytes) + threadIdx.x;  // [kAside][2][kThreads]
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int share = a.share, rank = blockIdx.x % share;
   const int c0 = (int)(blockIdx.x / share) * kWidth, c = c0 + lane * 2, axis = blockIdx.y;
   const size_t row0 = (size_t)axis * a.T;
   const T* const from[4] = {x + row0 * a.xs, r + row0 * a.rs, i + row0 * a.is, dy + row0 * a.D};
   const uint32_t step[4] = {(uint32_t)a.xs, (uint32_t)a.rs, (uint32_t)a.is, (uint32_t)a.D};
-  const int nt = (a.T + L - 1) / L, rounds = (nt + share - 1) / share;
+  const int nt = (a.T + L - 1) / L, rounds = (nt + share - 1) / share, nm = (a.T + kRun - 1) / kRun;
   Tile tiles(from, step, c0, a.D, a.T, (nt - 1 - rank) * L, -share);
   const auto bring = [&](int stage) {
     tiles.bring(ring + stage * Tile::kBytes);
@@ -62,6 +62,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   P back = !kPacked && dh_final ? load_two(dh_final + (size_t)axis * a.D, c, a.D) : both(0.f);  // D behind the round
   P qsum = both(0.f);
   if (kPacked && dh0 && rank == 0) empty_sequences(cu, a, c0, dh_final, dh0);
+  // The state that enters this thread's run of the j-th tile, on its way one tile ahead.
+  const auto mark = [&](int j) {
+    const int t = (nt - 1 - (j * share + rank)) * L + w * kRun;
+    return j < rounds && t >= 0 && t < a.T ? load_two(marks + ((size_t)axis * nm + t / kRun) * a.D, c, a.D) : both(0.f);
+  };
+  P next = mark(0);
   copies_wait<kStages - 1>();
   __syncthreads();
   if (share > 1) {  // (the other blocks of the cluster have begun before anything is written to them)
@@ -74,10 +80,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int j = 0; j < rounds; ++j, sg.next(), cd.next()) {
     const int tile = nt - 1 - (j * share + rank), t0 = tile < 0 ? a.T : tile * L + w * kRun;
     const Word* stage = reinterpret_cast<const Word*>(ring + sg.at * Tile::kBytes) + w * kRun * 32 + lane;
-    // per step: a, the state's increment b, a n, a u / m, dx / dh, di / dh, 1 - s(r), dy
-    P av[kRun], bv[kRun], an[kRun], um[kRun], mi[kRun], ki[kRun], r1[kRun], up[kRun];
-    P h = tile >= 0 ? load_two(marks + ((size_t)axis * nt + tile) * a.D, c, a.D) : both(0.f);
-    const auto maps_of_steps = [&](auto is_far) {
+    const Bits bits = bits_of<kPacked, kRun>(&code[cd.at][kPacked ? w * kRun : 0], t0, a.T, lane);
+    const bool odd = (bits.first | bits.none | (kPacked ? bits.last : 0)) != 0;
+    // per step: a, dy; of the last four: dx / dh, di / dh, q / dh, 1 - s(r)
+    P av[kRun], up[kRun], mi[4], ki[4], kq[4], r1[4];
+    P h = next;
+    const auto factors = [&](auto is_far, auto is_odd) {
 #pragma unroll
       for (int s = 0; s < kRun; ++s) {
         const auto most = [](float v) { return min_nan(v, 1e30f); };
@@ -86,54 +94,43 @@ __global__ void __launch_bounds__(kThreads, 2)
         const P ei = each(exp_neg(Words<T>::open(stage[(2 * L + s) * 32])), most), si = inv_one_more(ei);
         up[s] = Words<T>::open(stage[(3 * L + s) * 32]);
         const P n = rate * sr, o = one_minus_exp<decltype(is_far)::value>(n);
-        r1[s] = er * sr;
         av[s] = one_less(o);
         const P m2 = o * one_more(av[s]);
         const P rm = each(m2, [](float v) { return rsqrt_f(fmaxf(v, 1e-37f)); });  // (m2 = 0: n is 0 too)
-        const P sm = si * rm;
-        mi[s] = m2 * sm;
-        bv[s] = mi[s] * xv;
-        ki[s] = bv[s] * (ei * si);
-        an[s] = av[s] * n;
-        um[s] = av[s] * (sm * xv);
+        const P sm = si * rm, fx = m2 * sm, b = fx * xv, fi = b * (ei * si), fr = er * sr;
+        if (decltype(is_odd)::value) {
+          if (bits.none >> s & 1) {
+            av[s] = both(1.f), up[s] = both(0.f);
+          } else if (kPacked) {
+            const size_t at = (size_t)(code[cd.at][w * kRun + s] & kSeq) * a.D;
+            if ((bits.first >> s & 1)) h = h0 ? load_two(h0 + at, c, a.D) : both(0.f);
+            if ((bits.last >> s & 1) && dh_final) up[s] = up[s] + load_two(dh_final + at, c, a.D);
+          }
+        }
+        const P fq = av[s] * n * less(av[s] * (sm * xv), h);
+        h = fma(av[s], h, b);
+        if (s < kAside) {
+          aside[(2 * s) * kThreads] = Map{fx, fi};
+          aside[(2 * s + 1) * kThreads] = Map{fq, fr};
+        } else {
+          mi[s - kAside] = fx, ki[s - kAside] = fi, kq[s - kAside] = fq, r1[s - kAside] = fr;
+        }
       }
     };
-    if (far)
-      maps_of_steps(std::true_type());
+    if (far || odd)  // (one copy of the rare forms)
+      factors(std::true_type(), std::true_type());
     else
-      maps_of_steps(std::false_type());
-    const Bits bits = bits_of<kPacked, kRun>(&code[cd.at][kPacked ? w * kRun : 0], t0, a.T, lane);
-    if (bits.first | bits.none | (kPacked ? bits.last : 0)) {
-#pragma unroll
-      for (int s = 0; s < kRun; ++s) {
-        if (bits.none >> s & 1) {
-          av[s] = both(1.f), bv[s] = up[s] = both(0.f);
-          continue;
-        }
-        if (!kPacked) continue;
-        const size_t at = (size_t)(code[cd.at][w * kRun + s] & kSeq) * a.D;
-        if ((bits.last >> s & 1) && dh_final) up[s] = up[s] + load_two(dh_final + at, c, a.D);
-        if ((bits.first >> s & 1) && h0) bv[s] = fma(av[s], load_two(h0 + at, c, a.D), bv[s]);
-      }
-    }
-    Map f, b;
+      factors(std::false_type(), std::false_type());
+    Map b = {both(1.f), both(0.f)};
     if (kPacked && bits.first) {
-      f = Map{both(1.f), both(0.f)};
-      b = f;
-#pragma unroll
-      for (int s = 0; s < kRun; ++s) f = after<true>(f, Map{bits.first >> s & 1 ? anew() : av[s], bv[s]});
 #pragma unroll
       for (int s = kRun - 1; s >= 0; --s)  // (what a first step hands on goes to dh0, not to the step before it)
         b = bits.first >> s & 1 ? Map{anew(), both(0.f)} : after<true>(b, Map{av[s], av[s] * up[s]});
     } else {
-      f = Map{av[0], bv[0]};
+      b = Map{av[kRun - 1], av[kRun - 1] * up[kRun - 1]};
 #pragma unroll
-      for (int s = 1; s < kRun; ++s) f = Map{f.a * av[s], fma(av[s], f.b, bv[s])};
-      b = Map{f.a, av[kRun - 1] * up[kRun - 1]};
-#pragma unroll
-      for (int s = kRun - 2; s >= 0; --s) b.b = av[s] * (up[s] + b.b);
+      for (int s = kRun - 2; s >= 0; --s) b = Map{av[s] * b.a, av[s] * (up[s] + b.b)};
     }
-    fwd[j & 1][w][lane] = f;
     rev[j & 1][w][lane] = b;
     codes(j + 1, cd.at == 2 ? 0 : cd.at + 1);
     // the runs' maps are there, the next tile has come, and this one's stage is free
@@ -152,24 +149,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     bring(sg.at);
-    // the states before each step; from here on an holds a n (a u / m - h_{t-1})
-    const auto join = [&](auto anew_too) {
-#pragma unroll
-      for (int v = 0; v < kWarps - 1; ++v)
-        if (v < w) h = through<decltype(anew_too)::value>(fwd[j & 1][v][lane], h);
-    };
-    if (kPacked && resets)
-      join(std::true_type());
-    else
-      join(std::false_type());
-#pragma unroll
-    for (int s = 0; s < kRun; ++s) {
-      const bool start = kPacked && (bits.first >> s & 1);
-      if (start)
-        h = h0 && !(bits.none >> s & 1) ? load_two(h0 + (size_t)(code[cd.at][w * kRun + s] & kSeq) * a.D, c, a.D) : both(0.f);
-      an[s] = an[s] * less(um[s], h);
-      h = start ? bv[s] : fma(av[s], h, bv[s]);
-    }
+    next = mark(j + 1);
     P d = back;  // D of the step behind this thread's
     if (share > 1) {
       cluster_wait();
@@ -199,39 +179,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (t0 >= a.T) continue;
     const size_t at = (row0 + (size_t)tile * L) * a.D;
     T *px = dx + at, *pr = dr + at, *pi = di + at;
-    if (!(bits.first | bits.none) && (kPacked || t0 > 0)) {
-      P q[kRun];
-#pragma unroll
-      for (int s = kRun - 1; s >= 0; --s) {
-        const P dh = up[s] + d;
-        d = av[s] * dh;
-        q[s] = dh * an[s];
-        qsum = qsum + q[s];
-        mi[s] = dh * mi[s], ki[s] = dh * ki[s];
-      }
-      if (c < a.D) {
-#pragma unroll
-        for (int s = 0; s < kRun; ++s) {
-          const uint32_t o = o0 + s * (uint32_t)a.D;
-          store_row<T, kVec>(px + o, second, mi[s]);
-          store_row<T, kVec>(pr + o, second, q[s] * r1[s]);
-          store_row<T, kVec>(pi + o, second, ki[s]);
-        }
-      }
-      continue;
-    }
+    const bool plain = !(bits.first | bits.none) && (kPacked || t0 > 0), live = c < a.D;
 #pragma unroll
     for (int s = kRun - 1; s >= 0; --s) {
+      Map f, g;
+      if (s < kAside) {
+        f = aside[(2 * s) * kThreads];
+        g = aside[(2 * s + 1) * kThreads];
+      } else {
+        f = Map{mi[s - kAside], ki[s - kAside]};
+        g = Map{kq[s - kAside], r1[s - kAside]};
+      }
       const P dh = up[s] + d;
       d = av[s] * dh;
-      P q = dh * an[s], vx = dh * mi[s], vi = dh * ki[s], vr = q * r1[s];
-      if (bits.none >> s & 1) q = vx = vi = vr = both(0.f);
-      if (dh0 && (kPacked ? (bits.first & ~bits.none) >> s & 1 : t0 + s == 0))
-        store_two(dh0 + (size_t)(kPacked ? code[cd.at][w * kRun + s] & kSeq : axis) * a.D, c, a.D, d);
-      if (kPacked && (bits.first >> s & 1)) d = both(0.f);
-      if (t0 + s >= a.T) continue;
+      P q = dh * g.a, vx = dh * f.a, vi = dh * f.b, vr = q * g.b;
+      if (!plain) {
+        if (bits.none >> s & 1) q = vx = vi = vr = both(0.f);
+        if (dh0 && (kPacked ? (bits.first & ~bits.none) >> s & 1 : t0 + s == 0))
+          store_two(dh0 + (size_t)(kPacked ? code[cd.at][w * kRun + s] & kSeq : axis) * a.D, c, a.D, d);
+        if (kPacked && (bits.first >> s & 1)) d = both(0.f);
+      }
       qsum = qsum + q;
-      if (c < a.D) {
+      if (live && (plain || t0 + s < a.T)) {
         const uint32_t o = o0 + s * (uint32_t)a.D;
         store_row<T, kVec>(px + o, second, vx);
         store_row<T, kVec>(pr + o, second, vr);
@@ -242,12 +211,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   copies_wait<0>();
   // the warps' sums of q, in order
   __syncthreads();
-  fwd[0][w][lane].a = qsum;
+  rev[0][w][lane].a = qsum;
   __syncthreads();
   if (w == 0) {
-    P s = fwd[0][0][lane].a;
+    P s = rev[0][0][lane].a;
 #pragma unroll
-    for (int v = 1; v < kWarps; ++v) s = s + fwd[0][v][lane].a;
+    for (int v = 1; v < kWarps; ++v) s = s + rev[0][v][lane].a;
     for (int k = rank; k < kMostShare; k += share)
       store_two(part + ((size_t)axis * kMostShare + k) * a.D, c, a.D, k == rank ? s : both(0.f));
   }
@@ -256,9 +225,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <typename T, bool kVec, bool kPacked>
 cudaError_t run(const Call& c, cudaStream_t st) {
   auto* kernel = &k_glr_backward<T, kVec, kPacked>;
-  constexpr int smem = stages_of<T>() * Tiles<T, kVec, kWarps, kRun, 4>::kBytes;
+  constexpr int kRun = mark_of(sizeof(T) == 4);
+  constexpr int smem = kStages * Tiles<T, kVec, kWarps, kRun, 4>::kBytes + (kRun - 4) * 2 * kThreads * (int)sizeof(Map);
   static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
-  return launch_cluster("k_glr_backward", kernel, fit, c.a, L, kThreads, smem, st, (const T*)c.dy, c.dh_final, (const T*)c.x,
+  return launch_cluster("k_glr_backward", kernel, fit, c.a, kRun * kWarps, kThreads, smem, st, (const T*)c.dy, c.dh_final, (const T*)c.x,
                         (const T*)c.r, (const T*)c.i, c.lam, c.h0, c.cu, (const float*)c.marks, (T*)c.dx, (T*)c.dr, (T*)c.di,
                         c.dh0, c.part);
 }

@@ -13,16 +13,20 @@ constexpr int kStages = 2;  // tiles in shared memory or on their way there
 // sequence of 16384 steps of 2560 channels takes 91 us in runs of 16 (two blocks an SM), 106 us in runs of 8 (three).  The
 // packed form's code for sequences' ends does not fit the registers with runs of 16 (24 sequences of 20011 steps: 202 us
 // against 171 us).
+#ifndef PKR
+#define PKR 8
+#define PKB 2
+#endif
 template <typename T, bool kPacked>
 constexpr int run_of() {
-  return sizeof(T) == 4 ? 4 : kPacked ? 8 : 16;
+  return sizeof(T) == 4 ? 4 : kPacked ? PKR : 16;
 }
 template <typename T, bool kPacked>
 constexpr int blocks_of() {
-  return run_of<T, kPacked>() == 16 ? 2 : 3;
+  return sizeof(T) == 4 ? 3 : kPacked ? PKB : 2;
 }
 
-// y, the final states and the marks (the states that enter every kMark-th step).  Grid: (64-channel slabs x a.share,
+// y, the final states and the marks (the states that enter the backward's runs).  Grid: (64-channel slabs x a.share,
 // sequences; one for a packed batch).  Tile j share + k of a sequence is block k's of its cluster.  One warp joins the
 // runs' maps of each tile to one that goes to all blocks of the cluster; one barrier of the cluster later each of them has
 // the state that enters its tile.
@@ -32,7 +36,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
                   const float* __restrict__ lam, const float* __restrict__ h0, const int* __restrict__ cu, T* y,
                   float* h_final, float* marks) {
   constexpr int kRun = run_of<T, kPacked>(), L = kRun * kWarps;
-  static_assert(L % kMark == 0 && kMark % kRun == 0, "states are kept where runs begin");
+  constexpr int kMark = mark_of(sizeof(T) == 4);
+  static_assert(kRun % kMark == 0, "runs begin where states are kept");
   using Tile = Tiles<T, kVec, kWarps, kRun, 3>;
   using Word = typename Words<T>::Word;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -157,10 +162,11 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
     else
       join(std::false_type());
     if (t0 >= a.T) continue;
-    if (marks && t0 % kMark == 0) store_two(marks + ((size_t)axis * nm + t0 / kMark) * a.D, c, a.D, h);
+    float* kept = marks ? marks + ((size_t)axis * nm + t0 / kMark) * a.D : nullptr;
     if (bits.first | bits.last | bits.none) {
 #pragma unroll
       for (int s = 0; s < kRun; ++s) {
+        if (kept && s % kMark == 0 && t0 + s < a.T) store_two(kept + (size_t)(s / kMark) * a.D, c, a.D, h);
         h = through<kPacked>(Map{av[s], bv[s]}, h);
         if (t0 + s >= a.T) continue;
         if (y && c < a.D) store_row<T, kVec>(ty + (oy + s * (uint32_t)a.D), second, h);
@@ -169,11 +175,12 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
           store_two(h_final + (size_t)n * a.D, c, a.D, h);
         }
       }
-    } else if (y && c < a.D) {
+    } else if (c < a.D) {
 #pragma unroll
       for (int s = 0; s < kRun; ++s) {
+        if (kept && s % kMark == 0) store_row<float, kVec>(kept + (size_t)(s / kMark) * a.D + c, second, h);
         h = fma(av[s], h, bv[s]);
-        store_row<T, kVec>(ty + (oy + s * (uint32_t)a.D), second, h);
+        if (y) store_row<T, kVec>(ty + (oy + s * (uint32_t)a.D), second, h);
       }
     }
   }

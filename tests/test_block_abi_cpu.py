@@ -51,11 +51,12 @@ def test_problem_checks(cuda_lib, kind, over, code):
 def test_sizes(cuda_lib):
     for kind in ("glr", "conv", "ffn"):
         assert size_status(cuda_lib, kind, None) == 1
-    marks = 2 * 4 * 48 * 4  # every 32nd step's states
+    marks = 2 * 13 * 48 * 4  # every eighth step's states
     assert binding.ssd_glr_stash_size(struct("glr")) == marks
     a, b = (binding.ssd_glr_workspace_size(struct("glr"), s) for s in (False, True))
     assert b < a and a - b >= marks
     assert binding.ssd_glr_stash_size(struct("glr", packed=1)) == marks // 2  # 100 steps in all
+    assert binding.ssd_glr_stash_size(struct("glr", io_dtype=0)) == 2 * 25 * 48 * 4  # every fourth in fp32
     assert binding.ssd_ffn_stash_size(struct("ffn")) == 128 * 96 * 6
     p = struct("ffn")
     assert 256 <= binding.ssd_ffn_workspace_size(p, False) < binding.ssd_ffn_workspace_size(p, True, True)
