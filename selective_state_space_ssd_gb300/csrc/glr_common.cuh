@@ -193,21 +193,21 @@ __device__ __forceinline__ void prefetch_state(const float* p, int code, int c0,
 }
 // What sequences without steps leave behind: their first state (the backward: the last state's gradient), or zeros.
 __device__ __forceinline__ void empty_sequences(const int* cu, const Args& a, int c0, const float* from, float* to) {
-  for (long long e = threadIdx.x; e < (long long)a.N * kWidth; e += blockDim.x) {
-    const int n = (int)(e / kWidth), c = c0 + (int)(e % kWidth);
-    if (c < a.D && clamp_cu(cu, n + 1, a.T) <= clamp_cu(cu, n, a.T))
-      to[(size_t)n * a.D + c] = from ? from[(size_t)n * a.D + c] : 0.f;
-  }
+  for (int n = threadIdx.x; n < a.N; n += blockDim.x)
+    if (clamp_cu(cu, n + 1, a.T) <= clamp_cu(cu, n, a.T))
+      for (int c = c0; c < c0 + kWidth && c < a.D; ++c) to[(size_t)n * a.D + c] = from ? from[(size_t)n * a.D + c] : 0.f;
 }
 // The steps of a run that begin a sequence, end one, or belong to none (bit s: step s).
 struct Bits {
   uint32_t first, last, none;
+  int code;  // lane s: step s's
+  __device__ __forceinline__ int seq(int s) const { return __shfl_sync(0xffffffffu, code, s) & kSeq; }
 };
 template <bool kPacked, int kRun>
 __device__ __forceinline__ Bits bits_of(const int* code, int t0, int T, int lane) {
-  Bits b = {0, 0, 0};
+  Bits b = {0, 0, 0, 0};
   if (kPacked) {
-    const int cd = lane < kRun ? code[lane] : 0;
+    const int cd = b.code = lane < kRun ? code[lane] : 0;
     b.none = __ballot_sync(0xffffffffu, cd < 0);
     b.first = __ballot_sync(0xffffffffu, cd < 0 || (cd & kFirst));
     b.last = __ballot_sync(0xffffffffu, cd >= 0 && (cd & kLast));

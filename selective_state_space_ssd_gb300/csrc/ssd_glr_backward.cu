@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ Map rev[2][kWarps][32];
   __shared__ Map xchg[2][kMostShare][32];
-  __shared__ int code[3][kPacked ? L : 1];
+  __shared__ int code[2][kPacked ? L : 1];
   Map* aside = reinterpret_cast<Map*>(ring + kStages * Tile::kBytes) + threadIdx.x;  // [kAside][2][kThreads]
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int share = a.share, rank = blockIdx.x % share;
@@ -47,16 +47,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   int near = 0;
   // (below 0: there is no such tile)
-  const auto codes = [&](int j, int place) {
+  const auto codes = [&](int j) {
     if (!kPacked || threadIdx.x >= L) return;
     const int found = code_of(cu, a.N, a.T, (nt - 1 - (j * share + rank)) * L + (int)threadIdx.x, near);
-    code[place][threadIdx.x] = found;
+    code[j & 1][threadIdx.x] = found;
     if (h0 && found >= 0 && (found & kFirst)) prefetch_state(h0, found, c0, a.D);
     if (dh_final && found >= 0 && (found & kLast)) prefetch_state(dh_final, found, c0, a.D);
   };
 #pragma unroll
   for (int s = 0; s < kStages; ++s) bring(s);
-  codes(0, 0);
+  codes(0);
   const P rate = load_rate(lam, c, a.D, a.scale);
   const bool far = any_far(rate), second = c + 1 < a.D;
   P back = !kPacked && dh_final ? load_two(dh_final + (size_t)axis * a.D, c, a.D) : both(0.f);  // D behind the round
@@ -76,11 +76,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const uint32_t o0 = (uint32_t)(w * kRun) * a.D + c;  // from a tile's first step
   Ring<kStages> sg;
-  Ring<3> cd;
-  for (int j = 0; j < rounds; ++j, sg.next(), cd.next()) {
+  for (int j = 0; j < rounds; ++j, sg.next()) {
     const int tile = nt - 1 - (j * share + rank), t0 = tile < 0 ? a.T : tile * L + w * kRun;
     const Word* stage = reinterpret_cast<const Word*>(ring + sg.at * Tile::kBytes) + w * kRun * 32 + lane;
-    const Bits bits = bits_of<kPacked, kRun>(&code[cd.at][kPacked ? w * kRun : 0], t0, a.T, lane);
+    const Bits bits = bits_of<kPacked, kRun>(&code[j & 1][kPacked ? w * kRun : 0], t0, a.T, lane);
     const bool odd = (bits.first | bits.none | (kPacked ? bits.last : 0)) != 0;
     // per step: a, dy; of the last four: dx / dh, di / dh, q / dh, 1 - s(r)
     P av[kRun], up[kRun], mi[4], ki[4], kq[4], r1[4];
@@ -102,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (bits.none >> s & 1) {
             av[s] = both(1.f), up[s] = both(0.f);
           } else if (kPacked) {
-            const size_t at = (size_t)(code[cd.at][w * kRun + s] & kSeq) * a.D;
+            const size_t at = (size_t)bits.seq(s) * a.D;
             if ((bits.first >> s & 1)) h = h0 ? load_two(h0 + at, c, a.D) : both(0.f);
             if ((bits.last >> s & 1) && dh_final) up[s] = up[s] + load_two(dh_final + at, c, a.D);
           }
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int s = kRun - 2; s >= 0; --s) b = Map{av[s] * b.a, av[s] * (up[s] + b.b)};
     }
     rev[j & 1][w][lane] = b;
-    codes(j + 1, cd.at == 2 ? 0 : cd.at + 1);
+    codes(j + 1);
     // the runs' maps are there, the next tile has come, and this one's stage is free
     copies_wait<kStages - 2>();
     const bool resets = kPacked && __syncthreads_or(bits.first != 0);
@@ -140,8 +139,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (share > 1) {
       if (w == kWarps - 1) {
         b = rev[j & 1][kWarps - 1][lane];
+        if (kPacked && resets) {
+#pragma unroll 1
+          for (int v = kWarps - 2; v >= 0; --v) b = after<true>(b, rev[j & 1][v][lane]);
+        } else {
 #pragma unroll
-        for (int v = kWarps - 2; v >= 0; --v) b = after<kPacked>(b, rev[j & 1][v][lane]);
+          for (int v = kWarps - 2; v >= 0; --v) b = after<false>(b, rev[j & 1][v][lane]);
+        }
         for (int k = 0; k < share; ++k) store_to(&xchg[j & 1][rank][lane], k, b);
         cluster_arrive();
       } else {
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!plain) {
         if (bits.none >> s & 1) q = vx = vi = vr = both(0.f);
         if (dh0 && (kPacked ? (bits.first & ~bits.none) >> s & 1 : t0 + s == 0))
-          store_two(dh0 + (size_t)(kPacked ? code[cd.at][w * kRun + s] & kSeq : axis) * a.D, c, a.D, d);
+          store_two(dh0 + (size_t)(kPacked ? bits.seq(s) : axis) * a.D, c, a.D, d);
         if (kPacked && (bits.first >> s & 1)) d = both(0.f);
       }
       qsum = qsum + q;

@@ -10,20 +10,15 @@ namespace {
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStages = 2;  // tiles in shared memory or on their way there
 // Steps a thread has of a tile, and blocks an SM.  Long runs share the joining of their maps and the cluster's barriers: one
-// sequence of 16384 steps of 2560 channels takes 91 us in runs of 16 (two blocks an SM), 106 us in runs of 8 (three).  The
-// packed form's code for sequences' ends does not fit the registers with runs of 16 (24 sequences of 20011 steps: 202 us
-// against 171 us).
-#ifndef PKR
-#define PKR 8
-#define PKB 2
-#endif
-template <typename T, bool kPacked>
+// sequence of 16384 steps of 2560 channels takes 91 us in runs of 16 (two blocks an SM), 106 us in runs of 8 (three); packed,
+// 24 sequences of 20011 steps take 149 us and 182 us.  fp32 words are twice as wide.
+template <typename T>
 constexpr int run_of() {
-  return sizeof(T) == 4 ? 4 : kPacked ? PKR : 16;
+  return sizeof(T) == 4 ? 4 : 16;
 }
-template <typename T, bool kPacked>
+template <typename T>
 constexpr int blocks_of() {
-  return sizeof(T) == 4 ? 3 : kPacked ? PKB : 2;
+  return sizeof(T) == 4 ? 3 : 2;
 }
 
 // y, the final states and the marks (the states that enter the backward's runs).  Grid: (64-channel slabs x a.share,
@@ -31,11 +26,11 @@ constexpr int blocks_of() {
 // runs' maps of each tile to one that goes to all blocks of the cluster; one barrier of the cluster later each of them has
 // the state that enters its tile.
 template <typename T, bool kVec, bool kPacked>
-__global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
+__global__ void __launch_bounds__(kThreads, blocks_of<T>())
     k_glr_forward(Args a, const T* __restrict__ x, const T* __restrict__ r, const T* __restrict__ i,
                   const float* __restrict__ lam, const float* __restrict__ h0, const int* __restrict__ cu, T* y,
                   float* h_final, float* marks) {
-  constexpr int kRun = run_of<T, kPacked>(), L = kRun * kWarps;
+  constexpr int kRun = run_of<T>(), L = kRun * kWarps;
   constexpr int kMark = mark_of(sizeof(T) == 4);
   static_assert(kRun % kMark == 0, "runs begin where states are kept");
   using Tile = Tiles<T, kVec, kWarps, kRun, 3>;
@@ -43,7 +38,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ Map maps[2][kWarps][32];
   __shared__ Map xchg[2][kMostShare][32];
-  __shared__ int code[3][kPacked ? L : 1];
+  __shared__ int code[2][kPacked ? L : 1];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int share = a.share, rank = blockIdx.x % share;
   const int c0 = (int)(blockIdx.x / share) * kWidth, c = c0 + lane * 2, axis = blockIdx.y;
@@ -57,15 +52,15 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
     copies_commit();
   };
   int near = 0;
-  const auto codes = [&](int j, int place) {
+  const auto codes = [&](int j) {
     if (!kPacked || threadIdx.x >= L) return;
     const int found = code_of(cu, a.N, a.T, (j * share + rank) * L + threadIdx.x, near);
-    code[place][threadIdx.x] = found;
+    code[j & 1][threadIdx.x] = found;
     if (h0 && found >= 0 && (found & kFirst)) prefetch_state(h0, found, c0, a.D);
   };
 #pragma unroll
   for (int s = 0; s < kStages; ++s) bring(s);
-  codes(0, 0);
+  codes(0);
   const P rate = load_rate(lam, c, a.D, a.scale);
   const bool far = any_far(rate), second = c + 1 < a.D;
   P carry = !kPacked && h0 ? load_two(h0 + (size_t)axis * a.D, c, a.D) : both(0.f);  // the state that enters the round
@@ -80,8 +75,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
   T* ty = y + (row0 + rank * L) * a.D;  // the tile's first step
   const uint32_t oy = (uint32_t)(w * kRun) * a.D + c;
   Ring<kStages> sg;
-  Ring<3> cd;
-  for (int j = 0; j < rounds; ++j, t0 += share * L, ty += (long long)(share * L) * a.D, sg.next(), cd.next()) {
+  for (int j = 0; j < rounds; ++j, t0 += share * L, ty += (long long)(share * L) * a.D, sg.next()) {
     const Word* stage = reinterpret_cast<const Word*>(ring + sg.at * Tile::kBytes) + w * kRun * 32 + lane;
     P av[kRun], bv[kRun];
     const auto maps_of_steps = [&](auto is_far) {
@@ -97,28 +91,35 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
       maps_of_steps(std::true_type());
     else
       maps_of_steps(std::false_type());
-    const Bits bits = bits_of<kPacked, kRun>(&code[cd.at][kPacked ? w * kRun : 0], t0, a.T, lane);
+    const Bits bits = bits_of<kPacked, kRun>(&code[j & 1][kPacked ? w * kRun : 0], t0, a.T, lane);
     if (bits.first | bits.none) {
+      // (one step at a time in one copy of the code; the steps' registers are chosen by comparisons)
+      if (kPacked && h0)
+        for (uint32_t left = bits.first & ~bits.none; left; left &= left - 1) {
+          const int at = __ffs(left) - 1;
+          const P from = load_two(h0 + (size_t)bits.seq(at) * a.D, c, a.D);
+#pragma unroll
+          for (int s = 0; s < kRun; ++s)
+            if (s == at) bv[s] = fma(av[s], from, bv[s]);
+        }
 #pragma unroll
       for (int s = 0; s < kRun; ++s) {
-        if (bits.none >> s & 1) {
-          av[s] = kPacked ? anew() : both(1.f), bv[s] = both(0.f);
-        } else if (kPacked && (bits.first >> s & 1)) {
-          if (h0) bv[s] = fma(av[s], load_two(h0 + (size_t)(code[cd.at][w * kRun + s] & kSeq) * a.D, c, a.D), bv[s]);
-          av[s] = anew();
-        }
+        if (bits.none >> s & 1) av[s] = both(1.f), bv[s] = both(0.f);
       }
     }
+    // (a packed batch's first steps are told by their bits, in the one copy of the code: a second one for runs that have any
+    // would be fetched anew each time)
+    const auto starts = [&](int s) { return kPacked && (bits.first >> s & 1); };
     Map m = {av[0], bv[0]};
-    if (kPacked && bits.first) {
 #pragma unroll
-      for (int s = 1; s < kRun; ++s) m = after<true>(m, Map{av[s], bv[s]});
-    } else {
-#pragma unroll
-      for (int s = 1; s < kRun; ++s) m = Map{m.a * av[s], fma(av[s], m.b, bv[s])};
+    for (int s = 1; s < kRun; ++s) {
+      m.a = m.a * av[s];
+      const P n = fma(av[s], m.b, bv[s]);
+      m.b = starts(s) ? bv[s] : n;
     }
+    if (kPacked && bits.first) m.a = anew();
     maps[j & 1][w][lane] = m;
-    codes(j + 1, cd.at == 2 ? 0 : cd.at + 1);
+    codes(j + 1);
     // the runs' maps are there, the next tile has come, and this one's stage is free
     copies_wait<kStages - 2>();
     const bool resets = kPacked && __syncthreads_or(bits.first != 0);
@@ -126,8 +127,13 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
     if (share > 1) {
       if (w == kWarps - 1) {
         m = maps[j & 1][0][lane];
+        if (kPacked && resets) {
+#pragma unroll 1
+          for (int v = 1; v < kWarps; ++v) m = after<true>(m, maps[j & 1][v][lane]);
+        } else {
 #pragma unroll
-        for (int v = 1; v < kWarps; ++v) m = after<kPacked>(m, maps[j & 1][v][lane]);
+          for (int v = 1; v < kWarps; ++v) m = after<false>(m, maps[j & 1][v][lane]);
+        }
         for (int k = 0; k < share; ++k) store_to(&xchg[j & 1][rank][lane], k, m);
         cluster_arrive();
       } else {
@@ -163,25 +169,30 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
       join(std::false_type());
     if (t0 >= a.T) continue;
     float* kept = marks ? marks + ((size_t)axis * nm + t0 / kMark) * a.D : nullptr;
-    if (bits.first | bits.last | bits.none) {
+    if (h_final)
+      for (uint32_t left = bits.last; left; left &= left - 1) {  // the state after each last step, walked to once more
+        const int at = __ffs(left) - 1, n = kPacked ? bits.seq(at) : axis;
+        P g = h;
+#pragma unroll
+        for (int s = 0; s < kRun; ++s)
+          if (s <= at) g = starts(s) ? bv[s] : fma(av[s], g, bv[s]);
+        store_two(h_final + (size_t)n * a.D, c, a.D, g);
+      }
+    const auto outputs = [&](auto is_short) {
 #pragma unroll
       for (int s = 0; s < kRun; ++s) {
-        if (kept && s % kMark == 0 && t0 + s < a.T) store_two(kept + (size_t)(s / kMark) * a.D, c, a.D, h);
-        h = through<kPacked>(Map{av[s], bv[s]}, h);
-        if (t0 + s >= a.T) continue;
-        if (y && c < a.D) store_row<T, kVec>(ty + (oy + s * (uint32_t)a.D), second, h);
-        if (h_final && (bits.last >> s & 1)) {
-          const int n = kPacked ? code[cd.at][w * kRun + s] & kSeq : axis;
-          store_two(h_final + (size_t)n * a.D, c, a.D, h);
-        }
+        const bool there = !decltype(is_short)::value || t0 + s < a.T;
+        if (kept && s % kMark == 0 && there) store_row<float, kVec>(kept + (size_t)(s / kMark) * a.D + c, second, h);
+        const P n = fma(av[s], h, bv[s]);
+        h = starts(s) ? bv[s] : n;
+        if (y && there) store_row<T, kVec>(ty + (oy + s * (uint32_t)a.D), second, h);
       }
-    } else if (c < a.D) {
-#pragma unroll
-      for (int s = 0; s < kRun; ++s) {
-        if (kept && s % kMark == 0) store_row<float, kVec>(kept + (size_t)(s / kMark) * a.D + c, second, h);
-        h = fma(av[s], h, bv[s]);
-        if (y) store_row<T, kVec>(ty + (oy + s * (uint32_t)a.D), second, h);
-      }
+    };
+    if (c < a.D) {
+      if (t0 + kRun > a.T)
+        outputs(std::true_type());
+      else
+        outputs(std::false_type());
     }
   }
   copies_wait<0>();
@@ -190,9 +201,9 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T, kPacked>())
 template <typename T, bool kVec, bool kPacked>
 cudaError_t run(const Call& c, cudaStream_t st) {
   auto* kernel = &k_glr_forward<T, kVec, kPacked>;
-  constexpr int smem = kStages * Tiles<T, kVec, kWarps, run_of<T, kPacked>(), 3>::kBytes;
+  constexpr int smem = kStages * Tiles<T, kVec, kWarps, run_of<T>(), 3>::kBytes;
   static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
-  return launch_cluster("k_glr_forward", kernel, fit, c.a, run_of<T, kPacked>() * kWarps, kThreads, smem, st, (const T*)c.x, (const T*)c.r, (const T*)c.i,
+  return launch_cluster("k_glr_forward", kernel, fit, c.a, run_of<T>() * kWarps, kThreads, smem, st, (const T*)c.x, (const T*)c.r, (const T*)c.i,
                         c.lam, c.h0, c.cu, (T*)c.y, c.h_final, c.marks);
 }
 template <typename T>
