@@ -415,26 +415,23 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks)
   }
 }
 
-// dw[c][j] and db[c] from n rows of partial sums: 32 channels a block, 32 rows at a time; blockIdx.y: the tap, K: db.
+// dw[c][j] and db[c] from n rows of partial sums: 32 channels a block, blockDim.y rows at a time; blockIdx.y: the tap, K: db.
 __global__ void __launch_bounds__(1024) k_conv_sums(const float* __restrict__ part, int n, int D, int K, void* dw, void* db,
                                                      bool wbf16) {
-  __shared__ float s[32][33];
+  __shared__ float s[32][32];
   const int j = blockIdx.y;
   if (j == K ? !db : !dw) return;
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (c < D) {
 #pragma unroll 4
-    for (int i = threadIdx.y; i < n; i += 32) v += part[((size_t)i * (K + 1) + j) * D + c];
+    for (int i = threadIdx.y; i < n; i += blockDim.y) v += part[((size_t)i * (K + 1) + j) * D + c];
   }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  v = s[threadIdx.x][threadIdx.y];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int col = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x != 0 || col >= D) return;
-  const size_t at = j == K ? (size_t)col : (size_t)col * K + j;
+  if (threadIdx.y != 0 || c >= D) return;
+  for (int i = 1; i < blockDim.y; ++i) v += s[i][threadIdx.x];
+  const size_t at = j == K ? (size_t)c : (size_t)c * K + j;
   if (wbf16)
     static_cast<bf16*>(j == K ? db : dw)[at] = __float2bfloat16_rn(v);
   else
@@ -522,10 +519,12 @@ void backward_of(const Call& c, cudaStream_t st) {
   SSD_LAUNCH("k_conv_backward", st,
              k_conv_backward<T, K, kW><<<grid, kThreads, 0, st>>>(c.a, (const T*)c.dy, (const T*)c.x, c.w, c.b,
                                                                   (const T*)c.taps, c.cu, (T*)c.dx, c.part, s));
-  if (c.dw || c.db)
+  if (c.dw || c.db) {
+    const int rows = (int)(axes(c.a) * chunks(c.a));
     SSD_LAUNCH("k_conv_sums", st,
-               k_conv_sums<<<dim3((c.a.D + 31) / 32, K + 1), dim3(32, 32), 0, st>>>(
-                   c.part, (int)(axes(c.a) * chunks(c.a)), c.a.D, K, c.dw, c.db, c.a.wbf16));
+               k_conv_sums<<<dim3((c.a.D + 31) / 32, K + 1), dim3(32, rows > 256 ? 32 : 8), 0, st>>>(c.part, rows, c.a.D, K, c.dw,
+                                                                                                   c.db, c.a.wbf16));
+  }
   if (c.dtaps)
     SSD_LAUNCH("k_conv_dtaps", st,
                k_conv_dtaps<T, K><<<dim3((c.a.D + kThreads - 1) / kThreads, c.a.N < 65535 ? c.a.N : 65535), kThreads, 0, st>>>(

@@ -11,6 +11,7 @@
 // The training forward keeps G and U for the backward.  dG and dU are rounded to bf16, as operands of the tensor cores have
 // to be: the one rounding of the backward before its results'.
 #include <initializer_list>
+#include <type_traits>
 
 #include "ssd.h"
 #include "ssd_device.cuh"
@@ -25,14 +26,11 @@ namespace {
 using namespace tc;
 
 constexpr int BM = 128, BK = 64;
-constexpr int kThreads = 256, kSMs = 152;
+constexpr int kThreads = 256, kSMs = 152;  // a warp for copies, one for products, four for results
 constexpr int kBytesA = BM * BK * 2;
 constexpr int kBytesOut = 2 * BM * 64 * 2;  // two tiles of 64 columns on their way out
 constexpr int kGroup = 16;  // row tiles that are walked over together, so that their operands stay in L2
 constexpr int kMostSmem = 232448;
-#ifndef FFN_NARROW
-#define FFN_NARROW 2
-#endif
 
 // Stages of a result's tile of BN columns: as many as shared memory holds.
 template <int BN>
@@ -260,12 +258,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           settled(g), settled(u);
           float h[32];
+          const auto products = [&](auto gelu) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float a, s;
-            act_and_slope(__uint_as_float(g[e]), args.gelu, a, s);
-            h[e] = a * __uint_as_float(u[e]);
-          }
+            for (int e = 0; e < 32; ++e) {
+              float a, s;
+              act_and_slope(__uint_as_float(g[e]), decltype(gelu)::value, a, s);
+              h[e] = a * __uint_as_float(u[e]);
+            }
+          };
+          if (args.gelu)
+            products(std::true_type());
+          else
+            products(std::false_type());
           store_row_bf16(out + (c >> 1) * (BM * 128), row, (c & 1) * 4, h, 4);
           if (stash) {
 #pragma unroll
@@ -373,11 +377,23 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m = blockIdx.x % few.m_tiles, n = blockIdx.x / few.m_tiles, steps = (args.D + BK - 1) / BK;
   const int bytes_a = few.rows * 128, bytes_b = few.wide * 128, bytes = bytes_a + 2 * bytes_b;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < few.stages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
-    mbar_init(&done, 1);
-    mbar_init_fence();
-    if (blockIdx.x == 0) *status = 0;
+  const auto load = [&](int k, int s) {
+    uint8_t *a = smem + s * bytes, *b = a + bytes_a;
+    mbar_expect_tx(full + s, bytes);
+    tma_load_2d(b, &maps.b[0], k * BK, n * few.wide, full + s);
+    tma_load_2d(b + bytes_b, &maps.b[1], k * BK, n * few.wide, full + s);
+    tma_load_2d(a, &maps.a[0], k * BK, m * few.rows, full + s);
+  };
+  const int ahead = steps < few.stages ? steps : few.stages;
+  if (warp == 0) {  // the first stages' copies set out before the block is ready for them
+    if (elect_one()) {
+      for (int s = 0; s < few.stages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+      mbar_init(&done, 1);
+      mbar_init_fence();
+      if (blockIdx.x == 0) *status = 0;
+      for (int k = 0; k < ahead; ++k) load(k, k);
+    }
+    __syncwarp();
   }
   if (warp == 1) tmem_alloc(&slot, 256);
   tc_fence_before();
@@ -385,16 +401,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   tc_fence_after();
   const uint32_t tmem = slot;
   if (warp == 0) {  // copies
-    int k = 0;
+    int k = ahead;
     for (int s = 0, turn = 0; k < steps; ++k) {
-      if (turn > 0 && !mbar_wait(empty + s, (turn - 1) & 1, status, 1)) break;
-      if (elect_one()) {
-        uint8_t *a = smem + s * bytes, *b = a + bytes_a;
-        mbar_expect_tx(full + s, bytes);
-        tma_load_2d(b, &maps.b[0], k * BK, n * few.wide, full + s);
-        tma_load_2d(b + bytes_b, &maps.b[1], k * BK, n * few.wide, full + s);
-        tma_load_2d(a, &maps.a[0], k * BK, m * few.rows, full + s);
-      }
+      if (!mbar_wait(empty + s, turn & 1, status, 1)) break;
+      if (elect_one()) load(k, s);
       __syncwarp();
       if (++s == few.stages) s = 0, ++turn;
     }
@@ -555,10 +565,10 @@ cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
   if (e == cudaSuccess) e = map(&maps.wo[1], c.dwu, a.D, a.F, a.D, 64, BM);
   if (e != cudaSuccess) return e;
   maps.o[1] = maps.o[0];
-  // Tiles of 128 columns where that still is two tiles an SM at most: they wait for their operands, and twice the blocks
-  // have twice as many on their way.
+  // Tiles of 128 columns where that still is three tiles an SM at most: they wait for their operands, and twice the blocks
+  // have twice as many on their way (1501 rows of 776 and 2056: 41 us, in tiles of 256 columns 43 us).
   Plan p = {up(a.M, BM), up(a.D, 128), 2 * up(a.F, BK), up(a.F, BK), 2 * up(a.F, BM), up(a.D, 128), up(a.M, BK), up(a.F, BM), 0};
-  const bool narrow = ((long long)p.m_tiles + p.w_m_tiles) * p.n_tiles <= FFN_NARROW * kSMs;
+  const bool narrow = ((long long)p.m_tiles + p.w_m_tiles) * p.n_tiles <= 3 * kSMs;
   if (!narrow) p.n_tiles = p.w_n_tiles = up(a.D, 256);
   balance(&p);
   return narrow ? launch<kGrads, 128>("k_ffn_grads", maps, p, c, st) : launch<kGrads, 256>("k_ffn_grads", maps, p, c, st);

@@ -10,21 +10,19 @@ namespace {
 
 // dlam = s(lam) / softplus(lam) sum of n rows of part; the factor goes to 1 where both vanish.
 __global__ void __launch_bounds__(1024) k_glr_lam(const float* __restrict__ part, int n, int D, const float* lam, float* dlam) {
-  __shared__ float s[32][33];
+  __shared__ float s[32][32];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
-  if (c < D)
-    for (int i = threadIdx.y; i < n; i += 32) v += part[(size_t)i * D + c];
+  if (c < D) {
+#pragma unroll 4
+    for (int i = threadIdx.y; i < n; i += blockDim.y) v += part[(size_t)i * D + c];
+  }
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  v = s[threadIdx.x][threadIdx.y];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int col = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && col < D) {
-    const float l = lam[col];
-    dlam[col] = v * (l < -60.f ? 1.f : sigmoid_f(l) / softplus_f(l));
-  }
+  if (threadIdx.y != 0 || c >= D) return;
+  for (int i = 1; i < blockDim.y; ++i) v += s[i][threadIdx.x];
+  const float l = lam[c];
+  dlam[c] = v * (l < -60.f ? 1.f : sigmoid_f(l) / softplus_f(l));
 }
 
 long long mark_count(const Args& a) { return (long long)axes(a) * ((a.T + mark_of(a.f32) - 1) / mark_of(a.f32)) * a.D; }
@@ -139,8 +137,9 @@ ssd_status ssd_glr_backward(const ssd_glr_problem* prob, const void* dy, const f
   c.dy = dy, c.dh_final = dh_final, c.dx = dx, c.dr = dr, c.di = di, c.dh0 = dh0;
   e = glr::backward(c, st);
   if (e != cudaSuccess) return SSD_ERR_CUDA;
+  const int rows = glr::axes(c.a) * glr::kMostShare;
   SSD_LAUNCH("k_glr_lam", st,
-             glr::k_glr_lam<<<(c.a.D + 31) / 32, dim3(32, 32), 0, st>>>(c.part, glr::axes(c.a) * glr::kMostShare, c.a.D, lam, dlam));
+             glr::k_glr_lam<<<(c.a.D + 31) / 32, dim3(32, rows > 256 ? 32 : 8), 0, st>>>(c.part, rows, c.a.D, lam, dlam));
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
