@@ -200,13 +200,15 @@ __device__ __forceinline__ P slope(P z, bool silu) {  // s (1 + z (1 - s))
   return silu ? s * fma(z, one_less(s), both(1.f)) : both(1.f);
 }
 
-// A block: 32 kW channels, eight runs of steps one after another.  Grid: (chunks of eight runs x channel slabs, sequences).
+// A block: 32 kW channels, eight runs of steps one after another (those of all sequences on one axis, `runs` of each).
+// Grid: chunks of eight runs x channel slabs.
 template <typename T, int K, int kW>
 __global__ void __launch_bounds__(kThreads, kFwdBlocks) k_conv_forward(Args a, const T* __restrict__ x, const void* __restrict__ w,
                                                            const void* __restrict__ b, const T* __restrict__ taps,
-                                                           const int* __restrict__ cu, T* y, T* taps_out, int slabs) {
+                                                           const int* __restrict__ cu, T* y, T* taps_out, int slabs,
+                                                           int runs) {
   constexpr int kP = Chan<kW>::kP;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, axis = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = blockIdx.x / slabs, c = ((blockIdx.x - chunk * slabs) * 32 + lane) * kW;
   if (c >= a.D) return;
   if (a.packed && taps_out && chunk == 0)  // sequences without steps keep their taps
@@ -216,9 +218,10 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) k_conv_forward(Args a, c
           const size_t at = ((size_t)n * (K - 1) + p) * a.D + c;
           put<T, kW>(taps_out + at, taps ? get<T, kW>(taps + at) : none<kW>());
         }
-  const long long first = ((long long)chunk * kWarps + warp) * a.run;
-  if (first >= a.T) return;
-  const int t0 = (int)first, t1 = (int)(first + a.run < a.T ? first + a.run : a.T);
+  const long long id = (long long)chunk * kWarps + warp;
+  const int axis = (int)(id / runs);
+  if (axis >= (a.packed ? 1 : a.N)) return;
+  const int t0 = (int)(id - (long long)axis * runs) * a.run, t1 = a.T - t0 > a.run ? t0 + a.run : a.T;
   const T* px = x + ((size_t)axis * a.T + t0) * a.xs + c;
   T* py = y + ((size_t)axis * a.T + t0) * a.D + c;
   const T *x0 = x + (size_t)axis * a.T * a.xs + c, *pt = taps ? taps + c : nullptr;
@@ -284,17 +287,18 @@ template <typename T, int K, int kW>
 __global__ void __launch_bounds__(kThreads, kBackBlocks)
     k_conv_backward(Args a, const T* __restrict__ dy, const T* __restrict__ x, const void* __restrict__ w,
                     const void* __restrict__ b, const T* __restrict__ taps, const int* __restrict__ cu, T* dx, float* part,
-                    int slabs) {
+                    int slabs, int runs) {
   constexpr int kP = Chan<kW>::kP;
   __shared__ float red[kWarps][(K + 1) * kW][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, axis = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int chunk = blockIdx.x / slabs, c = ((blockIdx.x - chunk * slabs) * 32 + lane) * kW;
-  const long long first = ((long long)chunk * kWarps + warp) * a.run;
   Chan<kW> sum[K + 1];  // dw by tap, dbias
 #pragma unroll
   for (int j = 0; j <= K; ++j) sum[j] = none<kW>();
-  if (c < a.D && first < a.T) {
-    const int t0 = (int)first, t1 = (int)(first + a.run < a.T ? first + a.run : a.T);
+  const long long id = (long long)chunk * kWarps + warp;
+  const int axis = (int)(id / runs);
+  if (c < a.D && axis < (a.packed ? 1 : a.N)) {
+    const int t0 = (int)(id - (long long)axis * runs) * a.run, t1 = a.T - t0 > a.run ? t0 + a.run : a.T;
     const T *x0 = x + (size_t)axis * a.T * a.xs + c, *pt = taps ? taps + c : nullptr;
     const T* px = x0 + (long long)t0 * a.xs;
     const T* pg = dy + ((size_t)axis * a.T + t0) * a.D + c;
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks)
   }
   __syncthreads();
   // part [rows, K + 1, D]
-  float* to = part + ((size_t)axis * (gridDim.x / slabs) + chunk) * (K + 1) * a.D;
+  float* to = part + (size_t)chunk * (K + 1) * a.D;
   for (int e = threadIdx.x; e < (K + 1) * kW * 32; e += kThreads) {
     const int j = e / (kW * 32), col = e - j * (kW * 32);  // col: channel of the slab
     const int ch = (blockIdx.x - chunk * slabs) * 32 * kW + col;
@@ -501,29 +505,28 @@ __global__ void __launch_bounds__(128) k_conv_step(Args a, const T* __restrict__
 }
 
 int axes(const Args& a) { return a.packed ? 1 : a.N; }
-long long chunks(const Args& a) { return ((long long)a.T + (long long)a.run * kWarps - 1) / ((long long)a.run * kWarps); }
+int runs(const Args& a) { return (int)(((long long)a.T + a.run - 1) / a.run); }
+long long chunks(const Args& a) { return ((long long)axes(a) * runs(a) + kWarps - 1) / kWarps; }
 int slabs(const Args& a, int kW) { return (a.D + 32 * kW - 1) / (32 * kW); }
 
 template <typename T, int K, int kW>
 void forward_of(const Call& c, cudaStream_t st) {
   const int s = slabs(c.a, kW);
-  const dim3 grid((unsigned)(chunks(c.a) * s), axes(c.a));
   SSD_LAUNCH("k_conv_forward", st,
-             k_conv_forward<T, K, kW><<<grid, kThreads, 0, st>>>(c.a, (const T*)c.x, c.w, c.b, (const T*)c.taps, c.cu,
-                                                                 (T*)c.y, (T*)c.taps_out, s));
+             k_conv_forward<T, K, kW><<<(unsigned)(chunks(c.a) * s), kThreads, 0, st>>>(
+                 c.a, (const T*)c.x, c.w, c.b, (const T*)c.taps, c.cu, (T*)c.y, (T*)c.taps_out, s, runs(c.a)));
 }
 template <typename T, int K, int kW>
 void backward_of(const Call& c, cudaStream_t st) {
   const int s = slabs(c.a, kW);
-  const dim3 grid((unsigned)(chunks(c.a) * s), axes(c.a));
   SSD_LAUNCH("k_conv_backward", st,
-             k_conv_backward<T, K, kW><<<grid, kThreads, 0, st>>>(c.a, (const T*)c.dy, (const T*)c.x, c.w, c.b,
-                                                                  (const T*)c.taps, c.cu, (T*)c.dx, c.part, s));
+             k_conv_backward<T, K, kW><<<(unsigned)(chunks(c.a) * s), kThreads, 0, st>>>(
+                 c.a, (const T*)c.dy, (const T*)c.x, c.w, c.b, (const T*)c.taps, c.cu, (T*)c.dx, c.part, s, runs(c.a)));
   if (c.dw || c.db) {
-    const int rows = (int)(axes(c.a) * chunks(c.a));
+    const int n = (int)chunks(c.a);
     SSD_LAUNCH("k_conv_sums", st,
-               k_conv_sums<<<dim3((c.a.D + 31) / 32, K + 1), dim3(32, rows > 256 ? 32 : 8), 0, st>>>(c.part, rows, c.a.D, K, c.dw,
-                                                                                                   c.db, c.a.wbf16));
+               k_conv_sums<<<dim3((c.a.D + 31) / 32, K + 1), dim3(32, n > 256 ? 32 : 8), 0, st>>>(c.part, n, c.a.D, K, c.dw, c.db,
+                                                                                                c.a.wbf16));
   }
   if (c.dtaps)
     SSD_LAUNCH("k_conv_dtaps", st,
@@ -582,18 +585,18 @@ ssd_status make_args(const ssd_conv_problem* p, Args* a) {
   a->silu = p->activation == SSD_ACT_SILU;
   a->xs = p->x_stride ? p->x_stride : p->dim;
   // Long runs read little twice, short ones give work to the whole GPU: the longest of 64, 32, 16 and 8 steps that leaves
-  // about 24 warps an SM.  The grid and the rows of partial sums stay within bounds by longer runs.
+  // about 24 warps an SM.  Longer ones where the grid would pass 2^31 blocks.
   long long run = 64;
-  const long long rows = (long long)axes(*a) * a->T, warps = 152 * 24;
-  while (run > 8 && rows / run * ((a->D + 127) / 128) < warps) run /= 2;
-  while (rows / (run * kWarps) > 4096) run *= 2;
-  a->run = (int)(run < 0x40000000ll ? run : 0x40000000ll);
+  const long long steps = (long long)axes(*a) * a->T, warps = 152 * 24;
+  while (run > 8 && steps / run * ((a->D + 127) / 128) < warps) run /= 2;
+  a->run = (int)run;
+  while (chunks(*a) * slabs(*a, 1) > 0x7fffffffll) a->run *= 2;
   return SSD_OK;
 }
 
 size_t workspace(Call* c, void* ws) {
   Carver cv(ws);
-  c->part = cv.take<float>((size_t)axes(c->a) * chunks(c->a) * (c->a.K + 1) * c->a.D);
+  c->part = cv.take<float>((size_t)chunks(c->a) * (c->a.K + 1) * c->a.D);
   return cv.off;
 }
 

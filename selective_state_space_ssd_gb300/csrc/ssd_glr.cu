@@ -135,9 +135,9 @@ ssd_status ssd_glr_backward(const ssd_glr_problem* prob, const void* dy, const f
     e = glr::forward(c, st);
   if (e != cudaSuccess) return SSD_ERR_CUDA;
   c.dy = dy, c.dh_final = dh_final, c.dx = dx, c.dr = dr, c.di = di, c.dh0 = dh0;
-  e = glr::backward(c, st);
+  int rows = 0;
+  e = glr::backward(c, st, &rows);
   if (e != cudaSuccess) return SSD_ERR_CUDA;
-  const int rows = glr::axes(c.a) * glr::kMostShare;
   SSD_LAUNCH("k_glr_lam", st,
              glr::k_glr_lam<<<(c.a.D + 31) / 32, dim3(32, rows > 256 ? 32 : 8), 0, st>>>(c.part, rows, c.a.D, lam, dlam));
   return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;

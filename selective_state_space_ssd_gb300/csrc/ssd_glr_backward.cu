@@ -17,8 +17,7 @@ constexpr int kStages = 2;  // tiles in shared memory or on their way there
 // its gradients come without a word from other warps; only the upstream gradients' maps D -> a D + a dy are joined as the
 // states are forward, in the other direction.  The factors of a run's first steps wait for that in shared memory (eight
 // numbers a step and lane, written and read by the same thread), those of its last four in registers: runs of eight steps
-// halve the barriers that runs of four would take.  part [axes kMostShare, D]: the sums of q, and zeros where fewer blocks
-// share.
+// halve the barriers that runs of four would take.  part [axes share, D]: the sums of q.
 template <typename T, bool kVec, bool kPacked>
 __global__ void __launch_bounds__(kThreads, 2)
     k_glr_backward(Args a, const T* __restrict__ dy, const float* __restrict__ dh_final, const T* __restrict__ x,
@@ -49,7 +48,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // (below 0: there is no such tile)
   const auto codes = [&](int j) {
     if (!kPacked || threadIdx.x >= L) return;
-    const int found = code_of(cu, a.N, a.T, (nt - 1 - (j * share + rank)) * L + (int)threadIdx.x, near);
+    const int found = code_of(cu, a, (nt - 1 - (j * share + rank)) * L + (int)threadIdx.x, near);
     code[j & 1][threadIdx.x] = found;
     if (h0 && found >= 0 && (found & kFirst)) prefetch_state(h0, found, c0, a.D);
     if (dh_final && found >= 0 && (found & kLast)) prefetch_state(dh_final, found, c0, a.D);
@@ -221,13 +220,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     P s = rev[0][0][lane].a;
 #pragma unroll
     for (int v = 1; v < kWarps; ++v) s = s + rev[0][v][lane].a;
-    for (int k = rank; k < kMostShare; k += share)
-      store_two(part + ((size_t)axis * kMostShare + k) * a.D, c, a.D, k == rank ? s : both(0.f));
+    store_two(part + ((size_t)axis * share + rank) * a.D, c, a.D, s);
   }
 }
 
 template <typename T, bool kVec, bool kPacked>
-cudaError_t run(const Call& c, cudaStream_t st) {
+cudaError_t run(Call& c, cudaStream_t st) {
   auto* kernel = &k_glr_backward<T, kVec, kPacked>;
   constexpr int kRun = mark_of(sizeof(T) == 4);
   constexpr int smem = kStages * Tiles<T, kVec, kWarps, kRun, 4>::kBytes + (kRun - 4) * 2 * kThreads * (int)sizeof(Map);
@@ -237,14 +235,20 @@ cudaError_t run(const Call& c, cudaStream_t st) {
                         c.dh0, c.part);
 }
 template <typename T>
-cudaError_t by_type(const Call& c, cudaStream_t st) {
+cudaError_t by_type(Call& c, cudaStream_t st) {
   if (whole(c, true)) return c.a.packed ? run<T, true, true>(c, st) : run<T, true, false>(c, st);
   return c.a.packed ? run<T, false, true>(c, st) : run<T, false, false>(c, st);
 }
 
 }  // namespace
 
-cudaError_t backward(const Call& c, cudaStream_t st) { return c.a.f32 ? by_type<float>(c, st) : by_type<bf16>(c, st); }
+cudaError_t backward(const Call& call, cudaStream_t st, int* rows) {
+  Call c = call;
+  c.a = flattened(c.a);
+  const cudaError_t e = c.a.f32 ? by_type<float>(c, st) : by_type<bf16>(c, st);
+  *rows = axes(c.a) * c.a.share;
+  return e;
+}
 
 }  // namespace glr
 }  // namespace ssd

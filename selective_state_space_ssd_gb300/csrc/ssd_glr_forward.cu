@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T>())
   int near = 0;
   const auto codes = [&](int j) {
     if (!kPacked || threadIdx.x >= L) return;
-    const int found = code_of(cu, a.N, a.T, (j * share + rank) * L + threadIdx.x, near);
+    const int found = code_of(cu, a, (j * share + rank) * L + threadIdx.x, near);
     code[j & 1][threadIdx.x] = found;
     if (h0 && found >= 0 && (found & kFirst)) prefetch_state(h0, found, c0, a.D);
   };
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T>())
 }
 
 template <typename T, bool kVec, bool kPacked>
-cudaError_t run(const Call& c, cudaStream_t st) {
+cudaError_t run(Call& c, cudaStream_t st) {
   auto* kernel = &k_glr_forward<T, kVec, kPacked>;
   constexpr int smem = kStages * Tiles<T, kVec, kWarps, run_of<T>(), 3>::kBytes;
   static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
@@ -207,7 +207,8 @@ cudaError_t run(const Call& c, cudaStream_t st) {
                         c.lam, c.h0, c.cu, (T*)c.y, c.h_final, c.marks);
 }
 template <typename T>
-cudaError_t by_type(const Call& c, cudaStream_t st) {
+cudaError_t by_type(Call c, cudaStream_t st) {
+  c.a = flattened(c.a);
   if (whole(c, false)) return c.a.packed ? run<T, true, true>(c, st) : run<T, true, false>(c, st);
   return c.a.packed ? run<T, false, true>(c, st) : run<T, false, false>(c, st);
 }

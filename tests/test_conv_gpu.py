@@ -86,7 +86,7 @@ def compare(c, cu=None, bounds=None, act="silu", taps=True, bias=True):
 @pytest.mark.parametrize("io,wt", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
 @pytest.mark.parametrize("n,steps,dim,k", [(1, 1, 1, 4), (2, 2, 3, 4), (1, 3, 128, 4), (3, 4, 129, 3), (2, 7, 64, 2),
                                            (1, 8, 130, 4), (2, 9, 132, 4), (1, 64, 256, 4), (2, 65, 100, 3), (1, 129, 36, 2),
-                                           (4, 300, 40, 4), (1, 1000, 33, 4), (300, 5, 16, 4)])
+                                           (4, 300, 40, 4), (1, 1000, 33, 4), (300, 5, 16, 4), (9000, 3, 8, 4)])
 def test_matches_float64(n, steps, dim, k, io, wt):
     compare(make((n, steps), dim, k, io, wt, 1, n))
 

@@ -105,7 +105,7 @@ def compare(c, cu=None, bounds=None, h0=True, dh=True, stash=True):
 # one step, both sides of a run, a mark, a tile and several tiles; widths on both sides of a slab, whole and ragged pieces
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("n,steps,dim", [(1, 1, 1), (2, 2, 3), (1, 7, 64), (3, 8, 65), (2, 9, 32), (1, 31, 33), (2, 32, 8),
-                                         (1, 33, 72), (2, 63, 130), (1, 64, 128), (2, 65, 40), (1, 97, 63), (2, 129, 96),
+                                         (1, 33, 72), (2, 63, 130), (1, 64, 128), (2, 65, 40), (1, 97, 63), (2, 129, 96), (300, 5, 16), (50, 33, 40),
                                          (1, 257, 16), (5, 300, 100), (1, 1000, 24), (2, 517, 200)])
 def test_matches_float64(n, steps, dim, io):
     compare(make((n, steps), dim, io, 1, n))

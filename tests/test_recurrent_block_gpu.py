@@ -3,6 +3,10 @@ in plain torch in fp32 with the recurrence step by step, and prompts plus single
 
 Bounds: y carries a few bf16 roundings one after another (projections, norms, convolution, recurrence, feed-forward): 2e-2 of
 its largest value; the gradients pass them twice, through sums over tokens: 3e-2 in 2-norm."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -212,3 +216,27 @@ def test_calls_on_two_streams_at_once():
     for n, out in got:
         for a, b in zip(out, want[n]):
             assert torch.equal(a, b), n
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    code = """
+import torch
+from selective_state_space_ssd_gb300 import binding as b
+x = torch.randn((2, 200, 64), device="cuda").bfloat16()
+lam, w = torch.zeros(64, device="cuda") - 4, torch.randn((64, 4), device="cuda")
+wg = torch.randn((96, 64), device="cuda").bfloat16()
+def calls():
+    out = [*b.glr_forward(x, x, x, lam), *b.conv_forward(x, w), b.ffn_forward(x, wg, wg)]
+    out += [b.glr_backward(x, x, x, x, lam)["dx"], b.conv_backward(x, x, w)["dx"], b.ffn_backward(out[-1], x, wg, wg)["dx"]]
+    return out
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = calls()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(got, calls()))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
