@@ -7,6 +7,9 @@
 // One kernel for all of them, k_ffn_product: output tiles of 128 x 256, one block an SM that walks over tiles; a warp issues
 // the copies, one the products, four turn accumulators into results while the next tile is under way (two accumulators of
 // 256 columns).  In the forward's tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets both.
+// Blocks go in clusters of two, with tiles of the same columns: each copies half of the columns' operand into both, which
+// takes a third off what comes out of L2 (8192 rows of 2560 and 7680, forward and backward: 1375 -> 1340 us; 1501 of 776 and
+// 2056: 75 -> 61 us).  Tiles of 128 x 128 where they end sooner (sooner()).
 //
 // The training forward keeps G and U for the backward.  dG and dU are rounded to bf16, as operands of the tensor cores have
 // to be: the one rounding of the backward before its results'.
@@ -29,7 +32,7 @@ constexpr int BM = 128, BK = 64;
 constexpr int kThreads = 256, kSMs = 152;  // a warp for copies, one for products, four for results
 constexpr int kBytesA = BM * BK * 2;
 constexpr int kBytesOut = 2 * BM * 64 * 2;  // two tiles of 64 columns on their way out
-constexpr int kGroup = 16;  // row tiles that are walked over together, so that their operands stay in L2
+constexpr int kGroup = 8;  // pairs of row tiles that are walked over together, so that their operands stay in L2
 constexpr int kMostSmem = 232448;
 
 // Stages of a result's tile of BN columns: as many as shared memory holds.
@@ -57,26 +60,28 @@ struct Maps {
 struct Plan {
   int m_tiles, n_tiles, steps, half;      // tiles and steps of BK; dx: half of the steps are of the first pair of matrices
   int w_m_tiles, w_n_tiles, w_steps, w_half;  // the weights' gradients; half of the row tiles are of the first matrix
-  int both;                                   // of those, tiles that every block has
+  int both;                                   // of those, pairs of tiles that every pair of blocks has
 };
-// The n-th tile of a block.  The forward's go round the blocks.  dx's do too, and the first of them leave some blocks with
-// one more; the weights' gradients' follow, `both` for every block and the others for those with fewer of dx's, as many as
-// end the two kinds of blocks about together (balance()).
+// Two blocks, a cluster, work on two row tiles of the same columns side by side.  The n-th of such pairs of tiles of a pair
+// of blocks: the forward's go round.  dx's do too, and the first of them leave some with one more; the weights' gradients'
+// follow, `both` for every pair of blocks and the others for those with fewer of dx's, as many as end the two kinds about
+// together (balance()).
 struct Item {
   bool weights;
   int t;
 };
+__host__ __device__ __forceinline__ int pairs_of(int m_tiles, int n_tiles) { return (m_tiles + 1) / 2 * n_tiles; }
 template <int kKind>
 __device__ __forceinline__ bool item_of(const Plan& p, int n, Item& it) {
-  const int blocks = gridDim.x, i = blockIdx.x, tiles = p.m_tiles * p.n_tiles;
+  const int blocks = gridDim.x / 2, i = blockIdx.x / 2, tiles = pairs_of(p.m_tiles, p.n_tiles);
   it.weights = false;
   it.t = n * blocks + i;
   if (it.t < tiles) return true;
   if (kKind == kForward) return false;
-  const int more = tiles % blocks, k = n - (tiles / blocks + (i < more));  // blocks that have one more of dx's: 0 .. more - 1
+  const int more = tiles % blocks, k = n - (tiles / blocks + (i < more));  // those that have one more of dx's: 0 .. more - 1
   it.weights = true;
   it.t = k < p.both ? k * blocks + i : p.both * blocks + (k - p.both) * (blocks - more) + i - more;
-  return (k < p.both || i >= more) && it.t < p.w_m_tiles * p.w_n_tiles;
+  return (k < p.both || i >= more) && it.t < pairs_of(p.w_m_tiles, p.w_n_tiles);
 }
 
 __device__ __forceinline__ void act_and_slope(float g, bool gelu, float& a, float& s) {
@@ -128,10 +133,30 @@ __device__ __forceinline__ void kept_values(const Kept& k, float (&v)[8]) {
   }
 }
 
-__device__ __forceinline__ void tile_of(int m_tiles, int n_tiles, int t, int& m, int& n) {
-  const int per = kGroup * n_tiles, g = t / per, m0 = g * kGroup, gm = min(kGroup, m_tiles - m0), r = t - g * per;
-  m = m0 + r % gm;
+// This block's row tile (m_tiles: there is none) and column tile of an item.
+__device__ __forceinline__ void tile_of(const Plan& p, const Item& it, int& m, int& n) {
+  const int m_pairs = ((it.weights ? p.w_m_tiles : p.m_tiles) + 1) / 2, n_tiles = it.weights ? p.w_n_tiles : p.n_tiles;
+  const int per = kGroup * n_tiles, g = it.t / per, m0 = g * kGroup, gm = min(kGroup, m_pairs - m0), r = it.t - g * per;
+  m = 2 * (m0 + r % gm) + (blockIdx.x & 1);
   n = r / gm;
+}
+
+// The pair of blocks: copies that go to both, and arrivals at both blocks' barriers.
+__device__ __forceinline__ void tma_load_2d_both(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
+      "[%4], %5;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Registers of a tcgen05.ld after its wait: nothing that reads them may be moved in front of this.
@@ -144,7 +169,7 @@ template <int kKind, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_ffn_product(const __grid_constant__ Maps maps, Plan plan, Args args, uint8_t* stash, int* status) {
   constexpr int kStages = Stages<BN>::kN, kBytesStage = Stages<BN>::kBytes, kBytesB = Stages<BN>::kBytesB;
-  static_assert(kKind != kForward || BN == 256, "128 columns of G and of U");
+  constexpr int kOwn = BN / 2;  // the forward: columns of G, and of U
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
   uint8_t* out = smem + kStages * kBytesStage;
@@ -153,46 +178,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 2);
     for (int s = 0; s < 2; ++s) mbar_init(tfull + s, 1), mbar_init(tempty + s, 4);
     mbar_init_fence();
     if (kKind == kForward && blockIdx.x == 0) *status = 0;
   }
   if (warp == 2) tmem_alloc(slot, 2 * BN);
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // (both blocks' barriers are there before anything arrives at them)
   tc_fence_after();
   const uint32_t tmem = *slot;
 
   if (warp == 0) {  // copies
+    // A block's own rows, and half of the columns, which go to both blocks.
+    const int rank = blockIdx.x & 1;
     const auto load = [&](int s, bool weights, int m, int n, int k) {
       uint8_t *a = smem + s * kBytesStage, *b = a + kBytesA;
       mbar_expect_tx(full + s, kBytesStage);
       if (kKind == kForward) {
         tma_load_2d(a, &maps.a[0], k * BK, m * BM, full + s);
-        tma_load_2d(b, &maps.b[0], k * BK, n * 128, full + s);
-        tma_load_2d(b + kBytesB / 2, &maps.b[1], k * BK, n * 128, full + s);
+        tma_load_2d_both(b + rank * (kBytesB / 2), &maps.b[rank], k * BK, n * kOwn, full + s);
       } else if (!weights) {
         const int which = k >= plan.half, kk = (k - (which ? plan.half : 0)) * BK;
         tma_load_2d(a, &maps.a[which], kk, m * BM, full + s);
 #pragma unroll
-        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.b[which], n * BN + j * 64, kk, full + s);
+        for (int j = 0; j < BN / 128; ++j) {
+          const int col = rank * (BN / 128) + j;
+          tma_load_2d_both(b + col * 8192, &maps.b[which], n * BN + col * 64, kk, full + s);
+        }
       } else {
         const int which = m >= plan.w_half, row = (m - (which ? plan.w_half : 0)) * BM;
 #pragma unroll
         for (int j = 0; j < BM / 64; ++j) tma_load_2d(a + j * 8192, &maps.wa[which], row + j * 64, k * BK, full + s);
 #pragma unroll
-        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.wb, n * BN + j * 64, k * BK, full + s);
+        for (int j = 0; j < BN / 128; ++j) {
+          const int col = rank * (BN / 128) + j;
+          tma_load_2d_both(b + col * 8192, &maps.wb, n * BN + col * 64, k * BK, full + s);
+        }
       }
     };
     int it = 0;
     bool ok = true;
     Item tile;
     for (int i = 0; ok && item_of<kKind>(plan, i, tile); ++i) {
-      const int m_tiles = tile.weights ? plan.w_m_tiles : plan.m_tiles, n_tiles = tile.weights ? plan.w_n_tiles : plan.n_tiles;
       const int steps = tile.weights ? plan.w_steps : plan.steps;
       int m, n;
-      tile_of(m_tiles, n_tiles, tile.t, m, n);
+      tile_of(plan, tile, m, n);
       for (int k = 0; k < steps; ++k, ++it) {
         const int s = it % kStages;
         if (it >= kStages && !(ok = mbar_wait(empty + s, (it / kStages - 1) & 1, status, 1))) break;
@@ -200,8 +232,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    // what is still on its way has to arrive before the block may end
-    for (int j = max(0, it - kStages); j < it; ++j) mbar_wait(full + j % kStages, (j / kStages) & 1, status, 2);
+    // the last stages have to be done with, in both blocks, before this one may end: copies and arrivals come from both
+    for (int j = max(0, it - kStages); j < it; ++j) mbar_wait(empty + j % kStages, (j / kStages) & 1, status, 2);
   } else if (warp == 1) {  // products
     int it = 0, done = 0;
     bool ok = true;
@@ -226,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < BK; kk += 16)
             mma_bf16(tmem + acc * BN, da + (kk / 16) * step_a, db + (kBmn ? mdesc_step(kk) : kdesc_step(BN, kk)), idesc,
                      k > 0 || kk > 0);
-          mma_commit(empty + s);
+          mma_commit_both(empty + s);
         }
         __syncwarp();
       }
@@ -241,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item tile;
     for (; item_of<kKind>(plan, done, tile); ++done) {
       int m, n;
-      tile_of(tile.weights ? plan.w_m_tiles : plan.m_tiles, tile.weights ? plan.w_n_tiles : plan.n_tiles, tile.t, m, n);
+      tile_of(plan, tile, m, n);
+      const bool there = m < (tile.weights ? plan.w_m_tiles : plan.m_tiles);  // (an odd last row tile has no neighbour)
       const int acc = done & 1;
       const bool ok = mbar_wait(tfull + acc, (done / 2) & 1, status, 6);
       if (named_bar_or(1, 128, !ok)) break;
@@ -251,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q == 0 && lane == 0) tma_store_wait_read0();
         named_bar(1, 128);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kOwn / 32; ++c) {
           uint32_t g[32], u[32];
           tmem_ld32_nowait(base + c * 32, g);
-          tmem_ld32_nowait(base + 128 + c * 32, u);
+          tmem_ld32_nowait(base + kOwn + c * 32, u);
           tmem_wait_ld();
           settled(g), settled(u);
           float h[32];
@@ -271,20 +304,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             products(std::false_type());
           store_row_bf16(out + (c >> 1) * (BM * 128), row, (c & 1) * 4, h, 4);
-          if (stash) {
+          if (stash && there) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              if (n * 128 + c * 32 + j * 8 < args.F)
-                keep(stash, args, m * BM + row, n * 128 + c * 32 + j * 8, g + 8 * j, u + 8 * j);
+              if (n * kOwn + c * 32 + j * 8 < args.F)
+                keep(stash, args, m * BM + row, n * kOwn + c * 32 + j * 8, g + 8 * j, u + 8 * j);
           }
         }
         tc_fence_before();
         if (lane == 0) mbar_arrive(tempty + acc);
         fence_proxy_async();
         named_bar(1, 128);
-        if (q == 0 && lane == 0) {
-          tma_store_2d(&maps.o[0], out, n * 128, m * BM);
-          if (n * 128 + 64 < args.F) tma_store_2d(&maps.o[0], out + BM * 128, n * 128 + 64, m * BM);
+        if (q == 0 && lane == 0 && there) {
+#pragma unroll
+          for (int c = 0; c < kOwn; c += 64)
+            if (n * kOwn + c < args.F) tma_store_2d(&maps.o[0], out + c * BM * 2, n * kOwn + c, m * BM);
           tma_store_commit();
         }
       } else {
@@ -310,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async();
           named_bar(1, 128);
           if (q == 0 && lane == 0) {
-            if (n * BN + p * 64 < args.D) tma_store_2d(to_map, to, n * BN + p * 64, row0);
+            if (there && n * BN + p * 64 < args.D) tma_store_2d(to_map, to, n * BN + p * 64, row0);
             tma_store_commit();
           }
         }
@@ -320,8 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (q == 0 && lane == 0) tma_store_wait0();
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // (nothing of the other block's is on its way here any more)
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 2 * BN);
@@ -482,18 +517,31 @@ cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const C
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Stages<BN>::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  const int tiles = plan.m_tiles * plan.n_tiles + (kKind == kGrads ? plan.w_m_tiles * plan.w_n_tiles : 0);
+  const int pairs = pairs_of(plan.m_tiles, plan.n_tiles) + (kKind == kGrads ? pairs_of(plan.w_m_tiles, plan.w_n_tiles) : 0);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pairs < kSMs / 2 ? 2 * pairs : kSMs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Stages<BN>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t launched = cudaSuccess;
   SSD_LAUNCH(name, st,
-             kernel<<<tiles < kSMs ? tiles : kSMs, kThreads, Stages<BN>::kSmem, st>>>(
-                 maps, plan, c.a, kKind == kForward ? c.stash : nullptr, c.status));
-  return cudaGetLastError();
+             launched = cudaLaunchKernelEx(&cfg, kernel, maps, plan, c.a, kKind == kForward ? c.stash : (uint8_t*)nullptr,
+                                           c.status));
+  return launched;
 }
-// dx and the weights' gradients in one launch: how many of the latter's tiles every block takes, so that the last block
-// ends soonest (steps of a block with one more of dx's tiles, and of the others).  8192 rows of 2560 and 7680: 640 tiles of
-// 240 steps and 1200 of 128 on 152 blocks end after 2112 steps, one after the other they would after 2224.
-void balance(Plan* p) {
-  const int tiles = p->m_tiles * p->n_tiles, w_tiles = p->w_m_tiles * p->w_n_tiles;
-  const int blocks = tiles + w_tiles < kSMs ? tiles + w_tiles : kSMs;
+// dx and the weights' gradients in one launch: how many of the latter's pairs of tiles every pair of blocks takes, so
+// that the last ends soonest (steps of those with one more of dx's, and of the others).  Returns the steps until then.  8192
+// rows of 2560 and 7680: 320 pairs of tiles of 240 steps and 600 of 128 on 76 pairs of blocks end after 2112 steps, one kind
+// after the other they would after 2224.
+long long balance(Plan* p) {
+  const int tiles = pairs_of(p->m_tiles, p->n_tiles), w_tiles = pairs_of(p->w_m_tiles, p->w_n_tiles);
+  const int blocks = tiles + w_tiles < kSMs / 2 ? tiles + w_tiles : kSMs / 2;
   const int more = tiles % blocks, each = tiles / blocks, others = blocks - more;
   long long best = -1;
   const int least = w_tiles / blocks - p->steps / p->w_steps - 2;  // (with fewer, the others would end later than the first)
@@ -504,7 +552,14 @@ void balance(Plan* p) {
     const long long end = first > second ? first : second;
     if (best < 0 || end < best) best = end, p->both = both;
   }
+  return best;
 }
+
+// Whether tiles of half the columns end sooner: their step takes about 5/8 of a whole one's, and they are dealt out more
+// evenly.  Forward, us: 1501 rows of 776 and 2056 in narrow ones 22.6, in wide ones 25.2; 2048 of 1024 and 4096 42.0 and
+// 39.2; 8192 of 2560 and 7680 490 and 392.  Gradients, the same sizes: 32.2 and 32.7, 59 and 52, 916 and 725; 256 rows of
+// 2560 and 7680, whose few long sums of dx are what it waits for, 64 and 97.
+bool sooner(long long narrow_steps, long long wide_steps) { return narrow_steps * 5 < wide_steps * 8; }
 
 int up(long long a, int b) { return (int)((a + b - 1) / b); }
 
@@ -524,7 +579,9 @@ cudaError_t forward(const Call& c, cudaStream_t st) {
   Maps maps;
   Few few;
   const bool is_few = few_rows(c.a, &few);
-  const int wide = is_few ? few.wide : 128;
+  const auto rounds = [&](int cols) { return up(pairs_of(up(c.a.M, BM), up(c.a.F, cols)), kSMs / 2); };
+  const bool narrow = sooner(rounds(64), rounds(128));
+  const int wide = is_few ? few.wide : narrow ? 64 : 128;
   cudaError_t e = map(&maps.a[0], c.x, c.a.D, c.a.M, c.a.xs, BK, is_few ? few.rows : BM);
   if (e == cudaSuccess) e = map(&maps.b[0], c.wg, c.a.D, c.a.F, c.a.D, BK, wide);
   if (e == cudaSuccess) e = map(&maps.b[1], c.wu, c.a.D, c.a.F, c.a.D, BK, wide);
@@ -533,7 +590,9 @@ cudaError_t forward(const Call& c, cudaStream_t st) {
   maps.a[1] = maps.a[0];
   if (!is_few) {
     maps.o[1] = maps.o[0], maps.wa[0] = maps.wa[1] = maps.wb = maps.wo[0] = maps.wo[1] = maps.a[0];
-    return launch<kForward, 256>("k_ffn_forward", maps, Plan{up(c.a.M, BM), up(c.a.F, 128), up(c.a.D, BK)}, c, st);
+    const Plan p = {up(c.a.M, BM), up(c.a.F, wide), up(c.a.D, BK)};
+    return narrow ? launch<kForward, 128>("k_ffn_forward", maps, p, c, st)
+                  : launch<kForward, 256>("k_ffn_forward", maps, p, c, st);
   }
   maps.o[0] = maps.o[1] = maps.wa[0] = maps.wa[1] = maps.wb = maps.wo[0] = maps.wo[1] = maps.a[0];
   // (behind the last stage's rows the products still read what 128 rows would take)
@@ -565,12 +624,12 @@ cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
   if (e == cudaSuccess) e = map(&maps.wo[1], c.dwu, a.D, a.F, a.D, 64, BM);
   if (e != cudaSuccess) return e;
   maps.o[1] = maps.o[0];
-  // Tiles of 128 columns where that still is three tiles an SM at most: they wait for their operands, and twice the blocks
-  // have twice as many on their way (1501 rows of 776 and 2056: 41 us, in tiles of 256 columns 43 us).
-  Plan p = {up(a.M, BM), up(a.D, 128), 2 * up(a.F, BK), up(a.F, BK), 2 * up(a.F, BM), up(a.D, 128), up(a.M, BK), up(a.F, BM), 0};
-  const bool narrow = ((long long)p.m_tiles + p.w_m_tiles) * p.n_tiles <= 3 * kSMs;
-  if (!narrow) p.n_tiles = p.w_n_tiles = up(a.D, 256);
-  balance(&p);
+  Plan wide = {up(a.M, BM),     up(a.D, 256), 2 * up(a.F, BK), up(a.F, BK),
+               2 * up(a.F, BM), up(a.D, 256), up(a.M, BK),     up(a.F, BM), 0};
+  Plan p = wide;
+  p.n_tiles = p.w_n_tiles = up(a.D, 128);
+  const bool narrow = sooner(balance(&p), balance(&wide));
+  if (!narrow) p = wide;
   return narrow ? launch<kGrads, 128>("k_ffn_grads", maps, p, c, st) : launch<kGrads, 256>("k_ffn_grads", maps, p, c, st);
 }
 

@@ -67,8 +67,10 @@ def test_matches_float64(m, d, f, act):
     compare(make(m, d, f, 1), act)
 
 
-def test_more_tiles_than_blocks():
-    compare(make(2100, 328, 2568, 2), "silu")
+@pytest.mark.parametrize("m,d,f", [(2100, 328, 2568), (1100, 1544, 2568), (1100, 72, 2568)])
+def test_more_tiles_than_blocks(m, d, f):
+    """An odd number of row tiles, whose last has no neighbour; wide and narrow tiles, forward and backward."""
+    compare(make(m, d, f, 2), "silu")
 
 
 def test_stash_changes_no_bit():
