@@ -28,7 +28,8 @@ def first_orders(grads, *of):
 
 
 class ShortConv(torch.autograd.Function):
-    """``binding.conv_forward`` / ``binding.conv_backward`` on whole sequences [b, T, D]: y and the taps that follow."""
+    """``binding.conv_forward`` / ``binding.conv_backward`` on whole sequences [b, T, D] (or [T, D]): y and the taps that
+    follow."""
 
     @staticmethod
     def forward(ctx, x, weight, bias=None, taps=None, activation="silu"):
@@ -45,9 +46,9 @@ class ShortConv(torch.autograd.Function):
         g = binding.conv_backward(dy, x, weight, bias, ctx.activation, taps)
         dx, dtaps = g["dx"], g["dtaps"]
         if dlast is not None:  # the taps that follow are the last of the taps before and the inputs
-            steps, held = x.shape[1], dlast.shape[1]
+            steps, held = x.shape[-2], dlast.shape[1]
             own = min(steps, held)
-            dx[:, steps - own:] += dlast[:, held - own:]
+            dx.view(-1, *x.shape[-2:])[:, steps - own:] += dlast[:, held - own:]
             if dtaps is not None and own < held:
                 dtaps[:, own:] += dlast[:, :held - own]
         grads = first_orders((dx, g["dw"], g["db"], dtaps), dy, dlast, x, weight, bias, taps)

@@ -139,6 +139,22 @@ def test_sequences_in_two_pieces_have_the_same_gradients():
             assert rel(a, c) <= 1e-5
 
 
+@pytest.mark.parametrize("steps", [2, 9])
+def test_one_sequence_without_a_batch_axis(steps):
+    """The gradients of y, the taps and the state that follow, of [T, D] and of [1, T, D]: the same calls, the same bits."""
+    _, rn = make(6)
+    base, w, taps, dy, dl, ds = rn(steps, 24), rn(24, 4), rn(1, 3, 24), rn(steps, 24), rn(1, 3, 24), rn(1, 24).float()
+    lam = torch.zeros(24, device="cuda")
+    got = []
+    for lead in ((), (1,)):
+        x = base.reshape(*lead, steps, 24).clone().requires_grad_()
+        k = taps.clone().requires_grad_()
+        y, last = ShortConv.apply(x, w, None, k)
+        s, h = Recurrence.apply(y, y, y, lam)
+        got.append(torch.autograd.grad([s, last, h], [x, k], [dy.reshape(s.shape), dl, ds]))
+    assert torch.equal(got[0][0], got[1][0][0]) and torch.equal(got[0][1], got[1][1])
+
+
 def test_gradients_that_are_not_asked_for():
     gen = torch.Generator(device="cuda").manual_seed(8)
     rn = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
