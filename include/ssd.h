@@ -536,9 +536,9 @@ ssd_status ssd_norm_backward(const ssd_norm_problem* prob, const void* dy, const
  *               values are clamped to 0 .. seqlen; empty sequences are allowed:
  *               their h_final is their h0).  y and the gradients are zero at
  *               steps of no sequence.  ssd_glr_step takes packed = 0.
- *   batch, seqlen, dim (D): >= 1.  Limits of this build (SSD_ERR_SHAPE): steps
- *               below 2^31 - 4095, D and strides up to 2^24, batch below 2^29,
- *               and up to 65535 where sequences are not packed.
+ *   batch, seqlen, dim (D): >= 1.  Limits of this build (SSD_ERR_SHAPE): T up
+ *               to 2^31 - 65536 and below 2^31 steps in all, D and strides up to
+ *               2^24, batch below 2^29, and up to 65535 where not packed.
  *   x_stride, r_stride, i_stride: elements from a step to the next, for
  *               tensors that lie inside wider ones; 0 = dense.  Batches follow
  *               one another at T strides.  Everything else is dense.

@@ -26,9 +26,10 @@ namespace glr {
 
 // The stash holds the state that enters every so many steps: each run of the backward's threads.
 constexpr int mark_of(bool f32) { return f32 ? 4 : 8; }
-constexpr int kWidth = 64;    // channels of a block
-constexpr int kMostShare = 8;   // blocks that share a sequence, at most
+constexpr int kWidth = 64;     // channels of a block
+constexpr int kMostShare = 8;  // blocks that share a sequence, at most
 constexpr long long kMostStride = 1 << 24;  // elements from a step to the next: those of a tile's 128 steps fit 32 bits
+constexpr long long kMostSteps = 0x7fff0000;  // of an axis: a few tiles more than it has are counted in 32 bits
 
 struct Args {
   int N, T, D;  // sequences, steps (of each, or of the packed axis), channels
@@ -296,10 +297,6 @@ struct Ring {
   __device__ __forceinline__ void next() { at = at + 1 == kN ? 0 : at + 1; }
 };
 
-// Launches a kernel in clusters of a.share blocks (1: none), which it sets: as many as leave every block a tile of L steps
-// and all clusters room on the GPU at once, by the runtime's count (a cluster that has to wait for its turn doubles the
-// time: 40 slabs of one sequence of 16384 steps took 209 us backward in clusters of six, 313 in clusters of eight, of which
-// only 36 fit).
 template <typename... KArgs>
 cudaLaunchConfig_t config_of(void (*kernel)(KArgs...), int threads, int smem, cudaLaunchAttribute* attr, int share) {
   cudaLaunchConfig_t cfg = {};
@@ -333,6 +330,10 @@ struct Fit {  // of one kernel: clusters of 1 .. kMostShare blocks that fit at o
     return s;
   }
 };
+// Launches a kernel in clusters of a.share blocks (1: none), which it sets: as many as leave every block a tile of L steps
+// and all clusters room on the GPU at once, by the runtime's count.  A cluster that has to wait for its turn costs more than
+// it brings: 40 slabs of one sequence of 16384 steps take 90 us forward and 166 backward in clusters of six, 110 and 246 in
+// clusters of eight, of which only 36 fit.
 template <typename Kernel, typename... Args_>
 cudaError_t launch_cluster(const char* name, Kernel kernel, const Fit<Kernel>& fit, Args& a, int L, int threads, int smem,
                            cudaStream_t st, Args_... args) {
@@ -354,7 +355,7 @@ cudaError_t launch_cluster(const char* name, Kernel kernel, const Fit<Kernel>& f
 inline Args flattened(const Args& a) {
   const int L = 8 * mark_of(a.f32);
   Args f = a;
-  if (a.packed || a.N < 2 || a.T >= L || (long long)a.N * a.T > 0x7ffff000ll) return f;
+  if (a.packed || a.N < 2 || a.T >= L || (long long)a.N * a.T > kMostSteps) return f;
   const long long room = 2 * 152, wide = slabs(a), share = room / wide < 1 ? 1 : room / wide < kMostShare ? room / wide : kMostShare;
   const long long apart = (wide * a.N + room - 1) / room;
   const long long joined = ((long long)a.N * a.T + L * share - 1) / (L * share) * ((wide + room - 1) / room);

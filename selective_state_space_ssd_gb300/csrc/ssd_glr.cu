@@ -51,7 +51,7 @@ ssd_status make_args(const ssd_glr_problem* p, Args* a) {
   if ((p->io_dtype != SSD_F32 && p->io_dtype != SSD_BF16) || (p->packed != 0 && p->packed != 1)) return SSD_ERR_INVALID_ARG;
   if (p->batch < 1 || p->seqlen < 1 || p->dim < 1 || p->x_stride < 0 || p->r_stride < 0 || p->i_stride < 0)
     return SSD_ERR_INVALID_ARG;
-  if (p->seqlen > 0x7ffff000ll || p->batch >= kLast || p->dim > kMostStride) return SSD_ERR_SHAPE;
+  if (p->seqlen > kMostSteps || p->batch >= kLast || p->dim > kMostStride) return SSD_ERR_SHAPE;
   if (!p->packed && (p->batch > 65535 || p->batch * p->seqlen > 0x7fffffffll)) return SSD_ERR_SHAPE;
   for (const int64_t s : {p->x_stride, p->r_stride, p->i_stride})
     if ((s && s < p->dim) || s > kMostStride) return SSD_ERR_SHAPE;

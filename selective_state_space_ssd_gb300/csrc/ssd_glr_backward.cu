@@ -230,9 +230,9 @@ cudaError_t run(Call& c, cudaStream_t st) {
   constexpr int kRun = mark_of(sizeof(T) == 4);
   constexpr int smem = kStages * Tiles<T, kVec, kWarps, kRun, 4>::kBytes + (kRun - 4) * 2 * kThreads * (int)sizeof(Map);
   static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
-  return launch_cluster("k_glr_backward", kernel, fit, c.a, kRun * kWarps, kThreads, smem, st, (const T*)c.dy, c.dh_final, (const T*)c.x,
-                        (const T*)c.r, (const T*)c.i, c.lam, c.h0, c.cu, (const float*)c.marks, (T*)c.dx, (T*)c.dr, (T*)c.di,
-                        c.dh0, c.part);
+  return launch_cluster("k_glr_backward", kernel, fit, c.a, kRun * kWarps, kThreads, smem, st, (const T*)c.dy, c.dh_final,
+                        (const T*)c.x, (const T*)c.r, (const T*)c.i, c.lam, c.h0, c.cu, (const float*)c.marks, (T*)c.dx,
+                        (T*)c.dr, (T*)c.di, c.dh0, c.part);
 }
 template <typename T>
 cudaError_t by_type(Call& c, cudaStream_t st) {

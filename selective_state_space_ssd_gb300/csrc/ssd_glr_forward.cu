@@ -21,6 +21,12 @@ constexpr int blocks_of() {
   return sizeof(T) == 4 ? 3 : 2;
 }
 
+// 1 / sqrt(m2 e1^2): with e1 = 1 + e^-i, m2 times it is m s(i), by one root in place of a root and a reciprocal (16384 steps
+// of 2560 channels: 90 us, 93 with both).  0 where m2 is, and where e1^2 is infinite (a gate below 2^-63).
+__device__ __forceinline__ P inv_root(P m2, P e1) {
+  return each(each(m2, [](float v) { return fmaxf(v, 1e-37f); }) * (e1 * e1), [](float v) { return rsqrt_f(v); });
+}
+
 // y, the final states and the marks (the states that enter the backward's runs).  Grid: (64-channel slabs x a.share,
 // sequences; one for a packed batch).  Tile j share + k of a sequence is block k's of its cluster.  One warp joins the
 // runs' maps of each tile to one that goes to all blocks of the cluster; one barrier of the cluster later each of them has
@@ -83,8 +89,8 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T>())
       for (int s = 0; s < kRun; ++s) {
         const P o = one_minus_exp<decltype(is_far)::value>(rate * sigmoid(Words<T>::open(stage[(L + s) * 32])));
         av[s] = one_less(o);
-        const P m = each(o * one_more(av[s]), [](float v) { return sqrt_f(v); });
-        bv[s] = m * (sigmoid(Words<T>::open(stage[(2 * L + s) * 32])) * Words<T>::open(stage[s * 32]));
+        const P m2 = o * one_more(av[s]), e1 = one_more(exp_neg(Words<T>::open(stage[(2 * L + s) * 32])));
+        bv[s] = m2 * inv_root(m2, e1) * Words<T>::open(stage[s * 32]);
       }
     };
     if (far)
@@ -203,8 +209,8 @@ cudaError_t run(Call& c, cudaStream_t st) {
   auto* kernel = &k_glr_forward<T, kVec, kPacked>;
   constexpr int smem = kStages * Tiles<T, kVec, kWarps, run_of<T>(), 3>::kBytes;
   static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
-  return launch_cluster("k_glr_forward", kernel, fit, c.a, run_of<T>() * kWarps, kThreads, smem, st, (const T*)c.x, (const T*)c.r, (const T*)c.i,
-                        c.lam, c.h0, c.cu, (T*)c.y, c.h_final, c.marks);
+  return launch_cluster("k_glr_forward", kernel, fit, c.a, run_of<T>() * kWarps, kThreads, smem, st, (const T*)c.x,
+                        (const T*)c.r, (const T*)c.i, c.lam, c.h0, c.cu, (T*)c.y, c.h_final, c.marks);
 }
 template <typename T>
 cudaError_t by_type(Call c, cudaStream_t st) {
