@@ -8,8 +8,8 @@
 // the copies, one the products, four turn accumulators into results while the next tile is under way (two accumulators of
 // 256 columns).  In the forward's tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets both.
 // Blocks go in clusters of two, with tiles of the same columns: each copies half of the columns' operand into both, which
-// takes a third off what comes out of L2 (8192 rows of 2560 and 7680, forward and backward: 1375 -> 1340 us; 1501 of 776 and
-// 2056: 75 -> 61 us).  Tiles of 128 x 128 where they end sooner (sooner()).
+// takes a third off what comes out of L2 (8192 rows of 2560 and 7680, forward and backward: 1340 us in place of 1375; 1501 of
+// 776 and 2056: 61 in place of 75).  Tiles of 128 x 128 where they end sooner (sooner()).
 //
 // The training forward keeps G and U for the backward.  dG and dU are rounded to bf16, as operands of the tensor cores have
 // to be: the one rounding of the backward before its results'.
@@ -32,7 +32,6 @@ constexpr int BM = 128, BK = 64;
 constexpr int kThreads = 256, kSMs = 152;  // a warp for copies, one for products, four for results
 constexpr int kBytesA = BM * BK * 2;
 constexpr int kBytesOut = 2 * BM * 64 * 2;  // two tiles of 64 columns on their way out
-constexpr int kGroup = 8;  // pairs of row tiles that are walked over together, so that their operands stay in L2
 constexpr int kMostSmem = 232448;
 
 // Stages of a result's tile of BN columns: as many as shared memory holds.
@@ -45,6 +44,10 @@ struct Stages {
 };
 
 enum Kind { kForward, kGrads };
+// Pairs of row tiles that are walked over together, column by column, so that their operands stay in L2.  8192 rows of 2560
+// and 7680, us: forward 432 with 4, 393 with 8, 384 with 16, 389 with 32; gradients 712 with 2, 719 with 4, 722 with 8, 778
+// with 32.
+constexpr int group_of(Kind kind) { return kind == kForward ? 16 : 2; }
 
 struct Args {
   int M, D, F;
@@ -71,7 +74,7 @@ struct Item {
   int t;
 };
 __host__ __device__ __forceinline__ int pairs_of(int m_tiles, int n_tiles) { return (m_tiles + 1) / 2 * n_tiles; }
-template <int kKind>
+template <Kind kKind>
 __device__ __forceinline__ bool item_of(const Plan& p, int n, Item& it) {
   const int blocks = gridDim.x / 2, i = blockIdx.x / 2, tiles = pairs_of(p.m_tiles, p.n_tiles);
   it.weights = false;
@@ -134,7 +137,9 @@ __device__ __forceinline__ void kept_values(const Kept& k, float (&v)[8]) {
 }
 
 // This block's row tile (m_tiles: there is none) and column tile of an item.
+template <Kind kKind>
 __device__ __forceinline__ void tile_of(const Plan& p, const Item& it, int& m, int& n) {
+  constexpr int kGroup = group_of(kKind);
   const int m_pairs = ((it.weights ? p.w_m_tiles : p.m_tiles) + 1) / 2, n_tiles = it.weights ? p.w_n_tiles : p.n_tiles;
   const int per = kGroup * n_tiles, g = it.t / per, m0 = g * kGroup, gm = min(kGroup, m_pairs - m0), r = it.t - g * per;
   m = 2 * (m0 + r % gm) + (blockIdx.x & 1);
@@ -165,7 +170,7 @@ __device__ __forceinline__ void settled(uint32_t (&r)[32]) {
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-template <int kKind, int BN>
+template <Kind kKind, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_ffn_product(const __grid_constant__ Maps maps, Plan plan, Args args, uint8_t* stash, int* status) {
   constexpr int kStages = Stages<BN>::kN, kBytesStage = Stages<BN>::kBytes, kBytesB = Stages<BN>::kBytesB;
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; ok && item_of<kKind>(plan, i, tile); ++i) {
       const int steps = tile.weights ? plan.w_steps : plan.steps;
       int m, n;
-      tile_of(plan, tile, m, n);
+      tile_of<kKind>(plan, tile, m, n);
       for (int k = 0; k < steps; ++k, ++it) {
         const int s = it % kStages;
         if (it >= kStages && !(ok = mbar_wait(empty + s, (it / kStages - 1) & 1, status, 1))) break;
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item tile;
     for (; item_of<kKind>(plan, done, tile); ++done) {
       int m, n;
-      tile_of(plan, tile, m, n);
+      tile_of<kKind>(plan, tile, m, n);
       const bool there = m < (tile.weights ? plan.w_m_tiles : plan.m_tiles);  // (an odd last row tile has no neighbour)
       const int acc = done & 1;
       const bool ok = mbar_wait(tfull + acc, (done / 2) & 1, status, 6);
@@ -511,7 +516,7 @@ cudaError_t map(CUtensorMap* m, const void* p, int cols, int rows, long long str
   return make_tmap_rows_bf16(m, p, cols, rows, stride, box_cols, box_rows);
 }
 
-template <int kKind, int BN>
+template <Kind kKind, int BN>
 cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const Call& c, cudaStream_t st) {
   const auto kernel = k_ffn_product<kKind, BN>;
   static std::atomic<unsigned long long> allowed{0};
