@@ -5,11 +5,15 @@
 // accumulators in tensor memory.
 //
 // One kernel for all of them, k_ffn_product: output tiles of 128 x 256, one block an SM that walks over tiles; a warp issues
-// the copies, one the products, four turn accumulators into results while the next tile is under way (two accumulators of
-// 256 columns).  In the forward's tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets both.
+// the copies, one the products, four turn an accumulator into results while the next tile is under way (two accumulators of
+// 256 columns, four warps each: with four for both, tiles of four steps waited for them, 256 rows of 2560 and 7680 backward
+// 62 us in place of 58).  In the forward's tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets
+// both.
 // Blocks go in clusters of two, with tiles of the same columns: each copies half of the columns' operand into both, which
 // takes a third off what comes out of L2 (8192 rows of 2560 and 7680, forward and backward: 1340 us in place of 1375; 1501 of
 // 776 and 2056: 61 in place of 75).  Tiles of 128 x 128 where they end sooner (sooner()).
+//
+// dx sums over 2 F numbers; with few rows its sums are taken in pieces, fp32, that another launch joins (grads_plan()).
 //
 // The training forward keeps G and U for the backward.  dG and dU are rounded to bf16, as operands of the tensor cores have
 // to be: the one rounding of the backward before its results'.
@@ -29,9 +33,9 @@ namespace {
 using namespace tc;
 
 constexpr int BM = 128, BK = 64;
-constexpr int kThreads = 256, kSMs = 152;  // a warp for copies, one for products, four for results
+constexpr int kThreads = 384, kSMs = 152;  // a warp for copies, one for products, four for the results of every other tile
 constexpr int kBytesA = BM * BK * 2;
-constexpr int kBytesOut = 2 * BM * 64 * 2;  // two tiles of 64 columns on their way out
+constexpr int kBytesPiece = BM * 64 * 2, kBytesOut = 2 * kBytesPiece;  // 64 columns on their way out, of two tiles
 constexpr int kMostSmem = 232448;
 
 // Stages of a result's tile of BN columns: as many as shared memory holds.
@@ -64,23 +68,32 @@ struct Plan {
   int m_tiles, n_tiles, steps, half;      // tiles and steps of BK; dx: half of the steps are of the first pair of matrices
   int w_m_tiles, w_n_tiles, w_steps, w_half;  // the weights' gradients; half of the row tiles are of the first matrix
   int both;                                   // of those, pairs of tiles that every pair of blocks has
+  int pieces;                                 // of each sum of dx, taken as tiles of their own and joined by k_ffn_join
 };
 // Two blocks, a cluster, work on two row tiles of the same columns side by side.  The n-th of such pairs of tiles of a pair
-// of blocks: the forward's go round.  dx's do too, and the first of them leave some with one more; the weights' gradients'
-// follow, `both` for every pair of blocks and the others for those with fewer of dx's, as many as end the two kinds about
-// together (balance()).
+// of blocks: the forward's go round.  dx's (piece by piece) do too, and the first of them leave some with one more; the
+// weights' gradients' follow, `both` for every pair of blocks and the others for those with fewer of dx's, as many as end the
+// two kinds about together (balance()).
 struct Item {
   bool weights;
-  int t;
+  int t, from, to, piece;  // tile, steps of its sum
 };
 __host__ __device__ __forceinline__ int pairs_of(int m_tiles, int n_tiles) { return (m_tiles + 1) / 2 * n_tiles; }
 template <Kind kKind>
 __device__ __forceinline__ bool item_of(const Plan& p, int n, Item& it) {
-  const int blocks = gridDim.x / 2, i = blockIdx.x / 2, tiles = pairs_of(p.m_tiles, p.n_tiles);
-  it.weights = false;
-  it.t = n * blocks + i;
-  if (it.t < tiles) return true;
+  const int blocks = gridDim.x / 2, i = blockIdx.x / 2, whole = pairs_of(p.m_tiles, p.n_tiles), tiles = whole * p.pieces;
+  it = Item{false, n * blocks + i, 0, p.steps, 0};
+  if (it.t < tiles) {
+    if (kKind == kGrads && p.pieces > 1) {
+      it.piece = it.t / whole;
+      it.t -= it.piece * whole;
+      it.from = (int)((long long)p.steps * it.piece / p.pieces);
+      it.to = (int)((long long)p.steps * (it.piece + 1) / p.pieces);
+    }
+    return true;
+  }
   if (kKind == kForward) return false;
+  it.to = p.w_steps;
   const int more = tiles % blocks, k = n - (tiles / blocks + (i < more));  // those that have one more of dx's: 0 .. more - 1
   it.weights = true;
   it.t = k < p.both ? k * blocks + i : p.both * blocks + (k - p.both) * (blocks - more) + i - more;
@@ -172,7 +185,7 @@ __device__ __forceinline__ void settled(uint32_t (&r)[32]) {
 
 template <Kind kKind, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_ffn_product(const __grid_constant__ Maps maps, Plan plan, Args args, uint8_t* stash, int* status) {
+    k_ffn_product(const __grid_constant__ Maps maps, Plan plan, Args args, uint8_t* stash, float4* part, int* status) {
   constexpr int kStages = Stages<BN>::kN, kBytesStage = Stages<BN>::kBytes, kBytesB = Stages<BN>::kBytesB;
   constexpr int kOwn = BN / 2;  // the forward: columns of G, and of U
   extern __shared__ uint8_t raw_smem[];
@@ -227,10 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Item tile;
     for (int i = 0; ok && item_of<kKind>(plan, i, tile); ++i) {
-      const int steps = tile.weights ? plan.w_steps : plan.steps;
       int m, n;
       tile_of<kKind>(plan, tile, m, n);
-      for (int k = 0; k < steps; ++k, ++it) {
+      for (int k = tile.from; k < tile.to; ++k, ++it) {
         const int s = it % kStages;
         if (it >= kStages && !(ok = mbar_wait(empty + s, (it / kStages - 1) & 1, status, 1))) break;
         if (elect_one()) load(s, tile.weights, m, n, k);
@@ -248,11 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool a_mn = kKind == kGrads && tile.weights;
       constexpr bool kBmn = kKind == kGrads;
       const uint32_t idesc = idesc_bf16(BM, BN, a_mn, kBmn);
-      const int steps = tile.weights ? plan.w_steps : plan.steps, acc = done & 1;
+      const int acc = done & 1;
       const uint64_t step_a = a_mn ? mdesc_step(16) : kdesc_step(BM, 16);
       if (done >= 2 && !(ok = mbar_wait(tempty + acc, (done / 2 - 1) & 1, status, 3))) break;
       tc_fence_after();
-      for (int k = 0; k < steps; ++k, ++it) {
+      for (int k = tile.from; k < tile.to; ++k, ++it) {
         const int s = it % kStages;
         if (!(ok = mbar_wait(full + s, (it / kStages) & 1, status, 4))) break;
         tc_fence_after();
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < BK; kk += 16)
             mma_bf16(tmem + acc * BN, da + (kk / 16) * step_a, db + (kBmn ? mdesc_step(kk) : kdesc_step(BN, kk)), idesc,
-                     k > 0 || kk > 0);
+                     k > tile.from || kk > 0);
           mma_commit_both(empty + s);
         }
         __syncwarp();
@@ -273,21 +285,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the last products have to end before the tensor memory is given back
     for (int d = max(0, done - 2); d < done; ++d) mbar_wait(tfull + (d & 1), (d / 2) & 1, status, 5);
   } else if (warp >= 4) {  // results
-    const int q = warp & 3, row = q * 32 + lane;
-    int done = 0;
+    const int q = warp & 3, row = q * 32 + lane, acc = (warp >> 2) - 1, bar = 1 + acc;
+    const bool leader = q == 0 && lane == 0;
+    out += acc * kBytesPiece;
     Item tile;
-    for (; item_of<kKind>(plan, done, tile); ++done) {
+    for (int done = acc; item_of<kKind>(plan, done, tile); done += 2) {
       int m, n;
       tile_of<kKind>(plan, tile, m, n);
       const bool there = m < (tile.weights ? plan.w_m_tiles : plan.m_tiles);  // (an odd last row tile has no neighbour)
-      const int acc = done & 1;
       const bool ok = mbar_wait(tfull + acc, (done / 2) & 1, status, 6);
-      if (named_bar_or(1, 128, !ok)) break;
+      if (named_bar_or(bar, 128, !ok)) break;
       tc_fence_after();
       const uint32_t base = taddr(tmem, q * 32, acc * BN);
       if (kKind == kForward) {
-        if (q == 0 && lane == 0) tma_store_wait_read0();
-        named_bar(1, 128);
 #pragma unroll
         for (int c = 0; c < kOwn / 32; ++c) {
           uint32_t g[32], u[32];
@@ -308,7 +318,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             products(std::true_type());
           else
             products(std::false_type());
-          store_row_bf16(out + (c >> 1) * (BM * 128), row, (c & 1) * 4, h, 4);
+          if (c % 2 == 0) {
+            if (leader) tma_store_wait_read0();
+            named_bar(bar, 128);
+          }
+          store_row_bf16(out, row, (c & 1) * 4, h, 4);
+          if (c % 2) {
+            fence_proxy_async();
+            named_bar(bar, 128);
+            const int col = n * kOwn + (c - 1) * 32;
+            if (leader && there && col < args.F) {
+              tma_store_2d(&maps.o[0], out, col, m * BM);
+              tma_store_commit();
+            }
+          }
           if (stash && there) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -318,14 +341,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         if (lane == 0) mbar_arrive(tempty + acc);
-        fence_proxy_async();
-        named_bar(1, 128);
-        if (q == 0 && lane == 0 && there) {
+      } else if (!tile.weights && plan.pieces > 1) {
+        if (there) {
+          float4* to = part + (((size_t)tile.piece * plan.m_tiles + m) * (args.D / 4) + n * (BN / 4)) * BM + row;
+#pragma unroll 1
+          for (int c = 0; c < BN / 32 && n * BN + c * 32 < args.D; ++c, to += 8 * BM) {
+            uint32_t v[32];
+            tmem_ld32_nowait(base + c * 32, v);
+            tmem_wait_ld();
+            settled(v);
 #pragma unroll
-          for (int c = 0; c < kOwn; c += 64)
-            if (n * kOwn + c < args.F) tma_store_2d(&maps.o[0], out + c * BM * 2, n * kOwn + c, m * BM);
-          tma_store_commit();
+            for (int e = 0; e < 8; ++e)
+              if (n * BN + c * 32 + e * 4 < args.D)
+                to[e * BM] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                         __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
+          }
         }
+        tc_fence_before();
+        if (lane == 0) mbar_arrive(tempty + acc);
       } else {
         const int which = tile.weights && m >= plan.w_half, row0 = (m - (which ? plan.w_half : 0)) * BM;
         const CUtensorMap* to_map = tile.weights ? &maps.wo[which] : &maps.o[0];
@@ -334,22 +367,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[2][32];
           tmem_ld32_nowait(base + p * 64, v[0]);
           tmem_ld32_nowait(base + p * 64 + 32, v[1]);
-          if (q == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          if (leader) tma_store_wait_read0();
           tmem_wait_ld();
           settled(v[0]), settled(v[1]);
-          named_bar(1, 128);
-          uint8_t* to = out + (p & 1) * (BM * 128);
+          named_bar(bar, 128);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float f[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(v[c][e]);
-            store_row_bf16(to, row, c * 4, f, 4);
+            store_row_bf16(out, row, c * 4, f, 4);
           }
           fence_proxy_async();
-          named_bar(1, 128);
-          if (q == 0 && lane == 0) {
-            if (there && n * BN + p * 64 < args.D) tma_store_2d(to_map, to, n * BN + p * 64, row0);
+          named_bar(bar, 128);
+          if (leader && there && n * BN + p * 64 < args.D) {
+            tma_store_2d(to_map, out, n * BN + p * 64, row0);
             tma_store_commit();
           }
         }
@@ -357,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(tempty + acc);
       }
     }
-    if (q == 0 && lane == 0) tma_store_wait0();
+    if (leader) tma_store_wait0();
   }
   __syncwarp();
   tc_fence_before();
@@ -399,6 +431,24 @@ __global__ void __launch_bounds__(256)
   }
   *reinterpret_cast<uint4*>(dg + (size_t)row * a.F + f) = make_uint4(og[0], og[1], og[2], og[3]);
   *reinterpret_cast<uint4*>(du + (size_t)row * a.F + f) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+}
+
+// dx of its sums' pieces [pieces, row tiles, D / 4, 128] of four columns, in order: a warp has eight rows of four pieces of
+// eight columns.
+__global__ void __launch_bounds__(256)
+    k_ffn_join(Args a, const float4* __restrict__ part, int m_tiles, int pieces, bf16* dx) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = (blockIdx.y * 32 + warp * 4 + (lane & 3)) * 8, row = blockIdx.x * 8 + (lane >> 2);
+  if (row >= a.M || c >= a.D) return;
+  const float4* from = part + ((size_t)(row / BM) * (a.D / 4) + c / 4) * BM + row % BM;
+  float s[8] = {};
+#pragma unroll 4
+  for (int p = 0; p < pieces; ++p, from += (size_t)m_tiles * (a.D / 4) * BM) {
+    const float4 x = from[0], y = from[BM];
+    s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w, s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
+  }
+  *reinterpret_cast<uint4*>(dx + (size_t)row * a.D + c) = make_uint4(pack2(s[0], s[1]), pack2(s[2], s[3]), pack2(s[4], s[5]),
+                                                                     pack2(s[6], s[7]));
 }
 
 // The forward with few rows, where all that counts is how fast the weights come in: one tile a block, of up to 128 rows and
@@ -509,6 +559,7 @@ struct Call {
   void *h, *dx, *dwg, *dwu;
   uint8_t* stash;
   bf16 *dg, *du;
+  float4* part;  // room for dx's sums' pieces
   int* status;
 };
 
@@ -522,7 +573,8 @@ cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const C
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Stages<BN>::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  const int pairs = pairs_of(plan.m_tiles, plan.n_tiles) + (kKind == kGrads ? pairs_of(plan.w_m_tiles, plan.w_n_tiles) : 0);
+  const int pairs = pairs_of(plan.m_tiles, plan.n_tiles) * plan.pieces +
+                    (kKind == kGrads ? pairs_of(plan.w_m_tiles, plan.w_n_tiles) : 0);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pairs < kSMs / 2 ? 2 * pairs : kSMs);
   cfg.blockDim = dim3(kThreads);
@@ -537,23 +589,27 @@ cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const C
   cudaError_t launched = cudaSuccess;
   SSD_LAUNCH(name, st,
              launched = cudaLaunchKernelEx(&cfg, kernel, maps, plan, c.a, kKind == kForward ? c.stash : (uint8_t*)nullptr,
-                                           c.status));
+                                           c.part, c.status));
   return launched;
 }
+int up(long long a, int b) { return (int)((a + b - 1) / b); }
+
+constexpr int kLeast = 4;  // steps that a tile's results take: a tile of fewer ends no sooner
 // dx and the weights' gradients in one launch: how many of the latter's pairs of tiles every pair of blocks takes, so
 // that the last ends soonest (steps of those with one more of dx's, and of the others).  Returns the steps until then.  8192
 // rows of 2560 and 7680: 320 pairs of tiles of 240 steps and 600 of 128 on 76 pairs of blocks end after 2112 steps, one kind
 // after the other they would after 2224.
 long long balance(Plan* p) {
-  const int tiles = pairs_of(p->m_tiles, p->n_tiles), w_tiles = pairs_of(p->w_m_tiles, p->w_n_tiles);
+  const int tiles = pairs_of(p->m_tiles, p->n_tiles) * p->pieces, w_tiles = pairs_of(p->w_m_tiles, p->w_n_tiles);
+  const int steps = up(p->steps, p->pieces), w_steps = p->w_steps > kLeast ? p->w_steps : kLeast;
   const int blocks = tiles + w_tiles < kSMs / 2 ? tiles + w_tiles : kSMs / 2;
   const int more = tiles % blocks, each = tiles / blocks, others = blocks - more;
   long long best = -1;
-  const int least = w_tiles / blocks - p->steps / p->w_steps - 2;  // (with fewer, the others would end later than the first)
+  const int least = w_tiles / blocks - steps / w_steps - 2;  // (with fewer, the others would end later than the first)
   for (int both = least > 0 ? least : 0; both <= (w_tiles + blocks - 1) / blocks; ++both) {
     const int left = w_tiles - both * blocks > 0 ? w_tiles - both * blocks : 0;
-    const long long first = more ? (each + 1ll) * p->steps + (long long)both * p->w_steps : 0;
-    const long long second = (long long)each * p->steps + (both + (left + others - 1) / others) * (long long)p->w_steps;
+    const long long first = more ? (each + 1ll) * steps + (long long)both * w_steps : 0;
+    const long long second = (long long)each * steps + (both + (left + others - 1) / others) * (long long)w_steps;
     const long long end = first > second ? first : second;
     if (best < 0 || end < best) best = end, p->both = both;
   }
@@ -564,9 +620,32 @@ long long balance(Plan* p) {
 // evenly.  Forward, us: 1501 rows of 776 and 2056 in narrow ones 22.6, in wide ones 25.2; 2048 of 1024 and 4096 42.0 and
 // 39.2; 8192 of 2560 and 7680 490 and 392.  Gradients, the same sizes: 32.2 and 32.7, 59 and 52, 916 and 725; 256 rows of
 // 2560 and 7680, whose few long sums of dx are what it waits for, 64 and 97.
-bool sooner(long long narrow_steps, long long wide_steps) { return narrow_steps * 5 < wide_steps * 8; }
+constexpr int kWideStep = 8, kNarrowStep = 5;
+bool sooner(long long narrow_steps, long long wide_steps) { return narrow_steps * kNarrowStep < wide_steps * kWideStep; }
 
-int up(long long a, int b) { return (int)((a + b - 1) / b); }
+// The gradients' tiles: wide or narrow, and dx's sums in as many pieces as end soonest, the launch that joins them (12 steps)
+// and the bytes it reads counted in.  With few rows dx is a few tiles of long sums (backward, us, in pieces and in one: 125
+// rows of 288 and 8816 30 and 74; 256 of 2560 and 7680 58 and 76; 453 of 712 and 11912 64 and 115; 1501 of 776 and 2056 stay
+// in one, 44 and 48 in two).
+constexpr int kMostPieces = 16, kLeastSteps = 8, kJoinSteps = 12;  // pieces, steps of one
+Plan grads_plan(const Args& a, bool* narrow) {
+  Plan best = {};
+  long long least = -1;
+  for (const int cols : {256, 128}) {
+    Plan p = {up(a.M, BM),     up(a.D, cols), 2 * up(a.F, BK), up(a.F, BK),
+              2 * up(a.F, BM), up(a.D, cols), up(a.M, BK),     up(a.F, BM)};
+    const auto fits = [&](int pieces) {
+      return pieces <= kMostPieces && p.steps >= kLeastSteps * pieces &&
+             (long long)pairs_of(p.m_tiles, p.n_tiles) * pieces <= 4 * kSMs;
+    };
+    for (p.pieces = 1; p.pieces == 1 || fits(p.pieces); ++p.pieces) {
+      long long end = balance(&p) * (cols == 256 ? kWideStep : kNarrowStep);
+      if (p.pieces > 1) end += kWideStep * (kJoinSteps + (long long)p.pieces * a.M * a.D / (1 << 18));  // (2 MB a step)
+      if (least < 0 || end < least) least = end, best = p, *narrow = cols == 128;
+    }
+  }
+  return best;
+}
 
 // Few rows: where tiles of 128 rows and 128 features leave SMs without one.
 bool few_rows(const Args& a, Few* few) {
@@ -595,7 +674,7 @@ cudaError_t forward(const Call& c, cudaStream_t st) {
   maps.a[1] = maps.a[0];
   if (!is_few) {
     maps.o[1] = maps.o[0], maps.wa[0] = maps.wa[1] = maps.wb = maps.wo[0] = maps.wo[1] = maps.a[0];
-    const Plan p = {up(c.a.M, BM), up(c.a.F, wide), up(c.a.D, BK)};
+    const Plan p = {up(c.a.M, BM), up(c.a.F, wide), up(c.a.D, BK), 0, 0, 0, 0, 0, 0, 1};
     return narrow ? launch<kForward, 128>("k_ffn_forward", maps, p, c, st)
                   : launch<kForward, 256>("k_ffn_forward", maps, p, c, st);
   }
@@ -629,13 +708,13 @@ cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
   if (e == cudaSuccess) e = map(&maps.wo[1], c.dwu, a.D, a.F, a.D, 64, BM);
   if (e != cudaSuccess) return e;
   maps.o[1] = maps.o[0];
-  Plan wide = {up(a.M, BM),     up(a.D, 256), 2 * up(a.F, BK), up(a.F, BK),
-               2 * up(a.F, BM), up(a.D, 256), up(a.M, BK),     up(a.F, BM), 0};
-  Plan p = wide;
-  p.n_tiles = p.w_n_tiles = up(a.D, 128);
-  const bool narrow = sooner(balance(&p), balance(&wide));
-  if (!narrow) p = wide;
-  return narrow ? launch<kGrads, 128>("k_ffn_grads", maps, p, c, st) : launch<kGrads, 256>("k_ffn_grads", maps, p, c, st);
+  bool narrow = false;
+  const Plan p = grads_plan(a, &narrow);
+  e = narrow ? launch<kGrads, 128>("k_ffn_grads", maps, p, c, st) : launch<kGrads, 256>("k_ffn_grads", maps, p, c, st);
+  if (e != cudaSuccess || p.pieces == 1) return e;
+  SSD_LAUNCH("k_ffn_join", st,
+             k_ffn_join<<<dim3(up(a.M, 8), up(a.D, 256)), 256, 0, st>>>(a, c.part, p.m_tiles, p.pieces, (bf16*)c.dx));
+  return cudaGetLastError();
 }
 
 ssd_status make_args(const ssd_ffn_problem* p, Args* a) {
@@ -660,6 +739,9 @@ size_t workspace(Call* c, bool back, bool stashed, void* ws) {
   if (back) {
     c->dg = cv.take<bf16>((size_t)c->a.M * c->a.F);
     c->du = cv.take<bf16>((size_t)c->a.M * c->a.F);
+    bool narrow;
+    const Plan p = grads_plan(c->a, &narrow);
+    if (p.pieces > 1) c->part = cv.take<float4>((size_t)p.pieces * p.m_tiles * BM * (c->a.D / 4));
     if (!stashed) {
       c->stash = cv.take<uint8_t>(stash_bytes_of(c->a));
       c->h = cv.take<bf16>((size_t)c->a.M * c->a.F);  // of the forward that is made again

@@ -73,8 +73,15 @@ def test_more_tiles_than_blocks(m, d, f):
     compare(make(m, d, f, 2), "silu")
 
 
-def test_stash_changes_no_bit():
-    c = make(150, 264, 392, 3)
+@pytest.mark.parametrize("m,d,f", [(1, 8, 1024), (65, 264, 2056), (130, 40, 5000), (300, 72, 4104), (257, 520, 1032)])
+def test_long_sums_of_few_rows(m, d, f):
+    """dx of sums that are taken in pieces."""
+    compare(make(m, d, f, 9), "gelu")
+
+
+@pytest.mark.parametrize("m,d,f", [(150, 264, 392), (70, 136, 2568)])
+def test_stash_changes_no_bit(m, d, f):
+    c = make(m, d, f, 3)
     a, b = compare(c, "silu"), compare(c, "silu", stash=False)
     assert all(torch.equal(p, q) for p, q in zip(a, b))
 
