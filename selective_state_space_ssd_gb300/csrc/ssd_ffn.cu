@@ -561,6 +561,8 @@ struct Call {
   bf16 *dg, *du;
   float4* part;  // room for dx's sums' pieces
   int* status;
+  Plan plan;     // the gradients'
+  bool narrow;
 };
 
 cudaError_t map(CUtensorMap* m, const void* p, int cols, int rows, long long stride, int box_cols, int box_rows) {
@@ -708,9 +710,8 @@ cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
   if (e == cudaSuccess) e = map(&maps.wo[1], c.dwu, a.D, a.F, a.D, 64, BM);
   if (e != cudaSuccess) return e;
   maps.o[1] = maps.o[0];
-  bool narrow = false;
-  const Plan p = grads_plan(a, &narrow);
-  e = narrow ? launch<kGrads, 128>("k_ffn_grads", maps, p, c, st) : launch<kGrads, 256>("k_ffn_grads", maps, p, c, st);
+  const Plan& p = c.plan;
+  e = c.narrow ? launch<kGrads, 128>("k_ffn_grads", maps, p, c, st) : launch<kGrads, 256>("k_ffn_grads", maps, p, c, st);
   if (e != cudaSuccess || p.pieces == 1) return e;
   SSD_LAUNCH("k_ffn_join", st,
              k_ffn_join<<<dim3(up(a.M, 8), up(a.D, 256)), 256, 0, st>>>(a, c.part, p.m_tiles, p.pieces, (bf16*)c.dx));
@@ -739,9 +740,8 @@ size_t workspace(Call* c, bool back, bool stashed, void* ws) {
   if (back) {
     c->dg = cv.take<bf16>((size_t)c->a.M * c->a.F);
     c->du = cv.take<bf16>((size_t)c->a.M * c->a.F);
-    bool narrow;
-    const Plan p = grads_plan(c->a, &narrow);
-    if (p.pieces > 1) c->part = cv.take<float4>((size_t)p.pieces * p.m_tiles * BM * (c->a.D / 4));
+    c->plan = grads_plan(c->a, &c->narrow);
+    if (c->plan.pieces > 1) c->part = cv.take<float4>((size_t)c->plan.pieces * c->plan.m_tiles * BM * (c->a.D / 4));
     if (!stashed) {
       c->stash = cv.take<uint8_t>(stash_bytes_of(c->a));
       c->h = cv.take<bf16>((size_t)c->a.M * c->a.F);  // of the forward that is made again
@@ -805,8 +805,7 @@ ssd_status ssd_ffn_backward(const ssd_ffn_problem* prob, const void* dh, const v
   if (s != SSD_OK) return s;
   if ((s = ffn::check({dh, x, w_gate, w_up, dx, dw_gate, dw_up, ws}, stash)) != SSD_OK) return s;
   if (stash && stash_bytes < ffn::stash_bytes_of(c.a)) return SSD_ERR_WORKSPACE;
-  if (ws_bytes < ffn::workspace(&c, true, stash != nullptr, nullptr)) return SSD_ERR_WORKSPACE;
-  ffn::workspace(&c, true, stash != nullptr, ws);
+  if (ws_bytes < ffn::workspace(&c, true, stash != nullptr, ws)) return SSD_ERR_WORKSPACE;
   c.x = x, c.wg = w_gate, c.wu = w_up, c.dh = dh, c.dx = dx, c.dwg = dw_gate, c.dwu = dw_up;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   cudaError_t e = cudaSuccess;
