@@ -229,7 +229,8 @@ __device__ __forceinline__ Bits bits_of(const int* code, int t0, int T, int lane
 
 // ------------------------------------------------------------ tiles on their way to shared memory
 // A stage holds a tile of each of kArrays arrays: [array][step][32 words].  kVec: 16-byte pieces; otherwise each thread
-// copies the words that it reads itself, element by element.  Steps outside 0 .. T - 1 are left as they are (whatever they
+// copies the words that it reads itself, four bytes at a time or, where rows of bf16 begin inside such, element by element
+// (11811 packed steps forward: 157 us with 1582 channels, 345 with 1583).  Steps outside 0 .. T - 1 are left as they are (whatever they
 // hold is masked), channels from D on are zeros.
 template <typename T, bool kVec, int kWarps, int kRun, int kArrays>
 struct Tiles {
@@ -242,6 +243,7 @@ struct Tiles {
   uint32_t from[kArrays];     // elements from src to what this thread copies first
   int t, hop, steps, left;    // the step of that; steps from a tile to the block's next; T; channels from this thread's on
   uint32_t at;                // this thread's place in a stage
+  bool inside;                // rows of bf16 begin inside four bytes
 
   // first: the first tile's first step; hop_tiles: tiles from one to the next (below 0: towards the beginning).
   __device__ __forceinline__ Tiles(const T* const (&rows)[kArrays], const uint32_t (&step)[kArrays], int c0, int D, int T_,
@@ -253,11 +255,13 @@ struct Tiles {
     hop = hop_tiles * L;
     steps = T_;
     at = kVec ? row * 32 * sizeof(Word) + (threadIdx.x % PP) * 16 : (row * 32 + lane) * sizeof(Word);
+    inside = false;
 #pragma unroll
     for (int a = 0; a < kArrays; ++a) {
       stride[a] = step[a];
       src[a] = rows[a] + c0 + (long long)first * step[a];
       from[a] = row * step[a] + (left > 0 ? c : 0);
+      if (!kVec && sizeof(T) == 2 && ((reinterpret_cast<uintptr_t>(rows[a]) & 3) || step[a] % 2)) inside = true;
     }
   }
   // The next tile, to a stage.
@@ -275,6 +279,8 @@ struct Tiles {
           } else if constexpr (sizeof(T) == 4) {
             copy4(to, p, left > 0);
             copy4(to + 4, left > 1 ? p + 1 : p, left > 1);
+          } else if (!inside) {
+            copy4_of(to, p, left > 1 ? 4 : left > 0 ? 2 : 0);
           } else {
             uint32_t v = 0;
             if (left > 0) v = *reinterpret_cast<const uint16_t*>(p);

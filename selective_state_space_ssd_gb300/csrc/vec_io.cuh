@@ -25,11 +25,12 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
                "r"(ok ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copy4(void* dst, const void* src, bool ok) {
+__device__ __forceinline__ void copy4_of(void* dst, const void* src, int bytes) {  // the first bytes, the others are zeros
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-               "r"(ok ? 4 : 0)
+               "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool ok) { copy4_of(dst, src, ok ? 4 : 0); }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kN>
 __device__ __forceinline__ void copies_wait() {  // all but the last kN groups have arrived
