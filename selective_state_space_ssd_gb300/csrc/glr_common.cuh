@@ -230,8 +230,8 @@ __device__ __forceinline__ Bits bits_of(const int* code, int t0, int T, int lane
 // ------------------------------------------------------------ tiles on their way to shared memory
 // A stage holds a tile of each of kArrays arrays: [array][step][32 words].  kVec: 16-byte pieces; otherwise each thread
 // copies the words that it reads itself, four bytes at a time or, where rows of bf16 begin inside such, element by element
-// (11811 packed steps forward: 157 us with 1582 channels, 345 with 1583).  Steps outside 0 .. T - 1 are left as they are (whatever they
-// hold is masked), channels from D on are zeros.
+// (11811 packed steps forward: 157 us with 1582 channels, 345 with 1583).  Steps outside 0 .. T - 1 are left as they are
+// (whatever they hold is masked), channels from D on are zeros.
 template <typename T, bool kVec, int kWarps, int kRun, int kArrays>
 struct Tiles {
   static constexpr int kThreads = 32 * kWarps, L = kRun * kWarps;
@@ -362,7 +362,8 @@ inline Args flattened(const Args& a) {
   const int L = 8 * mark_of(a.f32);
   Args f = a;
   if (a.packed || a.N < 2 || a.T >= L || (long long)a.N * a.T > kMostSteps) return f;
-  const long long room = 2 * 152, wide = slabs(a), share = room / wide < 1 ? 1 : room / wide < kMostShare ? room / wide : kMostShare;
+  const long long room = 2 * 152, wide = slabs(a);
+  const long long share = room / wide < 1 ? 1 : room / wide < kMostShare ? room / wide : kMostShare;
   const long long apart = (wide * a.N + room - 1) / room;
   const long long joined = ((long long)a.N * a.T + L * share - 1) / (L * share) * ((wide + room - 1) / room);
   if (joined > apart) return f;

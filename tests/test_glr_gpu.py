@@ -208,7 +208,7 @@ def test_gates_far_from_zero_are_finite():
     check("dr", torch.where(torch.from_numpy(ok), g["dr"].cpu(), 0.0), np.where(ok, ref["dr"], 0))
 
 
-@pytest.mark.parametrize("io,dim,wide", [("bf16", 64, 192), ("bf16", 40, 83), ("f32", 33, 70), ("f32", 64, 128)])
+@pytest.mark.parametrize("io,dim,wide", [("bf16", 64, 192), ("bf16", 40, 83), ("bf16", 33, 70), ("f32", 33, 70), ("f32", 64, 128)])
 def test_strided_inputs(io, dim, wide):
     c = make((3, 70), dim, io, 9, 3)
     d = {k: t.cuda() for k, t in c.items()}
