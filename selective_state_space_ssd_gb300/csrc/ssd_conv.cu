@@ -22,8 +22,8 @@ namespace {
 constexpr int kThreads = 256, kWarps = 8;
 // Steps loaded ahead, channels a thread has (where rows are whole pieces of them) and blocks an SM.  Measured at 4 x 4096
 // steps of 5120 channels: forward 61 us with eight steps, 3 blocks (four steps 65, 2 blocks 71; two channels a thread 69),
-// backward 128 us with four channels, four steps and 2 blocks (two channels 157 to 163; without the next steps on their way
-// 140).
+// backward, in runs of 64 steps, 125 us with four channels, four steps and 2 blocks (two channels 157 to 163; without the next
+// steps on their way 140).
 constexpr int kAhead = 8, kFwdBlocks = 3, kWide = 4;
 constexpr int kBack = 4, kBackBlocks = 2;
 
@@ -584,18 +584,29 @@ ssd_status make_args(const ssd_conv_problem* p, Args* a) {
   a->wbf16 = p->weight_dtype == SSD_BF16;
   a->silu = p->activation == SSD_ACT_SILU;
   a->xs = p->x_stride ? p->x_stride : p->dim;
-  // Long runs read little twice, short ones give work to the whole GPU: the longest of 64, 32, 16 and 8 steps that leaves
-  // about 24 warps an SM.  Longer ones where the grid would pass 2^31 blocks.
-  long long run = 64;
-  const long long steps = (long long)axes(*a) * a->T, warps = 152 * 24;
-  while (run > 8 && steps / run * ((a->D + 127) / 128) < warps) run /= 2;
-  a->run = (int)run;
-  while (chunks(*a) * slabs(*a, 1) > 0x7fffffffll) a->run *= 2;
   return SSD_OK;
+}
+// Steps of a run (a multiple of kAhead): those with which the blocks that fit the GPU at once end soonest, turn after turn; a
+// run starts with loads that take about as long as 16 steps.  Forward and backward, us: 20011 steps of 2560 channels 45 and
+// 68, in runs of 64 46 and 85; 16384 of 2560 38 and 59, 46 and 74; 4 x 4096 of 5120 66 and 112, 65 and 125.  Longer ones
+// where the grid would pass 2^31 blocks.
+constexpr int kStart = 16, kMostRun = 256;
+void set_run(Args* a, int blocks_of_an_sm) {
+  const long long slots = 152 * blocks_of_an_sm;
+  long long least = -1;
+  int run = kAhead;
+  for (a->run = kAhead; a->run <= kMostRun; a->run += kAhead) {
+    const long long turns = (chunks(*a) * slabs(*a, kWide) + slots - 1) / slots, end = turns * (a->run + kStart);
+    if (least < 0 || end < least) least = end, run = a->run;
+    if (turns == 1) break;
+  }
+  a->run = run;
+  while (chunks(*a) * slabs(*a, 1) > 0x7fffffffll) a->run *= 2;
 }
 
 size_t workspace(Call* c, void* ws) {
   Carver cv(ws);
+  set_run(&c->a, kBackBlocks);
   c->part = cv.take<float>((size_t)chunks(c->a) * (c->a.K + 1) * c->a.D);
   return cv.off;
 }
@@ -641,6 +652,7 @@ ssd_status ssd_conv_forward(const ssd_conv_problem* prob, const void* x, const v
   if (!y || c.a.packed != (cu_seqlens != nullptr)) return SSD_ERR_INVALID_ARG;
   if ((s = conv::check_inputs(c)) != SSD_OK) return s;
   if (off(y, c.a.f32 ? 4 : 2) || off(taps_final, c.a.f32 ? 4 : 2)) return SSD_ERR_ALIGNMENT;
+  conv::set_run(&c.a, conv::kFwdBlocks);
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   conv::by_shape(c, conv::whole(c, {x, taps, y, taps_final}), [&](auto t, auto k, auto w) {
     conv::forward_of<decltype(t), decltype(k)::value, decltype(w)::value>(c, st);
@@ -660,8 +672,7 @@ ssd_status ssd_conv_backward(const ssd_conv_problem* prob, const void* dy, const
   if ((s = conv::check_inputs(c)) != SSD_OK) return s;
   const uintptr_t elem = c.a.f32 ? 4 : 2, we = c.a.wbf16 ? 2 : 4;
   if (off(dy, elem) || off(dx, elem) || off(dw, we) || off(db, we) || off(dtaps, elem) || off(ws, 16)) return SSD_ERR_ALIGNMENT;
-  if (ws_bytes < conv::workspace(&c, nullptr)) return SSD_ERR_WORKSPACE;
-  conv::workspace(&c, ws);
+  if (ws_bytes < conv::workspace(&c, ws)) return SSD_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   conv::by_shape(c, conv::whole(c, {x, taps, dy, dx}), [&](auto t, auto k, auto w) {
     conv::backward_of<decltype(t), decltype(k)::value, decltype(w)::value>(c, st);
