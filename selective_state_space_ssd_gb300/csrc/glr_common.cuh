@@ -6,7 +6,7 @@
 // a slow decay (a near 1) is about.
 //
 // A step is an affine map h -> a h + b of each channel, and maps compose: (A, B) after (A', B') is (A A', A B' + B).  A
-// block takes 64 channels, two a lane, and walks a sequence in tiles; each of its warps has a run of a tile's steps.
+// block takes 64 channels, two a lane, and walks a sequence in tiles; each of its 8 or 16 warps has a run of a tile's steps.
 // The runs' maps are joined in order through shared memory, and the tiles' maps, where several blocks of a cluster share the
 // sequence, through their shared memories.
 // In packed batches the first step of a sequence starts anew (b + a h0, and steps of no sequence with zero); the map of a
@@ -28,7 +28,8 @@ namespace glr {
 constexpr int mark_of(bool f32) { return f32 ? 4 : 8; }
 constexpr int kWidth = 64;     // channels of a block
 constexpr int kMostShare = 8;  // blocks that share a sequence, at most
-constexpr long long kMostStride = 1 << 24;  // elements from a step to the next: those of a tile's 128 steps fit 32 bits
+constexpr int kFewWarps = 8, kManyWarps = 16;  // of a block
+constexpr long long kMostStride = 1 << 24;  // elements from a step to the next: those of a tile's 256 steps fit 32 bits
 constexpr long long kMostSteps = 0x7fff0000;  // of an axis: a few tiles more than it has are counted in 32 bits
 
 struct Args {
@@ -316,11 +317,11 @@ cudaLaunchConfig_t config_of(void (*kernel)(KArgs...), int threads, int smem, cu
   cfg.numAttrs = share > 1 ? 1 : 0;
   return cfg;
 }
-template <typename Kernel>
 struct Fit {  // of one kernel: clusters of 1 .. kMostShare blocks that fit at once
   int clusters[kMostShare + 1] = {};
   cudaError_t error = cudaSuccess;
   mutable std::atomic<unsigned long long> allowed{0};
+  template <typename Kernel>
   Fit(Kernel kernel, int threads, int smem) {
     error = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     for (int s = 1; s <= kMostShare && error == cudaSuccess; ++s) {
@@ -335,24 +336,38 @@ struct Fit {  // of one kernel: clusters of 1 .. kMostShare blocks that fit at o
     while (s > 1 && (clusters[s] < groups || s > (a.T + L - 1) / L)) --s;
     return s;
   }
+  bool room(const Args& a, int L) const { return clusters[sharers(a, L)] >= (long long)slabs(a) * axes(a); }
+  int rounds(const Args& a, int L) const {  // tiles that a block takes one after another
+    const int s = sharers(a, L);
+    return ((a.T + L - 1) / L + s - 1) / s;
+  }
 };
-// Launches a kernel in clusters of a.share blocks (1: none), which it sets: as many as leave every block a tile of L steps
-// and all clusters room on the GPU at once, by the runtime's count.  A cluster that has to wait for its turn costs more than
-// it brings: 40 slabs of one sequence of 16384 steps take 90 us forward and 166 backward in clusters of six, 110 and 246 in
-// clusters of eight, of which only 36 fit.
-template <typename Kernel, typename... Args_>
-cudaError_t launch_cluster(const char* name, Kernel kernel, const Fit<Kernel>& fit, Args& a, int L, int threads, int smem,
-                           cudaStream_t st, Args_... args) {
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, fit.allowed);
+template <typename Shape, typename... Args_>
+cudaError_t launch_shape(const char* name, const Fit& fit, Args& a, cudaStream_t st, Args_... args) {
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(Shape::kernel), Shape::smem, fit.allowed);
   if (e == cudaSuccess) e = fit.error;
   if (e != cudaSuccess) return e;
-  a.share = fit.sharers(a, L);
+  a.share = fit.sharers(a, Shape::run * Shape::warps);
   cudaLaunchAttribute attr;
-  cudaLaunchConfig_t cfg = config_of(kernel, threads, smem, &attr, a.share);
+  cudaLaunchConfig_t cfg = config_of(Shape::kernel, 32 * Shape::warps, Shape::smem, &attr, a.share);
   cfg.gridDim = dim3(slabs(a) * a.share, axes(a));
   cfg.stream = st;
-  SSD_LAUNCH(name, st, e = cudaLaunchKernelEx(&cfg, kernel, a, args...));
+  SSD_LAUNCH(name, st, e = cudaLaunchKernelEx(&cfg, Shape::kernel, a, args...));
   return e;
+}
+// Launches a kernel in clusters of a.share blocks (1: none), which it sets: as many as leave every block a tile and all
+// clusters room on the GPU at once, by the runtime's count.  A cluster that has to wait for its turn costs more than it
+// brings: 40 slabs of one sequence of 16384 steps take 90 us forward and 166 backward in clusters of six, 110 and 246 in
+// clusters of eight, of which only 36 fit.  Blocks of twice the warps, one an SM, where all have room and take fewer tiles
+// one after another: 16384 steps of 1024 channels take 62 and 100 us, 66 and 128 in blocks of eight warps; 24318 packed ones
+// of 320 79 and 125, 93 and 170.  (16 sequences of 512 steps of 1024 channels, which have no room, would take 33 and 41
+// in place of 23 and 33.)
+template <typename Few, typename Many, typename... Args_>
+cudaError_t launch_cluster(const char* name, Args& a, cudaStream_t st, Args_... args) {
+  static const Fit few(Few::kernel, 32 * Few::warps, Few::smem), many(Many::kernel, 32 * Many::warps, Many::smem);
+  if (many.room(a, Many::run * Many::warps) && many.rounds(a, Many::run * Many::warps) < few.rounds(a, Few::run * Few::warps))
+    return launch_shape<Many>(name, many, a, st, args...);
+  return launch_shape<Few>(name, few, a, st, args...);
 }
 // Many short sequences are taken as one packed axis, as which they lie in memory: in tiles of their own most of a block would
 // have no step.  By the tiles that one SM's blocks take one after another, either way (two blocks an SM, and as many sharers

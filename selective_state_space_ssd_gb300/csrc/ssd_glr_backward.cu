@@ -10,7 +10,6 @@ namespace ssd {
 namespace glr {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStages = 2;  // tiles in shared memory or on their way there
 
 // Tile by tile from the end.  The stash holds the state that enters each thread's run, so a run's states and all factors of
@@ -18,13 +17,13 @@ constexpr int kStages = 2;  // tiles in shared memory or on their way there
 // states are forward, in the other direction.  The factors of a run's first steps wait for that in shared memory (eight
 // numbers a step and lane, written and read by the same thread), those of its last four in registers: runs of eight steps
 // halve the barriers that runs of four would take.  part [axes share, D]: the sums of q.
-template <typename T, bool kVec, bool kPacked>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, bool kVec, bool kPacked, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? 2 : 1)
     k_glr_backward(Args a, const T* __restrict__ dy, const float* __restrict__ dh_final, const T* __restrict__ x,
                    const T* __restrict__ r, const T* __restrict__ i, const float* __restrict__ lam,
                    const float* __restrict__ h0, const int* __restrict__ cu, const float* __restrict__ marks, T* dx, T* dr,
                    T* di, float* dh0, float* part) {
-  constexpr int kRun = mark_of(sizeof(T) == 4), L = kRun * kWarps, kAside = kRun - 4;
+  constexpr int kThreads = 32 * kWarps, kRun = mark_of(sizeof(T) == 4), L = kRun * kWarps, kAside = kRun - 4;
   using Tile = Tiles<T, kVec, kWarps, kRun, 4>;
   using Word = typename Words<T>::Word;
   extern __shared__ __align__(16) uint8_t ring[];
@@ -224,15 +223,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
+template <typename T, bool kVec, bool kPacked, int kWarps>
+struct Shape {
+  static constexpr auto kernel = &k_glr_backward<T, kVec, kPacked, kWarps>;
+  static constexpr int warps = kWarps, run = mark_of(sizeof(T) == 4);
+  static constexpr int aside = (run - 4) * 2 * 32 * kWarps * (int)sizeof(Map);
+  static constexpr int smem = kStages * Tiles<T, kVec, kWarps, run, 4>::kBytes + aside;
+};
 template <typename T, bool kVec, bool kPacked>
 cudaError_t run(Call& c, cudaStream_t st) {
-  auto* kernel = &k_glr_backward<T, kVec, kPacked>;
-  constexpr int kRun = mark_of(sizeof(T) == 4);
-  constexpr int smem = kStages * Tiles<T, kVec, kWarps, kRun, 4>::kBytes + (kRun - 4) * 2 * kThreads * (int)sizeof(Map);
-  static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
-  return launch_cluster("k_glr_backward", kernel, fit, c.a, kRun * kWarps, kThreads, smem, st, (const T*)c.dy, c.dh_final,
-                        (const T*)c.x, (const T*)c.r, (const T*)c.i, c.lam, c.h0, c.cu, (const float*)c.marks, (T*)c.dx,
-                        (T*)c.dr, (T*)c.di, c.dh0, c.part);
+  return launch_cluster<Shape<T, kVec, kPacked, kFewWarps>, Shape<T, kVec, kPacked, kManyWarps>>(
+      "k_glr_backward", c.a, st, (const T*)c.dy, c.dh_final, (const T*)c.x, (const T*)c.r, (const T*)c.i, c.lam, c.h0, c.cu,
+      (const float*)c.marks, (T*)c.dx, (T*)c.dr, (T*)c.di, c.dh0, c.part);
 }
 template <typename T>
 cudaError_t by_type(Call& c, cudaStream_t st) {

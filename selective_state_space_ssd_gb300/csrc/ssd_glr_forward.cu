@@ -7,7 +7,6 @@ namespace ssd {
 namespace glr {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStages = 2;  // tiles in shared memory or on their way there
 // Steps a thread has of a tile, and blocks an SM.  Long runs share the joining of their maps and the cluster's barriers: one
 // sequence of 16384 steps of 2560 channels takes 91 us in runs of 16 (two blocks an SM), 106 us in runs of 8 (three); packed,
@@ -31,8 +30,8 @@ __device__ __forceinline__ P inv_root(P m2, P e1) {
 // sequences; one for a packed batch).  Tile j share + k of a sequence is block k's of its cluster.  One warp joins the
 // runs' maps of each tile to one that goes to all blocks of the cluster; one barrier of the cluster later each of them has
 // the state that enters its tile.
-template <typename T, bool kVec, bool kPacked>
-__global__ void __launch_bounds__(kThreads, blocks_of<T>())
+template <typename T, bool kVec, bool kPacked, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == kFewWarps ? blocks_of<T>() : 1)
     k_glr_forward(Args a, const T* __restrict__ x, const T* __restrict__ r, const T* __restrict__ i,
                   const float* __restrict__ lam, const float* __restrict__ h0, const int* __restrict__ cu, T* y,
                   float* h_final, float* marks) {
@@ -204,13 +203,15 @@ __global__ void __launch_bounds__(kThreads, blocks_of<T>())
   copies_wait<0>();
 }
 
+template <typename T, bool kVec, bool kPacked, int kWarps>
+struct Shape {
+  static constexpr auto kernel = &k_glr_forward<T, kVec, kPacked, kWarps>;
+  static constexpr int warps = kWarps, run = run_of<T>(), smem = kStages * Tiles<T, kVec, kWarps, run, 3>::kBytes;
+};
 template <typename T, bool kVec, bool kPacked>
 cudaError_t run(Call& c, cudaStream_t st) {
-  auto* kernel = &k_glr_forward<T, kVec, kPacked>;
-  constexpr int smem = kStages * Tiles<T, kVec, kWarps, run_of<T>(), 3>::kBytes;
-  static const Fit<decltype(kernel)> fit(kernel, kThreads, smem);
-  return launch_cluster("k_glr_forward", kernel, fit, c.a, run_of<T>() * kWarps, kThreads, smem, st, (const T*)c.x,
-                        (const T*)c.r, (const T*)c.i, c.lam, c.h0, c.cu, (T*)c.y, c.h_final, c.marks);
+  return launch_cluster<Shape<T, kVec, kPacked, kFewWarps>, Shape<T, kVec, kPacked, kManyWarps>>(
+      "k_glr_forward", c.a, st, (const T*)c.x, (const T*)c.r, (const T*)c.i, c.lam, c.h0, c.cu, (T*)c.y, c.h_final, c.marks);
 }
 template <typename T>
 cudaError_t by_type(Call c, cudaStream_t st) {

@@ -276,6 +276,20 @@ def test_long_sequences_in_many_tiles():
     compare(c)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("n,steps,dim", [(1, 3000, 70), (3, 1400, 33), (1, 1700, 2624)])
+def test_more_tiles_than_blocks_that_share_them(n, steps, dim, io):
+    """Few channels (blocks of many warps) and many of them (of few), over several rounds of a cluster."""
+    compare(make((n, steps), dim, io, 14, n))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths,dim", [([1200, 0, 1, 700, 65, 1100], 70), ([2900, 3], 64), ([129] * 20 + [0, 1], 33)])
+def test_packed_over_several_rounds(lengths, dim, io):
+    bounds = np.concatenate([[0], np.cumsum(lengths)]).tolist()
+    compare(make((bounds[-1],), dim, io, 15, len(lengths)), torch.tensor(bounds, dtype=torch.int32, device="cuda"), bounds)
+
+
 def test_same_bits_again_on_another_stream_and_in_a_graph():
     c = make((2, 300), 128, "bf16", 14, 2)
     d = {k: t.cuda() for k, t in c.items()}
