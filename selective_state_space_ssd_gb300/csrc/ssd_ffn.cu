@@ -9,9 +9,8 @@
 // 256 columns, four warps each: with four for both, tiles of four steps waited for them, 256 rows of 2560 and 7680 backward
 // 62 us in place of 58).  In the forward's tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets
 // both.
-// Blocks go in clusters of two, with tiles of the same columns: each copies half of the columns' operand into both, which
-// takes a third off what comes out of L2 (8192 rows of 2560 and 7680, forward and backward: 1340 us in place of 1375; 1501 of
-// 776 and 2056: 61 in place of 75).  Tiles of 128 x 128 where they end sooner (sooner()).
+// Tiles of 128 x 128 where they end sooner (sooner()).  Every block copies its whole operands: no copy goes to another
+// block's shared memory, so that operands may lie in any memory that a TMA load reads.
 //
 // dx sums over 2 F numbers; with few rows its sums are taken in pieces, fp32, that another launch joins (grads_plan()).
 //
@@ -48,10 +47,9 @@ struct Stages {
 };
 
 enum Kind { kForward, kGrads };
-// Pairs of row tiles that are walked over together, column by column, so that their operands stay in L2.  8192 rows of 2560
-// and 7680, us: forward 432 with 4, 393 with 8, 384 with 16, 389 with 32; gradients 712 with 2, 719 with 4, 722 with 8, 778
-// with 32.
-constexpr int group_of(Kind kind) { return kind == kForward ? 16 : 2; }
+// Row tiles that are walked over together, column by column, so that their operands stay in L2.  8192 rows of 2560 and 7680,
+// us: forward 436 with 8, 400 with 16 and with 32, 416 with 64; gradients 715 with 2 and with 4, 762 with 8, 751 with 16.
+constexpr int group_of(Kind kind) { return kind == kForward ? 32 : 4; }
 
 struct Args {
   int M, D, F;
@@ -67,21 +65,19 @@ struct Maps {
 struct Plan {
   int m_tiles, n_tiles, steps, half;      // tiles and steps of BK; dx: half of the steps are of the first pair of matrices
   int w_m_tiles, w_n_tiles, w_steps, w_half;  // the weights' gradients; half of the row tiles are of the first matrix
-  int both;                                   // of those, pairs of tiles that every pair of blocks has
+  int both;                                   // of those, tiles that every block has
   int pieces;                                 // of each sum of dx, taken as tiles of their own and joined by k_ffn_join
 };
-// Two blocks, a cluster, work on two row tiles of the same columns side by side.  The n-th of such pairs of tiles of a pair
-// of blocks: the forward's go round.  dx's (piece by piece) do too, and the first of them leave some with one more; the
-// weights' gradients' follow, `both` for every pair of blocks and the others for those with fewer of dx's, as many as end the
-// two kinds about together (balance()).
+// The n-th tile of a block: the forward's go round.  dx's (piece by piece) do too, and the first of them leave some blocks
+// with one more; the weights' gradients' follow, `both` for every block and the others for those with fewer of dx's, as many
+// as end the two kinds about together (balance()).
 struct Item {
   bool weights;
   int t, from, to, piece;  // tile, steps of its sum
 };
-__host__ __device__ __forceinline__ int pairs_of(int m_tiles, int n_tiles) { return (m_tiles + 1) / 2 * n_tiles; }
 template <Kind kKind>
 __device__ __forceinline__ bool item_of(const Plan& p, int n, Item& it) {
-  const int blocks = gridDim.x / 2, i = blockIdx.x / 2, whole = pairs_of(p.m_tiles, p.n_tiles), tiles = whole * p.pieces;
+  const int blocks = gridDim.x, i = blockIdx.x, whole = p.m_tiles * p.n_tiles, tiles = whole * p.pieces;
   it = Item{false, n * blocks + i, 0, p.steps, 0};
   if (it.t < tiles) {
     if (kKind == kGrads && p.pieces > 1) {
@@ -97,7 +93,7 @@ __device__ __forceinline__ bool item_of(const Plan& p, int n, Item& it) {
   const int more = tiles % blocks, k = n - (tiles / blocks + (i < more));  // those that have one more of dx's: 0 .. more - 1
   it.weights = true;
   it.t = k < p.both ? k * blocks + i : p.both * blocks + (k - p.both) * (blocks - more) + i - more;
-  return (k < p.both || i >= more) && it.t < pairs_of(p.w_m_tiles, p.w_n_tiles);
+  return (k < p.both || i >= more) && it.t < p.w_m_tiles * p.w_n_tiles;
 }
 
 __device__ __forceinline__ void act_and_slope(float g, bool gelu, float& a, float& s) {
@@ -149,32 +145,14 @@ __device__ __forceinline__ void kept_values(const Kept& k, float (&v)[8]) {
   }
 }
 
-// This block's row tile (m_tiles: there is none) and column tile of an item.
+// The row tile and column tile of an item.
 template <Kind kKind>
 __device__ __forceinline__ void tile_of(const Plan& p, const Item& it, int& m, int& n) {
   constexpr int kGroup = group_of(kKind);
-  const int m_pairs = ((it.weights ? p.w_m_tiles : p.m_tiles) + 1) / 2, n_tiles = it.weights ? p.w_n_tiles : p.n_tiles;
-  const int per = kGroup * n_tiles, g = it.t / per, m0 = g * kGroup, gm = min(kGroup, m_pairs - m0), r = it.t - g * per;
-  m = 2 * (m0 + r % gm) + (blockIdx.x & 1);
+  const int m_tiles = it.weights ? p.w_m_tiles : p.m_tiles, n_tiles = it.weights ? p.w_n_tiles : p.n_tiles;
+  const int per = kGroup * n_tiles, g = it.t / per, m0 = g * kGroup, gm = min(kGroup, m_tiles - m0), r = it.t - g * per;
+  m = m0 + r % gm;
   n = r / gm;
-}
-
-// The pair of blocks: copies that go to both, and arrivals at both blocks' barriers.
-__device__ __forceinline__ void tma_load_2d_both(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
-      "[%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"((uint16_t)3)
-      : "memory");
-}
-__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                   smem_u32(bar)),
-               "h"((uint16_t)3)
-               : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Registers of a tcgen05.ld after its wait: nothing that reads them may be moved in front of this.
@@ -196,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* slot = reinterpret_cast<uint32_t*>(tempty + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 2);
+    for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
     for (int s = 0; s < 2; ++s) mbar_init(tfull + s, 1), mbar_init(tempty + s, 4);
     mbar_init_fence();
     if (kKind == kForward && blockIdx.x == 0) *status = 0;
@@ -204,36 +182,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_alloc(slot, 2 * BN);
   __syncwarp();
   tc_fence_before();
-  cluster_sync();  // (both blocks' barriers are there before anything arrives at them)
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
 
   if (warp == 0) {  // copies
-    // A block's own rows, and half of the columns, which go to both blocks.
-    const int rank = blockIdx.x & 1;
     const auto load = [&](int s, bool weights, int m, int n, int k) {
       uint8_t *a = smem + s * kBytesStage, *b = a + kBytesA;
       mbar_expect_tx(full + s, kBytesStage);
       if (kKind == kForward) {
         tma_load_2d(a, &maps.a[0], k * BK, m * BM, full + s);
-        tma_load_2d_both(b + rank * (kBytesB / 2), &maps.b[rank], k * BK, n * kOwn, full + s);
+        tma_load_2d(b, &maps.b[0], k * BK, n * kOwn, full + s);
+        tma_load_2d(b + kBytesB / 2, &maps.b[1], k * BK, n * kOwn, full + s);
       } else if (!weights) {
         const int which = k >= plan.half, kk = (k - (which ? plan.half : 0)) * BK;
         tma_load_2d(a, &maps.a[which], kk, m * BM, full + s);
 #pragma unroll
-        for (int j = 0; j < BN / 128; ++j) {
-          const int col = rank * (BN / 128) + j;
-          tma_load_2d_both(b + col * 8192, &maps.b[which], n * BN + col * 64, kk, full + s);
-        }
+        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.b[which], n * BN + j * 64, kk, full + s);
       } else {
         const int which = m >= plan.w_half, row = (m - (which ? plan.w_half : 0)) * BM;
 #pragma unroll
         for (int j = 0; j < BM / 64; ++j) tma_load_2d(a + j * 8192, &maps.wa[which], row + j * 64, k * BK, full + s);
 #pragma unroll
-        for (int j = 0; j < BN / 128; ++j) {
-          const int col = rank * (BN / 128) + j;
-          tma_load_2d_both(b + col * 8192, &maps.wb, n * BN + col * 64, k * BK, full + s);
-        }
+        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.wb, n * BN + j * 64, k * BK, full + s);
       }
     };
     int it = 0;
@@ -249,8 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    // the last stages have to be done with, in both blocks, before this one may end: copies and arrivals come from both
-    for (int j = max(0, it - kStages); j < it; ++j) mbar_wait(empty + j % kStages, (j / kStages) & 1, status, 2);
+    // what is still on its way has to arrive before the block may end
+    for (int j = max(0, it - kStages); j < it; ++j) mbar_wait(full + j % kStages, (j / kStages) & 1, status, 2);
   } else if (warp == 1) {  // products
     int it = 0, done = 0;
     bool ok = true;
@@ -275,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < BK; kk += 16)
             mma_bf16(tmem + acc * BN, da + (kk / 16) * step_a, db + (kBmn ? mdesc_step(kk) : kdesc_step(BN, kk)), idesc,
                      k > tile.from || kk > 0);
-          mma_commit_both(empty + s);
+          mma_commit(empty + s);
         }
         __syncwarp();
       }
@@ -292,7 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int done = acc; item_of<kKind>(plan, done, tile); done += 2) {
       int m, n;
       tile_of<kKind>(plan, tile, m, n);
-      const bool there = m < (tile.weights ? plan.w_m_tiles : plan.m_tiles);  // (an odd last row tile has no neighbour)
       const bool ok = mbar_wait(tfull + acc, (done / 2) & 1, status, 6);
       if (named_bar_or(bar, 128, !ok)) break;
       tc_fence_after();
@@ -327,12 +297,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async();
             named_bar(bar, 128);
             const int col = n * kOwn + (c - 1) * 32;
-            if (leader && there && col < args.F) {
+            if (leader && col < args.F) {
               tma_store_2d(&maps.o[0], out, col, m * BM);
               tma_store_commit();
             }
           }
-          if (stash && there) {
+          if (stash) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (n * kOwn + c * 32 + j * 8 < args.F)
@@ -342,20 +312,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         if (lane == 0) mbar_arrive(tempty + acc);
       } else if (!tile.weights && plan.pieces > 1) {
-        if (there) {
-          float4* to = part + (((size_t)tile.piece * plan.m_tiles + m) * (args.D / 4) + n * (BN / 4)) * BM + row;
+        float4* to = part + (((size_t)tile.piece * plan.m_tiles + m) * (args.D / 4) + n * (BN / 4)) * BM + row;
 #pragma unroll 1
-          for (int c = 0; c < BN / 32 && n * BN + c * 32 < args.D; ++c, to += 8 * BM) {
-            uint32_t v[32];
-            tmem_ld32_nowait(base + c * 32, v);
-            tmem_wait_ld();
-            settled(v);
+        for (int c = 0; c < BN / 32 && n * BN + c * 32 < args.D; ++c, to += 8 * BM) {
+          uint32_t v[32];
+          tmem_ld32_nowait(base + c * 32, v);
+          tmem_wait_ld();
+          settled(v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (n * BN + c * 32 + e * 4 < args.D)
-                to[e * BM] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                         __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-          }
+          for (int e = 0; e < 8; ++e)
+            if (n * BN + c * 32 + e * 4 < args.D)
+              to[e * BM] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
+                                       __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
         }
         tc_fence_before();
         if (lane == 0) mbar_arrive(tempty + acc);
@@ -380,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async();
           named_bar(bar, 128);
-          if (leader && there && n * BN + p * 64 < args.D) {
+          if (leader && n * BN + p * 64 < args.D) {
             tma_store_2d(to_map, out, n * BN + p * 64, row0);
             tma_store_commit();
           }
@@ -393,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync();  // (nothing of the other block's is on its way here any more)
+  __syncthreads();
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 2 * BN);
@@ -575,36 +543,24 @@ cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const C
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Stages<BN>::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  const int pairs = pairs_of(plan.m_tiles, plan.n_tiles) * plan.pieces +
-                    (kKind == kGrads ? pairs_of(plan.w_m_tiles, plan.w_n_tiles) : 0);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pairs < kSMs / 2 ? 2 * pairs : kSMs);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Stages<BN>::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t launched = cudaSuccess;
+  const long long tiles = (long long)plan.m_tiles * plan.n_tiles * plan.pieces +
+                          (kKind == kGrads ? (long long)plan.w_m_tiles * plan.w_n_tiles : 0);
   SSD_LAUNCH(name, st,
-             launched = cudaLaunchKernelEx(&cfg, kernel, maps, plan, c.a, kKind == kForward ? c.stash : (uint8_t*)nullptr,
-                                           c.part, c.status));
-  return launched;
+             kernel<<<tiles < kSMs ? (unsigned)tiles : kSMs, kThreads, Stages<BN>::kSmem, st>>>(
+                 maps, plan, c.a, kKind == kForward ? c.stash : nullptr, c.part, c.status));
+  return cudaGetLastError();
 }
 int up(long long a, int b) { return (int)((a + b - 1) / b); }
 
 constexpr int kLeast = 4;  // steps that a tile's results take: a tile of fewer ends no sooner
-// dx and the weights' gradients in one launch: how many of the latter's pairs of tiles every pair of blocks takes, so
-// that the last ends soonest (steps of those with one more of dx's, and of the others).  Returns the steps until then.  8192
-// rows of 2560 and 7680: 320 pairs of tiles of 240 steps and 600 of 128 on 76 pairs of blocks end after 2112 steps, one kind
-// after the other they would after 2224.
+// dx and the weights' gradients in one launch: how many of the latter's tiles every block takes, so that the last ends
+// soonest (steps of those with one more of dx's, and of the others).  Returns the steps until then.  8192 rows of 2560 and
+// 7680: 640 tiles of 240 steps and 1200 of 128 on 152 blocks end after 2112 steps, one kind after the other they would after
+// 2224.
 long long balance(Plan* p) {
-  const int tiles = pairs_of(p->m_tiles, p->n_tiles) * p->pieces, w_tiles = pairs_of(p->w_m_tiles, p->w_n_tiles);
+  const int tiles = p->m_tiles * p->n_tiles * p->pieces, w_tiles = p->w_m_tiles * p->w_n_tiles;
   const int steps = up(p->steps, p->pieces), w_steps = p->w_steps > kLeast ? p->w_steps : kLeast;
-  const int blocks = tiles + w_tiles < kSMs / 2 ? tiles + w_tiles : kSMs / 2;
+  const int blocks = tiles + w_tiles < kSMs ? tiles + w_tiles : kSMs;
   const int more = tiles % blocks, each = tiles / blocks, others = blocks - more;
   long long best = -1;
   const int least = w_tiles / blocks - steps / w_steps - 2;  // (with fewer, the others would end later than the first)
@@ -619,16 +575,15 @@ long long balance(Plan* p) {
 }
 
 // Whether tiles of half the columns end sooner: their step takes about 5/8 of a whole one's, and they are dealt out more
-// evenly.  Forward, us: 1501 rows of 776 and 2056 in narrow ones 22.6, in wide ones 25.2; 2048 of 1024 and 4096 42.0 and
-// 39.2; 8192 of 2560 and 7680 490 and 392.  Gradients, the same sizes: 32.2 and 32.7, 59 and 52, 916 and 725; 256 rows of
-// 2560 and 7680, whose few long sums of dx are what it waits for, 64 and 97.
+// evenly.  Forward, us: 1501 rows of 776 and 2056 in narrow ones 25.6, in wide ones 29.0; 2048 of 1024 and 4096 42.9 and
+// 41.0; 8192 of 2560 and 7680 505 and 400.  Gradients, the same sizes: 41.3 and 43.1, 59 and 54, 908 and 717.
 constexpr int kWideStep = 8, kNarrowStep = 5;
 bool sooner(long long narrow_steps, long long wide_steps) { return narrow_steps * kNarrowStep < wide_steps * kWideStep; }
 
 // The gradients' tiles: wide or narrow, and dx's sums in as many pieces as end soonest, the launch that joins them (12 steps)
-// and the bytes it reads counted in.  With few rows dx is a few tiles of long sums (backward, us, in pieces and in one: 125
-// rows of 288 and 8816 30 and 74; 256 of 2560 and 7680 58 and 76; 453 of 712 and 11912 64 and 115; 1501 of 776 and 2056 stay
-// in one, 44 and 48 in two).
+// and the bytes it reads counted in.  With few rows dx is a few tiles of long sums (the backward's launches, us, in pieces
+// and in one: 125 rows of 288 and 8816 33 and 75; 256 of 2560 and 7680 59 and 72; 453 of 712 and 11912 71 and 154; 1501 of
+// 776 and 2056 stay in one, 51 and 56 in two).
 constexpr int kMostPieces = 16, kLeastSteps = 8, kJoinSteps = 12;  // pieces, steps of one
 Plan grads_plan(const Args& a, bool* narrow) {
   Plan best = {};
@@ -638,7 +593,7 @@ Plan grads_plan(const Args& a, bool* narrow) {
               2 * up(a.F, BM), up(a.D, cols), up(a.M, BK),     up(a.F, BM)};
     const auto fits = [&](int pieces) {
       return pieces <= kMostPieces && p.steps >= kLeastSteps * pieces &&
-             (long long)pairs_of(p.m_tiles, p.n_tiles) * pieces <= 4 * kSMs;
+             (long long)p.m_tiles * p.n_tiles * pieces <= 8 * kSMs;
     };
     for (p.pieces = 1; p.pieces == 1 || fits(p.pieces); ++p.pieces) {
       long long end = balance(&p) * (cols == 256 ? kWideStep : kNarrowStep);
@@ -665,7 +620,7 @@ cudaError_t forward(const Call& c, cudaStream_t st) {
   Maps maps;
   Few few;
   const bool is_few = few_rows(c.a, &few);
-  const auto rounds = [&](int cols) { return up(pairs_of(up(c.a.M, BM), up(c.a.F, cols)), kSMs / 2); };
+  const auto rounds = [&](int cols) { return up((long long)up(c.a.M, BM) * up(c.a.F, cols), kSMs); };
   const bool narrow = sooner(rounds(64), rounds(128));
   const int wide = is_few ? few.wide : narrow ? 64 : 128;
   cudaError_t e = map(&maps.a[0], c.x, c.a.D, c.a.M, c.a.xs, BK, is_few ? few.rows : BM);
