@@ -44,10 +44,15 @@ __device__ __forceinline__ float rsqrt_f(float x) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// The smaller one; NaN if one is.
+// The smaller one, the greater one; NaN if one is.
 __device__ __forceinline__ float min_nan(float x, float y) {
   float z;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
   return z;
 }
 constexpr float kLog2e = 1.4426950408889634f;

@@ -22,6 +22,7 @@
 #include "ssd.h"
 #include "ssd_device.cuh"
 #include "ssd_internal.h"
+#include "pair.cuh"
 #include "tc_common.cuh"
 #include "vec_io.cuh"
 
@@ -96,17 +97,20 @@ __device__ __forceinline__ bool item_of(const Plan& p, int n, Item& it) {
   return (k < p.both || i >= more) && it.t < p.w_m_tiles * p.w_n_tiles;
 }
 
+// The activation and its slope at g, right for every finite g and NaN of a NaN: q = s(z) is 0 or 1 where e^-z is beyond fp32,
+// and 1 - q is taken of q, so that no infinity meets a zero.
 __device__ __forceinline__ void act_and_slope(float g, bool gelu, float& a, float& s) {
   if (gelu) {
-    // tanh form: g s(2 z) with z = sqrt(2 / pi) (g + 0.044715 g^3)
-    const float c = 1.5957691216057308f, e = __expf(fminf(-c * fmaf(0.044715f * g * g, g, g), 80.f));
-    const float q = __fdividef(1.f, 1.f + e);
+    // tanh form: g s(z) with z = 2 sqrt(2 / pi) (g + 0.044715 g^3).  From |g| = 16 on, where |z| is 317, q no longer changes
+    // and the term of 1 - q is 0, so powers of g stay below.
+    const float c = 1.5957691216057308f, v = max_nan(min_nan(g, 16.f), -16.f), v2 = v * v;
+    const float q = __fdividef(1.f, 1.f + __expf(-c * fmaf(0.044715f * v2, v, v)));
     a = g * q;
-    s = fmaf(g * q * (e * q), c * fmaf(3.f * 0.044715f * g, g, 1.f), q);
+    s = fmaf(v * q * (1.f - q), c * fmaf(3.f * 0.044715f, v2, 1.f), q);
   } else {
-    const float e = __expf(fminf(-g, 80.f)), q = __fdividef(1.f, 1.f + e);
+    const float q = __fdividef(1.f, 1.f + __expf(-g));
     a = g * q;
-    s = q * fmaf(g, e * q, 1.f);
+    s = q * fmaf(g, 1.f - q, 1.f);
   }
 }
 
