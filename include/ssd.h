@@ -667,11 +667,12 @@ ssd_status ssd_conv_step(const ssd_conv_problem* prob, const void* x, const void
  * Layouts: x, dx [M,D]; w_gate, w_up, dw_gate, dw_up [F,D]; h, dh [M,F].
  * Every pointer is 16-byte aligned.  Outputs must not overlap inputs.
  *
- * Precision.  h is rounded once.  The stash holds 24 bits of each number of G
- * and U, and the backward's products read dG and dU rounded to bf16: 2^-8 of
- * each term at most, so the gradients are good to that of their terms' size and
- * rounded once more.  A NaN or infinity reaches its own row of h and dx, and
- * every element of the weights' gradients that sums over that row.
+ * Precision.  h is rounded once.  The stash holds each number of G and U
+ * rounded to 24 bits (2^-16 of it at most), and the backward's products read dG
+ * and dU rounded to bf16: 2^-8 of each term at most, so the gradients are good
+ * to that of their terms' size and rounded once more.  A NaN or infinity reaches
+ * its own row of h and dx, and every element of the weights' gradients that sums
+ * over that row.
  *
  * ssd_ffn_stash_size: bytes of the stash that a training forward may keep for
  *   its backward (6 F bytes for each of M rows, M rounded up to 128).

@@ -114,9 +114,9 @@ __device__ __forceinline__ void act_and_slope(float g, bool gelu, float& a, floa
   }
 }
 
-// The stash: G and U with 24 bits of each number (their last eight are cut off: less than 2^-15 of a value, where bf16
-// would leave 2^-8 in every factor of dG and dU), as the upper 16 and the next 8 bits in planes of their own.  A piece is
-// eight columns of a row; pieces of 128 rows follow one another, as the forward's threads write them.
+// The stash: G and U with 24 bits of each number, rounded to nearest (2^-16 of a value at most, where bf16 would leave 2^-8
+// in every factor of dG and dU), as the upper 16 and the next 8 bits in planes of their own.  A piece is eight columns of a
+// row; pieces of 128 rows follow one another, as the forward's threads write them.
 struct Kept {
   uint4* hi;
   uint2* lo;
@@ -126,7 +126,12 @@ __device__ __forceinline__ Kept kept(uint8_t* stash, const Args& a, int row, int
   const size_t n = kept_pieces(a), at = ((size_t)(row / BM) * (a.F / 8) + f / 8) * BM + row % BM;
   return Kept{reinterpret_cast<uint4*>(stash) + which * n + at, reinterpret_cast<uint2*>(stash + 2 * n * 16) + which * n + at};
 }
-__device__ __forceinline__ void keep_one(const Kept& k, const uint32_t* v) {
+// (numbers that would become infinite are cut off, as are infinities and NaN, whose upper bits stay as they are)
+__device__ __forceinline__ uint32_t nearest24(uint32_t v) { return (v & 0x7fffffffu) < 0x7f7fff80u ? v + 0x80u : v; }
+__device__ __forceinline__ void keep_one(const Kept& k, const uint32_t* full) {
+  uint32_t v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = nearest24(full[e]);
   const auto hi = [](uint32_t x, uint32_t y) { return __byte_perm(x, y, 0x7632); };
   const auto lo = [](const uint32_t* x) {
     return __byte_perm(__byte_perm(x[0], x[1], 0x0051), __byte_perm(x[2], x[3], 0x0051), 0x5410);
