@@ -50,7 +50,7 @@ class ShortConv(torch.autograd.Function):
             own = min(steps, held)
             dx.view(-1, *x.shape[-2:])[:, steps - own:] += dlast[:, held - own:]
             if dtaps is not None and own < held:
-                dtaps[:, own:] += dlast[:, :held - own]
+                dtaps.view(-1, *dtaps.shape[-2:])[:, own:] += dlast[:, :held - own]
         grads = first_orders((dx, g["dw"], g["db"], dtaps), dy, dlast, x, weight, bias, taps)
         return *(t if need else None for t, need in zip(grads, ctx.needs_input_grad)), None
 
