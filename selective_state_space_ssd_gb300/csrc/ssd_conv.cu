@@ -479,28 +479,27 @@ __global__ void __launch_bounds__(128) k_conv_step(Args a, const T* __restrict__
   const int c = (blockIdx.x * 128 + threadIdx.x) * kW;
   if (c >= a.D) return;
   const Weights<K, kW> wt(w, b, a.wbf16, c);
-  for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
-    const long long slot = slots ? slots[n] : n;
-    const bool held = slot >= 0 && slot < num_slots;  // else: a place without a sequence, y = 0
-    T* s = state + (held ? (size_t)slot * (K - 1) * a.D : 0) + c;
-    Chan<kW> win[K - 1];
+  const int n = blockIdx.y;
+  const long long slot = slots ? slots[n] : n;
+  const bool held = slot >= 0 && slot < num_slots;  // else: a place without a sequence, y = 0
+  T* s = state + (held ? (size_t)slot * (K - 1) * a.D : 0) + c;
+  Chan<kW> win[K - 1];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) win[j] = held ? get<T, kW>(s + (size_t)(K - 2 - j) * a.D) : none<kW>();
-    for (int t = 0; t < a.T; ++t) {
-      const size_t at = (size_t)n * a.T + t;
-      Chan<kW> o = none<kW>();
-      if (held) {
-        const Chan<kW> v = get<T, kW>(x + at * a.xs + c);
-#pragma unroll
-        for (int i = 0; i < Chan<kW>::kP; ++i) o.p[i] = act(product<K, kW>(wt, win, v, i), a.silu);
-        shift<K, kW>(win, v);
-      }
-      put<T, kW>(y + at * a.D + c, o);
-    }
+  for (int j = 0; j < K - 1; ++j) win[j] = held ? get<T, kW>(s + (size_t)(K - 2 - j) * a.D) : none<kW>();
+  for (int t = 0; t < a.T; ++t) {
+    const size_t at = (size_t)n * a.T + t;
+    Chan<kW> o = none<kW>();
     if (held) {
+      const Chan<kW> v = get<T, kW>(x + at * a.xs + c);
 #pragma unroll
-      for (int j = 0; j < K - 1; ++j) put<T, kW>(s + (size_t)(K - 2 - j) * a.D, win[j]);
+      for (int i = 0; i < Chan<kW>::kP; ++i) o.p[i] = act(product<K, kW>(wt, win, v, i), a.silu);
+      shift<K, kW>(win, v);
     }
+    put<T, kW>(y + at * a.D + c, o);
+  }
+  if (held) {
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) put<T, kW>(s + (size_t)(K - 2 - j) * a.D, win[j]);
   }
 }
 
@@ -535,9 +534,9 @@ void backward_of(const Call& c, cudaStream_t st) {
 }
 template <typename T, int K, int kW>
 void step_of(const Call& c, void* state, const int32_t* slots, long long num_slots, cudaStream_t st) {
-  const int groups = (c.a.D + kW - 1) / kW;
+  const int groups = (c.a.D + kW - 1) / kW;  // (make_args: 65535 sequences at most)
   SSD_LAUNCH("k_conv_step", st,
-             k_conv_step<T, K, kW><<<dim3((groups + 127) / 128, c.a.N < 65535 ? c.a.N : 65535), 128, 0, st>>>(
+             k_conv_step<T, K, kW><<<dim3((groups + 127) / 128, c.a.N), 128, 0, st>>>(
                  c.a, (const T*)c.x, c.w, c.b, (T*)state, slots, num_slots, (T*)c.y));
 }
 

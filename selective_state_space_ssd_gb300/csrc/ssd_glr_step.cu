@@ -16,42 +16,41 @@ __global__ void __launch_bounds__(kStepThreads)
                const float* __restrict__ lam, float* state, const int* __restrict__ slots, long long num_slots, T* y) {
   const int c = (blockIdx.x * kStepThreads + threadIdx.x) * kW;
   if (c >= a.D) return;
-  for (int n = blockIdx.y; n < a.N; n += gridDim.y) {
-    const long long slot = slots ? slots[n] : n;
-    const bool held = slot >= 0 && slot < num_slots;  // else: a place without a sequence, y = 0
-    float* s = state + (held ? (size_t)slot * a.D : 0) + c;
-    constexpr int kP = (kW + 1) / 2;
-    const auto two = [](const float(&v)[kW], int p) { return pair(v[2 * p], kW > 1 ? v[(2 * p + 1) % kW] : 0.f); };
-    float h[kW] = {}, l[kW];
-    load<float, kW>(lam + c, l);
-    if (held) load<float, kW>(s, h);
-    P rate[kP];
+  const int n = blockIdx.y;
+  const long long slot = slots ? slots[n] : n;
+  const bool held = slot >= 0 && slot < num_slots;  // else: a place without a sequence, y = 0
+  float* s = state + (held ? (size_t)slot * a.D : 0) + c;
+  constexpr int kP = (kW + 1) / 2;
+  const auto two = [](const float(&v)[kW], int p) { return pair(v[2 * p], kW > 1 ? v[(2 * p + 1) % kW] : 0.f); };
+  float h[kW] = {}, l[kW];
+  load<float, kW>(lam + c, l);
+  if (held) load<float, kW>(s, h);
+  P rate[kP];
 #pragma unroll
-    for (int p = 0; p < kP; ++p) {
-      rate[p] = each(two(l, p), [&](float v) { return a.scale * softplus_f(v); });
-    }
-    for (int t = 0; t < a.T; ++t) {
-      const size_t at = (size_t)n * a.T + t;
-      if (held) {
-        float xv[kW], rv[kW], iv[kW];
-        load<T, kW>(x + at * a.xs + c, xv);
-        load<T, kW>(r + at * a.rs + c, rv);
-        load<T, kW>(i + at * a.is + c, iv);
-#pragma unroll
-        for (int p = 0; p < kP; ++p) {
-          const P o = one_minus_exp<true>(rate[p] * sigmoid(two(rv, p))), av = one_less(o);
-          const P m = each(o * one_more(av), [](float v) { return sqrt_f(v); });
-          const P hn = fma(av, two(h, p), m * (sigmoid(two(iv, p)) * two(xv, p)));
-          float h0, h1;
-          split(hn, h0, h1);
-          h[2 * p] = h0;
-          if (kW > 1) h[(2 * p + 1) % kW] = h1;
-        }
-      }
-      save<T, kW>(y + at * a.D + c, h);
-    }
-    if (held) save<float, kW>(s, h);
+  for (int p = 0; p < kP; ++p) {
+    rate[p] = each(two(l, p), [&](float v) { return a.scale * softplus_f(v); });
   }
+  for (int t = 0; t < a.T; ++t) {
+    const size_t at = (size_t)n * a.T + t;
+    if (held) {
+      float xv[kW], rv[kW], iv[kW];
+      load<T, kW>(x + at * a.xs + c, xv);
+      load<T, kW>(r + at * a.rs + c, rv);
+      load<T, kW>(i + at * a.is + c, iv);
+#pragma unroll
+      for (int p = 0; p < kP; ++p) {
+        const P o = one_minus_exp<true>(rate[p] * sigmoid(two(rv, p))), av = one_less(o);
+        const P m = each(o * one_more(av), [](float v) { return sqrt_f(v); });
+        const P hn = fma(av, two(h, p), m * (sigmoid(two(iv, p)) * two(xv, p)));
+        float h0, h1;
+        split(hn, h0, h1);
+        h[2 * p] = h0;
+        if (kW > 1) h[(2 * p + 1) % kW] = h1;
+      }
+    }
+    save<T, kW>(y + at * a.D + c, h);
+  }
+  if (held) save<float, kW>(s, h);
 }
 
 template <typename T>
@@ -61,7 +60,7 @@ void launch(const Args& a, const void* x, const void* r, const void* i, const fl
   const bool whole = !(a.D % 4 || a.xs % 4 || a.rs % 4 || a.is % 4 || off(x, piece) || off(r, piece) || off(i, piece) ||
                        off(y, piece) || off(lam, 16) || off(state, 16));
   const int w = whole ? 4 : 1, groups = (a.D + w - 1) / w;
-  const dim3 grid((groups + kStepThreads - 1) / kStepThreads, a.N < 65535 ? a.N : 65535);
+  const dim3 grid((groups + kStepThreads - 1) / kStepThreads, a.N);  // (make_args: 65535 sequences at most)
   if (whole)
     SSD_LAUNCH("k_glr_step", st,
                k_glr_step<T, 4><<<grid, kStepThreads, 0, st>>>(a, (const T*)x, (const T*)r, (const T*)i, lam, state, slots,
