@@ -61,7 +61,7 @@ struct Args {
 // Operands a (rows of the result), b (its columns), results o; of the forward's product (or dx) and of the weights'
 // gradients, two of each where there are two matrices.
 struct Maps {
-  CUtensorMap a[2], b[2], o[2], wa[2], wb, wo[2];
+  CUtensorMap a[2], b[2], o, wa[2], wb, wo[2];
 };
 struct Plan {
   int m_tiles, n_tiles, steps, half;      // tiles and steps of BK; dx: half of the steps are of the first pair of matrices
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar(bar, 128);
             const int col = n * kOwn + (c - 1) * 32;
             if (leader && col < args.F) {
-              tma_store_2d(&maps.o[0], out, col, m * BM);
+              tma_store_2d(&maps.o, out, col, m * BM);
               tma_store_commit();
             }
           }
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(tempty + acc);
       } else {
         const int which = tile.weights && m >= plan.w_half, row0 = (m - (which ? plan.w_half : 0)) * BM;
-        const CUtensorMap* to_map = tile.weights ? &maps.wo[which] : &maps.o[0];
+        const CUtensorMap* to_map = tile.weights ? &maps.wo[which] : &maps.o;
 #pragma unroll 1
         for (int p = 0; p < BN / 64; ++p) {
           uint32_t v[2][32];
@@ -635,16 +635,16 @@ cudaError_t forward(const Call& c, cudaStream_t st) {
   cudaError_t e = map(&maps.a[0], c.x, c.a.D, c.a.M, c.a.xs, BK, is_few ? few.rows : BM);
   if (e == cudaSuccess) e = map(&maps.b[0], c.wg, c.a.D, c.a.F, c.a.D, BK, wide);
   if (e == cudaSuccess) e = map(&maps.b[1], c.wu, c.a.D, c.a.F, c.a.D, BK, wide);
-  if (e == cudaSuccess && !is_few) e = map(&maps.o[0], c.h, c.a.F, c.a.M, c.a.F, 64, BM);
+  if (e == cudaSuccess && !is_few) e = map(&maps.o, c.h, c.a.F, c.a.M, c.a.F, 64, BM);
   if (e != cudaSuccess) return e;
   maps.a[1] = maps.a[0];
   if (!is_few) {
-    maps.o[1] = maps.o[0], maps.wa[0] = maps.wa[1] = maps.wb = maps.wo[0] = maps.wo[1] = maps.a[0];
+    maps.wa[0] = maps.wa[1] = maps.wb = maps.wo[0] = maps.wo[1] = maps.a[0];
     const Plan p = {up(c.a.M, BM), up(c.a.F, wide), up(c.a.D, BK), 0, 0, 0, 0, 0, 0, 1};
     return narrow ? launch<kForward, 128>("k_ffn_forward", maps, p, c, st)
                   : launch<kForward, 256>("k_ffn_forward", maps, p, c, st);
   }
-  maps.o[0] = maps.o[1] = maps.wa[0] = maps.wa[1] = maps.wb = maps.wo[0] = maps.wo[1] = maps.a[0];
+  maps.o = maps.wa[0] = maps.wa[1] = maps.wb = maps.wo[0] = maps.wo[1] = maps.a[0];
   // (behind the last stage's rows the products still read what 128 rows would take)
   const int smem = few.stages * (few.rows + 2 * few.wide) * 128 + kBytesA + 1024;
   static std::atomic<unsigned long long> allowed{0};
@@ -666,14 +666,13 @@ cudaError_t backward(const Call& c, bool first, cudaStream_t st) {
   if (e == cudaSuccess) e = map(&maps.a[1], c.du, a.F, a.M, a.F, BK, BM);
   if (e == cudaSuccess) e = map(&maps.b[0], c.wg, a.D, a.F, a.D, 64, BK);
   if (e == cudaSuccess) e = map(&maps.b[1], c.wu, a.D, a.F, a.D, 64, BK);
-  if (e == cudaSuccess) e = map(&maps.o[0], c.dx, a.D, a.M, a.D, 64, BM);
+  if (e == cudaSuccess) e = map(&maps.o, c.dx, a.D, a.M, a.D, 64, BM);
   if (e == cudaSuccess) e = map(&maps.wa[0], c.dg, a.F, a.M, a.F, 64, BK);
   if (e == cudaSuccess) e = map(&maps.wa[1], c.du, a.F, a.M, a.F, 64, BK);
   if (e == cudaSuccess) e = map(&maps.wb, c.x, a.D, a.M, a.xs, 64, BK);
   if (e == cudaSuccess) e = map(&maps.wo[0], c.dwg, a.D, a.F, a.D, 64, BM);
   if (e == cudaSuccess) e = map(&maps.wo[1], c.dwu, a.D, a.F, a.D, 64, BM);
   if (e != cudaSuccess) return e;
-  maps.o[1] = maps.o[0];
   const Plan& p = c.plan;
   e = c.narrow ? launch<kGrads, 128>("k_ffn_grads", maps, p, c, st) : launch<kGrads, 256>("k_ffn_grads", maps, p, c, st);
   if (e != cudaSuccess || p.pieces == 1) return e;
