@@ -4,13 +4,16 @@
 // weights' gradients.  The products run on the tensor cores: bf16 operands by TMA into 128-byte swizzled tiles, fp32
 // accumulators in tensor memory.
 //
-// One kernel for all of them, k_ffn_product: output tiles of 128 x 256, one block an SM that walks over tiles; a warp issues
-// the copies, one the products, four turn an accumulator into results while the next tile is under way (two accumulators of
-// 256 columns, four warps each: with four for both, tiles of four steps waited for them, 256 rows of 2560 and 7680 backward
-// 62 us in place of 58).  In the forward's tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets
-// both.
-// Tiles of 128 x 128 where they end sooner (sooner()).  Every block copies its whole operands: no copy goes to another
-// block's shared memory, so that operands may lie in any memory that a TMA load reads.
+// One kernel for all of them, k_ffn_product: pairs of blocks, one block an SM, that walk over pairs of output tiles of 128 x
+// 256; a warp issues the copies, one the products, four turn an accumulator into results while the next tile is under way (two
+// accumulators of 256 columns, four warps each: with four for both, tiles of four steps waited for them).  In the forward's
+// tile the 256 columns are 128 of G and the same 128 of U, so that a thread meets both.
+// A pair's product is one of 256 rows: each block brings its own rows and half of the columns' operand, which the tensor cores
+// of both read, so that a third less comes out of L2 than with whole operands in every block and six stages fit in place of
+// four.  Per launch, us, pairs and single blocks: 8192 rows of 2560 and 7680 forward 371 and 401, gradients 688 and 725; 1501
+// of 776 and 2056 25 and 27, 35 and 41; 4000 of 1536 and 4608 83 and 92, 131 and 141; 125 of 288 and 8816, with few steps a
+// tile, gradients 25 and 24.  (One copy of the operand that goes to both blocks would do the same; it is not for memory of
+// other GPUs, and these calls take any.)  Tiles of 128 x 128 where they end sooner (sooner()).
 //
 // dx sums over 2 F numbers; with few rows its sums are taken in pieces, fp32, that another launch joins (grads_plan()).
 //
@@ -41,16 +44,17 @@ constexpr int kMostSmem = 232448;
 // Stages of a result's tile of BN columns: as many as shared memory holds.
 template <int BN>
 struct Stages {
-  static constexpr int kBytesB = BN * BK * 2, kBytes = kBytesA + kBytesB;
-  static constexpr int kN = BN == 256 ? 4 : 6;
+  static constexpr int kBytesB = BN / 2 * BK * 2, kBytes = kBytesA + kBytesB;  // of a block
+  static constexpr int kN = BN == 256 ? 6 : 8;
   static constexpr int kSmem = kN * kBytes + kBytesOut + 1024 + 256;
   static_assert(kSmem <= kMostSmem, "");
 };
 
 enum Kind { kForward, kGrads };
-// Row tiles that are walked over together, column by column, so that their operands stay in L2.  8192 rows of 2560 and 7680,
-// us: forward 436 with 8, 400 with 16 and with 32, 416 with 64; gradients 715 with 2 and with 4, 762 with 8, 751 with 16.
-constexpr int group_of(Kind kind) { return kind == kForward ? 32 : 4; }
+// Pairs of row tiles that are walked over together, column by column, so that their operands stay in L2.  8192 rows of 2560
+// and 7680, us: forward 393 with 4, 375 with 8, 368 with 16, 384 with 32; gradients 687 with 1, 683 with 2, 692 with 4 and
+// with 8, 699 with 16.
+constexpr int group_of(Kind kind) { return kind == kForward ? 16 : 2; }
 
 struct Args {
   int M, D, F;
@@ -66,19 +70,21 @@ struct Maps {
 struct Plan {
   int m_tiles, n_tiles, steps, half;      // tiles and steps of BK; dx: half of the steps are of the first pair of matrices
   int w_m_tiles, w_n_tiles, w_steps, w_half;  // the weights' gradients; half of the row tiles are of the first matrix
-  int both;                                   // of those, tiles that every block has
+  int both;                                   // of those, pairs of tiles that every pair of blocks has
   int pieces;                                 // of each sum of dx, taken as tiles of their own and joined by k_ffn_join
 };
-// The n-th tile of a block: the forward's go round.  dx's (piece by piece) do too, and the first of them leave some blocks
-// with one more; the weights' gradients' follow, `both` for every block and the others for those with fewer of dx's, as many
-// as end the two kinds about together (balance()).
+// Two blocks, a cluster, work on two row tiles of the same columns.  The n-th of such pairs of tiles of a pair of blocks: the
+// forward's go round.  dx's (piece by piece) do too, and the first of them leave some with one more; the weights' gradients'
+// follow, `both` for every pair of blocks and the others for those with fewer of dx's, as many as end the two kinds about
+// together (balance()).
 struct Item {
   bool weights;
-  int t, from, to, piece;  // tile, steps of its sum
+  int t, from, to, piece;  // pair of tiles, steps of its sum
 };
+__host__ __device__ __forceinline__ int pairs_of(int m_tiles, int n_tiles) { return (m_tiles + 1) / 2 * n_tiles; }
 template <Kind kKind>
 __device__ __forceinline__ bool item_of(const Plan& p, int n, Item& it) {
-  const int blocks = gridDim.x, i = blockIdx.x, whole = p.m_tiles * p.n_tiles, tiles = whole * p.pieces;
+  const int blocks = gridDim.x / 2, i = blockIdx.x / 2, whole = pairs_of(p.m_tiles, p.n_tiles), tiles = whole * p.pieces;
   it = Item{false, n * blocks + i, 0, p.steps, 0};
   if (it.t < tiles) {
     if (kKind == kGrads && p.pieces > 1) {
@@ -94,7 +100,7 @@ __device__ __forceinline__ bool item_of(const Plan& p, int n, Item& it) {
   const int more = tiles % blocks, k = n - (tiles / blocks + (i < more));  // those that have one more of dx's: 0 .. more - 1
   it.weights = true;
   it.t = k < p.both ? k * blocks + i : p.both * blocks + (k - p.both) * (blocks - more) + i - more;
-  return (k < p.both || i >= more) && it.t < p.w_m_tiles * p.w_n_tiles;
+  return (k < p.both || i >= more) && it.t < pairs_of(p.w_m_tiles, p.w_n_tiles);
 }
 
 // The activation and its slope at g, right for every finite g and NaN of a NaN: q = s(z) is 0 or 1 where e^-z is beyond fp32,
@@ -154,15 +160,63 @@ __device__ __forceinline__ void kept_values(const Kept& k, float (&v)[8]) {
   }
 }
 
-// The row tile and column tile of an item.
+// This block's row tile (m_tiles: there is none) and column tile of an item.
 template <Kind kKind>
 __device__ __forceinline__ void tile_of(const Plan& p, const Item& it, int& m, int& n) {
   constexpr int kGroup = group_of(kKind);
-  const int m_tiles = it.weights ? p.w_m_tiles : p.m_tiles, n_tiles = it.weights ? p.w_n_tiles : p.n_tiles;
-  const int per = kGroup * n_tiles, g = it.t / per, m0 = g * kGroup, gm = min(kGroup, m_tiles - m0), r = it.t - g * per;
-  m = m0 + r % gm;
+  const int m_pairs = ((it.weights ? p.w_m_tiles : p.m_tiles) + 1) / 2, n_tiles = it.weights ? p.w_n_tiles : p.n_tiles;
+  const int per = kGroup * n_tiles, g = it.t / per, m0 = g * kGroup, gm = min(kGroup, m_pairs - m0), r = it.t - g * per;
+  m = 2 * (m0 + r % gm) + (blockIdx.x & 1);
   n = r / gm;
 }
+
+// ------------------------------------------------------------ two blocks on one product
+// A product of 256 rows: each block has 128 of them, in its own shared memory and as its own lanes of tensor memory, and half
+// of the columns' operand, which the tensor cores of both read from where it lies.  The first block of the pair issues it.
+__device__ __forceinline__ uint32_t in_first_block(const void* p) {  // the same place in the first block's shared memory
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_u32(p)));
+  return at;
+}
+// Into this block's shared memory; the bytes are counted by the first block's barrier.
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t first_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+          "r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(first_bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+// Arrives at both blocks' barriers once the products so far have ended.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                   smem_u32(bar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_in_first_block(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// (all of it: the accumulators then lie at the same place in both)
+constexpr int kTmemAll = 512;
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols));
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols));
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // Registers of a tcgen05.ld after its wait: nothing that reads them may be moved in front of this.
 __device__ __forceinline__ void settled(uint32_t (&r)[32]) {
@@ -173,7 +227,7 @@ __device__ __forceinline__ void settled(uint32_t (&r)[32]) {
 template <Kind kKind, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_ffn_product(const __grid_constant__ Maps maps, Plan plan, Args args, uint8_t* stash, float4* part, int* status) {
-  constexpr int kStages = Stages<BN>::kN, kBytesStage = Stages<BN>::kBytes, kBytesB = Stages<BN>::kBytesB;
+  constexpr int kStages = Stages<BN>::kN, kBytesStage = Stages<BN>::kBytes;
   constexpr int kOwn = BN / 2;  // the forward: columns of G, and of U
   extern __shared__ uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
@@ -184,36 +238,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(full + s, 1), mbar_init(empty + s, 1);
-    for (int s = 0; s < 2; ++s) mbar_init(tfull + s, 1), mbar_init(tempty + s, 4);
+    for (int s = 0; s < 2; ++s) mbar_init(tfull + s, 1), mbar_init(tempty + s, 8);
     mbar_init_fence();
     if (kKind == kForward && blockIdx.x == 0) *status = 0;
   }
-  if (warp == 2) tmem_alloc(slot, 2 * BN);
+  if (warp == 2) pair_tmem_alloc(slot, kTmemAll);
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // (both blocks' barriers are there before anything arrives at them)
   tc_fence_after();
   const uint32_t tmem = *slot;
+  const int rank = blockIdx.x & 1;
 
-  if (warp == 0) {  // copies
+  if (warp == 0) {  // copies: the block's own rows, and its half of the columns (the forward's: G's or U's)
     const auto load = [&](int s, bool weights, int m, int n, int k) {
       uint8_t *a = smem + s * kBytesStage, *b = a + kBytesA;
-      mbar_expect_tx(full + s, kBytesStage);
+      const uint32_t bar = in_first_block(full + s);
+      if (rank == 0) mbar_expect_tx(full + s, 2 * kBytesStage);
       if (kKind == kForward) {
-        tma_load_2d(a, &maps.a[0], k * BK, m * BM, full + s);
-        tma_load_2d(b, &maps.b[0], k * BK, n * kOwn, full + s);
-        tma_load_2d(b + kBytesB / 2, &maps.b[1], k * BK, n * kOwn, full + s);
+        pair_load_2d(a, &maps.a[0], k * BK, m * BM, bar);
+        pair_load_2d(b, &maps.b[rank], k * BK, n * kOwn, bar);
       } else if (!weights) {
         const int which = k >= plan.half, kk = (k - (which ? plan.half : 0)) * BK;
-        tma_load_2d(a, &maps.a[which], kk, m * BM, full + s);
+        pair_load_2d(a, &maps.a[which], kk, m * BM, bar);
 #pragma unroll
-        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.b[which], n * BN + j * 64, kk, full + s);
+        for (int j = 0; j < BN / 128; ++j)
+          pair_load_2d(b + j * 8192, &maps.b[which], n * BN + (rank * (BN / 128) + j) * 64, kk, bar);
       } else {
         const int which = m >= plan.w_half, row = (m - (which ? plan.w_half : 0)) * BM;
 #pragma unroll
-        for (int j = 0; j < BM / 64; ++j) tma_load_2d(a + j * 8192, &maps.wa[which], row + j * 64, k * BK, full + s);
+        for (int j = 0; j < BM / 64; ++j) pair_load_2d(a + j * 8192, &maps.wa[which], row + j * 64, k * BK, bar);
 #pragma unroll
-        for (int j = 0; j < BN / 64; ++j) tma_load_2d(b + j * 8192, &maps.wb, n * BN + j * 64, k * BK, full + s);
+        for (int j = 0; j < BN / 128; ++j)
+          pair_load_2d(b + j * 8192, &maps.wb, n * BN + (rank * (BN / 128) + j) * 64, k * BK, bar);
       }
     };
     int it = 0;
@@ -229,9 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    // what is still on its way has to arrive before the block may end
-    for (int j = max(0, it - kStages); j < it; ++j) mbar_wait(full + j % kStages, (j / kStages) & 1, status, 2);
-  } else if (warp == 1) {  // products
+    // the last stages have to be done with before the block may end
+    for (int j = max(0, it - kStages); j < it; ++j) mbar_wait(empty + j % kStages, (j / kStages) & 1, status, 2);
+  } else if (warp == 1 && rank == 0) {  // products of both blocks
     int it = 0, done = 0;
     bool ok = true;
     Item tile;
@@ -239,27 +296,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the forward's operands lie along the sum; dx's right one across it, the weights' gradients' both
       const bool a_mn = kKind == kGrads && tile.weights;
       constexpr bool kBmn = kKind == kGrads;
-      const uint32_t idesc = idesc_bf16(BM, BN, a_mn, kBmn);
+      const uint32_t idesc = idesc_bf16(2 * BM, BN, a_mn, kBmn);
       const int acc = done & 1;
       const uint64_t step_a = a_mn ? mdesc_step(16) : kdesc_step(BM, 16);
       if (done >= 2 && !(ok = mbar_wait(tempty + acc, (done / 2 - 1) & 1, status, 3))) break;
+      fence_cluster();
       tc_fence_after();
       for (int k = tile.from; k < tile.to; ++k, ++it) {
         const int s = it % kStages;
         if (!(ok = mbar_wait(full + s, (it / kStages) & 1, status, 4))) break;
         tc_fence_after();
         uint8_t *a = smem + s * kBytesStage, *b = a + kBytesA;
-        const uint64_t da = a_mn ? mdesc(a, BK, 0) : kdesc(a, BM, 0), db = kBmn ? mdesc(b, BK, 0) : kdesc(b, BN, 0);
+        const uint64_t da = a_mn ? mdesc(a, BK, 0) : kdesc(a, BM, 0), db = kBmn ? mdesc(b, BK, 0) : kdesc(b, BN / 2, 0);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < BK; kk += 16)
-            mma_bf16(tmem + acc * BN, da + (kk / 16) * step_a, db + (kBmn ? mdesc_step(kk) : kdesc_step(BN, kk)), idesc,
-                     k > tile.from || kk > 0);
-          mma_commit(empty + s);
+            pair_mma_bf16(tmem + acc * BN, da + (kk / 16) * step_a, db + (kBmn ? mdesc_step(kk) : kdesc_step(BN / 2, kk)),
+                          idesc, k > tile.from || kk > 0);
+          pair_commit(empty + s);
         }
         __syncwarp();
       }
-      if (elect_one()) mma_commit(tfull + acc);
+      if (elect_one()) pair_commit(tfull + acc);
       __syncwarp();
     }
     // the last products have to end before the tensor memory is given back
@@ -268,10 +326,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, row = q * 32 + lane, acc = (warp >> 2) - 1, bar = 1 + acc;
     const bool leader = q == 0 && lane == 0;
     out += acc * kBytesPiece;
+    const uint32_t drained = in_first_block(tempty + acc);
     Item tile;
     for (int done = acc; item_of<kKind>(plan, done, tile); done += 2) {
       int m, n;
       tile_of<kKind>(plan, tile, m, n);
+      const bool there = m < (tile.weights ? plan.w_m_tiles : plan.m_tiles);  // (an odd last row tile has no neighbour)
       const bool ok = mbar_wait(tfull + acc, (done / 2) & 1, status, 6);
       if (named_bar_or(bar, 128, !ok)) break;
       tc_fence_after();
@@ -306,12 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async();
             named_bar(bar, 128);
             const int col = n * kOwn + (c - 1) * 32;
-            if (leader && col < args.F) {
+            if (leader && there && col < args.F) {
               tma_store_2d(&maps.o, out, col, m * BM);
               tma_store_commit();
             }
           }
-          if (stash) {
+          if (stash && there) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (n * kOwn + c * 32 + j * 8 < args.F)
@@ -319,11 +379,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
-        if (lane == 0) mbar_arrive(tempty + acc);
+        if (lane == 0) arrive_in_first_block(drained);
       } else if (!tile.weights && plan.pieces > 1) {
         float4* to = part + (((size_t)tile.piece * plan.m_tiles + m) * (args.D / 4) + n * (BN / 4)) * BM + row;
 #pragma unroll 1
-        for (int c = 0; c < BN / 32 && n * BN + c * 32 < args.D; ++c, to += 8 * BM) {
+        for (int c = 0; there && c < BN / 32 && n * BN + c * 32 < args.D; ++c, to += 8 * BM) {
           uint32_t v[32];
           tmem_ld32_nowait(base + c * 32, v);
           tmem_wait_ld();
@@ -335,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
         }
         tc_fence_before();
-        if (lane == 0) mbar_arrive(tempty + acc);
+        if (lane == 0) arrive_in_first_block(drained);
       } else {
         const int which = tile.weights && m >= plan.w_half, row0 = (m - (which ? plan.w_half : 0)) * BM;
         const CUtensorMap* to_map = tile.weights ? &maps.wo[which] : &maps.o;
@@ -357,23 +417,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async();
           named_bar(bar, 128);
-          if (leader && n * BN + p * 64 < args.D) {
+          if (leader && there && n * BN + p * 64 < args.D) {
             tma_store_2d(to_map, out, n * BN + p * 64, row0);
             tma_store_commit();
           }
         }
         tc_fence_before();
-        if (lane == 0) mbar_arrive(tempty + acc);
+        if (lane == 0) arrive_in_first_block(drained);
       }
     }
     if (leader) tma_store_wait0();
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // (nothing of the other block's is on its way here any more)
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * BN);
+    pair_tmem_dealloc(tmem, kTmemAll);
   }
 }
 
@@ -552,24 +612,38 @@ cudaError_t launch(const char* name, const Maps& maps, const Plan& plan, const C
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), Stages<BN>::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  const long long tiles = (long long)plan.m_tiles * plan.n_tiles * plan.pieces +
-                          (kKind == kGrads ? (long long)plan.w_m_tiles * plan.w_n_tiles : 0);
+  const int pairs = pairs_of(plan.m_tiles, plan.n_tiles) * plan.pieces +
+                    (kKind == kGrads ? pairs_of(plan.w_m_tiles, plan.w_n_tiles) : 0);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pairs < kSMs / 2 ? 2 * pairs : kSMs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Stages<BN>::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t launched = cudaSuccess;
   SSD_LAUNCH(name, st,
-             kernel<<<tiles < kSMs ? (unsigned)tiles : kSMs, kThreads, Stages<BN>::kSmem, st>>>(
-                 maps, plan, c.a, kKind == kForward ? c.stash : nullptr, c.part, c.status));
-  return cudaGetLastError();
+             launched = cudaLaunchKernelEx(&cfg, kernel, maps, plan, c.a, kKind == kForward ? c.stash : (uint8_t*)nullptr,
+                                           c.part, c.status));
+  return launched;
 }
 int up(long long a, int b) { return (int)((a + b - 1) / b); }
 
-constexpr int kLeast = 4;  // steps that a tile's results take: a tile of fewer ends no sooner
-// dx and the weights' gradients in one launch: how many of the latter's tiles every block takes, so that the last ends
-// soonest (steps of those with one more of dx's, and of the others).  Returns the steps until then.  8192 rows of 2560 and
-// 7680: 640 tiles of 240 steps and 1200 of 128 on 152 blocks end after 2112 steps, one kind after the other they would after
-// 2224.
+// Steps that a tile's results take: a tile of fewer ends no sooner.  Gradients with 10 and with 4, us: 256 rows of 2560 and
+// 7680 53 and 63; 512 of 2560 and 7680 69 and 76; 453 of 712 and 11912 51 and 55; 128 of 1024 and 4096 26 with either.
+constexpr int kLeast = 10;
+// dx and the weights' gradients in one launch: how many of the latter's pairs of tiles every pair of blocks takes, so
+// that the last ends soonest (steps of those with one more of dx's, and of the others).  Returns the steps until then.  8192
+// rows of 2560 and 7680: 320 pairs of tiles of 240 steps and 600 of 128 on 76 pairs of blocks end after 2112 steps, one kind
+// after the other they would after 2224.
 long long balance(Plan* p) {
-  const int tiles = p->m_tiles * p->n_tiles * p->pieces, w_tiles = p->w_m_tiles * p->w_n_tiles;
+  const int tiles = pairs_of(p->m_tiles, p->n_tiles) * p->pieces, w_tiles = pairs_of(p->w_m_tiles, p->w_n_tiles);
   const int steps = up(p->steps, p->pieces), w_steps = p->w_steps > kLeast ? p->w_steps : kLeast;
-  const int blocks = tiles + w_tiles < kSMs ? tiles + w_tiles : kSMs;
+  const int blocks = tiles + w_tiles < kSMs / 2 ? tiles + w_tiles : kSMs / 2;
   const int more = tiles % blocks, each = tiles / blocks, others = blocks - more;
   long long best = -1;
   const int least = w_tiles / blocks - steps / w_steps - 2;  // (with fewer, the others would end later than the first)
@@ -584,15 +658,16 @@ long long balance(Plan* p) {
 }
 
 // Whether tiles of half the columns end sooner: their step takes about 5/8 of a whole one's, and they are dealt out more
-// evenly.  Forward, us: 1501 rows of 776 and 2056 in narrow ones 25.6, in wide ones 29.0; 2048 of 1024 and 4096 42.9 and
-// 41.0; 8192 of 2560 and 7680 505 and 400.  Gradients, the same sizes: 41.3 and 43.1, 59 and 54, 908 and 717.
+// evenly.  Forward, us: 2088 rows of 568 and 2096 in narrow ones 25.3, in wide ones 26.9; 2048 of 1024 and 4096 43.6 and
+// 39.4; 8192 of 2560 and 7680 449 and 368.  Gradients: 131 rows of 632 and 832 14.2 and 20.2; 6800 of 272 and 2000 44 and 61;
+// 2048 of 1024 and 4096 55 and 48; 8192 of 2560 and 7680 830 and 681.
 constexpr int kWideStep = 8, kNarrowStep = 5;
 bool sooner(long long narrow_steps, long long wide_steps) { return narrow_steps * kNarrowStep < wide_steps * kWideStep; }
 
 // The gradients' tiles: wide or narrow, and dx's sums in as many pieces as end soonest, the launch that joins them (12 steps)
-// and the bytes it reads counted in.  With few rows dx is a few tiles of long sums (the backward's launches, us, in pieces
-// and in one: 125 rows of 288 and 8816 33 and 75; 256 of 2560 and 7680 59 and 72; 453 of 712 and 11912 71 and 154; 1501 of
-// 776 and 2056 stay in one, 51 and 56 in two).
+// and the bytes it reads counted in.  With few rows dx is a few tiles of long sums (the gradients and the joining
+// launch, us, in pieces and in one: 125 rows of 288 and 8816 25 and 59; 453 of 712 and 11912 51 and 111; 256 of 2560 and 7680
+// 53 and 56; 1501 of 776 and 2056 stay in one, 35 and 41 in two).
 constexpr int kMostPieces = 16, kLeastSteps = 8, kJoinSteps = 12;  // pieces, steps of one
 Plan grads_plan(const Args& a, bool* narrow) {
   Plan best = {};
@@ -602,7 +677,7 @@ Plan grads_plan(const Args& a, bool* narrow) {
               2 * up(a.F, BM), up(a.D, cols), up(a.M, BK),     up(a.F, BM)};
     const auto fits = [&](int pieces) {
       return pieces <= kMostPieces && p.steps >= kLeastSteps * pieces &&
-             (long long)p.m_tiles * p.n_tiles * pieces <= 8 * kSMs;
+             (long long)pairs_of(p.m_tiles, p.n_tiles) * pieces <= 4 * kSMs;
     };
     for (p.pieces = 1; p.pieces == 1 || fits(p.pieces); ++p.pieces) {
       long long end = balance(&p) * (cols == 256 ? kWideStep : kNarrowStep);
@@ -629,7 +704,7 @@ cudaError_t forward(const Call& c, cudaStream_t st) {
   Maps maps;
   Few few;
   const bool is_few = few_rows(c.a, &few);
-  const auto rounds = [&](int cols) { return up((long long)up(c.a.M, BM) * up(c.a.F, cols), kSMs); };
+  const auto rounds = [&](int cols) { return up(pairs_of(up(c.a.M, BM), up(c.a.F, cols)), kSMs / 2); };
   const bool narrow = sooner(rounds(64), rounds(128));
   const int wide = is_few ? few.wide : narrow ? 64 : 128;
   cudaError_t e = map(&maps.a[0], c.x, c.a.D, c.a.M, c.a.xs, BK, is_few ? few.rows : BM);
