@@ -550,6 +550,8 @@ ssd_status ssd_norm_backward(const ssd_norm_problem* prob, const void* dy, const
  *
  * A NaN or infinity reaches the later steps of its channel and sequence only
  * (the earlier ones' gradients); other sequences take nothing from it.
+ * ssd_glr_forward takes a gate s(i) below 2^-64 as 0 (i below about -44), and
+ * ssd_glr_backward gates below 1e-30 as 1e-30 (below about -69).
  *
  * ssd_glr_stash_size: bytes of the stash a training forward may keep for its
  *   backward: the fp32 state that enters every eighth step (bf16), or every

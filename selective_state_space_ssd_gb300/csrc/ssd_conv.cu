@@ -20,10 +20,10 @@ namespace conv {
 namespace {
 
 constexpr int kThreads = 256, kWarps = 8;
-// Steps loaded ahead, channels a thread has (where rows are whole pieces of them) and blocks an SM.  Measured at 4 x 4096
-// steps of 5120 channels: forward 61 us with eight steps, 3 blocks (four steps 65, 2 blocks 71; two channels a thread 69),
-// backward, in runs of 64 steps, 125 us with four channels, four steps and 2 blocks (two channels 157 to 163; without the next
-// steps on their way 140).
+// Steps loaded ahead, channels a thread has (where rows are whole pieces of them) and blocks an SM.  Measured, L2 flushed:
+// 4 x 4096 steps of 5120 channels forward 66 us with eight steps and 3 blocks (four steps 66, 2 blocks 66, two channels a
+// thread 73), 11811 of 1582, one channel a thread, 33 us (four steps 41); backward 112 us with four channels, four steps and 2
+// blocks (two channels 137; registers for 3 blocks spill, 300).
 constexpr int kAhead = 8, kFwdBlocks = 3, kWide = 4;
 constexpr int kBack = 4, kBackBlocks = 2;
 
@@ -586,9 +586,10 @@ ssd_status make_args(const ssd_conv_problem* p, Args* a) {
   return SSD_OK;
 }
 // Steps of a run (a multiple of kAhead): those with which the blocks that fit the GPU at once end soonest, turn after turn; a
-// run starts with loads that take about as long as 16 steps.  Forward and backward, us: 20011 steps of 2560 channels 45 and
-// 68, in runs of 64 46 and 85; 16384 of 2560 38 and 59, 46 and 74; 4 x 4096 of 5120 66 and 112, 65 and 125.  Longer ones
-// where the grid would pass 2^31 blocks.
+// run starts with loads that take about as long as 16 steps.  Forward and backward, us: 20011 steps of 2560 channels 43 and
+// 68, in runs of 64 46 and 85; 16384 of 2560 39 and 60, 45 and 74; 4 x 4096 of 5120 66 and 112, 66 and 123.  Planned for four
+// channels a thread also where one is taken, which has four times the blocks: 11811 of 1582 33 and 67, in runs of 64 32 and
+// 68.  Longer ones where the grid would pass 2^31 blocks.
 constexpr int kStart = 16, kMostRun = 256;
 void set_run(Args* a, int blocks_of_an_sm) {
   const long long slots = 152 * blocks_of_an_sm;

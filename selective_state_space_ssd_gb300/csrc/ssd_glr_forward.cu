@@ -21,7 +21,7 @@ constexpr int blocks_of() {
 }
 
 // 1 / sqrt(m2 e1^2): with e1 = 1 + e^-i, m2 times it is m s(i), by one root in place of a root and a reciprocal (16384 steps
-// of 2560 channels: 90 us, 93 with both).  0 where m2 is, and where e1^2 is infinite (a gate below 2^-63).
+// of 2560 channels: 90 us, 93 with both).  0 where m2 is, and where e1^2 is infinite (a gate below 2^-64).
 __device__ __forceinline__ P inv_root(P m2, P e1) {
   return each(each(m2, [](float v) { return fmaxf(v, 1e-37f); }) * (e1 * e1), [](float v) { return rsqrt_f(v); });
 }
