@@ -64,7 +64,8 @@ def test_a_nan_stays_in_its_row(m, d, f, row):
     check("dx", dx[rest], ref["dx"][rest], 8e-3)
 
 
-@pytest.mark.parametrize("m,d,f", SIZES)
+# (with dx's sums in pieces too, an odd number of row tiles and one)
+@pytest.mark.parametrize("m,d,f", SIZES + [(300, 72, 4104), (1, 8, 1024)])
 def test_rows_behind_the_last_are_left_alone(m, d, f):
     d_ = cuda(make(m, d, f, 25))
     x, wg, wu, dh = (d_[k] for k in ("x", "wg", "wu", "dh"))
